@@ -9,6 +9,13 @@
  *   mamba_state_update   one generation step for one new token per sequence;
  *   mamba_scan_bwd       the gradients of mamba_scan_fwd (training), recomputing the state.
  *
+ *   mamba_delta_fwd, mamba_delta_update
+ *                        the gated delta rule, a recurrence of the same kind with a matrix state:
+ *                        whole sequences, and one generation step.
+ *
+ * Around them: the block's projections (mamba_gemm_bf16, mamba_block_fwd) and its norms
+ * (mamba_gated_norm_*, mamba_add_norm_*).
+ *
  * The model (sources by page title and section):
  *   - "Mamba" (elemedex dex entry), "How it works": h_t = Abar*h_{t-1} + Bbar*x_t, y_t = C*h_t,
  *     with Delta, B and C functions of the current token.
@@ -289,6 +296,162 @@ int mamba_block_fwd(const void* hidden, const void* w_in, const float* conv_weig
                     const float* dt_bias, const float* A, const float* D, const void* w_out,
                     void* out, const mamba_block_dims* dims, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/*
+ * The gated delta rule: a linear recurrence like the scan's ("Mamba" (elemedex), "How it works": the
+ * state is updated by quantities that depend on the current token) whose state is a matrix per head and
+ * whose update first removes what the state already holds for the token's key.  Per value head, with
+ * its key head's q and k:
+ *     S~_t = exp(g_t) S_{t-1}                     (dk x dv)
+ *     e_t  = v_t - S~_t^T k_t
+ *     S_t  = S~_t + beta_t k_t e_t^T
+ *     o_t  = scale S_t^T q_t
+ * Training and prefill run over the whole known sequence, generation one token at a time ("Mamba"
+ * (visual-learn), "Training without stepping token by token").
+ *
+ * g <= 0 is the log of the decay (values below -200, -infinity among them, reset the state); beta is
+ * usually in (0, 1) and the keys of unit length.  Value heads [h * rep, (h + 1) * rep), rep = v_heads /
+ * qk_heads, share query and key head h.  dk and dv are multiples of 8 with dk <= 128 and dv <= 1024
+ * (MAMBA_ERR_UNSUPPORTED otherwise).
+ */
+typedef struct mamba_delta_dims {
+  int64_t batch;    /* sequences, >= 1 */
+  int64_t seqlen;   /* tokens per sequence, >= 1; packed sequences: of all of them together */
+  int64_t qk_heads; /* heads of q and k, >= 1 */
+  int64_t v_heads;  /* heads of v, out, g, beta and the state; a multiple of qk_heads, <= 65535 */
+  int64_t dk, dv;   /* values per key and per value head */
+  int64_t q_stride, k_stride, v_stride; /* elements between tokens of q, k, v; 0: heads * values.
+                                           Multiples of 16 bytes (MAMBA_ERR_ALIGN otherwise), so that
+                                           q, k and v may be slices of one projection's rows.
+                                           Sequences follow each other at seqlen strides. */
+  int32_t io_dtype; /* enum mamba_dtype: q, k, v, g, beta, out and their gradients */
+  int32_t reserved; /* set to 0 */
+} mamba_delta_dims;
+
+/* Bytes of device workspace mamba_delta_fwd needs (0 for invalid dims); packed != 0: for a call with
+ * seq_offsets.  Per 64 tokens and value head it holds two 64 x 64 matrices and the decays: 25 KB in
+ * bf16, 33 KB in fp32. */
+size_t mamba_delta_workspace_bytes(const mamba_delta_dims* dims, int packed);
+
+/*
+ * The gated delta rule over whole sequences.
+ *   q, k          : (batch, seqlen, qk_heads, dk), io_dtype, tokens q_stride and k_stride apart
+ *   v             : (batch, seqlen, v_heads, dv), io_dtype, tokens v_stride apart
+ *   g, beta       : (batch, seqlen, v_heads), io_dtype, contiguous
+ *   initial_state : (batch, v_heads, dk, dv) fp32, or NULL: zero
+ *   seq_offsets   : NULL, or (batch + 1) device int64 token offsets of packed sequences, ascending from
+ *                   0 to seqlen: sequence s is tokens [seq_offsets[s], seq_offsets[s + 1]) of one long
+ *                   row of seqlen tokens (empty ones allowed).  They are read on the device and clamped
+ *                   to [0, seqlen]; tokens that no sequence holds are not written.
+ *   out           : (batch, seqlen, v_heads, dv), io_dtype, contiguous
+ *   last_state    : (batch, v_heads, dk, dv) fp32, or NULL; may be initial_state.  A sequence of no
+ *                   tokens hands its initial state on.
+ *   workspace     : >= mamba_delta_workspace_bytes bytes, 256-byte aligned; contents on entry ignored
+ * q, k, v, out and the states are 16-byte aligned.  The state is fp32 throughout; with bf16 storage the
+ * products that reach it carry 16 bits of each factor's mantissa (relative error about 1e-6), with fp32
+ * storage all 24.
+ */
+int mamba_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                    const float* initial_state, const int64_t* seq_offsets, float scale, void* out,
+                    float* last_state, const mamba_delta_dims* dims, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * One generation step of the gated delta rule for `batch` sequences (dims->seqlen must be 1): the
+ * state (batch, v_heads, dk, dv) fp32, 16-byte aligned, is updated in place.
+ *   q, k, v, g, beta, out : as for mamba_delta_fwd with one token per sequence
+ */
+int mamba_delta_update(float* state, const void* q, const void* k, const void* v, const void* g,
+                       const void* beta, float scale, void* out, const mamba_delta_dims* dims,
+                       void* stream);
+
+/* Sizes of the gated norm.  rows * groups is below 2^31, dim at most 16384 and groups at most 65535
+ * (MAMBA_ERR_SHAPE otherwise). */
+typedef struct mamba_gated_norm_dims {
+  int64_t rows;          /* tokens, >= 1 */
+  int64_t groups;        /* groups of a row that are normed by themselves (heads), >= 1 */
+  int64_t dim;           /* values per group, >= 1 */
+  int64_t y_stride;      /* elements between rows of y; 0: groups * dim */
+  int64_t z_stride;      /* elements between rows of z; 0: groups * dim */
+  int32_t io_dtype;      /* enum mamba_dtype: y, z, out and their gradients */
+  int32_t weight_groups; /* 1: one weight vector for every group; groups: one per group */
+  int32_t gate_first;    /* 0: norm, then gate; otherwise the gate comes before the norm */
+  int32_t reserved;      /* set to 0 */
+} mamba_gated_norm_dims;
+
+/*
+ * RMS norm with a multiplicative silu gate, between the mixer and its output projection
+ * ("Mamba" (elemedex), "How it works": the block ends in a multiplicative gate).  Per row and group:
+ *     gate_first == 0:  out = y rsqrt(mean(y^2) + eps) weight silu(z)
+ *     gate_first != 0:  a = y silu(z),  out = a rsqrt(mean(a^2) + eps) weight
+ *   y, z    : (rows, groups, dim), io_dtype, rows y_stride and z_stride apart; z NULL: no gate (the
+ *             plain norm per group, as for queries and keys)
+ *   weight  : (weight_groups, dim) fp32
+ *   out     : (rows, groups, dim), io_dtype, contiguous
+ * eps is >= 0 and finite (MAMBA_ERR_UNSUPPORTED otherwise).  Arithmetic is fp32, each output is
+ * rounded once.  Any element-aligned address and any dim run; 16-byte aligned rows are fastest.
+ */
+int mamba_gated_norm_fwd(const void* y, const void* z, const float* weight, float eps, void* out,
+                         const mamba_gated_norm_dims* dims, void* stream);
+
+/* Bytes of device workspace mamba_gated_norm_bwd needs (0 for invalid dims): one partial row of the
+ * weights' gradient per workgroup. */
+size_t mamba_gated_norm_bwd_workspace_bytes(const mamba_gated_norm_dims* dims);
+
+/*
+ * Gradients of mamba_gated_norm_fwd for the loss sum(out * dout).
+ *   dout, dy, dz : (rows, groups, dim), io_dtype, contiguous; dz may be NULL only without z
+ *   dweight      : (weight_groups, dim) fp32
+ * Outputs are overwritten; sums over rows are taken in a fixed order (bitwise reproducible).
+ */
+int mamba_gated_norm_bwd(const void* y, const void* z, const float* weight, float eps,
+                         const void* dout, void* dy, void* dz, float* dweight,
+                         const mamba_gated_norm_dims* dims, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Sizes of the add norm: rows below 2^31, dim at most 16384.  The residual stream is fp32, or of the
+ * block's own type (an fp32 block with a bf16 stream is MAMBA_ERR_UNSUPPORTED). */
+typedef struct mamba_add_norm_dims {
+  int64_t rows;      /* tokens, >= 1 */
+  int64_t dim;       /* model width, >= 1 */
+  int32_t io_dtype;  /* enum mamba_dtype: x, out and their gradients */
+  int32_t res_dtype; /* enum mamba_dtype: residual, residual_out and their gradients */
+} mamba_add_norm_dims;
+
+/*
+ * The join of two blocks ("Mamba" (elemedex), "How it works": blocks are stacked homogeneously): the
+ * block's output x goes, with an optional norm of its own and a scale per channel, into the residual
+ * stream, whose norm is the next block's input.  Per row:
+ *     n = x                                  (post_weight NULL)
+ *         x rsqrt(mean(x^2) + eps) post_weight
+ *     r = residual + scale n                 (residual NULL: zero; scale NULL: one)
+ *     out = r rsqrt(mean(r^2) + eps) weight,  residual_out = r
+ *   x, out                 : (rows, dim), io_dtype, contiguous
+ *   residual, residual_out : (rows, dim), res_dtype, contiguous; residual_out may be residual
+ *   weight, scale, post_weight : (dim) fp32
+ * out is the norm of the unrounded r.  eps as for mamba_gated_norm_fwd.
+ */
+int mamba_add_norm_fwd(const void* x, const void* residual, const float* weight, const float* scale,
+                       const float* post_weight, float eps, void* out, void* residual_out,
+                       const mamba_add_norm_dims* dims, void* stream);
+
+/* Bytes of device workspace mamba_add_norm_bwd needs (0 for invalid dims). */
+size_t mamba_add_norm_bwd_workspace_bytes(const mamba_add_norm_dims* dims);
+
+/*
+ * Gradients of mamba_add_norm_fwd for the loss sum(out * dout) + sum(residual_out * dresidual_out).
+ * r is recomputed from x and residual (the forward's inputs, residual as it was before the call).
+ *   dresidual_out : (rows, dim), res_dtype; NULL: zero
+ *   dx            : (rows, dim), io_dtype
+ *   dresidual     : (rows, dim), res_dtype; NULL: not written
+ *   dweight, dscale, dpost_weight : (dim) fp32; the last two NULL only where scale or post_weight is
+ * Outputs are overwritten; sums over rows are taken in a fixed order (bitwise reproducible).
+ */
+int mamba_add_norm_bwd(const void* x, const void* residual, const float* weight, const float* scale,
+                       const float* post_weight, float eps, const void* dout,
+                       const void* dresidual_out, void* dx, void* dresidual, float* dweight,
+                       float* dscale, float* dpost_weight, const mamba_add_norm_dims* dims,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static text for a status code (never NULL). */
 const char* mamba_status_string(int status);

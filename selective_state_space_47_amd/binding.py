@@ -37,10 +37,34 @@ class mamba_dims(ctypes.Structure):
                 ("chunk_len", ctypes.c_int32)]
 
 
+class mamba_delta_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("qk_heads", ctypes.c_int64), ("v_heads", ctypes.c_int64),
+                ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class mamba_gated_norm_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("weight_groups", ctypes.c_int32),
+                ("gate_first", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class mamba_add_norm_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32)]
+
+
 EXPORTS = ("mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "mamba_state_update",
            "mamba_scan_workspace_bytes",
            "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes", "mamba_gemm_bf16",
-           "mamba_block_fwd", "mamba_block_workspace_bytes", "mamba_status_string",
+           "mamba_block_fwd", "mamba_block_workspace_bytes", "mamba_delta_fwd",
+           "mamba_delta_workspace_bytes", "mamba_delta_update", "mamba_gated_norm_fwd",
+           "mamba_gated_norm_bwd", "mamba_gated_norm_bwd_workspace_bytes", "mamba_add_norm_fwd",
+           "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes", "mamba_status_string",
            "mamba_abi_version")
 
 
@@ -94,6 +118,29 @@ def lib():
             L.mamba_block_fwd.restype = ctypes.c_int
             L.mamba_block_workspace_bytes.argtypes = [bp]
             L.mamba_block_workspace_bytes.restype = ctypes.c_size_t
+            f32, sz = ctypes.c_float, ctypes.c_size_t
+            ep = ctypes.POINTER(mamba_delta_dims)
+            L.mamba_delta_fwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, f32, vp, fp, ep, vp, sz, vp]
+            L.mamba_delta_fwd.restype = ctypes.c_int
+            L.mamba_delta_workspace_bytes.argtypes = [ep, ctypes.c_int]
+            L.mamba_delta_workspace_bytes.restype = sz
+            L.mamba_delta_update.argtypes = [fp, vp, vp, vp, vp, vp, f32, vp, ep, vp]
+            L.mamba_delta_update.restype = ctypes.c_int
+            np_ = ctypes.POINTER(mamba_gated_norm_dims)
+            L.mamba_gated_norm_fwd.argtypes = [vp, vp, fp, f32, vp, np_, vp]
+            L.mamba_gated_norm_fwd.restype = ctypes.c_int
+            L.mamba_gated_norm_bwd.argtypes = [vp, vp, fp, f32, vp, vp, vp, fp, np_, vp, sz, vp]
+            L.mamba_gated_norm_bwd.restype = ctypes.c_int
+            L.mamba_gated_norm_bwd_workspace_bytes.argtypes = [np_]
+            L.mamba_gated_norm_bwd_workspace_bytes.restype = sz
+            ap = ctypes.POINTER(mamba_add_norm_dims)
+            L.mamba_add_norm_fwd.argtypes = [vp, vp, fp, fp, fp, f32, vp, vp, ap, vp]
+            L.mamba_add_norm_fwd.restype = ctypes.c_int
+            L.mamba_add_norm_bwd.argtypes = [vp, vp, fp, fp, fp, f32, vp, vp, vp, vp, fp, fp, fp,
+                                             ap, vp, sz, vp]
+            L.mamba_add_norm_bwd.restype = ctypes.c_int
+            L.mamba_add_norm_bwd_workspace_bytes.argtypes = [ap]
+            L.mamba_add_norm_bwd_workspace_bytes.restype = sz
             L.mamba_status_string.argtypes = [ctypes.c_int]
             L.mamba_status_string.restype = ctypes.c_char_p
             L.mamba_abi_version.argtypes = []
@@ -544,3 +591,362 @@ def mamba_block_fwd(hidden, w_in, conv_weight, conv_bias, w_x, w_dt, dt_bias, A,
                                 ws_len, stream)
     _raise(st)
     return out
+
+
+# ---------------------------------------------------------------------------- gated delta rule
+
+def _token_stride(t, name, vec):
+    """Elements between tokens of a (..., tokens, heads, values) tensor whose tokens lie at one
+    stride, heads and values packed inside each; raises where the layout is another."""
+    H, d = t.shape[-2:]
+    if t.dim() == 4:
+        batch, L = t.shape[:2]
+        stride = t.stride(1) if L > 1 else t.stride(0) if batch > 1 else H * d
+        one = L == 1 or batch == 1 or t.stride(0) == L * stride
+    else:
+        stride = t.stride(0) if t.shape[0] > 1 else H * d
+        one = True
+    if (not one or (d > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != d)
+            or stride < H * d or stride % vec):
+        raise ValueError(f"{name} must have packed heads and tokens at one stride, a multiple of "
+                         f"{vec} elements; its strides are {tuple(t.stride())}")
+    return stride
+
+
+# dims structs (read-only for the library), the workspace size and whether the tensors' metadata
+# passed the checks, per combination of shapes, strides, types and devices
+_DELTA_CACHE = {}
+
+
+def _meta(t):
+    """What the checks look at: two tensors of equal metadata pass or fail alike."""
+    if not isinstance(t, torch.Tensor):
+        return type(t)
+    return t.shape, t.stride(), t.dtype, t.get_device()
+
+
+def _delta_checked(q, k, v, g, beta, others, packed, n_seq, lead):
+    """Dims and workspace size of a call on these tensors; raises for tensors that do not belong
+    together.  `others`: (tensor or None, name, shape function of (batch, Hv, dk, dv), dtype or None
+    for the io dtype)."""
+    key = (_meta(q), _meta(k), _meta(v), _meta(g), _meta(beta),
+           tuple(_meta(o[0]) for o in others), packed, n_seq, lead)
+    hit = _DELTA_CACHE.get(key)
+    if hit is not None:
+        return hit
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != lead + 2:
+            raise ValueError(f"{name} must have {lead + 2} dimensions, it has shape "
+                             f"{tuple(t.shape)}")
+        if t.device != q.device or t.dtype != q.dtype:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, q {q.dtype} on {q.device}")
+    if q.device.type != "cuda":
+        raise ValueError("tensors must be on a HIP device")
+    io, dev = q.dtype, q.device
+    code = _io_code(io)
+    tokens, (Hk, dk), (Hv, dv) = q.shape[:lead], q.shape[lead:], v.shape[lead:]
+    if k.shape != q.shape or v.shape[:lead] != tokens:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not "
+                         "belong together")
+    if Hk == 0 or Hv % Hk:
+        raise ValueError(f"{Hv} value heads are no multiple of {Hk} key heads")
+    _check(g, "g", (*tokens, Hv), io, dev)
+    _check(beta, "beta", (*tokens, Hv), io, dev)
+    vec = 8 if code == MAMBA_BF16 else 4
+    if packed:
+        batch, L = n_seq, tokens[0]
+    elif lead == 1:  # one token per sequence
+        batch, L = tokens[0], 1
+    else:
+        batch, L = tokens
+    for t, name, shape, dt in others:
+        _check(t, name, shape((batch, *tokens), Hk, Hv, dk, dv), dt or io, dev)
+    dm = mamba_delta_dims(batch, L, Hk, Hv, dk, dv, _token_stride(q, "q", vec),
+                          _token_stride(k, "k", vec), _token_stride(v, "v", vec), code, 0)
+    hit = (dm, int(lib().mamba_delta_workspace_bytes(ctypes.byref(dm), int(packed))))
+    if len(_DELTA_CACHE) >= 1024:
+        _DELTA_CACHE.clear()
+    _DELTA_CACHE[key] = hit
+    return hit
+
+
+def _state_shape(n, Hk, Hv, dk, dv):
+    return (n[0], Hv, dk, dv)
+
+
+def _out_shape(n, Hk, Hv, dk, dv):
+    return (*n[1:], Hv, dv)
+
+
+def _offsets_count(seq_offsets, q):
+    """Number of packed sequences of a (n + 1) int64 offsets tensor; None without one."""
+    if seq_offsets is None:
+        return None
+    if not isinstance(seq_offsets, torch.Tensor) or not isinstance(q, torch.Tensor):
+        raise TypeError("q and seq_offsets must be torch.Tensors")
+    if (seq_offsets.dim() != 1 or seq_offsets.numel() < 2 or seq_offsets.dtype != torch.int64
+            or seq_offsets.device != q.device or not seq_offsets.is_contiguous()):
+        raise ValueError("seq_offsets must be a contiguous (sequences + 1,) int64 tensor on "
+                         f"{q.device}")
+    return seq_offsets.numel() - 1
+
+
+def mamba_delta_workspace_bytes(dims: mamba_delta_dims, packed=False) -> int:
+    return int(lib().mamba_delta_workspace_bytes(ctypes.byref(dims), int(bool(packed))))
+
+
+def mamba_delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, seq_offsets=None,
+                    return_last_state=False, out=None, last_state=None, workspace=None):
+    """The gated delta rule over whole sequences (mamba_delta_fwd in include/mamba_scan.h).
+
+    q, k: (batch, L, Hk, dk); v: (batch, L, Hv, dv); g (log decay), beta: (batch, L, Hv) -- all
+    float32 or all bfloat16; q, k and v may be slices of one projection's rows.  scale defaults to
+    dk ** -0.5.  initial_state: (batch, Hv, dk, dv) float32.  With seq_offsets, an (n + 1,) int64
+    tensor on the device, the token tensors have no batch axis: (tokens, H, d), sequence s being
+    tokens seq_offsets[s] .. seq_offsets[s + 1] - 1, and there are n states.
+    Returns out (batch, L, Hv, dv), or (out, last_state).
+    """
+    n_seq = _offsets_count(seq_offsets, q)
+    packed = n_seq is not None
+    dm, ws_bytes = _delta_checked(q, k, v, g, beta,
+                                  ((initial_state, "initial_state", _state_shape, torch.float32),
+                                   (out, "out", _out_shape, None),
+                                   (last_state, "last_state", _state_shape, torch.float32)),
+                                  packed, n_seq, 1 if packed else 2)
+    dev = q.device
+    if out is None:
+        out = torch.empty(v.shape, dtype=q.dtype, device=dev)
+    if return_last_state and last_state is None:
+        last_state = torch.empty((dm.batch, dm.v_heads, dm.dk, dm.dv), dtype=torch.float32,
+                                 device=dev)
+    workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
+    with _on(dev):
+        st = lib().mamba_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                   _ptr(initial_state), _ptr(seq_offsets),
+                                   dm.dk ** -0.5 if scale is None else scale, _ptr(out),
+                                   _ptr(last_state), ctypes.byref(dm), _ptr(workspace), ws_len,
+                                   _stream(dev))
+    _raise(st)
+    return (out, last_state) if return_last_state else out
+
+
+def mamba_delta_update(state, q, k, v, g, beta, scale=None, out=None):
+    """One generation step of the gated delta rule (mamba_delta_update in include/mamba_scan.h).
+
+    state: (batch, Hv, dk, dv) float32, updated in place; q, k: (batch, Hk, dk); v: (batch, Hv, dv);
+    g, beta: (batch, Hv).  Returns out (batch, Hv, dv).
+    """
+    if state is None:
+        raise ValueError("state is required")
+    dm, _ = _delta_checked(q, k, v, g, beta, ((state, "state", _state_shape, torch.float32),
+                                              (out, "out", _out_shape, None)), False, None, 1)
+    dev = q.device
+    if out is None:
+        out = torch.empty(v.shape, dtype=q.dtype, device=dev)
+    with _on(dev):
+        st = lib().mamba_delta_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                      dm.dk ** -0.5 if scale is None else scale, _ptr(out),
+                                      ctypes.byref(dm), _stream(dev))
+    _raise(st)
+    return out
+
+
+# ---------------------------------------------------------------------------- norms of a block
+
+def _row_stride(t, name):
+    """Elements between the rows of a (rows, groups, dim) tensor, packed inside each row."""
+    rows, G, d = t.shape
+    stride = t.stride(0) if rows > 1 else G * d
+    if (d > 1 and t.stride(2) != 1) or (G > 1 and t.stride(1) != d) or stride < G * d:
+        raise ValueError(f"{name} must have packed rows; its strides are {tuple(t.stride())}")
+    return stride
+
+
+_NORM_CACHE = {}
+
+
+def _gated_checked(y, z, weight, gate_first, others):
+    """Dims and workspace size of a gated norm; `others`: (tensor or None, name, "rows"|"weight")."""
+    key = (_meta(y), _meta(z), _meta(weight), gate_first, tuple(_meta(o[0]) for o in others))
+    hit = _NORM_CACHE.get(key)
+    if hit is not None:
+        return hit
+    for t, name in ((y, "y"), (weight, "weight")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if y.dim() != 3 or y.device.type != "cuda":
+        raise ValueError("y must be (rows, groups, dim) on a HIP device")
+    rows, G, d = y.shape
+    io, dev = y.dtype, y.device
+    code = _io_code(io)
+    if z is not None:
+        if not isinstance(z, torch.Tensor):
+            raise TypeError("z must be a torch.Tensor")
+        if z.shape != y.shape or z.dtype != io or z.device != dev:
+            raise ValueError(f"z must be like y, {tuple(y.shape)} {io} on {dev}")
+    per_group = weight.dim() == 2
+    wshape = (G, d) if per_group else (d,)
+    _check(weight, "weight", wshape, torch.float32, dev)
+    for t, name, kind in others:
+        if kind == "weight":
+            _check(t, name, wshape, torch.float32, dev)
+        else:
+            _check(t, name, (rows, G, d), io, dev)
+    dm = mamba_gated_norm_dims(rows, G, d, _row_stride(y, "y"),
+                               0 if z is None else _row_stride(z, "z"), code,
+                               G if per_group else 1, int(bool(gate_first)), 0)
+    hit = (dm, int(lib().mamba_gated_norm_bwd_workspace_bytes(ctypes.byref(dm))))
+    if len(_NORM_CACHE) >= 1024:
+        _NORM_CACHE.clear()
+    _NORM_CACHE[key] = hit
+    return hit
+
+
+def mamba_gated_norm_bwd_workspace_bytes(dims: mamba_gated_norm_dims) -> int:
+    return int(lib().mamba_gated_norm_bwd_workspace_bytes(ctypes.byref(dims)))
+
+
+def mamba_gated_norm_fwd(y, z, weight, eps=1e-5, gate_first=False, out=None):
+    """RMS norm per group with a silu gate (mamba_gated_norm_fwd in include/mamba_scan.h).
+
+    y, z: (rows, groups, dim) float32 or bfloat16, rows at any stride (z None: no gate); weight:
+    (dim,) or (groups, dim) float32.  norm(y) * weight * silu(z), or norm(y * silu(z)) * weight with
+    gate_first.  Returns out (rows, groups, dim).
+    """
+    dm, _ = _gated_checked(y, z, weight, gate_first, ((out, "out", "rows"),))
+    dev = y.device
+    if out is None:
+        out = torch.empty(y.shape, dtype=y.dtype, device=dev)
+    with _on(dev):
+        st = lib().mamba_gated_norm_fwd(_ptr(y), _ptr(z), _ptr(weight), eps, _ptr(out),
+                                        ctypes.byref(dm), _stream(dev))
+    _raise(st)
+    return out
+
+
+def mamba_gated_norm_bwd(y, z, weight, dout, eps=1e-5, gate_first=False, workspace=None,
+                         grads=None):
+    """Gradients of mamba_gated_norm_fwd: a dict with dy, dz (None without z) and dweight.  `grads`
+    may hold preallocated output tensors under the same keys."""
+    if dout is None:
+        raise ValueError("dout is required")
+    g = dict(grads or {})
+    dm, ws_bytes = _gated_checked(y, z, weight, gate_first,
+                                  ((dout, "dout", "rows"), (g.get("dy"), "dy", "rows"),
+                                   (g.get("dz"), "dz", "rows"),
+                                   (g.get("dweight"), "dweight", "weight")))
+    dev = y.device
+    if g.get("dy") is None:
+        g["dy"] = torch.empty(y.shape, dtype=y.dtype, device=dev)
+    if z is None:
+        g["dz"] = None
+    elif g.get("dz") is None:
+        g["dz"] = torch.empty(y.shape, dtype=y.dtype, device=dev)
+    if g.get("dweight") is None:
+        g["dweight"] = torch.empty(weight.shape, dtype=torch.float32, device=dev)
+    workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
+    with _on(dev):
+        st = lib().mamba_gated_norm_bwd(_ptr(y), _ptr(z), _ptr(weight), eps, _ptr(dout),
+                                        _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dweight"]),
+                                        ctypes.byref(dm), _ptr(workspace), ws_len, _stream(dev))
+    _raise(st)
+    return {n: g[n] for n in ("dy", "dz", "dweight")}
+
+
+def _add_checked(x, residual, vectors, others):
+    """Dims and workspace size of an add norm.  `vectors`: (tensor or None, name) of (dim,) float32;
+    `others`: (tensor or None, name, is of the residual's type)."""
+    key = (_meta(x), _meta(residual), tuple(_meta(t) for t, _ in vectors),
+           tuple(_meta(o[0]) for o in others))
+    hit = _NORM_CACHE.get(key)
+    if hit is not None:
+        return hit
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() != 2 or x.device.type != "cuda":
+        raise ValueError("x must be (rows, dim) on a HIP device")
+    rows, d = x.shape
+    io, dev = x.dtype, x.device
+    code = _io_code(io)
+    _check(x, "x", (rows, d), io, dev)
+    # the stream's type is the residual's, or that of the first of its companions
+    res = next((t.dtype for t, _, r in ((residual, "", True), *others) if r and t is not None), io)
+    res_code = _io_code(res)
+    _check(residual, "residual", (rows, d), res, dev)
+    if vectors[0][0] is None:
+        raise ValueError("weight is required")
+    for t, name in vectors:
+        _check(t, name, (d,), torch.float32, dev)
+    for t, name, of_res in others:
+        _check(t, name, (rows, d), res if of_res else io, dev)
+    dm = mamba_add_norm_dims(rows, d, code, res_code)
+    hit = (dm, int(lib().mamba_add_norm_bwd_workspace_bytes(ctypes.byref(dm))), res)
+    if len(_NORM_CACHE) >= 1024:
+        _NORM_CACHE.clear()
+    _NORM_CACHE[key] = hit
+    return hit
+
+
+def mamba_add_norm_bwd_workspace_bytes(dims: mamba_add_norm_dims) -> int:
+    return int(lib().mamba_add_norm_bwd_workspace_bytes(ctypes.byref(dims)))
+
+
+def mamba_add_norm_fwd(x, residual, weight, scale=None, post_weight=None, eps=1e-5, out=None,
+                       residual_out=None):
+    """The join of two blocks (mamba_add_norm_fwd in include/mamba_scan.h): r = residual + scale *
+    x (or norm(x) * post_weight in place of x), out = norm(r) * weight.
+
+    x: (rows, dim) float32 or bfloat16; residual: (rows, dim) of x's type or float32 (None: zero);
+    weight, scale, post_weight: (dim,) float32.  Returns (out, r), r of the residual's type (of x's
+    without one, or of residual_out's).
+    """
+    dm, _, res = _add_checked(x, residual, ((weight, "weight"), (scale, "scale"),
+                                            (post_weight, "post_weight")),
+                              ((out, "out", False), (residual_out, "residual_out", True)))
+    dev = x.device
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=res, device=dev)
+    with _on(dev):
+        st = lib().mamba_add_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(scale),
+                                      _ptr(post_weight), eps, _ptr(out), _ptr(residual_out),
+                                      ctypes.byref(dm), _stream(dev))
+    _raise(st)
+    return out, residual_out
+
+
+def mamba_add_norm_bwd(x, residual, weight, dout, dresidual_out=None, scale=None, post_weight=None,
+                       eps=1e-5, workspace=None, grads=None):
+    """Gradients of mamba_add_norm_fwd for the loss sum(out * dout) + sum(r * dresidual_out): a dict
+    with dx, dresidual (None without a residual), dweight, dscale and dpost_weight (None without
+    theirs).  x and residual are the forward's inputs.  `grads` may hold preallocated output tensors
+    under the same keys."""
+    if dout is None:
+        raise ValueError("dout is required")
+    g = dict(grads or {})
+    dm, ws_bytes, res = _add_checked(
+        x, residual, ((weight, "weight"), (scale, "scale"), (post_weight, "post_weight"),
+                      (g.get("dweight"), "dweight"), (g.get("dscale"), "dscale"),
+                      (g.get("dpost_weight"), "dpost_weight")),
+        ((dout, "dout", False), (dresidual_out, "dresidual_out", True),
+         (g.get("dx"), "dx", False), (g.get("dresidual"), "dresidual", True)))
+    dev = x.device
+    for name, like, dt in (("dx", x, x.dtype), ("dresidual", residual, res),
+                           ("dweight", weight, torch.float32), ("dscale", scale, torch.float32),
+                           ("dpost_weight", post_weight, torch.float32)):
+        if like is None:
+            g[name] = None
+        elif g.get(name) is None:
+            g[name] = torch.empty(like.shape, dtype=dt, device=dev)
+    workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
+    with _on(dev):
+        st = lib().mamba_add_norm_bwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(scale),
+                                      _ptr(post_weight), eps, _ptr(dout), _ptr(dresidual_out),
+                                      _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
+                                      _ptr(g["dscale"]), _ptr(g["dpost_weight"]),
+                                      ctypes.byref(dm), _ptr(workspace), ws_len, _stream(dev))
+    _raise(st)
+    return {n: g[n] for n in ("dx", "dresidual", "dweight", "dscale", "dpost_weight")}
