@@ -20,6 +20,7 @@ namespace delta {
 
 constexpr int kC = 64;          // tokens per chunk
 constexpr int kMaxDk = 128;
+constexpr int64_t kMaxStride = (int64_t)1 << 22;  // elements between tokens: 64 tokens of fp32 stay below 2^31 bytes
 constexpr int64_t kMaxDv = 1024;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -29,82 +30,63 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // Operands of the 16 x 16 matrix instructions.  Lane l (g = l / 16, r = l % 16) holds for operand A
 // the row r, for operand B the column r, and of the accumulator C the column r and rows 4g .. 4g+3.
-// A lane's k values may be any permutation of the depth, the same in A and B.  `chain` and `chain_t`
-// read an operand in the order in which accumulators hold their rows, so that the accumulators of
-// one product are (converted in place) the operand of the next: no exchange between lanes.
-//   row     natural order, from a row with k contiguous
-//   chain   accumulator order, from a row with k contiguous
-//   chain_t accumulator order, from rows of k: element (k, r) at tile[k ld + r]
-//   ctile   rows 4g .. 4g+3 of column r of a 16-row tile, as an accumulator
-//   pack    accumulators -> operand (kDepth / 16 of them)
-//   split   the same as a sum of kParts operands that together hold (about) the fp32 value
+// The k values that the lanes hold may be any permutation of the depth, the same one in A and B: all
+// tiles are read in the order in which accumulators hold their rows, so that the accumulators of one
+// product are (converted in place) the operand of the next and nothing moves between lanes.
+//   kDepth  depth of one operand: kDepth / 16 accumulator tiles
+//   pack    accumulators -> operand
+//   split   accumulators -> operands that together hold the fp32 value (bf16: three, 8 bits each)
 template <typename E>
 struct Mma;
 
 template <>
 struct Mma<uint16_t> {
   static constexpr int kDepth = 32;
-  static constexpr int kParts = 2;  // bf16 high part and remainder: 16 bits of the mantissa
-  static constexpr int kPad = 8;
+  static constexpr int kTiles = 2;
+  static constexpr int kParts = 3;
   using Frag = bf16x8;
   struct Parts { Frag p[kParts]; };
-  __device__ static __forceinline__ Frag row(const uint16_t* p, int g) {
-    return *reinterpret_cast<const bf16x8*>(p + 8 * g);
-  }
   __device__ static __forceinline__ Frag join(bf16x4 a, bf16x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-  __device__ static __forceinline__ Frag chain(const uint16_t* p, int g) {
-    return join(*reinterpret_cast<const bf16x4*>(p + 4 * g),
-                *reinterpret_cast<const bf16x4*>(p + 16 + 4 * g));
-  }
-  // transposing LDS read: 16 lanes address 4 rows of 16 values (lane r: row r / 4, values
-  // 4 (r % 4) ..) and lane r receives column r of the 4 rows
-  __device__ static __forceinline__ bf16x4 tr(const uint16_t* tile, int ld, int g, int r) {
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const uint16_t* p = tile + (4 * g + (r >> 2)) * ld + 4 * (r & 3);
-    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
-  }
-  __device__ static __forceinline__ Frag chain_t(const uint16_t* tile, int ld, int g, int r) {
-    return join(tr(tile, ld, g, r), tr(tile + 16 * ld, ld, g, r));
-  }
-  __device__ static __forceinline__ f32x4 ctile(const uint16_t* tile, int ld, int g, int r) {
-    return __builtin_convertvector(tr(tile, ld, g, r), f32x4);
   }
   __device__ static __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
+  // words of two values, so that the conversion of a pair serves the operand and the remainder
   __device__ static __forceinline__ Frag pack(const f32x4* c) {
-    return join(__builtin_convertvector(c[0], bf16x4), __builtin_convertvector(c[1], bf16x4));
+    return __builtin_bit_cast(Frag, make_uint4(pack_bf16(make_float2(c[0][0], c[0][1])),
+                                               pack_bf16(make_float2(c[0][2], c[0][3])),
+                                               pack_bf16(make_float2(c[1][0], c[1][1])),
+                                               pack_bf16(make_float2(c[1][2], c[1][3]))));
   }
   __device__ static __forceinline__ Parts split(const f32x4* c) {
-    const bf16x4 h0 = __builtin_convertvector(c[0], bf16x4);
-    const bf16x4 h1 = __builtin_convertvector(c[1], bf16x4);
-    const f32x4 l0 = c[0] - __builtin_convertvector(h0, f32x4);
-    const f32x4 l1 = c[1] - __builtin_convertvector(h1, f32x4);
-    return {{join(h0, h1), join(__builtin_convertvector(l0, bf16x4),
-                                __builtin_convertvector(l1, bf16x4))}};
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c[i >> 2][i & 3];
+    Parts s;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[i] = pack_bf16(make_float2(v[2 * i], v[2 * i + 1]));
+        const float2 f = unpack(h[i]);
+        v[2 * i] -= f.x;
+        v[2 * i + 1] -= f.y;
+      }
+      s.p[p] = __builtin_bit_cast(Frag, make_uint4(h[0], h[1], h[2], h[3]));
+    }
+    return s;
   }
 };
 
 template <>
 struct Mma<float> {
   static constexpr int kDepth = 16;
+  static constexpr int kTiles = 1;
   static constexpr int kParts = 1;
-  static constexpr int kPad = 4;
   using Frag = f32x4;
   struct Parts { Frag p[kParts]; };
-  __device__ static __forceinline__ Frag row(const float* p, int g) {
-    return *reinterpret_cast<const f32x4*>(p + 4 * g);
-  }
-  __device__ static __forceinline__ Frag chain(const float* p, int g) { return row(p, g); }
-  __device__ static __forceinline__ Frag chain_t(const float* tile, int ld, int g, int r) {
-    const float* p = tile + 4 * g * ld + r;
-    return Frag{p[0], p[ld], p[2 * ld], p[3 * ld]};
-  }
-  __device__ static __forceinline__ f32x4 ctile(const float* tile, int ld, int g, int r) {
-    return chain_t(tile, ld, g, r);
-  }
   // four 4-deep fp32 instructions: step j takes element j of both operands (k = 4g + j)
   __device__ static __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
 #pragma unroll
@@ -114,6 +96,123 @@ struct Mma<float> {
   __device__ static __forceinline__ Frag pack(const f32x4* c) { return c[0]; }
   __device__ static __forceinline__ Parts split(const f32x4* c) { return {{c[0]}}; }
 };
+
+typedef __attribute__((address_space(3))) const char* lds_ptr;
+
+template <typename V>
+__device__ __forceinline__ V lds_read(lds_ptr p) {
+  return *reinterpret_cast<__attribute__((address_space(3))) const V*>(p);
+}
+// transposing LDS read of bf16: 16 lanes address 4 rows of 16 values, lane r the values 4 (r % 4) ..
+// of row r / 4, and lane r receives the r-th value of the 4 rows
+__device__ __forceinline__ bf16x4 lds_tr(lds_ptr p) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+}
+
+// A 64-token tile of keys or queries in LDS: rows of kRow bytes, the 16-byte word w of row t kept at
+// w ^ key(t).  With this key the 16 rows of an operand read, and the 4 rows x 4 words of a transposing
+// read, lie in different banks.
+template <typename E, int DK>
+struct KeyTile {
+  static constexpr int kRow = DK * (int)sizeof(E);
+  static constexpr int kWords = kRow / 16;
+  static constexpr int kBytes = kC * kRow;
+  __device__ static __forceinline__ int key(int t) {
+    return kWords >= 16 ? 4 * (t & 3) + ((t >> 2) & 3) : 4 * ((t >> 1) & 1) + ((t >> 2) & 3);
+  }
+  // lane addresses of one tile
+  int row0, tr0, g, r;
+  __device__ __forceinline__ KeyTile(int lane) : g(lane >> 4), r(lane & 15) {
+    row0 = r * kRow;
+    tr0 = sizeof(E) == 2 ? (4 * g + (r >> 2)) * kRow : 4 * g * kRow + 4 * (r & 3);
+  }
+  // operand with rows = tokens 16 m + r, k = values [kDepth kb, kDepth (kb + 1)) in natural order
+  __device__ __forceinline__ typename Mma<E>::Frag rows(lds_ptr t, int m, int kb) const {
+    return lds_read<typename Mma<E>::Frag>(t + 16 * m * kRow + row0 + (((4 * kb + g) ^ key(r)) << 4));
+  }
+  // the value of the keys that row 4 g + x of accumulator tile m stands for, so that `rows` reads
+  // accumulator order in whole words
+  __device__ static __forceinline__ int value(int m, int g, int x) {
+    return sizeof(E) == 2 ? 32 * (m >> 1) + 8 * g + 4 * (m & 1) + x : 16 * m + 4 * g + x;
+  }
+  // transposed operand: rows = values of accumulator tile m, k = tokens of block kb in accumulator
+  // order
+  __device__ __forceinline__ typename Mma<E>::Frag cols(lds_ptr t, int m, int kb) const {
+    t += Mma<E>::kDepth * kb * kRow + tr0;
+    if constexpr (sizeof(E) == 2) {
+      t += (((4 * (m >> 1) + (r & 3)) ^ key(4 * g + (r >> 2))) << 4) + 8 * (m & 1);
+      return Mma<E>::join(lds_tr(t), lds_tr(t + 16 * kRow));
+    } else {
+      typename Mma<E>::Frag f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        f[j] = lds_read<float>(t + j * kRow + (((4 * m + (r >> 2)) ^ key(4 * g + j)) << 4));
+      return f;
+    }
+  }
+};
+
+// Lower triangular 64 x 64 matrix in LDS and in the workspace: blocks of kDepth columns, block kb
+// holding rows kDepth kb .. 63 of 64 bytes each, four words; word w of a row holds the values that
+// lane group w reads in accumulator order and is kept at w ^ (row / 4 % 4) (bank conflicts as above).
+template <typename E>
+struct TriTile {
+  static constexpr int kD = Mma<E>::kDepth;
+  static constexpr int kBlocks = kC / kD;
+  static constexpr int first_row(int kb) { return kb * kC - kD * (kb * (kb - 1) / 2) - kD * kb; }
+  // byte of row t, block kb (t >= kD kb)
+  __device__ static __forceinline__ int row_at(int kb, int t) { return (first_row(kb) + t) * 64; }
+  static constexpr int kRows = kC * kBlocks - kD * (kBlocks * (kBlocks - 1) / 2);
+  static constexpr int kBytes = kRows * 64;
+  // byte of word w of row t, block kb
+  __device__ static __forceinline__ int word_at(int kb, int t, int w) {
+    return row_at(kb, t) + ((w ^ ((t >> 2) & 3)) << 4);
+  }
+  int row0, g, r;
+  __device__ __forceinline__ TriTile(int lane) : g(lane >> 4), r(lane & 15) {
+    row0 = r * 64 + ((g ^ (r >> 2)) << 4);
+  }
+  // operand with rows 16 m + r, k = columns of block kb
+  __device__ __forceinline__ typename Mma<E>::Frag rows(lds_ptr t, int m, int kb) const {
+    return lds_read<typename Mma<E>::Frag>(t + row_at(kb, 16 * m) + row0);
+  }
+};
+
+// Copies from global memory straight into LDS, 16 bytes per lane and 1 KB per wave instruction:
+// lane l's word goes to lds + 16 l.  Words at or past `bytes` of the buffer read as zero.  There is
+// no register to wait for; the wave waits for its copies with copies_done().
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4 buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  i32x4 d;
+  d[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  d[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+  d[2] = __builtin_amdgcn_readfirstlane((int)bytes);
+  d[3] = 0x00020000;
+  return d;
+}
+__device__ __forceinline__ void copy_lds(i32x4 buf, uint32_t off, uint32_t lds) {
+  uint32_t saved;  // the compiler's m0
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %3\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(off), "s"(buf), "s"(lds)
+      : "memory");
+}
+constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer
+// every copy of this wave has landed, and every wave of the workgroup has come here
+__device__ __forceinline__ void copies_done() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p);
+}
 
 // exp(x) for x <= 0 (and moderate x > 0)
 __device__ __forceinline__ float exp_f32(float x) { return fast_exp2(x * kLog2e); }
@@ -170,14 +269,15 @@ __device__ __forceinline__ int64_t slot_seq(const Args& a, int64_t slot) {
   return lo;
 }
 
-// Workspace of one chunk and value head: T (64 x 64; bf16: high parts, then remainders), P
-// (64 x 64), then exp(G_i) (64 floats), c_j (64 floats), exp(G_64).
+// Workspace of one chunk and value head: T (in kParts parts), P, then 256 floats of gates:
+// exp(G_i) (64), c_j (64), exp(G_64), 63 unused.
 template <typename E>
 struct ChunkWs {
-  static constexpr int kT = kC * kC * 4;  // bytes: 64 x 64 fp32, or two bf16 parts
-  static constexpr int kP = kC * kC * (int)sizeof(E);
-  static constexpr int kGate = 192 * 4;
+  static constexpr int kT = Mma<E>::kParts * TriTile<E>::kBytes;
+  static constexpr int kP = TriTile<E>::kBytes;
+  static constexpr int kGate = 1024;
   static constexpr int kBytes = kT + kP + kGate;
+  static_assert(kBytes % 1024 == 0, "copied in whole wave instructions");
 };
 
 inline int64_t chunk_slots(const mamba_delta_dims* d, bool packed) {
@@ -210,7 +310,7 @@ inline int check_delta(const mamba_delta_dims* d, bool packed) {
   const int64_t s[3] = {d->q_stride, d->k_stride, d->v_stride};
   const int64_t w[3] = {d->qk_heads * d->dk, d->qk_heads * d->dk, d->v_heads * d->dv};
   for (int i = 0; i < 3; ++i) {
-    if (s[i] && (s[i] < w[i] || s[i] > lim)) return MAMBA_ERR_SHAPE;
+    if (w[i] > kMaxStride || s[i] > kMaxStride || (s[i] && s[i] < w[i])) return MAMBA_ERR_SHAPE;
     if (s[i] % vec) return MAMBA_ERR_ALIGN;
   }
   return MAMBA_OK;

@@ -10,9 +10,9 @@
 //   step_kernel   one token: the state is read and written once.
 //
 // Rounding (bf16 storage): products take bf16 operands into fp32 accumulators.  Whatever reaches the
-// state (S in K S, Y, T, E in K^T E) goes in as a bf16 pair (high part and remainder, 16 bits), so
-// that the fp32 state is right to about 1e-6; S and E enter the output O as one bf16 value, whose
-// error is that of rounding the output.  fp32 storage uses fp32 matrix instructions throughout.
+// state (S in K S, Y, T, E in K^T E) goes in as three bf16 parts, the fp32 value to 24 bits, so that
+// the state is fp32 in earnest; the output O takes S and E as two parts and P as one, whose rounding
+// is that of the output again.  fp32 storage uses fp32 matrix instructions throughout.
 #include "mamba_delta.h"
 
 namespace mamba {
@@ -32,7 +32,7 @@ __device__ __forceinline__ uint4 tile_word(const E* base, int64_t stride, int ro
 
 template <typename E, int DK>
 struct ChunkSmem {
-  static constexpr int kLd = DK + Mma<E>::kPad;
+  static constexpr int kLd = DK + 16 / (int)sizeof(E);
   static constexpr int kLf = kC + 4;
   union {
     struct { E k[kC * kLd], q[kC * kLd]; } in;
@@ -41,6 +41,16 @@ struct ChunkSmem {
   float d[4][16 * 20];      // inverted diagonal blocks
   float ghi[kC], glo[kC], beta[kC];
 };
+
+// 16 bytes of storage: bf16 takes the 4 values of each of two tiles, fp32 those of one
+template <typename E>
+__device__ __forceinline__ uint4 pack_word(const float (&a)[4], const float (&b)[4]) {
+  if constexpr (sizeof(E) == 2)
+    return make_uint4(pack_bf16(make_float2(a[0], a[1])), pack_bf16(make_float2(a[2], a[3])),
+                      pack_bf16(make_float2(b[0], b[1])), pack_bf16(make_float2(b[2], b[3])));
+  else
+    return __builtin_bit_cast(uint4, make_float4(a[0], a[1], a[2], a[3]));
+}
 
 // sum of v over lanes 0 .. lane
 __device__ __forceinline__ double wave_prefix(double v, int lane) {
@@ -88,12 +98,13 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
   for (int jt = 0; jt < 4; ++jt) kk[jt] = qk[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-    const auto ki = M::row(&sm.in.k[(16 * w + r) * Sm::kLd + kb * M::kDepth], g);
-    const auto qi = M::row(&sm.in.q[(16 * w + r) * Sm::kLd + kb * M::kDepth], g);
+    const int at = r * Sm::kLd + kb * M::kDepth + g * kV;
+    const auto ki = *reinterpret_cast<const typename M::Frag*>(&sm.in.k[16 * w * Sm::kLd + at]);
+    const auto qi = *reinterpret_cast<const typename M::Frag*>(&sm.in.q[16 * w * Sm::kLd + at]);
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt)
       if (jt <= w) {
-        const auto kj = M::row(&sm.in.k[(16 * jt + r) * Sm::kLd + kb * M::kDepth], g);
+        const auto kj = *reinterpret_cast<const typename M::Frag*>(&sm.in.k[16 * jt * Sm::kLd + at]);
         kk[jt] = M::mma(kj, ki, kk[jt]);
         qk[jt] = M::mma(kj, qi, qk[jt]);
       }
@@ -128,26 +139,27 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
     }
     __syncthreads();
     const float gi = sm.ghi[i], gil = sm.glo[i];
-    E* P = reinterpret_cast<E*>(ws + ChunkWs<E>::kT);
+    float p[4][4];
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
       const int j = 16 * jt + 4 * g;
-      float A[4], p[4];
+      float A[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const float d = jt <= w && j + x <= i
                             ? exp_f32((gi - sm.ghi[j + x]) + (gil - sm.glo[j + x])) * sm.beta[j + x]
                             : 0.f;
         A[x] = j + x < i ? d * kk[jt][x] : 0.f;
-        p[x] = d * qk[jt][x] * a.scale;
+        p[jt][x] = d * qk[jt][x] * a.scale;
       }
       *reinterpret_cast<float4*>(&sm.m.a[i * Sm::kLf + j]) = make_float4(A[0], A[1], A[2], A[3]);
-      if constexpr (sizeof(E) == 2)
-        *reinterpret_cast<uint2*>(P + i * kC + j) =
-            make_uint2(pack_bf16(make_float2(p[0], p[1])), pack_bf16(make_float2(p[2], p[3])));
-      else
-        *reinterpret_cast<float4*>(P + i * kC + j) = make_float4(p[0], p[1], p[2], p[3]);
     }
+    // a lane's accumulators of one block of P are one word of its image
+#pragma unroll
+    for (int kb = 0; kb < TriTile<E>::kBlocks; ++kb)
+      if (16 * w >= kb * M::kDepth)
+        *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kT + TriTile<E>::word_at(kb, i, g)) =
+            pack_word<E>(p[kb * M::kTiles], p[(kb + 1) * M::kTiles - 1]);
     __syncthreads();
     // T = (I + A)^-1 by blocks of 16.  Wave w inverts diagonal block w by substitution, lane r its
     // column r: x_m = [m = r] - sum_{j < m} A_mj x_j.
@@ -175,42 +187,45 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
       for (int b = 0; b < 4; ++b) T[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        if (b == w) T[b] = F::ctile(&sm.d[w][0], 20, g, r);
+        if (b == w)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) T[b][x] = sm.d[w][(4 * g + x) * 20 + r];
         if (b > w) {
           f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < b; ++k)
-            if (k >= w) acc = F::mma(F::row(&sm.m.a[(16 * b + r) * Sm::kLf + 16 * k], g), T[k], acc);
+            if (k >= w) acc = F::mma(*reinterpret_cast<const f32x4*>(&sm.m.a[(16 * b + r) * Sm::kLf + 16 * k + 4 * g]), T[k], acc);
           f32x4 z = {0.f, 0.f, 0.f, 0.f};
-          T[b] = F::mma(F::row(&sm.d[b][r * 20], g), -acc, z);
+          T[b] = F::mma(*reinterpret_cast<const f32x4*>(&sm.d[b][r * 20 + 4 * g]), -acc, z);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) sm.m.t[(16 * b + 4 * g + x) * Sm::kLf + 16 * w + r] = T[b][x];
       }
     }
     __syncthreads();
-    {
-      const int row = tid >> 2, c = (tid & 3) * 16;
-      const float* t = &sm.m.t[row * Sm::kLf + c];
-      if constexpr (sizeof(E) == 4) {
-        float* T = reinterpret_cast<float*>(ws) + row * kC + c;
+    // the image of T: one word per turn
+    for (int x = tid; x < TriTile<E>::kRows * 4; x += 256) {
+      int kb = 0, t = x >> 2;
+      while (t >= kC - kb * M::kDepth) t -= kC - M::kDepth * kb++;
+      t += kb * M::kDepth;
+      const float* src = &sm.m.t[t * Sm::kLf + kb * M::kDepth + 4 * (x & 3)];
+      float lo[4], hi[4];
 #pragma unroll
-        for (int x = 0; x < 16; x += 4)
-          *reinterpret_cast<float4*>(T + x) = *reinterpret_cast<const float4*>(t + x);
-      } else {
-        uint32_t hi[8], lo[8];
+      for (int y = 0; y < 4; ++y) {
+        lo[y] = src[y];
+        hi[y] = sizeof(E) == 2 ? src[16 + y] : src[y];
+      }
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float2 f = make_float2(t[2 * x], t[2 * x + 1]);
-          hi[x] = pack_bf16(f);
-          const float2 h = unpack(hi[x]);
-          lo[x] = pack_bf16(make_float2(f.x - h.x, f.y - h.y));
+      for (int part = 0; part < M::kParts; ++part) {
+        const uint4 word = pack_word<E>(lo, hi);
+        *reinterpret_cast<uint4*>(ws + part * TriTile<E>::kBytes +
+                                  TriTile<E>::word_at(kb, t, x & 3)) = word;
+        if (sizeof(E) == 2) {
+          const float2 a0 = unpack(word.x), a1 = unpack(word.y), b0 = unpack(word.z),
+                       b1 = unpack(word.w);
+          lo[0] -= a0.x; lo[1] -= a0.y; lo[2] -= a1.x; lo[3] -= a1.y;
+          hi[0] -= b0.x; hi[1] -= b0.y; hi[2] -= b1.x; hi[3] -= b1.y;
         }
-        uint4* T = reinterpret_cast<uint4*>(ws) + (row * kC + c) / 8;
-        T[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        T[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-        T[kC * kC / 8] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        T[kC * kC / 8 + 1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
       }
     }
   }
@@ -218,33 +233,35 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
 
 // ------------------------------------------------------------------ the state through the chunks
 
-template <typename E, int DK, int NW>
-struct ScanSmem {
-  static constexpr int kLd = DK + Mma<E>::kPad;
-  static constexpr int kLt = kC + Mma<E>::kPad;
-  static constexpr int kLv = 16 * NW + Mma<E>::kPad;
-  static constexpr int kParts = Mma<E>::kParts;
-  E k[kC * kLd], q[kC * kLd], t[kParts][kC * kLt], p[kC * kLt], v[kC * kLv];
-  float eg[kC], c[kC];
+// One stage of a workgroup's LDS: the chunk's K and Q, the chunk's workspace image (T, P, gates) and V.
+template <typename E, int DK, int NW, int NC>
+struct Stage {
+  static constexpr int kK = 0;
+  static constexpr int kQ = KeyTile<E, DK>::kBytes;
+  static constexpr int kWs = 2 * KeyTile<E, DK>::kBytes;
+  static constexpr int kGate = kWs + ChunkWs<E>::kT + ChunkWs<E>::kP;
+  static constexpr int kVv = kWs + ChunkWs<E>::kBytes;
+  static constexpr int kVRow = 16 * NC * NW * (int)sizeof(E);
+  static constexpr int kBytes = kVv + kC * kVRow;
+  static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
 };
 
-template <typename E, int DK, int NW>
+template <typename E, int DK, int NW, int NC>
 __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_blocks) {
   using M = Mma<E>;
-  using Sm = ScanSmem<E, DK, NW>;
-  constexpr int kThreads = 64 * NW;
-  constexpr int kV = 16 / sizeof(E);       // values per 16-byte word
-  constexpr int kTPF = M::kDepth / 16;     // accumulator tiles per operand
-  constexpr int kWk = kC * DK / kV / kThreads, kWt = kC * kC / kV / kThreads;
-  constexpr int kWv = kC * 16 * NW / kV / kThreads;
-  __shared__ __align__(16) Sm sm;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, r = lane & 15;
+  using St = Stage<E, DK, NW, NC>;
+  using KT = KeyTile<E, DK>;
+  using TT = TriTile<E>;
+  constexpr int kV = 16 / sizeof(E);  // values per word
+  __shared__ __align__(1024) char smem[St::kCount * St::kBytes];
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t wg = placed_index(blockIdx.x, gridDim.x);
   const int64_t sh = wg / col_blocks;
   const int64_t seq = sh / a.hv;
   const int vh = (int)(sh - seq * a.hv), kh = vh / a.rep;
-  const int col0 = (int)(wg - sh * col_blocks) * 16 * NW;  // this workgroup's first column
-  const int col = col0 + 16 * w;                           // this wave's
+  const int col0 = (int)(wg - sh * col_blocks) * 16 * NC * NW;  // this workgroup's first column
+  const int col = col0 + 16 * NC * w;                        // this wave's
   const Span sp = seq_span(a, seq);
   const int64_t slot0 = slot_base(a, seq, sp.first);
   const E* kp = static_cast<const E*>(a.k) + sp.first * a.k_stride + (int64_t)kh * a.dk;
@@ -252,168 +269,231 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
   const E* vp = static_cast<const E*>(a.v) + sp.first * a.v_stride + (int64_t)vh * a.dv + col0;
   E* op = static_cast<E*>(a.out) + (sp.first * a.hv + vh) * (int64_t)a.dv + col;
   const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
-  const bool has_col = col + r < a.dv;
 
-  f32x4 S[DK / 16];
+  f32x4 S[NC][DK / 16];
 #pragma unroll
-  for (int m = 0; m < DK / 16; ++m)
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int row = 16 * m + 4 * g + x;
-      S[m][x] = a.s0 && has_col && row < a.dk ? a.s0[s_at + (int64_t)row * a.dv] : 0.f;
-    }
-
-  const int64_t nchunks = (sp.len + kC - 1) / kC;
-  uint4 rk[kWk], rq[kWk], rt[M::kParts][kWt], rp[kWt], rv[kWv];
-  float rg;
-  float eg_last = 0.f, eg_next;
-  auto load = [&](int64_t ch) {
-    const int n = (int)min((int64_t)kC, sp.len - ch * kC);
-    const E* k0 = kp + ch * kC * a.k_stride;
-    const E* q0 = qp + ch * kC * a.q_stride;
-    const E* v0 = vp + ch * kC * a.v_stride;
-    const char* ws = a.ws + ((slot0 + ch) * a.hv + vh) * (int64_t)ChunkWs<E>::kBytes;
-#pragma unroll
-    for (int i = 0; i < kWk; ++i) {
-      const int x = tid + i * kThreads, row = x / (DK / kV), c = x % (DK / kV) * kV;
-      rk[i] = tile_word(k0, a.k_stride, row, c, n, a.dk);
-      rq[i] = tile_word(q0, a.q_stride, row, c, n, a.dk);
-    }
-#pragma unroll
-    for (int i = 0; i < kWt; ++i) {
-#pragma unroll
-      for (int p = 0; p < M::kParts; ++p)
-        rt[p][i] = reinterpret_cast<const uint4*>(ws)[p * (kC * kC / kV) + tid + i * kThreads];
-      rp[i] = reinterpret_cast<const uint4*>(ws + ChunkWs<E>::kT)[tid + i * kThreads];
-    }
-#pragma unroll
-    for (int i = 0; i < kWv; ++i) {
-      const int x = tid + i * kThreads, row = x / (16 * NW / kV), c = x % (16 * NW / kV) * kV;
-      rv[i] = tile_word(v0, a.v_stride, row, c, n, a.dv - col0);
-    }
-    const float* gate = reinterpret_cast<const float*>(ws + ChunkWs<E>::kT + ChunkWs<E>::kP);
-    if (tid < 2 * kC) rg = gate[tid];
-    eg_next = gate[2 * kC];
-  };
-
-  if (nchunks > 0) load(0);
-  for (int64_t ch = 0; ch < nchunks; ++ch) {
-    __syncthreads();  // the previous chunk's tiles have been read
-#pragma unroll
-    for (int i = 0; i < kWk; ++i) {
-      const int x = tid + i * kThreads, at = x / (DK / kV) * Sm::kLd + x % (DK / kV) * kV;
-      *reinterpret_cast<uint4*>(&sm.k[at]) = rk[i];
-      *reinterpret_cast<uint4*>(&sm.q[at]) = rq[i];
-    }
-#pragma unroll
-    for (int i = 0; i < kWt; ++i) {
-      const int x = tid + i * kThreads, at = x / (kC / kV) * Sm::kLt + x % (kC / kV) * kV;
-#pragma unroll
-      for (int p = 0; p < M::kParts; ++p) *reinterpret_cast<uint4*>(&sm.t[p][at]) = rt[p][i];
-      *reinterpret_cast<uint4*>(&sm.p[at]) = rp[i];
-    }
-#pragma unroll
-    for (int i = 0; i < kWv; ++i) {
-      const int x = tid + i * kThreads, at = x / (16 * NW / kV) * Sm::kLv + x % (16 * NW / kV) * kV;
-      *reinterpret_cast<uint4*>(&sm.v[at]) = rv[i];
-    }
-    if (tid < kC) sm.eg[tid] = rg;
-    else if (tid < 2 * kC) sm.c[tid - kC] = rg;
-    eg_last = eg_next;
-    __syncthreads();
-    if (ch + 1 < nchunks) load(ch + 1);
-    const int n = (int)min((int64_t)kC, sp.len - ch * kC);
-
-    // K S (tokens x columns) and (Q S)^T (columns x tokens)
-    f32x4 y[4], o[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) y[m] = o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      const auto s = M::split(&S[kb * kTPF]);
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const auto kf = M::chain(&sm.k[(16 * m + r) * Sm::kLd + kb * M::kDepth], g);
-        const auto qf = M::chain(&sm.q[(16 * m + r) * Sm::kLd + kb * M::kDepth], g);
-#pragma unroll
-        for (int p = 0; p < M::kParts; ++p) y[m] = M::mma(kf, s.p[p], y[m]);
-        o[m] = M::mma(s.p[0], qf, o[m]);
-      }
-    }
-    // Y = V - diag(exp G) K S;  O scaled by its token's factor
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const f32x4 v = M::ctile(&sm.v[16 * m * Sm::kLv + 16 * w], Sm::kLv, g, r);
-      const f32x4 eg = *reinterpret_cast<const f32x4*>(&sm.eg[16 * m + 4 * g]);
-      const float so = a.scale * sm.eg[16 * m + r];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        y[m][x] = fmaf(-eg[x], y[m][x], v[x]);
-        o[m][x] *= so;
-      }
-    }
-    // E = T Y, T lower triangular
-    f32x4 e[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) e[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kb = 0; kb < kC / M::kDepth; ++kb) {
-      const auto ys = M::split(&y[kb * kTPF]);
-#pragma unroll
-      for (int m = kb * kTPF; m < 4; ++m) {
-        const auto th = M::chain(&sm.t[0][(16 * m + r) * Sm::kLt + kb * M::kDepth], g);
-        e[m] = M::mma(th, ys.p[0], e[m]);
-        if constexpr (M::kParts == 2) {
-          const auto tl = M::chain(&sm.t[1][(16 * m + r) * Sm::kLt + kb * M::kDepth], g);
-          e[m] = M::mma(th, ys.p[1], e[m]);
-          e[m] = M::mma(tl, ys.p[0], e[m]);
-        }
-      }
-    }
-    // O += P E, transposed: a lane ends with 4 consecutive columns of one token
-#pragma unroll
-    for (int kb = 0; kb < kC / M::kDepth; ++kb) {
-      const auto ef = M::pack(&e[kb * kTPF]);
-#pragma unroll
-      for (int m = kb * kTPF; m < 4; ++m)
-        o[m] = M::mma(ef, M::chain(&sm.p[(16 * m + r) * Sm::kLt + kb * M::kDepth], g), o[m]);
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int t = 16 * m + r;
-      if (t < n && col + 4 * g < a.dv) {
-        E* dst = op + (ch * kC + t) * (int64_t)a.hv * a.dv + 4 * g;
-        if constexpr (sizeof(E) == 2)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(make_float2(o[m][0], o[m][1])),
-                                                      pack_bf16(make_float2(o[m][2], o[m][3])));
-        else
-          *reinterpret_cast<f32x4*>(dst) = o[m];
-      }
-    }
-    // S = exp(G_64) S + K^T diag(c) E
-#pragma unroll
-    for (int m = 0; m < 4; ++m) e[m] *= *reinterpret_cast<const f32x4*>(&sm.c[16 * m + 4 * g]);
-#pragma unroll
-    for (int m = 0; m < DK / 16; ++m) S[m] *= eg_last;
-#pragma unroll
-    for (int kb = 0; kb < kC / M::kDepth; ++kb) {
-      const auto es = M::split(&e[kb * kTPF]);
-#pragma unroll
-      for (int m = 0; m < DK / 16; ++m) {
-        const auto kt = M::chain_t(&sm.k[kb * M::kDepth * Sm::kLd + 16 * m], Sm::kLd, g, r);
-#pragma unroll
-        for (int p = 0; p < M::kParts; ++p) S[m] = M::mma(kt, es.p[p], S[m]);
-      }
-    }
-  }
-  if (a.last && has_col) {
+  for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int row = 16 * m + 4 * g + x;
-        if (row < a.dk) a.last[s_at + (int64_t)row * a.dv] = S[m][x];
+        const int row = KT::value(m, g, x);
+        S[c][m][x] = a.s0 && col + 16 * c + r < a.dv && row < a.dk
+                         ? a.s0[s_at + (int64_t)row * a.dv + 16 * c] : 0.f;
       }
+
+  // Byte offsets of the words this lane copies: instruction j of a tile fills its j-th KB, wave w the
+  // instructions w, w + NW, ...
+  constexpr int kKI = KT::kBytes / 1024 / NW;
+  constexpr int kVI = kC * St::kVRow / 1024 / NW;
+  static_assert(kKI * NW * 1024 == KT::kBytes && kVI * NW * 1024 == kC * St::kVRow, "whole KBs");
+  uint32_t ok[kKI], oq[kKI], ov[kVI];
+#pragma unroll
+  for (int i = 0; i < kKI; ++i) {
+    const int at = (w + i * NW) * 64 + lane, t = at / KT::kWords;
+    const int c = ((at % KT::kWords) ^ KT::key(t)) * kV;
+    ok[i] = c < a.dk ? (uint32_t)(t * a.k_stride + c) * sizeof(E) : kOutside;
+    oq[i] = c < a.dk ? (uint32_t)(t * a.q_stride + c) * sizeof(E) : kOutside;
+  }
+#pragma unroll
+  for (int i = 0; i < kVI; ++i) {
+    const int at = (w + i * NW) * 64 + lane, t = at / (St::kVRow / 16);
+    const int c = at % (St::kVRow / 16) * kV;
+    ov[i] = c < a.dv - col0 ? (uint32_t)(t * a.v_stride + c) * sizeof(E) : kOutside;
+  }
+  const uint32_t lds0 = lds_address(smem);
+  const int64_t nchunks = (sp.len + kC - 1) / kC;
+  const int vcols = min(a.dv - col0, 16 * NC * NW);
+  // copies chunk ch into stage st; tokens past the sequence are past the buffers and read as zero
+  auto copy = [&](int64_t ch, int st) {
+    const int64_t n = min((int64_t)kC, sp.len - ch * kC);
+    const i32x4 bk = buffer_of(kp + ch * kC * a.k_stride,
+                               (uint32_t)(((n - 1) * a.k_stride + a.dk) * sizeof(E)));
+    const i32x4 bq = buffer_of(qp + ch * kC * a.q_stride,
+                               (uint32_t)(((n - 1) * a.q_stride + a.dk) * sizeof(E)));
+    const i32x4 bv = buffer_of(vp + ch * kC * a.v_stride,
+                               (uint32_t)(((n - 1) * a.v_stride + vcols) * sizeof(E)));
+    const i32x4 bw = buffer_of(a.ws + ((slot0 + ch) * a.hv + vh) * (int64_t)ChunkWs<E>::kBytes,
+                               ChunkWs<E>::kBytes);
+    const uint32_t to = lds0 + st * St::kBytes + w * 1024;
+#pragma unroll
+    for (int i = 0; i < kKI; ++i) copy_lds(bk, ok[i], to + St::kK + i * NW * 1024);
+#pragma unroll
+    for (int i = 0; i < kVI; ++i) copy_lds(bv, ov[i], to + St::kVv + i * NW * 1024);
+#pragma unroll
+    for (int i = 0; i < kKI; ++i) copy_lds(bq, oq[i], to + St::kQ + i * NW * 1024);
+#pragma unroll
+    for (int i = 0; i < (ChunkWs<E>::kBytes / 1024 + NW - 1) / NW; ++i)
+      if ((i + 1) * NW <= ChunkWs<E>::kBytes / 1024 || w + i * NW < ChunkWs<E>::kBytes / 1024)
+        copy_lds(bw, (w + i * NW) * 1024 + lane * 16, to + St::kWs + i * NW * 1024);
+  };
+
+  const KT kt(lane);
+  const TT tt(lane);
+  const int vrow = sizeof(E) == 2 ? (4 * g + (r >> 2)) * St::kVRow + 32 * NC * w + 8 * (r & 3)
+                                  : 4 * g * St::kVRow + (16 * NC * w + r) * 4;
+  if (nchunks > 0) copy(0, 0);
+  for (int64_t ch = 0; ch < nchunks; ++ch) {
+    const int st = St::kCount == 2 ? (int)(ch & 1) : 0;
+    copies_done();
+    // with two stages the next chunk is copied while this one is worked on
+    if (St::kCount == 2 && ch + 1 < nchunks) copy(ch + 1, st ^ 1);
+    const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
+    const int n = (int)min((int64_t)kC, sp.len - ch * kC);
+
+    // K S (tokens x columns) and (Q S)^T (columns x tokens)
+    f32x4 y[NC][4], o[NC][4];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) y[c][m] = o[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+      typename M::Parts s[NC];
+      typename M::Frag kf[4], qf[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        kf[m] = kt.rows(sm + St::kK, m, kb);
+        qf[m] = kt.rows(sm + St::kQ, m, kb);
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) s[c] = M::split(&S[c][kb * M::kTiles]);
+#pragma unroll
+      for (int p = 0; p < M::kParts; ++p)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) y[c][m] = M::mma(kf[m], s[c].p[p], y[c][m]);
+#pragma unroll
+      for (int p = 0; p < (M::kParts + 1) / 2; ++p)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) o[c][m] = M::mma(s[c].p[p], qf[m], o[c][m]);
+    }
+    // Y = V - diag(exp G) K S;  O scaled by its token's factor
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 eg = lds_read<f32x4>(sm + St::kGate + (16 * m + 4 * g) * 4);
+      const float so = a.scale * lds_read<float>(sm + St::kGate + (16 * m + r) * 4);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        f32x4 v;
+        const lds_ptr vt = sm + St::kVv + 16 * m * St::kVRow + 16 * c * (int)sizeof(E) + vrow;
+        if constexpr (sizeof(E) == 2) {
+          v = __builtin_convertvector(lds_tr(vt), f32x4);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[x] = lds_read<float>(vt + x * St::kVRow);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          y[c][m][x] = fmaf(-eg[x], y[c][m][x], v[x]);
+          o[c][m][x] *= so;
+        }
+      }
+    }
+    // E = T Y, T lower triangular; of the parts' products those above 2^-24
+    f32x4 e[NC][4];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < TT::kBlocks; ++kb) {
+      typename M::Parts ys[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) ys[c] = M::split(&y[c][kb * M::kTiles]);
+#pragma unroll
+      for (int p = 0; p < M::kParts; ++p) {
+        typename M::Frag tf[4];
+#pragma unroll
+        for (int m = kb * M::kTiles; m < 4; ++m) tf[m] = tt.rows(sm + St::kWs + p * TT::kBytes, m, kb);
+#pragma unroll
+        for (int x = 0; x + p < M::kParts; ++x)
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int m = kb * M::kTiles; m < 4; ++m) e[c][m] = M::mma(tf[m], ys[c].p[x], e[c][m]);
+      }
+    }
+    // O += P E, transposed: a lane ends with 4 consecutive columns of one token
+#pragma unroll
+    for (int kb = 0; kb < TT::kBlocks; ++kb) {
+      typename M::Parts es[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) es[c] = M::split(&e[c][kb * M::kTiles]);
+      typename M::Frag pf[4];
+#pragma unroll
+      for (int m = kb * M::kTiles; m < 4; ++m) pf[m] = tt.rows(sm + St::kWs + ChunkWs<E>::kT, m, kb);
+#pragma unroll
+      for (int p = 0; p < (M::kParts + 1) / 2; ++p)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int m = kb * M::kTiles; m < 4; ++m) o[c][m] = M::mma(es[c].p[p], pf[m], o[c][m]);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int t = 16 * m + r;
+        if (t < n && col + 16 * c + 4 * g < a.dv) {
+          E* dst = op + (ch * kC + t) * (int64_t)a.hv * a.dv + 16 * c + 4 * g;
+          if constexpr (sizeof(E) == 2)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16(make_float2(o[c][m][0], o[c][m][1])),
+                           pack_bf16(make_float2(o[c][m][2], o[c][m][3])));
+          else
+            *reinterpret_cast<f32x4*>(dst) = o[c][m];
+        }
+      }
+    // S = exp(G_64) S + K^T diag(c) E
+    const float last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 cj = lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) e[c][m] *= cj;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int m = 0; m < DK / 16; ++m) S[c][m] *= last;
+#pragma unroll
+    for (int kb = 0; kb < TT::kBlocks; ++kb) {
+      typename M::Parts es[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) es[c] = M::split(&e[c][kb * M::kTiles]);
+#pragma unroll
+      for (int m0 = 0; m0 < DK / 16; m0 += 4) {
+        typename M::Frag kf[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) kf[m] = kt.cols(sm + St::kK, m0 + m, kb);
+#pragma unroll
+        for (int p = 0; p < M::kParts; ++p)
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) S[c][m0 + m] = M::mma(kf[m], es[c].p[p], S[c][m0 + m]);
+      }
+    }
+    if (St::kCount == 1 && ch + 1 < nchunks) {
+      __syncthreads();  // every wave has read the stage
+      copy(ch + 1, 0);
+    }
+  }
+  if (a.last) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int m = 0; m < DK / 16; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = KT::value(m, g, x);
+          if (row < a.dk && col + 16 * c + r < a.dv)
+            a.last[s_at + (int64_t)row * a.dv + 16 * c] = S[c][m][x];
+        }
   }
 }
 
@@ -550,12 +630,17 @@ int launch_chunks_t(const Args& a, hipStream_t s) {
   return launch_status();
 }
 
-template <typename E, int DK, int NW>
+template <typename E, int DK, int NW, int NC>
 int launch_scan_t(const Args& a, hipStream_t s) {
-  const int cols = (a.dv + 16 * NW - 1) / (16 * NW);
-  hipLaunchKernelGGL((scan_kernel<E, DK, NW>), dim3((unsigned)(a.nseq * a.hv * cols)),
+  const int cols = (a.dv + 16 * NC * NW - 1) / (16 * NC * NW);
+  hipLaunchKernelGGL((scan_kernel<E, DK, NW, NC>), dim3((unsigned)(a.nseq * a.hv * cols)),
                      dim3(64 * NW), 0, s, a, cols);
   return launch_status();
+}
+
+template <typename E, int DK>
+int launch_scan_d(const Args& a, hipStream_t s) {
+  return a.dv <= 64 ? launch_scan_t<E, DK, 4, 1>(a, s) : launch_scan_t<E, DK, 8, 1>(a, s);
 }
 
 }  // namespace
@@ -598,8 +683,8 @@ int mamba_delta_fwd(const void* q, const void* k, const void* v, const void* g, 
   const bool bf = dims->io_dtype == MAMBA_BF16;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = launch_chunks(a, bf, s)) != MAMBA_OK) return st;
-  if (bf) return a.dk <= 64 ? launch_scan_t<uint16_t, 64, 4>(a, s) : launch_scan_t<uint16_t, 128, 4>(a, s);
-  return a.dk <= 64 ? launch_scan_t<float, 64, 4>(a, s) : launch_scan_t<float, 128, 4>(a, s);
+  if (bf) return a.dk <= 64 ? launch_scan_d<uint16_t, 64>(a, s) : launch_scan_d<uint16_t, 128>(a, s);
+  return a.dk <= 64 ? launch_scan_d<float, 64>(a, s) : launch_scan_d<float, 128>(a, s);
 }
 
 int mamba_delta_update(float* state, const void* q, const void* k, const void* v, const void* g,
