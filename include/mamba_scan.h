@@ -9,9 +9,9 @@
  *   mamba_state_update   one generation step for one new token per sequence;
  *   mamba_scan_bwd       the gradients of mamba_scan_fwd (training), recomputing the state.
  *
- *   mamba_delta_fwd, mamba_delta_update
+ *   mamba_delta_fwd, mamba_delta_update, mamba_delta_bwd
  *                        the gated delta rule, a recurrence of the same kind with a matrix state:
- *                        whole sequences, and one generation step.
+ *                        whole sequences, one generation step, and the gradients.
  *
  * Around them: the block's projections (mamba_gemm_bf16, mamba_block_fwd) and its norms
  * (mamba_gated_norm_*, mamba_add_norm_*).
@@ -329,8 +329,8 @@ typedef struct mamba_delta_dims {
 } mamba_delta_dims;
 
 /* Bytes of device workspace mamba_delta_fwd needs (0 for invalid dims); packed != 0: for a call with
- * seq_offsets.  Per 64 tokens and value head it holds two 64 x 64 matrices and the decays: 25 KB in
- * bf16, 33 KB in fp32. */
+ * seq_offsets.  Per 64 tokens and value head it holds two 64 x 64 matrices and the decays: 20 KB in
+ * bf16, 22 KB in fp32. */
 size_t mamba_delta_workspace_bytes(const mamba_delta_dims* dims, int packed);
 
 /*
@@ -364,6 +364,33 @@ int mamba_delta_fwd(const void* q, const void* k, const void* v, const void* g, 
 int mamba_delta_update(float* state, const void* q, const void* k, const void* v, const void* g,
                        const void* beta, float scale, void* out, const mamba_delta_dims* dims,
                        void* stream);
+
+/* Bytes of device workspace mamba_delta_bwd needs (0 for invalid dims); packed as for
+ * mamba_delta_workspace_bytes.  Beside the forward's it holds, per 64 tokens and value head, the state
+ * before them, its adjoint after them (both in io_dtype) and the e_t. */
+size_t mamba_delta_bwd_workspace_bytes(const mamba_delta_dims* dims, int packed);
+
+/*
+ * Gradients of mamba_delta_fwd (same inputs) for the loss sum(out * dout) + sum(last_state * dlast); the
+ * states are recomputed.
+ *   dout            : (batch, seqlen, v_heads, dv), io_dtype, contiguous
+ *   dlast           : (batch, v_heads, dk, dv) fp32, or NULL: zero
+ *   dq, dk          : (batch, seqlen, qk_heads, dk), io_dtype, contiguous: summed over the value heads
+ *                     that share the key head
+ *   dv              : (batch, seqlen, v_heads, dv), io_dtype, contiguous
+ *   dg, dbeta       : (batch, seqlen, v_heads), io_dtype, contiguous
+ *   dinitial_state  : (batch, v_heads, dk, dv) fp32, or NULL: not written (written also where
+ *                     initial_state is NULL: then it is the gradient at a zero state)
+ *   workspace       : >= mamba_delta_bwd_workspace_bytes bytes, 256-byte aligned
+ * Every output is overwritten; with seq_offsets, tokens that no sequence holds are not written.  Sums are
+ * taken in a fixed order (bitwise reproducible).  With bf16 storage dinitial_state carries the accuracy
+ * of bf16 products (about 2e-3 relative).
+ */
+int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                    const float* initial_state, const int64_t* seq_offsets, float scale,
+                    const void* dout, const float* dlast, void* dq, void* dk, void* dv, void* dg,
+                    void* dbeta, float* dinitial_state, const mamba_delta_dims* dims,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Sizes of the gated norm.  rows * groups is below 2^31, dim at most 16384 and groups at most 65535
  * (MAMBA_ERR_SHAPE otherwise). */

@@ -11,7 +11,8 @@ __all__ = ["mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
            "mamba_scan_workspace_bytes", "mamba_scan_bwd", "mamba_gemm_bf16",
            "mamba_block_fwd", "mamba_block_workspace_bytes", "mamba_scan_bwd_workspace_bytes", "mamba_status_string",
            "mamba_abi_version", "library_path",
-           "mamba_delta_fwd", "mamba_delta_update", "mamba_delta_workspace_bytes",
+           "mamba_delta_fwd", "mamba_delta_update", "mamba_delta_bwd",
+           "mamba_delta_workspace_bytes", "mamba_delta_bwd_workspace_bytes",
            "mamba_gated_norm_fwd", "mamba_gated_norm_bwd", "mamba_gated_norm_bwd_workspace_bytes",
            "mamba_add_norm_fwd", "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes"]
 

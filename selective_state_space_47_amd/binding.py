@@ -62,7 +62,8 @@ EXPORTS = ("mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
            "mamba_scan_workspace_bytes",
            "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes", "mamba_gemm_bf16",
            "mamba_block_fwd", "mamba_block_workspace_bytes", "mamba_delta_fwd",
-           "mamba_delta_workspace_bytes", "mamba_delta_update", "mamba_gated_norm_fwd",
+           "mamba_delta_workspace_bytes", "mamba_delta_update", "mamba_delta_bwd",
+           "mamba_delta_bwd_workspace_bytes", "mamba_gated_norm_fwd",
            "mamba_gated_norm_bwd", "mamba_gated_norm_bwd_workspace_bytes", "mamba_add_norm_fwd",
            "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes", "mamba_status_string",
            "mamba_abi_version")
@@ -126,6 +127,11 @@ def lib():
             L.mamba_delta_workspace_bytes.restype = sz
             L.mamba_delta_update.argtypes = [fp, vp, vp, vp, vp, vp, f32, vp, ep, vp]
             L.mamba_delta_update.restype = ctypes.c_int
+            L.mamba_delta_bwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, f32, vp, fp, vp, vp, vp, vp,
+                                          vp, fp, ep, vp, sz, vp]
+            L.mamba_delta_bwd.restype = ctypes.c_int
+            L.mamba_delta_bwd_workspace_bytes.argtypes = [ep, ctypes.c_int]
+            L.mamba_delta_bwd_workspace_bytes.restype = sz
             np_ = ctypes.POINTER(mamba_gated_norm_dims)
             L.mamba_gated_norm_fwd.argtypes = [vp, vp, fp, f32, vp, np_, vp]
             L.mamba_gated_norm_fwd.restype = ctypes.c_int
@@ -626,7 +632,7 @@ def _meta(t):
 
 
 def _delta_checked(q, k, v, g, beta, others, packed, n_seq, lead):
-    """Dims and workspace size of a call on these tensors; raises for tensors that do not belong
+    """Dims and workspace sizes (forward, backward) of a call on these tensors; raises for tensors that do not belong
     together.  `others`: (tensor or None, name, shape function of (batch, Hv, dk, dv), dtype or None
     for the io dtype)."""
     key = (_meta(q), _meta(k), _meta(v), _meta(g), _meta(beta),
@@ -665,7 +671,8 @@ def _delta_checked(q, k, v, g, beta, others, packed, n_seq, lead):
         _check(t, name, shape((batch, *tokens), Hk, Hv, dk, dv), dt or io, dev)
     dm = mamba_delta_dims(batch, L, Hk, Hv, dk, dv, _token_stride(q, "q", vec),
                           _token_stride(k, "k", vec), _token_stride(v, "v", vec), code, 0)
-    hit = (dm, int(lib().mamba_delta_workspace_bytes(ctypes.byref(dm), int(packed))))
+    hit = (dm, int(lib().mamba_delta_workspace_bytes(ctypes.byref(dm), int(packed))),
+           int(lib().mamba_delta_bwd_workspace_bytes(ctypes.byref(dm), int(packed))))
     if len(_DELTA_CACHE) >= 1024:
         _DELTA_CACHE.clear()
     _DELTA_CACHE[key] = hit
@@ -710,11 +717,11 @@ def mamba_delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, seq_offset
     """
     n_seq = _offsets_count(seq_offsets, q)
     packed = n_seq is not None
-    dm, ws_bytes = _delta_checked(q, k, v, g, beta,
-                                  ((initial_state, "initial_state", _state_shape, torch.float32),
-                                   (out, "out", _out_shape, None),
-                                   (last_state, "last_state", _state_shape, torch.float32)),
-                                  packed, n_seq, 1 if packed else 2)
+    dm, ws_bytes, _ = _delta_checked(q, k, v, g, beta,
+                                     ((initial_state, "initial_state", _state_shape, torch.float32),
+                                      (out, "out", _out_shape, None),
+                                      (last_state, "last_state", _state_shape, torch.float32)),
+                                     packed, n_seq, 1 if packed else 2)
     dev = q.device
     if out is None:
         out = torch.empty(v.shape, dtype=q.dtype, device=dev)
@@ -740,8 +747,8 @@ def mamba_delta_update(state, q, k, v, g, beta, scale=None, out=None):
     """
     if state is None:
         raise ValueError("state is required")
-    dm, _ = _delta_checked(q, k, v, g, beta, ((state, "state", _state_shape, torch.float32),
-                                              (out, "out", _out_shape, None)), False, None, 1)
+    dm = _delta_checked(q, k, v, g, beta, ((state, "state", _state_shape, torch.float32),
+                                           (out, "out", _out_shape, None)), False, None, 1)[0]
     dev = q.device
     if out is None:
         out = torch.empty(v.shape, dtype=q.dtype, device=dev)
@@ -751,6 +758,59 @@ def mamba_delta_update(state, q, k, v, g, beta, scale=None, out=None):
                                       ctypes.byref(dm), _stream(dev))
     _raise(st)
     return out
+
+
+def _qk_shape(n, Hk, Hv, dk, dv):
+    return (*n[1:], Hk, dk)
+
+
+def _head_shape(n, Hk, Hv, dk, dv):
+    return (*n[1:], Hv)
+
+
+def mamba_delta_bwd_workspace_bytes(dims: mamba_delta_dims, packed=False) -> int:
+    return int(lib().mamba_delta_bwd_workspace_bytes(ctypes.byref(dims), int(bool(packed))))
+
+
+def mamba_delta_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, seq_offsets=None,
+                    dlast=None, workspace=None, grads=None):
+    """Gradients of mamba_delta_fwd (mamba_delta_bwd in include/mamba_scan.h).
+
+    Same inputs as mamba_delta_fwd plus dout (like out) and optionally dlast (like last_state).
+    Returns a dict with dq, dk, dv, dg, dbeta (io dtype, contiguous) and dinitial_state (float32;
+    None when initial_state is None).  `grads` may hold preallocated output tensors under the same
+    keys.
+    """
+    if dout is None:
+        raise ValueError("dout is required")
+    n_seq = _offsets_count(seq_offsets, q)
+    packed = n_seq is not None
+    gr = dict(grads or {})
+    spec = (("dq", _qk_shape, None), ("dk", _qk_shape, None), ("dv", _out_shape, None),
+            ("dg", _head_shape, None), ("dbeta", _head_shape, None),
+            ("dinitial_state", _state_shape, torch.float32))
+    dm, _, ws_bytes = _delta_checked(
+        q, k, v, g, beta,
+        ((initial_state, "initial_state", _state_shape, torch.float32), (dout, "dout", _out_shape, None),
+         (dlast, "dlast", _state_shape, torch.float32),
+         *((gr.get(name), name, shape, dt) for name, shape, dt in spec)),
+        packed, n_seq, 1 if packed else 2)
+    dev = q.device
+    for name, like in (("dq", q), ("dk", q), ("dv", v), ("dg", g), ("dbeta", g),
+                       ("dinitial_state", initial_state)):
+        if gr.get(name) is None:
+            gr[name] = None if like is None else torch.empty(like.shape, dtype=like.dtype,
+                                                             device=dev)
+    workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
+    with _on(dev):
+        st = lib().mamba_delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                   _ptr(initial_state), _ptr(seq_offsets),
+                                   dm.dk ** -0.5 if scale is None else scale, _ptr(dout),
+                                   _ptr(dlast), _ptr(gr["dq"]), _ptr(gr["dk"]), _ptr(gr["dv"]),
+                                   _ptr(gr["dg"]), _ptr(gr["dbeta"]), _ptr(gr["dinitial_state"]),
+                                   ctypes.byref(dm), _ptr(workspace), ws_len, _stream(dev))
+    _raise(st)
+    return {n: gr[n] for n in ("dq", "dk", "dv", "dg", "dbeta", "dinitial_state")}
 
 
 # ---------------------------------------------------------------------------- norms of a block

@@ -35,7 +35,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // product are (converted in place) the operand of the next and nothing moves between lanes.
 //   kDepth  depth of one operand: kDepth / 16 accumulator tiles
 //   pack    accumulators -> operand
-//   split   accumulators -> operands that together hold the fp32 value (bf16: three, 8 bits each)
+//   split   accumulators -> P operands that together hold the value to 8 P bits (fp32: one, whole)
+//   parts   how many operands stand for a value of which P are wanted
 template <typename E>
 struct Mma;
 
@@ -43,9 +44,9 @@ template <>
 struct Mma<uint16_t> {
   static constexpr int kDepth = 32;
   static constexpr int kTiles = 2;
-  static constexpr int kParts = 3;
+  static constexpr int parts(int wanted) { return wanted; }
   using Frag = bf16x8;
-  struct Parts { Frag p[kParts]; };
+  template <int P> struct Parts { Frag p[P]; };
   __device__ static __forceinline__ Frag join(bf16x4 a, bf16x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
@@ -59,13 +60,14 @@ struct Mma<uint16_t> {
                                                pack_bf16(make_float2(c[1][0], c[1][1])),
                                                pack_bf16(make_float2(c[1][2], c[1][3]))));
   }
-  __device__ static __forceinline__ Parts split(const f32x4* c) {
+  template <int P>
+  __device__ static __forceinline__ Parts<P> split(const f32x4* c) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c[i >> 2][i & 3];
-    Parts s;
+    Parts<P> s;
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
+    for (int p = 0; p < P; ++p) {
       uint32_t h[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -84,9 +86,9 @@ template <>
 struct Mma<float> {
   static constexpr int kDepth = 16;
   static constexpr int kTiles = 1;
-  static constexpr int kParts = 1;
+  static constexpr int parts(int) { return 1; }
   using Frag = f32x4;
-  struct Parts { Frag p[kParts]; };
+  template <int P> struct Parts { Frag p[P]; };
   // four 4-deep fp32 instructions: step j takes element j of both operands (k = 4g + j)
   __device__ static __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
 #pragma unroll
@@ -94,7 +96,8 @@ struct Mma<float> {
     return c;
   }
   __device__ static __forceinline__ Frag pack(const f32x4* c) { return c[0]; }
-  __device__ static __forceinline__ Parts split(const f32x4* c) { return {{c[0]}}; }
+  template <int P>
+  __device__ static __forceinline__ Parts<P> split(const f32x4* c) { return {{c[0]}}; }
 };
 
 typedef __attribute__((address_space(3))) const char* lds_ptr;
@@ -137,11 +140,19 @@ struct KeyTile {
     return sizeof(E) == 2 ? 32 * (m >> 1) + 8 * g + 4 * (m & 1) + x : 16 * m + 4 * g + x;
   }
   // transposed operand: rows = values of accumulator tile m, k = tokens of block kb in accumulator
-  // order
+  // order, or (kNatural) in natural order
+  template <bool kNatural = false>
   __device__ __forceinline__ typename Mma<E>::Frag cols(lds_ptr t, int m, int kb) const {
     t += Mma<E>::kDepth * kb * kRow + tr0;
     if constexpr (sizeof(E) == 2) {
-      t += (((4 * (m >> 1) + (r & 3)) ^ key(4 * g + (r >> 2))) << 4) + 8 * (m & 1);
+      const int w = 4 * (m >> 1) + (r & 3), half = 8 * (m & 1);
+      if constexpr (kNatural) {
+        t += 4 * g * kRow + half;  // tokens 8 g .. instead of 4 g ..
+        const int row = 8 * g + (r >> 2);
+        return Mma<E>::join(lds_tr(t + ((w ^ key(row)) << 4)),
+                            lds_tr(t + 4 * kRow + ((w ^ key(row + 4)) << 4)));
+      }
+      t += ((w ^ key(4 * g + (r >> 2))) << 4) + half;
       return Mma<E>::join(lds_tr(t), lds_tr(t + 16 * kRow));
     } else {
       typename Mma<E>::Frag f;
@@ -150,6 +161,42 @@ struct KeyTile {
         f[j] = lds_read<float>(t + j * kRow + (((4 * m + (r >> 2)) ^ key(4 * g + j)) << 4));
       return f;
     }
+  }
+};
+
+// Rows of kCols values as they lie (values, output gradients: read in accumulator order, column by
+// column).
+template <typename E, int kCols>
+struct ValueTile {
+  static constexpr int kRow = kCols * (int)sizeof(E);
+  static constexpr int kWords = kRow / 16;
+  static constexpr int kBytes = kC * kRow;
+  __device__ static __forceinline__ int key(int) { return 0; }
+  int at, g;
+  // this wave's 16 columns begin at `col`
+  __device__ __forceinline__ ValueTile(int lane, int col) : g(lane >> 4) {
+    const int r = lane & 15;
+    at = sizeof(E) == 2 ? (4 * g + (r >> 2)) * kRow + 2 * col + 8 * (r & 3)
+                        : 4 * g * kRow + (col + r) * 4;
+  }
+  // rows (tokens) 16 m + 4 g .. +3 of column r, in storage type
+  __device__ __forceinline__ auto four(lds_ptr t, int m) const {
+    t += 16 * m * kRow + at;
+    if constexpr (sizeof(E) == 2)
+      return lds_tr(t);
+    else
+      return f32x4{lds_read<float>(t), lds_read<float>(t + kRow), lds_read<float>(t + 2 * kRow),
+                   lds_read<float>(t + 3 * kRow)};
+  }
+  __device__ __forceinline__ f32x4 tile(lds_ptr t, int m) const {
+    return __builtin_convertvector(four(t, m), f32x4);
+  }
+  // the operand of token block kb
+  __device__ __forceinline__ typename Mma<E>::Frag operand(lds_ptr t, int kb) const {
+    if constexpr (sizeof(E) == 2)
+      return Mma<E>::join(four(t, 2 * kb), four(t, 2 * kb + 1));
+    else
+      return four(t, kb);
   }
 };
 
@@ -177,6 +224,18 @@ struct TriTile {
   __device__ __forceinline__ typename Mma<E>::Frag rows(lds_ptr t, int m, int kb) const {
     return lds_read<typename Mma<E>::Frag>(t + row_at(kb, 16 * m) + row0);
   }
+  // transposed operand: rows = columns 16 m + r, k = rows of block ib (ib >= the block of column 16 m)
+  // in accumulator order
+  __device__ __forceinline__ typename Mma<E>::Frag cols(lds_ptr t, int m, int ib) const {
+    if constexpr (sizeof(E) == 2) {
+      t += row_at(m >> 1, 32 * ib) + (4 * g + (r >> 2)) * 64 + (((r & 3) ^ g) << 4) + 8 * (m & 1);
+      return Mma<E>::join(lds_tr(t), lds_tr(t + 16 * 64));
+    } else {
+      t += row_at(m, 16 * ib) + 4 * g * 64 + (((r >> 2) ^ g) << 4) + 4 * (r & 3);
+      return typename Mma<E>::Frag{lds_read<float>(t), lds_read<float>(t + 64),
+                                   lds_read<float>(t + 128), lds_read<float>(t + 192)};
+    }
+  }
 };
 
 // Copies from global memory straight into LDS, 16 bytes per lane and 1 KB per wave instruction:
@@ -193,6 +252,7 @@ __device__ __forceinline__ i32x4 buffer_of(const void* p, uint32_t bytes) {
   return d;
 }
 __device__ __forceinline__ void copy_lds(i32x4 buf, uint32_t off, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
   uint32_t saved;  // the compiler's m0
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
@@ -208,6 +268,41 @@ constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer
 // every copy of this wave has landed, and every wave of the workgroup has come here
 __device__ __forceinline__ void copies_done() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+// Copy of R rows of a key tile layout (rows of Tile::kRow bytes, swizzled) from rows in memory by NW
+// waves: instruction j fills the tile's j-th KB, wave w takes the instructions w, w + NW, ...
+template <typename E, typename Tile, int R, int NW>
+struct RowCopy {
+  static constexpr int kI = R * Tile::kRow / 1024 / NW;
+  static_assert(kI * NW * 1024 == R * Tile::kRow, "whole wave instructions");
+  uint32_t off[kI];
+  // `stride` elements between rows, `cols` values of a row that exist
+  __device__ __forceinline__ RowCopy(int w, int lane, int64_t stride, int cols) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const int at = (w + i * NW) * 64 + lane, t = at / Tile::kWords;
+      const int c = ((at % Tile::kWords) ^ Tile::key(t)) * (16 / (int)sizeof(E));
+      off[i] = c < cols ? (uint32_t)(t * stride + c) * (uint32_t)sizeof(E) : kOutside;
+    }
+  }
+  __device__ __forceinline__ void operator()(i32x4 buf, uint32_t lds, int w) const {
+#pragma unroll
+    for (int i = 0; i < kI; ++i) copy_lds(buf, off[i], lds + (w + i * NW) * 1024);
+  }
+};
+// rows of `cols` values, `n` of them, as a buffer
+template <typename E>
+__device__ __forceinline__ i32x4 rows_buffer(const E* p, int64_t n, int64_t stride, int cols) {
+  return buffer_of(p, (uint32_t)(((n - 1) * stride + cols) * (int64_t)sizeof(E)));
+}
+// kBytes (whole KBs) as they lie
+template <int kBytes, int NW>
+__device__ __forceinline__ void copy_linear(const void* p, uint32_t lds, int w, int lane) {
+  const i32x4 buf = buffer_of(p, kBytes);
+#pragma unroll
+  for (int i = 0; i < (kBytes / 1024 + NW - 1) / NW; ++i)
+    if ((i + 1) * NW <= kBytes / 1024 || w + i * NW < kBytes / 1024)
+      copy_lds(buf, (w + i * NW) * 1024 + lane * 16, lds + (w + i * NW) * 1024);
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return __builtin_amdgcn_readfirstlane(
@@ -229,7 +324,10 @@ struct Args {
   const int64_t* offsets;  // (nseq + 1) token offsets of packed sequences, or NULL
   void* out;               // (tokens, hv, dv)
   float* last;             // (nseq, hv, dk, dv) or NULL
-  char* ws;                // per (chunk slot, value head): T, P, gates
+  char* ws;                // per (chunk slot, value head): ChunkWs
+  char* e_img;             // backward only, per (chunk slot, value head): images of E,
+  char* s_img;             // of the state before the chunk
+  char* ds_img;            // and of the adjoint of the state after it
   int64_t q_stride, k_stride, v_stride;  // elements between tokens
   int64_t seqlen;          // tokens per sequence (packed: of all sequences)
   int64_t nseq;
@@ -269,14 +367,19 @@ __device__ __forceinline__ int64_t slot_seq(const Args& a, int64_t slot) {
   return lo;
 }
 
-// Workspace of one chunk and value head: T (in kParts parts), P, then 256 floats of gates:
-// exp(G_i) (64), c_j (64), exp(G_64), 63 unused.
+// Parts of T that the forward uses and the workspace holds: T is unit on its diagonal and small off
+// it, so that two parts leave an error of 2^-18 of the small entries.
+constexpr int kTParts = 2;
+
+// Workspace of one chunk and value head: T (in parts), P, then floats: exp(G_i) (64), c_j (64),
+// exp(G_64) and 127 unused, G_i as two floats (64 + 64), beta (64), 64 unused.
 template <typename E>
 struct ChunkWs {
-  static constexpr int kT = Mma<E>::kParts * TriTile<E>::kBytes;
+  static constexpr int kT = Mma<E>::parts(kTParts) * TriTile<E>::kBytes;
   static constexpr int kP = TriTile<E>::kBytes;
-  static constexpr int kGate = 1024;
-  static constexpr int kBytes = kT + kP + kGate;
+  static constexpr int kGate = kT + kP;        // what the scan reads: 1 KB
+  static constexpr int kDecay = kGate + 1024;  // what only the gradients read: 1 KB
+  static constexpr int kBytes = kDecay + 1024;
   static_assert(kBytes % 1024 == 0, "copied in whole wave instructions");
 };
 
@@ -353,8 +456,21 @@ inline int check_delta_inputs(const mamba_delta_dims* d, const void* q, const vo
   return MAMBA_OK;
 }
 
+// What the backward keeps of one chunk and value head beside ChunkWs, as images of LDS tiles in blocks
+// of kDB columns of the state (dv is padded to whole blocks): E (in parts; tokens x columns), the state
+// before the chunk and the adjoint of the state after it (columns x dk).
+template <typename E>
+struct BwdBlock {
+  static constexpr int kDB = sizeof(E) == 2 ? 64 : 32;
+  static constexpr int kEParts = Mma<E>::parts(2);
+  static constexpr int kE = kC * kDB * (int)sizeof(E);  // bytes of one part
+  static int64_t blocks(int64_t dv) { return (dv + kDB - 1) / kDB; }
+};
+
 // Launches the chunk products (T, P and gates of every chunk and value head) into a.ws.
 __attribute__((visibility("hidden"))) int launch_chunks(const Args& a, bool bf, hipStream_t s);
+// Launches the state pass of the backward: E and the states before every chunk into a.e_img, a.s_img.
+__attribute__((visibility("hidden"))) int launch_states(const Args& a, bool bf, hipStream_t s);
 
 }  // namespace delta
 }  // namespace mamba

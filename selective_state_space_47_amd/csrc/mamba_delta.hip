@@ -132,10 +132,14 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
       sm.ghi[lane] = hi;
       sm.glo[lane] = (float)(G - (double)hi);
       sm.beta[lane] = bt;
-      float* gate = reinterpret_cast<float*>(ws + ChunkWs<E>::kT + ChunkWs<E>::kP);
+      float* gate = reinterpret_cast<float*>(ws + ChunkWs<E>::kGate);
       gate[lane] = exp_f32(hi);
       gate[kC + lane] = exp_f32((float)(total - G)) * bt;
       if (lane == 0) gate[2 * kC] = exp_f32((float)total);
+      float* decay = reinterpret_cast<float*>(ws + ChunkWs<E>::kDecay);
+      decay[lane] = hi;
+      decay[kC + lane] = sm.glo[lane];
+      decay[2 * kC + lane] = bt;
     }
     __syncthreads();
     const float gi = sm.ghi[i], gil = sm.glo[i];
@@ -216,7 +220,7 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
         hi[y] = sizeof(E) == 2 ? src[16 + y] : src[y];
       }
 #pragma unroll
-      for (int part = 0; part < M::kParts; ++part) {
+      for (int part = 0; part < M::parts(kTParts); ++part) {
         const uint4 word = pack_word<E>(lo, hi);
         *reinterpret_cast<uint4*>(ws + part * TriTile<E>::kBytes +
                                   TriTile<E>::word_at(kb, t, x & 3)) = word;
@@ -234,25 +238,31 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
 // ------------------------------------------------------------------ the state through the chunks
 
 // One stage of a workgroup's LDS: the chunk's K and Q, the chunk's workspace image (T, P, gates) and V.
-template <typename E, int DK, int NW, int NC>
+template <typename E, int DK, int NW>
 struct Stage {
   static constexpr int kK = 0;
   static constexpr int kQ = KeyTile<E, DK>::kBytes;
   static constexpr int kWs = 2 * KeyTile<E, DK>::kBytes;
-  static constexpr int kGate = kWs + ChunkWs<E>::kT + ChunkWs<E>::kP;
-  static constexpr int kVv = kWs + ChunkWs<E>::kBytes;
-  static constexpr int kVRow = 16 * NC * NW * (int)sizeof(E);
-  static constexpr int kBytes = kVv + kC * kVRow;
+  static constexpr int kWsBytes = ChunkWs<E>::kDecay;
+  static constexpr int kGate = kWs + ChunkWs<E>::kGate;
+  static constexpr int kVv = kWs + kWsBytes;
+  static constexpr int kBytes = kVv + ValueTile<E, 16 * NW>::kBytes;
   static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
 };
 
-template <typename E, int DK, int NW, int NC>
+// kStates: the backward's pass, which leaves E and the state before each chunk instead of the output.
+// Its results only enter gradients that are rounded to the storage type, so that with bf16 storage one
+// part of each factor is enough, two of Y (whose rounding alone would be as large as the gradients').
+template <typename E, int DK, int NW, bool kStates>
 __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_blocks) {
   using M = Mma<E>;
-  using St = Stage<E, DK, NW, NC>;
+  using St = Stage<E, DK, NW>;
   using KT = KeyTile<E, DK>;
   using TT = TriTile<E>;
-  constexpr int kV = 16 / sizeof(E);  // values per word
+  using VT = ValueTile<E, 16 * NW>;
+  constexpr int kPS = M::parts(kStates ? 1 : 3), kPT = M::parts(kStates ? 1 : kTParts);
+  constexpr int kPY = M::parts(kStates ? 2 : 3), kPE = M::parts(kStates ? 1 : 3);
+  constexpr int kPO = M::parts(2);  // of S and E in the output
   __shared__ __align__(1024) char smem[St::kCount * St::kBytes];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -260,8 +270,8 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
   const int64_t sh = wg / col_blocks;
   const int64_t seq = sh / a.hv;
   const int vh = (int)(sh - seq * a.hv), kh = vh / a.rep;
-  const int col0 = (int)(wg - sh * col_blocks) * 16 * NC * NW;  // this workgroup's first column
-  const int col = col0 + 16 * NC * w;                        // this wave's
+  const int col0 = (int)(wg - sh * col_blocks) * 16 * NW;  // this workgroup's first column
+  const int col = col0 + 16 * w;                           // this wave's
   const Span sp = seq_span(a, seq);
   const int64_t slot0 = slot_base(a, seq, sp.first);
   const E* kp = static_cast<const E*>(a.k) + sp.first * a.k_stride + (int64_t)kh * a.dk;
@@ -269,69 +279,40 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
   const E* vp = static_cast<const E*>(a.v) + sp.first * a.v_stride + (int64_t)vh * a.dv + col0;
   E* op = static_cast<E*>(a.out) + (sp.first * a.hv + vh) * (int64_t)a.dv + col;
   const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
+  const bool has_col = col + r < a.dv;
 
-  f32x4 S[NC][DK / 16];
+  f32x4 S[DK / 16];
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
+  for (int m = 0; m < DK / 16; ++m)
 #pragma unroll
-    for (int m = 0; m < DK / 16; ++m)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = KT::value(m, g, x);
-        S[c][m][x] = a.s0 && col + 16 * c + r < a.dv && row < a.dk
-                         ? a.s0[s_at + (int64_t)row * a.dv + 16 * c] : 0.f;
-      }
+    for (int x = 0; x < 4; ++x) {
+      const int row = KT::value(m, g, x);
+      S[m][x] = a.s0 && has_col && row < a.dk ? a.s0[s_at + (int64_t)row * a.dv] : 0.f;
+    }
 
-  // Byte offsets of the words this lane copies: instruction j of a tile fills its j-th KB, wave w the
-  // instructions w, w + NW, ...
-  constexpr int kKI = KT::kBytes / 1024 / NW;
-  constexpr int kVI = kC * St::kVRow / 1024 / NW;
-  static_assert(kKI * NW * 1024 == KT::kBytes && kVI * NW * 1024 == kC * St::kVRow, "whole KBs");
-  uint32_t ok[kKI], oq[kKI], ov[kVI];
-#pragma unroll
-  for (int i = 0; i < kKI; ++i) {
-    const int at = (w + i * NW) * 64 + lane, t = at / KT::kWords;
-    const int c = ((at % KT::kWords) ^ KT::key(t)) * kV;
-    ok[i] = c < a.dk ? (uint32_t)(t * a.k_stride + c) * sizeof(E) : kOutside;
-    oq[i] = c < a.dk ? (uint32_t)(t * a.q_stride + c) * sizeof(E) : kOutside;
-  }
-#pragma unroll
-  for (int i = 0; i < kVI; ++i) {
-    const int at = (w + i * NW) * 64 + lane, t = at / (St::kVRow / 16);
-    const int c = at % (St::kVRow / 16) * kV;
-    ov[i] = c < a.dv - col0 ? (uint32_t)(t * a.v_stride + c) * sizeof(E) : kOutside;
-  }
   const uint32_t lds0 = lds_address(smem);
   const int64_t nchunks = (sp.len + kC - 1) / kC;
-  const int vcols = min(a.dv - col0, 16 * NC * NW);
+  const int vcols = min(a.dv - col0, 16 * NW);
+  const RowCopy<E, KT, kC, NW> ck(w, lane, a.k_stride, a.dk), cq(w, lane, a.q_stride, a.dk);
+  const RowCopy<E, VT, kC, NW> cv(w, lane, a.v_stride, vcols);
   // copies chunk ch into stage st; tokens past the sequence are past the buffers and read as zero
   auto copy = [&](int64_t ch, int st) {
-    const int64_t n = min((int64_t)kC, sp.len - ch * kC);
-    const i32x4 bk = buffer_of(kp + ch * kC * a.k_stride,
-                               (uint32_t)(((n - 1) * a.k_stride + a.dk) * sizeof(E)));
-    const i32x4 bq = buffer_of(qp + ch * kC * a.q_stride,
-                               (uint32_t)(((n - 1) * a.q_stride + a.dk) * sizeof(E)));
-    const i32x4 bv = buffer_of(vp + ch * kC * a.v_stride,
-                               (uint32_t)(((n - 1) * a.v_stride + vcols) * sizeof(E)));
-    const i32x4 bw = buffer_of(a.ws + ((slot0 + ch) * a.hv + vh) * (int64_t)ChunkWs<E>::kBytes,
-                               ChunkWs<E>::kBytes);
-    const uint32_t to = lds0 + st * St::kBytes + w * 1024;
-#pragma unroll
-    for (int i = 0; i < kKI; ++i) copy_lds(bk, ok[i], to + St::kK + i * NW * 1024);
-#pragma unroll
-    for (int i = 0; i < kVI; ++i) copy_lds(bv, ov[i], to + St::kVv + i * NW * 1024);
-#pragma unroll
-    for (int i = 0; i < kKI; ++i) copy_lds(bq, oq[i], to + St::kQ + i * NW * 1024);
-#pragma unroll
-    for (int i = 0; i < (ChunkWs<E>::kBytes / 1024 + NW - 1) / NW; ++i)
-      if ((i + 1) * NW <= ChunkWs<E>::kBytes / 1024 || w + i * NW < ChunkWs<E>::kBytes / 1024)
-        copy_lds(bw, (w + i * NW) * 1024 + lane * 16, to + St::kWs + i * NW * 1024);
+    const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
+    const uint32_t to = lds0 + st * St::kBytes;
+    ck(rows_buffer(kp + t * a.k_stride, n, a.k_stride, a.dk), to + St::kK, w);
+    cv(rows_buffer(vp + t * a.v_stride, n, a.v_stride, vcols), to + St::kVv, w);
+    if (!kStates) cq(rows_buffer(qp + t * a.q_stride, n, a.q_stride, a.dk), to + St::kQ, w);
+    copy_linear<St::kWsBytes, NW>(a.ws + ((slot0 + ch) * a.hv + vh) * (int64_t)ChunkWs<E>::kBytes,
+                                  to + St::kWs, w, lane);
   };
 
+  // bytes of the backward's images of one chunk and value head
+  const int dv_pad = (a.dv + BwdBlock<E>::kDB - 1) / BwdBlock<E>::kDB * BwdBlock<E>::kDB;
+  const int64_t img_bytes = (int64_t)dv_pad * KT::kRow;
+  const int64_t e_bytes = (int64_t)dv_pad * kC * sizeof(E) * BwdBlock<E>::kEParts;
   const KT kt(lane);
   const TT tt(lane);
-  const int vrow = sizeof(E) == 2 ? (4 * g + (r >> 2)) * St::kVRow + 32 * NC * w + 8 * (r & 3)
-                                  : 4 * g * St::kVRow + (16 * NC * w + r) * 4;
+  const VT vt(lane, 16 * w);
   if (nchunks > 0) copy(0, 0);
   for (int64_t ch = 0; ch < nchunks; ++ch) {
     const int st = St::kCount == 2 ? (int)(ch & 1) : 0;
@@ -341,141 +322,145 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
     const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
     const int n = (int)min((int64_t)kC, sp.len - ch * kC);
 
+    if constexpr (kStates) {
+      // the state before the chunk: 16 bytes of one column per operand
+      char* img = a.s_img + ((slot0 + ch) * a.hv + vh) * img_bytes;
+#pragma unroll
+      for (int kb = 0; kb < DK / M::kDepth; ++kb)
+        if (col + r < dv_pad)
+          *reinterpret_cast<typename M::Frag*>(img + (int64_t)(col + r) * KT::kRow +
+                                               (((4 * kb + g) ^ KT::key(col + r)) << 4)) =
+              M::pack(&S[kb * M::kTiles]);
+    }
     // K S (tokens x columns) and (Q S)^T (columns x tokens)
-    f32x4 y[NC][4], o[NC][4];
+    f32x4 y[4], o[4];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int m = 0; m < 4; ++m) y[c][m] = o[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < 4; ++m) y[m] = o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      typename M::Parts s[NC];
+      const auto s = M::template split<kPS>(&S[kb * M::kTiles]);
       typename M::Frag kf[4], qf[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         kf[m] = kt.rows(sm + St::kK, m, kb);
-        qf[m] = kt.rows(sm + St::kQ, m, kb);
+        if (!kStates) qf[m] = kt.rows(sm + St::kQ, m, kb);
       }
 #pragma unroll
-      for (int c = 0; c < NC; ++c) s[c] = M::split(&S[c][kb * M::kTiles]);
+      for (int p = 0; p < kPS; ++p)
 #pragma unroll
-      for (int p = 0; p < M::kParts; ++p)
+        for (int m = 0; m < 4; ++m) y[m] = M::mma(kf[m], s.p[p], y[m]);
+      if constexpr (!kStates) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int p = 0; p < kPO; ++p)
 #pragma unroll
-          for (int m = 0; m < 4; ++m) y[c][m] = M::mma(kf[m], s[c].p[p], y[c][m]);
-#pragma unroll
-      for (int p = 0; p < (M::kParts + 1) / 2; ++p)
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) o[c][m] = M::mma(s[c].p[p], qf[m], o[c][m]);
+          for (int m = 0; m < 4; ++m) o[m] = M::mma(s.p[p], qf[m], o[m]);
+      }
     }
     // Y = V - diag(exp G) K S;  O scaled by its token's factor
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
+      const f32x4 v = vt.tile(sm + St::kVv, m);
       const f32x4 eg = lds_read<f32x4>(sm + St::kGate + (16 * m + 4 * g) * 4);
       const float so = a.scale * lds_read<float>(sm + St::kGate + (16 * m + r) * 4);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        f32x4 v;
-        const lds_ptr vt = sm + St::kVv + 16 * m * St::kVRow + 16 * c * (int)sizeof(E) + vrow;
-        if constexpr (sizeof(E) == 2) {
-          v = __builtin_convertvector(lds_tr(vt), f32x4);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) v[x] = lds_read<float>(vt + x * St::kVRow);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          y[c][m][x] = fmaf(-eg[x], y[c][m][x], v[x]);
-          o[c][m][x] *= so;
-        }
+      for (int x = 0; x < 4; ++x) {
+        y[m][x] = fmaf(-eg[x], y[m][x], v[x]);
+        if (!kStates) o[m][x] *= so;
       }
     }
-    // E = T Y, T lower triangular; of the parts' products those above 2^-24
-    f32x4 e[NC][4];
+    // E = T Y, T lower triangular; of the parts' products those above 2^-24.  The state pass also
+    // makes it transposed, to store it row by row.
+    f32x4 e[4], et[4];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int m = 0; m < 4; ++m) e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < 4; ++m) e[m] = et[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < TT::kBlocks; ++kb) {
-      typename M::Parts ys[NC];
+      const auto ys = M::template split<kPY>(&y[kb * M::kTiles]);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) ys[c] = M::split(&y[c][kb * M::kTiles]);
-#pragma unroll
-      for (int p = 0; p < M::kParts; ++p) {
+      for (int p = 0; p < kPT; ++p) {
         typename M::Frag tf[4];
 #pragma unroll
         for (int m = kb * M::kTiles; m < 4; ++m) tf[m] = tt.rows(sm + St::kWs + p * TT::kBytes, m, kb);
 #pragma unroll
-        for (int x = 0; x + p < M::kParts; ++x)
+        for (int x = 0; x < kPY && x + p < 3; ++x)
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int m = kb * M::kTiles; m < 4; ++m) e[c][m] = M::mma(tf[m], ys[c].p[x], e[c][m]);
+          for (int m = kb * M::kTiles; m < 4; ++m) {
+            e[m] = M::mma(tf[m], ys.p[x], e[m]);
+            if (kStates) et[m] = M::mma(ys.p[x], tf[m], et[m]);
+          }
       }
     }
-    // O += P E, transposed: a lane ends with 4 consecutive columns of one token
+    if constexpr (kStates) {
+      // token 16 m + r, columns col + 4 g .. +3 of the image of E
+      if (col + 4 * g < dv_pad) {
+        using ET = KeyTile<E, BwdBlock<E>::kDB>;
+        constexpr int kDB = BwdBlock<E>::kDB;
+        const int cw = (col + 4 * g) % kDB * (int)sizeof(E);  // byte in the block's rows
+        char* img = a.e_img + ((slot0 + ch) * a.hv + vh) * e_bytes +
+                    (int64_t)((col + 4 * g) / kDB) * BwdBlock<E>::kEParts * BwdBlock<E>::kE;
 #pragma unroll
-    for (int kb = 0; kb < TT::kBlocks; ++kb) {
-      typename M::Parts es[NC];
+        for (int m = 0; m < 4; ++m) {
+          const int t = 16 * m + r;
+          char* to = img + t * ET::kRow + (((cw >> 4) ^ ET::key(t)) << 4) + (cw & 15);
+          if constexpr (sizeof(E) == 2) {
+            const uint32_t h0 = pack_bf16(make_float2(et[m][0], et[m][1]));
+            const uint32_t h1 = pack_bf16(make_float2(et[m][2], et[m][3]));
+            const float2 f0 = unpack(h0), f1 = unpack(h1);
+            *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
+            *reinterpret_cast<uint2*>(to + BwdBlock<E>::kE) =
+                make_uint2(pack_bf16(make_float2(et[m][0] - f0.x, et[m][1] - f0.y)),
+                           pack_bf16(make_float2(et[m][2] - f1.x, et[m][3] - f1.y)));
+          } else {
+            *reinterpret_cast<f32x4*>(to) = et[m];
+          }
+        }
+      }
+    } else {
+      // O += P E, transposed: a lane ends with 4 consecutive columns of one token
 #pragma unroll
-      for (int c = 0; c < NC; ++c) es[c] = M::split(&e[c][kb * M::kTiles]);
-      typename M::Frag pf[4];
+      for (int kb = 0; kb < TT::kBlocks; ++kb) {
+        const auto es = M::template split<kPO>(&e[kb * M::kTiles]);
+        typename M::Frag pf[4];
 #pragma unroll
-      for (int m = kb * M::kTiles; m < 4; ++m) pf[m] = tt.rows(sm + St::kWs + ChunkWs<E>::kT, m, kb);
+        for (int m = kb * M::kTiles; m < 4; ++m)
+          pf[m] = tt.rows(sm + St::kWs + ChunkWs<E>::kT, m, kb);
 #pragma unroll
-      for (int p = 0; p < (M::kParts + 1) / 2; ++p)
+        for (int p = 0; p < kPO; ++p)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int m = kb * M::kTiles; m < 4; ++m) o[c][m] = M::mma(es[c].p[p], pf[m], o[c][m]);
-    }
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
+          for (int m = kb * M::kTiles; m < 4; ++m) o[m] = M::mma(es.p[p], pf[m], o[m]);
+      }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int t = 16 * m + r;
-        if (t < n && col + 16 * c + 4 * g < a.dv) {
-          E* dst = op + (ch * kC + t) * (int64_t)a.hv * a.dv + 16 * c + 4 * g;
+        if (t < n && col + 4 * g < a.dv) {
+          E* dst = op + (ch * kC + t) * (int64_t)a.hv * a.dv + 4 * g;
           if constexpr (sizeof(E) == 2)
             *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16(make_float2(o[c][m][0], o[c][m][1])),
-                           pack_bf16(make_float2(o[c][m][2], o[c][m][3])));
+                make_uint2(pack_bf16(make_float2(o[m][0], o[m][1])),
+                           pack_bf16(make_float2(o[m][2], o[m][3])));
           else
-            *reinterpret_cast<f32x4*>(dst) = o[c][m];
+            *reinterpret_cast<f32x4*>(dst) = o[m];
         }
       }
+    }
     // S = exp(G_64) S + K^T diag(c) E
+#pragma unroll
+    for (int m = 0; m < 4; ++m) e[m] *= lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
     const float last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const f32x4 cj = lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) e[c][m] *= cj;
-    }
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int m = 0; m < DK / 16; ++m) S[c][m] *= last;
+    for (int m = 0; m < DK / 16; ++m) S[m] *= last;
 #pragma unroll
     for (int kb = 0; kb < TT::kBlocks; ++kb) {
-      typename M::Parts es[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) es[c] = M::split(&e[c][kb * M::kTiles]);
+      const auto es = M::template split<kPE>(&e[kb * M::kTiles]);
 #pragma unroll
       for (int m0 = 0; m0 < DK / 16; m0 += 4) {
         typename M::Frag kf[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) kf[m] = kt.cols(sm + St::kK, m0 + m, kb);
 #pragma unroll
-        for (int p = 0; p < M::kParts; ++p)
+        for (int p = 0; p < kPE; ++p)
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) S[c][m0 + m] = M::mma(kf[m], es[c].p[p], S[c][m0 + m]);
+          for (int m = 0; m < 4; ++m) S[m0 + m] = M::mma(kf[m], es.p[p], S[m0 + m]);
       }
     }
     if (St::kCount == 1 && ch + 1 < nchunks) {
@@ -483,17 +468,14 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
       copy(ch + 1, 0);
     }
   }
-  if (a.last) {
+  if (!kStates && a.last && has_col) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int m = 0; m < DK / 16; ++m)
 #pragma unroll
-      for (int m = 0; m < DK / 16; ++m)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = KT::value(m, g, x);
-          if (row < a.dk && col + 16 * c + r < a.dv)
-            a.last[s_at + (int64_t)row * a.dv + 16 * c] = S[c][m][x];
-        }
+      for (int x = 0; x < 4; ++x) {
+        const int row = KT::value(m, g, x);
+        if (row < a.dk) a.last[s_at + (int64_t)row * a.dv] = S[m][x];
+      }
   }
 }
 
@@ -630,17 +612,19 @@ int launch_chunks_t(const Args& a, hipStream_t s) {
   return launch_status();
 }
 
-template <typename E, int DK, int NW, int NC>
+template <typename E, int DK, int NW, bool kStates>
 int launch_scan_t(const Args& a, hipStream_t s) {
-  const int cols = (a.dv + 16 * NC * NW - 1) / (16 * NC * NW);
-  hipLaunchKernelGGL((scan_kernel<E, DK, NW, NC>), dim3((unsigned)(a.nseq * a.hv * cols)),
+  const int cols = (a.dv + 16 * NW - 1) / (16 * NW);
+  hipLaunchKernelGGL((scan_kernel<E, DK, NW, kStates>), dim3((unsigned)(a.nseq * a.hv * cols)),
                      dim3(64 * NW), 0, s, a, cols);
   return launch_status();
 }
 
-template <typename E, int DK>
-int launch_scan_d(const Args& a, hipStream_t s) {
-  return a.dv <= 64 ? launch_scan_t<E, DK, 4, 1>(a, s) : launch_scan_t<E, DK, 8, 1>(a, s);
+template <typename E, bool kStates>
+int launch_scan(const Args& a, hipStream_t s) {
+  if (a.dk <= 64)
+    return a.dv <= 64 ? launch_scan_t<E, 64, 4, kStates>(a, s) : launch_scan_t<E, 64, 8, kStates>(a, s);
+  return a.dv <= 64 ? launch_scan_t<E, 128, 4, kStates>(a, s) : launch_scan_t<E, 128, 8, kStates>(a, s);
 }
 
 }  // namespace
@@ -648,6 +632,10 @@ int launch_scan_d(const Args& a, hipStream_t s) {
 int launch_chunks(const Args& a, bool bf, hipStream_t s) {
   if (bf) return a.dk <= 64 ? launch_chunks_t<uint16_t, 64>(a, s) : launch_chunks_t<uint16_t, 128>(a, s);
   return a.dk <= 64 ? launch_chunks_t<float, 64>(a, s) : launch_chunks_t<float, 128>(a, s);
+}
+
+int launch_states(const Args& a, bool bf, hipStream_t s) {
+  return bf ? launch_scan<uint16_t, true>(a, s) : launch_scan<float, true>(a, s);
 }
 
 }  // namespace delta
@@ -683,8 +671,7 @@ int mamba_delta_fwd(const void* q, const void* k, const void* v, const void* g, 
   const bool bf = dims->io_dtype == MAMBA_BF16;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = launch_chunks(a, bf, s)) != MAMBA_OK) return st;
-  if (bf) return a.dk <= 64 ? launch_scan_d<uint16_t, 64>(a, s) : launch_scan_d<uint16_t, 128>(a, s);
-  return a.dk <= 64 ? launch_scan_d<float, 64>(a, s) : launch_scan_d<float, 128>(a, s);
+  return bf ? launch_scan<uint16_t, false>(a, s) : launch_scan<float, false>(a, s);
 }
 
 int mamba_delta_update(float* state, const void* q, const void* k, const void* v, const void* g,

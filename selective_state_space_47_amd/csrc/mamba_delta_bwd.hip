@@ -1,0 +1,610 @@
+// mamba_delta_bwd.hip -- gradients of the gated delta rule on gfx950.
+//
+// In chunks (mamba_delta.h), with dS' the adjoint of the state after the chunk and dO that of O:
+//     dE = P^T dO + diag(c) K dS',   dV = dY = T^T dE
+//     dS = exp(G_64) dS' + Q^T diag(scale exp G) dO - K^T diag(exp G) dY
+//     M_ij = dO_i . e_j (j <= i),  N_ij = dY_i . e_j (j < i)
+//     B1_ij = scale D_ij beta_j M_ij,  B2_ij = -D_ij beta_j N_ij
+//     dQ_i = sum_j B1_ij k_j + scale exp(G_i) S dO_i
+//     dK_i = sum_j B2_ij k_j - exp(G_i) S dY_i + sum_t (B2_ti k_t + B1_ti q_t) + c_i dS' e_i
+//     dbeta_j = sum_i D_ij (scale (q_i . k_j) M_ij - (k_i . k_j) N_ij) + exp(G_64 - G_j) k_j . dS' e_j
+//     dg_t = exp(G_64) <dS', S> + sum_{j < t} Z_j + sum_{i >= t} R_i + sum_{i >= t > j} X_ij,
+//         Z_j = c_j k_j . dS' e_j,  X_ij = B1_ij (q_i . k_j) + B2_ij (k_i . k_j)
+//         R_i = exp(G_i) (scale q_i . S dO_i - k_i . S dY_i)
+// (the last sums leave out every pair that cancels: the decay of token t only weighs what crosses it).
+//
+// Four launches: the chunk products and the state pass of mamba_delta.hip (which leaves E and the state
+// before every chunk in the workspace), then
+//   adjoint_kernel  the adjoint of the state, backwards through the chunks: dV, and dS' of every chunk;
+//                   laid out like the forward's state pass (16 columns per wave, in accumulators)
+//   grad_kernel     one workgroup per chunk and key head: everything else.  The value heads that share
+//                   the key head add their dQ and dK in accumulators, in a fixed order: no atomics.
+// Every gradient is rounded once.  Rounding inside, bf16 storage: one bf16 part of each factor, two of
+// dE in dY and of E in M and N, which keeps each gradient's error within 1.5 times that of rounding it.
+#include "mamba_delta.h"
+
+namespace mamba {
+namespace delta {
+namespace {
+
+struct BwdArgs {
+  Args f;
+  const void* dout;    // (tokens, hv, dv)
+  const float* dlast;  // (nseq, hv, dk, dv) or NULL: zero
+  void* dq;            // (tokens, hk, dk)
+  void* dk;
+  void* dv;            // (tokens, hv, dv)
+  void* dg;            // (tokens, hv)
+  void* dbeta;
+  float* ds0;          // (nseq, hv, dk, dv) or NULL
+};
+
+// 8 (bf16) or 4 (fp32) consecutive values from one operand's accumulators
+template <typename E>
+__device__ __forceinline__ void store_values(E* p, const f32x4* c) {
+  *reinterpret_cast<typename Mma<E>::Frag*>(p) = Mma<E>::pack(c);
+}
+
+// ------------------------------------------------------------------ the adjoint of the state
+
+template <typename E, int DK, int NW>
+struct AdjStage {
+  using VT = ValueTile<E, 16 * NW>;
+  static constexpr int kK = 0;
+  static constexpr int kQ = KeyTile<E, DK>::kBytes;
+  static constexpr int kT = 2 * KeyTile<E, DK>::kBytes;
+  static constexpr int kP = kT + TriTile<E>::kBytes;
+  static constexpr int kGate = kP + TriTile<E>::kBytes;
+  static constexpr int kDO = kGate + 1024;
+  static constexpr int kBytes = kDO + VT::kBytes;
+  static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+};
+
+template <typename E, int DK, int NW>
+__global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col_blocks) {
+  using M = Mma<E>;
+  using St = AdjStage<E, DK, NW>;
+  using KT = KeyTile<E, DK>;
+  using TT = TriTile<E>;
+  using VT = typename St::VT;
+  using CW = ChunkWs<E>;
+  constexpr int kPE = M::parts(2);
+  __shared__ __align__(1024) char smem[St::kCount * St::kBytes];
+  const Args& a = b.f;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t wg = placed_index(blockIdx.x, gridDim.x);
+  const int64_t sh = wg / col_blocks;
+  const int64_t seq = sh / a.hv;
+  const int vh = (int)(sh - seq * a.hv), kh = vh / a.rep;
+  const int col0 = (int)(wg - sh * col_blocks) * 16 * NW;
+  const int col = col0 + 16 * w;
+  const Span sp = seq_span(a, seq);
+  const int64_t slot0 = slot_base(a, seq, sp.first);
+  const E* kp = static_cast<const E*>(a.k) + sp.first * a.k_stride + (int64_t)kh * a.dk;
+  const E* qp = static_cast<const E*>(a.q) + sp.first * a.q_stride + (int64_t)kh * a.dk;
+  const int64_t o_stride = (int64_t)a.hv * a.dv;
+  const int64_t o_at = (sp.first * a.hv + vh) * (int64_t)a.dv;
+  const E* dop = static_cast<const E*>(b.dout) + o_at + col0;
+  E* dvp = static_cast<E*>(b.dv) + o_at + col;
+  const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
+  const bool has_col = col + r < a.dv;
+
+  f32x4 S[DK / 16];  // the adjoint, rows (keys' values) permuted as in KeyTile
+#pragma unroll
+  for (int m = 0; m < DK / 16; ++m)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int row = KT::value(m, g, x);
+      S[m][x] = b.dlast && has_col && row < a.dk ? b.dlast[s_at + (int64_t)row * a.dv] : 0.f;
+    }
+
+  const uint32_t lds0 = lds_address(smem);
+  const int64_t nchunks = (sp.len + kC - 1) / kC;
+  const int vcols = min(a.dv - col0, 16 * NW);
+  const RowCopy<E, KT, kC, NW> ck(w, lane, a.k_stride, a.dk), cq(w, lane, a.q_stride, a.dk);
+  const RowCopy<E, VT, kC, NW> co(w, lane, o_stride, vcols);
+  auto copy = [&](int64_t ch, int st) {
+    const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
+    const uint32_t to = lds0 + st * St::kBytes;
+    const char* ws = a.ws + ((slot0 + ch) * a.hv + vh) * (int64_t)CW::kBytes;
+    ck(rows_buffer(kp + t * a.k_stride, n, a.k_stride, a.dk), to + St::kK, w);
+    co(rows_buffer(dop + t * o_stride, n, o_stride, vcols), to + St::kDO, w);
+    copy_linear<TT::kBytes, NW>(ws, to + St::kT, w, lane);
+    copy_linear<CW::kP + 1024, NW>(ws + CW::kT, to + St::kP, w, lane);
+    cq(rows_buffer(qp + t * a.q_stride, n, a.q_stride, a.dk), to + St::kQ, w);
+  };
+
+  const int dv_pad = (a.dv + BwdBlock<E>::kDB - 1) / BwdBlock<E>::kDB * BwdBlock<E>::kDB;
+  const int64_t img_bytes = (int64_t)dv_pad * KT::kRow;
+  const KT kt(lane);
+  const TT tt(lane);
+  const VT ot(lane, 16 * w);
+  if (nchunks > 0) copy(nchunks - 1, 0);
+  for (int64_t ch = nchunks - 1; ch >= 0; --ch) {
+    const int st = St::kCount == 2 ? (int)((nchunks - 1 - ch) & 1) : 0;
+    copies_done();
+    if (St::kCount == 2 && ch > 0) copy(ch - 1, st ^ 1);
+    const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
+    const int n = (int)min((int64_t)kC, sp.len - ch * kC);
+    {
+      char* img = a.ds_img + ((slot0 + ch) * a.hv + vh) * img_bytes;
+#pragma unroll
+      for (int kb = 0; kb < DK / M::kDepth; ++kb)
+        if (col + r < dv_pad)
+          *reinterpret_cast<typename M::Frag*>(img + (int64_t)(col + r) * KT::kRow +
+                                               (((4 * kb + g) ^ KT::key(col + r)) << 4)) =
+              M::pack(&S[kb * M::kTiles]);
+    }
+    // dE = diag(c) K dS' + P^T dO
+    f32x4 e[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) e[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+      const auto s = M::pack(&S[kb * M::kTiles]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) e[m] = M::mma(kt.rows(sm + St::kK, m, kb), s, e[m]);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) e[m] *= lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
+#pragma unroll
+    for (int ib = 0; ib < TT::kBlocks; ++ib) {
+      const auto d = ot.operand(sm + St::kDO, ib);
+#pragma unroll
+      for (int m = 0; m < (ib + 1) * M::kTiles; ++m) e[m] = M::mma(tt.cols(sm + St::kP, m, ib), d, e[m]);
+    }
+    // dY = T^T dE, and transposed for the store
+    f32x4 y[4], yt[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) y[m] = yt[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ib = 0; ib < TT::kBlocks; ++ib) {
+      const auto es = M::template split<kPE>(&e[ib * M::kTiles]);
+#pragma unroll
+      for (int m = 0; m < (ib + 1) * M::kTiles; ++m) {
+        const auto tf = tt.cols(sm + St::kT, m, ib);
+#pragma unroll
+        for (int p = 0; p < kPE; ++p) {
+          y[m] = M::mma(tf, es.p[p], y[m]);
+          yt[m] = M::mma(es.p[p], tf, yt[m]);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int t = 16 * m + r;
+      if (t < n && col + 4 * g < a.dv) {
+        E* dst = dvp + (ch * kC + t) * o_stride + 4 * g;
+        if constexpr (sizeof(E) == 2)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(make_float2(yt[m][0], yt[m][1])),
+                                                      pack_bf16(make_float2(yt[m][2], yt[m][3])));
+        else
+          *reinterpret_cast<f32x4*>(dst) = yt[m];
+      }
+    }
+    // dS = exp(G_64) dS' + Q^T diag(scale exp G) dO - K^T diag(exp G) dY
+    const float last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
+    f32x4 o[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 eg = lds_read<f32x4>(sm + St::kGate + (16 * m + 4 * g) * 4);
+      o[m] = ot.tile(sm + St::kDO, m) * (a.scale * eg);
+      y[m] *= -eg;
+    }
+#pragma unroll
+    for (int m = 0; m < DK / 16; ++m) S[m] *= last;
+#pragma unroll
+    for (int kb = 0; kb < TT::kBlocks; ++kb) {
+      const auto of = M::pack(&o[kb * M::kTiles]), yf = M::pack(&y[kb * M::kTiles]);
+#pragma unroll
+      for (int m = 0; m < DK / 16; ++m) S[m] = M::mma(kt.cols(sm + St::kQ, m, kb), of, S[m]);
+#pragma unroll
+      for (int m = 0; m < DK / 16; ++m) S[m] = M::mma(kt.cols(sm + St::kK, m, kb), yf, S[m]);
+    }
+    if (St::kCount == 1 && ch > 0) {
+      __syncthreads();  // every wave has read the stage
+      copy(ch - 1, 0);
+    }
+  }
+  if (b.ds0 && has_col) {
+#pragma unroll
+    for (int m = 0; m < DK / 16; ++m)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = KT::value(m, g, x);
+        if (row < a.dk) b.ds0[s_at + (int64_t)row * a.dv] = S[m][x];
+      }
+  }
+}
+
+// ------------------------------------------------------------------ dQ, dK, dg, dbeta
+
+// sum over the 16 lanes of a group, in every lane of it
+__device__ __forceinline__ float group_sum(float v) {
+  v += dpp_row<0x128>(v);
+  v += dpp_row<0x124>(v);
+  v += dpp_row<0x122>(v);
+  v += dpp_row<0x121>(v);
+  return v;
+}
+// sum over the four groups
+__device__ __forceinline__ float across_groups(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+// sum over lanes lane .. 63
+__device__ __forceinline__ float wave_suffix(float v, int lane) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    const float t = __shfl_down(v, m);
+    if (lane + m < 64) v += t;
+  }
+  return v;
+}
+
+template <typename E, int DK>
+struct GradSmem {
+  using B = BwdBlock<E>;
+  static constexpr int kK = 0;
+  static constexpr int kQ = KeyTile<E, DK>::kBytes;
+  static constexpr int kDO = 2 * KeyTile<E, DK>::kBytes;
+  static constexpr int kDY = kDO + B::kE;
+  static constexpr int kE = kDY + B::kE;
+  static constexpr int kS = kE + B::kEParts * B::kE;
+  static constexpr int kDS = kS + B::kDB * KeyTile<E, DK>::kRow;
+  static constexpr int kB1 = kDS + B::kDB * KeyTile<E, DK>::kRow;
+  static constexpr int kB2 = kB1 + TriTile<E>::kBytes;
+  static constexpr int kGate = kB2 + TriTile<E>::kBytes;  // gates and decays: 2 KB
+  static constexpr int kSums = kGate + 2048;              // per wave: column sums of X and of dbeta
+  static constexpr int kTok = kSums + 4 * 2 * kC * 4;     // per token: R + row sum of X, k . dS' e
+  static constexpr int kDot = kTok + 2 * kC * 4;
+  static constexpr int kBytes = kDot + 64;
+};
+
+template <typename E, int DK>
+__global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
+  using M = Mma<E>;
+  using Sm = GradSmem<E, DK>;
+  using KT = KeyTile<E, DK>;
+  using TT = TriTile<E>;
+  using BB = BwdBlock<E>;
+  using ET = KeyTile<E, BB::kDB>;
+  using CW = ChunkWs<E>;
+  constexpr int kTiles = DK / 16;
+  __shared__ __align__(1024) char smem[Sm::kBytes];
+  const Args& a = b.f;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t wg = placed_index(blockIdx.x, gridDim.x);
+  const int64_t slot = wg / a.hk;
+  const int kh = (int)(wg - slot * a.hk);
+  const int64_t seq = slot_seq(a, slot);
+  const Span sp = seq_span(a, seq);
+  const int64_t c0 = (slot - slot_base(a, seq, sp.first)) * kC;
+  if (c0 < 0 || c0 >= sp.len) return;
+  const int n = (int)min((int64_t)kC, sp.len - c0);
+  const int64_t t0 = sp.first + c0;
+  const uint32_t lds0 = lds_address(smem);
+  const lds_ptr sm = (lds_ptr)smem;
+  const int64_t o_stride = (int64_t)a.hv * a.dv;
+  const int blocks = (a.dv + BB::kDB - 1) / BB::kDB;
+  const int64_t img_bytes = (int64_t)blocks * BB::kDB * KT::kRow;
+  const int64_t e_bytes = (int64_t)blocks * BB::kEParts * BB::kE;
+  const KT kt(lane);
+  const TT tt(lane);
+  const ET et(lane);
+  const int i = 16 * w + r;  // this lane's token
+
+  {
+    const RowCopy<E, KT, kC, 4> ck(w, lane, a.k_stride, a.dk), cq(w, lane, a.q_stride, a.dk);
+    ck(rows_buffer(static_cast<const E*>(a.k) + t0 * a.k_stride + (int64_t)kh * a.dk, n, a.k_stride,
+                   a.dk), lds0 + Sm::kK, w);
+    cq(rows_buffer(static_cast<const E*>(a.q) + t0 * a.q_stride + (int64_t)kh * a.dk, n, a.q_stride,
+                   a.dk), lds0 + Sm::kQ, w);
+    copies_done();
+  }
+  // rows j (tiles up to w), column i: k_j . k_i and k_j . q_i
+  f32x4 kk[4], qk[4], dQ[kTiles], dK[kTiles];
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt) kk[jt] = qk[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m) dQ[m] = dK[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+    const auto ki = kt.rows(sm + Sm::kK, w, kb), qi = kt.rows(sm + Sm::kQ, w, kb);
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt)
+      if (jt <= w) {
+        const auto kj = kt.rows(sm + Sm::kK, jt, kb);
+        kk[jt] = M::mma(kj, ki, kk[jt]);
+        qk[jt] = M::mma(kj, qi, qk[jt]);
+      }
+  }
+
+  for (int h = 0; h < a.rep; ++h) {
+    const int vh = kh * a.rep + h;
+    const int64_t item = slot * a.hv + vh;
+    f32x4 Mt[4], Nt[4], sdo[kTiles], sdy[kTiles], dse[kTiles];
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) Mt[jt] = Nt[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) sdo[m] = sdy[m] = dse[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float dot = 0.f;  // this thread's part of <dS', S>
+    for (int db = 0; db < blocks; ++db) {
+      __syncthreads();  // the tiles of the block before have been read
+      const int cols = min(a.dv - db * BB::kDB, BB::kDB);
+      const RowCopy<E, ET, kC, 4> co(w, lane, o_stride, cols);
+      const int64_t at = (t0 * a.hv + vh) * (int64_t)a.dv + db * BB::kDB;
+      co(rows_buffer(static_cast<const E*>(b.dout) + at, n, o_stride, cols), lds0 + Sm::kDO, w);
+      co(rows_buffer(static_cast<const E*>(b.dv) + at, n, o_stride, cols), lds0 + Sm::kDY, w);
+      copy_linear<BB::kEParts * BB::kE, 4>(
+          a.e_img + item * e_bytes + (int64_t)db * BB::kEParts * BB::kE, lds0 + Sm::kE, w, lane);
+      constexpr int kBlock = BB::kDB * KT::kRow;
+      copy_linear<kBlock, 4>(a.s_img + item * img_bytes + (int64_t)db * kBlock, lds0 + Sm::kS, w, lane);
+      copy_linear<kBlock, 4>(a.ds_img + item * img_bytes + (int64_t)db * kBlock, lds0 + Sm::kDS, w, lane);
+      if (db == 0) copy_linear<2048, 4>(a.ws + item * (int64_t)CW::kBytes + CW::kGate, lds0 + Sm::kGate, w, lane);
+      copies_done();
+#pragma unroll
+      for (int kb = 0; kb < BB::kDB / M::kDepth; ++kb) {
+        const auto of = et.rows(sm + Sm::kDO, w, kb), yf = et.rows(sm + Sm::kDY, w, kb);
+        const auto ef = et.rows(sm + Sm::kE, w, kb);
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+          if (jt <= w) {
+#pragma unroll
+            for (int p = 0; p < BB::kEParts; ++p) {
+              const auto ej = et.rows(sm + Sm::kE + p * BB::kE, jt, kb);
+              Mt[jt] = M::mma(ej, of, Mt[jt]);
+              Nt[jt] = M::mma(ej, yf, Nt[jt]);
+            }
+          }
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const auto sf = kt.template cols<true>(sm + Sm::kS, m, kb);
+          sdo[m] = M::mma(sf, of, sdo[m]);
+          sdy[m] = M::mma(sf, yf, sdy[m]);
+          dse[m] = M::mma(kt.template cols<true>(sm + Sm::kDS, m, kb), ef, dse[m]);
+        }
+      }
+      for (int x = threadIdx.x; x < kBlock / 16; x += 256) {
+        const auto u = lds_read<typename M::Frag>(sm + Sm::kS + 16 * x);
+        const auto v = lds_read<typename M::Frag>(sm + Sm::kDS + 16 * x);
+#pragma unroll
+        for (int y = 0; y < 16 / (int)sizeof(E); ++y) dot = fmaf((float)u[y], (float)v[y], dot);
+      }
+    }
+    // B1, B2, and the sums that reach dbeta and dg
+    const lds_ptr decay = sm + Sm::kGate + 1024;
+    const float gi = lds_read<float>(decay + 4 * i), gil = lds_read<float>(decay + 4 * (kC + i));
+    float row_x = 0.f;
+    f32x4 b1[4], b2[4];
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      const int j = 16 * jt + 4 * g;
+      const f32x4 gj = lds_read<f32x4>(decay + 4 * j), gjl = lds_read<f32x4>(decay + 4 * (kC + j));
+      const f32x4 bj = lds_read<f32x4>(decay + 4 * (2 * kC + j));
+      f32x4 cx = {0.f, 0.f, 0.f, 0.f}, cb = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool in = jt <= w && j + x <= i;
+        const float d = in ? exp_f32((gi - gj[x]) + (gil - gjl[x])) : 0.f;
+        const float m1 = a.scale * d * Mt[jt][x], m2 = j + x < i ? -d * Nt[jt][x] : 0.f;
+        b1[jt][x] = m1 * bj[x];
+        b2[jt][x] = m2 * bj[x];
+        cb[x] = fmaf(m1, qk[jt][x], m2 * kk[jt][x]);
+        cx[x] = cb[x] * bj[x];
+        row_x += cx[x];
+      }
+      if (jt <= w) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float sx = group_sum(cx[x]), sb = group_sum(cb[x]);
+          if (r == 0) {
+            float* sums = reinterpret_cast<float*>(smem + Sm::kSums) + w * 2 * kC;
+            sums[j + x] = sx;
+            sums[kC + j + x] = sb;
+          }
+        }
+      }
+    }
+    row_x = across_groups(row_x);
+#pragma unroll
+    for (int kb = 0; kb < TT::kBlocks; ++kb)
+      if (16 * w >= kb * M::kDepth) {
+        const auto f1 = M::pack(&b1[kb * M::kTiles]), f2 = M::pack(&b2[kb * M::kTiles]);
+        const int at = TT::word_at(kb, i, g);
+        *reinterpret_cast<typename M::Frag*>(smem + Sm::kB1 + at) = f1;
+        *reinterpret_cast<typename M::Frag*>(smem + Sm::kB2 + at) = f2;
+        // sums over j: this wave's own tiles
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const auto kf = kt.cols(sm + Sm::kK, m, kb);
+          dQ[m] = M::mma(kf, f1, dQ[m]);
+          dK[m] = M::mma(kf, f2, dK[m]);
+        }
+      }
+    // the state's terms, and their dots with q_i and k_i
+    const float eg = lds_read<float>(sm + Sm::kGate + 4 * i), ci = lds_read<float>(sm + Sm::kGate + 4 * (kC + i));
+    float rdot = 0.f, kd = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+      const auto ki = kt.rows(sm + Sm::kK, w, kb), qi = kt.rows(sm + Sm::kQ, w, kb);
+#pragma unroll
+      for (int y = 0; y < M::kTiles; ++y) {
+        const int m = kb * M::kTiles + y;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float kx, qx;
+          if constexpr (sizeof(E) == 2) {
+            kx = (float)ki[4 * y + x];
+            qx = (float)qi[4 * y + x];
+          } else {
+            kx = ki[x];
+            qx = qi[x];
+          }
+          const float so = a.scale * eg * sdo[m][x], sy = -eg * sdy[m][x];
+          rdot = fmaf(qx, so, fmaf(kx, sy, rdot));
+          kd = fmaf(kx, dse[m][x], kd);
+          dQ[m][x] += so;
+          dK[m][x] += fmaf(ci, dse[m][x], sy);
+        }
+      }
+    }
+    rdot = across_groups(rdot);
+    kd = across_groups(kd);
+    if (g == 0) {
+      float* tok = reinterpret_cast<float*>(smem + Sm::kTok);
+      tok[i] = rdot + row_x;
+      tok[kC + i] = kd;
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
+    if (lane == 0) reinterpret_cast<float*>(smem + Sm::kDot)[w] = dot;
+    __syncthreads();
+    // sums over i: rows i of B1 and B2 at and below this wave's tile
+#pragma unroll
+    for (int ib = 0; ib < TT::kBlocks; ++ib)
+      if (16 * w < (ib + 1) * M::kDepth) {
+        const auto f1 = tt.cols(sm + Sm::kB1, w, ib), f2 = tt.cols(sm + Sm::kB2, w, ib);
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          dK[m] = M::mma(kt.cols(sm + Sm::kQ, m, ib), f1, dK[m]);
+          dK[m] = M::mma(kt.cols(sm + Sm::kK, m, ib), f2, dK[m]);
+        }
+      }
+    if (w == 0) {
+      const float* sums = reinterpret_cast<const float*>(smem + Sm::kSums);
+      const float* tok = reinterpret_cast<const float*>(smem + Sm::kTok);
+      const float* dots = reinterpret_cast<const float*>(smem + Sm::kDot);
+      const float* gate = reinterpret_cast<const float*>(smem + Sm::kGate);
+      const float* dec = gate + 256;
+      float cx = 0.f, cb = 0.f;
+      for (int x = lane >> 4; x < 4; ++x) {
+        cx += sums[x * 2 * kC + lane];
+        cb += sums[x * 2 * kC + kC + lane];
+      }
+      const float e = exp_f32((dec[kC - 1] - dec[lane]) + (dec[2 * kC - 1] - dec[kC + lane]));
+      const float kdt = tok[kC + lane], z = gate[kC + lane] * kdt;
+      const float after = wave_suffix(tok[lane] - cx, lane);
+      float before = z;  // sum of z over the tokens before
+#pragma unroll
+      for (int m = 1; m < 64; m *= 2) {
+        const float t = __shfl_up(before, m);
+        if (lane >= m) before += t;
+      }
+      before = __shfl_up(before, 1);
+      const float whole = gate[2 * kC] * ((dots[0] + dots[1]) + (dots[2] + dots[3]));
+      if (lane < n) {
+        const int64_t at = (t0 + lane) * a.hv + vh;
+        st_out(static_cast<E*>(b.dg), at, whole + (lane ? before : 0.f) + after);
+        st_out(static_cast<E*>(b.dbeta), at, fmaf(e, kdt, cb));
+      }
+    }
+  }
+  if (i < n) {
+    E* dqp = static_cast<E*>(b.dq) + ((t0 + i) * a.hk + kh) * (int64_t)a.dk;
+    E* dkp = static_cast<E*>(b.dk) + ((t0 + i) * a.hk + kh) * (int64_t)a.dk;
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+      const int v = KT::value(kb * M::kTiles, g, 0);
+      if (v < a.dk) {
+        store_values(dqp + v, &dQ[kb * M::kTiles]);
+        store_values(dkp + v, &dK[kb * M::kTiles]);
+      }
+    }
+  }
+}
+
+template <typename E, int DK, int NW>
+int launch_adjoint_t(const BwdArgs& b, hipStream_t s) {
+  const int cols = (b.f.dv + 16 * NW - 1) / (16 * NW);
+  hipLaunchKernelGGL((adjoint_kernel<E, DK, NW>), dim3((unsigned)(b.f.nseq * b.f.hv * cols)),
+                     dim3(64 * NW), 0, s, b, cols);
+  return launch_status();
+}
+template <typename E, int DK>
+int launch_bwd(const BwdArgs& b, hipStream_t s) {
+  // 8 waves of fp32 operands would not fit the registers
+  const int st = b.f.dv <= 64 || sizeof(E) == 4 ? launch_adjoint_t<E, DK, 4>(b, s)
+                                                : launch_adjoint_t<E, DK, sizeof(E) == 2 ? 8 : 4>(b, s);
+  if (st != MAMBA_OK) return st;
+  hipLaunchKernelGGL((grad_kernel<E, DK>), dim3((unsigned)(b.f.slots * b.f.hk)), dim3(256), 0, s, b);
+  return launch_status();
+}
+
+struct BwdLayout {  // workspace regions in bytes
+  size_t e, s, ds, total;
+};
+template <typename E>
+BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
+  const size_t items = (size_t)chunk_slots(d, packed) * (size_t)d->v_heads;
+  const size_t blocks = (size_t)BwdBlock<E>::blocks(d->dv);
+  const size_t row = (d->dk <= 64 ? 64 : 128) * sizeof(E);
+  BwdLayout l;
+  l.e = items * ChunkWs<E>::kBytes;
+  l.s = l.e + items * blocks * BwdBlock<E>::kEParts * BwdBlock<E>::kE;
+  l.ds = l.s + items * blocks * BwdBlock<E>::kDB * row;
+  l.total = l.ds + items * blocks * BwdBlock<E>::kDB * row;
+  return l;
+}
+BwdLayout layout(const mamba_delta_dims* d, bool packed) {
+  return d->io_dtype == MAMBA_BF16 ? layout_t<uint16_t>(d, packed) : layout_t<float>(d, packed);
+}
+
+}  // namespace
+}  // namespace delta
+}  // namespace mamba
+
+using namespace mamba;
+using namespace mamba::delta;
+
+extern "C" {
+
+size_t mamba_delta_bwd_workspace_bytes(const mamba_delta_dims* dims, int packed) {
+  if (check_delta(dims, packed != 0) != MAMBA_OK) return 0;
+  return layout(dims, packed != 0).total;
+}
+
+int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                    const float* initial_state, const int64_t* seq_offsets, float scale,
+                    const void* dout, const float* dlast, void* dq, void* dk, void* dv, void* dg,
+                    void* dbeta, float* dinitial_state, const mamba_delta_dims* dims,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  const bool packed = seq_offsets != nullptr;
+  int st = check_delta(dims, packed);
+  if (st != MAMBA_OK) return st;
+  if (!dout || !dq || !dk || !dv || !dg || !dbeta) return MAMBA_ERR_NULL;
+  if ((st = check_delta_inputs(dims, q, k, v, g, beta, initial_state, seq_offsets)) != MAMBA_OK)
+    return st;
+  const size_t es = dims->io_dtype == MAMBA_BF16 ? 2 : 4;
+  if (!aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
+      !aligned(dg, es) || !aligned(dbeta, es) || (dlast && !aligned(dlast, 16)) ||
+      (dinitial_state && !aligned(dinitial_state, 16)))
+    return MAMBA_ERR_ALIGN;
+  const BwdLayout l = layout(dims, packed);
+  if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
+  BwdArgs b = {};
+  b.f = make_args(dims, scale, q, k, v, g, beta, initial_state, seq_offsets);
+  b.f.ws = static_cast<char*>(workspace);
+  b.f.e_img = b.f.ws + l.e;
+  b.f.s_img = b.f.ws + l.s;
+  b.f.ds_img = b.f.ws + l.ds;
+  b.dout = dout;
+  b.dlast = dlast;
+  b.dq = dq;
+  b.dk = dk;
+  b.dv = dv;
+  b.dg = dg;
+  b.dbeta = dbeta;
+  b.ds0 = dinitial_state;
+  const bool bf = dims->io_dtype == MAMBA_BF16;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((st = launch_chunks(b.f, bf, s)) != MAMBA_OK) return st;
+  if ((st = launch_states(b.f, bf, s)) != MAMBA_OK) return st;
+  if (bf) return b.f.dk <= 64 ? launch_bwd<uint16_t, 64>(b, s) : launch_bwd<uint16_t, 128>(b, s);
+  return b.f.dk <= 64 ? launch_bwd<float, 64>(b, s) : launch_bwd<float, 128>(b, s);
+}
+
+}  // extern "C"
