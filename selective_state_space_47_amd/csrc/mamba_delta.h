@@ -324,10 +324,12 @@ struct Args {
   const int64_t* offsets;  // (nseq + 1) token offsets of packed sequences, or NULL
   void* out;               // (tokens, hv, dv)
   float* last;             // (nseq, hv, dk, dv) or NULL
-  char* ws;                // per (chunk slot, value head): ChunkWs
+  char* ws;                // per (chunk slot, value head): ChunkWs, ws_item bytes
+  int64_t ws_item;
   char* e_img;             // backward only, per (chunk slot, value head): images of E,
   char* s_img;             // of the state before the chunk
-  char* ds_img;            // and of the adjoint of the state after it
+  char* ds_img;            // and of the adjoint of the state after it;
+  char* s_low;             // what bf16 leaves of that state, a byte per value (bf16 storage)
   int64_t q_stride, k_stride, v_stride;  // elements between tokens
   int64_t seqlen;          // tokens per sequence (packed: of all sequences)
   int64_t nseq;
@@ -372,7 +374,8 @@ __device__ __forceinline__ int64_t slot_seq(const Args& a, int64_t slot) {
 constexpr int kTParts = 2;
 
 // Workspace of one chunk and value head: T (in parts), P, then floats: exp(G_i) (64), c_j (64),
-// exp(G_64) and 127 unused, G_i as two floats (64 + 64), beta (64), 64 unused.
+// exp(G_64) and 127 unused, G_i as two floats (64 + 64), beta (64), 64 unused; for the backward also the
+// second part of P (bf16 storage), whose rounding would weigh as much in dV as that of dV itself.
 template <typename E>
 struct ChunkWs {
   static constexpr int kT = Mma<E>::parts(kTParts) * TriTile<E>::kBytes;
@@ -380,7 +383,9 @@ struct ChunkWs {
   static constexpr int kGate = kT + kP;        // what the scan reads: 1 KB
   static constexpr int kDecay = kGate + 1024;  // what only the gradients read: 1 KB
   static constexpr int kBytes = kDecay + 1024;
-  static_assert(kBytes % 1024 == 0, "copied in whole wave instructions");
+  static constexpr int kPLow = kBytes;
+  static constexpr int kBwdBytes = kBytes + (Mma<E>::parts(2) - 1) * kP;
+  static_assert(kBytes % 1024 == 0 && kBwdBytes % 1024 == 0, "copied in whole wave instructions");
 };
 
 inline int64_t chunk_slots(const mamba_delta_dims* d, bool packed) {
@@ -442,6 +447,7 @@ inline Args make_args(const mamba_delta_dims* d, float scale, const void* q, con
   a.dk = (int32_t)d->dk;
   a.dv = (int32_t)d->dv;
   a.scale = scale;
+  a.ws_item = (int64_t)chunk_ws_bytes(d);
   return a;
 }
 
@@ -466,6 +472,21 @@ struct BwdBlock {
   static constexpr int kE = kC * kDB * (int)sizeof(E);  // bytes of one part
   static int64_t blocks(int64_t dv) { return (dv + kDB - 1) / kDB; }
 };
+
+// The byte that follows a value's bf16: the next 8 bits of its fp32 pattern, rounded.  Taken up again by
+// with_low the two are the value to 2^-17.
+__device__ __forceinline__ uint32_t low_byte(float v, uint32_t bf_bits_high) {
+  const int d = ((int)(__float_as_uint(v) - bf_bits_high) + 0x80) >> 8;
+  return (uint32_t)(d < 127 ? d : 127) & 0xffu;
+}
+__device__ __forceinline__ float with_low(uint32_t bf_bits_high, uint32_t low, int byte) {
+  return __uint_as_float(bf_bits_high + (uint32_t)(((int)(low << (24 - 8 * byte)) >> 24) << 8));
+}
+// byte of s_low that holds operand kb of a lane's state column block `cb` (16 columns) of an item
+template <int DK>
+__device__ __forceinline__ int64_t low_at(int64_t item, int cbs, int cb, int kb, int lane) {
+  return ((item * cbs + cb) * (DK / 32) + kb) * 512 + lane * 8;
+}
 
 // Launches the chunk products (T, P and gates of every chunk and value head) into a.ws.
 __attribute__((visibility("hidden"))) int launch_chunks(const Args& a, bool bf, hipStream_t s);

@@ -52,6 +52,13 @@ __device__ __forceinline__ uint4 pack_word(const float (&a)[4], const float (&b)
     return __builtin_bit_cast(uint4, make_float4(a[0], a[1], a[2], a[3]));
 }
 
+// what a bf16 word leaves of its values
+__device__ __forceinline__ void subtract_word(float (&a)[4], float (&b)[4], uint4 word) {
+  const float2 a0 = unpack(word.x), a1 = unpack(word.y), b0 = unpack(word.z), b1 = unpack(word.w);
+  a[0] -= a0.x; a[1] -= a0.y; a[2] -= a1.x; a[3] -= a1.y;
+  b[0] -= b0.x; b[1] -= b0.y; b[2] -= b1.x; b[3] -= b1.y;
+}
+
 // sum of v over lanes 0 .. lane
 __device__ __forceinline__ double wave_prefix(double v, int lane) {
 #pragma unroll
@@ -113,7 +120,7 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
   const int i = 16 * w + r;  // this lane's token
   for (int h = 0; h < a.rep; ++h) {
     const int vh = kh * a.rep + h;
-    char* ws = a.ws + (slot * a.hv + vh) * (int64_t)ChunkWs<E>::kBytes;
+    char* ws = a.ws + (slot * a.hv + vh) * a.ws_item;
     __syncthreads();  // the tiles of the previous head (or K and Q) have been read
     if (w == 0) {
       // Prefix sums of the log decays in fp64, kept as two floats: a difference of two of them is
@@ -161,9 +168,16 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
     // a lane's accumulators of one block of P are one word of its image
 #pragma unroll
     for (int kb = 0; kb < TriTile<E>::kBlocks; ++kb)
-      if (16 * w >= kb * M::kDepth)
-        *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kT + TriTile<E>::word_at(kb, i, g)) =
-            pack_word<E>(p[kb * M::kTiles], p[(kb + 1) * M::kTiles - 1]);
+      if (16 * w >= kb * M::kDepth) {
+        float (&lo)[4] = p[kb * M::kTiles], (&hi)[4] = p[(kb + 1) * M::kTiles - 1];
+        const int at = TriTile<E>::word_at(kb, i, g);
+        const uint4 word = pack_word<E>(lo, hi);
+        *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kT + at) = word;
+        if (M::parts(2) > 1 && a.e_img) {
+          subtract_word(lo, hi, word);
+          *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kPLow + at) = pack_word<E>(lo, hi);
+        }
+      }
     __syncthreads();
     // T = (I + A)^-1 by blocks of 16.  Wave w inverts diagonal block w by substitution, lane r its
     // column r: x_m = [m = r] - sum_{j < m} A_mj x_j.
@@ -224,12 +238,7 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
         const uint4 word = pack_word<E>(lo, hi);
         *reinterpret_cast<uint4*>(ws + part * TriTile<E>::kBytes +
                                   TriTile<E>::word_at(kb, t, x & 3)) = word;
-        if (sizeof(E) == 2) {
-          const float2 a0 = unpack(word.x), a1 = unpack(word.y), b0 = unpack(word.z),
-                       b1 = unpack(word.w);
-          lo[0] -= a0.x; lo[1] -= a0.y; lo[2] -= a1.x; lo[3] -= a1.y;
-          hi[0] -= b0.x; hi[1] -= b0.y; hi[2] -= b1.x; hi[3] -= b1.y;
-        }
+        if (sizeof(E) == 2) subtract_word(lo, hi, word);
       }
     }
   }
@@ -251,8 +260,8 @@ struct Stage {
 };
 
 // kStates: the backward's pass, which leaves E and the state before each chunk instead of the output.
-// Its results only enter gradients that are rounded to the storage type, so that with bf16 storage one
-// part of each factor is enough, two of Y (whose rounding alone would be as large as the gradients').
+// Its results only enter gradients that are rounded to the storage type: with bf16 storage two parts of
+// each factor keep them clear of those roundings, also where a sum of them cancels (dg).
 template <typename E, int DK, int NW, bool kStates>
 __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_blocks) {
   using M = Mma<E>;
@@ -260,8 +269,8 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
   using KT = KeyTile<E, DK>;
   using TT = TriTile<E>;
   using VT = ValueTile<E, 16 * NW>;
-  constexpr int kPS = M::parts(kStates ? 1 : 3), kPT = M::parts(kStates ? 1 : kTParts);
-  constexpr int kPY = M::parts(kStates ? 2 : 3), kPE = M::parts(kStates ? 1 : 3);
+  constexpr int kPS = M::parts(kStates ? 2 : 3), kPT = M::parts(kTParts);
+  constexpr int kPY = M::parts(kStates ? 2 : 3), kPE = M::parts(kStates ? 2 : 3);
   constexpr int kPO = M::parts(2);  // of S and E in the output
   __shared__ __align__(1024) char smem[St::kCount * St::kBytes];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
@@ -302,7 +311,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
     ck(rows_buffer(kp + t * a.k_stride, n, a.k_stride, a.dk), to + St::kK, w);
     cv(rows_buffer(vp + t * a.v_stride, n, a.v_stride, vcols), to + St::kVv, w);
     if (!kStates) cq(rows_buffer(qp + t * a.q_stride, n, a.q_stride, a.dk), to + St::kQ, w);
-    copy_linear<St::kWsBytes, NW>(a.ws + ((slot0 + ch) * a.hv + vh) * (int64_t)ChunkWs<E>::kBytes,
+    copy_linear<St::kWsBytes, NW>(a.ws + ((slot0 + ch) * a.hv + vh) * a.ws_item,
                                   to + St::kWs, w, lane);
   };
 
@@ -324,13 +333,28 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
 
     if constexpr (kStates) {
       // the state before the chunk: 16 bytes of one column per operand
-      char* img = a.s_img + ((slot0 + ch) * a.hv + vh) * img_bytes;
+      const int64_t item = (slot0 + ch) * a.hv + vh;
+      char* img = a.s_img + item * img_bytes;
+      if (col < dv_pad) {
 #pragma unroll
-      for (int kb = 0; kb < DK / M::kDepth; ++kb)
-        if (col + r < dv_pad)
+        for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+          const auto f = M::pack(&S[kb * M::kTiles]);
           *reinterpret_cast<typename M::Frag*>(img + (int64_t)(col + r) * KT::kRow +
-                                               (((4 * kb + g) ^ KT::key(col + r)) << 4)) =
-              M::pack(&S[kb * M::kTiles]);
+                                               (((4 * kb + g) ^ KT::key(col + r)) << 4)) = f;
+          if constexpr (sizeof(E) == 2) {
+            const uint4 h = __builtin_bit_cast(uint4, f);
+            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+            uint32_t low[2] = {0, 0};
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              low[x >> 2] |= low_byte(S[2 * kb + (x >> 2)][x & 3],
+                                      x & 1 ? hw[x >> 1] & 0xffff0000u : hw[x >> 1] << 16)
+                             << (8 * (x & 3));
+            *reinterpret_cast<uint2*>(a.s_low + low_at<DK>(item, dv_pad / 16, col / 16, kb, lane)) =
+                make_uint2(low[0], low[1]);
+          }
+        }
+      }
     }
     // K S (tokens x columns) and (Q S)^T (columns x tokens)
     f32x4 y[4], o[4];
@@ -368,7 +392,8 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
         if (!kStates) o[m][x] *= so;
       }
     }
-    // E = T Y, T lower triangular; of the parts' products those above 2^-24.  The state pass also
+    // E = T Y, T lower triangular; the parts' products down to the last part's
+    // size.  The state pass also
     // makes it transposed, to store it row by row.
     f32x4 e[4], et[4];
 #pragma unroll
@@ -382,7 +407,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
 #pragma unroll
         for (int m = kb * M::kTiles; m < 4; ++m) tf[m] = tt.rows(sm + St::kWs + p * TT::kBytes, m, kb);
 #pragma unroll
-        for (int x = 0; x < kPY && x + p < 3; ++x)
+        for (int x = 0; x + p < kPY; ++x)
 #pragma unroll
           for (int m = kb * M::kTiles; m < 4; ++m) {
             e[m] = M::mma(tf[m], ys.p[x], e[m]);

@@ -19,8 +19,10 @@
 //                   laid out like the forward's state pass (16 columns per wave, in accumulators)
 //   grad_kernel     one workgroup per chunk and key head: everything else.  The value heads that share
 //                   the key head add their dQ and dK in accumulators, in a fixed order: no atomics.
-// Every gradient is rounded once.  Rounding inside, bf16 storage: one bf16 part of each factor, two of
-// dE in dY and of E in M and N, which keeps each gradient's error within 1.5 times that of rounding it.
+// Every gradient is rounded once.  Rounding inside, bf16 storage: two bf16 parts of every factor, except
+// S, dS' and dY where dQ and dK take them (one part each: their rounding weighs less than the gradient's).
+// dg and dbeta are sums of signed terms that may cancel many times over: R, k . dS' e and <dS', S> are made
+// in adjoint_kernel from its accumulators, with S to 17 bits (a byte beside its bf16).
 #include "mamba_delta.h"
 
 namespace mamba {
@@ -37,12 +39,23 @@ struct BwdArgs {
   void* dg;            // (tokens, hv)
   void* dbeta;
   float* ds0;          // (nseq, hv, dk, dv) or NULL
+  float* sums;         // per chunk slot, value head and 16 columns: their part of AdjSums
 };
+
+// What the adjoint pass leaves for dg and dbeta, summed over 16 columns of the state: R_i and k_j . dS' e_j
+// of the chunk's tokens, and <dS', S>.
+constexpr int kSumR = 0, kSumKd = kC, kSumDot = 2 * kC, kAdjSums = 2 * kC + 16;
 
 // 8 (bf16) or 4 (fp32) consecutive values from one operand's accumulators
 template <typename E>
 __device__ __forceinline__ void store_values(E* p, const f32x4* c) {
   *reinterpret_cast<typename Mma<E>::Frag*>(p) = Mma<E>::pack(c);
+}
+
+// sum over the four groups
+__device__ __forceinline__ float across_groups(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
 }
 
 // ------------------------------------------------------------------ the adjoint of the state
@@ -52,10 +65,11 @@ struct AdjStage {
   using VT = ValueTile<E, 16 * NW>;
   static constexpr int kK = 0;
   static constexpr int kQ = KeyTile<E, DK>::kBytes;
-  static constexpr int kT = 2 * KeyTile<E, DK>::kBytes;
-  static constexpr int kP = kT + TriTile<E>::kBytes;
-  static constexpr int kGate = kP + TriTile<E>::kBytes;
-  static constexpr int kDO = kGate + 1024;
+  static constexpr int kWs = 2 * KeyTile<E, DK>::kBytes;  // T, P, gates
+  static constexpr int kP = kWs + ChunkWs<E>::kT;
+  static constexpr int kGate = kWs + ChunkWs<E>::kGate;
+  static constexpr int kPLow = kWs + ChunkWs<E>::kDecay;
+  static constexpr int kDO = kPLow + (Mma<E>::parts(2) - 1) * TriTile<E>::kBytes;
   static constexpr int kBytes = kDO + VT::kBytes;
   static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
 };
@@ -68,7 +82,9 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
   using TT = TriTile<E>;
   using VT = typename St::VT;
   using CW = ChunkWs<E>;
-  constexpr int kPE = M::parts(2);
+  using BB = BwdBlock<E>;
+  using ET = KeyTile<E, BB::kDB>;
+  constexpr int kP2 = M::parts(2);
   __shared__ __align__(1024) char smem[St::kCount * St::kBytes];
   const Args& a = b.f;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
@@ -107,16 +123,17 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
   auto copy = [&](int64_t ch, int st) {
     const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
     const uint32_t to = lds0 + st * St::kBytes;
-    const char* ws = a.ws + ((slot0 + ch) * a.hv + vh) * (int64_t)CW::kBytes;
+    const char* ws = a.ws + ((slot0 + ch) * a.hv + vh) * a.ws_item;
     ck(rows_buffer(kp + t * a.k_stride, n, a.k_stride, a.dk), to + St::kK, w);
     co(rows_buffer(dop + t * o_stride, n, o_stride, vcols), to + St::kDO, w);
-    copy_linear<TT::kBytes, NW>(ws, to + St::kT, w, lane);
-    copy_linear<CW::kP + 1024, NW>(ws + CW::kT, to + St::kP, w, lane);
+    copy_linear<CW::kDecay, NW>(ws, to + St::kWs, w, lane);
+    if constexpr (kP2 == 2) copy_linear<CW::kP, NW>(ws + CW::kPLow, to + St::kPLow, w, lane);
     cq(rows_buffer(qp + t * a.q_stride, n, a.q_stride, a.dk), to + St::kQ, w);
   };
 
   const int dv_pad = (a.dv + BwdBlock<E>::kDB - 1) / BwdBlock<E>::kDB * BwdBlock<E>::kDB;
   const int64_t img_bytes = (int64_t)dv_pad * KT::kRow;
+  const int64_t e_bytes = (int64_t)dv_pad / BB::kDB * BB::kEParts * BB::kE;
   const KT kt(lane);
   const TT tt(lane);
   const VT ot(lane, 16 * w);
@@ -127,32 +144,69 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
     if (St::kCount == 2 && ch > 0) copy(ch - 1, st ^ 1);
     const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
     const int n = (int)min((int64_t)kC, sp.len - ch * kC);
-    {
-      char* img = a.ds_img + ((slot0 + ch) * a.hv + vh) * img_bytes;
-#pragma unroll
-      for (int kb = 0; kb < DK / M::kDepth; ++kb)
-        if (col + r < dv_pad)
-          *reinterpret_cast<typename M::Frag*>(img + (int64_t)(col + r) * KT::kRow +
-                                               (((4 * kb + g) ^ KT::key(col + r)) << 4)) =
-              M::pack(&S[kb * M::kTiles]);
-    }
-    // dE = diag(c) K dS' + P^T dO
-    f32x4 e[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) e[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // dS' goes to its image.  The state before the chunk, in the same layout, meets it and its products
+    // with Q and K here, where dS' and dY are still accumulators.
+    const int64_t item = (slot0 + ch) * a.hv + vh;
+    const bool mine = col < dv_pad;
+    typename M::template Parts<kP2> ds[DK / M::kDepth], sf[DK / M::kDepth];
+    float dot = 0.f;
 #pragma unroll
     for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      const auto s = M::pack(&S[kb * M::kTiles]);
+      ds[kb] = M::template split<kP2>(&S[kb * M::kTiles]);
+      f32x4 f[M::kTiles];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) e[m] = M::mma(kt.rows(sm + St::kK, m, kb), s, e[m]);
+      for (int x = 0; x < M::kTiles; ++x) f[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (mine) {
+        const int64_t at = item * img_bytes + (int64_t)(col + r) * KT::kRow +
+                           (((4 * kb + g) ^ KT::key(col + r)) << 4);
+        *reinterpret_cast<typename M::Frag*>(a.ds_img + at) = ds[kb].p[0];
+        if constexpr (sizeof(E) == 2) {
+          const uint4 h = *reinterpret_cast<const uint4*>(a.s_img + at);
+          const uint2 l = *reinterpret_cast<const uint2*>(
+              a.s_low + low_at<DK>(item, dv_pad / 16, col / 16, kb, lane));
+          const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[2] = {l.x, l.y};
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            f[x >> 2][x & 3] =
+                with_low(x & 1 ? hw[x >> 1] & 0xffff0000u : hw[x >> 1] << 16, lw[x >> 2], x & 3);
+        } else {
+          f[0] = *reinterpret_cast<const f32x4*>(a.s_img + at);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < M::kTiles; ++y)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) dot = fmaf(S[kb * M::kTiles + y][x], f[y][x], dot);
+      sf[kb] = M::template split<kP2>(f);
     }
+    // K dS' both ways round, and (Q S)^T, (K S)^T: columns x tokens
+    f32x4 e[4], kd[4], qs[4], ks[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) e[m] = kd[m] = qs[m] = ks[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const auto kf = kt.rows(sm + St::kK, m, kb), qf = kt.rows(sm + St::kQ, m, kb);
+#pragma unroll
+        for (int p = 0; p < kP2; ++p) {
+          e[m] = M::mma(kf, ds[kb].p[p], e[m]);
+          kd[m] = M::mma(ds[kb].p[p], kf, kd[m]);
+          qs[m] = M::mma(sf[kb].p[p], qf, qs[m]);
+          ks[m] = M::mma(sf[kb].p[p], kf, ks[m]);
+        }
+      }
+    // dE = diag(c) K dS' + P^T dO
 #pragma unroll
     for (int m = 0; m < 4; ++m) e[m] *= lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
 #pragma unroll
     for (int ib = 0; ib < TT::kBlocks; ++ib) {
       const auto d = ot.operand(sm + St::kDO, ib);
 #pragma unroll
-      for (int m = 0; m < (ib + 1) * M::kTiles; ++m) e[m] = M::mma(tt.cols(sm + St::kP, m, ib), d, e[m]);
+      for (int m = 0; m < (ib + 1) * M::kTiles; ++m) {
+        e[m] = M::mma(tt.cols(sm + St::kP, m, ib), d, e[m]);
+        if constexpr (kP2 == 2) e[m] = M::mma(tt.cols(sm + St::kPLow, m, ib), d, e[m]);
+      }
     }
     // dY = T^T dE, and transposed for the store
     f32x4 y[4], yt[4];
@@ -160,17 +214,21 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
     for (int m = 0; m < 4; ++m) y[m] = yt[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ib = 0; ib < TT::kBlocks; ++ib) {
-      const auto es = M::template split<kPE>(&e[ib * M::kTiles]);
+      const auto es = M::template split<kP2>(&e[ib * M::kTiles]);
 #pragma unroll
-      for (int m = 0; m < (ib + 1) * M::kTiles; ++m) {
-        const auto tf = tt.cols(sm + St::kT, m, ib);
+      for (int m = 0; m < (ib + 1) * M::kTiles; ++m)
 #pragma unroll
-        for (int p = 0; p < kPE; ++p) {
-          y[m] = M::mma(tf, es.p[p], y[m]);
-          yt[m] = M::mma(es.p[p], tf, yt[m]);
+        for (int p = 0; p < kP2; ++p) {
+          const auto tf = tt.cols(sm + St::kWs + p * TT::kBytes, m, ib);
+#pragma unroll
+          for (int x = 0; x + p < kP2; ++x) {
+            y[m] = M::mma(tf, es.p[x], y[m]);
+            yt[m] = M::mma(es.p[x], tf, yt[m]);
+          }
         }
-      }
     }
+    // token 16 m + r, columns col + 4 g .. +3
+    float* sums = b.sums + (item * (dv_pad / 16) + col / 16) * kAdjSums;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int t = 16 * m + r;
@@ -182,7 +240,39 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
         else
           *reinterpret_cast<f32x4*>(dst) = yt[m];
       }
+      const float eg = lds_read<float>(sm + St::kGate + t * 4);
+      float rr = 0.f, kk = 0.f;
+      if (mine) {
+        f32x4 ev = {0.f, 0.f, 0.f, 0.f}, od;
+        const int cw = (col + 4 * g) % BB::kDB * (int)sizeof(E);
+        const char* img = a.e_img + item * e_bytes + (int64_t)((col + 4 * g) / BB::kDB) * BB::kEParts * BB::kE +
+                          t * ET::kRow + (((cw >> 4) ^ ET::key(t)) << 4) + (cw & 15);
+        const lds_ptr op = sm + St::kDO + t * VT::kRow + (16 * w + 4 * g) * (int)sizeof(E);
+        if constexpr (sizeof(E) == 2) {
+#pragma unroll
+          for (int p = 0; p < BB::kEParts; ++p)
+            ev += __builtin_convertvector(*reinterpret_cast<const bf16x4*>(img + p * BB::kE), f32x4);
+          od = __builtin_convertvector(lds_read<bf16x4>(op), f32x4);
+        } else {
+          ev = *reinterpret_cast<const f32x4*>(img);
+          od = lds_read<f32x4>(op);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          rr = fmaf(a.scale * qs[m][x], od[x], fmaf(-ks[m][x], yt[m][x], rr));
+          kk = fmaf(kd[m][x], ev[x], kk);
+        }
+      }
+      rr = across_groups(rr * eg);
+      kk = across_groups(kk);
+      if (mine && g == 0) {
+        sums[kSumR + t] = rr;
+        sums[kSumKd + t] = kk;
+      }
     }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
+    if (mine && lane == 0) sums[kSumDot] = dot;
     // dS = exp(G_64) dS' + Q^T diag(scale exp G) dO - K^T diag(exp G) dY
     const float last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
     f32x4 o[4];
@@ -196,11 +286,17 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
     for (int m = 0; m < DK / 16; ++m) S[m] *= last;
 #pragma unroll
     for (int kb = 0; kb < TT::kBlocks; ++kb) {
-      const auto of = M::pack(&o[kb * M::kTiles]), yf = M::pack(&y[kb * M::kTiles]);
+      const auto of = M::template split<kP2>(&o[kb * M::kTiles]);
+      const auto yf = M::template split<kP2>(&y[kb * M::kTiles]);
 #pragma unroll
-      for (int m = 0; m < DK / 16; ++m) S[m] = M::mma(kt.cols(sm + St::kQ, m, kb), of, S[m]);
+      for (int m = 0; m < DK / 16; ++m) {
+        const auto qf = kt.cols(sm + St::kQ, m, kb), kf = kt.cols(sm + St::kK, m, kb);
 #pragma unroll
-      for (int m = 0; m < DK / 16; ++m) S[m] = M::mma(kt.cols(sm + St::kK, m, kb), yf, S[m]);
+        for (int p = 0; p < kP2; ++p) {
+          S[m] = M::mma(qf, of.p[p], S[m]);
+          S[m] = M::mma(kf, yf.p[p], S[m]);
+        }
+      }
     }
     if (St::kCount == 1 && ch > 0) {
       __syncthreads();  // every wave has read the stage
@@ -228,11 +324,6 @@ __device__ __forceinline__ float group_sum(float v) {
   v += dpp_row<0x121>(v);
   return v;
 }
-// sum over the four groups
-__device__ __forceinline__ float across_groups(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
 // sum over lanes lane .. 63
 __device__ __forceinline__ float wave_suffix(float v, int lane) {
 #pragma unroll
@@ -254,12 +345,12 @@ struct GradSmem {
   static constexpr int kS = kE + B::kEParts * B::kE;
   static constexpr int kDS = kS + B::kDB * KeyTile<E, DK>::kRow;
   static constexpr int kB1 = kDS + B::kDB * KeyTile<E, DK>::kRow;
-  static constexpr int kB2 = kB1 + TriTile<E>::kBytes;
-  static constexpr int kGate = kB2 + TriTile<E>::kBytes;  // gates and decays: 2 KB
+  static constexpr int kBParts = Mma<E>::parts(2);
+  static constexpr int kB2 = kB1 + kBParts * TriTile<E>::kBytes;
+  static constexpr int kGate = kB2 + kBParts * TriTile<E>::kBytes;  // gates and decays: 2 KB
   static constexpr int kSums = kGate + 2048;              // per wave: column sums of X and of dbeta
-  static constexpr int kTok = kSums + 4 * 2 * kC * 4;     // per token: R + row sum of X, k . dS' e
-  static constexpr int kDot = kTok + 2 * kC * 4;
-  static constexpr int kBytes = kDot + 64;
+  static constexpr int kTok = kSums + 4 * 2 * kC * 4;     // per token: row sum of X
+  static constexpr int kBytes = kTok + kC * 4;
 };
 
 template <typename E, int DK>
@@ -271,7 +362,7 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
   using BB = BwdBlock<E>;
   using ET = KeyTile<E, BB::kDB>;
   using CW = ChunkWs<E>;
-  constexpr int kTiles = DK / 16;
+  constexpr int kTiles = DK / 16, kBP = Sm::kBParts;
   __shared__ __align__(1024) char smem[Sm::kBytes];
   const Args& a = b.f;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
@@ -330,7 +421,6 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
     for (int jt = 0; jt < 4; ++jt) Mt[jt] = Nt[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) sdo[m] = sdy[m] = dse[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float dot = 0.f;  // this thread's part of <dS', S>
     for (int db = 0; db < blocks; ++db) {
       __syncthreads();  // the tiles of the block before have been read
       const int cols = min(a.dv - db * BB::kDB, BB::kDB);
@@ -343,12 +433,14 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
       constexpr int kBlock = BB::kDB * KT::kRow;
       copy_linear<kBlock, 4>(a.s_img + item * img_bytes + (int64_t)db * kBlock, lds0 + Sm::kS, w, lane);
       copy_linear<kBlock, 4>(a.ds_img + item * img_bytes + (int64_t)db * kBlock, lds0 + Sm::kDS, w, lane);
-      if (db == 0) copy_linear<2048, 4>(a.ws + item * (int64_t)CW::kBytes + CW::kGate, lds0 + Sm::kGate, w, lane);
+      if (db == 0) copy_linear<2048, 4>(a.ws + item * a.ws_item + CW::kGate, lds0 + Sm::kGate, w, lane);
       copies_done();
 #pragma unroll
       for (int kb = 0; kb < BB::kDB / M::kDepth; ++kb) {
         const auto of = et.rows(sm + Sm::kDO, w, kb), yf = et.rows(sm + Sm::kDY, w, kb);
-        const auto ef = et.rows(sm + Sm::kE, w, kb);
+        typename M::Frag ef[BB::kEParts];
+#pragma unroll
+        for (int p = 0; p < BB::kEParts; ++p) ef[p] = et.rows(sm + Sm::kE + p * BB::kE, w, kb);
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
           if (jt <= w) {
@@ -364,14 +456,10 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
           const auto sf = kt.template cols<true>(sm + Sm::kS, m, kb);
           sdo[m] = M::mma(sf, of, sdo[m]);
           sdy[m] = M::mma(sf, yf, sdy[m]);
-          dse[m] = M::mma(kt.template cols<true>(sm + Sm::kDS, m, kb), ef, dse[m]);
-        }
-      }
-      for (int x = threadIdx.x; x < kBlock / 16; x += 256) {
-        const auto u = lds_read<typename M::Frag>(sm + Sm::kS + 16 * x);
-        const auto v = lds_read<typename M::Frag>(sm + Sm::kDS + 16 * x);
+          const auto df = kt.template cols<true>(sm + Sm::kDS, m, kb);
 #pragma unroll
-        for (int y = 0; y < 16 / (int)sizeof(E); ++y) dot = fmaf((float)u[y], (float)v[y], dot);
+          for (int p = 0; p < BB::kEParts; ++p) dse[m] = M::mma(df, ef[p], dse[m]);
+        }
       }
     }
     // B1, B2, and the sums that reach dbeta and dg
@@ -412,71 +500,70 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
 #pragma unroll
     for (int kb = 0; kb < TT::kBlocks; ++kb)
       if (16 * w >= kb * M::kDepth) {
-        const auto f1 = M::pack(&b1[kb * M::kTiles]), f2 = M::pack(&b2[kb * M::kTiles]);
+        const auto f1 = M::template split<kBP>(&b1[kb * M::kTiles]);
+        const auto f2 = M::template split<kBP>(&b2[kb * M::kTiles]);
         const int at = TT::word_at(kb, i, g);
-        *reinterpret_cast<typename M::Frag*>(smem + Sm::kB1 + at) = f1;
-        *reinterpret_cast<typename M::Frag*>(smem + Sm::kB2 + at) = f2;
+#pragma unroll
+        for (int p = 0; p < kBP; ++p) {
+          *reinterpret_cast<typename M::Frag*>(smem + Sm::kB1 + p * TT::kBytes + at) = f1.p[p];
+          *reinterpret_cast<typename M::Frag*>(smem + Sm::kB2 + p * TT::kBytes + at) = f2.p[p];
+        }
         // sums over j: this wave's own tiles
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
           const auto kf = kt.cols(sm + Sm::kK, m, kb);
-          dQ[m] = M::mma(kf, f1, dQ[m]);
-          dK[m] = M::mma(kf, f2, dK[m]);
-        }
-      }
-    // the state's terms, and their dots with q_i and k_i
-    const float eg = lds_read<float>(sm + Sm::kGate + 4 * i), ci = lds_read<float>(sm + Sm::kGate + 4 * (kC + i));
-    float rdot = 0.f, kd = 0.f;
 #pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      const auto ki = kt.rows(sm + Sm::kK, w, kb), qi = kt.rows(sm + Sm::kQ, w, kb);
-#pragma unroll
-      for (int y = 0; y < M::kTiles; ++y) {
-        const int m = kb * M::kTiles + y;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          float kx, qx;
-          if constexpr (sizeof(E) == 2) {
-            kx = (float)ki[4 * y + x];
-            qx = (float)qi[4 * y + x];
-          } else {
-            kx = ki[x];
-            qx = qi[x];
+          for (int p = 0; p < kBP; ++p) {
+            dQ[m] = M::mma(kf, f1.p[p], dQ[m]);
+            dK[m] = M::mma(kf, f2.p[p], dK[m]);
           }
-          const float so = a.scale * eg * sdo[m][x], sy = -eg * sdy[m][x];
-          rdot = fmaf(qx, so, fmaf(kx, sy, rdot));
-          kd = fmaf(kx, dse[m][x], kd);
-          dQ[m][x] += so;
-          dK[m][x] += fmaf(ci, dse[m][x], sy);
         }
       }
-    }
-    rdot = across_groups(rdot);
-    kd = across_groups(kd);
-    if (g == 0) {
-      float* tok = reinterpret_cast<float*>(smem + Sm::kTok);
-      tok[i] = rdot + row_x;
-      tok[kC + i] = kd;
-    }
+    // the state's terms
+    const float eg = lds_read<float>(sm + Sm::kGate + 4 * i), ci = lds_read<float>(sm + Sm::kGate + 4 * (kC + i));
+    const float seg = a.scale * eg;
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
-    if (lane == 0) reinterpret_cast<float*>(smem + Sm::kDot)[w] = dot;
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        dQ[m][x] = fmaf(seg, sdo[m][x], dQ[m][x]);
+        dK[m][x] = fmaf(ci, dse[m][x], fmaf(-eg, sdy[m][x], dK[m][x]));
+      }
+    if (g == 0) {
+      reinterpret_cast<float*>(smem + Sm::kTok)[i] = row_x;
+    }
     __syncthreads();
     // sums over i: rows i of B1 and B2 at and below this wave's tile
 #pragma unroll
     for (int ib = 0; ib < TT::kBlocks; ++ib)
       if (16 * w < (ib + 1) * M::kDepth) {
-        const auto f1 = tt.cols(sm + Sm::kB1, w, ib), f2 = tt.cols(sm + Sm::kB2, w, ib);
+        typename M::Frag f1[kBP], f2[kBP];
+#pragma unroll
+        for (int p = 0; p < kBP; ++p) {
+          f1[p] = tt.cols(sm + Sm::kB1 + p * TT::kBytes, w, ib);
+          f2[p] = tt.cols(sm + Sm::kB2 + p * TT::kBytes, w, ib);
+        }
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
-          dK[m] = M::mma(kt.cols(sm + Sm::kQ, m, ib), f1, dK[m]);
-          dK[m] = M::mma(kt.cols(sm + Sm::kK, m, ib), f2, dK[m]);
+          const auto qf = kt.cols(sm + Sm::kQ, m, ib), kf = kt.cols(sm + Sm::kK, m, ib);
+#pragma unroll
+          for (int p = 0; p < kBP; ++p) {
+            dK[m] = M::mma(qf, f1[p], dK[m]);
+            dK[m] = M::mma(kf, f2[p], dK[m]);
+          }
         }
       }
     if (w == 0) {
       const float* sums = reinterpret_cast<const float*>(smem + Sm::kSums);
       const float* tok = reinterpret_cast<const float*>(smem + Sm::kTok);
-      const float* dots = reinterpret_cast<const float*>(smem + Sm::kDot);
+      const int cbs = blocks * BB::kDB / 16;
+      const float* adj = b.sums + item * cbs * kAdjSums;
+      float rt = 0.f, kdt = 0.f, dot = 0.f;
+      for (int x = 0; x < cbs; ++x) {
+        rt += adj[x * kAdjSums + kSumR + lane];
+        kdt += adj[x * kAdjSums + kSumKd + lane];
+        dot += adj[x * kAdjSums + kSumDot];
+      }
       const float* gate = reinterpret_cast<const float*>(smem + Sm::kGate);
       const float* dec = gate + 256;
       float cx = 0.f, cb = 0.f;
@@ -485,8 +572,8 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
         cb += sums[x * 2 * kC + kC + lane];
       }
       const float e = exp_f32((dec[kC - 1] - dec[lane]) + (dec[2 * kC - 1] - dec[kC + lane]));
-      const float kdt = tok[kC + lane], z = gate[kC + lane] * kdt;
-      const float after = wave_suffix(tok[lane] - cx, lane);
+      const float z = gate[kC + lane] * kdt;
+      const float after = wave_suffix(rt + (tok[lane] - cx), lane);
       float before = z;  // sum of z over the tokens before
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) {
@@ -494,7 +581,7 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
         if (lane >= m) before += t;
       }
       before = __shfl_up(before, 1);
-      const float whole = gate[2 * kC] * ((dots[0] + dots[1]) + (dots[2] + dots[3]));
+      const float whole = gate[2 * kC] * dot;
       if (lane < n) {
         const int64_t at = (t0 + lane) * a.hv + vh;
         st_out(static_cast<E*>(b.dg), at, whole + (lane ? before : 0.f) + after);
@@ -534,7 +621,7 @@ int launch_bwd(const BwdArgs& b, hipStream_t s) {
 }
 
 struct BwdLayout {  // workspace regions in bytes
-  size_t e, s, ds, total;
+  size_t item, e, s, ds, low, sums, total;
 };
 template <typename E>
 BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
@@ -542,10 +629,13 @@ BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
   const size_t blocks = (size_t)BwdBlock<E>::blocks(d->dv);
   const size_t row = (d->dk <= 64 ? 64 : 128) * sizeof(E);
   BwdLayout l;
-  l.e = items * ChunkWs<E>::kBytes;
+  l.item = ChunkWs<E>::kBwdBytes;
+  l.e = items * l.item;
   l.s = l.e + items * blocks * BwdBlock<E>::kEParts * BwdBlock<E>::kE;
   l.ds = l.s + items * blocks * BwdBlock<E>::kDB * row;
-  l.total = l.ds + items * blocks * BwdBlock<E>::kDB * row;
+  l.low = l.ds + items * blocks * BwdBlock<E>::kDB * row;
+  l.sums = l.low + (sizeof(E) == 2 ? items * blocks * BwdBlock<E>::kDB * (row / 2) : 0);
+  l.total = l.sums + items * blocks * (BwdBlock<E>::kDB / 16) * kAdjSums * sizeof(float);
   return l;
 }
 BwdLayout layout(const mamba_delta_dims* d, bool packed) {
@@ -588,9 +678,12 @@ int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, 
   BwdArgs b = {};
   b.f = make_args(dims, scale, q, k, v, g, beta, initial_state, seq_offsets);
   b.f.ws = static_cast<char*>(workspace);
+  b.f.ws_item = l.item;
   b.f.e_img = b.f.ws + l.e;
   b.f.s_img = b.f.ws + l.s;
   b.f.ds_img = b.f.ws + l.ds;
+  b.f.s_low = b.f.ws + l.low;
+  b.sums = reinterpret_cast<float*>(b.f.ws + l.sums);
   b.dout = dout;
   b.dlast = dlast;
   b.dq = dq;

@@ -10,7 +10,7 @@
 //
 // All four are bound by memory: each input is read once into registers and each output written
 // once.  A unit (one group of one row) belongs to a team of T lanes, T = 8..1024, that holds it as
-// R vectors of 8 values per lane; sums and statistics are fp32.  Vectors are read and written as
+// R vectors of 8 values per lane; sums and statistics are fp32, the gradients' fp64.  Vectors are read and written as
 // 16-byte words at any address (rows of odd length start anywhere), the last one value by value.
 // The weights' gradients are sums over all units: a team keeps its columns' sums in registers over
 // the units it visits, the teams of a workgroup add theirs in LDS, each workgroup writes one
@@ -102,12 +102,12 @@ struct Cols {
 
 // Sum of v over the team, in every lane.  T > 64 goes through LDS; the two slots alternate so that
 // one barrier per call is enough (a slot is written again only after the barrier of the next call).
-template <int T>
+template <int T, typename V>
 struct TeamSum {
-  float (*slot)[kBlock<T> / 64][2];
+  V (*slot)[kBlock<T> / 64][2];
   int turn = 0;
   template <int N>
-  __device__ __forceinline__ void operator()(float (&v)[N]) {
+  __device__ __forceinline__ void operator()(V (&v)[N]) {
     static_assert(N <= 2, "slots hold two sums");
 #pragma unroll
     for (int m = 1; m < (T < 64 ? T : 64); m *= 2)
@@ -133,6 +133,13 @@ struct TeamSum {
 // sigmoid(z); exp(-z) overflows to infinity and the reciprocal is then 0
 __device__ __forceinline__ float sigmoid_f32(float z) {
   return __builtin_amdgcn_rcpf(1.f + fast_exp2(-z * kLog2e));
+}
+
+// dh - v m: what is left of dh when its part along v is taken out.  Next to nothing is left where a
+// unit has few values or dh is nearly parallel to v, so that m comes from sums in fp64 and the difference
+// is taken there (fp64 fused multiply-adds run at the rate of unpacked fp32 ones on this target).
+__device__ __forceinline__ float minus(float dh, float v, double m) {
+  return (float)fma(-(double)v, m, (double)dh);
 }
 
 // Adds the workgroup's per-team column sums and writes them as one row of partials.
@@ -191,7 +198,7 @@ __device__ __forceinline__ Unit unit_of(const GatedArgs& a, uint32_t u) {
 template <typename E, int T, int R>
 __global__ __launch_bounds__(kBlock<T>) void gated_norm_kernel(GatedArgs a, uint32_t units) {
   __shared__ float slot[2][kBlock<T> / 64][2];
-  TeamSum<T> team_sum{slot};
+  TeamSum<T, float> team_sum{slot};
   const Cols<T, R> cols{(int)(threadIdx.x % T), a.dim};
   const uint32_t u = blockIdx.x * (kBlock<T> / T) + threadIdx.x / T;
   const bool live = u < units;
@@ -228,9 +235,9 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_kernel(GatedArgs a, uint
 template <typename E, int T, int R>
 __global__ __launch_bounds__(kBlock<T>) void gated_norm_bwd_kernel(GatedArgs a, uint32_t units) {
   constexpr int kTeams = kBlock<T> / T;
-  __shared__ float slot[2][kBlock<T> / 64][2];
+  __shared__ double slot[2][kBlock<T> / 64][2];
   __shared__ float sum[kTeams > 1 ? 8 * T * R : 1];
-  TeamSum<T> team_sum{slot};
+  TeamSum<T, double> team_sum{slot};
   const Cols<T, R> cols{(int)(threadIdx.x % T), a.dim};
   float w[R][8], acc[R][8];
   cols.load(a.w + (a.per_group ? (int64_t)blockIdx.y * a.dim : 0), w);
@@ -238,7 +245,7 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_bwd_kernel(GatedArgs a, 
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[r][k] = 0.f;
-  const float inv = 1.f / a.dim;
+  const double inv = 1.0 / a.dim;
   // every team runs the same number of turns (the reductions hold barriers)
   for (uint32_t base = blockIdx.x * kTeams; base < units; base += gridDim.x * kTeams) {
     const uint32_t u = base + threadIdx.x / T;
@@ -251,7 +258,7 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_bwd_kernel(GatedArgs a, 
     if (a.z)
       cols.load(static_cast<const E*>(a.z) + at.row * a.z_stride + (int64_t)at.grp * a.dim, z, live);
     // v = the normed value (y, or y silu(z)); s = sum v^2, sum dh v
-    float s[2] = {0.f, 0.f};
+    double s[2] = {0.0, 0.0};
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -259,11 +266,12 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_bwd_kernel(GatedArgs a, 
         const float g = a.z ? silu_f32(z[r][k]) : 1.f;
         const float v = a.gate_first ? y[r][k] * g : y[r][k];
         const float dh = d[r][k] * w[r][k] * (a.gate_first ? 1.f : g);
-        s[0] = fmaf(v, v, s[0]);
-        s[1] = fmaf(dh, v, s[1]);
+        s[0] = fma((double)v, (double)v, s[0]);
+        s[1] = fma((double)dh, (double)v, s[1]);
       }
     team_sum(s);
-    const float rs = rsqrtf(s[0] * inv + a.eps), m = s[1] * rs * rs * inv;
+    const double r2 = 1.0 / fma(s[0], inv, (double)a.eps), m = s[1] * r2 * inv;
+    const float rs = sqrtf((float)r2);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -272,7 +280,7 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_bwd_kernel(GatedArgs a, 
         const float g = a.z ? z[r][k] * sg : 1.f;
         const float slope = a.z ? sg * fmaf(z[r][k], 1.f - sg, 1.f) : 0.f;  // silu'(z)
         if (a.gate_first) {
-          const float v = y[r][k] * g, da = rs * (d[r][k] * w[r][k] - v * m);
+          const float v = y[r][k] * g, da = rs * minus(d[r][k] * w[r][k], v, m);
           acc[r][k] = fmaf(d[r][k], v * rs, acc[r][k]);
           z[r][k] = da * y[r][k] * slope;
           y[r][k] = da * g;
@@ -280,7 +288,7 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_bwd_kernel(GatedArgs a, 
           const float h = y[r][k] * rs, dg = d[r][k] * g;
           acc[r][k] = fmaf(dg, h, acc[r][k]);
           z[r][k] = d[r][k] * h * w[r][k] * slope;
-          y[r][k] = rs * (dg * w[r][k] - y[r][k] * m);
+          y[r][k] = rs * minus(d[r][k] * w[r][k] * g, y[r][k], m);
         }
       }
     if (live) {
@@ -313,7 +321,7 @@ struct AddArgs {
 template <typename E, typename S, int T, int R>
 __global__ __launch_bounds__(kBlock<T>) void add_norm_kernel(AddArgs a) {
   __shared__ float slot[2][kBlock<T> / 64][2];
-  TeamSum<T> team_sum{slot};
+  TeamSum<T, float> team_sum{slot};
   const Cols<T, R> cols{(int)(threadIdx.x % T), a.dim};
   const int64_t row = (int64_t)blockIdx.x * (kBlock<T> / T) + threadIdx.x / T;
   const bool live = row < a.rows;
@@ -367,16 +375,16 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_kernel(AddArgs a) {
 template <typename E, typename S, int T, int R>
 __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
   constexpr int kTeams = kBlock<T> / T;
-  __shared__ float slot[2][kBlock<T> / 64][2];
+  __shared__ double slot[2][kBlock<T> / 64][2];
   __shared__ float sum[kTeams > 1 ? 8 * T * R : 1];
-  TeamSum<T> team_sum{slot};
+  TeamSum<T, double> team_sum{slot};
   const Cols<T, R> cols{(int)(threadIdx.x % T), a.dim};
   float aw[R][8], ah[R][8];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int k = 0; k < 8; ++k) aw[r][k] = ah[r][k] = 0.f;
-  const float inv = 1.f / a.dim;
+  const double inv = 1.0 / a.dim;
   for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows;
        base += (int64_t)gridDim.x * kTeams) {
     const int64_t row = base + threadIdx.x / T;
@@ -392,16 +400,17 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[r][k] = 0.f;
     cols.load(static_cast<const E*>(a.dout) + at, d, live);
-    float rx = 1.f;
+    double rx2 = 1.0;
     if (a.post) {
-      float s[1] = {0.f};
+      double s[1] = {0.0};
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s[0] = fmaf(x[r][k], x[r][k], s[0]);
+        for (int k = 0; k < 8; ++k) s[0] = fma((double)x[r][k], (double)x[r][k], s[0]);
       team_sum(s);
-      rx = rsqrtf(s[0] * inv + a.eps);
+      rx2 = 1.0 / fma(s[0], inv, (double)a.eps);
     }
+    const float rx = sqrtf((float)rx2);  // the normed x is x rx
     // p = scale post (the weight of the normed x in r); v = r; d = dout w
     if (a.post) {
       cols.load(a.post, p);
@@ -419,7 +428,7 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) p[r][k] *= t[r][k];
     }
-    float s[2] = {0.f, 0.f};
+    double s[2] = {0.0, 0.0};
     {
       float w[R][8];
       cols.load(a.w, w);
@@ -427,19 +436,19 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          x[r][k] *= rx;  // the normed x
-          v[r][k] = fmaf(p[r][k], x[r][k], v[r][k]);
-          s[0] = fmaf(v[r][k], v[r][k], s[0]);
-          s[1] = fmaf(d[r][k] * w[r][k], v[r][k], s[1]);
+          v[r][k] = fmaf(p[r][k], x[r][k] * rx, v[r][k]);
+          s[0] = fma((double)v[r][k], (double)v[r][k], s[0]);
+          s[1] = fma((double)(d[r][k] * w[r][k]), (double)v[r][k], s[1]);
         }
       team_sum(s);
-      const float rs = rsqrtf(s[0] * inv + a.eps), m = s[1] * rs * rs * inv;
+      const double r2 = 1.0 / fma(s[0], inv, (double)a.eps), m = s[1] * r2 * inv;
+      const float rs = sqrtf((float)r2);
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           aw[r][k] = fmaf(d[r][k], v[r][k] * rs, aw[r][k]);
-          v[r][k] = rs * (d[r][k] * w[r][k] - v[r][k] * m);
+          v[r][k] = rs * minus(d[r][k] * w[r][k], v[r][k], m);
         }
     }
     if (a.dres) {
@@ -457,20 +466,20 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ah[r][k] = fmaf(v[r][k], x[r][k], ah[r][k]);
+        for (int k = 0; k < 8; ++k) ah[r][k] = fmaf(v[r][k], x[r][k] * rx, ah[r][k]);
     }
     if (a.post) {
-      float t[1] = {0.f};
+      double t[1] = {0.0};
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[0] = fmaf(v[r][k] * p[r][k], x[r][k], t[0]);
+        for (int k = 0; k < 8; ++k) t[0] = fma((double)(v[r][k] * p[r][k]), (double)x[r][k], t[0]);
       team_sum(t);
-      const float m = t[0] * inv;
+      const double m = t[0] * rx2 * inv;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[r][k] = rx * (v[r][k] * p[r][k] - x[r][k] * m);
+        for (int k = 0; k < 8; ++k) x[r][k] = rx * minus(v[r][k] * p[r][k], x[r][k], m);
     } else {
 #pragma unroll
       for (int r = 0; r < R; ++r)
