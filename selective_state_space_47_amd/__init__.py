@@ -20,5 +20,6 @@ __all__ = ["mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # the next use finds it without this detour
+        return value
     raise AttributeError(name)

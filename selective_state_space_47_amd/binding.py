@@ -626,17 +626,34 @@ _DELTA_CACHE = {}
 
 def _meta(t):
     """What the checks look at: two tensors of equal metadata pass or fail alike."""
+    if t is None:
+        return None
     if not isinstance(t, torch.Tensor):
         return type(t)
     return t.shape, t.stride(), t.dtype, t.get_device()
 
 
+# device that a launch would go to, without torch.cuda's own checks (a host-side cost per call)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream) on `dev` and its current stream; raises what the library refuses."""
+    if _current_device() == dev.index:
+        st = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    if st:
+        _raise(st)
+
+
 def _delta_checked(q, k, v, g, beta, others, packed, n_seq, lead):
-    """Dims and workspace sizes (forward, backward) of a call on these tensors; raises for tensors that do not belong
+    """Dims, their reference and workspace sizes (forward, backward) of a call on these tensors; raises for tensors that do not belong
     together.  `others`: (tensor or None, name, shape function of (batch, Hv, dk, dv), dtype or None
     for the io dtype)."""
     key = (_meta(q), _meta(k), _meta(v), _meta(g), _meta(beta),
-           tuple(_meta(o[0]) for o in others), packed, n_seq, lead)
+           packed, n_seq, lead, *[_meta(t[0]) for t in others])
     hit = _DELTA_CACHE.get(key)
     if hit is not None:
         return hit
@@ -671,8 +688,9 @@ def _delta_checked(q, k, v, g, beta, others, packed, n_seq, lead):
         _check(t, name, shape((batch, *tokens), Hk, Hv, dk, dv), dt or io, dev)
     dm = mamba_delta_dims(batch, L, Hk, Hv, dk, dv, _token_stride(q, "q", vec),
                           _token_stride(k, "k", vec), _token_stride(v, "v", vec), code, 0)
-    hit = (dm, int(lib().mamba_delta_workspace_bytes(ctypes.byref(dm), int(packed))),
-           int(lib().mamba_delta_bwd_workspace_bytes(ctypes.byref(dm), int(packed))))
+    ref = ctypes.byref(dm)
+    hit = (dm, ref, int(lib().mamba_delta_workspace_bytes(ref, int(packed))),
+           int(lib().mamba_delta_bwd_workspace_bytes(ref, int(packed))))
     if len(_DELTA_CACHE) >= 1024:
         _DELTA_CACHE.clear()
     _DELTA_CACHE[key] = hit
@@ -717,25 +735,21 @@ def mamba_delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, seq_offset
     """
     n_seq = _offsets_count(seq_offsets, q)
     packed = n_seq is not None
-    dm, ws_bytes, _ = _delta_checked(q, k, v, g, beta,
-                                     ((initial_state, "initial_state", _state_shape, torch.float32),
-                                      (out, "out", _out_shape, None),
-                                      (last_state, "last_state", _state_shape, torch.float32)),
-                                     packed, n_seq, 1 if packed else 2)
+    dm, ref, ws_bytes, _ = _delta_checked(
+        q, k, v, g, beta, ((initial_state, "initial_state", _state_shape, torch.float32),
+                           (out, "out", _out_shape, None),
+                           (last_state, "last_state", _state_shape, torch.float32)),
+        packed, n_seq, 1 if packed else 2)
     dev = q.device
     if out is None:
-        out = torch.empty(v.shape, dtype=q.dtype, device=dev)
+        out = q.new_empty(v.shape)
     if return_last_state and last_state is None:
         last_state = torch.empty((dm.batch, dm.v_heads, dm.dk, dm.dv), dtype=torch.float32,
                                  device=dev)
     workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
-    with _on(dev):
-        st = lib().mamba_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                   _ptr(initial_state), _ptr(seq_offsets),
-                                   dm.dk ** -0.5 if scale is None else scale, _ptr(out),
-                                   _ptr(last_state), ctypes.byref(dm), _ptr(workspace), ws_len,
-                                   _stream(dev))
-    _raise(st)
+    _call(dev, lib().mamba_delta_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+          _ptr(initial_state), _ptr(seq_offsets), dm.dk ** -0.5 if scale is None else scale,
+          _ptr(out), _ptr(last_state), ref, _ptr(workspace), ws_len)
     return (out, last_state) if return_last_state else out
 
 
@@ -747,16 +761,13 @@ def mamba_delta_update(state, q, k, v, g, beta, scale=None, out=None):
     """
     if state is None:
         raise ValueError("state is required")
-    dm = _delta_checked(q, k, v, g, beta, ((state, "state", _state_shape, torch.float32),
-                                           (out, "out", _out_shape, None)), False, None, 1)[0]
-    dev = q.device
+    dm, ref, _, _ = _delta_checked(q, k, v, g, beta, ((state, "state", _state_shape, torch.float32),
+                                                      (out, "out", _out_shape, None)), False, None, 1)
     if out is None:
-        out = torch.empty(v.shape, dtype=q.dtype, device=dev)
-    with _on(dev):
-        st = lib().mamba_delta_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                      dm.dk ** -0.5 if scale is None else scale, _ptr(out),
-                                      ctypes.byref(dm), _stream(dev))
-    _raise(st)
+        out = q.new_empty(v.shape)
+    _call(q.device, lib().mamba_delta_update, state.data_ptr(), q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), g.data_ptr(), beta.data_ptr(), dm.dk ** -0.5 if scale is None else scale,
+          out.data_ptr(), ref)
     return out
 
 
@@ -789,7 +800,7 @@ def mamba_delta_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, seq_
     spec = (("dq", _qk_shape, None), ("dk", _qk_shape, None), ("dv", _out_shape, None),
             ("dg", _head_shape, None), ("dbeta", _head_shape, None),
             ("dinitial_state", _state_shape, torch.float32))
-    dm, _, ws_bytes = _delta_checked(
+    dm, ref, _, ws_bytes = _delta_checked(
         q, k, v, g, beta,
         ((initial_state, "initial_state", _state_shape, torch.float32), (dout, "dout", _out_shape, None),
          (dlast, "dlast", _state_shape, torch.float32),
@@ -802,14 +813,10 @@ def mamba_delta_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, seq_
             gr[name] = None if like is None else torch.empty(like.shape, dtype=like.dtype,
                                                              device=dev)
     workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
-    with _on(dev):
-        st = lib().mamba_delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                   _ptr(initial_state), _ptr(seq_offsets),
-                                   dm.dk ** -0.5 if scale is None else scale, _ptr(dout),
-                                   _ptr(dlast), _ptr(gr["dq"]), _ptr(gr["dk"]), _ptr(gr["dv"]),
-                                   _ptr(gr["dg"]), _ptr(gr["dbeta"]), _ptr(gr["dinitial_state"]),
-                                   ctypes.byref(dm), _ptr(workspace), ws_len, _stream(dev))
-    _raise(st)
+    _call(dev, lib().mamba_delta_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+          _ptr(initial_state), _ptr(seq_offsets), dm.dk ** -0.5 if scale is None else scale,
+          _ptr(dout), _ptr(dlast), _ptr(gr["dq"]), _ptr(gr["dk"]), _ptr(gr["dv"]), _ptr(gr["dg"]),
+          _ptr(gr["dbeta"]), _ptr(gr["dinitial_state"]), ref, _ptr(workspace), ws_len)
     return {n: gr[n] for n in ("dq", "dk", "dv", "dg", "dbeta", "dinitial_state")}
 
 
@@ -828,8 +835,8 @@ _NORM_CACHE = {}
 
 
 def _gated_checked(y, z, weight, gate_first, others):
-    """Dims and workspace size of a gated norm; `others`: (tensor or None, name, "rows"|"weight")."""
-    key = (_meta(y), _meta(z), _meta(weight), gate_first, tuple(_meta(o[0]) for o in others))
+    """Dims (by reference) and workspace size of a gated norm; `others`: (tensor or None, name, "rows"|"weight")."""
+    key = (_meta(y), _meta(z), _meta(weight), gate_first, *[_meta(t[0]) for t in others])
     hit = _NORM_CACHE.get(key)
     if hit is not None:
         return hit
@@ -857,7 +864,8 @@ def _gated_checked(y, z, weight, gate_first, others):
     dm = mamba_gated_norm_dims(rows, G, d, _row_stride(y, "y"),
                                0 if z is None else _row_stride(z, "z"), code,
                                G if per_group else 1, int(bool(gate_first)), 0)
-    hit = (dm, int(lib().mamba_gated_norm_bwd_workspace_bytes(ctypes.byref(dm))))
+    ref = ctypes.byref(dm)
+    hit = (ref, int(lib().mamba_gated_norm_bwd_workspace_bytes(ref)))
     if len(_NORM_CACHE) >= 1024:
         _NORM_CACHE.clear()
     _NORM_CACHE[key] = hit
@@ -875,14 +883,11 @@ def mamba_gated_norm_fwd(y, z, weight, eps=1e-5, gate_first=False, out=None):
     (dim,) or (groups, dim) float32.  norm(y) * weight * silu(z), or norm(y * silu(z)) * weight with
     gate_first.  Returns out (rows, groups, dim).
     """
-    dm, _ = _gated_checked(y, z, weight, gate_first, ((out, "out", "rows"),))
-    dev = y.device
+    ref, _ = _gated_checked(y, z, weight, gate_first, ((out, "out", "rows"),))
     if out is None:
-        out = torch.empty(y.shape, dtype=y.dtype, device=dev)
-    with _on(dev):
-        st = lib().mamba_gated_norm_fwd(_ptr(y), _ptr(z), _ptr(weight), eps, _ptr(out),
-                                        ctypes.byref(dm), _stream(dev))
-    _raise(st)
+        out = y.new_empty(y.shape)
+    _call(y.device, lib().mamba_gated_norm_fwd, y.data_ptr(), _ptr(z), weight.data_ptr(), eps,
+          out.data_ptr(), ref)
     return out
 
 
@@ -893,10 +898,10 @@ def mamba_gated_norm_bwd(y, z, weight, dout, eps=1e-5, gate_first=False, workspa
     if dout is None:
         raise ValueError("dout is required")
     g = dict(grads or {})
-    dm, ws_bytes = _gated_checked(y, z, weight, gate_first,
-                                  ((dout, "dout", "rows"), (g.get("dy"), "dy", "rows"),
-                                   (g.get("dz"), "dz", "rows"),
-                                   (g.get("dweight"), "dweight", "weight")))
+    ref, ws_bytes = _gated_checked(y, z, weight, gate_first,
+                                   ((dout, "dout", "rows"), (g.get("dy"), "dy", "rows"),
+                                    (g.get("dz"), "dz", "rows"),
+                                    (g.get("dweight"), "dweight", "weight")))
     dev = y.device
     if g.get("dy") is None:
         g["dy"] = torch.empty(y.shape, dtype=y.dtype, device=dev)
@@ -907,19 +912,16 @@ def mamba_gated_norm_bwd(y, z, weight, dout, eps=1e-5, gate_first=False, workspa
     if g.get("dweight") is None:
         g["dweight"] = torch.empty(weight.shape, dtype=torch.float32, device=dev)
     workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
-    with _on(dev):
-        st = lib().mamba_gated_norm_bwd(_ptr(y), _ptr(z), _ptr(weight), eps, _ptr(dout),
-                                        _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dweight"]),
-                                        ctypes.byref(dm), _ptr(workspace), ws_len, _stream(dev))
-    _raise(st)
+    _call(dev, lib().mamba_gated_norm_bwd, _ptr(y), _ptr(z), _ptr(weight), eps, _ptr(dout),
+          _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dweight"]), ref, _ptr(workspace), ws_len)
     return {n: g[n] for n in ("dy", "dz", "dweight")}
 
 
 def _add_checked(x, residual, vectors, others):
-    """Dims and workspace size of an add norm.  `vectors`: (tensor or None, name) of (dim,) float32;
+    """Dims (by reference), workspace size and residual type of an add norm.  `vectors`: (tensor or None, name) of (dim,) float32;
     `others`: (tensor or None, name, is of the residual's type)."""
-    key = (_meta(x), _meta(residual), tuple(_meta(t) for t, _ in vectors),
-           tuple(_meta(o[0]) for o in others))
+    key = (_meta(x), _meta(residual), *[_meta(t[0]) for t in vectors], None,
+           *[_meta(t[0]) for t in others])
     hit = _NORM_CACHE.get(key)
     if hit is not None:
         return hit
@@ -942,7 +944,8 @@ def _add_checked(x, residual, vectors, others):
     for t, name, of_res in others:
         _check(t, name, (rows, d), res if of_res else io, dev)
     dm = mamba_add_norm_dims(rows, d, code, res_code)
-    hit = (dm, int(lib().mamba_add_norm_bwd_workspace_bytes(ctypes.byref(dm))), res)
+    ref = ctypes.byref(dm)
+    hit = (ref, int(lib().mamba_add_norm_bwd_workspace_bytes(ref)), res)
     if len(_NORM_CACHE) >= 1024:
         _NORM_CACHE.clear()
     _NORM_CACHE[key] = hit
@@ -962,19 +965,16 @@ def mamba_add_norm_fwd(x, residual, weight, scale=None, post_weight=None, eps=1e
     weight, scale, post_weight: (dim,) float32.  Returns (out, r), r of the residual's type (of x's
     without one, or of residual_out's).
     """
-    dm, _, res = _add_checked(x, residual, ((weight, "weight"), (scale, "scale"),
-                                            (post_weight, "post_weight")),
-                              ((out, "out", False), (residual_out, "residual_out", True)))
-    dev = x.device
+    ref, _, res = _add_checked(x, residual, ((weight, "weight"), (scale, "scale"),
+                                             (post_weight, "post_weight")),
+                               ((out, "out", False), (residual_out, "residual_out", True)))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(x.shape)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=res, device=dev)
-    with _on(dev):
-        st = lib().mamba_add_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(scale),
-                                      _ptr(post_weight), eps, _ptr(out), _ptr(residual_out),
-                                      ctypes.byref(dm), _stream(dev))
-    _raise(st)
+        residual_out = (residual.new_empty(x.shape) if residual is not None
+                        else x.new_empty(x.shape))
+    _call(x.device, lib().mamba_add_norm_fwd, x.data_ptr(), _ptr(residual), weight.data_ptr(),
+          _ptr(scale), _ptr(post_weight), eps, out.data_ptr(), residual_out.data_ptr(), ref)
     return out, residual_out
 
 
@@ -987,7 +987,7 @@ def mamba_add_norm_bwd(x, residual, weight, dout, dresidual_out=None, scale=None
     if dout is None:
         raise ValueError("dout is required")
     g = dict(grads or {})
-    dm, ws_bytes, res = _add_checked(
+    ref, ws_bytes, res = _add_checked(
         x, residual, ((weight, "weight"), (scale, "scale"), (post_weight, "post_weight"),
                       (g.get("dweight"), "dweight"), (g.get("dscale"), "dscale"),
                       (g.get("dpost_weight"), "dpost_weight")),
@@ -1002,11 +1002,8 @@ def mamba_add_norm_bwd(x, residual, weight, dout, dresidual_out=None, scale=None
         elif g.get(name) is None:
             g[name] = torch.empty(like.shape, dtype=dt, device=dev)
     workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
-    with _on(dev):
-        st = lib().mamba_add_norm_bwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(scale),
-                                      _ptr(post_weight), eps, _ptr(dout), _ptr(dresidual_out),
-                                      _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
-                                      _ptr(g["dscale"]), _ptr(g["dpost_weight"]),
-                                      ctypes.byref(dm), _ptr(workspace), ws_len, _stream(dev))
-    _raise(st)
+    _call(dev, lib().mamba_add_norm_bwd, _ptr(x), _ptr(residual), _ptr(weight), _ptr(scale),
+          _ptr(post_weight), eps, _ptr(dout), _ptr(dresidual_out), _ptr(g["dx"]),
+          _ptr(g["dresidual"]), _ptr(g["dweight"]), _ptr(g["dscale"]), _ptr(g["dpost_weight"]), ref,
+          _ptr(workspace), ws_len)
     return {n: g[n] for n in ("dx", "dresidual", "dweight", "dscale", "dpost_weight")}
