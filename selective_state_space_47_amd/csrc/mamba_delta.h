@@ -265,6 +265,19 @@ __device__ __forceinline__ void copy_lds(i32x4 buf, uint32_t off, uint32_t lds) 
       : "memory");
 }
 constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer
+// Four values of one row, rounded to the storage type, to a buffer; an offset past it drops them (no
+// branch around the store, so that the chunk's loop stays one block for the scheduler).
+template <typename E>
+__device__ __forceinline__ void store_four(__amdgpu_buffer_rsrc_t buf, uint32_t off, f32x4 v) {
+  typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+  typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+  if constexpr (sizeof(E) == 2)
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(make_float2(v[0], v[1])),
+                                                pack_bf16(make_float2(v[2], v[3]))},
+                                          buf, off, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), buf, off, 0, 0);
+}
 // every copy of this wave has landed, and every wave of the workgroup has come here
 __device__ __forceinline__ void copies_done() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");

@@ -38,8 +38,7 @@ struct ChunkSmem {
     struct { E k[kC * kLd], q[kC * kLd]; } in;
     struct { float a[kC * kLf], t[kC * kLf]; } m;
   };
-  float d[4][16 * 20];      // inverted diagonal blocks
-  float ghi[kC], glo[kC], beta[kC];
+  float ghi[4][kC], glo[4][kC], beta[4][kC];  // of four value heads
 };
 
 // 16 bytes of storage: bf16 takes the 4 values of each of two tiles, fp32 those of one
@@ -70,7 +69,7 @@ __device__ __forceinline__ double wave_prefix(double v, int lane) {
 }
 
 template <typename E, int DK>
-__global__ __launch_bounds__(256) void chunk_kernel(Args a) {
+__global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kernel(Args a) {
   using M = Mma<E>;
   using Sm = ChunkSmem<E, DK>;
   __shared__ __align__(16) Sm sm;
@@ -122,34 +121,35 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
     const int vh = kh * a.rep + h;
     char* ws = a.ws + (slot * a.hv + vh) * a.ws_item;
     __syncthreads();  // the tiles of the previous head (or K and Q) have been read
-    if (w == 0) {
-      // Prefix sums of the log decays in fp64, kept as two floats: a difference of two of them is
-      // then as exact as its own size, whatever came before in the chunk.  Below -200 exp is 0 in
-      // fp32; the clamp keeps -inf (a reset) out of the differences and lets NaN through.
+    const int hs = h & 3;
+    if (hs == 0 && h + w < a.rep) {
+      // Wave w: prefix sums of head h + w's log decays in fp64, kept as two floats: a difference of two
+      // of them is then as exact as its own size, whatever came before in the chunk.  Below -200 exp is
+      // 0 in fp32; the clamp keeps -inf (a reset) out of the differences and lets NaN through.
       float gl = 0.f, bt = 0.f;
       if (lane < n) {
-        const int64_t at = (t0 + lane) * a.hv + vh;
+        const int64_t at = (t0 + lane) * a.hv + vh + w;
         gl = ld_f32(static_cast<const E*>(a.g), at);
         bt = ld_f32(static_cast<const E*>(a.beta), at);
         gl = gl < -200.f ? -200.f : gl;
       }
       const double G = wave_prefix((double)gl, lane);
       const double total = __shfl(G, 63);
-      const float hi = (float)G;
-      sm.ghi[lane] = hi;
-      sm.glo[lane] = (float)(G - (double)hi);
-      sm.beta[lane] = bt;
-      float* gate = reinterpret_cast<float*>(ws + ChunkWs<E>::kGate);
+      const float hi = (float)G, lo = (float)(G - (double)hi);
+      sm.ghi[w][lane] = hi;
+      sm.glo[w][lane] = lo;
+      sm.beta[w][lane] = bt;
+      float* gate = reinterpret_cast<float*>(ws + w * a.ws_item + ChunkWs<E>::kGate);
       gate[lane] = exp_f32(hi);
       gate[kC + lane] = exp_f32((float)(total - G)) * bt;
       if (lane == 0) gate[2 * kC] = exp_f32((float)total);
-      float* decay = reinterpret_cast<float*>(ws + ChunkWs<E>::kDecay);
+      float* decay = reinterpret_cast<float*>(ws + w * a.ws_item + ChunkWs<E>::kDecay);
       decay[lane] = hi;
-      decay[kC + lane] = sm.glo[lane];
+      decay[kC + lane] = lo;
       decay[2 * kC + lane] = bt;
     }
     __syncthreads();
-    const float gi = sm.ghi[i], gil = sm.glo[i];
+    const float gi = sm.ghi[hs][i], gil = sm.glo[hs][i];
     float p[4][4];
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
@@ -157,9 +157,10 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
       float A[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float d = jt <= w && j + x <= i
-                            ? exp_f32((gi - sm.ghi[j + x]) + (gil - sm.glo[j + x])) * sm.beta[j + x]
-                            : 0.f;
+        const float d = jt <= w && j + x <= i ? exp_f32((gi - sm.ghi[hs][j + x]) +
+                                                        (gil - sm.glo[hs][j + x])) *
+                                                    sm.beta[hs][j + x]
+                                              : 0.f;
         A[x] = j + x < i ? d * kk[jt][x] : 0.f;
         p[jt][x] = d * qk[jt][x] * a.scale;
       }
@@ -180,44 +181,54 @@ __global__ __launch_bounds__(256) void chunk_kernel(Args a) {
       }
     __syncthreads();
     // T = (I + A)^-1 by blocks of 16.  Wave w inverts diagonal block w by substitution, lane r its
-    // column r: x_m = [m = r] - sum_{j < m} A_mj x_j.
+    // column r: x_m = [m = r] - sum_{j < m} A_mj x_j, in four partial sums.
     {
       const float* Ab = &sm.m.a[16 * w * Sm::kLf + 16 * w];
       float x[16];
 #pragma unroll
       for (int m = 0; m < 16; ++m) {
-        float t = m == r ? 1.f : 0.f;
+        f32x4 t = {m == r ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < m; ++j) t = fmaf(-Ab[m * Sm::kLf + j], x[j], t);
-        x[m] = t;
+        for (int j = 0; j < m; j += 4) {
+          const f32x4 row = *reinterpret_cast<const f32x4*>(Ab + m * Sm::kLf + j);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (j + y < m) t[y] = fmaf(-row[y], x[j + y], t[y]);
+        }
+        x[m] = (t[0] + t[1]) + (t[2] + t[3]);
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m)  // the four lane groups hold the same columns: 4 rows each
-        sm.d[w][(4 * g + m) * 20 + r] = g == 0 ? x[m] : g == 1 ? x[4 + m] : g == 2 ? x[8 + m] : x[12 + m];
+        sm.m.t[(16 * w + 4 * g + m) * Sm::kLf + 16 * w + r] =
+            g == 0 ? x[m] : g == 1 ? x[4 + m] : g == 2 ? x[8 + m] : x[12 + m];
     }
     __syncthreads();
     // Wave w makes block column w below the diagonal: T_iw = -T_ii (sum_{k=w}^{i-1} A_ik T_kw), its
-    // own blocks staying in accumulators.
+    // own blocks staying in accumulators.  (Blocks above the diagonal inside a block of the image are
+    // zero.)
     {
       using F = Mma<float>;
       f32x4 T[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) T[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
       for (int b = 0; b < 4; ++b) {
+        T[b] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (b == w)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) T[b][x] = sm.d[w][(4 * g + x) * 20 + r];
+          for (int x = 0; x < 4; ++x) T[b][x] = sm.m.t[(16 * b + 4 * g + x) * Sm::kLf + 16 * w + r];
         if (b > w) {
           f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < b; ++k)
-            if (k >= w) acc = F::mma(*reinterpret_cast<const f32x4*>(&sm.m.a[(16 * b + r) * Sm::kLf + 16 * k + 4 * g]), T[k], acc);
-          f32x4 z = {0.f, 0.f, 0.f, 0.f};
-          T[b] = F::mma(*reinterpret_cast<const f32x4*>(&sm.d[b][r * 20 + 4 * g]), -acc, z);
+            if (k >= w)
+              acc = F::mma(*reinterpret_cast<const f32x4*>(
+                               &sm.m.a[(16 * b + r) * Sm::kLf + 16 * k + 4 * g]), T[k], acc);
+          T[b] = F::mma(*reinterpret_cast<const f32x4*>(
+                            &sm.m.t[(16 * b + r) * Sm::kLf + 16 * b + 4 * g]), -acc,
+                        f32x4{0.f, 0.f, 0.f, 0.f});
         }
+        if (b != w)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sm.m.t[(16 * b + 4 * g + x) * Sm::kLf + 16 * w + r] = T[b][x];
+          for (int x = 0; x < 4; ++x) sm.m.t[(16 * b + 4 * g + x) * Sm::kLf + 16 * w + r] = T[b][x];
       }
     }
     __syncthreads();
@@ -286,7 +297,8 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
   const E* kp = static_cast<const E*>(a.k) + sp.first * a.k_stride + (int64_t)kh * a.dk;
   const E* qp = static_cast<const E*>(a.q) + sp.first * a.q_stride + (int64_t)kh * a.dk;
   const E* vp = static_cast<const E*>(a.v) + sp.first * a.v_stride + (int64_t)vh * a.dv + col0;
-  E* op = static_cast<E*>(a.out) + (sp.first * a.hv + vh) * (int64_t)a.dv + col;
+  const int64_t o_stride = (int64_t)a.hv * a.dv;
+  E* op = static_cast<E*>(a.out) + sp.first * o_stride + (int64_t)vh * a.dv + col;
   const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
   const bool has_col = col + r < a.dv;
 
@@ -454,19 +466,13 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
 #pragma unroll
           for (int m = kb * M::kTiles; m < 4; ++m) o[m] = M::mma(es.p[p], pf[m], o[m]);
       }
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(
+          op + ch * kC * o_stride, 0, (int)(((n - 1) * o_stride + max(a.dv - col, 0)) * (int64_t)sizeof(E)),
+          0x00020000);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int t = 16 * m + r;
-        if (t < n && col + 4 * g < a.dv) {
-          E* dst = op + (ch * kC + t) * (int64_t)a.hv * a.dv + 4 * g;
-          if constexpr (sizeof(E) == 2)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16(make_float2(o[m][0], o[m][1])),
-                           pack_bf16(make_float2(o[m][2], o[m][3])));
-          else
-            *reinterpret_cast<f32x4*>(dst) = o[m];
-        }
-      }
+      for (int m = 0; m < 4; ++m)
+        store_four<E>(buf, col + 4 * g < a.dv ? (uint32_t)((16 * m + r) * o_stride + 4 * g) * (uint32_t)sizeof(E)
+                                              : kOutside, o[m]);
     }
     // S = exp(G_64) S + K^T diag(c) E
 #pragma unroll
