@@ -347,6 +347,11 @@ struct Args {
   int64_t seqlen;          // tokens per sequence (packed: of all sequences)
   int64_t nseq;
   int64_t slots;           // chunk slots
+  // long sequences in segments of seg_chunks chunks (0: one segment per sequence)
+  int64_t seg_chunks;
+  int64_t seg_slots;
+  float* seg_state;        // (segment slots, hv, dk, dv): the state before each segment but the first
+  float* seg_map;          // (segment slots, hv, dk, dk): what a segment does to the state before it
   int32_t hk, hv, rep, dk, dv;
   float scale;
 };
@@ -364,22 +369,33 @@ __device__ __forceinline__ Span seq_span(const Args& a, int64_t seq) {
   return {b, max(e - b, (int64_t)0)};
 }
 
-// Chunk slots: sequence s owns the slots from slot_base(s) on.  For packed sequences
-// offset / 64 + s leaves room for a last, partial chunk in each, without a scan over the lengths.
-__device__ __forceinline__ int64_t slot_base(const Args& a, int64_t seq, int64_t first) {
-  return a.offsets ? first / kC + seq : seq * ((a.seqlen + kC - 1) / kC);
+// Slots of `unit` tokens (chunks, segments): sequence s owns the slots from slot_base(s) on.  For packed
+// sequences offset / unit + s leaves room for a last, partial one in each, without a scan over the lengths.
+__device__ __forceinline__ int64_t slot_base(const Args& a, int64_t seq, int64_t first,
+                                             int64_t unit = kC) {
+  return a.offsets ? first / unit + seq : seq * ((a.seqlen + unit - 1) / unit);
 }
 
 // slot -> sequence (the last one whose base is not past the slot)
-__device__ __forceinline__ int64_t slot_seq(const Args& a, int64_t slot) {
-  if (!a.offsets) return slot / ((a.seqlen + kC - 1) / kC);
+__device__ __forceinline__ int64_t slot_seq(const Args& a, int64_t slot, int64_t unit = kC) {
+  if (!a.offsets) return slot / ((a.seqlen + unit - 1) / unit);
   int64_t lo = 0, hi = a.nseq - 1;
   while (lo < hi) {
     const int64_t mid = (lo + hi + 1) >> 1;
     const int64_t first = min(max(a.offsets[mid], (int64_t)0), a.seqlen);
-    if (first / kC + mid <= slot) lo = mid; else hi = mid - 1;
+    if (first / unit + mid <= slot) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// Workgroups in groups of `group` that read the same keys: a group stays on one XCD (one L2), and
+// consecutive groups, which are heads of one sequence and so equally long, go to different XCDs.
+// (Workgroup id runs on XCD id % 8.)  A bijection of [0, n), n a multiple of `group`.
+__device__ __forceinline__ int64_t spread_index(uint32_t id, uint32_t n, uint32_t group) {
+  const uint32_t whole = n / group / 8 * 8 * group;
+  if (id >= whole) return id;
+  const uint32_t x = id & 7, l = id >> 3;
+  return (int64_t)(l / group * 8 + x) * group + l % group;
 }
 
 // Parts of T that the forward uses and the workspace holds: T is unit on its diagonal and small off
@@ -401,9 +417,10 @@ struct ChunkWs {
   static_assert(kBytes % 1024 == 0 && kBwdBytes % 1024 == 0, "copied in whole wave instructions");
 };
 
-inline int64_t chunk_slots(const mamba_delta_dims* d, bool packed) {
-  return packed ? d->seqlen / kC + d->batch : d->batch * ((d->seqlen + kC - 1) / kC);
+inline int64_t slots_of(const mamba_delta_dims* d, bool packed, int64_t unit) {
+  return packed ? d->seqlen / unit + d->batch : d->batch * ((d->seqlen + unit - 1) / unit);
 }
+inline int64_t chunk_slots(const mamba_delta_dims* d, bool packed) { return slots_of(d, packed, kC); }
 inline size_t chunk_ws_bytes(const mamba_delta_dims* d) {
   return d->io_dtype == MAMBA_BF16 ? ChunkWs<uint16_t>::kBytes : ChunkWs<float>::kBytes;
 }
@@ -454,6 +471,7 @@ inline Args make_args(const mamba_delta_dims* d, float scale, const void* q, con
   a.seqlen = d->seqlen;
   a.nseq = d->batch;
   a.slots = chunk_slots(d, offsets != nullptr);
+  a.seg_slots = d->batch;
   a.hk = (int32_t)d->qk_heads;
   a.hv = (int32_t)d->v_heads;
   a.rep = (int32_t)(d->v_heads / d->qk_heads);

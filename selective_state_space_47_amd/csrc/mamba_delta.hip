@@ -7,12 +7,17 @@
 //                 goes through the chunks.  A wave owns 16 columns; its state stays in accumulators
 //                 from the first chunk to the last, and every product's accumulators are the next
 //                 product's operand, so that waves share nothing but the tiles they read.
+//   segments_kernel  a long sequence of few heads goes through scan_kernel in segments, side by side: first
+//                 each segment's effect on the state, then the states before them one after another,
+//                 then every segment from its own.
 //   step_kernel   one token: the state is read and written once.
 //
 // Rounding (bf16 storage): products take bf16 operands into fp32 accumulators.  Whatever reaches the
 // state (S in K S, Y, T, E in K^T E) goes in as three bf16 parts, the fp32 value to 24 bits, so that
 // the state is fp32 in earnest; the output O takes S and E as two parts and P as one, whose rounding
 // is that of the output again.  fp32 storage uses fp32 matrix instructions throughout.
+#include <cmath>
+
 #include "mamba_delta.h"
 
 namespace mamba {
@@ -270,37 +275,57 @@ struct Stage {
   static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
 };
 
-// kStates: the backward's pass, which leaves E and the state before each chunk instead of the output.
-// Its results only enter gradients that are rounded to the storage type: with bf16 storage two parts of
+// What a pass leaves: the output and the last state; the backward's E and the state before each chunk; or,
+// for a segment of a long sequence, the state that it makes from zero (columns of the state) and from the
+// identity without values (dk more columns: the segment's map of the state before it).
+enum Pass { kOut, kBackward, kSummary };
+
+// The results of the backward's pass only enter gradients that are rounded to the storage type: with bf16 storage two parts of
 // each factor keep them clear of those roundings, also where a sum of them cancels (dg).
-template <typename E, int DK, int NW, bool kStates>
+template <typename E, int DK, int NW, Pass kPass>
 __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_blocks) {
   using M = Mma<E>;
   using St = Stage<E, DK, NW>;
   using KT = KeyTile<E, DK>;
   using TT = TriTile<E>;
   using VT = ValueTile<E, 16 * NW>;
+  constexpr bool kStates = kPass == kBackward, kO = kPass == kOut;
   constexpr int kPS = M::parts(kStates ? 2 : 3), kPT = M::parts(kTParts);
   constexpr int kPY = M::parts(kStates ? 2 : 3), kPE = M::parts(kStates ? 2 : 3);
   constexpr int kPO = M::parts(2);  // of S and E in the output
   __shared__ __align__(1024) char smem[St::kCount * St::kBytes];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wg = placed_index(blockIdx.x, gridDim.x);
+  const int64_t wg = spread_index(blockIdx.x, gridDim.x, a.rep * col_blocks);
   const int64_t sh = wg / col_blocks;
-  const int64_t seq = sh / a.hv;
-  const int vh = (int)(sh - seq * a.hv), kh = vh / a.rep;
-  const int col0 = (int)(wg - sh * col_blocks) * 16 * NW;  // this workgroup's first column
-  const int col = col0 + 16 * w;                           // this wave's
+  const int64_t seg_slot = sh / a.hv;
+  const int vh = (int)(sh - seg_slot * a.hv), kh = vh / a.rep;
+  const int64_t unit = a.seg_chunks * kC;
+  const int64_t seq = a.seg_chunks ? slot_seq(a, seg_slot, unit) : seg_slot;
   const Span sp = seq_span(a, seq);
+  const int64_t seg = a.seg_chunks ? seg_slot - slot_base(a, seq, sp.first, unit) : 0;
+  const int64_t nchunks = (sp.len + kC - 1) / kC;
+  const int64_t first = seg * a.seg_chunks;  // this segment's chunks
+  const int64_t end = a.seg_chunks ? min(first + a.seg_chunks, nchunks) : nchunks;
+  if (seg < 0 || (first >= end && seg > 0)) return;  // an unused slot of a packed batch
+  if (kPass == kSummary && end == nchunks) return;   // nothing follows the last segment
+  const int vblocks = (a.dv + 16 * NW - 1) / (16 * NW);
+  const int cb = (int)(wg - sh * col_blocks);
+  const bool map = kPass == kSummary && cb >= vblocks;  // columns of the identity
+  const int width = map ? a.dk : a.dv;
+  const int col0 = (map ? cb - vblocks : cb) * 16 * NW;  // this workgroup's first column
+  const int col = col0 + 16 * w;                         // this wave's
   const int64_t slot0 = slot_base(a, seq, sp.first);
   const E* kp = static_cast<const E*>(a.k) + sp.first * a.k_stride + (int64_t)kh * a.dk;
   const E* qp = static_cast<const E*>(a.q) + sp.first * a.q_stride + (int64_t)kh * a.dk;
   const E* vp = static_cast<const E*>(a.v) + sp.first * a.v_stride + (int64_t)vh * a.dv + col0;
   const int64_t o_stride = (int64_t)a.hv * a.dv;
   E* op = static_cast<E*>(a.out) + sp.first * o_stride + (int64_t)vh * a.dv + col;
+  const bool has_col = col + r < width;
+  // (dk, width) matrices of this head: the sequence's states, and this segment's
   const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
-  const bool has_col = col + r < a.dv;
+  const int64_t g_at = (seg_slot * a.hv + vh) * (int64_t)a.dk * width + col + r;
+  const float* from = kPass == kSummary ? nullptr : seg ? a.seg_state + g_at : a.s0 ? a.s0 + s_at : nullptr;
 
   f32x4 S[DK / 16];
 #pragma unroll
@@ -308,12 +333,12 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int row = KT::value(m, g, x);
-      S[m][x] = a.s0 && has_col && row < a.dk ? a.s0[s_at + (int64_t)row * a.dv] : 0.f;
+      S[m][x] = map ? (row == col + r ? 1.f : 0.f)
+                    : from && has_col && row < a.dk ? from[(int64_t)row * a.dv] : 0.f;
     }
 
   const uint32_t lds0 = lds_address(smem);
-  const int64_t nchunks = (sp.len + kC - 1) / kC;
-  const int vcols = min(a.dv - col0, 16 * NW);
+  const int vcols = map ? 0 : min(a.dv - col0, 16 * NW);  // (without values: words outside, zeros)
   const RowCopy<E, KT, kC, NW> ck(w, lane, a.k_stride, a.dk), cq(w, lane, a.q_stride, a.dk);
   const RowCopy<E, VT, kC, NW> cv(w, lane, a.v_stride, vcols);
   // copies chunk ch into stage st; tokens past the sequence are past the buffers and read as zero
@@ -322,7 +347,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
     const uint32_t to = lds0 + st * St::kBytes;
     ck(rows_buffer(kp + t * a.k_stride, n, a.k_stride, a.dk), to + St::kK, w);
     cv(rows_buffer(vp + t * a.v_stride, n, a.v_stride, vcols), to + St::kVv, w);
-    if (!kStates) cq(rows_buffer(qp + t * a.q_stride, n, a.q_stride, a.dk), to + St::kQ, w);
+    if (kO) cq(rows_buffer(qp + t * a.q_stride, n, a.q_stride, a.dk), to + St::kQ, w);
     copy_linear<St::kWsBytes, NW>(a.ws + ((slot0 + ch) * a.hv + vh) * a.ws_item,
                                   to + St::kWs, w, lane);
   };
@@ -334,12 +359,12 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
   const KT kt(lane);
   const TT tt(lane);
   const VT vt(lane, 16 * w);
-  if (nchunks > 0) copy(0, 0);
-  for (int64_t ch = 0; ch < nchunks; ++ch) {
-    const int st = St::kCount == 2 ? (int)(ch & 1) : 0;
+  if (first < end) copy(first, 0);
+  for (int64_t ch = first; ch < end; ++ch) {
+    const int st = St::kCount == 2 ? (int)((ch - first) & 1) : 0;
     copies_done();
     // with two stages the next chunk is copied while this one is worked on
-    if (St::kCount == 2 && ch + 1 < nchunks) copy(ch + 1, st ^ 1);
+    if (St::kCount == 2 && ch + 1 < end) copy(ch + 1, st ^ 1);
     const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
     const int n = (int)min((int64_t)kC, sp.len - ch * kC);
 
@@ -379,13 +404,13 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         kf[m] = kt.rows(sm + St::kK, m, kb);
-        if (!kStates) qf[m] = kt.rows(sm + St::kQ, m, kb);
+        if (kO) qf[m] = kt.rows(sm + St::kQ, m, kb);
       }
 #pragma unroll
       for (int p = 0; p < kPS; ++p)
 #pragma unroll
         for (int m = 0; m < 4; ++m) y[m] = M::mma(kf[m], s.p[p], y[m]);
-      if constexpr (!kStates) {
+      if constexpr (kO) {
 #pragma unroll
         for (int p = 0; p < kPO; ++p)
 #pragma unroll
@@ -401,7 +426,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         y[m][x] = fmaf(-eg[x], y[m][x], v[x]);
-        if (!kStates) o[m][x] *= so;
+        if (kO) o[m][x] *= so;
       }
     }
     // E = T Y, T lower triangular; the parts' products down to the last part's
@@ -452,7 +477,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
           }
         }
       }
-    } else {
+    } else if constexpr (kO) {
       // O += P E, transposed: a lane ends with 4 consecutive columns of one token
 #pragma unroll
       for (int kb = 0; kb < TT::kBlocks; ++kb) {
@@ -494,19 +519,87 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
           for (int m = 0; m < 4; ++m) S[m0 + m] = M::mma(kf[m], es.p[p], S[m0 + m]);
       }
     }
-    if (St::kCount == 1 && ch + 1 < nchunks) {
+    if (St::kCount == 1 && ch + 1 < end) {
       __syncthreads();  // every wave has read the stage
       copy(ch + 1, 0);
     }
   }
-  if (!kStates && a.last && has_col) {
+  float* to = kPass == kSummary ? (map ? a.seg_map : a.seg_state) + g_at
+              : kO && a.last && end == nchunks ? a.last + s_at : nullptr;
+  if (to && has_col) {
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int row = KT::value(m, g, x);
-        if (row < a.dk) a.last[s_at + (int64_t)row * a.dv] = S[m][x];
+        if (row < a.dk) to[(int64_t)row * width] = S[m][x];
       }
+  }
+}
+
+// The states before the segments, one after another: S <- map S + (the segment's own).  A workgroup has 16
+// columns, its waves 16 rows each; fp32 matrix instructions, S handed round through LDS.  seg_state holds
+// each segment's own result on entry and the state before it on return.
+template <int DK>
+__global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_blocks) {
+  using M = Mma<float>;
+  constexpr int kLd = DK + 4;
+  __shared__ __align__(16) float sm[2][16 * kLd];  // S transposed: column r, then row
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15, w = threadIdx.x >> 6;
+  const int64_t sh = blockIdx.x / col_blocks;
+  const int64_t seq = sh / a.hv;
+  const int vh = (int)(sh - seq * a.hv);
+  const int col = (int)(blockIdx.x - sh * col_blocks) * 16 + r;
+  const int64_t unit = a.seg_chunks * kC;
+  const Span sp = seq_span(a, seq);
+  const int64_t base = slot_base(a, seq, sp.first, unit);
+  const int64_t nseg = (sp.len + unit - 1) / unit;
+  const bool has_col = col < a.dv;
+  const int row0 = 16 * w + 4 * g;  // this lane's rows of S
+  auto state = [&](int64_t slot) {
+    return a.seg_state + (slot * a.hv + vh) * (int64_t)a.dk * a.dv + (int64_t)row0 * a.dv + col;
+  };
+  auto load_own = [&](int64_t s) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (has_col && row0 < a.dk)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = state(base + s)[(int64_t)x * a.dv];
+    return v;
+  };
+  f32x4 map[DK / 16];  // operands: row 16 w + r of the segment's map
+  auto load_map = [&](int64_t s) {
+    const float* p = a.seg_map + ((base + s) * a.hv + vh) * (int64_t)a.dk * a.dk +
+                     (int64_t)(16 * w + r) * a.dk + 4 * g;
+#pragma unroll
+    for (int kb = 0; kb < DK / 16; ++kb)
+      map[kb] = 16 * w + r < a.dk && 16 * kb + 4 * g < a.dk
+                    ? *reinterpret_cast<const f32x4*>(p + 16 * kb) : f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  if (a.s0 && has_col && row0 < a.dk)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      S[x] = a.s0[((seq * a.hv + vh) * (int64_t)a.dk + row0 + x) * a.dv + col];
+  f32x4 own = S;
+  if (nseg > 1) {
+    load_map(0);
+    own = load_own(0);
+  }
+  for (int64_t s = 0; s + 1 < nseg; ++s) {
+    float* buf = sm[s & 1];
+    *reinterpret_cast<f32x4*>(&buf[r * kLd + row0]) = S;
+    __syncthreads();
+    S = own;
+#pragma unroll
+    for (int kb = 0; kb < DK / 16; ++kb)
+      S = M::mma(map[kb], *reinterpret_cast<const f32x4*>(&buf[r * kLd + 16 * kb + 4 * g]), S);
+    if (s + 2 < nseg) {
+      load_map(s + 1);
+      own = load_own(s + 1);
+    }
+    if (has_col && row0 < a.dk)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) state(base + s + 1)[(int64_t)x * a.dv] = S[x];
   }
 }
 
@@ -643,19 +736,88 @@ int launch_chunks_t(const Args& a, hipStream_t s) {
   return launch_status();
 }
 
-template <typename E, int DK, int NW, bool kStates>
+// columns of the state per workgroup
+int scan_columns(int64_t dv) { return dv <= 64 ? 64 : 128; }
+
+template <typename E, int DK, int NW, Pass kPass>
 int launch_scan_t(const Args& a, hipStream_t s) {
-  const int cols = (a.dv + 16 * NW - 1) / (16 * NW);
-  hipLaunchKernelGGL((scan_kernel<E, DK, NW, kStates>), dim3((unsigned)(a.nseq * a.hv * cols)),
+  const int cols = (a.dv + 16 * NW - 1) / (16 * NW) +
+                   (kPass == kSummary ? (a.dk + 16 * NW - 1) / (16 * NW) : 0);
+  hipLaunchKernelGGL((scan_kernel<E, DK, NW, kPass>), dim3((unsigned)(a.seg_slots * a.hv * cols)),
                      dim3(64 * NW), 0, s, a, cols);
   return launch_status();
 }
 
-template <typename E, bool kStates>
+template <typename E, Pass kPass>
 int launch_scan(const Args& a, hipStream_t s) {
+  const bool narrow = scan_columns(a.dv) == 64;
   if (a.dk <= 64)
-    return a.dv <= 64 ? launch_scan_t<E, 64, 4, kStates>(a, s) : launch_scan_t<E, 64, 8, kStates>(a, s);
-  return a.dv <= 64 ? launch_scan_t<E, 128, 4, kStates>(a, s) : launch_scan_t<E, 128, 8, kStates>(a, s);
+    return narrow ? launch_scan_t<E, 64, 4, kPass>(a, s) : launch_scan_t<E, 64, 8, kPass>(a, s);
+  return narrow ? launch_scan_t<E, 128, 4, kPass>(a, s) : launch_scan_t<E, 128, 8, kPass>(a, s);
+}
+
+template <typename E>
+int launch_forward(const Args& a, hipStream_t s) {
+  if (a.seg_chunks) {
+    int st = launch_scan<E, kSummary>(a, s);
+    if (st != MAMBA_OK) return st;
+    const int cols = (a.dv + 15) / 16;
+    if (a.dk <= 64)
+      hipLaunchKernelGGL(segments_kernel<64>, dim3((unsigned)(a.nseq * a.hv * cols)), dim3(256), 0, s,
+                         a, cols);
+    else
+      hipLaunchKernelGGL(segments_kernel<128>, dim3((unsigned)(a.nseq * a.hv * cols)), dim3(512), 0, s,
+                         a, cols);
+    if ((st = launch_status()) != MAMBA_OK) return st;
+  }
+  return launch_scan<E, kOut>(a, s);
+}
+
+// Chunks per segment, 0 for whole sequences.  A pass costs one unit per chunk and round of 256
+// workgroups (one per CU); segments add a summary pass over their own and the map's columns, about 0.8
+// of a unit per chunk, and a quarter of a unit per segment to join them.  Packed sequences are taken to
+// be up to twice as long as their mean.  Segments are used where that model gains a quarter.
+// Measured, 65536 tokens x 12 heads of 128, bf16: PENDING.
+int64_t plan_segments(const mamba_delta_dims* d, bool packed) {
+  constexpr double kCUs = 256.0;
+  const int64_t per = scan_columns(d->dv);
+  const double vb = (double)((d->dv + per - 1) / per), kb = (double)((d->dk + per - 1) / per);
+  const int64_t nseq = packed ? std::min(d->batch, d->seqlen) : d->batch;
+  const double heads = (double)nseq * (double)d->v_heads;
+  double chunks = (double)((d->seqlen + kC - 1) / kC);
+  if (packed && nseq > 1) chunks = std::min(chunks, 2.0 * chunks / (double)nseq);
+  const double whole = std::ceil(heads * vb / kCUs) * chunks;
+  double best = 0.75 * whole;
+  int64_t pick = 0;
+  for (int64_t c = 8; c <= 256; c += 4) {
+    const double n = std::ceil(chunks / (double)c);
+    if (n < 2) break;
+    if ((n + 1) * heads * (vb + kb) > 2147483647.0) continue;  // one grid
+    const double t = std::ceil((n - 1) * heads * (vb + kb) / kCUs) * (double)c * 0.8 +
+                     std::ceil(n * heads * vb / kCUs) * (double)c + 0.25 * n + 4.0;
+    if (t < best) {
+      best = t;
+      pick = c;
+    }
+  }
+  return pick;
+}
+
+struct FwdLayout {  // workspace regions in bytes
+  int64_t seg_chunks, seg_slots;
+  size_t state, map, total;
+};
+FwdLayout fwd_layout(const mamba_delta_dims* d, bool packed) {
+  FwdLayout l = {plan_segments(d, packed), d->batch, 0, 0, 0};
+  l.state = (size_t)chunk_slots(d, packed) * (size_t)d->v_heads * chunk_ws_bytes(d);
+  l.map = l.total = l.state;
+  if (l.seg_chunks) {
+    l.seg_slots = slots_of(d, packed, l.seg_chunks * kC);
+    const size_t rows = (size_t)l.seg_slots * (size_t)d->v_heads * (size_t)d->dk * sizeof(float);
+    l.map = l.state + rows * (size_t)d->dv;
+    l.total = l.map + rows * (size_t)d->dk;
+  }
+  return l;
 }
 
 }  // namespace
@@ -666,7 +828,7 @@ int launch_chunks(const Args& a, bool bf, hipStream_t s) {
 }
 
 int launch_states(const Args& a, bool bf, hipStream_t s) {
-  return bf ? launch_scan<uint16_t, true>(a, s) : launch_scan<float, true>(a, s);
+  return bf ? launch_scan<uint16_t, kBackward>(a, s) : launch_scan<float, kBackward>(a, s);
 }
 
 }  // namespace delta
@@ -679,7 +841,7 @@ extern "C" {
 
 size_t mamba_delta_workspace_bytes(const mamba_delta_dims* dims, int packed) {
   if (check_delta(dims, packed != 0) != MAMBA_OK) return 0;
-  return (size_t)chunk_slots(dims, packed != 0) * (size_t)dims->v_heads * chunk_ws_bytes(dims);
+  return fwd_layout(dims, packed != 0).total;
 }
 
 int mamba_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -692,17 +854,21 @@ int mamba_delta_fwd(const void* q, const void* k, const void* v, const void* g, 
   if ((st = check_delta_inputs(dims, q, k, v, g, beta, initial_state, seq_offsets)) != MAMBA_OK)
     return st;
   if (!aligned(out, 16) || (last_state && !aligned(last_state, 16))) return MAMBA_ERR_ALIGN;
-  if (!workspace || workspace_bytes < mamba_delta_workspace_bytes(dims, seq_offsets != nullptr))
-    return MAMBA_ERR_WORKSPACE;
+  const FwdLayout l = fwd_layout(dims, seq_offsets != nullptr);
+  if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
   Args a = make_args(dims, scale, q, k, v, g, beta, initial_state, seq_offsets);
   a.out = out;
   a.last = last_state;
   a.ws = static_cast<char*>(workspace);
+  a.seg_chunks = l.seg_chunks;
+  a.seg_slots = l.seg_slots;
+  a.seg_state = reinterpret_cast<float*>(a.ws + l.state);
+  a.seg_map = reinterpret_cast<float*>(a.ws + l.map);
   const bool bf = dims->io_dtype == MAMBA_BF16;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = launch_chunks(a, bf, s)) != MAMBA_OK) return st;
-  return bf ? launch_scan<uint16_t, false>(a, s) : launch_scan<float, false>(a, s);
+  return bf ? launch_forward<uint16_t>(a, s) : launch_forward<float>(a, s);
 }
 
 int mamba_delta_update(float* state, const void* q, const void* k, const void* v, const void* g,

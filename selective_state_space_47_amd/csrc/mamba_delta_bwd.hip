@@ -89,7 +89,7 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
   const Args& a = b.f;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wg = placed_index(blockIdx.x, gridDim.x);
+  const int64_t wg = spread_index(blockIdx.x, gridDim.x, a.rep * col_blocks);
   const int64_t sh = wg / col_blocks;
   const int64_t seq = sh / a.hv;
   const int vh = (int)(sh - seq * a.hv), kh = vh / a.rep;

@@ -196,6 +196,44 @@ def test_packed(lengths, io):
 
 
 @pytest.mark.parametrize("io", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 4133, 1, 2, 64, 64), (2, 2600, 1, 1, 40, 136),
+                                   (1, 4096, 1, 1, 128, 72)], ids=ids)
+def test_long_sequence_of_few_heads(shape, io):
+    """Few heads and many chunks: the sequence goes through in segments, side by side (the workspace shows
+    it: it holds more than the chunks')."""
+    B, L, Hk, Hv, dk, dv = shape
+    x, t = case(L, *shape, io)
+    code = binding.MAMBA_BF16 if io == BF else binding.MAMBA_F32
+    few = binding.mamba_delta_workspace_bytes(binding.mamba_delta_dims(B, L, Hk, Hv, dk, dv, 0, 0, 0, code, 0))
+    per = binding.mamba_delta_workspace_bytes(binding.mamba_delta_dims(1, 1, 1, 1, dk, dv, 0, 0, 0, code, 0))
+    assert few > per * B * Hv * ((L + 63) // 64)
+    print(f"[delta long] {shape} {io}", flush=True)
+    out, last = run_fwd(t, initial_state=t["state"])
+    ref, rlast = ref_fwd(x, dk ** -0.5, x["state"])
+    check(out, ref, "out", io)
+    check(last, rlast, "last_state", io, state=True)
+
+
+@pytest.mark.parametrize("lengths", [[3000, 0, 1, 2100, 64], [1, 5000]],
+                         ids=lambda v: "-".join(map(str, v)))
+def test_long_packed(lengths):
+    """Packed sequences, some of several segments and some of none.  bf16."""
+    total = sum(lengths)
+    Hk, Hv, dk, dv = 1, 2, 64, 64
+    x, t = case(len(lengths), 1, total, Hk, Hv, dk, dv, BF)
+    st = np.random.default_rng(9).standard_normal((len(lengths), Hv, dk, dv)).astype(np.float32)
+    off = np.cumsum([0] + lengths)
+    args = {m: t[m][0] for m in ("q", "k", "v", "g", "beta")}
+    print(f"[delta long packed] {lengths}", flush=True)
+    out, last = run_fwd(args, initial_state=torch.from_numpy(st).to(DEV),
+                        seq_offsets=torch.from_numpy(off).to(DEV))
+    outs, lasts = zip(*(ref_fwd({m: x[m][:, off[s]:off[s + 1]] for m in args}, dk ** -0.5,
+                                st[s:s + 1]) for s in range(len(lengths))))
+    check(out, np.concatenate([o[0] for o in outs]), "out", BF)
+    check(last, np.concatenate(lasts), "last_state", BF, state=True)
+
+
+@pytest.mark.parametrize("io", [F32, BF], ids=["f32", "bf16"])
 def test_packed_offsets_out_of_range(io):
     """Offsets past the tokens, or backwards, are clamped: the sequences that are right stay right, and
     nothing outside is read or written (the outputs' canaries stay)."""
