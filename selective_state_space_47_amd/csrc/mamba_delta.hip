@@ -12,10 +12,11 @@
 //                 then every segment from its own.
 //   step_kernel   one token: the state is read and written once.
 //
-// Rounding (bf16 storage): products take bf16 operands into fp32 accumulators.  Whatever reaches the
-// state (S in K S, Y, T, E in K^T E) goes in as three bf16 parts, the fp32 value to 24 bits, so that
-// the state is fp32 in earnest; the output O takes S and E as two parts and P as one, whose rounding
-// is that of the output again.  fp32 storage uses fp32 matrix instructions throughout.
+// Rounding (bf16 storage): products take bf16 operands into fp32 accumulators.  What makes E and enters the
+// state by K^T E goes in as three bf16 parts (Y and c E: the fp32 value to 24 bits) or two (S, and T, which
+// is one on its diagonal and small off it): the state is within about 3e-7 of fp64.  The output takes S and
+// E as two parts and P as one, whose rounding is that of the output again.  fp32 storage uses fp32 matrix
+// instructions throughout.
 #include <cmath>
 
 #include "mamba_delta.h"
@@ -290,9 +291,9 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
   using TT = TriTile<E>;
   using VT = ValueTile<E, 16 * NW>;
   constexpr bool kStates = kPass == kBackward, kO = kPass == kOut;
-  constexpr int kPS = M::parts(kStates ? 2 : 3), kPT = M::parts(kTParts);
+  constexpr int kPS = M::parts(2), kPT = M::parts(kTParts);
   constexpr int kPY = M::parts(kStates ? 2 : 3), kPE = M::parts(kStates ? 2 : 3);
-  constexpr int kPO = M::parts(2);  // of S and E in the output
+  constexpr int kPO = M::parts(2);  // of E in the output
   __shared__ __align__(1024) char smem[St::kCount * St::kBytes];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -412,7 +413,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
         for (int m = 0; m < 4; ++m) y[m] = M::mma(kf[m], s.p[p], y[m]);
       if constexpr (kO) {
 #pragma unroll
-        for (int p = 0; p < kPO; ++p)
+        for (int p = 0; p < kPS; ++p)
 #pragma unroll
           for (int m = 0; m < 4; ++m) o[m] = M::mma(s.p[p], qf[m], o[m]);
       }
@@ -566,8 +567,9 @@ __global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_bl
       for (int x = 0; x < 4; ++x) v[x] = state(base + s)[(int64_t)x * a.dv];
     return v;
   };
-  f32x4 map[DK / 16];  // operands: row 16 w + r of the segment's map
-  auto load_map = [&](int64_t s) {
+  // operands: row 16 w + r of the segment's map; the next segment's are on their way meanwhile
+  f32x4 map[2][DK / 16];
+  auto load_map = [&](int64_t s, f32x4 (&map)[DK / 16]) {
     const float* p = a.seg_map + ((base + s) * a.hv + vh) * (int64_t)a.dk * a.dk +
                      (int64_t)(16 * w + r) * a.dk + 4 * g;
 #pragma unroll
@@ -580,26 +582,35 @@ __global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_bl
 #pragma unroll
     for (int x = 0; x < 4; ++x)
       S[x] = a.s0[((seq * a.hv + vh) * (int64_t)a.dk + row0 + x) * a.dv + col];
-  f32x4 own = S;
-  if (nseg > 1) {
-    load_map(0);
-    own = load_own(0);
-  }
-  for (int64_t s = 0; s + 1 < nseg; ++s) {
-    float* buf = sm[s & 1];
-    *reinterpret_cast<f32x4*>(&buf[r * kLd + row0]) = S;
-    __syncthreads();
-    S = own;
+  f32x4 own[2] = {S, S};
 #pragma unroll
-    for (int kb = 0; kb < DK / 16; ++kb)
-      S = M::mma(map[kb], *reinterpret_cast<const f32x4*>(&buf[r * kLd + 16 * kb + 4 * g]), S);
-    if (s + 2 < nseg) {
-      load_map(s + 1);
-      own = load_own(s + 1);
+  for (int i = 0; i < 2; ++i)
+    if (i + 1 < nseg) {
+      load_map(i, map[i]);
+      own[i] = load_own(i);
     }
-    if (has_col && row0 < a.dk)
+  for (int64_t s0 = 0; s0 + 1 < nseg; s0 += 2) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) state(base + s + 1)[(int64_t)x * a.dv] = S[x];
+    for (int i = 0; i < 2; ++i) {
+      const int64_t s = s0 + i;
+      if (s + 1 >= nseg) break;
+      *reinterpret_cast<f32x4*>(&sm[i][r * kLd + row0]) = S;
+      __syncthreads();
+      f32x4 acc[2] = {own[i], f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int kb = 0; kb < DK / 16; ++kb)
+        acc[kb & 1] = M::mma(map[i][kb],
+                             *reinterpret_cast<const f32x4*>(&sm[i][r * kLd + 16 * kb + 4 * g]),
+                             acc[kb & 1]);
+      S = acc[0] + acc[1];
+      if (s + 3 < nseg) {
+        load_map(s + 2, map[i]);
+        own[i] = load_own(s + 2);
+      }
+      if (has_col && row0 < a.dk)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) state(base + s + 1)[(int64_t)x * a.dv] = S[x];
+    }
   }
 }
 
@@ -736,8 +747,11 @@ int launch_chunks_t(const Args& a, hipStream_t s) {
   return launch_status();
 }
 
-// columns of the state per workgroup
-int scan_columns(int64_t dv) { return dv <= 64 ? 64 : 128; }
+// Columns of the state per workgroup.  128 (8 waves) share a chunk's tiles best; where workgroups of 64
+// (4 waves) leave CUs idle as well, they finish sooner: 3.4 against 4.4 us a chunk (12 heads, dk = 128).
+int scan_columns(int64_t segments, int64_t dv) {
+  return dv <= 64 || segments * ((dv + 63) / 64) <= 256 ? 64 : 128;
+}
 
 template <typename E, int DK, int NW, Pass kPass>
 int launch_scan_t(const Args& a, hipStream_t s) {
@@ -750,7 +764,7 @@ int launch_scan_t(const Args& a, hipStream_t s) {
 
 template <typename E, Pass kPass>
 int launch_scan(const Args& a, hipStream_t s) {
-  const bool narrow = scan_columns(a.dv) == 64;
+  const bool narrow = scan_columns(a.seg_slots * a.hv, a.dv) == 64;
   if (a.dk <= 64)
     return narrow ? launch_scan_t<E, 64, 4, kPass>(a, s) : launch_scan_t<E, 64, 8, kPass>(a, s);
   return narrow ? launch_scan_t<E, 128, 4, kPass>(a, s) : launch_scan_t<E, 128, 8, kPass>(a, s);
@@ -780,7 +794,7 @@ int launch_forward(const Args& a, hipStream_t s) {
 // Measured, 65536 tokens x 12 heads of 128, bf16: PENDING.
 int64_t plan_segments(const mamba_delta_dims* d, bool packed) {
   constexpr double kCUs = 256.0;
-  const int64_t per = scan_columns(d->dv);
+  const int64_t per = d->dv <= 64 ? 64 : 128;
   const double vb = (double)((d->dv + per - 1) / per), kb = (double)((d->dk + per - 1) / per);
   const int64_t nseq = packed ? std::min(d->batch, d->seqlen) : d->batch;
   const double heads = (double)nseq * (double)d->v_heads;

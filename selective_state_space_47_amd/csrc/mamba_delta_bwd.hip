@@ -612,9 +612,11 @@ int launch_adjoint_t(const BwdArgs& b, hipStream_t s) {
 }
 template <typename E, int DK>
 int launch_bwd(const BwdArgs& b, hipStream_t s) {
-  // 8 waves of fp32 operands would not fit the registers
-  const int st = b.f.dv <= 64 || sizeof(E) == 4 ? launch_adjoint_t<E, DK, 4>(b, s)
-                                                : launch_adjoint_t<E, DK, sizeof(E) == 2 ? 8 : 4>(b, s);
+  // 64 or 128 columns per workgroup as in the forward (8 waves of fp32 operands would not fit the
+  // registers)
+  const bool narrow = b.f.dv <= 64 || sizeof(E) == 4 || b.f.nseq * b.f.hv * ((b.f.dv + 63) / 64) <= 256;
+  const int st = narrow ? launch_adjoint_t<E, DK, 4>(b, s)
+                        : launch_adjoint_t<E, DK, sizeof(E) == 2 ? 8 : 4>(b, s);
   if (st != MAMBA_OK) return st;
   hipLaunchKernelGGL((grad_kernel<E, DK>), dim3((unsigned)(b.f.slots * b.f.hk)), dim3(256), 0, s, b);
   return launch_status();
