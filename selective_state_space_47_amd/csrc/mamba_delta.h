@@ -115,14 +115,16 @@ __device__ __forceinline__ bf16x4 lds_tr(lds_ptr p) {
 
 // A 64-token tile of keys or queries in LDS: rows of kRow bytes, the 16-byte word w of row t kept at
 // w ^ key(t).  With this key the 16 rows of an operand read, and the 4 rows x 4 words of a transposing
-// read, lie in different banks.
+// read (of rows of 8 or more words), lie in different banks.
 template <typename E, int DK>
 struct KeyTile {
   static constexpr int kRow = DK * (int)sizeof(E);
   static constexpr int kWords = kRow / 16;
   static constexpr int kBytes = kC * kRow;
   __device__ static __forceinline__ int key(int t) {
-    return kWords >= 16 ? 4 * (t & 3) + ((t >> 2) & 3) : 4 * ((t >> 1) & 1) + ((t >> 2) & 3);
+    return kWords >= 16  ? 4 * (t & 3) + ((t >> 2) & 3)
+           : kWords == 8 ? 4 * ((t >> 1) & 1) + ((t >> 2) & 3)
+                         : (t >> 2) & 3;
   }
   // lane addresses of one tile
   int row0, tr0, g, r;
@@ -498,7 +500,7 @@ inline int check_delta_inputs(const mamba_delta_dims* d, const void* q, const vo
 // before the chunk and the adjoint of the state after it (columns x dk).
 template <typename E>
 struct BwdBlock {
-  static constexpr int kDB = sizeof(E) == 2 ? 64 : 32;
+  static constexpr int kDB = 32;
   static constexpr int kEParts = Mma<E>::parts(2);
   static constexpr int kE = kC * kDB * (int)sizeof(E);  // bytes of one part
   static int64_t blocks(int64_t dv) { return (dv + kDB - 1) / kDB; }

@@ -337,24 +337,31 @@ __device__ __forceinline__ float wave_suffix(float v, int lane) {
 template <typename E, int DK>
 struct GradSmem {
   using B = BwdBlock<E>;
-  static constexpr int kK = 0;
-  static constexpr int kQ = KeyTile<E, DK>::kBytes;
-  static constexpr int kDO = 2 * KeyTile<E, DK>::kBytes;
+  // one block of columns of the state: dO, dY, E, S, dS'
+  static constexpr int kDO = 0;
   static constexpr int kDY = kDO + B::kE;
   static constexpr int kE = kDY + B::kE;
   static constexpr int kS = kE + B::kEParts * B::kE;
   static constexpr int kDS = kS + B::kDB * KeyTile<E, DK>::kRow;
-  static constexpr int kB1 = kDS + B::kDB * KeyTile<E, DK>::kRow;
+  static constexpr int kStage = kDS + B::kDB * KeyTile<E, DK>::kRow;
   static constexpr int kBParts = Mma<E>::parts(2);
+  static constexpr int kK = 0;
+  static constexpr int kQ = KeyTile<E, DK>::kBytes;
+  static constexpr int kB1 = 2 * KeyTile<E, DK>::kBytes;
   static constexpr int kB2 = kB1 + kBParts * TriTile<E>::kBytes;
-  static constexpr int kGate = kB2 + kBParts * TriTile<E>::kBytes;  // gates and decays: 2 KB
-  static constexpr int kSums = kGate + 2048;              // per wave: column sums of X and of dbeta
-  static constexpr int kTok = kSums + 4 * 2 * kC * 4;     // per token: row sum of X
-  static constexpr int kBytes = kTok + kC * 4;
+  static constexpr int kGate = kB2 + kBParts * TriTile<E>::kBytes;  // gates and decays of two heads
+  static constexpr int kSums = kGate + 2 * 2048;                    // per wave: column sums
+  static constexpr int kTok = kSums + 8 * 2 * kC * 4;               // per half and token: row sums
+  static constexpr int kStages = (kTok + 2 * kC * 4 + 1023) / 1024 * 1024;
+  static constexpr int kCount = kStages + 2 * kStage <= 160 * 1024 ? 2 : 1;
+  static constexpr int kBytes = kStages + kCount * kStage;
 };
 
+// Eight waves: wave (tile, half) has the tokens 16 tile .. 16 tile + 15.  Half 0 makes M and B1, half 1 N
+// and B2; of dQ and dK each half has half of the keys' values.  The state's columns come in blocks of kDB,
+// head after head: the next block is copied while one is worked on.
 template <typename E, int DK>
-__global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
+__global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
   using M = Mma<E>;
   using Sm = GradSmem<E, DK>;
   using KT = KeyTile<E, DK>;
@@ -362,11 +369,12 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
   using BB = BwdBlock<E>;
   using ET = KeyTile<E, BB::kDB>;
   using CW = ChunkWs<E>;
-  constexpr int kTiles = DK / 16, kBP = Sm::kBParts;
+  constexpr int kTiles = DK / 32, kBP = Sm::kBParts;  // accumulator tiles of a wave's values
   __shared__ __align__(1024) char smem[Sm::kBytes];
   const Args& a = b.f;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = w & 3, half = w >> 2, m0 = half * kTiles;
   const int64_t wg = placed_index(blockIdx.x, gridDim.x);
   const int64_t slot = wg / a.hk;
   const int kh = (int)(wg - slot * a.hk);
@@ -385,167 +393,185 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
   const KT kt(lane);
   const TT tt(lane);
   const ET et(lane);
-  const int i = 16 * w + r;  // this lane's token
+  const int i = 16 * tile + r;  // this lane's token
+
+  // block db of head h into a stage, the head's gates with its first block
+  auto copy = [&](int h, int db, int st) {
+    const int64_t vh = kh * a.rep + h, item = slot * a.hv + vh;
+    const uint32_t to = lds0 + Sm::kStages + st * Sm::kStage;
+    const int cols = min(a.dv - db * BB::kDB, BB::kDB);
+    const int64_t at = (t0 * a.hv + vh) * (int64_t)a.dv + db * BB::kDB;
+    // dO and dY: a tile of 4 (bf16) or 8 KB each, the first by waves 0-3 and the second by 4-7
+    const RowCopy<E, ET, kC, 4> co(tile, lane, o_stride, cols);
+    co(rows_buffer(static_cast<const E*>(half ? b.dv : b.dout) + at, n, o_stride, cols),
+       to + (half ? Sm::kDY : Sm::kDO), tile);
+    constexpr int kBlock = BB::kDB * KT::kRow;
+    copy_linear<BB::kEParts * BB::kE, 8>(
+        a.e_img + item * e_bytes + (int64_t)db * BB::kEParts * BB::kE, to + Sm::kE, w, lane);
+    copy_linear<kBlock, 8>(a.s_img + item * img_bytes + (int64_t)db * kBlock, to + Sm::kS, w, lane);
+    copy_linear<kBlock, 8>(a.ds_img + item * img_bytes + (int64_t)db * kBlock, to + Sm::kDS, w, lane);
+    if (db == 0)
+      copy_linear<2048, 8>(a.ws + item * a.ws_item + CW::kGate, lds0 + Sm::kGate + (h & 1) * 2048, w, lane);
+  };
 
   {
-    const RowCopy<E, KT, kC, 4> ck(w, lane, a.k_stride, a.dk), cq(w, lane, a.q_stride, a.dk);
+    const RowCopy<E, KT, kC, 8> ck(w, lane, a.k_stride, a.dk), cq(w, lane, a.q_stride, a.dk);
     ck(rows_buffer(static_cast<const E*>(a.k) + t0 * a.k_stride + (int64_t)kh * a.dk, n, a.k_stride,
                    a.dk), lds0 + Sm::kK, w);
     cq(rows_buffer(static_cast<const E*>(a.q) + t0 * a.q_stride + (int64_t)kh * a.dk, n, a.q_stride,
                    a.dk), lds0 + Sm::kQ, w);
+    copy(0, 0, 0);
     copies_done();
   }
-  // rows j (tiles up to w), column i: k_j . k_i and k_j . q_i
-  f32x4 kk[4], qk[4], dQ[kTiles], dK[kTiles];
+  // rows j (tiles up to this one), column i: k_j . q_i, or k_j . k_i
+  f32x4 kx[4], dQ[kTiles], dK[kTiles];
 #pragma unroll
-  for (int jt = 0; jt < 4; ++jt) kk[jt] = qk[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int jt = 0; jt < 4; ++jt) kx[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int m = 0; m < kTiles; ++m) dQ[m] = dK[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-    const auto ki = kt.rows(sm + Sm::kK, w, kb), qi = kt.rows(sm + Sm::kQ, w, kb);
+    const auto xi = kt.rows(sm + (half ? Sm::kK : Sm::kQ), tile, kb);
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt)
-      if (jt <= w) {
-        const auto kj = kt.rows(sm + Sm::kK, jt, kb);
-        kk[jt] = M::mma(kj, ki, kk[jt]);
-        qk[jt] = M::mma(kj, qi, qk[jt]);
-      }
+      if (jt <= tile) kx[jt] = M::mma(kt.rows(sm + Sm::kK, jt, kb), xi, kx[jt]);
   }
 
+  int st = 0;
   for (int h = 0; h < a.rep; ++h) {
-    const int vh = kh * a.rep + h;
-    const int64_t item = slot * a.hv + vh;
-    f32x4 Mt[4], Nt[4], sdo[kTiles], sdy[kTiles], dse[kTiles];
+    f32x4 mn[4], sdo[kTiles], sdy[kTiles], dse[kTiles];
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) Mt[jt] = Nt[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int jt = 0; jt < 4; ++jt) mn[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) sdo[m] = sdy[m] = dse[m] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int db = 0; db < blocks; ++db) {
-      __syncthreads();  // the tiles of the block before have been read
-      const int cols = min(a.dv - db * BB::kDB, BB::kDB);
-      const RowCopy<E, ET, kC, 4> co(w, lane, o_stride, cols);
-      const int64_t at = (t0 * a.hv + vh) * (int64_t)a.dv + db * BB::kDB;
-      co(rows_buffer(static_cast<const E*>(b.dout) + at, n, o_stride, cols), lds0 + Sm::kDO, w);
-      co(rows_buffer(static_cast<const E*>(b.dv) + at, n, o_stride, cols), lds0 + Sm::kDY, w);
-      copy_linear<BB::kEParts * BB::kE, 4>(
-          a.e_img + item * e_bytes + (int64_t)db * BB::kEParts * BB::kE, lds0 + Sm::kE, w, lane);
-      constexpr int kBlock = BB::kDB * KT::kRow;
-      copy_linear<kBlock, 4>(a.s_img + item * img_bytes + (int64_t)db * kBlock, lds0 + Sm::kS, w, lane);
-      copy_linear<kBlock, 4>(a.ds_img + item * img_bytes + (int64_t)db * kBlock, lds0 + Sm::kDS, w, lane);
-      if (db == 0) copy_linear<2048, 4>(a.ws + item * a.ws_item + CW::kGate, lds0 + Sm::kGate, w, lane);
-      copies_done();
+      const bool more = db + 1 < blocks || h + 1 < a.rep;
+      const int nh = db + 1 < blocks ? h : h + 1, nb = db + 1 < blocks ? db + 1 : 0;
+      if (h + db > 0) copies_done();
+      if (Sm::kCount == 2 && more) copy(nh, nb, st ^ 1);
+      const lds_ptr bl = sm + Sm::kStages + st * Sm::kStage;
 #pragma unroll
       for (int kb = 0; kb < BB::kDB / M::kDepth; ++kb) {
-        const auto of = et.rows(sm + Sm::kDO, w, kb), yf = et.rows(sm + Sm::kDY, w, kb);
+        const auto of = et.rows(bl + Sm::kDO, tile, kb), yf = et.rows(bl + Sm::kDY, tile, kb);
+        const auto xf = half ? yf : of;
         typename M::Frag ef[BB::kEParts];
 #pragma unroll
-        for (int p = 0; p < BB::kEParts; ++p) ef[p] = et.rows(sm + Sm::kE + p * BB::kE, w, kb);
+        for (int p = 0; p < BB::kEParts; ++p) ef[p] = et.rows(bl + Sm::kE + p * BB::kE, tile, kb);
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
-          if (jt <= w) {
+          if (jt <= tile)
 #pragma unroll
-            for (int p = 0; p < BB::kEParts; ++p) {
-              const auto ej = et.rows(sm + Sm::kE + p * BB::kE, jt, kb);
-              Mt[jt] = M::mma(ej, of, Mt[jt]);
-              Nt[jt] = M::mma(ej, yf, Nt[jt]);
-            }
-          }
+            for (int p = 0; p < BB::kEParts; ++p)
+              mn[jt] = M::mma(et.rows(bl + Sm::kE + p * BB::kE, jt, kb), xf, mn[jt]);
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
-          const auto sf = kt.template cols<true>(sm + Sm::kS, m, kb);
+          const auto sf = kt.template cols<true>(bl + Sm::kS, m0 + m, kb);
+          const auto df = kt.template cols<true>(bl + Sm::kDS, m0 + m, kb);
           sdo[m] = M::mma(sf, of, sdo[m]);
           sdy[m] = M::mma(sf, yf, sdy[m]);
-          const auto df = kt.template cols<true>(sm + Sm::kDS, m, kb);
 #pragma unroll
           for (int p = 0; p < BB::kEParts; ++p) dse[m] = M::mma(df, ef[p], dse[m]);
         }
       }
-    }
-    // B1, B2, and the sums that reach dbeta and dg
-    const lds_ptr decay = sm + Sm::kGate + 1024;
-    const float gi = lds_read<float>(decay + 4 * i), gil = lds_read<float>(decay + 4 * (kC + i));
-    float row_x = 0.f;
-    f32x4 b1[4], b2[4];
-#pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      const int j = 16 * jt + 4 * g;
-      const f32x4 gj = lds_read<f32x4>(decay + 4 * j), gjl = lds_read<f32x4>(decay + 4 * (kC + j));
-      const f32x4 bj = lds_read<f32x4>(decay + 4 * (2 * kC + j));
-      f32x4 cx = {0.f, 0.f, 0.f, 0.f}, cb = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool in = jt <= w && j + x <= i;
-        const float d = in ? exp_f32((gi - gj[x]) + (gil - gjl[x])) : 0.f;
-        const float m1 = a.scale * d * Mt[jt][x], m2 = j + x < i ? -d * Nt[jt][x] : 0.f;
-        b1[jt][x] = m1 * bj[x];
-        b2[jt][x] = m2 * bj[x];
-        cb[x] = fmaf(m1, qk[jt][x], m2 * kk[jt][x]);
-        cx[x] = cb[x] * bj[x];
-        row_x += cx[x];
+      if (Sm::kCount == 2) {
+        st ^= 1;
+      } else if (more) {
+        __syncthreads();  // every wave has read the stage
+        copy(nh, nb, 0);
       }
-      if (jt <= w) {
+    }
+    const int64_t vh = kh * a.rep + h, item = slot * a.hv + vh;
+    const lds_ptr gate = sm + Sm::kGate + (h & 1) * 2048, decay = gate + 1024;
+    // B1 or B2, and the sums that reach dbeta and dg
+    {
+      const float gi = lds_read<float>(decay + 4 * i), gil = lds_read<float>(decay + 4 * (kC + i));
+      const float sign = half ? -1.f : a.scale;
+      const int last = half ? i - 1 : i;  // j up to here
+      float row_x = 0.f;
+      f32x4 bx[4];
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        const int j = 16 * jt + 4 * g;
+        const f32x4 gj = lds_read<f32x4>(decay + 4 * j), gjl = lds_read<f32x4>(decay + 4 * (kC + j));
+        const f32x4 bj = lds_read<f32x4>(decay + 4 * (2 * kC + j));
+        f32x4 cx, cb;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const float sx = group_sum(cx[x]), sb = group_sum(cb[x]);
-          if (r == 0) {
-            float* sums = reinterpret_cast<float*>(smem + Sm::kSums) + w * 2 * kC;
-            sums[j + x] = sx;
-            sums[kC + j + x] = sb;
+          const bool in = jt <= tile && j + x <= last;
+          const float m = in ? sign * exp_f32((gi - gj[x]) + (gil - gjl[x])) * mn[jt][x] : 0.f;
+          bx[jt][x] = m * bj[x];
+          cb[x] = m * kx[jt][x];
+          cx[x] = cb[x] * bj[x];
+          row_x += cx[x];
+        }
+        if (jt <= tile) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float sx = group_sum(cx[x]), sb = group_sum(cb[x]);
+            if (r == 0) {
+              float* sums = reinterpret_cast<float*>(smem + Sm::kSums) + w * 2 * kC;
+              sums[j + x] = sx;
+              sums[kC + j + x] = sb;
+            }
           }
         }
       }
+      row_x = across_groups(row_x);
+      if (g == 0) reinterpret_cast<float*>(smem + Sm::kTok)[half * kC + i] = row_x;
+#pragma unroll
+      for (int kb = 0; kb < TT::kBlocks; ++kb)
+        if (16 * tile >= kb * M::kDepth) {
+          const auto f = M::template split<kBP>(&bx[kb * M::kTiles]);
+#pragma unroll
+          for (int p = 0; p < kBP; ++p)
+            *reinterpret_cast<typename M::Frag*>(smem + (half ? Sm::kB2 : Sm::kB1) + p * TT::kBytes +
+                                                 TT::word_at(kb, i, g)) = f.p[p];
+        }
     }
-    row_x = across_groups(row_x);
-#pragma unroll
-    for (int kb = 0; kb < TT::kBlocks; ++kb)
-      if (16 * w >= kb * M::kDepth) {
-        const auto f1 = M::template split<kBP>(&b1[kb * M::kTiles]);
-        const auto f2 = M::template split<kBP>(&b2[kb * M::kTiles]);
-        const int at = TT::word_at(kb, i, g);
-#pragma unroll
-        for (int p = 0; p < kBP; ++p) {
-          *reinterpret_cast<typename M::Frag*>(smem + Sm::kB1 + p * TT::kBytes + at) = f1.p[p];
-          *reinterpret_cast<typename M::Frag*>(smem + Sm::kB2 + p * TT::kBytes + at) = f2.p[p];
-        }
-        // sums over j: this wave's own tiles
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          const auto kf = kt.cols(sm + Sm::kK, m, kb);
-#pragma unroll
-          for (int p = 0; p < kBP; ++p) {
-            dQ[m] = M::mma(kf, f1.p[p], dQ[m]);
-            dK[m] = M::mma(kf, f2.p[p], dK[m]);
-          }
-        }
-      }
     // the state's terms
-    const float eg = lds_read<float>(sm + Sm::kGate + 4 * i), ci = lds_read<float>(sm + Sm::kGate + 4 * (kC + i));
-    const float seg = a.scale * eg;
+    {
+      const float eg = lds_read<float>(gate + 4 * i), ci = lds_read<float>(gate + 4 * (kC + i));
+      const float seg = a.scale * eg;
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
+      for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        dQ[m][x] = fmaf(seg, sdo[m][x], dQ[m][x]);
-        dK[m][x] = fmaf(ci, dse[m][x], fmaf(-eg, sdy[m][x], dK[m][x]));
-      }
-    if (g == 0) {
-      reinterpret_cast<float*>(smem + Sm::kTok)[i] = row_x;
+        for (int x = 0; x < 4; ++x) {
+          dQ[m][x] = fmaf(seg, sdo[m][x], dQ[m][x]);
+          dK[m][x] = fmaf(ci, dse[m][x], fmaf(-eg, sdy[m][x], dK[m][x]));
+        }
     }
-    __syncthreads();
-    // sums over i: rows i of B1 and B2 at and below this wave's tile
+    // B1 and B2 are whole.  (Not a full barrier of the copies: the next block's are on their way.)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // sums over j (rows i of B1, B2), then over i (their columns)
 #pragma unroll
-    for (int ib = 0; ib < TT::kBlocks; ++ib)
-      if (16 * w < (ib + 1) * M::kDepth) {
+    for (int kb = 0; kb < TT::kBlocks; ++kb) {
+      if (16 * tile >= kb * M::kDepth) {
         typename M::Frag f1[kBP], f2[kBP];
 #pragma unroll
         for (int p = 0; p < kBP; ++p) {
-          f1[p] = tt.cols(sm + Sm::kB1 + p * TT::kBytes, w, ib);
-          f2[p] = tt.cols(sm + Sm::kB2 + p * TT::kBytes, w, ib);
+          f1[p] = tt.rows(sm + Sm::kB1 + p * TT::kBytes, tile, kb);
+          f2[p] = tt.rows(sm + Sm::kB2 + p * TT::kBytes, tile, kb);
         }
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
-          const auto qf = kt.cols(sm + Sm::kQ, m, ib), kf = kt.cols(sm + Sm::kK, m, ib);
+          const auto kf = kt.cols(sm + Sm::kK, m0 + m, kb);
+#pragma unroll
+          for (int p = 0; p < kBP; ++p) {
+            dQ[m] = M::mma(kf, f1[p], dQ[m]);
+            dK[m] = M::mma(kf, f2[p], dK[m]);
+          }
+        }
+      }
+      if (16 * tile < (kb + 1) * M::kDepth) {
+        typename M::Frag f1[kBP], f2[kBP];
+#pragma unroll
+        for (int p = 0; p < kBP; ++p) {
+          f1[p] = tt.cols(sm + Sm::kB1 + p * TT::kBytes, tile, kb);
+          f2[p] = tt.cols(sm + Sm::kB2 + p * TT::kBytes, tile, kb);
+        }
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const auto qf = kt.cols(sm + Sm::kQ, m0 + m, kb), kf = kt.cols(sm + Sm::kK, m0 + m, kb);
 #pragma unroll
           for (int p = 0; p < kBP; ++p) {
             dK[m] = M::mma(qf, f1[p], dK[m]);
@@ -553,9 +579,12 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
           }
         }
       }
+    }
     if (w == 0) {
       const float* sums = reinterpret_cast<const float*>(smem + Sm::kSums);
       const float* tok = reinterpret_cast<const float*>(smem + Sm::kTok);
+      const float* gt = reinterpret_cast<const float*>(smem + Sm::kGate + (h & 1) * 2048);
+      const float* dec = gt + 256;
       const int cbs = blocks * BB::kDB / 16;
       const float* adj = b.sums + item * cbs * kAdjSums;
       float rt = 0.f, kdt = 0.f, dot = 0.f;
@@ -564,16 +593,14 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
         kdt += adj[x * kAdjSums + kSumKd + lane];
         dot += adj[x * kAdjSums + kSumDot];
       }
-      const float* gate = reinterpret_cast<const float*>(smem + Sm::kGate);
-      const float* dec = gate + 256;
       float cx = 0.f, cb = 0.f;
-      for (int x = lane >> 4; x < 4; ++x) {
+      for (int x = lane >> 4; x < 8; x = x == 3 ? 4 + (lane >> 4) : x + 1) {
         cx += sums[x * 2 * kC + lane];
         cb += sums[x * 2 * kC + kC + lane];
       }
       const float e = exp_f32((dec[kC - 1] - dec[lane]) + (dec[2 * kC - 1] - dec[kC + lane]));
-      const float z = gate[kC + lane] * kdt;
-      const float after = wave_suffix(rt + (tok[lane] - cx), lane);
+      const float z = gt[kC + lane] * kdt;
+      const float after = wave_suffix(rt + ((tok[lane] + tok[kC + lane]) - cx), lane);
       float before = z;  // sum of z over the tokens before
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) {
@@ -581,7 +608,7 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
         if (lane >= m) before += t;
       }
       before = __shfl_up(before, 1);
-      const float whole = gate[2 * kC] * dot;
+      const float whole = gt[2 * kC] * dot;
       if (lane < n) {
         const int64_t at = (t0 + lane) * a.hv + vh;
         st_out(static_cast<E*>(b.dg), at, whole + (lane ? before : 0.f) + after);
@@ -593,11 +620,11 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdArgs b) {
     E* dqp = static_cast<E*>(b.dq) + ((t0 + i) * a.hk + kh) * (int64_t)a.dk;
     E* dkp = static_cast<E*>(b.dk) + ((t0 + i) * a.hk + kh) * (int64_t)a.dk;
 #pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      const int v = KT::value(kb * M::kTiles, g, 0);
+    for (int m = 0; m < kTiles; m += M::kTiles) {
+      const int v = KT::value(m0 + m, g, 0);
       if (v < a.dk) {
-        store_values(dqp + v, &dQ[kb * M::kTiles]);
-        store_values(dkp + v, &dK[kb * M::kTiles]);
+        store_values(dqp + v, &dQ[m]);
+        store_values(dkp + v, &dK[m]);
       }
     }
   }
@@ -618,7 +645,7 @@ int launch_bwd(const BwdArgs& b, hipStream_t s) {
   const int st = narrow ? launch_adjoint_t<E, DK, 4>(b, s)
                         : launch_adjoint_t<E, DK, sizeof(E) == 2 ? 8 : 4>(b, s);
   if (st != MAMBA_OK) return st;
-  hipLaunchKernelGGL((grad_kernel<E, DK>), dim3((unsigned)(b.f.slots * b.f.hk)), dim3(256), 0, s, b);
+  hipLaunchKernelGGL((grad_kernel<E, DK>), dim3((unsigned)(b.f.slots * b.f.hk)), dim3(512), 0, s, b);
   return launch_status();
 }
 
