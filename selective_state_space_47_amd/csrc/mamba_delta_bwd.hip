@@ -21,8 +21,8 @@
 //                   the key head add their dQ and dK in accumulators, in a fixed order: no atomics.
 // Every gradient is rounded once.  Rounding inside, bf16 storage: two bf16 parts of every factor, except
 // S, dS' and dY where dQ and dK take them (one part each: their rounding weighs less than the gradient's).
-// dg and dbeta are sums of signed terms that may cancel many times over: R, k . dS' e and <dS', S> are made
-// in adjoint_kernel from its accumulators, with S to 17 bits (a byte beside its bf16).
+// dg and dbeta are sums of signed terms that may cancel many times over: those that weigh most, k . dS' e and
+// <dS', S>, are made in adjoint_kernel from its accumulators, with S to 17 bits (a byte beside its bf16).
 #include "mamba_delta.h"
 
 namespace mamba {
@@ -42,9 +42,9 @@ struct BwdArgs {
   float* sums;         // per chunk slot, value head and 16 columns: their part of AdjSums
 };
 
-// What the adjoint pass leaves for dg and dbeta, summed over 16 columns of the state: R_i and k_j . dS' e_j
-// of the chunk's tokens, and <dS', S>.
-constexpr int kSumR = 0, kSumKd = kC, kSumDot = 2 * kC, kAdjSums = 2 * kC + 16;
+// What the adjoint pass leaves for dg and dbeta, summed over 16 columns of the state: k_j . dS' e_j of the
+// chunk's tokens, and <dS', S>.
+constexpr int kSumKd = 0, kSumDot = kC, kAdjSums = kC + 16;
 
 // 8 (bf16) or 4 (fp32) consecutive values from one operand's accumulators
 template <typename E>
@@ -137,63 +137,95 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
   const KT kt(lane);
   const TT tt(lane);
   const VT ot(lane, 16 * w);
-  if (nchunks > 0) copy(nchunks - 1, 0);
+  // The state before a chunk and its E come straight to registers, a chunk ahead like the copies.
+  const bool mine = col < dv_pad;
+  using E4 = decltype(ot.four(lds_ptr(), 0));  // four values as they are stored
+  typename M::Frag shi[DK / M::kDepth];
+  uint2 sl[DK / M::kDepth];
+  E4 ereg[BB::kEParts][4];
+  uint32_t s_off[DK / M::kDepth], e_off[4];
+  {
+    const int cw = (col + 4 * g) % BB::kDB * (int)sizeof(E);
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+      s_off[kb] = (col + r) * KT::kRow + (((4 * kb + g) ^ KT::key(col + r)) << 4);
+      shi[kb] = typename M::Frag{};
+      sl[kb] = make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int t = 16 * m + r;
+      e_off[m] = (col + 4 * g) / BB::kDB * BB::kEParts * BB::kE + t * ET::kRow +
+                 (((cw >> 4) ^ ET::key(t)) << 4) + (cw & 15);
+#pragma unroll
+      for (int p = 0; p < BB::kEParts; ++p) ereg[p][m] = E4{};
+    }
+  }
+  auto fetch_state = [&](int64_t ch) {
+    const int64_t item = (slot0 + ch) * a.hv + vh;
+    if (!mine) return;
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+      shi[kb] = *reinterpret_cast<const typename M::Frag*>(a.s_img + item * img_bytes + s_off[kb]);
+      if constexpr (sizeof(E) == 2)
+        sl[kb] = *reinterpret_cast<const uint2*>(
+            a.s_low + low_at<DK>(item, dv_pad / 16, col / 16, kb, lane));
+    }
+  };
+  auto fetch_e = [&](int64_t ch) {
+    const char* img = a.e_img + ((slot0 + ch) * a.hv + vh) * e_bytes;
+    if (!mine) return;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int p = 0; p < BB::kEParts; ++p)
+        ereg[p][m] = *reinterpret_cast<const E4*>(img + p * BB::kE + e_off[m]);
+  };
+  if (nchunks > 0) {
+    copy(nchunks - 1, 0);
+    fetch_state(nchunks - 1);
+    fetch_e(nchunks - 1);
+  }
   for (int64_t ch = nchunks - 1; ch >= 0; --ch) {
     const int st = St::kCount == 2 ? (int)((nchunks - 1 - ch) & 1) : 0;
     copies_done();
     if (St::kCount == 2 && ch > 0) copy(ch - 1, st ^ 1);
     const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
     const int n = (int)min((int64_t)kC, sp.len - ch * kC);
-    // dS' goes to its image.  The state before the chunk, in the same layout, meets it and its products
-    // with Q and K here, where dS' and dY are still accumulators.
+    // dS' goes to its image and meets the state before the chunk, in the same layout
     const int64_t item = (slot0 + ch) * a.hv + vh;
-    const bool mine = col < dv_pad;
-    typename M::template Parts<kP2> ds[DK / M::kDepth], sf[DK / M::kDepth];
+    typename M::template Parts<kP2> ds[DK / M::kDepth];
     float dot = 0.f;
 #pragma unroll
     for (int kb = 0; kb < DK / M::kDepth; ++kb) {
       ds[kb] = M::template split<kP2>(&S[kb * M::kTiles]);
-      f32x4 f[M::kTiles];
+      if (mine) *reinterpret_cast<typename M::Frag*>(a.ds_img + item * img_bytes + s_off[kb]) = ds[kb].p[0];
+      if constexpr (sizeof(E) == 2) {
+        const uint4 h = __builtin_bit_cast(uint4, shi[kb]);
+        const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[2] = {sl[kb].x, sl[kb].y};
 #pragma unroll
-      for (int x = 0; x < M::kTiles; ++x) f[x] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (mine) {
-        const int64_t at = item * img_bytes + (int64_t)(col + r) * KT::kRow +
-                           (((4 * kb + g) ^ KT::key(col + r)) << 4);
-        *reinterpret_cast<typename M::Frag*>(a.ds_img + at) = ds[kb].p[0];
-        if constexpr (sizeof(E) == 2) {
-          const uint4 h = *reinterpret_cast<const uint4*>(a.s_img + at);
-          const uint2 l = *reinterpret_cast<const uint2*>(
-              a.s_low + low_at<DK>(item, dv_pad / 16, col / 16, kb, lane));
-          const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[2] = {l.x, l.y};
+        for (int x = 0; x < 8; ++x)
+          dot = fmaf(S[2 * kb + (x >> 2)][x & 3],
+                     with_low(x & 1 ? hw[x >> 1] & 0xffff0000u : hw[x >> 1] << 16, lw[x >> 2], x & 3), dot);
+      } else {
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            f[x >> 2][x & 3] =
-                with_low(x & 1 ? hw[x >> 1] & 0xffff0000u : hw[x >> 1] << 16, lw[x >> 2], x & 3);
-        } else {
-          f[0] = *reinterpret_cast<const f32x4*>(a.s_img + at);
-        }
+        for (int x = 0; x < 4; ++x) dot = fmaf(S[kb][x], shi[kb][x], dot);
       }
-#pragma unroll
-      for (int y = 0; y < M::kTiles; ++y)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) dot = fmaf(S[kb * M::kTiles + y][x], f[y][x], dot);
-      sf[kb] = M::template split<kP2>(f);
     }
-    // K dS' both ways round, and (Q S)^T, (K S)^T: columns x tokens
-    f32x4 e[4], kd[4], qs[4], ks[4];
+    if (ch > 0) fetch_state(ch - 1);
+    // K dS' both ways round
+    f32x4 e[4], kd[4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) e[m] = kd[m] = qs[m] = ks[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < 4; ++m) e[m] = kd[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < DK / M::kDepth; ++kb)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const auto kf = kt.rows(sm + St::kK, m, kb), qf = kt.rows(sm + St::kQ, m, kb);
+        const auto kf = kt.rows(sm + St::kK, m, kb);
 #pragma unroll
         for (int p = 0; p < kP2; ++p) {
           e[m] = M::mma(kf, ds[kb].p[p], e[m]);
           kd[m] = M::mma(ds[kb].p[p], kf, kd[m]);
-          qs[m] = M::mma(sf[kb].p[p], qf, qs[m]);
-          ks[m] = M::mma(sf[kb].p[p], kf, ks[m]);
         }
       }
     // dE = diag(c) K dS' + P^T dO
@@ -229,47 +261,23 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
     }
     // token 16 m + r, columns col + 4 g .. +3
     float* sums = b.sums + (item * (dv_pad / 16) + col / 16) * kAdjSums;
+    const auto buf = __builtin_amdgcn_make_buffer_rsrc(
+        dvp + ch * kC * o_stride, 0, (int)(((n - 1) * o_stride + max(a.dv - col, 0)) * (int64_t)sizeof(E)),
+        0x00020000);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int t = 16 * m + r;
-      if (t < n && col + 4 * g < a.dv) {
-        E* dst = dvp + (ch * kC + t) * o_stride + 4 * g;
-        if constexpr (sizeof(E) == 2)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(make_float2(yt[m][0], yt[m][1])),
-                                                      pack_bf16(make_float2(yt[m][2], yt[m][3])));
-        else
-          *reinterpret_cast<f32x4*>(dst) = yt[m];
-      }
-      const float eg = lds_read<float>(sm + St::kGate + t * 4);
-      float rr = 0.f, kk = 0.f;
-      if (mine) {
-        f32x4 ev = {0.f, 0.f, 0.f, 0.f}, od;
-        const int cw = (col + 4 * g) % BB::kDB * (int)sizeof(E);
-        const char* img = a.e_img + item * e_bytes + (int64_t)((col + 4 * g) / BB::kDB) * BB::kEParts * BB::kE +
-                          t * ET::kRow + (((cw >> 4) ^ ET::key(t)) << 4) + (cw & 15);
-        const lds_ptr op = sm + St::kDO + t * VT::kRow + (16 * w + 4 * g) * (int)sizeof(E);
-        if constexpr (sizeof(E) == 2) {
+      store_four<E>(buf, col + 4 * g < a.dv ? (uint32_t)(t * o_stride + 4 * g) * (uint32_t)sizeof(E) : kOutside,
+                    yt[m]);
+      f32x4 ev = __builtin_convertvector(ereg[0][m], f32x4);
+      if constexpr (BB::kEParts == 2) ev += __builtin_convertvector(ereg[1][m], f32x4);
+      float kk = 0.f;
 #pragma unroll
-          for (int p = 0; p < BB::kEParts; ++p)
-            ev += __builtin_convertvector(*reinterpret_cast<const bf16x4*>(img + p * BB::kE), f32x4);
-          od = __builtin_convertvector(lds_read<bf16x4>(op), f32x4);
-        } else {
-          ev = *reinterpret_cast<const f32x4*>(img);
-          od = lds_read<f32x4>(op);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          rr = fmaf(a.scale * qs[m][x], od[x], fmaf(-ks[m][x], yt[m][x], rr));
-          kk = fmaf(kd[m][x], ev[x], kk);
-        }
-      }
-      rr = across_groups(rr * eg);
+      for (int x = 0; x < 4; ++x) kk = fmaf(kd[m][x], ev[x], kk);
       kk = across_groups(kk);
-      if (mine && g == 0) {
-        sums[kSumR + t] = rr;
-        sums[kSumKd + t] = kk;
-      }
+      if (mine && g == 0) sums[kSumKd + t] = kk;
     }
+    if (ch > 0) fetch_e(ch - 1);
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
     if (mine && lane == 0) sums[kSumDot] = dot;
@@ -352,7 +360,8 @@ struct GradSmem {
   static constexpr int kGate = kB2 + kBParts * TriTile<E>::kBytes;  // gates and decays of two heads
   static constexpr int kSums = kGate + 2 * 2048;                    // per wave: column sums
   static constexpr int kTok = kSums + 8 * 2 * kC * 4;               // per half and token: row sums
-  static constexpr int kStages = (kTok + 2 * kC * 4 + 1023) / 1024 * 1024;
+  static constexpr int kAdj = kTok + 2 * kC * 4;                    // per wave: adjoint pass's sums
+  static constexpr int kStages = (kAdj + 8 * kAdjSums * 4 + 1023) / 1024 * 1024;
   static constexpr int kCount = kStages + 2 * kStage <= 160 * 1024 ? 2 : 1;
   static constexpr int kBytes = kStages + kCount * kStage;
 };
@@ -439,6 +448,17 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
 
   int st = 0;
   for (int h = 0; h < a.rep; ++h) {
+    const int64_t vh = kh * a.rep + h, item = slot * a.hv + vh;
+    // this wave's share of the adjoint pass's sums, on their way while the blocks are worked on
+    float kd = 0.f, dot = 0.f;
+    {
+      const int cbs = blocks * BB::kDB / 16;
+      const float* adj = b.sums + item * cbs * kAdjSums;
+      for (int x = w; x < cbs; x += 8) {
+        kd += adj[x * kAdjSums + kSumKd + lane];
+        dot += adj[x * kAdjSums + kSumDot];
+      }
+    }
     f32x4 mn[4], sdo[kTiles], sdy[kTiles], dse[kTiles];
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) mn[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -480,14 +500,13 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
         copy(nh, nb, 0);
       }
     }
-    const int64_t vh = kh * a.rep + h, item = slot * a.hv + vh;
     const lds_ptr gate = sm + Sm::kGate + (h & 1) * 2048, decay = gate + 1024;
     // B1 or B2, and the sums that reach dbeta and dg
+    float row_x = 0.f;
     {
       const float gi = lds_read<float>(decay + 4 * i), gil = lds_read<float>(decay + 4 * (kC + i));
       const float sign = half ? -1.f : a.scale;
       const int last = half ? i - 1 : i;  // j up to here
-      float row_x = 0.f;
       f32x4 bx[4];
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
@@ -517,7 +536,6 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
         }
       }
       row_x = across_groups(row_x);
-      if (g == 0) reinterpret_cast<float*>(smem + Sm::kTok)[half * kC + i] = row_x;
 #pragma unroll
       for (int kb = 0; kb < TT::kBlocks; ++kb)
         if (16 * tile >= kb * M::kDepth) {
@@ -528,17 +546,31 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
                                                  TT::word_at(kb, i, g)) = f.p[p];
         }
     }
-    // the state's terms
+    // the state's terms, and their dots with q_i and k_i (half of the values each half)
     {
       const float eg = lds_read<float>(gate + 4 * i), ci = lds_read<float>(gate + 4 * (kC + i));
-      const float seg = a.scale * eg;
+      float rdot = 0.f;
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m)
+      for (int kb = 0; kb < kTiles / M::kTiles; ++kb) {
+        const auto ki = kt.rows(sm + Sm::kK, tile, m0 / M::kTiles + kb);
+        const auto qi = kt.rows(sm + Sm::kQ, tile, m0 / M::kTiles + kb);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          dQ[m][x] = fmaf(seg, sdo[m][x], dQ[m][x]);
-          dK[m][x] = fmaf(ci, dse[m][x], fmaf(-eg, sdy[m][x], dK[m][x]));
-        }
+        for (int y = 0; y < M::kTiles; ++y)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int m = kb * M::kTiles + y;
+            const float so = a.scale * eg * sdo[m][x], sy = -eg * sdy[m][x];
+            rdot = fmaf((float)qi[4 * y + x], so, fmaf((float)ki[4 * y + x], sy, rdot));
+            dQ[m][x] += so;
+            dK[m][x] += fmaf(ci, dse[m][x], sy);
+          }
+      }
+      rdot = across_groups(rdot);
+      float* tok = reinterpret_cast<float*>(smem + Sm::kTok);
+      if (g == 0) tok[half * kC + i] = row_x + rdot;
+      float* adj = reinterpret_cast<float*>(smem + Sm::kAdj) + w * kAdjSums;
+      adj[kSumKd + lane] = kd;
+      if (lane == 0) adj[kSumDot] = dot;
     }
     // B1 and B2 are whole.  (Not a full barrier of the copies: the next block's are on their way.)
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -585,13 +617,12 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
       const float* tok = reinterpret_cast<const float*>(smem + Sm::kTok);
       const float* gt = reinterpret_cast<const float*>(smem + Sm::kGate + (h & 1) * 2048);
       const float* dec = gt + 256;
-      const int cbs = blocks * BB::kDB / 16;
-      const float* adj = b.sums + item * cbs * kAdjSums;
-      float rt = 0.f, kdt = 0.f, dot = 0.f;
-      for (int x = 0; x < cbs; ++x) {
-        rt += adj[x * kAdjSums + kSumR + lane];
+      const float* adj = reinterpret_cast<const float*>(smem + Sm::kAdj);
+      float kdt = 0.f, all = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
         kdt += adj[x * kAdjSums + kSumKd + lane];
-        dot += adj[x * kAdjSums + kSumDot];
+        all += adj[x * kAdjSums + kSumDot];
       }
       float cx = 0.f, cb = 0.f;
       for (int x = lane >> 4; x < 8; x = x == 3 ? 4 + (lane >> 4) : x + 1) {
@@ -600,7 +631,7 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
       }
       const float e = exp_f32((dec[kC - 1] - dec[lane]) + (dec[2 * kC - 1] - dec[kC + lane]));
       const float z = gt[kC + lane] * kdt;
-      const float after = wave_suffix(rt + ((tok[lane] + tok[kC + lane]) - cx), lane);
+      const float after = wave_suffix((tok[lane] + tok[kC + lane]) - cx, lane);
       float before = z;  // sum of z over the tokens before
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) {
@@ -608,7 +639,7 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
         if (lane >= m) before += t;
       }
       before = __shfl_up(before, 1);
-      const float whole = gt[2 * kC] * dot;
+      const float whole = gt[2 * kC] * all;
       if (lane < n) {
         const int64_t at = (t0 + lane) * a.hv + vh;
         st_out(static_cast<E*>(b.dg), at, whole + (lane ? before : 0.f) + after);
