@@ -20,9 +20,9 @@
 namespace mamba {
 namespace {
 
-// threads of a workgroup of teams of T lanes
+// threads of a workgroup of teams of T lanes: from two waves on a team is a workgroup
 template <int T>
-constexpr int kBlock = T > 256 ? T : 256;
+constexpr int kBlock = T >= 128 ? T : 256;
 constexpr int64_t kNormMaxDim = 16384;     // 1024 lanes x 2 vectors x 8 values
 constexpr int64_t kNormMaxUnits = 0x7fffffff;
 // Workgroups of a gradient launch: enough to fill 256 CUs at the kernel's occupancy, few enough
@@ -67,6 +67,39 @@ __device__ __forceinline__ void st8(float* p, const float (&v)[8]) {
   *reinterpret_cast<f32x4u*>(p + 4) = b;
 }
 
+// 8 values as they are stored (a row on its way takes half the registers of its values)
+template <typename E>
+struct RawVec;
+template <>
+struct RawVec<uint16_t> {
+  u32x4u w;
+  __device__ __forceinline__ void get(const uint16_t* p) { w = *reinterpret_cast<const u32x4u*>(p); }
+  __device__ __forceinline__ void some(const uint16_t* p, int n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = (2 * k < n ? (uint32_t)p[2 * k] : 0u) | (2 * k + 1 < n ? (uint32_t)p[2 * k + 1] << 16 : 0u);
+  }
+  __device__ __forceinline__ float operator[](int k) const {
+    return __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
+  }
+};
+template <>
+struct RawVec<float> {
+  f32x4u a, b;
+  __device__ __forceinline__ void get(const float* p) {
+    a = *reinterpret_cast<const f32x4u*>(p);
+    b = *reinterpret_cast<const f32x4u*>(p + 4);
+  }
+  __device__ __forceinline__ void some(const float* p, int n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = k < n ? p[k] : 0.f;
+      b[k] = 4 + k < n ? p[4 + k] : 0.f;
+    }
+  }
+  __device__ __forceinline__ float operator[](int k) const { return k < 4 ? a[k & 3] : b[k & 3]; }
+};
+
 // A lane's R vectors of one unit: vector r covers columns 8 (l + r T) .. +7 of `dim`.
 template <int T, int R>
 struct Cols {
@@ -85,6 +118,17 @@ struct Cols {
     }
   }
   template <typename E>
+  __device__ __forceinline__ void load(const E* p, RawVec<E> (&v)[R], bool live) const {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int c = 8 * (l + r * T);
+      if (live && c + 8 <= dim)
+        v[r].get(p + c);
+      else
+        v[r].some(p + c, live ? dim - c : 0);
+    }
+  }
+  template <typename E>
   __device__ __forceinline__ void store(E* p, const float (&v)[R][8]) const {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -100,6 +144,16 @@ struct Cols {
   }
 };
 
+template <int kCtrl>
+__device__ __forceinline__ float dpp_any(float v) { return dpp_row<kCtrl>(v); }
+template <int kCtrl>
+__device__ __forceinline__ double dpp_any(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __float_as_uint(dpp_row<kCtrl>(__uint_as_float((uint32_t)b)));
+  const uint32_t hi = __float_as_uint(dpp_row<kCtrl>(__uint_as_float((uint32_t)(b >> 32))));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // Sum of v over the team, in every lane.  T > 64 goes through LDS; the two slots alternate so that
 // one barrier per call is enough (a slot is written again only after the barrier of the next call).
 template <int T, typename V>
@@ -108,11 +162,23 @@ struct TeamSum {
   int turn = 0;
   template <int N>
   __device__ __forceinline__ void operator()(V (&v)[N]) {
-    static_assert(N <= 2, "slots hold two sums");
+    static_assert(N <= 2 && (T == 8 || T >= 16), "slots hold two sums");
+    // inside rows of 16 lanes by DPP rotations (a team of 8: xor by mirrors), further by lane exchange
 #pragma unroll
-    for (int m = 1; m < (T < 64 ? T : 64); m *= 2)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m);
+    for (int i = 0; i < N; ++i) {
+      if constexpr (T >= 16) {
+        v[i] += dpp_any<0x128>(v[i]);
+        v[i] += dpp_any<0x124>(v[i]);
+        v[i] += dpp_any<0x122>(v[i]);
+        v[i] += dpp_any<0x121>(v[i]);
+      } else {
+        v[i] += dpp_any<0xb1>(v[i]);   // quad_perm 1,0,3,2
+        v[i] += dpp_any<0x4e>(v[i]);   // quad_perm 2,3,0,1
+        v[i] += dpp_any<0x141>(v[i]);  // half row mirrored: lane 7 - l
+      }
+      if constexpr (T >= 32) v[i] += __shfl_xor(v[i], 16);
+      if constexpr (T >= 64) v[i] += __shfl_xor(v[i], 32);
+    }
     if constexpr (T > 64) {
       const int w = threadIdx.x >> 6, first = w / (T / 64) * (T / 64);
       if ((threadIdx.x & 63) == 0)
@@ -246,17 +312,35 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_bwd_kernel(GatedArgs a, 
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[r][k] = 0.f;
   const double inv = 1.0 / a.dim;
-  // every team runs the same number of turns (the reductions hold barriers)
-  for (uint32_t base = blockIdx.x * kTeams; base < units; base += gridDim.x * kTeams) {
+  // every team runs the same number of turns (the reductions hold barriers); the next unit is on its way
+  // while one is worked on
+  RawVec<E> yn[R], zn[R], dn[R];
+  auto fetch = [&](uint32_t base) {
+    const uint32_t u = base + threadIdx.x / T;
+    const bool live = u < units;
+    const Unit at = unit_of(a, live ? u : 0);
+    const int64_t grp = (int64_t)at.grp * a.dim;
+    cols.load(static_cast<const E*>(a.y) + at.row * a.y_stride + grp, yn, live);
+    cols.load(static_cast<const E*>(a.z) + at.row * a.z_stride + grp, zn, live && a.z);
+    cols.load(static_cast<const E*>(a.dout) + at.row * a.groups * (int64_t)a.dim + grp, dn, live);
+  };
+  const uint32_t stride = gridDim.x * kTeams;
+  fetch(blockIdx.x * kTeams);
+  for (uint32_t base = blockIdx.x * kTeams; base < units; base += stride) {
     const uint32_t u = base + threadIdx.x / T;
     const bool live = u < units;
     const Unit at = unit_of(a, live ? u : 0);
     const int64_t packed = (at.row * a.groups + at.grp) * (int64_t)a.dim;
     float y[R][8], z[R][8], d[R][8];
-    cols.load(static_cast<const E*>(a.y) + at.row * a.y_stride + (int64_t)at.grp * a.dim, y, live);
-    cols.load(static_cast<const E*>(a.dout) + packed, d, live);
-    if (a.z)
-      cols.load(static_cast<const E*>(a.z) + at.row * a.z_stride + (int64_t)at.grp * a.dim, z, live);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        y[r][k] = yn[r][k];
+        z[r][k] = zn[r][k];
+        d[r][k] = dn[r][k];
+      }
+    if (units - base > stride) fetch(base + stride);
     // v = the normed value (y, or y silu(z)); s = sum v^2, sum dh v
     double s[2] = {0.0, 0.0};
 #pragma unroll
@@ -379,27 +463,48 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
   __shared__ float sum[kTeams > 1 ? 8 * T * R : 1];
   TeamSum<T, double> team_sum{slot};
   const Cols<T, R> cols{(int)(threadIdx.x % T), a.dim};
-  float aw[R][8], ah[R][8];
+  // per column, for all rows: w; p = scale post (the weight of the normed x in r); and the sums
+  float w[R][8], p[R][8], aw[R][8], ah[R][8];
+  cols.load(a.w, w);
+  if (a.post) cols.load(a.post, p);
+  if (a.scale) cols.load(a.scale, aw);
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) aw[r][k] = ah[r][k] = 0.f;
+    for (int k = 0; k < 8; ++k) {
+      p[r][k] = (a.post ? p[r][k] : 1.f) * (a.scale ? aw[r][k] : 1.f);
+      aw[r][k] = ah[r][k] = 0.f;
+    }
   const double inv = 1.0 / a.dim;
-  for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows;
-       base += (int64_t)gridDim.x * kTeams) {
+  const int64_t stride = (int64_t)gridDim.x * kTeams;
+  // the next row is on its way while one is worked on
+  RawVec<E> xn[R], dn[R];
+  RawVec<S> qn[R], en[R];
+  auto fetch = [&](int64_t base) {
     const int64_t row = base + threadIdx.x / T;
     const bool live = row < a.rows;
     const int64_t at = (live ? row : 0) * a.dim;
-    float x[R][8], v[R][8], d[R][8], p[R][8];
-    cols.load(static_cast<const E*>(a.x) + at, x, live);
-    if (a.residual)
-      cols.load(static_cast<const S*>(a.residual) + at, v, live);
-    else
+    cols.load(static_cast<const E*>(a.x) + at, xn, live);
+    cols.load(static_cast<const S*>(a.residual) + at, qn, live && a.residual);
+    cols.load(static_cast<const E*>(a.dout) + at, dn, live);
+    cols.load(static_cast<const S*>(a.dres) + at, en, live && a.dres);
+  };
+  fetch((int64_t)blockIdx.x * kTeams);
+  for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows; base += stride) {
+    const int64_t row = base + threadIdx.x / T;
+    const bool live = row < a.rows;
+    const int64_t at = (live ? row : 0) * a.dim;
+    float x[R][8], v[R][8], d[R][8], e[R][8];
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[r][k] = 0.f;
-    cols.load(static_cast<const E*>(a.dout) + at, d, live);
+      for (int k = 0; k < 8; ++k) {
+        x[r][k] = xn[r][k];
+        v[r][k] = qn[r][k];
+        d[r][k] = dn[r][k];
+        e[r][k] = en[r][k];
+      }
+    if (base + stride < a.rows) fetch(base + stride);
     double rx2 = 1.0;
     if (a.post) {
       double s[1] = {0.0};
@@ -411,63 +516,29 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
       rx2 = 1.0 / fma(s[0], inv, (double)a.eps);
     }
     const float rx = sqrtf((float)rx2);  // the normed x is x rx
-    // p = scale post (the weight of the normed x in r); v = r; d = dout w
-    if (a.post) {
-      cols.load(a.post, p);
-    } else {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[r][k] = 1.f;
-    }
-    if (a.scale) {
-      float t[R][8];
-      cols.load(a.scale, t);
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[r][k] *= t[r][k];
-    }
     double s[2] = {0.0, 0.0};
-    {
-      float w[R][8];
-      cols.load(a.w, w);
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[r][k] = fmaf(p[r][k], x[r][k] * rx, v[r][k]);
-          s[0] = fma((double)v[r][k], (double)v[r][k], s[0]);
-          s[1] = fma((double)(d[r][k] * w[r][k]), (double)v[r][k], s[1]);
-        }
-      team_sum(s);
-      const double r2 = 1.0 / fma(s[0], inv, (double)a.eps), m = s[1] * r2 * inv;
-      const float rs = sqrtf((float)r2);
+      for (int k = 0; k < 8; ++k) {
+        v[r][k] = fmaf(p[r][k], x[r][k] * rx, v[r][k]);  // r
+        s[0] = fma((double)v[r][k], (double)v[r][k], s[0]);
+        s[1] = fma((double)(d[r][k] * w[r][k]), (double)v[r][k], s[1]);
+      }
+    team_sum(s);
+    const double r2 = 1.0 / fma(s[0], inv, (double)a.eps), m = s[1] * r2 * inv;
+    const float rs = sqrtf((float)r2);
+    // v = dr.  With h the normed x, dscale = sum(dr post h) and dpost = sum(dr scale h): the other factor is
+    // constant per column, so that both come from one sum.
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          aw[r][k] = fmaf(d[r][k], v[r][k] * rs, aw[r][k]);
-          v[r][k] = rs * minus(d[r][k] * w[r][k], v[r][k], m);
-        }
-    }
-    if (a.dres) {
-      cols.load(static_cast<const S*>(a.dres) + at, d, live);
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[r][k] += d[r][k];
-    }
-    // v = dr
+      for (int k = 0; k < 8; ++k) {
+        aw[r][k] = fmaf(d[r][k], v[r][k] * rs, aw[r][k]);
+        v[r][k] = fmaf(rs, minus(d[r][k] * w[r][k], v[r][k], m), e[r][k]);
+        ah[r][k] = fmaf(v[r][k], x[r][k] * rx, ah[r][k]);
+      }
     if (live && a.res_out) cols.store(static_cast<S*>(a.res_out) + at, v);
-    if (a.scale || a.post) {
-      // with h the normed x: dscale = sum(dr post h), dpost = sum(dr scale h).  The other factor is
-      // constant per column, so that both come from one sum.
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) ah[r][k] = fmaf(v[r][k], x[r][k] * rx, ah[r][k]);
-    }
     if (a.post) {
       double t[1] = {0.0};
 #pragma unroll
@@ -475,11 +546,11 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) t[0] = fma((double)(v[r][k] * p[r][k]), (double)x[r][k], t[0]);
       team_sum(t);
-      const double m = t[0] * rx2 * inv;
+      const double mx = t[0] * rx2 * inv;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[r][k] = rx * minus(v[r][k] * p[r][k], x[r][k], m);
+        for (int k = 0; k < 8; ++k) x[r][k] = rx * minus(v[r][k] * p[r][k], x[r][k], mx);
     } else {
 #pragma unroll
       for (int r = 0; r < R; ++r)
@@ -532,21 +603,22 @@ __global__ __launch_bounds__(1024) void norm_fold_kernel(FoldArgs a) {
 
 // ------------------------------------------------------------------ host
 
-// The team of a unit of `dim` values: calls f.template operator()<T, R>().  The narrowest team
-// with at most 3 vectors per lane: up to 1536 values the sums stay inside a wave, wider rows take 2
-// or 4 waves, and past 6144 values 16 (the gradients hold six values per column in registers).
+// The team of a unit of `dim` values: calls f.template operator()<T, R>().  One vector per lane, so that a
+// gradient's rows (up to six values per column) leave room for many waves: 2560 values, gradients, 16384
+// rows, bf16 with an fp32 stream: 164 us with 5 waves of one vector, 316 us with 2
+// waves of three.
 template <typename F>
 int with_team(int64_t dim, F f) {
   if (dim <= 64) return f.template operator()<8, 1>();
   if (dim <= 128) return f.template operator()<16, 1>();
   if (dim <= 256) return f.template operator()<32, 1>();
   if (dim <= 512) return f.template operator()<64, 1>();
-  if (dim <= 1024) return f.template operator()<64, 2>();
-  if (dim <= 8 * 64 * 3) return f.template operator()<64, 3>();
-  if (dim <= 2048) return f.template operator()<128, 2>();
-  if (dim <= 8 * 128 * 3) return f.template operator()<128, 3>();
-  if (dim <= 4096) return f.template operator()<256, 2>();
-  if (dim <= 8 * 256 * 3) return f.template operator()<256, 3>();
+  if (dim <= 1024) return f.template operator()<128, 1>();
+  if (dim <= 8 * 192) return f.template operator()<192, 1>();
+  if (dim <= 2048) return f.template operator()<256, 1>();
+  if (dim <= 8 * 320) return f.template operator()<320, 1>();
+  if (dim <= 4096) return f.template operator()<512, 1>();
+  if (dim <= 8 * 640) return f.template operator()<640, 1>();
   if (dim <= 8192) return f.template operator()<1024, 1>();
   return f.template operator()<1024, 2>();
 }
@@ -607,7 +679,7 @@ uint32_t gated_units(const GatedArgs& a) {
   return (uint32_t)(a.per_group ? a.rows : a.rows * a.groups);
 }
 uint32_t bwd_wgs(int64_t units, int64_t dim, int64_t ny) {
-  const int64_t teams = std::max(1, 256 / team_lanes(dim));
+  const int64_t teams = team_lanes(dim) >= 128 ? 1 : 256 / team_lanes(dim);
   const int64_t need = (units + teams - 1) / teams;
   return (uint32_t)std::min(need, std::max<int64_t>(1, kNormBwdWG / ny));
 }
