@@ -10,6 +10,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmamba_scan.so")
+MARSHAL_PATH = os.path.join(LIB_DIR, "mamba_marshal.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("mamba_scan.hip", "mamba_scan_ts.hip",
                                             "mamba_scan_bwd.hip", "mamba_gemm.hip",
                                             "mamba_block.hip", "mamba_norm.hip", "mamba_delta.hip",
@@ -28,8 +29,31 @@ def hipcc() -> str:
     return os.path.join(rocm, "bin", "hipcc")
 
 
+def build_marshal() -> str:
+    """Compile the binding's per-call part (host code only) against torch's headers and the library."""
+    import sysconfig
+
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    tmp = MARSHAL_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", INCLUDE, "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "mamba_marshal.cpp"),
+           "-o", tmp, "-L", LIB_DIR, "-l:libmamba_scan.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(torch_dir, "lib"), "-Wl,--no-as-needed", "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, MARSHAL_PATH)
+    return MARSHAL_PATH
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into selective_state_space_47_amd/_lib/libmamba_scan.so."""
+    """Compile every HIP source into selective_state_space_47_amd/_lib/libmamba_scan.so, and the
+    binding's per-call part beside it."""
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [hipcc()] + HIPCC_FLAGS + ["-I", INCLUDE, "-o", tmp] + SOURCES
@@ -39,6 +63,7 @@ def build(verbose: bool = False) -> str:
     if verbose and res.stderr:
         print(res.stderr)
     os.replace(tmp, LIB_PATH)
+    build_marshal()
     return LIB_PATH
 
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -619,51 +620,78 @@ def _token_stride(t, name, vec):
     return stride
 
 
-# dims structs (read-only for the library), the workspace size and whether the tensors' metadata
-# passed the checks, per combination of shapes, strides, types and devices
-_DELTA_CACHE = {}
+# The per-call part in native code (mamba_marshal.cpp): a call's tensors as one bytes key of their types,
+# shapes, strides and devices, and their addresses handed to the entry point.  A key that has passed the
+# checks below passes them again; its entry in _CHECKED holds the dims struct (read-only for the library),
+# its address, the workspace size and the device.
+_CHECKED = {}
+_MARSHAL = None
+(_DELTA_FWD, _DELTA_UPDATE, _DELTA_BWD, _GATED_FWD, _GATED_BWD, _ADD_FWD, _ADD_BWD) = range(7)
 
 
-def _meta(t):
-    """What the checks look at: two tensors of equal metadata pass or fail alike."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        return type(t)
-    return t.shape, t.stride(), t.dtype, t.get_device()
+def _marshal():
+    """The native module (raises RuntimeError if it has not been built)."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        lib()
+        with _lock:
+            path = _build.MARSHAL_PATH
+            if not os.path.exists(path):
+                raise RuntimeError(
+                    f"native module {path} is missing: build it with "
+                    "`python -c 'import __graft_entry__ as g; g.build()'`")
+            spec = importlib.util.spec_from_file_location("mamba_marshal", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _MARSHAL = module
+    return _MARSHAL
+
+
+class _Entry:
+    """What a checked call needs again."""
+    __slots__ = ("dims", "address", "workspace_bytes", "device", "index", "factor", "extra")
+
+    def __init__(self, dims, workspace_bytes, device, factor=0.0, extra=None):
+        self.dims, self.address = dims, ctypes.addressof(dims)
+        self.workspace_bytes, self.device, self.index = workspace_bytes, device, device.index
+        self.factor, self.extra = factor, extra
+
+
+def _remember(key, entry):
+    if len(_CHECKED) >= 2048:
+        _CHECKED.clear()
+    _CHECKED[key] = entry
+    return entry
 
 
 # device that a launch would go to, without torch.cuda's own checks (a host-side cost per call)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call(dev, fn, *args):
-    """fn(*args, stream) on `dev` and its current stream; raises what the library refuses."""
-    if _current_device() == dev.index:
-        st = fn(*args, _stream(dev))
+def _call(which, e, factor, ws_len, *tensors):
+    """The entry point on the entry's device and its current stream; raises what the library refuses."""
+    if _current_device() == e.index:
+        st = _MARSHAL.call(which, e.address, _stream(e.device), factor, ws_len, *tensors)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(dev))
+        with torch.cuda.device(e.device):
+            st = _MARSHAL.call(which, e.address, _stream(e.device), factor, ws_len, *tensors)
     if st:
         _raise(st)
 
 
-def _delta_checked(q, k, v, g, beta, others, packed, n_seq, lead):
-    """Dims, their reference and workspace sizes (forward, backward) of a call on these tensors; raises for tensors that do not belong
-    together.  `others`: (tensor or None, name, shape function of (batch, Hv, dk, dv), dtype or None
-    for the io dtype)."""
-    key = (_meta(q), _meta(k), _meta(v), _meta(g), _meta(beta),
-           packed, n_seq, lead, *[_meta(t[0]) for t in others])
-    hit = _DELTA_CACHE.get(key)
-    if hit is not None:
-        return hit
+def _delta_check(q, k, v, g, beta, others, seq_offsets, lead, workspace_bytes):
+    """The entry of a call on these tensors; raises for tensors that do not belong together.  `others`:
+    (tensor or None, name, shape function of (states, *token axes), Hk, Hv, dk, dv, dtype or None for
+    the io dtype); lead: token axes of q; workspace_bytes: the library's query, or None."""
+    n_seq = _offsets_count(seq_offsets, q)
+    packed = n_seq is not None
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != lead + 2:
             raise ValueError(f"{name} must have {lead + 2} dimensions, it has shape "
                              f"{tuple(t.shape)}")
-        if t.device != q.device or t.dtype != q.dtype:
+        if t.device != q.device or t.dtype != q.dtype or t.layout != torch.strided:
             raise ValueError(f"{name} is {t.dtype} on {t.device}, q {q.dtype} on {q.device}")
     if q.device.type != "cuda":
         raise ValueError("tensors must be on a HIP device")
@@ -675,8 +703,10 @@ def _delta_checked(q, k, v, g, beta, others, packed, n_seq, lead):
                          "belong together")
     if Hk == 0 or Hv % Hk:
         raise ValueError(f"{Hv} value heads are no multiple of {Hk} key heads")
-    _check(g, "g", (*tokens, Hv), io, dev)
-    _check(beta, "beta", (*tokens, Hv), io, dev)
+    for t, name in ((g, "g"), (beta, "beta")):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _check(t, name, (*tokens, Hv), io, dev)
     vec = 8 if code == MAMBA_BF16 else 4
     if packed:
         batch, L = n_seq, tokens[0]
@@ -688,13 +718,8 @@ def _delta_checked(q, k, v, g, beta, others, packed, n_seq, lead):
         _check(t, name, shape((batch, *tokens), Hk, Hv, dk, dv), dt or io, dev)
     dm = mamba_delta_dims(batch, L, Hk, Hv, dk, dv, _token_stride(q, "q", vec),
                           _token_stride(k, "k", vec), _token_stride(v, "v", vec), code, 0)
-    ref = ctypes.byref(dm)
-    hit = (dm, ref, int(lib().mamba_delta_workspace_bytes(ref, int(packed))),
-           int(lib().mamba_delta_bwd_workspace_bytes(ref, int(packed))))
-    if len(_DELTA_CACHE) >= 1024:
-        _DELTA_CACHE.clear()
-    _DELTA_CACHE[key] = hit
-    return hit
+    need = 0 if workspace_bytes is None else int(workspace_bytes(ctypes.byref(dm), int(packed)))
+    return _Entry(dm, need, dev, dk ** -0.5 if dk else 0.0)
 
 
 def _state_shape(n, Hk, Hv, dk, dv):
@@ -733,23 +758,24 @@ def mamba_delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, seq_offset
     tokens seq_offsets[s] .. seq_offsets[s + 1] - 1, and there are n states.
     Returns out (batch, L, Hv, dv), or (out, last_state).
     """
-    n_seq = _offsets_count(seq_offsets, q)
-    packed = n_seq is not None
-    dm, ref, ws_bytes, _ = _delta_checked(
-        q, k, v, g, beta, ((initial_state, "initial_state", _state_shape, torch.float32),
-                           (out, "out", _out_shape, None),
-                           (last_state, "last_state", _state_shape, torch.float32)),
-        packed, n_seq, 1 if packed else 2)
-    dev = q.device
+    m = _MARSHAL or _marshal()
+    key = m.key(_DELTA_FWD, q, k, v, g, beta, initial_state, seq_offsets, out, last_state)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _delta_check(
+            q, k, v, g, beta, ((initial_state, "initial_state", _state_shape, torch.float32),
+                               (out, "out", _out_shape, None),
+                               (last_state, "last_state", _state_shape, torch.float32)),
+            seq_offsets, 2 if seq_offsets is None else 1, lib().mamba_delta_workspace_bytes))
     if out is None:
         out = q.new_empty(v.shape)
     if return_last_state and last_state is None:
+        dm = e.dims
         last_state = torch.empty((dm.batch, dm.v_heads, dm.dk, dm.dv), dtype=torch.float32,
-                                 device=dev)
-    workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
-    _call(dev, lib().mamba_delta_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-          _ptr(initial_state), _ptr(seq_offsets), dm.dk ** -0.5 if scale is None else scale,
-          _ptr(out), _ptr(last_state), ref, _ptr(workspace), ws_len)
+                                 device=e.device)
+    workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
+    _call(_DELTA_FWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, beta,
+          initial_state, seq_offsets, out, last_state, workspace)
     return (out, last_state) if return_last_state else out
 
 
@@ -759,15 +785,18 @@ def mamba_delta_update(state, q, k, v, g, beta, scale=None, out=None):
     state: (batch, Hv, dk, dv) float32, updated in place; q, k: (batch, Hk, dk); v: (batch, Hv, dv);
     g, beta: (batch, Hv).  Returns out (batch, Hv, dv).
     """
-    if state is None:
-        raise ValueError("state is required")
-    dm, ref, _, _ = _delta_checked(q, k, v, g, beta, ((state, "state", _state_shape, torch.float32),
-                                                      (out, "out", _out_shape, None)), False, None, 1)
+    m = _MARSHAL or _marshal()
+    key = m.key(_DELTA_UPDATE, state, q, k, v, g, beta, out)
+    e = _CHECKED.get(key)
+    if e is None:
+        if state is None:
+            raise ValueError("state is required")
+        e = _remember(key, _delta_check(q, k, v, g, beta,
+                                        ((state, "state", _state_shape, torch.float32),
+                                         (out, "out", _out_shape, None)), None, 1, None))
     if out is None:
         out = q.new_empty(v.shape)
-    _call(q.device, lib().mamba_delta_update, state.data_ptr(), q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), g.data_ptr(), beta.data_ptr(), dm.dk ** -0.5 if scale is None else scale,
-          out.data_ptr(), ref)
+    _call(_DELTA_UPDATE, e, e.factor if scale is None else scale, 0, state, q, k, v, g, beta, out)
     return out
 
 
@@ -783,6 +812,9 @@ def mamba_delta_bwd_workspace_bytes(dims: mamba_delta_dims, packed=False) -> int
     return int(lib().mamba_delta_bwd_workspace_bytes(ctypes.byref(dims), int(bool(packed))))
 
 
+_DELTA_GRADS = ("dq", "dk", "dv", "dg", "dbeta", "dinitial_state")
+
+
 def mamba_delta_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, seq_offsets=None,
                     dlast=None, workspace=None, grads=None):
     """Gradients of mamba_delta_fwd (mamba_delta_bwd in include/mamba_scan.h).
@@ -794,30 +826,28 @@ def mamba_delta_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, seq_
     """
     if dout is None:
         raise ValueError("dout is required")
-    n_seq = _offsets_count(seq_offsets, q)
-    packed = n_seq is not None
     gr = dict(grads or {})
-    spec = (("dq", _qk_shape, None), ("dk", _qk_shape, None), ("dv", _out_shape, None),
-            ("dg", _head_shape, None), ("dbeta", _head_shape, None),
-            ("dinitial_state", _state_shape, torch.float32))
-    dm, ref, _, ws_bytes = _delta_checked(
-        q, k, v, g, beta,
-        ((initial_state, "initial_state", _state_shape, torch.float32), (dout, "dout", _out_shape, None),
-         (dlast, "dlast", _state_shape, torch.float32),
-         *((gr.get(name), name, shape, dt) for name, shape, dt in spec)),
-        packed, n_seq, 1 if packed else 2)
-    dev = q.device
-    for name, like in (("dq", q), ("dk", q), ("dv", v), ("dg", g), ("dbeta", g),
-                       ("dinitial_state", initial_state)):
+    given = [gr.get(name) for name in _DELTA_GRADS]
+    m = _MARSHAL or _marshal()
+    key = m.key(_DELTA_BWD, q, k, v, g, beta, initial_state, seq_offsets, dout, dlast, *given)
+    e = _CHECKED.get(key)
+    if e is None:
+        spec = (_qk_shape, _qk_shape, _out_shape, _head_shape, _head_shape, _state_shape)
+        e = _remember(key, _delta_check(
+            q, k, v, g, beta,
+            ((initial_state, "initial_state", _state_shape, torch.float32),
+             (dout, "dout", _out_shape, None), (dlast, "dlast", _state_shape, torch.float32),
+             *((t, name, shape, torch.float32 if name == "dinitial_state" else None)
+               for t, name, shape in zip(given, _DELTA_GRADS, spec))),
+            seq_offsets, 2 if seq_offsets is None else 1, lib().mamba_delta_bwd_workspace_bytes))
+    for name, like in zip(_DELTA_GRADS, (q, q, v, g, beta, initial_state)):
         if gr.get(name) is None:
-            gr[name] = None if like is None else torch.empty(like.shape, dtype=like.dtype,
-                                                             device=dev)
-    workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
-    _call(dev, lib().mamba_delta_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-          _ptr(initial_state), _ptr(seq_offsets), dm.dk ** -0.5 if scale is None else scale,
-          _ptr(dout), _ptr(dlast), _ptr(gr["dq"]), _ptr(gr["dk"]), _ptr(gr["dv"]), _ptr(gr["dg"]),
-          _ptr(gr["dbeta"]), _ptr(gr["dinitial_state"]), ref, _ptr(workspace), ws_len)
-    return {n: gr[n] for n in ("dq", "dk", "dv", "dg", "dbeta", "dinitial_state")}
+            gr[name] = None if like is None else like.new_empty(like.shape)
+    workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
+    res = {name: gr[name] for name in _DELTA_GRADS}
+    _call(_DELTA_BWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, beta,
+          initial_state, seq_offsets, dout, dlast, *res.values(), workspace)
+    return res
 
 
 # ---------------------------------------------------------------------------- norms of a block
@@ -831,19 +861,12 @@ def _row_stride(t, name):
     return stride
 
 
-_NORM_CACHE = {}
-
-
-def _gated_checked(y, z, weight, gate_first, others):
-    """Dims (by reference) and workspace size of a gated norm; `others`: (tensor or None, name, "rows"|"weight")."""
-    key = (_meta(y), _meta(z), _meta(weight), gate_first, *[_meta(t[0]) for t in others])
-    hit = _NORM_CACHE.get(key)
-    if hit is not None:
-        return hit
+def _gated_check(y, z, weight, gate_first, others):
+    """The entry of a gated norm; `others`: (tensor or None, name, "rows" or "weight")."""
     for t, name in ((y, "y"), (weight, "weight")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-    if y.dim() != 3 or y.device.type != "cuda":
+    if y.dim() != 3 or y.device.type != "cuda" or y.layout != torch.strided:
         raise ValueError("y must be (rows, groups, dim) on a HIP device")
     rows, G, d = y.shape
     io, dev = y.dtype, y.device
@@ -851,7 +874,7 @@ def _gated_checked(y, z, weight, gate_first, others):
     if z is not None:
         if not isinstance(z, torch.Tensor):
             raise TypeError("z must be a torch.Tensor")
-        if z.shape != y.shape or z.dtype != io or z.device != dev:
+        if z.shape != y.shape or z.dtype != io or z.device != dev or z.layout != torch.strided:
             raise ValueError(f"z must be like y, {tuple(y.shape)} {io} on {dev}")
     per_group = weight.dim() == 2
     wshape = (G, d) if per_group else (d,)
@@ -864,12 +887,7 @@ def _gated_checked(y, z, weight, gate_first, others):
     dm = mamba_gated_norm_dims(rows, G, d, _row_stride(y, "y"),
                                0 if z is None else _row_stride(z, "z"), code,
                                G if per_group else 1, int(bool(gate_first)), 0)
-    ref = ctypes.byref(dm)
-    hit = (ref, int(lib().mamba_gated_norm_bwd_workspace_bytes(ref)))
-    if len(_NORM_CACHE) >= 1024:
-        _NORM_CACHE.clear()
-    _NORM_CACHE[key] = hit
-    return hit
+    return _Entry(dm, mamba_gated_norm_bwd_workspace_bytes(dm), dev)
 
 
 def mamba_gated_norm_bwd_workspace_bytes(dims: mamba_gated_norm_dims) -> int:
@@ -883,11 +901,14 @@ def mamba_gated_norm_fwd(y, z, weight, eps=1e-5, gate_first=False, out=None):
     (dim,) or (groups, dim) float32.  norm(y) * weight * silu(z), or norm(y * silu(z)) * weight with
     gate_first.  Returns out (rows, groups, dim).
     """
-    ref, _ = _gated_checked(y, z, weight, gate_first, ((out, "out", "rows"),))
+    m = _MARSHAL or _marshal()
+    key = m.key(_GATED_FWD, y, z, weight, bool(gate_first), out)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _gated_check(y, z, weight, gate_first, ((out, "out", "rows"),)))
     if out is None:
         out = y.new_empty(y.shape)
-    _call(y.device, lib().mamba_gated_norm_fwd, y.data_ptr(), _ptr(z), weight.data_ptr(), eps,
-          out.data_ptr(), ref)
+    _call(_GATED_FWD, e, eps, 0, y, z, weight, out)
     return out
 
 
@@ -898,33 +919,32 @@ def mamba_gated_norm_bwd(y, z, weight, dout, eps=1e-5, gate_first=False, workspa
     if dout is None:
         raise ValueError("dout is required")
     g = dict(grads or {})
-    ref, ws_bytes = _gated_checked(y, z, weight, gate_first,
-                                   ((dout, "dout", "rows"), (g.get("dy"), "dy", "rows"),
-                                    (g.get("dz"), "dz", "rows"),
-                                    (g.get("dweight"), "dweight", "weight")))
-    dev = y.device
-    if g.get("dy") is None:
-        g["dy"] = torch.empty(y.shape, dtype=y.dtype, device=dev)
+    given = [g.get(name) for name in ("dy", "dz", "dweight")]
+    m = _MARSHAL or _marshal()
+    key = m.key(_GATED_BWD, y, z, weight, bool(gate_first), dout, *given)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _gated_check(y, z, weight, gate_first,
+                                        ((dout, "dout", "rows"), (given[0], "dy", "rows"),
+                                         (given[1], "dz", "rows"),
+                                         (given[2], "dweight", "weight"))))
+    dy, dz, dw = given
+    if dy is None:
+        dy = y.new_empty(y.shape)
     if z is None:
-        g["dz"] = None
-    elif g.get("dz") is None:
-        g["dz"] = torch.empty(y.shape, dtype=y.dtype, device=dev)
-    if g.get("dweight") is None:
-        g["dweight"] = torch.empty(weight.shape, dtype=torch.float32, device=dev)
-    workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
-    _call(dev, lib().mamba_gated_norm_bwd, _ptr(y), _ptr(z), _ptr(weight), eps, _ptr(dout),
-          _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dweight"]), ref, _ptr(workspace), ws_len)
-    return {n: g[n] for n in ("dy", "dz", "dweight")}
+        dz = None
+    elif dz is None:
+        dz = y.new_empty(y.shape)
+    if dw is None:
+        dw = weight.new_empty(weight.shape)
+    workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
+    _call(_GATED_BWD, e, eps, ws_len, y, z, weight, dout, dy, dz, dw, workspace)
+    return {"dy": dy, "dz": dz, "dweight": dw}
 
 
-def _add_checked(x, residual, vectors, others):
-    """Dims (by reference), workspace size and residual type of an add norm.  `vectors`: (tensor or None, name) of (dim,) float32;
-    `others`: (tensor or None, name, is of the residual's type)."""
-    key = (_meta(x), _meta(residual), *[_meta(t[0]) for t in vectors], None,
-           *[_meta(t[0]) for t in others])
-    hit = _NORM_CACHE.get(key)
-    if hit is not None:
-        return hit
+def _add_check(x, residual, vectors, others):
+    """The entry of an add norm (extra: the residual's type).  `vectors`: (tensor or None, name) of
+    (dim,) float32; `others`: (tensor or None, name, is of the residual's type)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() != 2 or x.device.type != "cuda":
@@ -934,7 +954,8 @@ def _add_checked(x, residual, vectors, others):
     code = _io_code(io)
     _check(x, "x", (rows, d), io, dev)
     # the stream's type is the residual's, or that of the first of its companions
-    res = next((t.dtype for t, _, r in ((residual, "", True), *others) if r and t is not None), io)
+    res = next((t.dtype for t, _, r in ((residual, "", True), *others)
+                if r and isinstance(t, torch.Tensor)), io)
     res_code = _io_code(res)
     _check(residual, "residual", (rows, d), res, dev)
     if vectors[0][0] is None:
@@ -944,12 +965,7 @@ def _add_checked(x, residual, vectors, others):
     for t, name, of_res in others:
         _check(t, name, (rows, d), res if of_res else io, dev)
     dm = mamba_add_norm_dims(rows, d, code, res_code)
-    ref = ctypes.byref(dm)
-    hit = (ref, int(lib().mamba_add_norm_bwd_workspace_bytes(ref)), res)
-    if len(_NORM_CACHE) >= 1024:
-        _NORM_CACHE.clear()
-    _NORM_CACHE[key] = hit
-    return hit
+    return _Entry(dm, mamba_add_norm_bwd_workspace_bytes(dm), dev, extra=res)
 
 
 def mamba_add_norm_bwd_workspace_bytes(dims: mamba_add_norm_dims) -> int:
@@ -965,17 +981,23 @@ def mamba_add_norm_fwd(x, residual, weight, scale=None, post_weight=None, eps=1e
     weight, scale, post_weight: (dim,) float32.  Returns (out, r), r of the residual's type (of x's
     without one, or of residual_out's).
     """
-    ref, _, res = _add_checked(x, residual, ((weight, "weight"), (scale, "scale"),
-                                             (post_weight, "post_weight")),
-                               ((out, "out", False), (residual_out, "residual_out", True)))
+    m = _MARSHAL or _marshal()
+    key = m.key(_ADD_FWD, x, residual, weight, scale, post_weight, out, residual_out)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _add_check(x, residual, ((weight, "weight"), (scale, "scale"),
+                                                    (post_weight, "post_weight")),
+                                      ((out, "out", False),
+                                       (residual_out, "residual_out", True))))
     if out is None:
         out = x.new_empty(x.shape)
     if residual_out is None:
-        residual_out = (residual.new_empty(x.shape) if residual is not None
-                        else x.new_empty(x.shape))
-    _call(x.device, lib().mamba_add_norm_fwd, x.data_ptr(), _ptr(residual), weight.data_ptr(),
-          _ptr(scale), _ptr(post_weight), eps, out.data_ptr(), residual_out.data_ptr(), ref)
+        residual_out = (x if residual is None else residual).new_empty(x.shape)
+    _call(_ADD_FWD, e, eps, 0, x, residual, weight, scale, post_weight, out, residual_out)
     return out, residual_out
+
+
+_ADD_GRADS = ("dx", "dresidual", "dweight", "dscale", "dpost_weight")
 
 
 def mamba_add_norm_bwd(x, residual, weight, dout, dresidual_out=None, scale=None, post_weight=None,
@@ -987,23 +1009,23 @@ def mamba_add_norm_bwd(x, residual, weight, dout, dresidual_out=None, scale=None
     if dout is None:
         raise ValueError("dout is required")
     g = dict(grads or {})
-    ref, ws_bytes, res = _add_checked(
-        x, residual, ((weight, "weight"), (scale, "scale"), (post_weight, "post_weight"),
-                      (g.get("dweight"), "dweight"), (g.get("dscale"), "dscale"),
-                      (g.get("dpost_weight"), "dpost_weight")),
-        ((dout, "dout", False), (dresidual_out, "dresidual_out", True),
-         (g.get("dx"), "dx", False), (g.get("dresidual"), "dresidual", True)))
-    dev = x.device
-    for name, like, dt in (("dx", x, x.dtype), ("dresidual", residual, res),
-                           ("dweight", weight, torch.float32), ("dscale", scale, torch.float32),
-                           ("dpost_weight", post_weight, torch.float32)):
+    given = [g.get(name) for name in _ADD_GRADS]
+    m = _MARSHAL or _marshal()
+    key = m.key(_ADD_BWD, x, residual, weight, scale, post_weight, dout, dresidual_out, *given)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _add_check(
+            x, residual, ((weight, "weight"), (scale, "scale"), (post_weight, "post_weight"),
+                          *zip(given[2:], _ADD_GRADS[2:])),
+            ((dout, "dout", False), (dresidual_out, "dresidual_out", True),
+             (given[0], "dx", False), (given[1], "dresidual", True))))
+    for name, like in zip(_ADD_GRADS, (x, residual, weight, scale, post_weight)):
         if like is None:
             g[name] = None
         elif g.get(name) is None:
-            g[name] = torch.empty(like.shape, dtype=dt, device=dev)
-    workspace, ws_len = _workspace(workspace, ws_bytes, dev, min_bytes=1)
-    _call(dev, lib().mamba_add_norm_bwd, _ptr(x), _ptr(residual), _ptr(weight), _ptr(scale),
-          _ptr(post_weight), eps, _ptr(dout), _ptr(dresidual_out), _ptr(g["dx"]),
-          _ptr(g["dresidual"]), _ptr(g["dweight"]), _ptr(g["dscale"]), _ptr(g["dpost_weight"]), ref,
-          _ptr(workspace), ws_len)
-    return {n: g[n] for n in ("dx", "dresidual", "dweight", "dscale", "dpost_weight")}
+            g[name] = like.new_empty(like.shape)
+    workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
+    res = {name: g[name] for name in _ADD_GRADS}
+    _call(_ADD_BWD, e, eps, ws_len, x, residual, weight, scale, post_weight, dout, dresidual_out,
+          *res.values(), workspace)
+    return res
