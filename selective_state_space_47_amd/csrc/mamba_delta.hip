@@ -123,18 +123,20 @@ __global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kern
   }
 
   const int i = 16 * w + r;  // this lane's token
-  for (int h = 0; h < a.rep; ++h) {
+  // value heads blockIdx.y, blockIdx.y + gridDim.y, ... of the key head
+  const int step = gridDim.y;
+  for (int h = blockIdx.y, turn = 0; h < a.rep; h += step, ++turn) {
     const int vh = kh * a.rep + h;
     char* ws = a.ws + (slot * a.hv + vh) * a.ws_item;
     __syncthreads();  // the tiles of the previous head (or K and Q) have been read
-    const int hs = h & 3;
-    if (hs == 0 && h + w < a.rep) {
-      // Wave w: prefix sums of head h + w's log decays in fp64, kept as two floats: a difference of two
+    const int hs = turn & 3;
+    if (hs == 0 && h + w * step < a.rep) {
+      // Wave w: prefix sums of the w-th next head's log decays in fp64, kept as two floats: a difference of two
       // of them is then as exact as its own size, whatever came before in the chunk.  Below -200 exp is
       // 0 in fp32; the clamp keeps -inf (a reset) out of the differences and lets NaN through.
       float gl = 0.f, bt = 0.f;
       if (lane < n) {
-        const int64_t at = (t0 + lane) * a.hv + vh + w;
+        const int64_t at = (t0 + lane) * a.hv + vh + w * step;
         gl = ld_f32(static_cast<const E*>(a.g), at);
         bt = ld_f32(static_cast<const E*>(a.beta), at);
         gl = gl < -200.f ? -200.f : gl;
@@ -145,11 +147,11 @@ __global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kern
       sm.ghi[w][lane] = hi;
       sm.glo[w][lane] = lo;
       sm.beta[w][lane] = bt;
-      float* gate = reinterpret_cast<float*>(ws + w * a.ws_item + ChunkWs<E>::kGate);
+      float* gate = reinterpret_cast<float*>(ws + w * step * a.ws_item + ChunkWs<E>::kGate);
       gate[lane] = exp_f32(hi);
       gate[kC + lane] = exp_f32((float)(total - G)) * bt;
       if (lane == 0) gate[2 * kC] = exp_f32((float)total);
-      float* decay = reinterpret_cast<float*>(ws + w * a.ws_item + ChunkWs<E>::kDecay);
+      float* decay = reinterpret_cast<float*>(ws + w * step * a.ws_item + ChunkWs<E>::kDecay);
       decay[lane] = hi;
       decay[kC + lane] = lo;
       decay[2 * kC + lane] = bt;
@@ -743,7 +745,10 @@ int launch_step(const StepArgs& a, int64_t heads, hipStream_t s) {
 
 template <typename E, int DK>
 int launch_chunks_t(const Args& a, hipStream_t s) {
-  hipLaunchKernelGGL((chunk_kernel<E, DK>), dim3((unsigned)(a.slots * a.hk)), dim3(256), 0, s, a);
+  // value heads of a key head one after another share K K^T and Q K^T; where that leaves CUs idle, each
+  // has a workgroup of its own
+  const unsigned split = a.slots * a.hk * a.rep <= 512 ? (unsigned)a.rep : 1;
+  hipLaunchKernelGGL((chunk_kernel<E, DK>), dim3((unsigned)(a.slots * a.hk), split), dim3(256), 0, s, a);
   return launch_status();
 }
 
