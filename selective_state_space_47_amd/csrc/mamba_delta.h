@@ -113,18 +113,27 @@ __device__ __forceinline__ bf16x4 lds_tr(lds_ptr p) {
   return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
 }
 
+// Swizzle of the 16-byte words of LDS rows.  One pass of a 16-byte read serves 8 lanes of one group and 8
+// of the next: rows 0-3 and 12-15 of group g with rows 4-11 of group g + 1, or the other way round (counted:
+// with the plain row number / 4 in place of this code an operand read took two passes more).  The two sets
+// of rows get codes that never differ by 1, as their words do.
+__device__ __forceinline__ int row_code(int t) {
+  const int q = (t >> 2) & 3;  // 0 2 3 1
+  return 2 * ((q ^ (q >> 1)) & 1) + (q >> 1);
+}
+
 // A 64-token tile of keys or queries in LDS: rows of kRow bytes, the 16-byte word w of row t kept at
-// w ^ key(t).  With this key the 16 rows of an operand read, and the 4 rows x 4 words of a transposing
-// read (of rows of 8 or more words), lie in different banks.
+// w ^ key(t).  With this key the rows of one pass of an operand read, and the 4 rows x 4 words of a
+// transposing read (of rows of 8 or more words), lie in different banks.
 template <typename E, int DK>
 struct KeyTile {
   static constexpr int kRow = DK * (int)sizeof(E);
   static constexpr int kWords = kRow / 16;
   static constexpr int kBytes = kC * kRow;
   __device__ static __forceinline__ int key(int t) {
-    return kWords >= 16  ? 4 * (t & 3) + ((t >> 2) & 3)
-           : kWords == 8 ? 4 * ((t >> 1) & 1) + ((t >> 2) & 3)
-                         : (t >> 2) & 3;
+    return kWords >= 16  ? 4 * (t & 3) + row_code(t)
+           : kWords == 8 ? 4 * ((t >> 1) & 1) + row_code(t)
+                         : row_code(t);
   }
   // lane addresses of one tile
   int row0, tr0, g, r;
@@ -166,20 +175,23 @@ struct KeyTile {
   }
 };
 
-// Rows of kCols values as they lie (values, output gradients: read in accumulator order, column by
-// column).
+// Rows of kCols values (values, output gradients), read in accumulator order, column by column.  Words are
+// swizzled in pairs (bf16; fp32: in fours), a wave's 16 columns, so that the rows of one read lie in
+// different banks.
 template <typename E, int kCols>
 struct ValueTile {
   static constexpr int kRow = kCols * (int)sizeof(E);
   static constexpr int kWords = kRow / 16;
   static constexpr int kBytes = kC * kRow;
-  __device__ static __forceinline__ int key(int) { return 0; }
+  __device__ static __forceinline__ int key(int t) {
+    return sizeof(E) == 4 ? 4 * ((t >> 2) & 3) : kWords >= 16 ? 2 * (t & 7) : 2 * ((t >> 1) & 3);
+  }
   int at, g;
   // this wave's 16 columns begin at `col`
   __device__ __forceinline__ ValueTile(int lane, int col) : g(lane >> 4) {
-    const int r = lane & 15;
-    at = sizeof(E) == 2 ? (4 * g + (r >> 2)) * kRow + 2 * col + 8 * (r & 3)
-                        : 4 * g * kRow + (col + r) * 4;
+    const int r = lane & 15, t = sizeof(E) == 2 ? 4 * g + (r >> 2) : 4 * g;
+    const int byte = sizeof(E) == 2 ? 2 * col + 8 * (r & 3) : (col + r) * 4;
+    at = t * kRow + (((byte >> 4) ^ key(t)) << 4) + (byte & 15);
   }
   // rows (tokens) 16 m + 4 g .. +3 of column r, in storage type
   __device__ __forceinline__ auto four(lds_ptr t, int m) const {
@@ -204,7 +216,7 @@ struct ValueTile {
 
 // Lower triangular 64 x 64 matrix in LDS and in the workspace: blocks of kDepth columns, block kb
 // holding rows kDepth kb .. 63 of 64 bytes each, four words; word w of a row holds the values that
-// lane group w reads in accumulator order and is kept at w ^ (row / 4 % 4) (bank conflicts as above).
+// lane group w reads in accumulator order and is kept at w ^ row_code(row).
 template <typename E>
 struct TriTile {
   static constexpr int kD = Mma<E>::kDepth;
@@ -216,11 +228,11 @@ struct TriTile {
   static constexpr int kBytes = kRows * 64;
   // byte of word w of row t, block kb
   __device__ static __forceinline__ int word_at(int kb, int t, int w) {
-    return row_at(kb, t) + ((w ^ ((t >> 2) & 3)) << 4);
+    return row_at(kb, t) + ((w ^ row_code(t)) << 4);
   }
   int row0, g, r;
   __device__ __forceinline__ TriTile(int lane) : g(lane >> 4), r(lane & 15) {
-    row0 = r * 64 + ((g ^ (r >> 2)) << 4);
+    row0 = r * 64 + ((g ^ row_code(r)) << 4);
   }
   // operand with rows 16 m + r, k = columns of block kb
   __device__ __forceinline__ typename Mma<E>::Frag rows(lds_ptr t, int m, int kb) const {
@@ -230,10 +242,11 @@ struct TriTile {
   // in accumulator order
   __device__ __forceinline__ typename Mma<E>::Frag cols(lds_ptr t, int m, int ib) const {
     if constexpr (sizeof(E) == 2) {
-      t += row_at(m >> 1, 32 * ib) + (4 * g + (r >> 2)) * 64 + (((r & 3) ^ g) << 4) + 8 * (m & 1);
+      t += row_at(m >> 1, 32 * ib) + (4 * g + (r >> 2)) * 64 + (((r & 3) ^ row_code(4 * g)) << 4) +
+           8 * (m & 1);
       return Mma<E>::join(lds_tr(t), lds_tr(t + 16 * 64));
     } else {
-      t += row_at(m, 16 * ib) + 4 * g * 64 + (((r >> 2) ^ g) << 4) + 4 * (r & 3);
+      t += row_at(m, 16 * ib) + 4 * g * 64 + (((r >> 2) ^ row_code(4 * g)) << 4) + 4 * (r & 3);
       return typename Mma<E>::Frag{lds_read<float>(t), lds_read<float>(t + 64),
                                    lds_read<float>(t + 128), lds_read<float>(t + 192)};
     }
