@@ -14,8 +14,9 @@
 //
 // Rounding (bf16 storage): products take bf16 operands into fp32 accumulators.  What makes E and enters the
 // state by K^T E goes in as three bf16 parts (Y and c E: the fp32 value to 24 bits) or two (S, and T, which
-// is one on its diagonal and small off it): the state is within about 3e-7 of fp64.  The output takes S and
-// E as two parts and P as one, whose rounding is that of the output again.  fp32 storage uses fp32 matrix
+// is one on its diagonal and small off it): the state is within about 3e-7 of fp64.  The output takes E as
+// two parts, S and P as one: each rounds its own share of the output, so that together they weigh at most as
+// much as the output's own rounding.  fp32 storage uses fp32 matrix
 // instructions throughout.
 #include <cmath>
 
@@ -415,9 +416,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
         for (int m = 0; m < 4; ++m) y[m] = M::mma(kf[m], s.p[p], y[m]);
       if constexpr (kO) {
 #pragma unroll
-        for (int p = 0; p < kPS; ++p)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) o[m] = M::mma(s.p[p], qf[m], o[m]);
+        for (int m = 0; m < 4; ++m) o[m] = M::mma(s.p[0], qf[m], o[m]);
       }
     }
     // Y = V - diag(exp G) K S;  O scaled by its token's factor
