@@ -13,6 +13,8 @@
 //     S' = exp(G_64) S + K^T diag(c) E,   c_j = exp(G_64 - G_j) beta_j
 // T and P do not depend on the state: one launch makes them for all chunks.
 #pragma once
+#include <cmath>
+
 #include "mamba_common.h"
 
 namespace mamba {
@@ -403,6 +405,21 @@ __device__ __forceinline__ int64_t slot_seq(const Args& a, int64_t slot, int64_t
   return lo;
 }
 
+// The sequence of a workgroup of the state passes: packed sequences (up to a wave's lanes of them) the longest
+// first, so that none starts late and runs on alone.
+__device__ __forceinline__ int64_t seq_by_length(const Args& a, int64_t rank) {
+  if (!a.offsets || a.nseq < 2 || a.nseq > 64) return rank;
+  const int lane = threadIdx.x & 63, n = (int)a.nseq;
+  const int len = lane < n ? (int)min(seq_span(a, lane).len, (int64_t)0x7fffffff) : -1;
+  int before = 0;  // sequences that come before this lane's
+  for (int j = 0; j < n; ++j) {
+    const int other = __shfl(len, j);
+    before += other > len || (other == len && j < lane);
+  }
+  const uint64_t found = __ballot(lane < n && before == (int)rank);
+  return __builtin_amdgcn_readfirstlane(__builtin_ctzll(found));
+}
+
 // Workgroups in groups of `group` that read the same keys: a group stays on one XCD (one L2), and
 // consecutive groups, which are heads of one sequence and so equally long, go to different XCDs.
 // (Workgroup id runs on XCD id % 8.)  A bijection of [0, n), n a multiple of `group`.
@@ -436,6 +453,20 @@ inline int64_t slots_of(const mamba_delta_dims* d, bool packed, int64_t unit) {
   return packed ? d->seqlen / unit + d->batch : d->batch * ((d->seqlen + unit - 1) / unit);
 }
 inline int64_t chunk_slots(const mamba_delta_dims* d, bool packed) { return slots_of(d, packed, kC); }
+
+// Whether a state pass takes workgroups of 64 columns (4 waves) instead of 128 (8 waves); `runs` sequences or segments
+// per head, equally long (`even`) or not.  One workgroup runs on a CU at a time and goes through its chunks one
+// after another: 128 columns share a chunk's tiles better (4.9 us a chunk with all CUs busy, dk = 128, bf16),
+// 64 are through sooner (3.4 us) and leave less idle at the end.
+inline bool narrow_pass(int64_t heads, int64_t runs, bool even, int64_t dv) {
+  if (dv <= 64) return true;
+  const double n = (double)heads * (double)runs, wide = n * (double)((dv + 127) / 128) / 256.0,
+               slim = n * (double)((dv + 63) / 64) / 256.0;
+  // lengths that differ: the longest, taken as twice the mean, or all of them spread over the CUs
+  const double tw = even ? std::ceil(wide) : std::max(2.0, wide);
+  const double ts = even ? std::ceil(slim) : std::max(2.0, slim);
+  return ts * 3.4 < tw * 4.9;
+}
 inline size_t chunk_ws_bytes(const mamba_delta_dims* d) {
   return d->io_dtype == MAMBA_BF16 ? ChunkWs<uint16_t>::kBytes : ChunkWs<float>::kBytes;
 }

@@ -18,8 +18,6 @@
 // two parts, S and P as one: each rounds its own share of the output, so that together they weigh at most as
 // much as the output's own rounding.  fp32 storage uses fp32 matrix
 // instructions throughout.
-#include <cmath>
-
 #include "mamba_delta.h"
 
 namespace mamba {
@@ -305,7 +303,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_block
   const int64_t seg_slot = sh / a.hv;
   const int vh = (int)(sh - seg_slot * a.hv), kh = vh / a.rep;
   const int64_t unit = a.seg_chunks * kC;
-  const int64_t seq = a.seg_chunks ? slot_seq(a, seg_slot, unit) : seg_slot;
+  const int64_t seq = a.seg_chunks ? slot_seq(a, seg_slot, unit) : seq_by_length(a, seg_slot);
   const Span sp = seq_span(a, seq);
   const int64_t seg = a.seg_chunks ? seg_slot - slot_base(a, seq, sp.first, unit) : 0;
   const int64_t nchunks = (sp.len + kC - 1) / kC;
@@ -751,12 +749,6 @@ int launch_chunks_t(const Args& a, hipStream_t s) {
   return launch_status();
 }
 
-// Columns of the state per workgroup.  128 (8 waves) share a chunk's tiles best; where workgroups of 64
-// (4 waves) leave CUs idle as well, they finish sooner: 3.4 against 4.4 us a chunk (12 heads, dk = 128).
-int scan_columns(int64_t segments, int64_t dv) {
-  return dv <= 64 || segments * ((dv + 63) / 64) <= 256 ? 64 : 128;
-}
-
 template <typename E, int DK, int NW, Pass kPass>
 int launch_scan_t(const Args& a, hipStream_t s) {
   const int cols = (a.dv + 16 * NW - 1) / (16 * NW) +
@@ -768,7 +760,8 @@ int launch_scan_t(const Args& a, hipStream_t s) {
 
 template <typename E, Pass kPass>
 int launch_scan(const Args& a, hipStream_t s) {
-  const bool narrow = scan_columns(a.seg_slots * a.hv, a.dv) == 64;
+  const bool even = !a.offsets || a.nseq == 1;
+  const bool narrow = narrow_pass(a.hv, a.seg_slots, even, a.dv);
   if (a.dk <= 64)
     return narrow ? launch_scan_t<E, 64, 4, kPass>(a, s) : launch_scan_t<E, 64, 8, kPass>(a, s);
   return narrow ? launch_scan_t<E, 128, 4, kPass>(a, s) : launch_scan_t<E, 128, 8, kPass>(a, s);
@@ -792,7 +785,7 @@ int launch_forward(const Args& a, hipStream_t s) {
 }
 
 // Chunks per segment, 0 for whole sequences.  A pass costs one unit per chunk and round of 256
-// workgroups (one per CU); segments add a summary pass over their own and the map's columns, about 0.8
+// workgroups (one per CU); segments add a summary pass over their own and the map's columns, about 0.65
 // of a unit per chunk, and a quarter of a unit per segment to join them.  Packed sequences are taken to
 // be up to twice as long as their mean.  Segments are used where that model gains a quarter.
 // Measured, 65536 tokens x 12 heads of 128, bf16: PENDING.
@@ -807,11 +800,11 @@ int64_t plan_segments(const mamba_delta_dims* d, bool packed) {
   const double whole = std::ceil(heads * vb / kCUs) * chunks;
   double best = 0.75 * whole;
   int64_t pick = 0;
-  for (int64_t c = 8; c <= 256; c += 4) {
+  for (int64_t c = 8; c <= 256; ++c) {
     const double n = std::ceil(chunks / (double)c);
     if (n < 2) break;
     if ((n + 1) * heads * (vb + kb) > 2147483647.0) continue;  // one grid
-    const double t = std::ceil((n - 1) * heads * (vb + kb) / kCUs) * (double)c * 0.8 +
+    const double t = std::ceil((n - 1) * heads * (vb + kb) / kCUs) * (double)c * 0.65 +
                      std::ceil(n * heads * vb / kCUs) * (double)c + 0.25 * n + 4.0;
     if (t < best) {
       best = t;

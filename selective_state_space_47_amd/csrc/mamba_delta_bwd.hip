@@ -91,8 +91,8 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t wg = spread_index(blockIdx.x, gridDim.x, a.rep * col_blocks);
   const int64_t sh = wg / col_blocks;
-  const int64_t seq = sh / a.hv;
-  const int vh = (int)(sh - seq * a.hv), kh = vh / a.rep;
+  const int64_t rank = sh / a.hv, seq = seq_by_length(a, rank);
+  const int vh = (int)(sh - rank * a.hv), kh = vh / a.rep;
   const int col0 = (int)(wg - sh * col_blocks) * 16 * NW;
   const int col = col0 + 16 * w;
   const Span sp = seq_span(a, seq);
@@ -672,7 +672,8 @@ template <typename E, int DK>
 int launch_bwd(const BwdArgs& b, hipStream_t s) {
   // 64 or 128 columns per workgroup as in the forward (8 waves of fp32 operands would not fit the
   // registers)
-  const bool narrow = b.f.dv <= 64 || sizeof(E) == 4 || b.f.nseq * b.f.hv * ((b.f.dv + 63) / 64) <= 256;
+  const bool narrow = sizeof(E) == 4 ||
+                      narrow_pass(b.f.hv, b.f.nseq, !b.f.offsets || b.f.nseq == 1, b.f.dv);
   const int st = narrow ? launch_adjoint_t<E, DK, 4>(b, s)
                         : launch_adjoint_t<E, DK, sizeof(E) == 2 ? 8 : 4>(b, s);
   if (st != MAMBA_OK) return st;
