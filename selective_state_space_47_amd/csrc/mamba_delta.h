@@ -358,8 +358,9 @@ struct Args {
   int64_t ws_item;
   char* e_img;             // backward only, per (chunk slot, value head): images of E,
   char* s_img;             // of the state before the chunk
-  char* ds_img;            // and of the adjoint of the state after it;
-  char* s_low;             // what bf16 leaves of that state, a byte per value (bf16 storage)
+  char* s_low;             // (bf16 storage: and what bf16 leaves of it, a byte per value)
+  char* ds_img;            // of the adjoint of the state after it
+  char* ds_low;            // (bf16 storage: and what bf16 leaves of it, as bf16)
   int64_t q_stride, k_stride, v_stride;  // elements between tokens
   int64_t seqlen;          // tokens per sequence (packed: of all sequences)
   int64_t nseq;
@@ -559,16 +560,8 @@ __device__ __forceinline__ uint32_t low_byte(float v, uint32_t bf_bits_high) {
 __device__ __forceinline__ float with_low(uint32_t bf_bits_high, uint32_t low, int byte) {
   return __uint_as_float(bf_bits_high + (uint32_t)(((int)(low << (24 - 8 * byte)) >> 24) << 8));
 }
-// byte of s_low that holds operand kb of a lane's state column block `cb` (16 columns) of an item
-template <int DK>
-__device__ __forceinline__ int64_t low_at(int64_t item, int cbs, int cb, int kb, int lane) {
-  return ((item * cbs + cb) * (DK / 32) + kb) * 512 + lane * 8;
-}
-
 // Launches the chunk products (T, P and gates of every chunk and value head) into a.ws.
 __attribute__((visibility("hidden"))) int launch_chunks(const Args& a, bool bf, hipStream_t s);
-// Launches the state pass of the backward: E and the states before every chunk into a.e_img, a.s_img.
-__attribute__((visibility("hidden"))) int launch_states(const Args& a, bool bf, hipStream_t s);
 
 }  // namespace delta
 }  // namespace mamba

@@ -13,17 +13,17 @@
 //         R_i = exp(G_i) (scale q_i . S dO_i - k_i . S dY_i)
 // (the last sums leave out every pair that cancels: the decay of token t only weighs what crosses it).
 //
-// Four launches: the chunk products and the state pass of mamba_delta.hip (which leaves E and the state
-// before every chunk in the workspace), then
-//   adjoint_kernel  the adjoint of the state, backwards through the chunks: dV, and dS' of every chunk;
-//                   laid out like the forward's state pass (16 columns per wave, in accumulators)
+// Three launches: the chunk products of mamba_delta.hip, then
+//   passes_kernel   the state forwards through the chunks (mamba_delta_scan.h; it leaves E and the state before
+//                   every chunk) and, beside it, the adjoint of the state backwards: dV, and dS' of every
+//                   chunk; laid out like the state's pass (16 columns per wave, in accumulators)
 //   grad_kernel     one workgroup per chunk and key head: everything else.  The value heads that share
 //                   the key head add their dQ and dK in accumulators, in a fixed order: no atomics.
 // Every gradient is rounded once.  Rounding inside, bf16 storage: two bf16 parts of every factor, except
-// S, dS' and dY where dQ and dK take them (one part each: their rounding weighs less than the gradient's).
+// S and dY where dQ and dK take them (one part each: their rounding weighs less than the gradient's).
 // dg and dbeta are sums of signed terms that may cancel many times over: those that weigh most, k . dS' e and
-// <dS', S>, are made in adjoint_kernel from its accumulators, with S to 17 bits (a byte beside its bf16).
-#include "mamba_delta.h"
+// <dS', S>, take dS' as two parts and S to 17 bits (a byte beside its bf16).
+#include "mamba_delta_scan.h"
 
 namespace mamba {
 namespace delta {
@@ -39,12 +39,7 @@ struct BwdArgs {
   void* dg;            // (tokens, hv)
   void* dbeta;
   float* ds0;          // (nseq, hv, dk, dv) or NULL
-  float* sums;         // per chunk slot, value head and 16 columns: their part of AdjSums
 };
-
-// What the adjoint pass leaves for dg and dbeta, summed over 16 columns of the state: k_j . dS' e_j of the
-// chunk's tokens, and <dS', S>.
-constexpr int kSumKd = 0, kSumDot = kC, kAdjSums = kC + 16;
 
 // 8 (bf16) or 4 (fp32) consecutive values from one operand's accumulators
 template <typename E>
@@ -72,24 +67,23 @@ struct AdjStage {
   static constexpr int kDO = kPLow + (Mma<E>::parts(2) - 1) * TriTile<E>::kBytes;
   static constexpr int kBytes = kDO + VT::kBytes;
   static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+  static constexpr int kLds = kCount * kBytes;
 };
 
 template <typename E, int DK, int NW>
-__global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col_blocks) {
+__device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_blocks, char* smem, uint32_t id,
+                                             uint32_t grid) {
   using M = Mma<E>;
   using St = AdjStage<E, DK, NW>;
   using KT = KeyTile<E, DK>;
   using TT = TriTile<E>;
   using VT = typename St::VT;
   using CW = ChunkWs<E>;
-  using BB = BwdBlock<E>;
-  using ET = KeyTile<E, BB::kDB>;
   constexpr int kP2 = M::parts(2);
-  __shared__ __align__(1024) char smem[St::kCount * St::kBytes];
   const Args& a = b.f;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wg = spread_index(blockIdx.x, gridDim.x, a.rep * col_blocks);
+  const int64_t wg = spread_index(id, grid, a.rep * col_blocks);
   const int64_t sh = wg / col_blocks;
   const int64_t rank = sh / a.hv, seq = seq_by_length(a, rank);
   const int vh = (int)(sh - rank * a.hv), kh = vh / a.rep;
@@ -133,101 +127,40 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
 
   const int dv_pad = (a.dv + BwdBlock<E>::kDB - 1) / BwdBlock<E>::kDB * BwdBlock<E>::kDB;
   const int64_t img_bytes = (int64_t)dv_pad * KT::kRow;
-  const int64_t e_bytes = (int64_t)dv_pad / BB::kDB * BB::kEParts * BB::kE;
   const KT kt(lane);
   const TT tt(lane);
   const VT ot(lane, 16 * w);
-  // The state before a chunk and its E come straight to registers, a chunk ahead like the copies.
-  const bool mine = col < dv_pad;
-  using E4 = decltype(ot.four(lds_ptr(), 0));  // four values as they are stored
-  typename M::Frag shi[DK / M::kDepth];
-  uint2 sl[DK / M::kDepth];
-  E4 ereg[BB::kEParts][4];
-  uint32_t s_off[DK / M::kDepth], e_off[4];
-  {
-    const int cw = (col + 4 * g) % BB::kDB * (int)sizeof(E);
+  uint32_t s_off[DK / M::kDepth];  // this lane's words of the images
 #pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      s_off[kb] = (col + r) * KT::kRow + (((4 * kb + g) ^ KT::key(col + r)) << 4);
-      shi[kb] = typename M::Frag{};
-      sl[kb] = make_uint2(0, 0);
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int t = 16 * m + r;
-      e_off[m] = (col + 4 * g) / BB::kDB * BB::kEParts * BB::kE + t * ET::kRow +
-                 (((cw >> 4) ^ ET::key(t)) << 4) + (cw & 15);
-#pragma unroll
-      for (int p = 0; p < BB::kEParts; ++p) ereg[p][m] = E4{};
-    }
-  }
-  auto fetch_state = [&](int64_t ch) {
-    const int64_t item = (slot0 + ch) * a.hv + vh;
-    if (!mine) return;
-#pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      shi[kb] = *reinterpret_cast<const typename M::Frag*>(a.s_img + item * img_bytes + s_off[kb]);
-      if constexpr (sizeof(E) == 2)
-        sl[kb] = *reinterpret_cast<const uint2*>(
-            a.s_low + low_at<DK>(item, dv_pad / 16, col / 16, kb, lane));
-    }
-  };
-  auto fetch_e = [&](int64_t ch) {
-    const char* img = a.e_img + ((slot0 + ch) * a.hv + vh) * e_bytes;
-    if (!mine) return;
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int p = 0; p < BB::kEParts; ++p)
-        ereg[p][m] = *reinterpret_cast<const E4*>(img + p * BB::kE + e_off[m]);
-  };
-  if (nchunks > 0) {
-    copy(nchunks - 1, 0);
-    fetch_state(nchunks - 1);
-    fetch_e(nchunks - 1);
-  }
+  for (int kb = 0; kb < DK / M::kDepth; ++kb)
+    s_off[kb] = (col + r) * KT::kRow + (((4 * kb + g) ^ KT::key(col + r)) << 4);
+  if (nchunks > 0) copy(nchunks - 1, 0);
   for (int64_t ch = nchunks - 1; ch >= 0; --ch) {
     const int st = St::kCount == 2 ? (int)((nchunks - 1 - ch) & 1) : 0;
     copies_done();
     if (St::kCount == 2 && ch > 0) copy(ch - 1, st ^ 1);
     const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
     const int n = (int)min((int64_t)kC, sp.len - ch * kC);
-    // dS' goes to its image and meets the state before the chunk, in the same layout
-    const int64_t item = (slot0 + ch) * a.hv + vh;
-    typename M::template Parts<kP2> ds[DK / M::kDepth];
-    float dot = 0.f;
+    // dS' goes to its image, and K dS'
+    const int64_t at = ((slot0 + ch) * a.hv + vh) * img_bytes;
+    f32x4 e[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) e[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      ds[kb] = M::template split<kP2>(&S[kb * M::kTiles]);
-      if (mine) *reinterpret_cast<typename M::Frag*>(a.ds_img + item * img_bytes + s_off[kb]) = ds[kb].p[0];
-      if constexpr (sizeof(E) == 2) {
-        const uint4 h = __builtin_bit_cast(uint4, shi[kb]);
-        const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[2] = {sl[kb].x, sl[kb].y};
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          dot = fmaf(S[2 * kb + (x >> 2)][x & 3],
-                     with_low(x & 1 ? hw[x >> 1] & 0xffff0000u : hw[x >> 1] << 16, lw[x >> 2], x & 3), dot);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) dot = fmaf(S[kb][x], shi[kb][x], dot);
+      const auto ds = M::template split<kP2>(&S[kb * M::kTiles]);
+      if (col < dv_pad) {
+        *reinterpret_cast<typename M::Frag*>(a.ds_img + at + s_off[kb]) = ds.p[0];
+        if constexpr (kP2 == 2) *reinterpret_cast<typename M::Frag*>(a.ds_low + at + s_off[kb]) = ds.p[1];
       }
+      typename M::Frag kf[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) kf[m] = kt.rows(sm + St::kK, m, kb);
+#pragma unroll
+      for (int p = 0; p < kP2; ++p)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) e[m] = M::mma(kf[m], ds.p[p], e[m]);
     }
-    if (ch > 0) fetch_state(ch - 1);
-    // K dS' both ways round
-    f32x4 e[4], kd[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) e[m] = kd[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb)
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const auto kf = kt.rows(sm + St::kK, m, kb);
-#pragma unroll
-        for (int p = 0; p < kP2; ++p) {
-          e[m] = M::mma(kf, ds[kb].p[p], e[m]);
-          kd[m] = M::mma(ds[kb].p[p], kf, kd[m]);
-        }
-      }
     // dE = diag(c) K dS' + P^T dO
 #pragma unroll
     for (int m = 0; m < 4; ++m) e[m] *= lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
@@ -260,27 +193,13 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
         }
     }
     // token 16 m + r, columns col + 4 g .. +3
-    float* sums = b.sums + (item * (dv_pad / 16) + col / 16) * kAdjSums;
     const auto buf = __builtin_amdgcn_make_buffer_rsrc(
         dvp + ch * kC * o_stride, 0, (int)(((n - 1) * o_stride + max(a.dv - col, 0)) * (int64_t)sizeof(E)),
         0x00020000);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int t = 16 * m + r;
-      store_four<E>(buf, col + 4 * g < a.dv ? (uint32_t)(t * o_stride + 4 * g) * (uint32_t)sizeof(E) : kOutside,
-                    yt[m]);
-      f32x4 ev = __builtin_convertvector(ereg[0][m], f32x4);
-      if constexpr (BB::kEParts == 2) ev += __builtin_convertvector(ereg[1][m], f32x4);
-      float kk = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) kk = fmaf(kd[m][x], ev[x], kk);
-      kk = across_groups(kk);
-      if (mine && g == 0) sums[kSumKd + t] = kk;
-    }
-    if (ch > 0) fetch_e(ch - 1);
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
-    if (mine && lane == 0) sums[kSumDot] = dot;
+    for (int m = 0; m < 4; ++m)
+      store_four<E>(buf, col + 4 * g < a.dv ? (uint32_t)((16 * m + r) * o_stride + 4 * g) * (uint32_t)sizeof(E)
+                                            : kOutside, yt[m]);
     // dS = exp(G_64) dS' + Q^T diag(scale exp G) dO - K^T diag(exp G) dY
     const float last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
     f32x4 o[4];
@@ -322,6 +241,18 @@ __global__ __launch_bounds__(64 * NW) void adjoint_kernel(BwdArgs b, int32_t col
   }
 }
 
+// The state forwards and its adjoint backwards need nothing of each other: their workgroups share a launch,
+// the adjoint's first (they take longer).
+template <typename E, int DK, int NW>
+__global__ __launch_bounds__(64 * NW) void passes_kernel(BwdArgs b, int32_t col_blocks, uint32_t each) {
+  constexpr int kA = AdjStage<E, DK, NW>::kLds, kS = Stage<E, DK, NW>::kLds;
+  __shared__ __align__(1024) char smem[kA > kS ? kA : kS];
+  if (blockIdx.x < each)
+    adjoint_pass<E, DK, NW>(b, col_blocks, smem, blockIdx.x, each);
+  else
+    scan_pass<E, DK, NW, kBackward>(b.f, col_blocks, smem, blockIdx.x - each, each);
+}
+
 // ------------------------------------------------------------------ dQ, dK, dg, dbeta
 
 // sum over the 16 lanes of a group, in every lane of it
@@ -345,13 +276,17 @@ __device__ __forceinline__ float wave_suffix(float v, int lane) {
 template <typename E, int DK>
 struct GradSmem {
   using B = BwdBlock<E>;
-  // one block of columns of the state: dO, dY, E, S, dS'
+  // one block of columns of the state: dO, dY, E, S, dS', and what bf16 leaves of the last two
   static constexpr int kDO = 0;
   static constexpr int kDY = kDO + B::kE;
   static constexpr int kE = kDY + B::kE;
   static constexpr int kS = kE + B::kEParts * B::kE;
   static constexpr int kDS = kS + B::kDB * KeyTile<E, DK>::kRow;
-  static constexpr int kStage = kDS + B::kDB * KeyTile<E, DK>::kRow;
+  static constexpr int kBlock = B::kDB * KeyTile<E, DK>::kRow;
+  static constexpr bool kLow = sizeof(E) == 2;  // what bf16 leaves of S (bytes) and dS'
+  static constexpr int kDSLow = kDS + kBlock;
+  static constexpr int kSLow = kDSLow + (kLow ? kBlock : 0);
+  static constexpr int kStage = kSLow + (kLow ? kBlock / 2 : 0);
   static constexpr int kBParts = Mma<E>::parts(2);
   static constexpr int kK = 0;
   static constexpr int kQ = KeyTile<E, DK>::kBytes;
@@ -359,9 +294,10 @@ struct GradSmem {
   static constexpr int kB2 = kB1 + kBParts * TriTile<E>::kBytes;
   static constexpr int kGate = kB2 + kBParts * TriTile<E>::kBytes;  // gates and decays of two heads
   static constexpr int kSums = kGate + 2 * 2048;                    // per wave: column sums
-  static constexpr int kTok = kSums + 8 * 2 * kC * 4;               // per half and token: row sums
-  static constexpr int kAdj = kTok + 2 * kC * 4;                    // per wave: adjoint pass's sums
-  static constexpr int kStages = (kAdj + 8 * kAdjSums * 4 + 1023) / 1024 * 1024;
+  static constexpr int kTok = kSums + 8 * 2 * kC * 4;               // per half and token: R + row sum of X,
+                                                                    // then k . dS' e
+  static constexpr int kDot = kTok + 4 * kC * 4;  // per wave: <dS', S>
+  static constexpr int kStages = (kDot + 32 + 1023) / 1024 * 1024;
   static constexpr int kCount = kStages + 2 * kStage <= 160 * 1024 ? 2 : 1;
   static constexpr int kBytes = kStages + kCount * kStage;
 };
@@ -414,11 +350,15 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
     const RowCopy<E, ET, kC, 4> co(tile, lane, o_stride, cols);
     co(rows_buffer(static_cast<const E*>(half ? b.dv : b.dout) + at, n, o_stride, cols),
        to + (half ? Sm::kDY : Sm::kDO), tile);
-    constexpr int kBlock = BB::kDB * KT::kRow;
+    constexpr int kBlock = Sm::kBlock;
     copy_linear<BB::kEParts * BB::kE, 8>(
         a.e_img + item * e_bytes + (int64_t)db * BB::kEParts * BB::kE, to + Sm::kE, w, lane);
     copy_linear<kBlock, 8>(a.s_img + item * img_bytes + (int64_t)db * kBlock, to + Sm::kS, w, lane);
     copy_linear<kBlock, 8>(a.ds_img + item * img_bytes + (int64_t)db * kBlock, to + Sm::kDS, w, lane);
+    if constexpr (Sm::kLow) {
+      copy_linear<kBlock, 8>(a.ds_low + item * img_bytes + (int64_t)db * kBlock, to + Sm::kDSLow, w, lane);
+      copy_linear<kBlock / 2, 8>(a.s_low + (item * img_bytes + (int64_t)db * kBlock) / 2, to + Sm::kSLow, w, lane);
+    }
     if (db == 0)
       copy_linear<2048, 8>(a.ws + item * a.ws_item + CW::kGate, lds0 + Sm::kGate + (h & 1) * 2048, w, lane);
   };
@@ -449,16 +389,7 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
   int st = 0;
   for (int h = 0; h < a.rep; ++h) {
     const int64_t vh = kh * a.rep + h, item = slot * a.hv + vh;
-    // this wave's share of the adjoint pass's sums, on their way while the blocks are worked on
-    float kd = 0.f, dot = 0.f;
-    {
-      const int cbs = blocks * BB::kDB / 16;
-      const float* adj = b.sums + item * cbs * kAdjSums;
-      for (int x = w; x < cbs; x += 8) {
-        kd += adj[x * kAdjSums + kSumKd + lane];
-        dot += adj[x * kAdjSums + kSumDot];
-      }
-    }
+    float dot = 0.f;  // this thread's part of <dS', S>
     f32x4 mn[4], sdo[kTiles], sdy[kTiles], dse[kTiles];
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) mn[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -491,6 +422,26 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
           sdy[m] = M::mma(sf, yf, sdy[m]);
 #pragma unroll
           for (int p = 0; p < BB::kEParts; ++p) dse[m] = M::mma(df, ef[p], dse[m]);
+          if constexpr (Sm::kLow)
+            dse[m] = M::mma(kt.template cols<true>(bl + Sm::kDSLow, m0 + m, kb), ef[0], dse[m]);
+        }
+      }
+      for (int x = threadIdx.x; x < Sm::kBlock / 16; x += 512) {
+        const auto s = lds_read<typename M::Frag>(bl + Sm::kS + 16 * x);
+        const auto d = lds_read<typename M::Frag>(bl + Sm::kDS + 16 * x);
+        if constexpr (Sm::kLow) {
+          typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+          typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+          const u32x4 sw = __builtin_bit_cast(u32x4, s);
+          const u32x2 lw = lds_read<u32x2>(bl + Sm::kSLow + 8 * x);
+          const auto dl = lds_read<typename M::Frag>(bl + Sm::kDSLow + 16 * x);
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            dot = fmaf(with_low(y & 1 ? sw[y >> 1] & 0xffff0000u : sw[y >> 1] << 16, lw[y >> 2], y & 3),
+                       (float)d[y] + (float)dl[y], dot);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) dot = fmaf((float)s[y], (float)d[y], dot);
         }
       }
       if (Sm::kCount == 2) {
@@ -549,7 +500,7 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
     // the state's terms, and their dots with q_i and k_i (half of the values each half)
     {
       const float eg = lds_read<float>(gate + 4 * i), ci = lds_read<float>(gate + 4 * (kC + i));
-      float rdot = 0.f;
+      float rdot = 0.f, kd = 0.f;
 #pragma unroll
       for (int kb = 0; kb < kTiles / M::kTiles; ++kb) {
         const auto ki = kt.rows(sm + Sm::kK, tile, m0 / M::kTiles + kb);
@@ -561,16 +512,21 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
             const int m = kb * M::kTiles + y;
             const float so = a.scale * eg * sdo[m][x], sy = -eg * sdy[m][x];
             rdot = fmaf((float)qi[4 * y + x], so, fmaf((float)ki[4 * y + x], sy, rdot));
+            kd = fmaf((float)ki[4 * y + x], dse[m][x], kd);
             dQ[m][x] += so;
             dK[m][x] += fmaf(ci, dse[m][x], sy);
           }
       }
       rdot = across_groups(rdot);
+      kd = across_groups(kd);
       float* tok = reinterpret_cast<float*>(smem + Sm::kTok);
-      if (g == 0) tok[half * kC + i] = row_x + rdot;
-      float* adj = reinterpret_cast<float*>(smem + Sm::kAdj) + w * kAdjSums;
-      adj[kSumKd + lane] = kd;
-      if (lane == 0) adj[kSumDot] = dot;
+      if (g == 0) {
+        tok[half * kC + i] = row_x + rdot;
+        tok[(2 + half) * kC + i] = kd;
+      }
+#pragma unroll
+      for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
+      if (lane == 0) reinterpret_cast<float*>(smem + Sm::kDot)[w] = dot;
     }
     // B1 and B2 are whole.  (Not a full barrier of the copies: the next block's are on their way.)
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -617,13 +573,11 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
       const float* tok = reinterpret_cast<const float*>(smem + Sm::kTok);
       const float* gt = reinterpret_cast<const float*>(smem + Sm::kGate + (h & 1) * 2048);
       const float* dec = gt + 256;
-      const float* adj = reinterpret_cast<const float*>(smem + Sm::kAdj);
-      float kdt = 0.f, all = 0.f;
+      const float* dots = reinterpret_cast<const float*>(smem + Sm::kDot);
+      const float kdt = tok[2 * kC + lane] + tok[3 * kC + lane];
+      float all = 0.f;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        kdt += adj[x * kAdjSums + kSumKd + lane];
-        all += adj[x * kAdjSums + kSumDot];
-      }
+      for (int x = 0; x < 8; ++x) all += dots[x];
       float cx = 0.f, cb = 0.f;
       for (int x = lane >> 4; x < 8; x = x == 3 ? 4 + (lane >> 4) : x + 1) {
         cx += sums[x * 2 * kC + lane];
@@ -662,10 +616,10 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
 }
 
 template <typename E, int DK, int NW>
-int launch_adjoint_t(const BwdArgs& b, hipStream_t s) {
+int launch_passes_t(const BwdArgs& b, hipStream_t s) {
   const int cols = (b.f.dv + 16 * NW - 1) / (16 * NW);
-  hipLaunchKernelGGL((adjoint_kernel<E, DK, NW>), dim3((unsigned)(b.f.nseq * b.f.hv * cols)),
-                     dim3(64 * NW), 0, s, b, cols);
+  const uint32_t each = (uint32_t)(b.f.nseq * b.f.hv * cols);
+  hipLaunchKernelGGL((passes_kernel<E, DK, NW>), dim3(2 * each), dim3(64 * NW), 0, s, b, cols, each);
   return launch_status();
 }
 template <typename E, int DK>
@@ -673,16 +627,16 @@ int launch_bwd(const BwdArgs& b, hipStream_t s) {
   // 64 or 128 columns per workgroup as in the forward (8 waves of fp32 operands would not fit the
   // registers)
   const bool narrow = sizeof(E) == 4 ||
-                      narrow_pass(b.f.hv, b.f.nseq, !b.f.offsets || b.f.nseq == 1, b.f.dv);
-  const int st = narrow ? launch_adjoint_t<E, DK, 4>(b, s)
-                        : launch_adjoint_t<E, DK, sizeof(E) == 2 ? 8 : 4>(b, s);
+                      narrow_pass(b.f.hv, 2 * b.f.nseq, !b.f.offsets || b.f.nseq == 1, b.f.dv);
+  const int st = narrow ? launch_passes_t<E, DK, 4>(b, s)
+                        : launch_passes_t<E, DK, sizeof(E) == 2 ? 8 : 4>(b, s);
   if (st != MAMBA_OK) return st;
   hipLaunchKernelGGL((grad_kernel<E, DK>), dim3((unsigned)(b.f.slots * b.f.hk)), dim3(512), 0, s, b);
   return launch_status();
 }
 
 struct BwdLayout {  // workspace regions in bytes
-  size_t item, e, s, ds, low, sums, total;
+  size_t item, e, s, ds, s_low, ds_low, total;
 };
 template <typename E>
 BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
@@ -694,9 +648,10 @@ BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
   l.e = items * l.item;
   l.s = l.e + items * blocks * BwdBlock<E>::kEParts * BwdBlock<E>::kE;
   l.ds = l.s + items * blocks * BwdBlock<E>::kDB * row;
-  l.low = l.ds + items * blocks * BwdBlock<E>::kDB * row;
-  l.sums = l.low + (sizeof(E) == 2 ? items * blocks * BwdBlock<E>::kDB * (row / 2) : 0);
-  l.total = l.sums + items * blocks * (BwdBlock<E>::kDB / 16) * kAdjSums * sizeof(float);
+  const size_t img = items * blocks * BwdBlock<E>::kDB * row, low = sizeof(E) == 2 ? img : 0;
+  l.s_low = l.ds + img;
+  l.ds_low = l.s_low + low / 2;
+  l.total = l.ds_low + low;
   return l;
 }
 BwdLayout layout(const mamba_delta_dims* d, bool packed) {
@@ -743,8 +698,8 @@ int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, 
   b.f.e_img = b.f.ws + l.e;
   b.f.s_img = b.f.ws + l.s;
   b.f.ds_img = b.f.ws + l.ds;
-  b.f.s_low = b.f.ws + l.low;
-  b.sums = reinterpret_cast<float*>(b.f.ws + l.sums);
+  b.f.s_low = b.f.ws + l.s_low;
+  b.f.ds_low = b.f.ws + l.ds_low;
   b.dout = dout;
   b.dlast = dlast;
   b.dq = dq;
@@ -756,7 +711,6 @@ int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, 
   const bool bf = dims->io_dtype == MAMBA_BF16;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = launch_chunks(b.f, bf, s)) != MAMBA_OK) return st;
-  if ((st = launch_states(b.f, bf, s)) != MAMBA_OK) return st;
   if (bf) return b.f.dk <= 64 ? launch_bwd<uint16_t, 64>(b, s) : launch_bwd<uint16_t, 128>(b, s);
   return b.f.dk <= 64 ? launch_bwd<float, 64>(b, s) : launch_bwd<float, 128>(b, s);
 }
