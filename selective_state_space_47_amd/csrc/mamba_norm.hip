@@ -10,11 +10,18 @@
 //
 // All four are bound by memory: each input is read once into registers and each output written
 // once.  A unit (one group of one row) belongs to a team of T lanes, T = 8..1024, that holds it as
-// R vectors of 8 values per lane; sums and statistics are fp32, the gradients' fp64.  Vectors are read and written as
-// 16-byte words at any address (rows of odd length start anywhere), the last one value by value.
-// The weights' gradients are sums over all units: a team keeps its columns' sums in registers over
+// R vectors of 8 values per lane; sums and statistics are fp32, the gradients' fp64.  Vectors are read
+// and written as 16-byte words at any address (rows of odd length start anywhere), the last one value by
+// value.  The weights' gradients are sums over all units: a team keeps its columns' sums in registers over
 // the units it visits, the teams of a workgroup add theirs in LDS, each workgroup writes one
 // partial row, and a second launch adds the partial rows.  Every order is fixed: no atomics.
+//
+// Measured, 16384 rows, bf16 (a large copy reaches 4.9 to 5.4 TB/s):
+//   gated norm, 40 groups of 128: 90 us forward (5.6 TB/s), 199 us gradients (4.2 TB/s) and 7 us their second
+//   launch
+//   add norm, 2560 wide, fp32 stream, norm after the block: 104 us forward (4.8 TB/s), 164 us gradients
+//   (4.6 TB/s) and 9 us
+// 256 rows of 40 groups, or one row of 768: 3 to 4 us, latency.
 #include "mamba_common.h"
 
 namespace mamba {
