@@ -329,8 +329,9 @@ typedef struct mamba_delta_dims {
 } mamba_delta_dims;
 
 /* Bytes of device workspace mamba_delta_fwd needs (0 for invalid dims); packed != 0: for a call with
- * seq_offsets.  Per 64 tokens and value head it holds two 64 x 64 matrices and the decays: 20 KB in
- * bf16, 22 KB in fp32. */
+ * seq_offsets.  Per 64 tokens and value head it holds two triangular 64 x 64 matrices and the decays: 20 KB
+ * in bf16, 22 KB in fp32; long sequences of few heads are worked on in segments and add an fp32 state
+ * (dk x dv) and a map (dk x dk) per segment and value head. */
 size_t mamba_delta_workspace_bytes(const mamba_delta_dims* dims, int packed);
 
 /*
@@ -348,8 +349,11 @@ size_t mamba_delta_workspace_bytes(const mamba_delta_dims* dims, int packed);
  *                   tokens hands its initial state on.
  *   workspace     : >= mamba_delta_workspace_bytes bytes, 256-byte aligned; contents on entry ignored
  * q, k, v, out and the states are 16-byte aligned.  The state is fp32 throughout; with bf16 storage the
- * products that reach it carry 16 bits of each factor's mantissa (relative error about 1e-6), with fp32
- * storage all 24.
+ * products that reach it take their factors as two or three bf16 parts (relative error of last_state
+ * about 3e-7), with fp32 storage as they are.  Sequences are worked on in chunks of 64 tokens: a NaN or
+ * an infinity in a token's inputs also reaches the outputs of the tokens before it in its chunk (of the
+ * same value column if it is in v, of the heads that use it otherwise), never an earlier chunk or another
+ * sequence.
  */
 int mamba_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                     const float* initial_state, const int64_t* seq_offsets, float scale, void* out,
@@ -367,7 +371,8 @@ int mamba_delta_update(float* state, const void* q, const void* k, const void* v
 
 /* Bytes of device workspace mamba_delta_bwd needs (0 for invalid dims); packed as for
  * mamba_delta_workspace_bytes.  Beside the forward's it holds, per 64 tokens and value head, the state
- * before them, its adjoint after them (both in io_dtype) and the e_t. */
+ * before them, its adjoint after them and the e_t: with bf16 storage 3 + 4 bytes per value of the
+ * (dk x dv) state and 4 per e_t (bf16 and what it leaves), with fp32 storage 4 each. */
 size_t mamba_delta_bwd_workspace_bytes(const mamba_delta_dims* dims, int packed);
 
 /*
@@ -383,8 +388,8 @@ size_t mamba_delta_bwd_workspace_bytes(const mamba_delta_dims* dims, int packed)
  *                     initial_state is NULL: then it is the gradient at a zero state)
  *   workspace       : >= mamba_delta_bwd_workspace_bytes bytes, 256-byte aligned
  * Every output is overwritten; with seq_offsets, tokens that no sequence holds are not written.  Sums are
- * taken in a fixed order (bitwise reproducible).  With bf16 storage dinitial_state carries the accuracy
- * of bf16 products (about 2e-3 relative).
+ * taken in a fixed order (bitwise reproducible).  With bf16 storage dinitial_state is
+ * within about 3e-6 (relative), the others round once to bf16.
  */
 int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                     const float* initial_state, const int64_t* seq_offsets, float scale,
