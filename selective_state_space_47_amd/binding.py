@@ -768,7 +768,7 @@ def mamba_delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, seq_offset
                                (last_state, "last_state", _state_shape, torch.float32)),
             seq_offsets, 2 if seq_offsets is None else 1, lib().mamba_delta_workspace_bytes))
     if out is None:
-        out = q.new_empty(v.shape)
+        out = m.empty(v)
     if return_last_state and last_state is None:
         dm = e.dims
         last_state = torch.empty((dm.batch, dm.v_heads, dm.dk, dm.dv), dtype=torch.float32,
@@ -795,7 +795,7 @@ def mamba_delta_update(state, q, k, v, g, beta, scale=None, out=None):
                                         ((state, "state", _state_shape, torch.float32),
                                          (out, "out", _out_shape, None)), None, 1, None))
     if out is None:
-        out = q.new_empty(v.shape)
+        out = m.empty(v)
     _call(_DELTA_UPDATE, e, e.factor if scale is None else scale, 0, state, q, k, v, g, beta, out)
     return out
 
@@ -842,7 +842,7 @@ def mamba_delta_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, seq_
             seq_offsets, 2 if seq_offsets is None else 1, lib().mamba_delta_bwd_workspace_bytes))
     for name, like in zip(_DELTA_GRADS, (q, q, v, g, beta, initial_state)):
         if gr.get(name) is None:
-            gr[name] = None if like is None else like.new_empty(like.shape)
+            gr[name] = None if like is None else m.empty(like)
     workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
     res = {name: gr[name] for name in _DELTA_GRADS}
     _call(_DELTA_BWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, beta,
@@ -907,7 +907,7 @@ def mamba_gated_norm_fwd(y, z, weight, eps=1e-5, gate_first=False, out=None):
     if e is None:
         e = _remember(key, _gated_check(y, z, weight, gate_first, ((out, "out", "rows"),)))
     if out is None:
-        out = y.new_empty(y.shape)
+        out = m.empty(y)
     _call(_GATED_FWD, e, eps, 0, y, z, weight, out)
     return out
 
@@ -930,13 +930,13 @@ def mamba_gated_norm_bwd(y, z, weight, dout, eps=1e-5, gate_first=False, workspa
                                          (given[2], "dweight", "weight"))))
     dy, dz, dw = given
     if dy is None:
-        dy = y.new_empty(y.shape)
+        dy = m.empty(y)
     if z is None:
         dz = None
     elif dz is None:
-        dz = y.new_empty(y.shape)
+        dz = m.empty(y)
     if dw is None:
-        dw = weight.new_empty(weight.shape)
+        dw = m.empty(weight)
     workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
     _call(_GATED_BWD, e, eps, ws_len, y, z, weight, dout, dy, dz, dw, workspace)
     return {"dy": dy, "dz": dz, "dweight": dw}
@@ -990,9 +990,9 @@ def mamba_add_norm_fwd(x, residual, weight, scale=None, post_weight=None, eps=1e
                                       ((out, "out", False),
                                        (residual_out, "residual_out", True))))
     if out is None:
-        out = x.new_empty(x.shape)
+        out = m.empty(x)
     if residual_out is None:
-        residual_out = (x if residual is None else residual).new_empty(x.shape)
+        residual_out = m.empty(x if residual is None else residual)
     _call(_ADD_FWD, e, eps, 0, x, residual, weight, scale, post_weight, out, residual_out)
     return out, residual_out
 
@@ -1023,7 +1023,7 @@ def mamba_add_norm_bwd(x, residual, weight, dout, dresidual_out=None, scale=None
         if like is None:
             g[name] = None
         elif g.get(name) is None:
-            g[name] = like.new_empty(like.shape)
+            g[name] = m.empty(like)
     workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
     res = {name: g[name] for name in _ADD_GRADS}
     _call(_ADD_BWD, e, eps, ws_len, x, residual, weight, scale, post_weight, dout, dresidual_out,

@@ -2,8 +2,9 @@
 // bytes object, and their addresses handed to the C entry point.  Checks, allocation and errors stay in
 // binding.py; it looks a call's key up in a cache of keys that have passed the checks.  A launch of a few
 // microseconds (one token, one row) would otherwise be dominated by reading tensors' metadata from Python:
-// 9 to 10 us a call against 5 to 6.
+// 9 to 10 us a call against 5.
 #include <Python.h>
+#include <ATen/ATen.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
@@ -58,6 +59,22 @@ void* address(PyObject* o) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) throw std::invalid_argument("a tensor or None");
   return THPVariable_Unpack(o).data_ptr();
+}
+
+// empty(like) -> a new contiguous tensor of its shape, type and device (0.9 us; like.new_empty(like.shape) from
+// Python takes 1.8)
+PyObject* empty(PyObject*, PyObject* like) {
+  if (!THPVariable_Check(like)) {
+    PyErr_SetString(PyExc_TypeError, "a tensor");
+    return nullptr;
+  }
+  try {
+    const at::Tensor& t = THPVariable_Unpack(like);
+    return THPVariable_Wrap(at::empty(t.sizes(), t.options()));
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
 }
 
 enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd };
@@ -126,6 +143,7 @@ PyMethodDef kMethods[] = {
     {"key", (PyCFunction)(void (*)())key, METH_FASTCALL, "key(*args) -> bytes: types, shapes, strides, devices"},
     {"call", (PyCFunction)(void (*)())call, METH_FASTCALL,
      "call(entry, dims address, stream, factor, workspace bytes, *tensors) -> status"},
+    {"empty", empty, METH_O, "empty(like) -> a new contiguous tensor of its shape, type and device"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "mamba_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
