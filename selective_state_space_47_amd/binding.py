@@ -679,6 +679,14 @@ def _call(which, e, factor, ws_len, *tensors):
         _raise(st)
 
 
+def _scratch(workspace, like, e):
+    """The caller's workspace, checked, or a new one on like's device: (tensor, its size in bytes)."""
+    if workspace is not None:
+        return _workspace(workspace, e.workspace_bytes, e.device)
+    n = e.workspace_bytes or 1
+    return _MARSHAL.empty(like, "b", n), n
+
+
 def _delta_check(q, k, v, g, beta, others, seq_offsets, lead, workspace_bytes):
     """The entry of a call on these tensors; raises for tensors that do not belong together.  `others`:
     (tensor or None, name, shape function of (states, *token axes), Hk, Hv, dk, dv, dtype or None for
@@ -771,9 +779,8 @@ def mamba_delta_fwd(q, k, v, g, beta, scale=None, initial_state=None, seq_offset
         out = m.empty(v)
     if return_last_state and last_state is None:
         dm = e.dims
-        last_state = torch.empty((dm.batch, dm.v_heads, dm.dk, dm.dv), dtype=torch.float32,
-                                 device=e.device)
-    workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
+        last_state = m.empty(q, "f", dm.batch, dm.v_heads, dm.dk, dm.dv)
+    workspace, ws_len = _scratch(workspace, q, e)
     _call(_DELTA_FWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, beta,
           initial_state, seq_offsets, out, last_state, workspace)
     return (out, last_state) if return_last_state else out
@@ -843,7 +850,7 @@ def mamba_delta_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, seq_
     for name, like in zip(_DELTA_GRADS, (q, q, v, g, beta, initial_state)):
         if gr.get(name) is None:
             gr[name] = None if like is None else m.empty(like)
-    workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
+    workspace, ws_len = _scratch(workspace, q, e)
     res = {name: gr[name] for name in _DELTA_GRADS}
     _call(_DELTA_BWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, beta,
           initial_state, seq_offsets, dout, dlast, *res.values(), workspace)
@@ -937,7 +944,7 @@ def mamba_gated_norm_bwd(y, z, weight, dout, eps=1e-5, gate_first=False, workspa
         dz = m.empty(y)
     if dw is None:
         dw = m.empty(weight)
-    workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
+    workspace, ws_len = _scratch(workspace, y, e)
     _call(_GATED_BWD, e, eps, ws_len, y, z, weight, dout, dy, dz, dw, workspace)
     return {"dy": dy, "dz": dz, "dweight": dw}
 
@@ -1024,7 +1031,7 @@ def mamba_add_norm_bwd(x, residual, weight, dout, dresidual_out=None, scale=None
             g[name] = None
         elif g.get(name) is None:
             g[name] = m.empty(like)
-    workspace, ws_len = _workspace(workspace, e.workspace_bytes, e.device, min_bytes=1)
+    workspace, ws_len = _scratch(workspace, x, e)
     res = {name: g[name] for name in _ADD_GRADS}
     _call(_ADD_BWD, e, eps, ws_len, x, residual, weight, scale, post_weight, dout, dresidual_out,
           *res.values(), workspace)
