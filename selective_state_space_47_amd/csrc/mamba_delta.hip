@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kern
 // ------------------------------------------------------------------ the state through the chunks
 
 template <typename E, int DK, int NW, Pass kPass>
-__global__ __launch_bounds__(64 * NW) void scan_kernel(Args a, int32_t col_blocks) {
+__global__ __launch_bounds__(kPassThreads) void scan_kernel(Args a, int32_t col_blocks) {
   __shared__ __align__(1024) char smem[Stage<E, DK, NW>::kLds];
   scan_pass<E, DK, NW, kPass>(a, col_blocks, smem, blockIdx.x, gridDim.x);
 }

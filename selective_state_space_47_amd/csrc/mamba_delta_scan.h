@@ -29,6 +29,11 @@ struct Stage {
   static constexpr int kLds = kCount * kBytes;
 };
 
+// Threads that a pass is compiled for: 512 (256 registers each), though a workgroup of 4 waves could have 512
+// registers.  With no more than 256 the compiler keeps accumulators where vector instructions reach them;
+// otherwise a fifth of its vector instructions move values to and from the accumulation registers.
+constexpr int kPassThreads = 512;
+
 // What a pass leaves: the output and the last state; the backward's E and the state before each chunk; or,
 // for a segment of a long sequence, the state that it makes from zero (columns of the state) and from the
 // identity without values (dk more columns: the segment's map of the state before it).
