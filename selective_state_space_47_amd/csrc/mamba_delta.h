@@ -1,4 +1,4 @@
-// mamba_delta.h -- what the gated delta rule's kernels share (mamba_delta.hip, mamba_delta_bwd.hip):
+// mamba_delta.h -- what the gated delta rule's kernels share (mamba_delta.hip, _step.hip, _bwd.hip):
 // the chunk form, matrix-core operands, launch arguments and host-side validation.
 //
 // Per value head, with state S (dk x dv), keys k and queries q of its key head:
