@@ -468,7 +468,7 @@ inline bool narrow_pass(int64_t heads, int64_t runs, bool even, int64_t dv) {
   // lengths that differ: the longest, taken as twice the mean, or all of them spread over the CUs
   const double tw = even ? std::ceil(wide) : std::max(2.0, wide);
   const double ts = even ? std::ceil(slim) : std::max(2.0, slim);
-  return ts * 3.4 < tw * 4.9;
+  return ts * 3.15 < tw * 4.4;
 }
 inline size_t chunk_ws_bytes(const mamba_delta_dims* d) {
   return d->io_dtype == MAMBA_BF16 ? ChunkWs<uint16_t>::kBytes : ChunkWs<float>::kBytes;

@@ -122,10 +122,22 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
   for (int64_t ch = first; ch < end; ++ch) {
     const int st = St::kCount == 2 ? (int)((ch - first) & 1) : 0;
     copies_done();
-    // with two stages the next chunk is copied while this one is worked on
-    if (St::kCount == 2 && ch + 1 < end) copy(ch + 1, st ^ 1);
     const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
     const int n = (int)min((int64_t)kC, sp.len - ch * kC);
+    // Operands are read a step before the products that take them: one or two waves per SIMD leave nobody
+    // else to hide the reads behind.  A step ends where nothing is moved past.
+    typename M::Frag kf[2][4], qf[2][4];
+    auto read_kq = [&](int kb) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        kf[kb & 1][m] = kt.rows(sm + St::kK, m, kb);
+        if (kO) qf[kb & 1][m] = kt.rows(sm + St::kQ, m, kb);
+      }
+    };
+    auto step = [] { __builtin_amdgcn_sched_barrier(0); };
+    read_kq(0);
+    // with two stages the next chunk is copied while this one is worked on
+    if (St::kCount == 2 && ch + 1 < end) copy(ch + 1, st ^ 1);
 
     if constexpr (kStates) {
       // the state before the chunk: 16 bytes of one column per operand
@@ -153,39 +165,71 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
       }
     }
     // K S (tokens x columns) and (Q S)^T (columns x tokens)
-    f32x4 y[4], o[4];
+    f32x4 y[4], o[4], vv[4], eg[4];
+    float so[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) y[m] = o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      const auto s = M::template split<kPS>(&S[kb * M::kTiles]);
-      typename M::Frag kf[4], qf[4];
+      step();
+      if (kb + 1 < DK / M::kDepth) {
+        read_kq(kb + 1);
+      } else {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        kf[m] = kt.rows(sm + St::kK, m, kb);
-        if (kO) qf[m] = kt.rows(sm + St::kQ, m, kb);
+        for (int m = 0; m < 4; ++m) {
+          vv[m] = vt.tile(sm + St::kVv, m);
+          eg[m] = lds_read<f32x4>(sm + St::kGate + (16 * m + 4 * g) * 4);
+          so[m] = lds_read<float>(sm + St::kGate + (16 * m + r) * 4);
+        }
       }
+      const auto s = M::template split<kPS>(&S[kb * M::kTiles]);
 #pragma unroll
       for (int p = 0; p < kPS; ++p)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) y[m] = M::mma(kf[m], s.p[p], y[m]);
+        for (int m = 0; m < 4; ++m) y[m] = M::mma(kf[kb & 1][m], s.p[p], y[m]);
       if constexpr (kO) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) o[m] = M::mma(s.p[0], qf[m], o[m]);
+        for (int m = 0; m < 4; ++m) o[m] = M::mma(s.p[0], qf[kb & 1][m], o[m]);
       }
     }
     // Y = V - diag(exp G) K S;  O scaled by its token's factor
+    step();
+    typename M::Frag tf[2][kPT][4], pf[2][4];
+    auto read_t = [&](int kb) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const f32x4 v = vt.tile(sm + St::kVv, m);
-      const f32x4 eg = lds_read<f32x4>(sm + St::kGate + (16 * m + 4 * g) * 4);
-      const float so = a.scale * lds_read<float>(sm + St::kGate + (16 * m + r) * 4);
+      for (int p = 0; p < kPT; ++p)
+#pragma unroll
+        for (int m = kb * M::kTiles; m < 4; ++m)
+          tf[kb & 1][p][m] = tt.rows(sm + St::kWs + p * TT::kBytes, m, kb);
+    };
+    auto read_p = [&](int kb) {
+#pragma unroll
+      for (int m = kb * M::kTiles; m < 4; ++m)
+        pf[kb & 1][m] = tt.rows(sm + St::kWs + ChunkWs<E>::kT, m, kb);
+    };
+    read_t(0);
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        y[m][x] = fmaf(-eg[x], y[m][x], v[x]);
-        if (kO) o[m][x] *= so;
+        y[m][x] = fmaf(-eg[m][x], y[m][x], vv[m][x]);
+        if (kO) o[m][x] *= a.scale * so[m];
       }
-    }
+    // what the state takes: factors c, then operands of K in fours
+    constexpr int kFours = TT::kBlocks * (DK / 64);
+    f32x4 cf[4];
+    float last = 0.f;
+    auto read_c = [&] {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) cf[m] = lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
+      last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
+    };
+    typename M::Frag cols[2][4];
+    auto read_cols = [&](int i) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        cols[i & 1][m] = kt.cols(sm + St::kK, i % (DK / 64) * 4 + m, i / (DK / 64));
+    };
     // E = T Y, T lower triangular; the parts' products down to the last part's size.  The state pass
     // also makes it transposed, to store it row by row.
     f32x4 e[4], et[4];
@@ -193,21 +237,25 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
     for (int m = 0; m < 4; ++m) e[m] = et[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < TT::kBlocks; ++kb) {
+      step();
+      if (kb + 1 < TT::kBlocks) {
+        read_t(kb + 1);
+      } else {
+        if (kO) read_p(0); else read_cols(0);
+        read_c();
+      }
       const auto ys = M::template split<kPY>(&y[kb * M::kTiles]);
 #pragma unroll
-      for (int p = 0; p < kPT; ++p) {
-        typename M::Frag tf[4];
-#pragma unroll
-        for (int m = kb * M::kTiles; m < 4; ++m) tf[m] = tt.rows(sm + St::kWs + p * TT::kBytes, m, kb);
+      for (int p = 0; p < kPT; ++p)
 #pragma unroll
         for (int x = 0; x + p < kPY; ++x)
 #pragma unroll
           for (int m = kb * M::kTiles; m < 4; ++m) {
-            e[m] = M::mma(tf[m], ys.p[x], e[m]);
-            if (kStates) et[m] = M::mma(ys.p[x], tf[m], et[m]);
+            e[m] = M::mma(tf[kb & 1][p][m], ys.p[x], e[m]);
+            if (kStates) et[m] = M::mma(ys.p[x], tf[kb & 1][p][m], et[m]);
           }
-      }
     }
+    step();
     if constexpr (kStates) {
       // token 16 m + r, columns col + 4 g .. +3 of the image of E
       if (col + 4 * g < dv_pad) {
@@ -237,15 +285,13 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
       // O += P E, transposed: a lane ends with 4 consecutive columns of one token
 #pragma unroll
       for (int kb = 0; kb < TT::kBlocks; ++kb) {
+        if (kb + 1 < TT::kBlocks) read_p(kb + 1); else read_cols(0);
         const auto es = M::template split<kPO>(&e[kb * M::kTiles]);
-        typename M::Frag pf[4];
-#pragma unroll
-        for (int m = kb * M::kTiles; m < 4; ++m)
-          pf[m] = tt.rows(sm + St::kWs + ChunkWs<E>::kT, m, kb);
 #pragma unroll
         for (int p = 0; p < kPO; ++p)
 #pragma unroll
-          for (int m = kb * M::kTiles; m < 4; ++m) o[m] = M::mma(es.p[p], pf[m], o[m]);
+          for (int m = kb * M::kTiles; m < 4; ++m) o[m] = M::mma(es.p[p], pf[kb & 1][m], o[m]);
+        step();
       }
       const auto buf = __builtin_amdgcn_make_buffer_rsrc(
           op + ch * kC * o_stride, 0, (int)(((n - 1) * o_stride + max(a.dv - col, 0)) * (int64_t)sizeof(E)),
@@ -257,22 +303,21 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
     }
     // S = exp(G_64) S + K^T diag(c) E
 #pragma unroll
-    for (int m = 0; m < 4; ++m) e[m] *= lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
-    const float last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
+    for (int m = 0; m < 4; ++m) e[m] *= cf[m];
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m) S[m] *= last;
 #pragma unroll
     for (int kb = 0; kb < TT::kBlocks; ++kb) {
       const auto es = M::template split<kPE>(&e[kb * M::kTiles]);
 #pragma unroll
-      for (int m0 = 0; m0 < DK / 16; m0 += 4) {
-        typename M::Frag kf[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) kf[m] = kt.cols(sm + St::kK, m0 + m, kb);
+      for (int j = 0; j < DK / 64; ++j) {
+        const int i = kb * (DK / 64) + j;
+        if (i + 1 < kFours) read_cols(i + 1);
 #pragma unroll
         for (int p = 0; p < kPE; ++p)
 #pragma unroll
-          for (int m = 0; m < 4; ++m) S[m0 + m] = M::mma(kf[m], es.p[p], S[m0 + m]);
+          for (int m = 0; m < 4; ++m) S[4 * j + m] = M::mma(cols[i & 1][m], es.p[p], S[4 * j + m]);
+        step();
       }
     }
     if (St::kCount == 1 && ch + 1 < end) {
