@@ -3,8 +3,6 @@ from __future__ import annotations
 
 import os
 import subprocess
-import tempfile
-from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,12 +22,6 @@ HIPCC_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument",
 ]
-
-# Per source.  The state passes of mamba_delta.hip have one or two waves per SIMD, so that only a wave's own
-# independent instructions hide the LDS: scheduling for those takes its output pass from 245 to 223 us (packed
-# prefill) and from 322 to 309 us (8 x 2048 tokens).  The gradients' last kernel (617 to 627 us) and the step
-# (271 to 275 us) lose by it.
-SOURCE_FLAGS = {"mamba_delta.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]}
 
 
 def hipcc() -> str:
@@ -64,20 +56,12 @@ def build(verbose: bool = False) -> str:
     binding's per-call part beside it."""
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
-
-    def run(cmd):
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
-        if verbose and res.stderr:
-            print(res.stderr)
-
-    flags = [hipcc()] + HIPCC_FLAGS + ["-I", INCLUDE]
-    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(4) as pool:
-        outs = [os.path.join(objects, os.path.basename(f) + ".o") for f in SOURCES]
-        list(pool.map(lambda f, o: run(flags + SOURCE_FLAGS.get(os.path.basename(f), []) +
-                                       ["-c", f, "-o", o]), SOURCES, outs))
-        run(flags + ["-o", tmp] + outs)
+    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", INCLUDE, "-o", tmp] + SOURCES
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
+    if verbose and res.stderr:
+        print(res.stderr)
     os.replace(tmp, LIB_PATH)
     build_marshal()
     return LIB_PATH
