@@ -138,60 +138,113 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
   for (int64_t ch = nchunks - 1; ch >= 0; --ch) {
     const int st = St::kCount == 2 ? (int)((nchunks - 1 - ch) & 1) : 0;
     copies_done();
-    if (St::kCount == 2 && ch > 0) copy(ch - 1, st ^ 1);
     const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
     const int n = (int)min((int64_t)kC, sp.len - ch * kC);
+    // (operands are read a step before their products, as in the state's pass)
+    auto step = [] { __builtin_amdgcn_sched_barrier(0); };
+    typename M::Frag kf[2][4];
+    auto read_k = [&](int kb) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) kf[kb & 1][m] = kt.rows(sm + St::kK, m, kb);
+    };
+    read_k(0);
+    if (St::kCount == 2 && ch > 0) copy(ch - 1, st ^ 1);
     // dS' goes to its image, and K dS'
     const int64_t at = ((slot0 + ch) * a.hv + vh) * img_bytes;
-    f32x4 e[4];
+    f32x4 e[4], cf[4];
+    typename M::Frag pf[2][kP2][4], df[2];
+    auto read_p = [&](int ib) {
+      df[ib & 1] = ot.operand(sm + St::kDO, ib);
+#pragma unroll
+      for (int m = 0; m < (ib + 1) * M::kTiles; ++m) {
+        pf[ib & 1][0][m] = tt.cols(sm + St::kP, m, ib);
+        if constexpr (kP2 == 2) pf[ib & 1][1][m] = tt.cols(sm + St::kPLow, m, ib);
+      }
+    };
 #pragma unroll
     for (int m = 0; m < 4; ++m) e[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+      step();
+      if (kb + 1 < DK / M::kDepth) {
+        read_k(kb + 1);
+      } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) cf[m] = lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
+        read_p(0);
+      }
       const auto ds = M::template split<kP2>(&S[kb * M::kTiles]);
       if (col < dv_pad) {
         *reinterpret_cast<typename M::Frag*>(a.ds_img + at + s_off[kb]) = ds.p[0];
         if constexpr (kP2 == 2) *reinterpret_cast<typename M::Frag*>(a.ds_low + at + s_off[kb]) = ds.p[1];
       }
-      typename M::Frag kf[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) kf[m] = kt.rows(sm + St::kK, m, kb);
 #pragma unroll
       for (int p = 0; p < kP2; ++p)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) e[m] = M::mma(kf[m], ds.p[p], e[m]);
+        for (int m = 0; m < 4; ++m) e[m] = M::mma(kf[kb & 1][m], ds.p[p], e[m]);
     }
     // dE = diag(c) K dS' + P^T dO
+    typename M::Frag tf[2][kP2][4];
+    auto read_t = [&](int ib) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) e[m] *= lds_read<f32x4>(sm + St::kGate + (kC + 16 * m + 4 * g) * 4);
+      for (int p = 0; p < kP2; ++p)
+#pragma unroll
+        for (int m = 0; m < (ib + 1) * M::kTiles; ++m)
+          tf[ib & 1][p][m] = tt.cols(sm + St::kWs + p * TT::kBytes, m, ib);
+    };
 #pragma unroll
     for (int ib = 0; ib < TT::kBlocks; ++ib) {
-      const auto d = ot.operand(sm + St::kDO, ib);
+      step();
+      if (ib + 1 < TT::kBlocks) read_p(ib + 1); else read_t(0);
+      if (ib == 0)
 #pragma unroll
-      for (int m = 0; m < (ib + 1) * M::kTiles; ++m) {
-        e[m] = M::mma(tt.cols(sm + St::kP, m, ib), d, e[m]);
-        if constexpr (kP2 == 2) e[m] = M::mma(tt.cols(sm + St::kPLow, m, ib), d, e[m]);
-      }
+        for (int m = 0; m < 4; ++m) e[m] *= cf[m];
+#pragma unroll
+      for (int p = 0; p < kP2; ++p)
+#pragma unroll
+        for (int m = 0; m < (ib + 1) * M::kTiles; ++m) e[m] = M::mma(pf[ib & 1][p][m], df[ib & 1], e[m]);
     }
-    // dY = T^T dE, and transposed for the store
+    // dY = T^T dE, and transposed for the store; then what dS takes
+    f32x4 eg[4], o[4];
+    float last = 0.f;
+    typename M::Frag qc[2][4], kc[2][4];
+    auto read_cols = [&](int i) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        qc[i & 1][m] = kt.cols(sm + St::kQ, i % (DK / 64) * 4 + m, i / (DK / 64));
+        kc[i & 1][m] = kt.cols(sm + St::kK, i % (DK / 64) * 4 + m, i / (DK / 64));
+      }
+    };
     f32x4 y[4], yt[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) y[m] = yt[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ib = 0; ib < TT::kBlocks; ++ib) {
+      step();
+      if (ib + 1 < TT::kBlocks) {
+        read_t(ib + 1);
+      } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          eg[m] = lds_read<f32x4>(sm + St::kGate + (16 * m + 4 * g) * 4);
+          o[m] = ot.tile(sm + St::kDO, m);
+        }
+        last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
+        read_cols(0);
+      }
       const auto es = M::template split<kP2>(&e[ib * M::kTiles]);
 #pragma unroll
       for (int m = 0; m < (ib + 1) * M::kTiles; ++m)
 #pragma unroll
         for (int p = 0; p < kP2; ++p) {
-          const auto tf = tt.cols(sm + St::kWs + p * TT::kBytes, m, ib);
 #pragma unroll
           for (int x = 0; x + p < kP2; ++x) {
-            y[m] = M::mma(tf, es.p[x], y[m]);
-            yt[m] = M::mma(es.p[x], tf, yt[m]);
+            y[m] = M::mma(tf[ib & 1][p][m], es.p[x], y[m]);
+            yt[m] = M::mma(es.p[x], tf[ib & 1][p][m], yt[m]);
           }
         }
     }
+    step();
     // token 16 m + r, columns col + 4 g .. +3
     const auto buf = __builtin_amdgcn_make_buffer_rsrc(
         dvp + ch * kC * o_stride, 0, (int)(((n - 1) * o_stride + max(a.dv - col, 0)) * (int64_t)sizeof(E)),
@@ -201,13 +254,10 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
       store_four<E>(buf, col + 4 * g < a.dv ? (uint32_t)((16 * m + r) * o_stride + 4 * g) * (uint32_t)sizeof(E)
                                             : kOutside, yt[m]);
     // dS = exp(G_64) dS' + Q^T diag(scale exp G) dO - K^T diag(exp G) dY
-    const float last = lds_read<float>(sm + St::kGate + 2 * kC * 4);
-    f32x4 o[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const f32x4 eg = lds_read<f32x4>(sm + St::kGate + (16 * m + 4 * g) * 4);
-      o[m] = ot.tile(sm + St::kDO, m) * (a.scale * eg);
-      y[m] *= -eg;
+      o[m] *= a.scale * eg[m];
+      y[m] *= -eg[m];
     }
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m) S[m] *= last;
@@ -216,13 +266,17 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
       const auto of = M::template split<kP2>(&o[kb * M::kTiles]);
       const auto yf = M::template split<kP2>(&y[kb * M::kTiles]);
 #pragma unroll
-      for (int m = 0; m < DK / 16; ++m) {
-        const auto qf = kt.cols(sm + St::kQ, m, kb), kf = kt.cols(sm + St::kK, m, kb);
+      for (int j = 0; j < DK / 64; ++j) {
+        const int i = kb * (DK / 64) + j;
+        if (i + 1 < TT::kBlocks * (DK / 64)) read_cols(i + 1);
 #pragma unroll
-        for (int p = 0; p < kP2; ++p) {
-          S[m] = M::mma(qf, of.p[p], S[m]);
-          S[m] = M::mma(kf, yf.p[p], S[m]);
-        }
+        for (int p = 0; p < kP2; ++p)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            S[4 * j + m] = M::mma(qc[i & 1][m], of.p[p], S[4 * j + m]);
+            S[4 * j + m] = M::mma(kc[i & 1][m], yf.p[p], S[4 * j + m]);
+          }
+        step();
       }
     }
     if (St::kCount == 1 && ch > 0) {
