@@ -457,10 +457,10 @@ inline int64_t chunk_slots(const mamba_delta_dims* d, bool packed) { return slot
 
 // Whether a state pass takes workgroups of 64 columns (4 waves) instead of 128 (8 waves); `runs` sequences or
 // segments per head, equally long (`even`) or not.  One workgroup runs on a CU at a time and goes through
-// its chunks one after another: 128 columns share a chunk's tiles better (4.9 us a chunk with all CUs busy,
-// dk = 128, bf16), 64 are through sooner (3.4 us) and leave less idle at the end.  Measured, sequences of 2048,
-// heads of 128, 64 and 128 columns: forward of 120 heads 176 and 195 us, of 240 349 and 262 us; backward of 40
-// 250 and 291 us, of 240 1151 and 1017 us.
+// its chunks one after another: 128 columns share a chunk's tiles better (4.3 us a chunk with all CUs busy,
+// dk = 128, bf16), 64 are through sooner (3.1 us) and leave less idle at the end.  Measured, sequences of 2048,
+// heads of 128, 64 and 128 columns: forward of 120 heads 149 and 175 us, of 240 310 and 254 us; backward of 40
+// 232 and 285 us, of 240 1086 and 1006 us.
 inline bool narrow_pass(int64_t heads, int64_t runs, bool even, int64_t dv) {
   if (dv <= 64) return true;
   const double n = (double)heads * (double)runs, wide = n * (double)((dv + 127) / 128) / 256.0,
@@ -468,7 +468,7 @@ inline bool narrow_pass(int64_t heads, int64_t runs, bool even, int64_t dv) {
   // lengths that differ: the longest, taken as twice the mean, or all of them spread over the CUs
   const double tw = even ? std::ceil(wide) : std::max(2.0, wide);
   const double ts = even ? std::ceil(slim) : std::max(2.0, slim);
-  return ts * 3.15 < tw * 4.4;
+  return ts * 3.1 < tw * 4.3;
 }
 inline size_t chunk_ws_bytes(const mamba_delta_dims* d) {
   return d->io_dtype == MAMBA_BF16 ? ChunkWs<uint16_t>::kBytes : ChunkWs<float>::kBytes;

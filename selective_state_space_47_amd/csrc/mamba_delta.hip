@@ -273,7 +273,7 @@ __global__ __launch_bounds__(kPassThreads) void scan_kernel(Args a, int32_t col_
 
 // The states before the segments, one after another: S <- map S + (the segment's own).  A workgroup has 16
 // columns, its waves 16 rows each; fp32 matrix instructions, S handed round through LDS.  Bound by that chain:
-// 62 us of the 800 that 65536 tokens x 12 heads of 128 take.  seg_state holds
+// 62 us of the 720 that 65536 tokens x 12 heads of 128 take.  seg_state holds
 // each segment's own result on entry and the state before it on return.
 template <int DK>
 __global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_blocks) {
@@ -351,8 +351,8 @@ __global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_bl
 template <typename E, int DK>
 int launch_chunks_t(const Args& a, hipStream_t s) {
   // value heads of a key head one after another share K K^T and Q K^T; where that leaves CUs idle, each
-  // has a workgroup of its own (whole forward, two value heads per key head: 400 chunks x heads 52 us
-  // against 57, 10240 482 us against 435)
+  // has a workgroup of its own (whole forward, two value heads per key head: 40 chunks x heads 17 us
+  // against 22, 400 44 us against 47, 10240 462 us against 408)
   const unsigned split = a.slots * a.hk * a.rep <= 512 ? (unsigned)a.rep : 1;
   hipLaunchKernelGGL((chunk_kernel<E, DK>), dim3((unsigned)(a.slots * a.hk), split), dim3(256), 0, s, a);
   return launch_status();
@@ -397,8 +397,8 @@ int launch_forward(const Args& a, hipStream_t s) {
 // workgroups (one per CU); segments add a summary pass over their own and the map's columns, about 0.65
 // of a unit per chunk, and a quarter of a unit per segment to join them.  Packed sequences are taken to
 // be up to twice as long as their mean.  Segments are used where that model gains a quarter.
-// Measured, heads of 128, bf16, whole and in segments: 65536 tokens x 12 heads 3708 and 807 us, 16384 x 12
-// 895 and 269 us.
+// Measured, heads of 128, bf16, whole and in segments: 65536 tokens x 12 heads 2757 and 757 us, 16384 x 12
+// 642 and 258 us.
 int64_t plan_segments(const mamba_delta_dims* d, bool packed) {
   constexpr double kCUs = 256.0;
   const int64_t per = d->dv <= 64 ? 64 : 128;
