@@ -301,7 +301,8 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
 // the last round's idle CUs.  S and dS' of every chunk are 60% of it; making them again from the chunks'
 // inputs would take the passes' products a second time.  (fp32 tiles of 128 keys do not fit 256 registers.)
 template <typename E, int DK, int NW>
-__global__ __launch_bounds__((sizeof(E) * DK <= 256 ? kPassThreads : 64 * NW)) void passes_kernel(BwdArgs b, int32_t col_blocks, uint32_t each) {
+__global__ __launch_bounds__((sizeof(E) * DK <= 256 ? kPassThreads : 64 * NW)) void passes_kernel(
+    BwdArgs b, int32_t col_blocks, uint32_t each) {
   constexpr int kA = AdjStage<E, DK, NW>::kLds, kS = Stage<E, DK, NW>::kLds;
   __shared__ __align__(1024) char smem[kA > kS ? kA : kS];
   if (blockIdx.x < each)
