@@ -329,7 +329,7 @@ typedef struct mamba_delta_dims {
 } mamba_delta_dims;
 
 /* Bytes of device workspace mamba_delta_fwd needs (0 for invalid dims); packed != 0: for a call with
- * seq_offsets.  Per 64 tokens and value head it holds two triangular 64 x 64 matrices and the decays: 20 KB
+ * seq_offsets.  Per 64 tokens and value head it holds two triangular 64 x 64 matrices and the decays: 26 KB
  * in bf16, 22 KB in fp32; long sequences of few heads are worked on in segments and add an fp32 state
  * (dk x dv) and a map (dk x dk) per segment and value head. */
 size_t mamba_delta_workspace_bytes(const mamba_delta_dims* dims, int packed);
@@ -350,7 +350,8 @@ size_t mamba_delta_workspace_bytes(const mamba_delta_dims* dims, int packed);
  *   workspace     : >= mamba_delta_workspace_bytes bytes, 256-byte aligned; contents on entry ignored
  * q, k, v, out and the states are 16-byte aligned.  The state is fp32 throughout; with bf16 storage the
  * products that reach it take their factors as two or three bf16 parts (relative error of last_state
- * about 3e-7), with fp32 storage as they are.  Sequences are worked on in chunks of 64 tokens: a NaN or
+ * about 3e-7) and those that reach out as two, so that out is the fp32 result rounded once; with fp32
+ * storage as they are.  Sequences are worked on in chunks of 64 tokens: a NaN or
  * an infinity in a token's inputs also reaches the outputs of the tokens before it in its chunk (of the
  * same value column if it is in v, of the heads that use it otherwise), never an earlier chunk or another
  * sequence.

@@ -435,19 +435,18 @@ __device__ __forceinline__ int64_t spread_index(uint32_t id, uint32_t n, uint32_
 // it, so that two parts leave an error of 2^-18 of the small entries.
 constexpr int kTParts = 2;
 
-// Workspace of one chunk and value head: T (in parts), P, then floats: exp(G_i) (64), c_j (64),
-// exp(G_64) and 127 unused, G_i as two floats (64 + 64), beta (64), 64 unused; for the backward also the
-// second part of P (bf16 storage), whose rounding would weigh as much in dV as that of dV itself.
+// Workspace of one chunk and value head: P and T (in parts), then floats: exp(G_i) (64), c_j (64),
+// exp(G_64) and 127 unused, G_i as two floats (64 + 64), beta (64), 64 unused.  P has a second part with bf16
+// storage, as its rounding would weigh as much in the output and in dV as their own.
 template <typename E>
 struct ChunkWs {
-  static constexpr int kT = Mma<E>::parts(kTParts) * TriTile<E>::kBytes;
-  static constexpr int kP = TriTile<E>::kBytes;
-  static constexpr int kGate = kT + kP;        // what the scan reads: 1 KB
-  static constexpr int kDecay = kGate + 1024;  // what only the gradients read: 1 KB
+  static constexpr int kPart = TriTile<E>::kBytes;
+  static constexpr int kP = 0;                            // read where an output is made
+  static constexpr int kT = Mma<E>::parts(2) * kPart;     // from here on: what every pass reads
+  static constexpr int kGate = kT + Mma<E>::parts(kTParts) * kPart;
+  static constexpr int kDecay = kGate + 1024;             // what only the gradients read: 1 KB
   static constexpr int kBytes = kDecay + 1024;
-  static constexpr int kPLow = kBytes;
-  static constexpr int kBwdBytes = kBytes + (Mma<E>::parts(2) - 1) * kP;
-  static_assert(kBytes % 1024 == 0 && kBwdBytes % 1024 == 0, "copied in whole wave instructions");
+  static_assert(kPart % 1024 == 0, "copied in whole wave instructions");
 };
 
 inline int64_t slots_of(const mamba_delta_dims* d, bool packed, int64_t unit) {

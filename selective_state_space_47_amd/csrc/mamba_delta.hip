@@ -10,9 +10,10 @@
 //
 // Rounding (bf16 storage): products take bf16 operands into fp32 accumulators.  What makes E and enters the
 // state by K^T E goes in as three bf16 parts (Y and c E: the fp32 value to 24 bits) or two (S, and T, which
-// is one on its diagonal and small off it): the state is within about 3e-7 of fp64.  The output takes E
-// as two parts, S and P as one: each rounds its own share of the output, so that together they weigh at
-// most as much as the output's own rounding.  fp32 storage uses fp32 matrix instructions throughout.
+// is one on its diagonal and small off it): the state is within about 3e-7 of fp64.  The output takes S, P
+// and E as two parts each (2^-17 of every product), so that its own rounding to bf16 is the only one that
+// shows; with S and P in one part its error was 1.4 to 1.8 times as large.  fp32 storage uses fp32 matrix
+// instructions throughout.
 #include "mamba_delta_scan.h"
 
 namespace mamba {
@@ -181,10 +182,10 @@ __global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kern
         float (&lo)[4] = p[kb * M::kTiles], (&hi)[4] = p[(kb + 1) * M::kTiles - 1];
         const int at = TriTile<E>::word_at(kb, i, g);
         const uint4 word = pack_word<E>(lo, hi);
-        *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kT + at) = word;
-        if (M::parts(2) > 1 && a.e_img) {
+        *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kP + at) = word;
+        if (M::parts(2) > 1) {
           subtract_word(lo, hi, word);
-          *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kPLow + at) = pack_word<E>(lo, hi);
+          *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kP + ChunkWs<E>::kPart + at) = pack_word<E>(lo, hi);
         }
       }
     __syncthreads();
@@ -255,7 +256,7 @@ __global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kern
 #pragma unroll
       for (int part = 0; part < M::parts(kTParts); ++part) {
         const uint4 word = pack_word<E>(lo, hi);
-        *reinterpret_cast<uint4*>(ws + part * TriTile<E>::kBytes +
+        *reinterpret_cast<uint4*>(ws + ChunkWs<E>::kT + part * ChunkWs<E>::kPart +
                                   TriTile<E>::word_at(kb, t, x & 3)) = word;
         if (sizeof(E) == 2) subtract_word(lo, hi, word);
       }
@@ -267,7 +268,7 @@ __global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kern
 
 template <typename E, int DK, int NW, Pass kPass>
 __global__ __launch_bounds__(kPassThreads) void scan_kernel(Args a, int32_t col_blocks) {
-  __shared__ __align__(1024) char smem[Stage<E, DK, NW>::kLds];
+  __shared__ __align__(1024) char smem[Stage<E, DK, NW, kPass>::kLds];
   scan_pass<E, DK, NW, kPass>(a, col_blocks, smem, blockIdx.x, gridDim.x);
 }
 

@@ -60,11 +60,11 @@ struct AdjStage {
   using VT = ValueTile<E, 16 * NW>;
   static constexpr int kK = 0;
   static constexpr int kQ = KeyTile<E, DK>::kBytes;
-  static constexpr int kWs = 2 * KeyTile<E, DK>::kBytes;  // T, P, gates
-  static constexpr int kP = kWs + ChunkWs<E>::kT;
+  static constexpr int kWs = 2 * KeyTile<E, DK>::kBytes;  // P, T, gates
+  static constexpr int kP = kWs + ChunkWs<E>::kP;
+  static constexpr int kT = kWs + ChunkWs<E>::kT;
   static constexpr int kGate = kWs + ChunkWs<E>::kGate;
-  static constexpr int kPLow = kWs + ChunkWs<E>::kDecay;
-  static constexpr int kDO = kPLow + (Mma<E>::parts(2) - 1) * TriTile<E>::kBytes;
+  static constexpr int kDO = kWs + ChunkWs<E>::kDecay;
   static constexpr int kBytes = kDO + VT::kBytes;
   static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
   static constexpr int kLds = kCount * kBytes;
@@ -121,7 +121,6 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
     ck(rows_buffer(kp + t * a.k_stride, n, a.k_stride, a.dk), to + St::kK, w);
     co(rows_buffer(dop + t * o_stride, n, o_stride, vcols), to + St::kDO, w);
     copy_linear<CW::kDecay, NW>(ws, to + St::kWs, w, lane);
-    if constexpr (kP2 == 2) copy_linear<CW::kP, NW>(ws + CW::kPLow, to + St::kPLow, w, lane);
     cq(rows_buffer(qp + t * a.q_stride, n, a.q_stride, a.dk), to + St::kQ, w);
   };
 
@@ -157,8 +156,8 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
       df[ib & 1] = ot.operand(sm + St::kDO, ib);
 #pragma unroll
       for (int m = 0; m < (ib + 1) * M::kTiles; ++m) {
-        pf[ib & 1][0][m] = tt.cols(sm + St::kP, m, ib);
-        if constexpr (kP2 == 2) pf[ib & 1][1][m] = tt.cols(sm + St::kPLow, m, ib);
+#pragma unroll
+        for (int p = 0; p < kP2; ++p) pf[ib & 1][p][m] = tt.cols(sm + St::kP + p * TT::kBytes, m, ib);
       }
     };
 #pragma unroll
@@ -190,7 +189,7 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
       for (int p = 0; p < kP2; ++p)
 #pragma unroll
         for (int m = 0; m < (ib + 1) * M::kTiles; ++m)
-          tf[ib & 1][p][m] = tt.cols(sm + St::kWs + p * TT::kBytes, m, ib);
+          tf[ib & 1][p][m] = tt.cols(sm + St::kT + p * TT::kBytes, m, ib);
     };
 #pragma unroll
     for (int ib = 0; ib < TT::kBlocks; ++ib) {
@@ -303,7 +302,7 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
 template <typename E, int DK, int NW>
 __global__ __launch_bounds__((sizeof(E) * DK <= 256 ? kPassThreads : 64 * NW)) void passes_kernel(
     BwdArgs b, int32_t col_blocks, uint32_t each) {
-  constexpr int kA = AdjStage<E, DK, NW>::kLds, kS = Stage<E, DK, NW>::kLds;
+  constexpr int kA = AdjStage<E, DK, NW>::kLds, kS = Stage<E, DK, NW, kBackward>::kLds;
   __shared__ __align__(1024) char smem[kA > kS ? kA : kS];
   if (blockIdx.x < each)
     adjoint_pass<E, DK, NW>(b, col_blocks, smem, blockIdx.x, each);
@@ -704,7 +703,7 @@ BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
   const size_t blocks = (size_t)BwdBlock<E>::blocks(d->dv);
   const size_t row = (d->dk <= 64 ? 64 : 128) * sizeof(E);
   BwdLayout l;
-  l.item = ChunkWs<E>::kBwdBytes;
+  l.item = ChunkWs<E>::kBytes;
   l.e = items * l.item;
   l.s = l.e + items * blocks * BwdBlock<E>::kEParts * BwdBlock<E>::kE;
   l.ds = l.s + items * blocks * BwdBlock<E>::kDB * row;
@@ -754,7 +753,6 @@ int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, 
   BwdArgs b = {};
   b.f = make_args(dims, scale, q, k, v, g, beta, initial_state, seq_offsets);
   b.f.ws = static_cast<char*>(workspace);
-  b.f.ws_item = l.item;
   b.f.e_img = b.f.ws + l.e;
   b.f.s_img = b.f.ws + l.s;
   b.f.ds_img = b.f.ws + l.ds;

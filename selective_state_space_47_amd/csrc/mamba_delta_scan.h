@@ -15,20 +15,6 @@
 namespace mamba {
 namespace delta {
 
-// One stage of a workgroup's LDS: the chunk's K and Q, the chunk's workspace image (T, P, gates) and V.
-template <typename E, int DK, int NW>
-struct Stage {
-  static constexpr int kK = 0;
-  static constexpr int kQ = KeyTile<E, DK>::kBytes;
-  static constexpr int kWs = 2 * KeyTile<E, DK>::kBytes;
-  static constexpr int kWsBytes = ChunkWs<E>::kDecay;
-  static constexpr int kGate = kWs + ChunkWs<E>::kGate;
-  static constexpr int kVv = kWs + kWsBytes;
-  static constexpr int kBytes = kVv + ValueTile<E, 16 * NW>::kBytes;
-  static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
-  static constexpr int kLds = kCount * kBytes;
-};
-
 // Threads that a pass is compiled for: 512 (256 registers each), though a workgroup of 4 waves could have 512
 // registers.  With no more than 256 the compiler keeps accumulators where vector instructions reach them;
 // otherwise a fifth of its vector instructions move values to and from the accumulation registers.
@@ -39,20 +25,39 @@ constexpr int kPassThreads = 512;
 // identity without values (dk more columns: the segment's map of the state before it).
 enum Pass { kOut, kBackward, kSummary };
 
+// One stage of a workgroup's LDS: the chunk's K and Q, what the pass reads of the chunk's workspace (P for an
+// output; T and gates) and V.
+template <typename E, int DK, int NW, Pass kPass>
+struct Stage {
+  using CW = ChunkWs<E>;
+  static constexpr int kK = 0;
+  static constexpr int kQ = KeyTile<E, DK>::kBytes;
+  static constexpr int kWs = 2 * KeyTile<E, DK>::kBytes;
+  static constexpr int kFrom = kPass == kOut ? CW::kP : CW::kT;
+  static constexpr int kWsBytes = CW::kDecay - kFrom;
+  static constexpr int kP = kWs + CW::kP - kFrom;
+  static constexpr int kT = kWs + CW::kT - kFrom;
+  static constexpr int kGate = kWs + CW::kGate - kFrom;
+  static constexpr int kVv = kWs + kWsBytes;
+  static constexpr int kBytes = kVv + ValueTile<E, 16 * NW>::kBytes;
+  static constexpr int kCount = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+  static constexpr int kLds = kCount * kBytes;
+};
+
 // The results of the backward's pass only enter gradients that are rounded to the storage type: with bf16
 // storage two parts of each factor keep them clear of those roundings, also where a sum of them cancels (dg).
 template <typename E, int DK, int NW, Pass kPass>
 __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, char* smem, uint32_t id,
                                           uint32_t grid) {
   using M = Mma<E>;
-  using St = Stage<E, DK, NW>;
+  using St = Stage<E, DK, NW, kPass>;
   using KT = KeyTile<E, DK>;
   using TT = TriTile<E>;
   using VT = ValueTile<E, 16 * NW>;
   constexpr bool kStates = kPass == kBackward, kO = kPass == kOut;
   constexpr int kPS = M::parts(2), kPT = M::parts(kTParts);
   constexpr int kPY = M::parts(kStates ? 2 : 3), kPE = M::parts(kStates ? 2 : 3);
-  constexpr int kPO = M::parts(2);  // of E in the output
+  constexpr int kPO = M::parts(2);  // of S, of P and of E in the output
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t wg = spread_index(id, grid, a.rep * col_blocks);
@@ -107,7 +112,7 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
     ck(rows_buffer(kp + t * a.k_stride, n, a.k_stride, a.dk), to + St::kK, w);
     cv(rows_buffer(vp + t * a.v_stride, n, a.v_stride, vcols), to + St::kVv, w);
     if (kO) cq(rows_buffer(qp + t * a.q_stride, n, a.q_stride, a.dk), to + St::kQ, w);
-    copy_linear<St::kWsBytes, NW>(a.ws + ((slot0 + ch) * a.hv + vh) * a.ws_item,
+    copy_linear<St::kWsBytes, NW>(a.ws + ((slot0 + ch) * a.hv + vh) * a.ws_item + St::kFrom,
                                   to + St::kWs, w, lane);
   };
 
@@ -190,23 +195,27 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
         for (int m = 0; m < 4; ++m) y[m] = M::mma(kf[kb & 1][m], s.p[p], y[m]);
       if constexpr (kO) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) o[m] = M::mma(s.p[0], qf[kb & 1][m], o[m]);
+        for (int p = 0; p < kPO; ++p)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) o[m] = M::mma(s.p[p], qf[kb & 1][m], o[m]);
       }
     }
     // Y = V - diag(exp G) K S;  O scaled by its token's factor
     step();
-    typename M::Frag tf[2][kPT][4], pf[2][4];
+    typename M::Frag tf[2][kPT][4], pf[2][kPO][4];
     auto read_t = [&](int kb) {
 #pragma unroll
       for (int p = 0; p < kPT; ++p)
 #pragma unroll
         for (int m = kb * M::kTiles; m < 4; ++m)
-          tf[kb & 1][p][m] = tt.rows(sm + St::kWs + p * TT::kBytes, m, kb);
+          tf[kb & 1][p][m] = tt.rows(sm + St::kT + p * TT::kBytes, m, kb);
     };
     auto read_p = [&](int kb) {
 #pragma unroll
-      for (int m = kb * M::kTiles; m < 4; ++m)
-        pf[kb & 1][m] = tt.rows(sm + St::kWs + ChunkWs<E>::kT, m, kb);
+      for (int p = 0; p < kPO; ++p)
+#pragma unroll
+        for (int m = kb * M::kTiles; m < 4; ++m)
+          pf[kb & 1][p][m] = tt.rows(sm + St::kP + p * TT::kBytes, m, kb);
     };
     read_t(0);
 #pragma unroll
@@ -291,7 +300,9 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
 #pragma unroll
         for (int p = 0; p < kPO; ++p)
 #pragma unroll
-          for (int m = kb * M::kTiles; m < 4; ++m) o[m] = M::mma(es.p[p], pf[kb & 1][m], o[m]);
+          for (int x = 0; x + p < kPO; ++x)
+#pragma unroll
+            for (int m = kb * M::kTiles; m < 4; ++m) o[m] = M::mma(es.p[x], pf[kb & 1][p][m], o[m]);
         step();
       }
       const auto buf = __builtin_amdgcn_make_buffer_rsrc(
