@@ -373,7 +373,8 @@ int mamba_delta_update(float* state, const void* q, const void* k, const void* v
 /* Bytes of device workspace mamba_delta_bwd needs (0 for invalid dims); packed as for
  * mamba_delta_workspace_bytes.  Beside the forward's it holds, per 64 tokens and value head, the state
  * before them, its adjoint after them and the e_t: with bf16 storage 3 + 4 bytes per value of the
- * (dk x dv) state and 4 per e_t (bf16 and what it leaves), with fp32 storage 4 each. */
+ * (dk x dv) state and 4 per e_t (bf16 and what it leaves), with fp32 storage 4 each; with bf16 storage also
+ * what bf16 leaves of dv. */
 size_t mamba_delta_bwd_workspace_bytes(const mamba_delta_dims* dims, int packed);
 
 /*

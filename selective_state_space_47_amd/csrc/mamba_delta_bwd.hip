@@ -19,10 +19,9 @@
 //                   chunk; laid out like the state's pass (16 columns per wave, in accumulators)
 //   grad_kernel     one workgroup per chunk and key head: everything else.  The value heads that share
 //                   the key head add their dQ and dK in accumulators, in a fixed order: no atomics.
-// Every gradient is rounded once.  Rounding inside, bf16 storage: two bf16 parts of every factor, except
-// S and dY where dQ and dK take them (one part each: their rounding weighs less than the gradient's).
-// dg and dbeta are sums of signed terms that may cancel many times over: those that weigh most, k . dS' e and
-// <dS', S>, take dS' as two parts and S to 17 bits (a byte beside its bf16).
+// Every gradient is rounded once.  Rounding inside, bf16 storage: two bf16 parts of every factor; S to 17 bits
+// (a byte beside its bf16).  One part of S and dY, which dQ, dK and the sums of dg take, cost up to 1.6 times the
+// error of rounding once where queries lie near their keys.
 #include "mamba_delta_scan.h"
 
 namespace mamba {
@@ -39,12 +38,19 @@ struct BwdArgs {
   void* dg;            // (tokens, hv)
   void* dbeta;
   float* ds0;          // (nseq, hv, dk, dv) or NULL
+  void* dy_low;        // bf16 storage: what bf16 leaves of dY, like dv
 };
 
 // 8 (bf16) or 4 (fp32) consecutive values from one operand's accumulators
 template <typename E>
 __device__ __forceinline__ void store_values(E* p, const f32x4* c) {
   *reinterpret_cast<typename Mma<E>::Frag*>(p) = Mma<E>::pack(c);
+}
+
+// what bf16 leaves of four values
+__device__ __forceinline__ f32x4 after_bf16(f32x4 v) {
+  const float2 a = unpack(pack_bf16(make_float2(v[0], v[1]))), b = unpack(pack_bf16(make_float2(v[2], v[3])));
+  return f32x4{v[0] - a.x, v[1] - a.y, v[2] - b.x, v[3] - b.y};
 }
 
 // sum over the four groups
@@ -97,6 +103,7 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
   const int64_t o_at = (sp.first * a.hv + vh) * (int64_t)a.dv;
   const E* dop = static_cast<const E*>(b.dout) + o_at + col0;
   E* dvp = static_cast<E*>(b.dv) + o_at + col;
+  E* low = static_cast<E*>(b.dy_low) + o_at + col;
   const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
   const bool has_col = col + r < a.dv;
 
@@ -245,13 +252,16 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
     }
     step();
     // token 16 m + r, columns col + 4 g .. +3
-    const auto buf = __builtin_amdgcn_make_buffer_rsrc(
-        dvp + ch * kC * o_stride, 0, (int)(((n - 1) * o_stride + max(a.dv - col, 0)) * (int64_t)sizeof(E)),
-        0x00020000);
+    const int bytes = (int)(((n - 1) * o_stride + max(a.dv - col, 0)) * (int64_t)sizeof(E));
+    const auto buf = __builtin_amdgcn_make_buffer_rsrc(dvp + ch * kC * o_stride, 0, bytes, 0x00020000);
+    const auto buf_low = __builtin_amdgcn_make_buffer_rsrc(low + ch * kC * o_stride, 0, bytes, 0x00020000);
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-      store_four<E>(buf, col + 4 * g < a.dv ? (uint32_t)((16 * m + r) * o_stride + 4 * g) * (uint32_t)sizeof(E)
-                                            : kOutside, yt[m]);
+    for (int m = 0; m < 4; ++m) {
+      const uint32_t to = col + 4 * g < a.dv ? (uint32_t)((16 * m + r) * o_stride + 4 * g) * (uint32_t)sizeof(E)
+                                             : kOutside;
+      store_four<E>(buf, to, yt[m]);
+      if constexpr (kP2 == 2) store_four<E>(buf_low, to, after_bf16(yt[m]));
+    }
     // dS = exp(G_64) dS' + Q^T diag(scale exp G) dO - K^T diag(exp G) dY
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -320,6 +330,10 @@ __device__ __forceinline__ float group_sum(float v) {
   v += dpp_row<0x121>(v);
   return v;
 }
+// every wave's LDS accesses are done (its copies may still be on their way)
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 // sum over lanes lane .. 63
 __device__ __forceinline__ float wave_suffix(float v, int lane) {
 #pragma unroll
@@ -333,30 +347,35 @@ __device__ __forceinline__ float wave_suffix(float v, int lane) {
 template <typename E, int DK>
 struct GradSmem {
   using B = BwdBlock<E>;
-  // one block of columns of the state: dO, dY, E, S, dS', and what bf16 leaves of the last two
+  // one block of columns of the state: dO, dY, E, S, dS', and what bf16 leaves of dY, S and dS'
   static constexpr int kDO = 0;
   static constexpr int kDY = kDO + B::kE;
   static constexpr int kE = kDY + B::kE;
   static constexpr int kS = kE + B::kEParts * B::kE;
   static constexpr int kDS = kS + B::kDB * KeyTile<E, DK>::kRow;
   static constexpr int kBlock = B::kDB * KeyTile<E, DK>::kRow;
-  static constexpr bool kLow = sizeof(E) == 2;  // what bf16 leaves of S (bytes) and dS'
+  static constexpr bool kLow = sizeof(E) == 2;
   static constexpr int kDSLow = kDS + kBlock;
-  static constexpr int kSLow = kDSLow + (kLow ? kBlock : 0);
-  static constexpr int kStage = kSLow + (kLow ? kBlock / 2 : 0);
+  static constexpr int kSLow = kDSLow + (kLow ? kBlock : 0);  // (of S: bytes)
+  static constexpr int kDYLow = kSLow + (kLow ? kBlock / 2 : 0);
+  static constexpr int kStage = kDYLow + (kLow ? B::kE : 0);
   static constexpr int kBParts = Mma<E>::parts(2);
   static constexpr int kK = 0;
   static constexpr int kQ = KeyTile<E, DK>::kBytes;
-  static constexpr int kB1 = 2 * KeyTile<E, DK>::kBytes;
-  static constexpr int kB2 = kB1 + kBParts * TriTile<E>::kBytes;
-  static constexpr int kGate = kB2 + kBParts * TriTile<E>::kBytes;  // gates and decays of two heads
-  static constexpr int kSums = kGate + 2 * 2048;                    // per wave: column sums
+  static constexpr int kSLowTile = 2 * KeyTile<E, DK>::kBytes;  // what bf16 leaves of the block's S, as bf16
+  // B1 and B2, after a head's last block: in its stage where there are two
+  static constexpr int kB = 2 * kBParts * TriTile<E>::kBytes;
+  static constexpr bool kBInStage = kLow;
+  static constexpr int kOwnB = kSLowTile + (kLow ? kBlock : 0);
+  static constexpr int kGate = kOwnB + (kBInStage ? 0 : kB);  // gates and decays of two heads
+  static constexpr int kSums = kGate + 2 * 2048;              // per wave: column sums
   static constexpr int kTok = kSums + 8 * 2 * kC * 4;               // per half and token: R + row sum of X,
                                                                     // then k . dS' e
   static constexpr int kDot = kTok + 4 * kC * 4;  // per wave: <dS', S>
   static constexpr int kStages = (kDot + 32 + 1023) / 1024 * 1024;
   static constexpr int kCount = kStages + 2 * kStage <= 160 * 1024 ? 2 : 1;
   static constexpr int kBytes = kStages + kCount * kStage;
+  static_assert(!kBInStage || (kCount == 2 && kB <= kStage), "a stage is free while the next block comes");
 };
 
 // Eight waves: wave (tile, half) has the tokens 16 tile .. 16 tile + 15.  Half 0 makes M and B1, half 1 N
@@ -409,6 +428,8 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
     const RowCopy<E, ET, kC, 4> co(tile, lane, o_stride, cols);
     co(rows_buffer(static_cast<const E*>(half ? b.dv : b.dout) + at, n, o_stride, cols),
        to + (half ? Sm::kDY : Sm::kDO), tile);
+    if constexpr (Sm::kLow)
+      if (!half) co(rows_buffer(static_cast<const E*>(b.dy_low) + at, n, o_stride, cols), to + Sm::kDYLow, tile);
     constexpr int kBlock = Sm::kBlock;
     copy_linear<BB::kEParts * BB::kE, 8>(
         a.e_img + item * e_bytes + (int64_t)db * BB::kEParts * BB::kE, to + Sm::kE, w, lane);
@@ -460,6 +481,33 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
       if (h + db > 0) copies_done();
       if (Sm::kCount == 2 && more) copy(nh, nb, st ^ 1);
       const lds_ptr bl = sm + Sm::kStages + st * Sm::kStage;
+      // <dS', S>, and what bf16 leaves of S from its bytes to operands
+      for (int x = threadIdx.x; x < Sm::kBlock / 16; x += 512) {
+        const auto s = lds_read<typename M::Frag>(bl + Sm::kS + 16 * x);
+        const auto d = lds_read<typename M::Frag>(bl + Sm::kDS + 16 * x);
+        if constexpr (Sm::kLow) {
+          typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+          typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+          const u32x4 sw = __builtin_bit_cast(u32x4, s);
+          const u32x2 lw = lds_read<u32x2>(bl + Sm::kSLow + 8 * x);
+          const auto dl = lds_read<typename M::Frag>(bl + Sm::kDSLow + 16 * x);
+          float sl[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const uint32_t high = y & 1 ? sw[y >> 1] & 0xffff0000u : sw[y >> 1] << 16;
+            const float whole = with_low(high, lw[y >> 2], y & 3);
+            dot = fmaf(whole, (float)d[y] + (float)dl[y], dot);
+            sl[y] = whole - __uint_as_float(high);  // (7 bits and a sign: exact as bf16)
+          }
+          *reinterpret_cast<uint4*>(smem + Sm::kSLowTile + 16 * x) =
+              make_uint4(pack_bf16(make_float2(sl[0], sl[1])), pack_bf16(make_float2(sl[2], sl[3])),
+                         pack_bf16(make_float2(sl[4], sl[5])), pack_bf16(make_float2(sl[6], sl[7])));
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) dot = fmaf((float)s[y], (float)d[y], dot);
+        }
+      }
+      if constexpr (Sm::kLow) lds_barrier();
 #pragma unroll
       for (int kb = 0; kb < BB::kDB / M::kDepth; ++kb) {
         const auto of = et.rows(bl + Sm::kDO, tile, kb), yf = et.rows(bl + Sm::kDY, tile, kb);
@@ -473,6 +521,14 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
 #pragma unroll
             for (int p = 0; p < BB::kEParts; ++p)
               mn[jt] = M::mma(et.rows(bl + Sm::kE + p * BB::kE, jt, kb), xf, mn[jt]);
+        typename M::Frag yl{};
+        if constexpr (Sm::kLow) {
+          yl = et.rows(bl + Sm::kDYLow, tile, kb);
+          if (half)
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+              if (jt <= tile) mn[jt] = M::mma(et.rows(bl + Sm::kE, jt, kb), yl, mn[jt]);
+        }
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
           const auto sf = kt.template cols<true>(bl + Sm::kS, m0 + m, kb);
@@ -481,26 +537,13 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
           sdy[m] = M::mma(sf, yf, sdy[m]);
 #pragma unroll
           for (int p = 0; p < BB::kEParts; ++p) dse[m] = M::mma(df, ef[p], dse[m]);
-          if constexpr (Sm::kLow)
+          if constexpr (Sm::kLow) {
             dse[m] = M::mma(kt.template cols<true>(bl + Sm::kDSLow, m0 + m, kb), ef[0], dse[m]);
-        }
-      }
-      for (int x = threadIdx.x; x < Sm::kBlock / 16; x += 512) {
-        const auto s = lds_read<typename M::Frag>(bl + Sm::kS + 16 * x);
-        const auto d = lds_read<typename M::Frag>(bl + Sm::kDS + 16 * x);
-        if constexpr (Sm::kLow) {
-          typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-          typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-          const u32x4 sw = __builtin_bit_cast(u32x4, s);
-          const u32x2 lw = lds_read<u32x2>(bl + Sm::kSLow + 8 * x);
-          const auto dl = lds_read<typename M::Frag>(bl + Sm::kDSLow + 16 * x);
-#pragma unroll
-          for (int y = 0; y < 8; ++y)
-            dot = fmaf(with_low(y & 1 ? sw[y >> 1] & 0xffff0000u : sw[y >> 1] << 16, lw[y >> 2], y & 3),
-                       (float)d[y] + (float)dl[y], dot);
-        } else {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) dot = fmaf((float)s[y], (float)d[y], dot);
+            const auto sl = kt.template cols<true>(sm + Sm::kSLowTile, m0 + m, kb);
+            sdo[m] = M::mma(sl, of, sdo[m]);
+            sdy[m] = M::mma(sl, yf, sdy[m]);
+            sdy[m] = M::mma(sf, yl, sdy[m]);
+          }
         }
       }
       if (Sm::kCount == 2) {
@@ -512,6 +555,9 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
     }
     const lds_ptr gate = sm + Sm::kGate + (h & 1) * 2048, decay = gate + 1024;
     // B1 or B2, and the sums that reach dbeta and dg
+    const int b1 = Sm::kBInStage ? Sm::kStages + (st ^ 1) * Sm::kStage : Sm::kOwnB;
+    const int b2 = b1 + kBP * TT::kBytes;
+    if (Sm::kBInStage) lds_barrier();  // every wave has read the last block
     float row_x = 0.f;
     {
       const float gi = lds_read<float>(decay + 4 * i), gil = lds_read<float>(decay + 4 * (kC + i));
@@ -552,7 +598,7 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
           const auto f = M::template split<kBP>(&bx[kb * M::kTiles]);
 #pragma unroll
           for (int p = 0; p < kBP; ++p)
-            *reinterpret_cast<typename M::Frag*>(smem + (half ? Sm::kB2 : Sm::kB1) + p * TT::kBytes +
+            *reinterpret_cast<typename M::Frag*>(smem + (half ? b2 : b1) + p * TT::kBytes +
                                                  TT::word_at(kb, i, g)) = f.p[p];
         }
     }
@@ -587,8 +633,7 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
       for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
       if (lane == 0) reinterpret_cast<float*>(smem + Sm::kDot)[w] = dot;
     }
-    // B1 and B2 are whole.  (Not a full barrier of the copies: the next block's are on their way.)
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    lds_barrier();  // B1 and B2 are whole
     // sums over j (rows i of B1, B2), then over i (their columns)
 #pragma unroll
     for (int kb = 0; kb < TT::kBlocks; ++kb) {
@@ -596,8 +641,8 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
         typename M::Frag f1[kBP], f2[kBP];
 #pragma unroll
         for (int p = 0; p < kBP; ++p) {
-          f1[p] = tt.rows(sm + Sm::kB1 + p * TT::kBytes, tile, kb);
-          f2[p] = tt.rows(sm + Sm::kB2 + p * TT::kBytes, tile, kb);
+          f1[p] = tt.rows(sm + b1 + p * TT::kBytes, tile, kb);
+          f2[p] = tt.rows(sm + b2 + p * TT::kBytes, tile, kb);
         }
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
@@ -613,8 +658,8 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
         typename M::Frag f1[kBP], f2[kBP];
 #pragma unroll
         for (int p = 0; p < kBP; ++p) {
-          f1[p] = tt.cols(sm + Sm::kB1 + p * TT::kBytes, tile, kb);
-          f2[p] = tt.cols(sm + Sm::kB2 + p * TT::kBytes, tile, kb);
+          f1[p] = tt.cols(sm + b1 + p * TT::kBytes, tile, kb);
+          f2[p] = tt.cols(sm + b2 + p * TT::kBytes, tile, kb);
         }
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
@@ -695,7 +740,7 @@ int launch_bwd(const BwdArgs& b, hipStream_t s) {
 }
 
 struct BwdLayout {  // workspace regions in bytes
-  size_t item, e, s, ds, s_low, ds_low, total;
+  size_t item, e, s, ds, s_low, ds_low, dy_low, total;
 };
 template <typename E>
 BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
@@ -710,7 +755,10 @@ BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
   const size_t img = items * blocks * BwdBlock<E>::kDB * row, low = sizeof(E) == 2 ? img : 0;
   l.s_low = l.ds + img;
   l.ds_low = l.s_low + low / 2;
-  l.total = l.ds_low + low;
+  l.dy_low = l.ds_low + low;
+  l.total = l.dy_low;
+  if (sizeof(E) == 2)
+    l.total += (size_t)(packed ? d->seqlen : d->batch * d->seqlen) * (size_t)(d->v_heads * d->dv) * sizeof(E);
   return l;
 }
 BwdLayout layout(const mamba_delta_dims* d, bool packed) {
@@ -758,6 +806,7 @@ int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, 
   b.f.ds_img = b.f.ws + l.ds;
   b.f.s_low = b.f.ws + l.s_low;
   b.f.ds_low = b.f.ws + l.ds_low;
+  b.dy_low = b.f.ws + l.dy_low;
   b.dout = dout;
   b.dlast = dlast;
   b.dq = dq;

@@ -14,6 +14,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import delta
 from selective_state_space_47_amd import _build, binding, synth
 from tests.test_gpu_delta import BF, DEV, case, ref_fwd, run_fwd
 
@@ -61,3 +62,20 @@ def test_output(heads, aligned):
     for state in (None, "state"):
         out, _ = run_fwd(t, initial_state=state and t[state])
         check(out, ref_fwd(x, heads[2] ** -0.5, state and x[state])[0], f"out, {state}")
+
+
+@pytest.mark.parametrize("aligned", [False, True], ids=["random", "aligned"])
+@pytest.mark.parametrize("heads", HEADS, ids=lambda h: "x".join(map(str, h)))
+def test_gradients(heads, aligned):
+    """Gradients of the outputs alone, with a state and without.  dg and dbeta are sums whose terms cancel in part:
+    ten times 2 d is 0.36 of one rounding, and they are allowed 1.4 of it."""
+    x, t = inputs(heads, aligned)
+    for state in (None, "state"):
+        print(f"[delta rounding] gradients {heads} aligned={aligned} state={state}", flush=True)
+        args = ("q", "k", "v", "g", "beta", "dout")
+        got = binding.mamba_delta_bwd(*(t[m] for m in args), initial_state=state and t[state])
+        ref = delta.delta_bwd_ref(*(x[m] for m in args[:5]), heads[2] ** -0.5, x["dout"], state and x[state])
+        for name in ("dq", "dk", "dv"):
+            check(got[name], ref[name], name)
+        for name in ("dg", "dbeta"):
+            check(got[name], ref[name], name, 1.4)
