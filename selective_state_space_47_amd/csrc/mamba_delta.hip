@@ -15,6 +15,7 @@
 // shows; with S and P in one part its error was 1.4 to 1.8 times as large.  fp32 storage uses fp32 matrix
 // instructions throughout.
 #include "mamba_delta_scan.h"
+#include "mamba_grid.h"
 
 namespace mamba {
 namespace delta {
@@ -267,9 +268,10 @@ __global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kern
 // ------------------------------------------------------------------ the state through the chunks
 
 template <typename E, int DK, int NW, Pass kPass>
-__global__ __launch_bounds__(kPassThreads) void scan_kernel(Args a, int32_t col_blocks) {
+__global__ __launch_bounds__(kPassThreads) void scan_kernel(Args a, int32_t col_blocks, uint32_t blocks) {
   __shared__ __align__(1024) char smem[Stage<E, DK, NW, kPass>::kLds];
-  scan_pass<E, DK, NW, kPass>(a, col_blocks, smem, blockIdx.x, gridDim.x);
+  const uint32_t id = wide_index();
+  if (id < blocks) scan_pass<E, DK, NW, kPass>(a, col_blocks, smem, id, blocks);
 }
 
 // The states before the segments, one after another: S <- map S + (the segment's own).  A workgroup has 16
@@ -363,8 +365,9 @@ template <typename E, int DK, int NW, Pass kPass>
 int launch_scan_t(const Args& a, hipStream_t s) {
   const int cols = (a.dv + 16 * NW - 1) / (16 * NW) +
                    (kPass == kSummary ? (a.dk + 16 * NW - 1) / (16 * NW) : 0);
-  hipLaunchKernelGGL((scan_kernel<E, DK, NW, kPass>), dim3((unsigned)(a.seg_slots * a.hv * cols)),
-                     dim3(64 * NW), 0, s, a, cols);
+  const uint32_t blocks = (uint32_t)(a.seg_slots * a.hv * cols);
+  hipLaunchKernelGGL((scan_kernel<E, DK, NW, kPass>), wide_grid(blocks, 64 * NW), dim3(64 * NW), 0, s, a, cols,
+                     blocks);
   return launch_status();
 }
 

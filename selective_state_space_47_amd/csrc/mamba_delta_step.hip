@@ -1,5 +1,6 @@
 // mamba_delta_step.hip -- one generation step of the gated delta rule on gfx950 (formulas in mamba_delta.h).
 #include "mamba_delta.h"
+#include "mamba_grid.h"
 
 namespace mamba {
 namespace delta {
@@ -16,6 +17,7 @@ struct StepArgs {
   const void* beta;
   void* out;
   int64_t q_stride, k_stride, v_stride;
+  int64_t heads;  // sequences x hv
   int32_t hv, rep, dk, dv;
   float scale;
 };
@@ -34,10 +36,12 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(StepArgs a, int32_t 
   __shared__ float red[kStepThreads / 64][2][4 * TC];
   __shared__ float skq[2];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t sh = blockIdx.x / col_blocks;
+  const uint32_t wg = wide_index();
+  const int64_t sh = wg / (uint32_t)col_blocks;
+  if (sh >= a.heads) return;
   const int64_t seq = sh / a.hv;
   const int vh = (int)(sh - seq * a.hv), kh = vh / a.rep;
-  const int c = (int)(blockIdx.x - sh * col_blocks) * 4 * TC + tid % TC * 4;
+  const int c = (int)(wg - sh * col_blocks) * 4 * TC + tid % TC * 4;
   const int row0 = tid / TC;
   float* sp = a.state + sh * (int64_t)a.dk * a.dv + c;
   const bool live = c < a.dv;
@@ -119,9 +123,9 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(StepArgs a, int32_t 
 }
 
 template <typename E>
-int launch_step(const StepArgs& a, int64_t heads, hipStream_t s) {
+int launch_step(const StepArgs& a, hipStream_t s) {
   const int64_t blocks = (a.dv + 31) / 32;
-  hipLaunchKernelGGL((step_kernel<E>), dim3((unsigned)(heads * blocks)), dim3(kStepThreads), 0, s, a,
+  hipLaunchKernelGGL((step_kernel<E>), wide_grid(a.heads * blocks, kStepThreads), dim3(kStepThreads), 0, s, a,
                      (int32_t)blocks);
   return launch_status();
 }
@@ -146,10 +150,9 @@ int mamba_delta_update(float* state, const void* q, const void* k, const void* v
   if (!aligned(out, dims->io_dtype == MAMBA_BF16 ? 2 : 4)) return MAMBA_ERR_ALIGN;
   const Args d = make_args(dims, scale, q, k, v, g, beta, nullptr, nullptr);
   StepArgs a = {state, q, k, v, g, beta, out, d.q_stride, d.k_stride, d.v_stride,
-                d.hv, d.rep, d.dk, d.dv, scale};
+                dims->batch * dims->v_heads, d.hv, d.rep, d.dk, d.dv, scale};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dims->io_dtype == MAMBA_BF16 ? launch_step<uint16_t>(a, dims->batch * dims->v_heads, s)
-                                      : launch_step<float>(a, dims->batch * dims->v_heads, s);
+  return dims->io_dtype == MAMBA_BF16 ? launch_step<uint16_t>(a, s) : launch_step<float>(a, s);
 }
 
 }  // extern "C"

@@ -23,6 +23,7 @@
 //   (4.6 TB/s) and 9 us
 // 256 rows of 40 groups, or one row of 768: 3 to 4 us, latency.
 #include "mamba_common.h"
+#include "mamba_grid.h"
 
 namespace mamba {
 namespace {
@@ -273,9 +274,9 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_kernel(GatedArgs a, uint
   __shared__ float slot[2][kBlock<T> / 64][2];
   TeamSum<T, float> team_sum{slot};
   const Cols<T, R> cols{(int)(threadIdx.x % T), a.dim};
-  const uint32_t u = blockIdx.x * (kBlock<T> / T) + threadIdx.x / T;
+  const uint64_t u = (uint64_t)wide_index() * (kBlock<T> / T) + threadIdx.x / T;
   const bool live = u < units;
-  const Unit at = unit_of(a, live ? u : 0);
+  const Unit at = unit_of(a, live ? (uint32_t)u : 0);
   float y[R][8], z[R][8], w[R][8];
   cols.load(static_cast<const E*>(a.y) + at.row * a.y_stride + (int64_t)at.grp * a.dim, y, live);
   if (a.z)
@@ -414,7 +415,7 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_kernel(AddArgs a) {
   __shared__ float slot[2][kBlock<T> / 64][2];
   TeamSum<T, float> team_sum{slot};
   const Cols<T, R> cols{(int)(threadIdx.x % T), a.dim};
-  const int64_t row = (int64_t)blockIdx.x * (kBlock<T> / T) + threadIdx.x / T;
+  const int64_t row = (int64_t)wide_index() * (kBlock<T> / T) + threadIdx.x / T;
   const bool live = row < a.rows;
   const int64_t at = (live ? row : 0) * a.dim;
   float x[R][8], q[R][8], p[R][8];
@@ -705,7 +706,7 @@ struct GatedFwd {
   int operator()() const {
     const uint32_t units = gated_units(a), teams = kBlock<T> / T;
     hipLaunchKernelGGL((gated_norm_kernel<E, T, R>),
-                       dim3((units + teams - 1) / teams, a.per_group ? a.groups : 1),
+                       wide_grid((units + teams - 1) / teams, kBlock<T>, a.per_group ? a.groups : 1),
                        dim3(kBlock<T>), 0, s, a, units);
     return launch_status();
   }
@@ -729,7 +730,7 @@ struct AddFwd {
   template <int T, int R>
   int operator()() const {
     const int64_t teams = kBlock<T> / T;
-    hipLaunchKernelGGL((add_norm_kernel<E, S, T, R>), dim3((unsigned)((a.rows + teams - 1) / teams)),
+    hipLaunchKernelGGL((add_norm_kernel<E, S, T, R>), wide_grid((a.rows + teams - 1) / teams, kBlock<T>),
                        dim3(kBlock<T>), 0, s, a);
     return launch_status();
   }
