@@ -209,6 +209,10 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
   return __builtin_amdgcn_rcpf(1.f + fast_exp2(-z * kLog2e));
 }
 
+// The gradients' statistics are 1 / (mean + eps) in fp64, and zero for a team without a unit, whose zeros would
+// make them infinite where eps is zero and leave NaN in the weights' sums.  Their root is taken in fp64 too, as an
+// eps below 3e-39 takes them out of fp32's range.
+
 // dh - v m: what is left of dh when its part along v is taken out.  Next to nothing is left where a
 // unit has few values or dh is nearly parallel to v, so that m comes from sums in fp64 and the difference
 // is taken there (fp64 fused multiply-adds run at the rate of unpacked fp32 ones on this target).
@@ -362,8 +366,8 @@ __global__ __launch_bounds__(kBlock<T>) void gated_norm_bwd_kernel(GatedArgs a, 
         s[1] = fma((double)dh, (double)v, s[1]);
       }
     team_sum(s);
-    const double r2 = 1.0 / fma(s[0], inv, (double)a.eps), m = s[1] * r2 * inv;
-    const float rs = sqrtf((float)r2);
+    const double r2 = live ? 1.0 / fma(s[0], inv, (double)a.eps) : 0.0, m = s[1] * r2 * inv;
+    const float rs = (float)sqrt(r2);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -521,9 +525,9 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[0] = fma((double)x[r][k], (double)x[r][k], s[0]);
       team_sum(s);
-      rx2 = 1.0 / fma(s[0], inv, (double)a.eps);
+      rx2 = live ? 1.0 / fma(s[0], inv, (double)a.eps) : 0.0;
     }
-    const float rx = sqrtf((float)rx2);  // the normed x is x rx
+    const float rx = (float)sqrt(rx2);  // the normed x is x rx
     double s[2] = {0.0, 0.0};
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -534,8 +538,8 @@ __global__ __launch_bounds__(kBlock<T>) void add_norm_bwd_kernel(AddArgs a) {
         s[1] = fma((double)(d[r][k] * w[r][k]), (double)v[r][k], s[1]);
       }
     team_sum(s);
-    const double r2 = 1.0 / fma(s[0], inv, (double)a.eps), m = s[1] * r2 * inv;
-    const float rs = sqrtf((float)r2);
+    const double r2 = live ? 1.0 / fma(s[0], inv, (double)a.eps) : 0.0, m = s[1] * r2 * inv;
+    const float rs = (float)sqrt(r2);
     // v = dr.  With h the normed x, dscale = sum(dr post h) and dpost = sum(dr scale h): the other factor is
     // constant per column, so that both come from one sum.
 #pragma unroll
