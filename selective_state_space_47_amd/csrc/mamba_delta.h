@@ -368,7 +368,7 @@ struct Args {
   // long sequences in segments of seg_chunks chunks (0: one segment per sequence)
   int64_t seg_chunks;
   int64_t seg_slots;
-  float* seg_state;        // (segment slots, hv, dk, dv): the state before each segment but the first
+  float* seg_state;        // (segment slots, hv, dk, dv): the state before each segment
   float* seg_map;          // (segment slots, hv, dk, dk): what a segment does to the state before it
   int32_t hk, hv, rep, dk, dv;
   float scale;

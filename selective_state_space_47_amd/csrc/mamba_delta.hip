@@ -276,8 +276,9 @@ __global__ __launch_bounds__(kPassThreads) void scan_kernel(Args a, int32_t col_
 
 // The states before the segments, one after another: S <- map S + (the segment's own).  A workgroup has 16
 // columns, its waves 16 rows each; fp32 matrix instructions, S handed round through LDS.  Bound by that chain:
-// 62 us of the 720 that 65536 tokens x 12 heads of 128 take.  seg_state holds
-// each segment's own result on entry and the state before it on return.
+// 62 us of the 720 that 65536 tokens x 12 heads of 128 take.  seg_state holds each segment's own result on
+// entry and the state before it on return, the first segment's (of sequences without tokens, too) being a copy
+// of the initial state: the output pass reads only these, as it may write the last state over the initial one.
 template <int DK>
 __global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_blocks) {
   using M = Mma<float>;
@@ -320,12 +321,18 @@ __global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_bl
     for (int x = 0; x < 4; ++x)
       S[x] = a.s0[((seq * a.hv + vh) * (int64_t)a.dk + row0 + x) * a.dv + col];
   f32x4 own[2] = {S, S};
+  auto store = [&](int64_t s) {
+    if (has_col && row0 < a.dk)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) state(base + s)[(int64_t)x * a.dv] = S[x];
+  };
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     if (i + 1 < nseg) {
       load_map(i, map[i]);
       own[i] = load_own(i);
     }
+  store(0);
   for (int64_t s0 = 0; s0 + 1 < nseg; s0 += 2) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -344,9 +351,7 @@ __global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_bl
         load_map(s + 2, map[i]);
         own[i] = load_own(s + 2);
       }
-      if (has_col && row0 < a.dk)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) state(base + s + 1)[(int64_t)x * a.dv] = S[x];
+      store(s + 1);
     }
   }
 }

@@ -89,7 +89,7 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
   // (dk, width) matrices of this head: the sequence's states, and this segment's
   const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
   const int64_t g_at = (seg_slot * a.hv + vh) * (int64_t)a.dk * width + col + r;
-  const float* from = kPass == kSummary ? nullptr : seg ? a.seg_state + g_at : a.s0 ? a.s0 + s_at : nullptr;
+  const float* from = kPass == kSummary ? nullptr : a.seg_chunks ? a.seg_state + g_at : a.s0 ? a.s0 + s_at : nullptr;
 
   f32x4 S[DK / 16];
 #pragma unroll
