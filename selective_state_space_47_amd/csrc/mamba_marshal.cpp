@@ -20,8 +20,8 @@ void put(std::string& s, T v) {
 }
 
 // key(*args) -> bytes.  Two argument lists with the same key have the same types, shapes, strides, devices
-// and small values; only addresses and contents differ.
-PyObject* key(PyObject*, PyObject* const* args, Py_ssize_t n) {
+// and small values; only addresses and contents differ.  A tensor without sizes or strides (a nested one) raises.
+PyObject* key(PyObject*, PyObject* const* args, Py_ssize_t n) try {
   std::string s;
   s.reserve(64 * n);
   for (Py_ssize_t i = 0; i < n; ++i) {
@@ -54,6 +54,12 @@ PyObject* key(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
   }
   return PyBytes_FromStringAndSize(s.data(), (Py_ssize_t)s.size());
+} catch (const c10::Error& e) {  // (not torch's macro around it: that has a cost where nothing is thrown)
+  PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+  return nullptr;
+} catch (const std::exception& e) {
+  PyErr_SetString(PyExc_RuntimeError, e.what());
+  return nullptr;
 }
 
 void* address(PyObject* o) {
