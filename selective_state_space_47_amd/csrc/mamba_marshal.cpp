@@ -20,7 +20,8 @@ void put(std::string& s, T v) {
 }
 
 // key(*args) -> bytes.  Two argument lists with the same key have the same types, shapes, strides, devices
-// and small values; only addresses and contents differ.  A tensor without sizes or strides (a nested one) raises.
+// and small values; only addresses and contents differ.  A tensor without sizes or strides (a nested one)
+// raises, and so does one whose values are not those in its memory.
 PyObject* key(PyObject*, PyObject* const* args, Py_ssize_t n) try {
   std::string s;
   s.reserve(64 * n);
@@ -33,6 +34,10 @@ PyObject* key(PyObject*, PyObject* const* args, Py_ssize_t n) try {
       if (t.layout() != at::kStrided) {
         s += 'L';  // (the checks refuse it: it has no strides)
         continue;
+      }
+      if (t.is_neg()) {
+        PyErr_SetString(PyExc_ValueError, "a tensor of the call is a lazily negated view: pass its resolve_neg()");
+        return nullptr;
       }
       s += 'T';
       put(s, (int8_t)t.scalar_type());

@@ -2,6 +2,11 @@
 import subprocess
 import sys
 
+import pytest
+import torch
+
+from selective_state_space_47_amd import binding
+
 CODE = """
 import warnings
 warnings.simplefilter("ignore")
@@ -27,3 +32,16 @@ def test_nested_tensor_is_refused():
     r = subprocess.run([sys.executable, "-c", CODE], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.split() == ["refused", "refused"]
+
+
+def test_negated_view_is_refused():
+    """Its memory holds the values with the other sign, which its sizes, strides and type do not tell."""
+    m = binding._marshal()
+    x = torch.randn(4, 1, 1, dtype=torch.complex64)
+    for t in (x.conj().imag, torch._neg_view(torch.zeros(4, 1, 8))):
+        assert t.is_neg()
+        with pytest.raises(ValueError, match="resolve_neg"):
+            m.key(1, t)
+        with pytest.raises(ValueError, match="resolve_neg"):
+            binding.mamba_gated_norm_fwd(t, None, torch.ones(t.shape[-1]))
+        assert m.key(1, t.resolve_neg()) == m.key(1, torch.zeros(t.shape))
