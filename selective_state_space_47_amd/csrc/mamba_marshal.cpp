@@ -125,6 +125,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   int st = 0;
+  // (a launch waits where the queue is full: other Python threads go on meanwhile)
+  Py_BEGIN_ALLOW_THREADS
   switch (entry) {
     case kDeltaFwd:
       st = mamba_delta_fwd(p[0], p[1], p[2], p[3], p[4], fp(5), static_cast<int64_t*>(p[6]), f, p[7], fp(8),
@@ -155,6 +157,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
                               static_cast<mamba_add_norm_dims*>(d), p[12], ws, stream);
       break;
   }
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
 
