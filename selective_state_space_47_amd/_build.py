@@ -38,6 +38,7 @@ def build_marshal() -> str:
     tmp = MARSHAL_PATH + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           '-DMAMBA_TORCH_VERSION="%s"' % torch.__version__,
            "-I", INCLUDE, "-I", os.path.join(torch_dir, "include"),
            "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "mamba_marshal.cpp"),

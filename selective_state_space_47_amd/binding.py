@@ -643,6 +643,11 @@ def _marshal():
             spec = importlib.util.spec_from_file_location("mamba_marshal", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
+            if module.torch_version != torch.__version__:  # it reads torch's own structures
+                raise RuntimeError(
+                    f"native module {path} was built for torch {module.torch_version}, this is "
+                    f"{torch.__version__}: build it again with "
+                    "`python -c 'import __graft_entry__ as g; g.build()'`")
             _MARSHAL = module
     return _MARSHAL
 

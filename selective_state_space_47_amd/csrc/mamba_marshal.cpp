@@ -171,4 +171,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "mamba_marshal", nullptr, -1, kMet
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_mamba_marshal(void) { return PyModule_Create(&kModule); }
+// torch_version: of the headers that this was compiled against, which the binding compares with the torch it has
+PyMODINIT_FUNC PyInit_mamba_marshal(void) {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "torch_version", MAMBA_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}

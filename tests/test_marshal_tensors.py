@@ -45,3 +45,11 @@ def test_negated_view_is_refused():
         with pytest.raises(ValueError, match="resolve_neg"):
             binding.mamba_gated_norm_fwd(t, None, torch.ones(t.shape[-1]))
         assert m.key(1, t.resolve_neg()) == m.key(1, torch.zeros(t.shape))
+
+
+def test_module_built_for_another_torch_is_refused(monkeypatch):
+    assert binding._marshal().torch_version == torch.__version__
+    monkeypatch.setattr(binding, "_MARSHAL", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with pytest.raises(RuntimeError, match="built for torch"):
+        binding._marshal()
