@@ -11,7 +11,8 @@
 //     dg_t = exp(G_64) <dS', S> + sum_{j < t} Z_j + sum_{i >= t} R_i + sum_{i >= t > j} X_ij,
 //         Z_j = c_j k_j . dS' e_j,  X_ij = B1_ij (q_i . k_j) + B2_ij (k_i . k_j)
 //         R_i = exp(G_i) (scale q_i . S dO_i - k_i . S dY_i)
-// (the last sums leave out every pair that cancels: the decay of token t only weighs what crosses it).
+// The last sum is that of the rows i >= t of X less that of its columns j >= t, whose common pairs cancel: they are
+// added in fp64, so that nothing of them is left where a strong decay makes the pairs that cross t small.
 //
 // Three launches: the chunk products of mamba_delta.hip, then
 //   passes_kernel   the state forwards through the chunks (mamba_delta_scan.h; it leaves E and the state before
@@ -54,7 +55,8 @@ __device__ __forceinline__ f32x4 after_bf16(f32x4 v) {
 }
 
 // sum over the four groups
-__device__ __forceinline__ float across_groups(float v) {
+template <typename V>
+__device__ __forceinline__ V across_groups(V v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
@@ -334,11 +336,27 @@ __device__ __forceinline__ float group_sum(float v) {
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
+// the same in fp64
+template <int kCtrl>
+__device__ __forceinline__ double dpp_row64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __float_as_uint(dpp_row<kCtrl>(__uint_as_float((uint32_t)b)));
+  const uint32_t hi = __float_as_uint(dpp_row<kCtrl>(__uint_as_float((uint32_t)(b >> 32))));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double group_sum(double v) {
+  v += dpp_row64<0x128>(v);
+  v += dpp_row64<0x124>(v);
+  v += dpp_row64<0x122>(v);
+  v += dpp_row64<0x121>(v);
+  return v;
+}
 // sum over lanes lane .. 63
-__device__ __forceinline__ float wave_suffix(float v, int lane) {
+template <typename V>
+__device__ __forceinline__ V wave_suffix(V v, int lane) {
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) {
-    const float t = __shfl_down(v, m);
+    const V t = __shfl_down(v, m);
     if (lane + m < 64) v += t;
   }
   return v;
@@ -368,10 +386,11 @@ struct GradSmem {
   static constexpr bool kBInStage = kLow;
   static constexpr int kOwnB = kSLowTile + (kLow ? kBlock : 0);
   static constexpr int kGate = kOwnB + (kBInStage ? 0 : kB);  // gates and decays of two heads
-  static constexpr int kSums = kGate + 2 * 2048;              // per wave: column sums
-  static constexpr int kTok = kSums + 8 * 2 * kC * 4;               // per half and token: R + row sum of X,
-                                                                    // then k . dS' e
-  static constexpr int kDot = kTok + 4 * kC * 4;  // per wave: <dS', S>
+  static constexpr int kSumX = kGate + 2 * 2048;  // per wave and column: sum of X (fp64)
+  static constexpr int kSumB = kSumX + 8 * kC * 8;  // and for dbeta
+  static constexpr int kRowX = kSumB + 8 * kC * 4;  // per half and token: row sum of X (fp64),
+  static constexpr int kTok = kRowX + 2 * kC * 8;   // R, then k . dS' e
+  static constexpr int kDot = kTok + 4 * kC * 4;    // per wave: <dS', S>
   static constexpr int kStages = (kDot + 32 + 1023) / 1024 * 1024;
   static constexpr int kCount = kStages + 2 * kStage <= 160 * 1024 ? 2 : 1;
   static constexpr int kBytes = kStages + kCount * kStage;
@@ -558,11 +577,13 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
     const int b1 = Sm::kBInStage ? Sm::kStages + (st ^ 1) * Sm::kStage : Sm::kOwnB;
     const int b2 = b1 + kBP * TT::kBytes;
     if (Sm::kBInStage) lds_barrier();  // every wave has read the last block
-    float row_x = 0.f;
     {
+      double row_x = 0.0;
       const float gi = lds_read<float>(decay + 4 * i), gil = lds_read<float>(decay + 4 * (kC + i));
       const float sign = half ? -1.f : a.scale;
       const int last = half ? i - 1 : i;  // j up to here
+      double* sum_x = reinterpret_cast<double*>(smem + Sm::kSumX) + w * kC + 4 * g;
+      float* sum_b = reinterpret_cast<float*>(smem + Sm::kSumB) + w * kC + 4 * g;
       f32x4 bx[4];
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
@@ -577,21 +598,22 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
           bx[jt][x] = m * bj[x];
           cb[x] = m * kx[jt][x];
           cx[x] = cb[x] * bj[x];
-          row_x += cx[x];
+          row_x += (double)cx[x];
         }
         if (jt <= tile) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float sx = group_sum(cx[x]), sb = group_sum(cb[x]);
+            const double sx = group_sum((double)cx[x]);
+            const float sb = group_sum(cb[x]);
             if (r == 0) {
-              float* sums = reinterpret_cast<float*>(smem + Sm::kSums) + w * 2 * kC;
-              sums[j + x] = sx;
-              sums[kC + j + x] = sb;
+              sum_x[16 * jt + x] = sx;
+              sum_b[16 * jt + x] = sb;
             }
           }
         }
       }
       row_x = across_groups(row_x);
+      if (g == 0) reinterpret_cast<double*>(smem + Sm::kRowX)[half * kC + i] = row_x;
 #pragma unroll
       for (int kb = 0; kb < TT::kBlocks; ++kb)
         if (16 * tile >= kb * M::kDepth) {
@@ -626,7 +648,7 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
       kd = across_groups(kd);
       float* tok = reinterpret_cast<float*>(smem + Sm::kTok);
       if (g == 0) {
-        tok[half * kC + i] = row_x + rdot;
+        tok[half * kC + i] = rdot;
         tok[(2 + half) * kC + i] = kd;
       }
 #pragma unroll
@@ -673,7 +695,9 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
       }
     }
     if (w == 0) {
-      const float* sums = reinterpret_cast<const float*>(smem + Sm::kSums);
+      const double* sum_x = reinterpret_cast<const double*>(smem + Sm::kSumX);
+      const float* sum_b = reinterpret_cast<const float*>(smem + Sm::kSumB);
+      const double* rows = reinterpret_cast<const double*>(smem + Sm::kRowX);
       const float* tok = reinterpret_cast<const float*>(smem + Sm::kTok);
       const float* gt = reinterpret_cast<const float*>(smem + Sm::kGate + (h & 1) * 2048);
       const float* dec = gt + 256;
@@ -682,14 +706,16 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
       float all = 0.f;
 #pragma unroll
       for (int x = 0; x < 8; ++x) all += dots[x];
-      float cx = 0.f, cb = 0.f;
+      double cx = 0.0;
+      float cb = 0.f;
       for (int x = lane >> 4; x < 8; x = x == 3 ? 4 + (lane >> 4) : x + 1) {
-        cx += sums[x * 2 * kC + lane];
-        cb += sums[x * 2 * kC + kC + lane];
+        cx += sum_x[x * kC + lane];
+        cb += sum_b[x * kC + lane];
       }
       const float e = exp_f32((dec[kC - 1] - dec[lane]) + (dec[2 * kC - 1] - dec[kC + lane]));
       const float z = gt[kC + lane] * kdt;
-      const float after = wave_suffix((tok[lane] + tok[kC + lane]) - cx, lane);
+      const float after = wave_suffix(tok[lane] + tok[kC + lane], lane) +
+                          (float)wave_suffix((rows[lane] + rows[kC + lane]) - cx, lane);
       float before = z;  // sum of z over the tokens before
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) {
