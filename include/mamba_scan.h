@@ -391,7 +391,8 @@ size_t mamba_delta_bwd_workspace_bytes(const mamba_delta_dims* dims, int packed)
  *   workspace       : >= mamba_delta_bwd_workspace_bytes bytes, 256-byte aligned
  * Every output is overwritten; with seq_offsets, tokens that no sequence holds are not written.  Sums are
  * taken in a fixed order (bitwise reproducible).  With bf16 storage dinitial_state is
- * within about 3e-6 (relative), the others round once to bf16.
+ * within about 1e-5 (relative, 2-norm; 3e-6 where keys and queries are independent), and the others are the fp32
+ * results rounded once.
  */
 int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                     const float* initial_state, const int64_t* seq_offsets, float scale,
