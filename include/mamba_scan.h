@@ -312,7 +312,8 @@ int mamba_block_fwd(const void* hidden, const void* w_in, const float* conv_weig
  * g <= 0 is the log of the decay (values below -200, -infinity among them, reset the state); beta is
  * usually in (0, 1) and the keys of unit length.  Value heads [h * rep, (h + 1) * rep), rep = v_heads /
  * qk_heads, share query and key head h.  dk and dv are multiples of 8 with dk <= 128 and dv <= 1024
- * (MAMBA_ERR_UNSUPPORTED otherwise).
+ * (MAMBA_ERR_UNSUPPORTED otherwise).  tokens * v_heads * max(dk, dv) is at most 2^40, and batch * v_heads
+ * below 2^25 (MAMBA_ERR_SHAPE otherwise).
  */
 typedef struct mamba_delta_dims {
   int64_t batch;    /* sequences, >= 1 */
@@ -323,7 +324,8 @@ typedef struct mamba_delta_dims {
   int64_t q_stride, k_stride, v_stride; /* elements between tokens of q, k, v; 0: heads * values.
                                            Multiples of 16 bytes (MAMBA_ERR_ALIGN otherwise), so that
                                            q, k and v may be slices of one projection's rows.
-                                           Sequences follow each other at seqlen strides. */
+                                           Sequences follow each other at seqlen strides.  A stride,
+                                           and heads * values, is at most 2^22 (MAMBA_ERR_SHAPE). */
   int32_t io_dtype; /* enum mamba_dtype: q, k, v, g, beta, out and their gradients */
   int32_t reserved; /* set to 0 */
 } mamba_delta_dims;

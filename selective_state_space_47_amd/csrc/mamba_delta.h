@@ -456,10 +456,12 @@ inline int64_t chunk_slots(const mamba_delta_dims* d, bool packed) { return slot
 
 // Whether a state pass takes workgroups of 64 columns (4 waves) instead of 128 (8 waves); `runs` sequences or
 // segments per head, equally long (`even`) or not.  One workgroup runs on a CU at a time and goes through
-// its chunks one after another: 128 columns share a chunk's tiles better (4.3 us a chunk with all CUs busy,
-// dk = 128, bf16), 64 are through sooner (3.1 us) and leave less idle at the end.  Measured, sequences of 2048,
-// heads of 128, 64 and 128 columns: forward of 120 heads 149 and 175 us, of 240 310 and 254 us; backward of 40
-// 232 and 285 us, of 240 1086 and 1006 us.
+// its chunks one after another: 128 columns share a chunk's tiles better (4.5 us a chunk of the output pass with all
+// CUs busy, dk = 128, bf16), 64 are through sooner (3.6 us) and leave less idle at the end.  The weights of a round,
+// 4.3 and 3.1, are those with which the rule takes the faster side in what was measured, 64 and 128 columns, bf16:
+// sequences of 2048, heads of 128: forward of 120 heads 163 and 191 us, of 240 333 and 276 us; backward of 40 heads
+// 248 and 317 us, of 240 1174 and 1080 us; forward of 300 heads of 192 613 and 640 us; packed, 40 heads: 8 sequences
+// of 0 to 4099 285 and 338 us, 16 of 512 222 and 194 us.
 inline bool narrow_pass(int64_t heads, int64_t runs, bool even, int64_t dv) {
   if (dv <= 64) return true;
   const double n = (double)heads * (double)runs, wide = n * (double)((dv + 127) / 128) / 256.0,

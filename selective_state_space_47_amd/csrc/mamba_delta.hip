@@ -73,8 +73,8 @@ __device__ __forceinline__ double wave_prefix(double v, int lane) {
 // T, P and the gates of one chunk, for the value heads of a key head.  Four waves share the 64 tokens, a wave's
 // block of 16 x 16 products being what one matrix instruction makes; T comes from the inverses of its four
 // diagonal blocks, which 16 substitution steps make in registers, and fp32 matrix products below them, so that
-// no chain of steps is as long as the chunk.  10240 chunks x heads of dk = 128, bf16: 125 us, 0.43 GB read and
-// written (3.4 TB/s); bound by the substitution's dependent steps and the barriers between the parts, which
+// no chain of steps is as long as the chunk.  10240 chunks x heads of dk = 128, bf16: 128 us, 0.45 GB read and
+// written (3.5 TB/s); bound by the substitution's dependent steps and the barriers between the parts, which
 // four workgroups per CU overlap.
 template <typename E, int DK>
 __global__ __launch_bounds__(256, sizeof(E) * DK <= 256 ? 4 : 2) void chunk_kernel(Args a) {
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kPassThreads) void scan_kernel(Args a, int32_t col_
 
 // The states before the segments, one after another: S <- map S + (the segment's own).  A workgroup has 16
 // columns, its waves 16 rows each; fp32 matrix instructions, S handed round through LDS.  Bound by that chain:
-// 62 us of the 720 that 65536 tokens x 12 heads of 128 take.  seg_state holds each segment's own result on
+// 65 us for 65536 tokens x 12 heads of 128, bf16.  seg_state holds each segment's own result on
 // entry and the state before it on return, the first segment's (of sequences without tokens, too) being a copy
 // of the initial state: the output pass reads only these, as it may write the last state over the initial one.
 template <int DK>
@@ -359,8 +359,8 @@ __global__ __launch_bounds__(DK * 4) void segments_kernel(Args a, int32_t col_bl
 template <typename E, int DK>
 int launch_chunks_t(const Args& a, hipStream_t s) {
   // value heads of a key head one after another share K K^T and Q K^T; where that leaves CUs idle, each
-  // has a workgroup of its own (whole forward, two value heads per key head: 40 chunks x heads 17 us
-  // against 22, 400 44 us against 47, 10240 462 us against 408)
+  // has a workgroup of its own (whole forward, each and together, two value heads per key head, the only ratio
+  // measured: 40 chunks x heads 17 and 22 us, 400 47 and 51 us, 800 76 and 80 us, 10240 480 and 446 us)
   const unsigned split = a.slots * a.hk * a.rep <= 512 ? (unsigned)a.rep : 1;
   hipLaunchKernelGGL((chunk_kernel<E, DK>), dim3((unsigned)(a.slots * a.hk), split), dim3(256), 0, s, a);
   return launch_status();
@@ -403,11 +403,12 @@ int launch_forward(const Args& a, hipStream_t s) {
 }
 
 // Chunks per segment, 0 for whole sequences.  A pass costs one unit per chunk and round of 256
-// workgroups (one per CU); segments add a summary pass over their own and the map's columns, about 0.65
-// of a unit per chunk, and a quarter of a unit per segment to join them.  Packed sequences are taken to
-// be up to twice as long as their mean.  Segments are used where that model gains a quarter.
-// Measured, heads of 128, bf16, whole and in segments: 65536 tokens x 12 heads 2757 and 757 us, 16384 x 12
-// 642 and 258 us.
+// workgroups (one per CU, counted as 128 columns each, also where narrow_pass then takes 64); segments add a
+// summary pass over their own and the map's columns, about 0.65 of a unit per chunk (65536 tokens x 12 heads: 378 us
+// in two rounds, the output pass 281 us in one), and a quarter of a unit per segment to join them.  Packed sequences
+// are taken to be up to twice as long as their mean.  Segments are used where that model gains a quarter.
+// Measured, heads of 128, bf16, whole and in segments: 65536 tokens x 12 heads 3025 and 778 us, 16384 x 12
+// 713 and 259 us.
 int64_t plan_segments(const mamba_delta_dims* d, bool packed) {
   constexpr double kCUs = 256.0;
   const int64_t per = d->dv <= 64 ? 64 : 128;

@@ -307,10 +307,10 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
 }
 
 // The state forwards and its adjoint backwards need nothing of each other: their workgroups share a launch,
-// the adjoint's first (they take longer).  8 x 2048 tokens x 40 heads of 128, bf16: 670 us (in launches of their
-// own two rounds of the CUs each, 371 and 608 us), 2.7 GB read and written, 4.0 TB/s: the memory's rate but for
-// the last round's idle CUs.  S and dS' of every chunk are 60% of it; making them again from the chunks'
-// inputs would take the passes' products a second time.  (fp32 tiles of 128 keys do not fit 256 registers.)
+// the adjoint's first (they take longer).  8 x 2048 tokens x 40 heads of 128, bf16: 714 us (before dY had a second
+// part 670, and in launches of their own, two rounds of the CUs each, 371 and 608), 2.8 GB read and written, 3.9 TB/s:
+// the memory's rate but for the last round's idle CUs.  S and dS' of every chunk are 1.2 GB of it; making them again
+// from the chunks' inputs would take the passes' products a second time.  (fp32 tiles of 128 keys do not fit 256 registers.)
 template <typename E, int DK, int NW>
 __global__ __launch_bounds__((sizeof(E) * DK <= 256 ? kPassThreads : 64 * NW)) void passes_kernel(
     BwdArgs b, int32_t col_blocks, uint32_t each) {
@@ -400,8 +400,9 @@ struct GradSmem {
 // Eight waves: wave (tile, half) has the tokens 16 tile .. 16 tile + 15.  Half 0 makes M and B1, half 1 N
 // and B2; of dQ and dK each half has half of the keys' values.  The state's columns come in blocks of kDB,
 // head after head: the next block is copied while one is worked on.
-// 10240 chunks x heads of 128 x 128, bf16: 610 us, 2.2 GB, 3.6 TB/s; 578 us of it without any product: bound by the
-// copies of the images, 44 KB of them on their way to a CU at a time (the LDS that is left).
+// 10240 chunks x heads of 128 x 128, bf16: 731 us, 2.4 GB, 3.3 TB/s; 619 us of it without the products and what is
+// made of them: bound first by the copies of the images, 48 KB of them on their way to a CU at a time (the LDS that
+// is left), then by what follows a head's last block, which nothing else on the CU overlaps.
 template <typename E, int DK>
 __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
   using M = Mma<E>;

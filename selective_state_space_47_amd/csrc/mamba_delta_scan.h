@@ -7,8 +7,8 @@
 // straight into LDS, a chunk ahead.
 //
 // Bound by the chain of a chunk's products (K S, T Y, K^T E: a wave waits for the matrix unit, for LDS and for
-// its own conversions in turn), 4.3 us a chunk with 8 waves on a CU and 3.1 us with 4.  Output pass, 8 x 2048
-// tokens x 40 heads of 128, bf16: 275 us; 320 workgroups are two rounds of 256 CUs.
+// its own conversions in turn), 4.5 us a chunk of the output pass with 8 waves on a CU and 3.6 us with 4.  8 x 2048
+// tokens x 40 heads of 128, bf16: 316 us; 320 workgroups are two rounds of 256 CUs.
 #pragma once
 #include "mamba_delta.h"
 
@@ -130,8 +130,8 @@ __device__ __forceinline__ void scan_pass(const Args& a, int32_t col_blocks, cha
     const lds_ptr sm = (lds_ptr)(smem + st * St::kBytes);
     const int n = (int)min((int64_t)kC, sp.len - ch * kC);
     // Operands are read a step before the products that take them: one or two waves per SIMD leave nobody
-    // else to hide the reads behind (the pass above took 313 us with reads where they are used).  Nothing is
-    // moved past the end of a step.
+    // else to hide the reads behind (an eighth more time with reads where they are used).  Nothing is moved past
+    // the end of a step.
     typename M::Frag kf[2][4], qf[2][4];
     auto read_kq = [&](int kb) {
 #pragma unroll

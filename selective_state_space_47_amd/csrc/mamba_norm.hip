@@ -17,10 +17,10 @@
 // partial row, and a second launch adds the partial rows.  Every order is fixed: no atomics.
 //
 // Measured, 16384 rows, bf16 (a large copy reaches 4.9 to 5.4 TB/s):
-//   gated norm, 40 groups of 128: 90 us forward (5.6 TB/s), 199 us gradients (4.2 TB/s) and 7 us their second
+//   gated norm, 40 groups of 128: 92 us forward (5.3 TB/s), 184 us gradients (4.5 TB/s) and 6 us their second
 //   launch
-//   add norm, 2560 wide, fp32 stream, norm after the block: 104 us forward (4.8 TB/s), 164 us gradients
-//   (4.6 TB/s) and 9 us
+//   add norm, 2560 wide, fp32 stream, norm after the block: 103 us forward (4.8 TB/s), 168 us gradients
+//   (4.5 TB/s) and 9 us
 // 256 rows of 40 groups, or one row of 768: 3 to 4 us, latency.
 #include "mamba_common.h"
 #include "mamba_grid.h"
@@ -622,8 +622,10 @@ __global__ __launch_bounds__(1024) void norm_fold_kernel(FoldArgs a) {
 
 // The team of a unit of `dim` values: calls f.template operator()<T, R>().  One vector per lane, so that a
 // gradient's rows (up to six values per column) leave room for many waves: 2560 values, gradients, 16384
-// rows, bf16 with an fp32 stream: 164 us with 5 waves of one vector, 316 us with 2
-// waves of three.
+// rows, bf16 with an fp32 stream: 168 us with 5 waves of one vector, 316 us with 2
+// waves of three.  Teams are powers of two and, between them, three, five and ten waves: the widths of the models
+// that the package's workloads come from (1536, 2560 and 5120).  Any other width takes the next larger team, up to
+// half of whose lanes then have no column.
 template <typename F>
 int with_team(int64_t dim, F f) {
   if (dim <= 64) return f.template operator()<8, 1>();
