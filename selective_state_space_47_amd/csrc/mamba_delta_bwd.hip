@@ -310,7 +310,8 @@ __device__ __forceinline__ void adjoint_pass(const BwdArgs& b, int32_t col_block
 // the adjoint's first (they take longer).  8 x 2048 tokens x 40 heads of 128, bf16: 714 us (before dY had a second
 // part 670, and in launches of their own, two rounds of the CUs each, 371 and 608), 2.8 GB read and written, 3.9 TB/s:
 // the memory's rate but for the last round's idle CUs.  S and dS' of every chunk are 1.2 GB of it; making them again
-// from the chunks' inputs would take the passes' products a second time.  (fp32 tiles of 128 keys do not fit 256 registers.)
+// from the chunks' inputs would take the passes' products a second time.  (fp32 tiles of 128 keys do not fit 256
+// registers.)
 template <typename E, int DK, int NW>
 __global__ __launch_bounds__((sizeof(E) * DK <= 256 ? kPassThreads : 64 * NW)) void passes_kernel(
     BwdArgs b, int32_t col_blocks, uint32_t each) {
@@ -324,6 +325,10 @@ __global__ __launch_bounds__((sizeof(E) * DK <= 256 ? kPassThreads : 64 * NW)) v
 
 // ------------------------------------------------------------------ dQ, dK, dg, dbeta
 
+// every wave's LDS accesses are done (its copies may still be on their way)
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 // sum over the 16 lanes of a group, in every lane of it
 __device__ __forceinline__ float group_sum(float v) {
   v += dpp_row<0x128>(v);
@@ -331,10 +336,6 @@ __device__ __forceinline__ float group_sum(float v) {
   v += dpp_row<0x122>(v);
   v += dpp_row<0x121>(v);
   return v;
-}
-// every wave's LDS accesses are done (its copies may still be on their way)
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 // the same in fp64
 template <int kCtrl>
@@ -444,7 +445,7 @@ __global__ __launch_bounds__(512) void grad_kernel(BwdArgs b) {
     const uint32_t to = lds0 + Sm::kStages + st * Sm::kStage;
     const int cols = min(a.dv - db * BB::kDB, BB::kDB);
     const int64_t at = (t0 * a.hv + vh) * (int64_t)a.dv + db * BB::kDB;
-    // dO and dY: a tile of 4 (bf16) or 8 KB each, the first by waves 0-3 and the second by 4-7
+    // dO and dY: a tile of 4 (bf16) or 8 KB each, the first (and what bf16 leaves of dY) by waves 0-3, dY by 4-7
     const RowCopy<E, ET, kC, 4> co(tile, lane, o_stride, cols);
     co(rows_buffer(static_cast<const E*>(half ? b.dv : b.dout) + at, n, o_stride, cols),
        to + (half ? Sm::kDY : Sm::kDO), tile);
