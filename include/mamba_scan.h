@@ -14,7 +14,7 @@
  *                        whole sequences, one generation step, and the gradients.
  *
  * Around them: the block's projections (mamba_gemm_bf16, mamba_block_fwd) and its norms
- * (mamba_gated_norm_*, mamba_add_norm_*).
+ * (mamba_gated_norm_*, mamba_add_norm_*; of queries and keys with the rotation, mamba_qk_norm_rope_*).
  *
  * The model (sources by page title and section):
  *   - "Mamba" (elemedex dex entry), "How it works": h_t = Abar*h_{t-1} + Bbar*x_t, y_t = C*h_t,
@@ -489,6 +489,51 @@ int mamba_add_norm_bwd(const void* x, const void* residual, const float* weight,
                        const void* dresidual_out, void* dx, void* dresidual, float* dweight,
                        float* dscale, float* dpost_weight, const mamba_add_norm_dims* dims,
                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sizes of the norm of queries and keys.  rows is below 2^31, heads at most 65535 each. */
+typedef struct mamba_qk_norm_rope_dims {
+  int64_t rows;        /* tokens, >= 1 */
+  int64_t q_heads;     /* >= 1 */
+  int64_t k_heads;     /* >= 1 */
+  int64_t dim;         /* values per head, a multiple of 8, <= 256 (MAMBA_ERR_UNSUPPORTED otherwise) */
+  int64_t rotary_dim;  /* values that turn, a multiple of 16, <= dim; 0: none */
+  int64_t q_stride;    /* elements between rows of q; 0: q_heads * dim.  A multiple of 16 bytes, <= 2^32 */
+  int64_t k_stride;    /* the same of k */
+  int32_t io_dtype;    /* enum mamba_dtype: q, k, the outputs and the gradients */
+  int32_t interleaved; /* 0: value i turns with i + rotary_dim / 2; otherwise 2 i with 2 i + 1 */
+} mamba_qk_norm_rope_dims;
+
+/*
+ * RMS norm of queries and keys per head, and the rotation by the token's position, in one pass.  Per row and head:
+ *     h = x rsqrt(mean(x^2) + eps) weight
+ *     pair i of h is turned by the angle positions[row] * inv_freq[i]
+ *   q, k               : (rows, heads, dim), io_dtype, rows q_stride and k_stride apart
+ *   q_weight, k_weight : (dim) fp32, 16-byte aligned
+ *   positions          : (rows) device int64;  inv_freq : (rotary_dim / 2) device fp64, radians per position
+ *                        (both may be NULL where rotary_dim is 0)
+ *   q_out, k_out       : (rows, heads, dim), io_dtype, contiguous
+ * q, k and the outputs are 16-byte aligned; eps as for mamba_gated_norm_fwd.  Angles are fp64 (within 2^-50 of
+ * themselves), everything else fp32, each output rounded once.
+ */
+int mamba_qk_norm_rope_fwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                           const int64_t* positions, const double* inv_freq, float eps, void* q_out, void* k_out,
+                           const mamba_qk_norm_rope_dims* dims, void* stream);
+
+/* Bytes of device workspace mamba_qk_norm_rope_bwd needs (0 for invalid dims): one partial row of a weight's
+ * gradient per workgroup. */
+size_t mamba_qk_norm_rope_bwd_workspace_bytes(const mamba_qk_norm_rope_dims* dims);
+
+/*
+ * Gradients of mamba_qk_norm_rope_fwd for the loss sum(q_out * dq_out) + sum(k_out * dk_out).
+ *   dq_out, dk_out, dq, dk : (rows, heads, dim), io_dtype, contiguous, 16-byte aligned
+ *   dq_weight, dk_weight   : (dim) fp32
+ * Outputs are overwritten; sums over rows are taken in a fixed order (bitwise reproducible).
+ */
+int mamba_qk_norm_rope_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                           const int64_t* positions, const double* inv_freq, float eps, const void* dq_out,
+                           const void* dk_out, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                           const mamba_qk_norm_rope_dims* dims, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /* Static text for a status code (never NULL). */
 const char* mamba_status_string(int status);

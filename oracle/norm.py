@@ -61,3 +61,25 @@ def add_norm_ref(x, residual, weight, scale, post, eps, dout=None, dres=None):
         g["dx"], h = _norm_bwd(x, p, dn, eps)
         g["dpost_weight"] = (dn * h).sum(0)
     return g
+
+
+def qk_norm_rope_ref(x, weight, positions, inv_freq, eps, interleaved, dout=None):
+    """The norm per head and the rotation of x (rows, heads, dim): out, or (dx, dweight) for dout."""
+    x, w, f = _f64(x), _f64(weight), _f64(inv_freq)
+    half = len(f)
+    angle = np.asarray(positions, dtype=np.float64)[:, None, None] * f
+    c, s = np.cos(angle), np.sin(angle)
+    i = np.arange(half)
+    one, two = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+
+    def turn(h, s):
+        out = h.copy()
+        out[..., one] = h[..., one] * c - h[..., two] * s
+        out[..., two] = h[..., two] * c + h[..., one] * s
+        return out
+
+    if dout is None:
+        return turn(x * _rms(x, eps) * w, s)
+    dh = turn(_f64(dout), -s)
+    dx, n = _norm_bwd(x, w, dh, eps)
+    return dx, (dh * n).sum((0, 1))

@@ -59,6 +59,13 @@ class mamba_add_norm_dims(ctypes.Structure):
                 ("res_dtype", ctypes.c_int32)]
 
 
+class mamba_qk_norm_rope_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("k_heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("rotary_dim", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 EXPORTS = ("mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "mamba_state_update",
            "mamba_scan_workspace_bytes",
            "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes", "mamba_gemm_bf16",
@@ -66,7 +73,8 @@ EXPORTS = ("mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
            "mamba_delta_workspace_bytes", "mamba_delta_update", "mamba_delta_bwd",
            "mamba_delta_bwd_workspace_bytes", "mamba_gated_norm_fwd",
            "mamba_gated_norm_bwd", "mamba_gated_norm_bwd_workspace_bytes", "mamba_add_norm_fwd",
-           "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes", "mamba_status_string",
+           "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes", "mamba_qk_norm_rope_fwd",
+           "mamba_qk_norm_rope_bwd", "mamba_qk_norm_rope_bwd_workspace_bytes", "mamba_status_string",
            "mamba_abi_version")
 
 
@@ -148,6 +156,14 @@ def lib():
             L.mamba_add_norm_bwd.restype = ctypes.c_int
             L.mamba_add_norm_bwd_workspace_bytes.argtypes = [ap]
             L.mamba_add_norm_bwd_workspace_bytes.restype = sz
+            kp = ctypes.POINTER(mamba_qk_norm_rope_dims)
+            L.mamba_qk_norm_rope_fwd.argtypes = [vp, vp, fp, fp, vp, vp, f32, vp, vp, kp, vp]
+            L.mamba_qk_norm_rope_fwd.restype = ctypes.c_int
+            L.mamba_qk_norm_rope_bwd.argtypes = [vp, vp, fp, fp, vp, vp, f32, vp, vp, vp, vp, fp,
+                                                 fp, kp, vp, sz, vp]
+            L.mamba_qk_norm_rope_bwd.restype = ctypes.c_int
+            L.mamba_qk_norm_rope_bwd_workspace_bytes.argtypes = [kp]
+            L.mamba_qk_norm_rope_bwd_workspace_bytes.restype = sz
             L.mamba_status_string.argtypes = [ctypes.c_int]
             L.mamba_status_string.restype = ctypes.c_char_p
             L.mamba_abi_version.argtypes = []
@@ -626,7 +642,8 @@ def _token_stride(t, name, vec):
 # its address, the workspace size and the device.
 _CHECKED = {}
 _MARSHAL = None
-(_DELTA_FWD, _DELTA_UPDATE, _DELTA_BWD, _GATED_FWD, _GATED_BWD, _ADD_FWD, _ADD_BWD) = range(7)
+(_DELTA_FWD, _DELTA_UPDATE, _DELTA_BWD, _GATED_FWD, _GATED_BWD, _ADD_FWD, _ADD_BWD, _QK_FWD,
+ _QK_BWD) = range(9)
 
 
 def _marshal():
@@ -1039,5 +1056,108 @@ def mamba_add_norm_bwd(x, residual, weight, dout, dresidual_out=None, scale=None
     workspace, ws_len = _scratch(workspace, x, e)
     res = {name: g[name] for name in _ADD_GRADS}
     _call(_ADD_BWD, e, eps, ws_len, x, residual, weight, scale, post_weight, dout, dresidual_out,
+          *res.values(), workspace)
+    return res
+
+
+# ---------------------------------------------------------------------------- norm of queries and keys
+
+def _qk_check(q, k, q_weight, k_weight, positions, inv_freq, interleaved, others):
+    """The entry of a norm of queries and keys; `others`: (tensor or None, name, "q", "k" or "weight")."""
+    for t, name in ((q, "q"), (k, "k"), (q_weight, "q_weight"), (k_weight, "k_weight")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if q.dim() != 3 or q.device.type != "cuda" or q.layout != torch.strided:
+        raise ValueError("q must be (rows, heads, dim) on a HIP device")
+    io, dev = q.dtype, q.device
+    code = _io_code(io)
+    rows, Hq, d = q.shape
+    if (k.dim() != 3 or k.dtype != io or k.device != dev or k.layout != torch.strided
+            or k.shape[0] != rows or k.shape[2] != d):
+        raise ValueError(f"k must be ({rows}, heads, {d}) {io} on {dev}")
+    Hk = k.shape[1]
+    rot = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a (rotary_dim / 2,) tensor")
+        rot = 2 * inv_freq.shape[0]
+        _check(inv_freq, "inv_freq", (rot // 2,), torch.float64, dev)
+        if positions is None:
+            raise ValueError("positions is required")
+    _check(positions, "positions", (rows,), torch.int64, dev)
+    _check(q_weight, "q_weight", (d,), torch.float32, dev)
+    _check(k_weight, "k_weight", (d,), torch.float32, dev)
+    for t, name, kind in others:
+        if kind == "weight":
+            _check(t, name, (d,), torch.float32, dev)
+        else:
+            _check(t, name, (rows, Hq if kind == "q" else Hk, d), io, dev)
+    vec = 8 if code == MAMBA_BF16 else 4
+    strides = []
+    for t, name in ((q, "q"), (k, "k")):
+        stride = _row_stride(t, name)
+        if stride % vec:
+            raise ValueError(f"{name} must have rows at a multiple of {vec} elements; its strides are "
+                             f"{tuple(t.stride())}")
+        strides.append(stride)
+    dm = mamba_qk_norm_rope_dims(rows, Hq, Hk, d, rot, *strides, code, int(bool(interleaved)))
+    return _Entry(dm, mamba_qk_norm_rope_bwd_workspace_bytes(dm), dev)
+
+
+def mamba_qk_norm_rope_bwd_workspace_bytes(dims: mamba_qk_norm_rope_dims) -> int:
+    return int(lib().mamba_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(dims)))
+
+
+def mamba_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions=None, inv_freq=None, eps=1e-5,
+                           interleaved=False, q_out=None, k_out=None):
+    """RMS norm of queries and keys per head and the rotation by position (mamba_qk_norm_rope_fwd in
+    include/mamba_scan.h).
+
+    q: (rows, Hq, dim), k: (rows, Hk, dim) float32 or bfloat16, rows at any stride of 16 bytes;
+    q_weight, k_weight: (dim,) float32; positions: (rows,) int64; inv_freq: (rotary_dim / 2,) float64,
+    radians per position (None: no rotation).  Value i turns with i + rotary_dim / 2, or with
+    interleaved 2 i with 2 i + 1.  Returns (q_out, k_out).
+    """
+    m = _MARSHAL or _marshal()
+    key = m.key(_QK_FWD, q, k, q_weight, k_weight, positions, inv_freq, bool(interleaved), q_out, k_out)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _qk_check(q, k, q_weight, k_weight, positions, inv_freq, interleaved,
+                                     ((q_out, "q_out", "q"), (k_out, "k_out", "k"))))
+    if q_out is None:
+        q_out = m.empty(q)
+    if k_out is None:
+        k_out = m.empty(k)
+    _call(_QK_FWD, e, eps, 0, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
+    return q_out, k_out
+
+
+_QK_GRADS = ("dq", "dk", "dq_weight", "dk_weight")
+
+
+def mamba_qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, eps=1e-5,
+                           interleaved=False, workspace=None, grads=None):
+    """Gradients of mamba_qk_norm_rope_fwd for the loss sum(q_out * dq_out) + sum(k_out * dk_out): a dict
+    with dq, dk, dq_weight and dk_weight.  `grads` may hold preallocated output tensors under the same
+    keys."""
+    if dq_out is None or dk_out is None:
+        raise ValueError("dq_out and dk_out are required")
+    g = dict(grads or {})
+    given = [g.get(name) for name in _QK_GRADS]
+    m = _MARSHAL or _marshal()
+    key = m.key(_QK_BWD, q, k, q_weight, k_weight, positions, inv_freq, bool(interleaved), dq_out, dk_out,
+                *given)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _qk_check(
+            q, k, q_weight, k_weight, positions, inv_freq, interleaved,
+            ((dq_out, "dq_out", "q"), (dk_out, "dk_out", "k"),
+             *zip(given, _QK_GRADS, ("q", "k", "weight", "weight")))))
+    for name, like in zip(_QK_GRADS, (q, k, q_weight, k_weight)):
+        if g.get(name) is None:
+            g[name] = m.empty(like)
+    workspace, ws_len = _scratch(workspace, q, e)
+    res = {name: g[name] for name in _QK_GRADS}
+    _call(_QK_BWD, e, eps, ws_len, q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out,
           *res.values(), workspace)
     return res

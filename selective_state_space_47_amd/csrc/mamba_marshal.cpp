@@ -96,7 +96,7 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd };
+enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd, kQkFwd, kQkBwd, kEntries };
 
 // call(entry, dims address, stream, factor, workspace bytes, *tensors) -> status.  The tensors stand in the
 // order of the entry point's pointers, `factor` is its scale or eps.
@@ -119,8 +119,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   auto fp = [&](int i) { return static_cast<float*>(p[i]); };
-  static const int kTensors[] = {10, 7, 16, 4, 8, 7, 13};
-  if (entry < kDeltaFwd || entry > kAddBwd || n - 5 != kTensors[entry]) {
+  static const int kTensors[] = {10, 7, 16, 4, 8, 7, 13, 8, 13};
+  if (entry < kDeltaFwd || entry >= kEntries || n - 5 != kTensors[entry]) {
     PyErr_SetString(PyExc_TypeError, "wrong number of tensors for the entry point");
     return nullptr;
   }
@@ -155,6 +155,15 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     case kAddBwd:
       st = mamba_add_norm_bwd(p[0], p[1], fp(2), fp(3), fp(4), f, p[5], p[6], p[7], p[8], fp(9), fp(10), fp(11),
                               static_cast<mamba_add_norm_dims*>(d), p[12], ws, stream);
+      break;
+    case kQkFwd:
+      st = mamba_qk_norm_rope_fwd(p[0], p[1], fp(2), fp(3), static_cast<int64_t*>(p[4]), static_cast<double*>(p[5]),
+                                  f, p[6], p[7], static_cast<mamba_qk_norm_rope_dims*>(d), stream);
+      break;
+    case kQkBwd:
+      st = mamba_qk_norm_rope_bwd(p[0], p[1], fp(2), fp(3), static_cast<int64_t*>(p[4]), static_cast<double*>(p[5]),
+                                  f, p[6], p[7], p[8], p[9], fp(10), fp(11),
+                                  static_cast<mamba_qk_norm_rope_dims*>(d), p[12], ws, stream);
       break;
   }
   Py_END_ALLOW_THREADS
