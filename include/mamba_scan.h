@@ -12,6 +12,8 @@
  *   mamba_delta_fwd, mamba_delta_update, mamba_delta_bwd
  *                        the gated delta rule, a recurrence of the same kind with a matrix state:
  *                        whole sequences, one generation step, and the gradients.
+ *   mamba_linear_attn_fwd, mamba_linear_attn_update, mamba_linear_attn_bwd
+ *                        linear attention with a decay per head, the same without the rule's correction.
  *
  * Around them: the block's projections (mamba_gemm_bf16, mamba_block_fwd) and its norms
  * (mamba_gated_norm_*, mamba_add_norm_*; of queries and keys with the rotation, mamba_qk_norm_rope_*).
@@ -401,6 +403,48 @@ int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, 
                     const void* dout, const float* dlast, void* dq, void* dk, void* dv, void* dg,
                     void* dbeta, float* dinitial_state, const mamba_delta_dims* dims,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Linear attention with a decay per head: a linear recurrence like the scan's ("Mamba" (elemedex), "How it
+ * works") whose state is a matrix per head.  Per value head, with its key head's q and k:
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T        (dk x dv)
+ *     o_t = scale S_t^T q_t
+ * (with q = C, k = B, v = Delta x and g = Delta A it is the selective scan with one decay for all channels of
+ * a head).  g <= 0 is the log of the decay, fp32 (values below -200, -infinity among them, reset the state); a
+ * fixed decay per head is a g with the same row for every token.  Sizes are a mamba_delta_dims with the same
+ * limits; its strides count for q, k and v.
+ */
+
+/* Bytes of device workspace mamba_linear_attn_fwd needs (0 for invalid dims; MAMBA_OK calls may need none).
+ * packed != 0: for a call with seq_offsets.  Sequences of few heads are worked on in segments and take an fp32
+ * state (dk x dv) per segment and value head. */
+size_t mamba_linear_attn_workspace_bytes(const mamba_delta_dims* dims, int packed);
+
+/*
+ * Linear attention over whole sequences.
+ *   q, k          : (batch, seqlen, qk_heads, dk), io_dtype, tokens q_stride and k_stride apart
+ *   v             : (batch, seqlen, v_heads, dv), io_dtype, tokens v_stride apart
+ *   g             : (batch, seqlen, v_heads) fp32, contiguous
+ *   initial_state, seq_offsets, out, last_state : as for mamba_delta_fwd
+ *   workspace     : >= mamba_linear_attn_workspace_bytes bytes, 256-byte aligned (NULL where that is 0);
+ *                   contents on entry ignored
+ * q, k, v, out and the states are 16-byte aligned.  With bf16 storage out is the fp32 result rounded once
+ * (the factors that reach it are two bf16 parts each) and last_state is within about 1e-6 of it in the 2-norm.
+ * Sequences are worked on in chunks of 64 tokens: a NaN or an infinity in a token's q, k or v also reaches the
+ * outputs of other tokens of its chunk, never an earlier chunk or another sequence.
+ */
+int mamba_linear_attn_fwd(const void* q, const void* k, const void* v, const float* g,
+                          const float* initial_state, const int64_t* seq_offsets, float scale, void* out,
+                          float* last_state, const mamba_delta_dims* dims, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * One generation step of it for `batch` sequences (dims->seqlen must be 1): the state (batch, v_heads, dk, dv)
+ * fp32, 16-byte aligned, is updated in place.  fp32 arithmetic.
+ *   q, k, v, g, out : as for mamba_linear_attn_fwd with one token per sequence
+ */
+int mamba_linear_attn_update(float* state, const void* q, const void* k, const void* v, const float* g,
+                             float scale, void* out, const mamba_delta_dims* dims, void* stream);
 
 /* Sizes of the gated norm.  rows * groups is below 2^31, dim at most 16384 and groups at most 65535
  * (MAMBA_ERR_SHAPE otherwise). */

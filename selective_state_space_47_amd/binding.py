@@ -74,7 +74,8 @@ EXPORTS = ("mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
            "mamba_delta_bwd_workspace_bytes", "mamba_gated_norm_fwd",
            "mamba_gated_norm_bwd", "mamba_gated_norm_bwd_workspace_bytes", "mamba_add_norm_fwd",
            "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes", "mamba_qk_norm_rope_fwd",
-           "mamba_qk_norm_rope_bwd", "mamba_qk_norm_rope_bwd_workspace_bytes", "mamba_status_string",
+           "mamba_qk_norm_rope_bwd", "mamba_qk_norm_rope_bwd_workspace_bytes", "mamba_linear_attn_fwd",
+           "mamba_linear_attn_workspace_bytes", "mamba_linear_attn_update", "mamba_status_string",
            "mamba_abi_version")
 
 
@@ -164,6 +165,12 @@ def lib():
             L.mamba_qk_norm_rope_bwd.restype = ctypes.c_int
             L.mamba_qk_norm_rope_bwd_workspace_bytes.argtypes = [kp]
             L.mamba_qk_norm_rope_bwd_workspace_bytes.restype = sz
+            L.mamba_linear_attn_fwd.argtypes = [vp, vp, vp, fp, fp, vp, f32, vp, fp, ep, vp, sz, vp]
+            L.mamba_linear_attn_fwd.restype = ctypes.c_int
+            L.mamba_linear_attn_workspace_bytes.argtypes = [ep, ctypes.c_int]
+            L.mamba_linear_attn_workspace_bytes.restype = sz
+            L.mamba_linear_attn_update.argtypes = [fp, vp, vp, vp, fp, f32, vp, ep, vp]
+            L.mamba_linear_attn_update.restype = ctypes.c_int
             L.mamba_status_string.argtypes = [ctypes.c_int]
             L.mamba_status_string.restype = ctypes.c_char_p
             L.mamba_abi_version.argtypes = []
@@ -643,7 +650,7 @@ def _token_stride(t, name, vec):
 _CHECKED = {}
 _MARSHAL = None
 (_DELTA_FWD, _DELTA_UPDATE, _DELTA_BWD, _GATED_FWD, _GATED_BWD, _ADD_FWD, _ADD_BWD, _QK_FWD,
- _QK_BWD) = range(9)
+ _QK_BWD, _LINEAR_FWD, _LINEAR_UPDATE) = range(11)
 
 
 def _marshal():
@@ -710,7 +717,14 @@ def _scratch(workspace, like, e):
 
 
 def _delta_check(q, k, v, g, beta, others, seq_offsets, lead, workspace_bytes):
-    """The entry of a call on these tensors; raises for tensors that do not belong together.  `others`:
+    """The entry of a delta rule's call on these tensors (_mixer_check with g and beta of the io dtype)."""
+    return _mixer_check(q, k, v, ((g, "g", None), (beta, "beta", None)), others, seq_offsets, lead,
+                        workspace_bytes)
+
+
+def _mixer_check(q, k, v, gates, others, seq_offsets, lead, workspace_bytes):
+    """The entry of a call on these tensors; raises for tensors that do not belong together.  `gates`:
+    (tensor, name, dtype or None for the io dtype) of a number per token and value head; `others`:
     (tensor or None, name, shape function of (states, *token axes), Hk, Hv, dk, dv, dtype or None for
     the io dtype); lead: token axes of q; workspace_bytes: the library's query, or None."""
     n_seq = _offsets_count(seq_offsets, q)
@@ -733,10 +747,10 @@ def _delta_check(q, k, v, g, beta, others, seq_offsets, lead, workspace_bytes):
                          "belong together")
     if Hk == 0 or Hv % Hk:
         raise ValueError(f"{Hv} value heads are no multiple of {Hk} key heads")
-    for t, name in ((g, "g"), (beta, "beta")):
+    for t, name, dt in gates:
         if t is None:
             raise ValueError(f"{name} is required")
-        _check(t, name, (*tokens, Hv), io, dev)
+        _check(t, name, (*tokens, Hv), dt or io, dev)
     vec = 8 if code == MAMBA_BF16 else 4
     if packed:
         batch, L = n_seq, tokens[0]
@@ -877,6 +891,64 @@ def mamba_delta_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, seq_
     _call(_DELTA_BWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, beta,
           initial_state, seq_offsets, dout, dlast, *res.values(), workspace)
     return res
+
+
+# ---------------------------------------------------------------------------- linear attention
+
+def mamba_linear_attn_workspace_bytes(dims: mamba_delta_dims, packed=False) -> int:
+    return int(lib().mamba_linear_attn_workspace_bytes(ctypes.byref(dims), int(bool(packed))))
+
+
+def mamba_linear_attn_fwd(q, k, v, g, scale=None, initial_state=None, seq_offsets=None,
+                          return_last_state=False, out=None, last_state=None, workspace=None):
+    """Linear attention with a decay per head over whole sequences (mamba_linear_attn_fwd in
+    include/mamba_scan.h).
+
+    q, k: (batch, L, Hk, dk); v: (batch, L, Hv, dv) -- all float32 or all bfloat16, also slices of one
+    projection's rows; g (log decay): (batch, L, Hv) float32.  scale, initial_state and seq_offsets as
+    for mamba_delta_fwd.  Returns out (batch, L, Hv, dv), or (out, last_state).
+    """
+    m = _MARSHAL or _marshal()
+    key = m.key(_LINEAR_FWD, q, k, v, g, initial_state, seq_offsets, out, last_state)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _mixer_check(
+            q, k, v, ((g, "g", torch.float32),),
+            ((initial_state, "initial_state", _state_shape, torch.float32),
+             (out, "out", _out_shape, None), (last_state, "last_state", _state_shape, torch.float32)),
+            seq_offsets, 2 if seq_offsets is None else 1, lib().mamba_linear_attn_workspace_bytes))
+    if out is None:
+        out = m.empty(v)
+    if return_last_state and last_state is None:
+        dm = e.dims
+        last_state = m.empty(q, "f", dm.batch, dm.v_heads, dm.dk, dm.dv)
+    ws_len = 0
+    if e.workspace_bytes or workspace is not None:
+        workspace, ws_len = _scratch(workspace, q, e)
+    _call(_LINEAR_FWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, initial_state,
+          seq_offsets, out, last_state, workspace)
+    return (out, last_state) if return_last_state else out
+
+
+def mamba_linear_attn_update(state, q, k, v, g, scale=None, out=None):
+    """One generation step of linear attention (mamba_linear_attn_update in include/mamba_scan.h).
+
+    state: (batch, Hv, dk, dv) float32, updated in place; q, k: (batch, Hk, dk); v: (batch, Hv, dv);
+    g: (batch, Hv) float32.  Returns out (batch, Hv, dv).
+    """
+    m = _MARSHAL or _marshal()
+    key = m.key(_LINEAR_UPDATE, state, q, k, v, g, out)
+    e = _CHECKED.get(key)
+    if e is None:
+        if state is None:
+            raise ValueError("state is required")
+        e = _remember(key, _mixer_check(q, k, v, ((g, "g", torch.float32),),
+                                        ((state, "state", _state_shape, torch.float32),
+                                         (out, "out", _out_shape, None)), None, 1, None))
+    if out is None:
+        out = m.empty(v)
+    _call(_LINEAR_UPDATE, e, e.factor if scale is None else scale, 0, state, q, k, v, g, out)
+    return out
 
 
 # ---------------------------------------------------------------------------- norms of a block
