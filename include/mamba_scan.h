@@ -446,6 +446,31 @@ int mamba_linear_attn_fwd(const void* q, const void* k, const void* v, const flo
 int mamba_linear_attn_update(float* state, const void* q, const void* k, const void* v, const float* g,
                              float scale, void* out, const mamba_delta_dims* dims, void* stream);
 
+/* Bytes of device workspace mamba_linear_attn_bwd needs (0 for invalid dims); packed as above.  It holds, per
+ * 128 tokens (fp32 storage: 64) and value head, the state before them and its adjoint after them, 4 bytes a
+ * value each, and where few units and key heads share many value heads fp32 sums of dq and dk. */
+size_t mamba_linear_attn_bwd_workspace_bytes(const mamba_delta_dims* dims, int packed);
+
+/*
+ * Gradients of mamba_linear_attn_fwd (same inputs) for the loss sum(out * dout) + sum(last_state * dlast); the
+ * states are recomputed.
+ *   dout           : (batch, seqlen, v_heads, dv), io_dtype, contiguous
+ *   dlast          : (batch, v_heads, dk, dv) fp32, or NULL: zero
+ *   dq, dk         : (batch, seqlen, qk_heads, dk), io_dtype, contiguous: summed over the value heads that
+ *                    share the key head
+ *   dv             : (batch, seqlen, v_heads, dv), io_dtype, contiguous
+ *   dg             : (batch, seqlen, v_heads) fp32, contiguous
+ *   dinitial_state : (batch, v_heads, dk, dv) fp32, or NULL: not written
+ *   workspace      : >= mamba_linear_attn_bwd_workspace_bytes bytes, 256-byte aligned
+ * Every output is overwritten; with seq_offsets, tokens that no sequence holds are not written.  Sums are taken
+ * in a fixed order (bitwise reproducible).
+ */
+int mamba_linear_attn_bwd(const void* q, const void* k, const void* v, const float* g,
+                          const float* initial_state, const int64_t* seq_offsets, float scale,
+                          const void* dout, const float* dlast, void* dq, void* dk, void* dv, float* dg,
+                          float* dinitial_state, const mamba_delta_dims* dims, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 /* Sizes of the gated norm.  rows * groups is below 2^31, dim at most 16384 and groups at most 65535
  * (MAMBA_ERR_SHAPE otherwise). */
 typedef struct mamba_gated_norm_dims {

@@ -15,7 +15,8 @@ __all__ = ["mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
            "mamba_delta_workspace_bytes", "mamba_delta_bwd_workspace_bytes",
            "mamba_gated_norm_fwd", "mamba_gated_norm_bwd", "mamba_gated_norm_bwd_workspace_bytes",
            "mamba_add_norm_fwd", "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes",
-           "mamba_linear_attn_fwd", "mamba_linear_attn_update", "mamba_linear_attn_workspace_bytes",
+           "mamba_linear_attn_fwd", "mamba_linear_attn_update", "mamba_linear_attn_bwd",
+           "mamba_linear_attn_workspace_bytes", "mamba_linear_attn_bwd_workspace_bytes",
            "mamba_qk_norm_rope_fwd", "mamba_qk_norm_rope_bwd", "mamba_qk_norm_rope_bwd_workspace_bytes"]
 
 

@@ -15,7 +15,8 @@ SOURCES = [os.path.join(CSRC, f) for f in ("mamba_scan.hip", "mamba_scan_ts.hip"
                                             "mamba_scan_bwd.hip", "mamba_gemm.hip",
                                             "mamba_block.hip", "mamba_norm.hip", "mamba_delta.hip",
                                             "mamba_delta_step.hip", "mamba_delta_bwd.hip",
-                                            "mamba_qk_norm.hip", "mamba_linear.hip")]
+                                            "mamba_qk_norm.hip", "mamba_linear.hip",
+                                            "mamba_linear_bwd.hip")]
 
 HIPCC_FLAGS = [
     "-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-shared",

@@ -75,7 +75,8 @@ EXPORTS = ("mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
            "mamba_gated_norm_bwd", "mamba_gated_norm_bwd_workspace_bytes", "mamba_add_norm_fwd",
            "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes", "mamba_qk_norm_rope_fwd",
            "mamba_qk_norm_rope_bwd", "mamba_qk_norm_rope_bwd_workspace_bytes", "mamba_linear_attn_fwd",
-           "mamba_linear_attn_workspace_bytes", "mamba_linear_attn_update", "mamba_status_string",
+           "mamba_linear_attn_workspace_bytes", "mamba_linear_attn_update", "mamba_linear_attn_bwd",
+           "mamba_linear_attn_bwd_workspace_bytes", "mamba_status_string",
            "mamba_abi_version")
 
 
@@ -171,6 +172,11 @@ def lib():
             L.mamba_linear_attn_workspace_bytes.restype = sz
             L.mamba_linear_attn_update.argtypes = [fp, vp, vp, vp, fp, f32, vp, ep, vp]
             L.mamba_linear_attn_update.restype = ctypes.c_int
+            L.mamba_linear_attn_bwd.argtypes = [vp, vp, vp, fp, fp, vp, f32, vp, fp, vp, vp, vp, fp, fp,
+                                                ep, vp, sz, vp]
+            L.mamba_linear_attn_bwd.restype = ctypes.c_int
+            L.mamba_linear_attn_bwd_workspace_bytes.argtypes = [ep, ctypes.c_int]
+            L.mamba_linear_attn_bwd_workspace_bytes.restype = sz
             L.mamba_status_string.argtypes = [ctypes.c_int]
             L.mamba_status_string.restype = ctypes.c_char_p
             L.mamba_abi_version.argtypes = []
@@ -650,7 +656,7 @@ def _token_stride(t, name, vec):
 _CHECKED = {}
 _MARSHAL = None
 (_DELTA_FWD, _DELTA_UPDATE, _DELTA_BWD, _GATED_FWD, _GATED_BWD, _ADD_FWD, _ADD_BWD, _QK_FWD,
- _QK_BWD, _LINEAR_FWD, _LINEAR_UPDATE) = range(11)
+ _QK_BWD, _LINEAR_FWD, _LINEAR_UPDATE, _LINEAR_BWD) = range(12)
 
 
 def _marshal():
@@ -949,6 +955,48 @@ def mamba_linear_attn_update(state, q, k, v, g, scale=None, out=None):
         out = m.empty(v)
     _call(_LINEAR_UPDATE, e, e.factor if scale is None else scale, 0, state, q, k, v, g, out)
     return out
+
+
+def mamba_linear_attn_bwd_workspace_bytes(dims: mamba_delta_dims, packed=False) -> int:
+    return int(lib().mamba_linear_attn_bwd_workspace_bytes(ctypes.byref(dims), int(bool(packed))))
+
+
+_LINEAR_GRADS = ("dq", "dk", "dv", "dg", "dinitial_state")
+
+
+def mamba_linear_attn_bwd(q, k, v, g, dout, scale=None, initial_state=None, seq_offsets=None, dlast=None,
+                          workspace=None, grads=None):
+    """Gradients of mamba_linear_attn_fwd (mamba_linear_attn_bwd in include/mamba_scan.h).
+
+    Same inputs as mamba_linear_attn_fwd plus dout (like out) and optionally dlast (like last_state).
+    Returns a dict with dq, dk, dv (io dtype), dg (float32), all contiguous, and dinitial_state
+    (float32; None when initial_state is None).  `grads` may hold preallocated output tensors under the
+    same keys.
+    """
+    if dout is None:
+        raise ValueError("dout is required")
+    gr = dict(grads or {})
+    given = [gr.get(name) for name in _LINEAR_GRADS]
+    m = _MARSHAL or _marshal()
+    key = m.key(_LINEAR_BWD, q, k, v, g, initial_state, seq_offsets, dout, dlast, *given)
+    e = _CHECKED.get(key)
+    if e is None:
+        spec = (_qk_shape, _qk_shape, _out_shape, _head_shape, _state_shape)
+        e = _remember(key, _mixer_check(
+            q, k, v, ((g, "g", torch.float32),),
+            ((initial_state, "initial_state", _state_shape, torch.float32),
+             (dout, "dout", _out_shape, None), (dlast, "dlast", _state_shape, torch.float32),
+             *((t, name, shape, torch.float32 if name in ("dg", "dinitial_state") else None)
+               for t, name, shape in zip(given, _LINEAR_GRADS, spec))),
+            seq_offsets, 2 if seq_offsets is None else 1, lib().mamba_linear_attn_bwd_workspace_bytes))
+    for name, like in zip(_LINEAR_GRADS, (q, q, v, g, initial_state)):
+        if gr.get(name) is None:
+            gr[name] = None if like is None else m.empty(like)
+    workspace, ws_len = _scratch(workspace, q, e)
+    res = {name: gr[name] for name in _LINEAR_GRADS}
+    _call(_LINEAR_BWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, initial_state,
+          seq_offsets, dout, dlast, *res.values(), workspace)
+    return res
 
 
 # ---------------------------------------------------------------------------- norms of a block

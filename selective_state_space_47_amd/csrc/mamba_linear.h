@@ -27,13 +27,15 @@ using namespace delta;
 
 constexpr int kWaves4 = 4;
 constexpr int kCols = 16 * kWaves4;  // columns of a workgroup
-constexpr int kUnit = 2 * kC;        // tokens between the states that the gradients keep
+// tokens between the states that the gradients keep (fp32: the gradients' tiles of more would not fit the LDS)
+template <typename E>
+constexpr int kUnit = sizeof(E) == 2 ? 2 * kC : kC;
 
 struct PassArgs {
   Args f;              // q, k, v, out in the pass's roles (backwards: k, q, dout, dv); offsets, s0 and last
   const float* gate;   // (tokens, hv)
   float* seg_decay;    // (segment slots, hv): what a segment leaves of the state before it
-  char* img;           // states before (backwards: after) every 128 tokens, as tiles of dv x dk
+  char* img;           // states before (backwards: after) every kUnit tokens, as tiles of dv x dk
   int64_t img_item;    // bytes of one unit and value head
 };
 
@@ -205,9 +207,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
 
     if constexpr (kI) {
       // the state before the unit: 16 bytes of one column per operand
-      if (kRev ? ch % 2 == 1 || ch == nchunks - 1 : ch % 2 == 0) {
+      constexpr int kPer = kUnit<E> / kC;
+      if (kRev ? ch % kPer == kPer - 1 || ch == nchunks - 1 : ch % kPer == 0) {
         const int64_t part = (a.dv + 31) / 32 * 32 * (int64_t)KT::kRow;
-        char* img = p.img + ((slot_base(a, seq, sp.first, kUnit) + ch / 2) * a.hv + vh) * p.img_item +
+        char* img = p.img + ((slot_base(a, seq, sp.first, kUnit<E>) + ch / kPer) * a.hv + vh) * p.img_item +
                     (int64_t)(col + r) * KT::kRow;
         if (col + r < (a.dv + 31) / 32 * 32) {
 #pragma unroll

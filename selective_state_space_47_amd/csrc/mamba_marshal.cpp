@@ -96,7 +96,7 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd, kQkFwd, kQkBwd, kLinearFwd, kLinearUpdate, kEntries };
+enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd, kQkFwd, kQkBwd, kLinearFwd, kLinearUpdate, kLinearBwd, kEntries };
 
 // call(entry, dims address, stream, factor, workspace bytes, *tensors) -> status.  The tensors stand in the
 // order of the entry point's pointers, `factor` is its scale or eps.
@@ -119,7 +119,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   auto fp = [&](int i) { return static_cast<float*>(p[i]); };
-  static const int kTensors[] = {10, 7, 16, 4, 8, 7, 13, 8, 13, 9, 6};
+  static const int kTensors[] = {10, 7, 16, 4, 8, 7, 13, 8, 13, 9, 6, 14};
   if (entry < kDeltaFwd || entry >= kEntries || n - 5 != kTensors[entry]) {
     PyErr_SetString(PyExc_TypeError, "wrong number of tensors for the entry point");
     return nullptr;
@@ -172,6 +172,10 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     case kLinearUpdate:
       st = mamba_linear_attn_update(fp(0), p[1], p[2], p[3], fp(4), f, p[5], static_cast<mamba_delta_dims*>(d),
                                     stream);
+      break;
+    case kLinearBwd:
+      st = mamba_linear_attn_bwd(p[0], p[1], p[2], fp(3), fp(4), static_cast<int64_t*>(p[5]), f, p[6], fp(7), p[8],
+                                 p[9], p[10], fp(11), fp(12), static_cast<mamba_delta_dims*>(d), p[13], ws, stream);
       break;
   }
   Py_END_ALLOW_THREADS

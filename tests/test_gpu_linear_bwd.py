@@ -1,0 +1,164 @@
+"""GPU parity of the gradients of linear attention with a decay per head (mamba_linear_attn_bwd through the C ABI)
+against their fp64 oracle (oracle.linear).  Bounds as in test_gpu_linear; dg additionally token by token, where it
+has to follow a strong decay down: within 1e-5 of the sum of the sizes of the token's own terms (each factor of a
+term carries 16 bits or more, 2^-17 of it, and the decays 2^-22)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import linear
+from selective_state_space_47_amd import binding
+
+from .test_gpu_linear import BF, DEV, F32, IO, LENGTHS, SHAPES, _native, case, check, ids, packed_case, ref_fwd  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+GRADS = ("dq", "dk", "dv", "dg")
+
+
+def run_bwd(t, **kw):
+    return binding.mamba_linear_attn_bwd(t["q"], t["k"], t["v"], t["g"], t["dout"], **kw)
+
+
+def ref_bwd(x, scale, state=None, dlast=None):
+    return linear.linear_bwd_ref(x["q"], x["k"], x["v"], x["g"], scale, x["dout"], state, dlast)
+
+
+def compare(got, ref, io, states=True):
+    for name in GRADS:
+        check(got[name], ref[name], name, io, wide=name == "dg")
+    if states:
+        check(got["dinitial_state"], ref["dinitial_state"], "dinitial_state", io, wide=True)
+
+
+@IO
+@pytest.mark.parametrize("shape", SHAPES, ids=ids)
+def test_backward(shape, io):
+    x, t = case(sum(shape) + 1, *shape, io, slices=shape[1] % 2 == 1)
+    for full in (True, False):
+        print(f"[linear bwd] {shape} {io} states={full}", flush=True)
+        kw = dict(initial_state=t["state"], dlast=t["dlast"]) if full else {}
+        got = run_bwd(t, **kw)
+        ref = ref_bwd(x, shape[4] ** -0.5, x["state"] if full else None, x["dlast"] if full else None)
+        compare(got, ref, io, states=full)
+        if not full:
+            assert got["dinitial_state"] is None
+
+
+@IO
+@pytest.mark.parametrize("lengths", LENGTHS, ids=lambda v: "-".join(map(str, v)))
+def test_packed(lengths, io):
+    x, t, off, one, total = packed_case(lengths, io)
+    print(f"[linear packed bwd] {lengths} {io}", flush=True)
+    grads = {n: torch.full_like(t[{"dv": "dout"}.get(n, n[1:])], 7.0) for n in GRADS}
+    grads = {n: v.contiguous() for n, v in grads.items()}
+    got = run_bwd(t, initial_state=t["state"], dlast=t["dlast"], seq_offsets=off, grads=grads)
+    refs = [ref_bwd(one(s), 72 ** -0.5, x["state"][s:s + 1], x["dlast"][s:s + 1]) for s in range(len(lengths))]
+    for name in GRADS:
+        assert bool((got[name][:3] == 7.0).all()), name
+        check(got[name][3:], np.concatenate([r[name][0] for r in refs]), name, io, wide=name == "dg")
+    check(got["dinitial_state"], np.concatenate([r["dinitial_state"] for r in refs]), "dinitial_state", io, wide=True)
+    for s, n in enumerate(lengths):
+        if n == 0:
+            assert torch.equal(got["dinitial_state"][s], t["dlast"][s])
+
+
+@IO
+@pytest.mark.parametrize("shape", [(1, 4133, 1, 2, 64, 64), (2, 2600, 1, 1, 40, 136), (1, 300, 1, 24, 128, 64)], ids=ids)
+def test_segments_and_split_heads(shape, io):
+    """Few heads and many chunks (segments side by side, both ways), and many value heads of one key head (split among
+    workgroups)."""
+    x, t = case(shape[1] + 1, *shape, io)
+    print(f"[linear long bwd] {shape} {io}", flush=True)
+    got = run_bwd(t, initial_state=t["state"], dlast=t["dlast"])
+    compare(got, ref_bwd(x, shape[4] ** -0.5, x["state"], x["dlast"]), io)
+
+
+@IO
+def test_decay_gradient_token_by_token(io):
+    """A token with a strong decay among tokens with weak ones: its gradient is as small as the pairs that cross it."""
+    B, L, Hk, Hv, dk, dv = 1, 300, 1, 2, 64, 64
+    x, t = case(21, B, L, Hk, Hv, dk, dv, io)
+    for at, v in ((40, -9.0), (64, -14.0), (127, -20.0), (128, -7.0), (200, -30.0), (255, -12.0)):
+        x["g"][:, at] = v
+    x["g"][:, 270] = -np.inf
+    t["g"] = torch.from_numpy(x["g"]).to(DEV)
+    got = run_bwd(t, initial_state=t["state"], dlast=t["dlast"])["dg"].double().cpu().numpy()
+    ref = ref_bwd(x, dk ** -0.5, x["state"], x["dlast"])["dg"]
+    # the sizes of a token's terms: the pairs' weights with every factor's absolute value
+    size = linear.linear_bwd_ref(*(np.abs(x[m]) for m in ("q", "k", "v")), x["g"], dk ** -0.5, np.abs(x["dout"]),
+                                 np.abs(x["state"]), np.abs(x["dlast"]))["dg"]
+    print(f"[linear dg] {io} {np.max(np.abs(got - ref) / (np.abs(ref) + size + 1e-300)):.2e}", flush=True)
+    assert (np.abs(got - ref) <= 1e-5 * size).all()
+    assert (got[:, 270] == 0.0).all()
+
+
+@IO
+def test_extreme_gates(io):
+    x, t = case(12, 2, 150, 1, 3, 64, 64, io)
+    for a in (x, t):
+        a["g"][0, :, 0] = 0.0
+        a["g"][0, 70, 1] = -float("inf")
+        a["g"][0, 100, 1] = -3.0e38
+        a["g"][1, :, 2] = -30.0
+        a["k"][1, 20:30] = 0.0
+        a["dout"][1, 25:40] = 0.0
+    compare(run_bwd(t, initial_state=t["state"], dlast=t["dlast"]), ref_bwd(x, 64 ** -0.5, x["state"], x["dlast"]), io)
+
+
+def test_against_differences():
+    """Directional derivatives of the fp32 forward's loss, taken in fp64."""
+    _, t = case(13, 1, 100, 1, 2, 32, 24, F32)
+    got = run_bwd(t, initial_state=t["state"], dlast=t["dlast"])
+    gen = torch.Generator().manual_seed(0)
+
+    def loss(t):
+        out, last = binding.mamba_linear_attn_fwd(t["q"], t["k"], t["v"], t["g"], initial_state=t["state"],
+                                                  return_last_state=True)
+        return float((out.double() * t["dout"].double()).sum() + (last.double() * t["dlast"].double()).sum())
+
+    for m, name in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("state", "dinitial_state")):
+        d = torch.randn(t[m].shape, generator=gen).to(DEV)
+        h = 2.0 ** -9
+        want = (loss({**t, m: t[m] + h * d}) - loss({**t, m: t[m] - h * d})) / (2 * h)
+        grad = float((got[name].double() * d.double()).sum())
+        size = float(got[name].double().norm() * d.double().norm())
+        # linear in all but g, whose third derivative weighs h^2 / 6 times the square of a few tokens' |d|; the ends
+        # carry 2^-24 of the loss's terms over h
+        assert abs(want - grad) <= 2.0 ** -10 * size, (m, want, grad)
+
+
+@IO
+def test_streams_graphs_and_repeats(io):
+    """The same bits from call to call, on another stream and from a replayed graph."""
+    x, t = case(6, 1, 700, 1, 6, 128, 64, io)
+    kw = dict(initial_state=t["state"], dlast=t["dlast"])
+    want = run_bwd(t, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run_bwd(t, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(want[n], got[n]) for n in want)
+    out = {n: torch.empty_like(v) for n, v in want.items()}
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run_bwd(t, **kw, grads=out, workspace=ws)
+    for turn in range(3):
+        t["dout"].mul_(-0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run_bwd(t, **kw)
+        assert all(torch.equal(want[n], out[n]) for n in want)
+
+
+def test_refusals():
+    _, t = case(7, 2, 10, 1, 2, 64, 64, F32)
+    with pytest.raises(ValueError):
+        run_bwd({**t, "dout": None})
+    with pytest.raises(ValueError):
+        run_bwd({**t, "dout": t["dout"][:, :5]})
+    with pytest.raises(ValueError):
+        run_bwd(t, grads=dict(dg=t["g"].double()))
+    with pytest.raises(ValueError):
+        run_bwd(t, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
