@@ -14,6 +14,8 @@
  *                        whole sequences, one generation step, and the gradients.
  *   mamba_linear_attn_fwd, mamba_linear_attn_update, mamba_linear_attn_bwd
  *                        linear attention with a decay per head, the same without the rule's correction.
+ *   mamba_window_attn_fwd, mamba_window_attn_update, mamba_window_attn_bwd, mamba_window_cache_store
+ *                        causal attention with a sliding window and sinks, and its ring caches.
  *
  * Around them: the block's projections (mamba_gemm_bf16, mamba_block_fwd) and its norms
  * (mamba_gated_norm_*, mamba_add_norm_*; of queries and keys with the rotation, mamba_qk_norm_rope_*).
@@ -470,6 +472,103 @@ int mamba_linear_attn_bwd(const void* q, const void* k, const void* v, const flo
                           const void* dout, const float* dlast, void* dq, void* dk, void* dv, float* dg,
                           float* dinitial_state, const mamba_delta_dims* dims, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/*
+ * Causal attention with a sliding window and sinks: the mixer of constant memory that stands beside the
+ * recurrent ones.  Key j is visible to the query at position p where j <= p and (p - j < window or j < sinks):
+ *     out = sum_j softmax_j(scale q . k_j) v_j over the visible keys
+ * The n_q queries of a sequence are the last of its n_k tokens (position i + n_k - n_q for query i).  A query that
+ * sees no key (only where n_k < n_q) has output zero, log-sum -infinity and no gradients.  Query heads
+ * [h * rep, (h + 1) * rep), rep = q_heads / kv_heads, share key and value head h.  dim is a multiple of 8, at
+ * most 128 (MAMBA_ERR_UNSUPPORTED otherwise).
+ */
+typedef struct mamba_window_dims {
+  int64_t batch;    /* sequences, 1 .. 2^20 */
+  int64_t seqlen;   /* queries per sequence, >= 1; packed: of all of them together */
+  int64_t kv_len;   /* keys per sequence, >= 1; packed: of all of them together */
+  int64_t q_heads;  /* heads of q and out; a multiple of kv_heads, <= 65535 */
+  int64_t kv_heads; /* heads of k and v */
+  int64_t dim;      /* values per head */
+  int64_t q_stride, k_stride, v_stride; /* elements between tokens; 0: heads * dim.  Multiples of 16 bytes
+                                           (MAMBA_ERR_ALIGN otherwise), at most 2^22 */
+  int64_t window;   /* 1 .. 2^40 (kv_len or more: every earlier key) */
+  int64_t sinks;    /* first tokens that stay visible, 0 .. 2^40 */
+  int32_t io_dtype; /* enum mamba_dtype: q, k, v, out, the caches and the gradients */
+  int32_t reserved; /* set to 0 */
+} mamba_window_dims;
+
+/*
+ * Attention over whole sequences.
+ *   q          : (batch, seqlen, q_heads, dim), io_dtype, tokens q_stride apart
+ *   k, v       : (batch, kv_len, kv_heads, dim), io_dtype, tokens k_stride and v_stride apart
+ *   q_offsets, kv_offsets : both NULL, or (batch + 1) device int64 token offsets of packed sequences, ascending
+ *                from 0 to seqlen and to kv_len (empty ones allowed; the two may be the same array).  They are
+ *                read on the device and clamped; tokens that no sequence holds are not written.
+ *   out        : (batch, seqlen, q_heads, dim), io_dtype, contiguous
+ *   lse        : (batch, seqlen, q_heads) fp32, or NULL: log sum_j exp(scale q . k_j)
+ * q, k, v and out are 16-byte aligned.  Scores, maximum, sum and output are fp32; with bf16 storage the
+ * probabilities enter the product with v as bf16.  seqlen and kv_len are below 2^31 - 1024, tokens * heads * dim
+ * at most 2^40 (MAMBA_ERR_SHAPE otherwise).  Work goes by 32 queries and 64 keys: a NaN or an infinity in a v reaches,
+ * of its value column, also queries that do not see it where one of the same 32 sees a key of its 64 (one in a k does
+ * not, and other sequences' tokens never do).  In the gradients one in any input reaches what shares such a block
+ * with it.
+ */
+int mamba_window_attn_fwd(const void* q, const void* k, const void* v, const int64_t* q_offsets,
+                          const int64_t* kv_offsets, float scale, void* out, float* lse,
+                          const mamba_window_dims* dims, void* stream);
+
+/* Bytes of device workspace mamba_window_attn_bwd needs (0 for invalid dims; packed != 0: for a call with offsets):
+ * two numbers per query and head, and with sinks that queries outside their window see, fp32 sums of dk and dv per
+ * 1024 queries and key head for each 128 (fp32 storage: 64) of the sinks. */
+size_t mamba_window_attn_bwd_workspace_bytes(const mamba_window_dims* dims, int packed);
+
+/*
+ * Gradients of mamba_window_attn_fwd for the loss sum(out * dout); out and lse are the forward's (with bf16 storage
+ * dout . out is taken from the weights, not from the rounded out).
+ *   dout       : (batch, seqlen, q_heads, dim), io_dtype, contiguous
+ *   dq         : like out;  dk, dv : (batch, kv_len, kv_heads, dim), io_dtype, contiguous, summed over the query
+ *                heads that share the head
+ *   workspace  : >= mamba_window_attn_bwd_workspace_bytes bytes, 16-byte aligned
+ * Every output is overwritten (keys that no query sees get zero); tokens that no sequence holds are not
+ * written.  Sums are taken in a fixed order (bitwise reproducible).
+ */
+int mamba_window_attn_bwd(const void* q, const void* k, const void* v, const int64_t* q_offsets,
+                          const int64_t* kv_offsets, float scale, const void* out, const float* lse,
+                          const void* dout, void* dq, void* dk, void* dv, const mamba_window_dims* dims,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Writes the keys and values of sequences that begin at position 0 into their ring caches: position p lies in
+ * slot p below `sinks`, in slot sinks + (p - sinks) mod window from there on; of several positions with one slot
+ * the last stays.  Slots without a position are not written.
+ *   k, v             : as for mamba_window_attn_fwd (kv_len, kv_heads, strides; seqlen and q_heads are ignored)
+ *   kv_offsets       : NULL, or as for mamba_window_attn_fwd
+ *   k_cache, v_cache : (batch, sinks + window, kv_heads, dim), io_dtype, contiguous, 16-byte aligned
+ */
+int mamba_window_cache_store(const void* k, const void* v, const int64_t* kv_offsets, void* k_cache,
+                             void* v_cache, const mamba_window_dims* dims, void* stream);
+
+/* Bytes of device workspace mamba_window_attn_update needs (0 for invalid dims, and where the sequences and heads
+ * alone fill the GPU): partial sums of the parts that the slots are split into. */
+size_t mamba_window_attn_update_workspace_bytes(const mamba_window_dims* dims);
+
+/*
+ * One generation step for `batch` sequences (dims->seqlen and kv_len must be 1) against their ring caches: the
+ * new token's key and value are written into their slot, and its query attends over every slot that holds a
+ * position.
+ *   q, k, v          : as for mamba_window_attn_fwd with one token per sequence
+ *   positions        : (batch) device int64: the new token's position, the number of tokens before it; below
+ *                      zero: the sequence has no token in this step, nothing of it is read or written but a
+ *                      row of zeros in out
+ *   k_cache, v_cache : as for mamba_window_cache_store.  Slots that no position of the sequence has written
+ *                      are not read
+ *   out              : (batch, q_heads, dim), io_dtype, contiguous
+ *   workspace        : >= mamba_window_attn_update_workspace_bytes bytes, 16-byte aligned (NULL where that is 0)
+ * fp32 arithmetic.
+ */
+int mamba_window_attn_update(void* k_cache, void* v_cache, const void* q, const void* k, const void* v,
+                             const int64_t* positions, float scale, void* out, const mamba_window_dims* dims,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* Sizes of the gated norm.  rows * groups is below 2^31, dim at most 16384 and groups at most 65535
  * (MAMBA_ERR_SHAPE otherwise). */

@@ -17,6 +17,8 @@ __all__ = ["mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
            "mamba_add_norm_fwd", "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes",
            "mamba_linear_attn_fwd", "mamba_linear_attn_update", "mamba_linear_attn_bwd",
            "mamba_linear_attn_workspace_bytes", "mamba_linear_attn_bwd_workspace_bytes",
+           "mamba_window_attn_fwd", "mamba_window_attn_update", "mamba_window_attn_bwd", "mamba_window_cache_store",
+           "mamba_window_attn_bwd_workspace_bytes", "mamba_window_attn_update_workspace_bytes",
            "mamba_qk_norm_rope_fwd", "mamba_qk_norm_rope_bwd", "mamba_qk_norm_rope_bwd_workspace_bytes"]
 
 

@@ -16,7 +16,8 @@ SOURCES = [os.path.join(CSRC, f) for f in ("mamba_scan.hip", "mamba_scan_ts.hip"
                                             "mamba_block.hip", "mamba_norm.hip", "mamba_delta.hip",
                                             "mamba_delta_step.hip", "mamba_delta_bwd.hip",
                                             "mamba_qk_norm.hip", "mamba_linear.hip",
-                                            "mamba_linear_bwd.hip")]
+                                            "mamba_linear_bwd.hip", "mamba_window.hip",
+                                            "mamba_window_bwd.hip", "mamba_window_step.hip")]
 
 HIPCC_FLAGS = [
     "-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-shared",

@@ -59,6 +59,14 @@ class mamba_add_norm_dims(ctypes.Structure):
                 ("res_dtype", ctypes.c_int32)]
 
 
+class mamba_window_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("kv_len", ctypes.c_int64),
+                ("q_heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("window", ctypes.c_int64), ("sinks", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class mamba_qk_norm_rope_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("k_heads", ctypes.c_int64),
                 ("dim", ctypes.c_int64), ("rotary_dim", ctypes.c_int64),
@@ -76,7 +84,9 @@ EXPORTS = ("mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_conv", "m
            "mamba_add_norm_bwd", "mamba_add_norm_bwd_workspace_bytes", "mamba_qk_norm_rope_fwd",
            "mamba_qk_norm_rope_bwd", "mamba_qk_norm_rope_bwd_workspace_bytes", "mamba_linear_attn_fwd",
            "mamba_linear_attn_workspace_bytes", "mamba_linear_attn_update", "mamba_linear_attn_bwd",
-           "mamba_linear_attn_bwd_workspace_bytes", "mamba_status_string",
+           "mamba_linear_attn_bwd_workspace_bytes", "mamba_window_attn_fwd", "mamba_window_attn_bwd",
+           "mamba_window_attn_bwd_workspace_bytes", "mamba_window_cache_store", "mamba_window_attn_update",
+           "mamba_window_attn_update_workspace_bytes", "mamba_status_string",
            "mamba_abi_version")
 
 
@@ -177,6 +187,20 @@ def lib():
             L.mamba_linear_attn_bwd.restype = ctypes.c_int
             L.mamba_linear_attn_bwd_workspace_bytes.argtypes = [ep, ctypes.c_int]
             L.mamba_linear_attn_bwd_workspace_bytes.restype = sz
+            wp = ctypes.POINTER(mamba_window_dims)
+            L.mamba_window_attn_fwd.argtypes = [vp, vp, vp, vp, vp, f32, vp, fp, wp, vp]
+            L.mamba_window_attn_fwd.restype = ctypes.c_int
+            L.mamba_window_attn_bwd.argtypes = [vp, vp, vp, vp, vp, f32, vp, fp, vp, vp, vp, vp, wp, vp,
+                                                sz, vp]
+            L.mamba_window_attn_bwd.restype = ctypes.c_int
+            L.mamba_window_attn_bwd_workspace_bytes.argtypes = [wp, ctypes.c_int]
+            L.mamba_window_attn_bwd_workspace_bytes.restype = sz
+            L.mamba_window_cache_store.argtypes = [vp, vp, vp, vp, vp, wp, vp]
+            L.mamba_window_cache_store.restype = ctypes.c_int
+            L.mamba_window_attn_update.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, wp, vp, sz, vp]
+            L.mamba_window_attn_update.restype = ctypes.c_int
+            L.mamba_window_attn_update_workspace_bytes.argtypes = [wp]
+            L.mamba_window_attn_update_workspace_bytes.restype = sz
             L.mamba_status_string.argtypes = [ctypes.c_int]
             L.mamba_status_string.restype = ctypes.c_char_p
             L.mamba_abi_version.argtypes = []
@@ -656,7 +680,8 @@ def _token_stride(t, name, vec):
 _CHECKED = {}
 _MARSHAL = None
 (_DELTA_FWD, _DELTA_UPDATE, _DELTA_BWD, _GATED_FWD, _GATED_BWD, _ADD_FWD, _ADD_BWD, _QK_FWD,
- _QK_BWD, _LINEAR_FWD, _LINEAR_UPDATE, _LINEAR_BWD) = range(12)
+ _QK_BWD, _LINEAR_FWD, _LINEAR_UPDATE, _LINEAR_BWD, _WINDOW_FWD, _WINDOW_BWD, _WINDOW_UPDATE,
+ _WINDOW_STORE) = range(16)
 
 
 def _marshal():
@@ -997,6 +1022,190 @@ def mamba_linear_attn_bwd(q, k, v, g, dout, scale=None, initial_state=None, seq_
     _call(_LINEAR_BWD, e, e.factor if scale is None else scale, ws_len, q, k, v, g, initial_state,
           seq_offsets, dout, dlast, *res.values(), workspace)
     return res
+
+
+# ---------------------------------------------------------------------------- window attention
+
+def _window_check(q, k, v, window, sinks, seq_offsets, kv_offsets, others, lead, workspace_bytes=None):
+    """The entry of a call on these tensors.  `others`: (tensor or None, name, "q", "kv" or "head", dtype
+    or None for the io dtype); lead: token axes of q (2: batch and tokens; 1: packed tokens, or one token
+    per sequence); workspace_bytes(dims): the library's query, or None."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != lead + 2:
+            raise ValueError(f"{name} must have {lead + 2} dimensions, it has shape {tuple(t.shape)}")
+        if t.device != q.device or t.dtype != q.dtype or t.layout != torch.strided:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, q {q.dtype} on {q.device}")
+    if q.device.type != "cuda":
+        raise ValueError("tensors must be on a HIP device")
+    if isinstance(window, bool) or isinstance(sinks, bool) or not isinstance(window, int) or not isinstance(sinks, int):
+        raise TypeError("window and sinks must be integers")
+    if not 1 <= window <= 1 << 40 or not 0 <= sinks <= 1 << 40:
+        raise ValueError(f"window must be in 1 .. 2^40 and sinks in 0 .. 2^40, not {window} and {sinks}")
+    n_seq = _offsets_count(seq_offsets, q)
+    if kv_offsets is not None and (n_seq is None or _offsets_count(kv_offsets, q) != n_seq):
+        raise ValueError("kv_offsets needs seq_offsets of as many sequences")
+    io, dev = q.dtype, q.device
+    code = _io_code(io)
+    (Hq, d), (Hk, dk) = q.shape[lead:], k.shape[lead:]
+    if v.shape != k.shape or d != dk or (lead == 2 and k.shape[0] != q.shape[0]):
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not belong "
+                         "together")
+    if Hk == 0 or Hq % Hk:
+        raise ValueError(f"{Hq} query heads are no multiple of {Hk} key heads")
+    if n_seq is not None:
+        if kv_offsets is None and k.shape[0] != q.shape[0]:
+            raise ValueError(f"q has {q.shape[0]} tokens, k {k.shape[0]}: kv_offsets is required")
+        batch, L, Lk = n_seq, q.shape[0], k.shape[0]
+    elif lead == 1:
+        if k.shape[0] != q.shape[0]:
+            raise ValueError(f"q has {q.shape[0]} sequences, k {k.shape[0]}")
+        batch, L, Lk = q.shape[0], 1, 1
+    else:
+        (batch, L), Lk = q.shape[:2], k.shape[1]
+    shapes = dict(q=q.shape, kv=k.shape, head=q.shape[:-1], cache=(batch, window + sinks, Hk, d))
+    for t, name, kind, dt in others:
+        _check(t, name, tuple(shapes[kind]), dt or io, dev)
+    vec = 8 if code == MAMBA_BF16 else 4
+    dm = mamba_window_dims(batch, L, Lk, Hq, Hk, d, _token_stride(q, "q", vec), _token_stride(k, "k", vec),
+                           _token_stride(v, "v", vec), window, sinks, code, 0)
+    need = 0 if workspace_bytes is None else int(workspace_bytes(dm))
+    return _Entry(dm, need, dev, d ** -0.5 if d else 0.0)
+
+
+def mamba_window_attn_fwd(q, k, v, window, sinks=0, scale=None, seq_offsets=None, kv_offsets=None,
+                          return_lse=False, out=None, lse=None):
+    """Causal attention with a sliding window and sinks (mamba_window_attn_fwd in include/mamba_scan.h).
+
+    q: (batch, L, Hq, dim); k, v: (batch, Lk, Hk, dim) -- all float32 or all bfloat16, also slices of one
+    projection's rows; the queries are the last L of Lk tokens.  A query sees the `window` last keys up to
+    its own and the first `sinks`; a window of Lk is plain causal attention.  scale defaults to
+    dim ** -0.5.  With seq_offsets, an (n + 1,) int64 tensor on the device, the token tensors have no batch
+    axis: (tokens, H, dim), sequence s being tokens seq_offsets[s] .. seq_offsets[s + 1] - 1, of k and v
+    those of kv_offsets where it is given.
+    Returns out (batch, L, Hq, dim), or (out, lse) with lse (batch, L, Hq) float32.
+    """
+    m = _MARSHAL or _marshal()
+    key = m.key(_WINDOW_FWD, q, k, v, window, sinks, seq_offsets, kv_offsets, out, lse)
+    e = _CHECKED.get(key)
+    if e is None:
+        e = _remember(key, _window_check(q, k, v, window, sinks, seq_offsets, kv_offsets,
+                                         ((out, "out", "q", None), (lse, "lse", "head", torch.float32)),
+                                         2 if seq_offsets is None else 1))
+    if out is None:
+        out = m.empty(q)
+    if return_lse and lse is None:
+        lse = m.empty(q, "f", *q.shape[:-1])
+    _call(_WINDOW_FWD, e, e.factor if scale is None else scale, 0, q, k, v, seq_offsets,
+          seq_offsets if kv_offsets is None else kv_offsets, out, lse)
+    return (out, lse) if return_lse else out
+
+
+def mamba_window_attn_bwd_workspace_bytes(dims: mamba_window_dims, packed=False) -> int:
+    return int(lib().mamba_window_attn_bwd_workspace_bytes(ctypes.byref(dims), int(bool(packed))))
+
+
+_WINDOW_GRADS = ("dq", "dk", "dv")
+
+
+def mamba_window_attn_bwd(q, k, v, out, lse, dout, window, sinks=0, scale=None, seq_offsets=None,
+                          kv_offsets=None, workspace=None, grads=None):
+    """Gradients of mamba_window_attn_fwd (mamba_window_attn_bwd in include/mamba_scan.h).
+
+    Same inputs as mamba_window_attn_fwd plus its out and lse, and dout (like out).  Returns a dict with
+    dq, dk and dv (io dtype, contiguous).  `grads` may hold preallocated output tensors under the same
+    keys.
+    """
+    for t, name in ((out, "out"), (lse, "lse"), (dout, "dout")):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    gr = dict(grads or {})
+    given = [gr.get(name) for name in _WINDOW_GRADS]
+    m = _MARSHAL or _marshal()
+    key = m.key(_WINDOW_BWD, q, k, v, window, sinks, seq_offsets, kv_offsets, out, lse, dout, *given)
+    e = _CHECKED.get(key)
+    if e is None:
+        packed = seq_offsets is not None
+        e = _remember(key, _window_check(
+            q, k, v, window, sinks, seq_offsets, kv_offsets,
+            ((out, "out", "q", None), (lse, "lse", "head", torch.float32), (dout, "dout", "q", None),
+             *zip(given, _WINDOW_GRADS, ("q", "kv", "kv"), (None,) * 3)),
+            1 if packed else 2, lambda dm: mamba_window_attn_bwd_workspace_bytes(dm, packed)))
+    for name, like in zip(_WINDOW_GRADS, (q, k, v)):
+        if gr.get(name) is None:
+            gr[name] = m.empty(like)
+    workspace, ws_len = _scratch(workspace, q, e)
+    res = {name: gr[name] for name in _WINDOW_GRADS}
+    _call(_WINDOW_BWD, e, e.factor if scale is None else scale, ws_len, q, k, v, seq_offsets,
+          seq_offsets if kv_offsets is None else kv_offsets, out, lse, dout, *res.values(), workspace)
+    return res
+
+
+def _cache_window(k_cache, v_cache, sinks):
+    """The window of a pair of ring caches."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be (batch, sinks + window, heads, dim), not {tuple(t.shape)}")
+    if isinstance(sinks, bool) or not isinstance(sinks, int):
+        raise TypeError("sinks must be an integer")
+    return k_cache.shape[1] - sinks
+
+
+def mamba_window_cache_store(k_cache, v_cache, k, v, sinks=0, seq_offsets=None):
+    """Fills ring caches from the keys and values of whole sequences (mamba_window_cache_store in
+    include/mamba_scan.h).
+
+    k_cache, v_cache: (batch, sinks + window, Hk, dim), written in place; k, v: (batch, Lk, Hk, dim), or
+    with seq_offsets (tokens, Hk, dim) as for mamba_window_attn_fwd.  Position p lies in slot p below
+    `sinks`, in slot sinks + (p - sinks) % window from there on; slots without one keep what they hold.
+    """
+    m = _MARSHAL or _marshal()
+    key = m.key(_WINDOW_STORE, k_cache, v_cache, k, v, sinks, seq_offsets)
+    e = _CHECKED.get(key)
+    if e is None:
+        window = _cache_window(k_cache, v_cache, sinks)
+        e = _remember(key, _window_check(k, k, v, window, sinks, seq_offsets, None,
+                                         ((k_cache, "k_cache", "cache", None),
+                                          (v_cache, "v_cache", "cache", None)),
+                                         2 if seq_offsets is None else 1))
+    _call(_WINDOW_STORE, e, 0.0, 0, k, v, seq_offsets, k_cache, v_cache)
+
+
+def mamba_window_attn_update_workspace_bytes(dims: mamba_window_dims) -> int:
+    return int(lib().mamba_window_attn_update_workspace_bytes(ctypes.byref(dims)))
+
+
+def mamba_window_attn_update(k_cache, v_cache, q, k, v, positions, sinks=0, scale=None, out=None,
+                             workspace=None):
+    """One generation step of window attention (mamba_window_attn_update in include/mamba_scan.h).
+
+    k_cache, v_cache: (batch, sinks + window, Hk, dim), updated in place; q: (batch, Hq, dim); k, v:
+    (batch, Hk, dim); positions: (batch,) int64, the tokens before the new one (below zero: no token, a
+    row of zeros).  Returns out (batch, Hq, dim).
+    """
+    m = _MARSHAL or _marshal()
+    key = m.key(_WINDOW_UPDATE, k_cache, v_cache, q, k, v, positions, sinks, out)
+    e = _CHECKED.get(key)
+    if e is None:
+        window = _cache_window(k_cache, v_cache, sinks)
+        e = _window_check(q, k, v, window, sinks, None, None,
+                          ((k_cache, "k_cache", "cache", None), (v_cache, "v_cache", "cache", None),
+                           (out, "out", "q", None)), 1, mamba_window_attn_update_workspace_bytes)
+        if positions is None:
+            raise ValueError("positions is required")
+        _check(positions, "positions", (q.shape[0],), torch.int64, q.device)
+        _remember(key, e)
+    if out is None:
+        out = m.empty(q)
+    ws_len = 0
+    if e.workspace_bytes or workspace is not None:
+        workspace, ws_len = _scratch(workspace, q, e)
+    _call(_WINDOW_UPDATE, e, e.factor if scale is None else scale, ws_len, k_cache, v_cache, q, k, v,
+          positions, out, workspace)
+    return out
 
 
 # ---------------------------------------------------------------------------- norms of a block

@@ -96,7 +96,8 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd, kQkFwd, kQkBwd, kLinearFwd, kLinearUpdate, kLinearBwd, kEntries };
+enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd, kQkFwd, kQkBwd, kLinearFwd, kLinearUpdate, kLinearBwd, kWindowFwd, kWindowBwd, kWindowUpdate,
+             kWindowStore, kEntries };
 
 // call(entry, dims address, stream, factor, workspace bytes, *tensors) -> status.  The tensors stand in the
 // order of the entry point's pointers, `factor` is its scale or eps.
@@ -119,7 +120,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   auto fp = [&](int i) { return static_cast<float*>(p[i]); };
-  static const int kTensors[] = {10, 7, 16, 4, 8, 7, 13, 8, 13, 9, 6, 14};
+  static const int kTensors[] = {10, 7, 16, 4, 8, 7, 13, 8, 13, 9, 6, 14, 7, 12, 8, 5};
   if (entry < kDeltaFwd || entry >= kEntries || n - 5 != kTensors[entry]) {
     PyErr_SetString(PyExc_TypeError, "wrong number of tensors for the entry point");
     return nullptr;
@@ -176,6 +177,22 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     case kLinearBwd:
       st = mamba_linear_attn_bwd(p[0], p[1], p[2], fp(3), fp(4), static_cast<int64_t*>(p[5]), f, p[6], fp(7), p[8],
                                  p[9], p[10], fp(11), fp(12), static_cast<mamba_delta_dims*>(d), p[13], ws, stream);
+      break;
+    case kWindowFwd:
+      st = mamba_window_attn_fwd(p[0], p[1], p[2], static_cast<int64_t*>(p[3]), static_cast<int64_t*>(p[4]), f, p[5],
+                                 fp(6), static_cast<mamba_window_dims*>(d), stream);
+      break;
+    case kWindowBwd:
+      st = mamba_window_attn_bwd(p[0], p[1], p[2], static_cast<int64_t*>(p[3]), static_cast<int64_t*>(p[4]), f, p[5],
+                                 fp(6), p[7], p[8], p[9], p[10], static_cast<mamba_window_dims*>(d), p[11], ws, stream);
+      break;
+    case kWindowUpdate:
+      st = mamba_window_attn_update(p[0], p[1], p[2], p[3], p[4], static_cast<int64_t*>(p[5]), f, p[6],
+                                    static_cast<mamba_window_dims*>(d), p[7], ws, stream);
+      break;
+    case kWindowStore:
+      st = mamba_window_cache_store(p[0], p[1], static_cast<int64_t*>(p[2]), p[3], p[4],
+                                    static_cast<mamba_window_dims*>(d), stream);
       break;
   }
   Py_END_ALLOW_THREADS

@@ -1,0 +1,210 @@
+// mamba_window.hip -- causal attention with a sliding window and sinks on gfx950, forward.
+//
+// For a query at position p, over the keys j <= p with p - j < window or j < sinks:
+//     s_j = scale q . k_j,  out = sum_j exp(s_j - lse) v_j,  lse = log sum_j exp(s_j)
+// in one pass over the keys with the running maximum m and sum l:
+//     m' = max(m, max s),  P = exp(s - m'),  l' = exp(m - m') l + sum P,  O' = exp(m - m') O + P V
+//
+// A workgroup has 4 waves of 32 queries (fp32 storage: 16) of one head and goes through the keys in tiles of 64: the
+// sinks' tiles first, then those that its queries' windows reach.  Products are made transposed, keys x queries and
+// values x queries: a lane holds one query's scores, so that the softmax needs two exchanges per tile, and the
+// accumulators of P are, rounded, the operand of the next product.
+//
+// Rounding, bf16 storage: P enters the product with V as one bf16 part (2^-9 of each weight, independent from key to
+// key, which weighs as much in the output as its own rounding); scores, m, l and O are fp32.
+#include "mamba_window.h"
+
+namespace mamba {
+namespace window {
+namespace {
+
+template <typename E>
+constexpr int kTilesQ = sizeof(E) == 2 ? 2 : 1;  // 16-query tiles of a wave
+template <typename E>
+constexpr int kQueries = 4 * 16 * kTilesQ<E>;    // of a workgroup
+
+template <typename E, int DK>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel(WinArgs a, uint32_t blocks) {
+  using M = Mma<E>;
+  using KT = KeyTile<E, DK>;
+  constexpr int kC2 = kTilesQ<E>, kQ = kQueries<E>, kStage = 2 * KT::kBytes;
+  __shared__ __align__(1024) char smem[2 * kStage];
+  const uint32_t id = wide_index();
+  if (id >= blocks) return;
+  const int64_t wg = spread_index(id, blocks, a.rep);
+  const int64_t slot = wg / a.hq;
+  const int h = (int)(wg - slot * a.hq), kh = h / a.rep;
+  const int64_t seq = tile_seq(a.q_offsets, a.seqlen, a.nseq, slot, kQ);
+  const Seq qs = seq_of(a.q_offsets, a.seqlen, seq), ks = seq_of(a.kv_offsets, a.kv_len, seq);
+  const int64_t tile = slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, kQ);
+  if (tile < 0 || tile * kQ >= qs.len) return;  // an unused slot of a packed batch
+  const int q0 = (int)tile * kQ, nq = min(qs.len - q0, kQ);
+  const int shift = ks.len - qs.len;  // position of query 0
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w0 = 16 * kC2 * w;  // this wave's first query in the tile
+  const Mask mask = mask_of(a);
+
+  // tiles of keys: the sinks' that lie before the windows, then the windows'
+  const int p0 = q0 + shift, p1 = p0 + nq - 1;  // positions
+  const int lo = (int)(max((int64_t)p0 - a.window + 1, (int64_t)0) / kKeys);
+  const int sink_tiles = min((mask.sinks + (kKeys - 1ll)) / kKeys, (int64_t)lo);
+  const int count = p1 < 0 ? 0 : sink_tiles + p1 / kKeys - lo + 1;
+  auto tile_at = [&](int i) { return i < sink_tiles ? i : lo + i - sink_tiles; };
+
+  const E* kp = static_cast<const E*>(a.k) + ks.first * a.k_stride + (int64_t)kh * a.dim;
+  const E* vp = static_cast<const E*>(a.v) + ks.first * a.v_stride + (int64_t)kh * a.dim;
+  const uint32_t lds0 = lds_address(smem);
+  const RowCopy<E, KT, kKeys, 4> ck(w, lane, a.k_stride, a.dim), cv(w, lane, a.v_stride, a.dim);
+  auto copy = [&](int t, int st) {  // keys past the sequence are past the buffers and read as zero
+    const int64_t j = (int64_t)t * kKeys, n = min((int64_t)kKeys, ks.len - j);
+    ck(rows_buffer(kp + j * a.k_stride, n, a.k_stride, a.dim), lds0 + st * kStage, w);
+    cv(rows_buffer(vp + j * a.v_stride, n, a.v_stride, a.dim), lds0 + st * kStage + KT::kBytes, w);
+  };
+  if (count) copy(tile_at(0), 0);
+
+  // operands: column = query; a negative scale goes into the sign of q, so that a maximum of q . k is one of s
+  typename M::Frag qf[kC2][DK / M::kDepth];
+  const E* qp = static_cast<const E*>(a.q) + (qs.first + q0) * a.q_stride + (int64_t)h * a.dim;
+#pragma unroll
+  for (int c = 0; c < kC2; ++c) {
+    load_rows<E, DK>(qp, a.q_stride, w0 + 16 * c + r, nq, a.dim, g, qf[c]);
+    if (a.scale < 0.f)
+#pragma unroll
+      for (int kb = 0; kb < DK / M::kDepth; ++kb) qf[c][kb] = -qf[c][kb];
+  }
+  const float sc = fabsf(a.scale) * kLog2e;
+  f32x4 o[kC2][DK / 16];
+  float mx[kC2], l[kC2];
+#pragma unroll
+  for (int c = 0; c < kC2; ++c) {
+    mx[c] = kMinusInf;
+    l[c] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) o[c][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  const KT kt(lane);
+  const int pw0 = p0 + w0, pw1 = pw0 + 16 * kC2 - 1;
+  for (int i = 0; i < count; ++i) {
+    const int st = i & 1, j0 = tile_at(i) * kKeys;
+    copies_done();
+    if (i + 1 < count) copy(tile_at(i + 1), st ^ 1);
+    if (mask.none(pw0, pw1, j0, j0 + kKeys - 1)) continue;
+    const lds_ptr sk = (lds_ptr)(smem + st * kStage), sv = sk + KT::kBytes;
+    f32x4 s[kC2][4];
+#pragma unroll
+    for (int c = 0; c < kC2; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) s[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const auto kf = kt.rows(sk, m, kb);
+#pragma unroll
+        for (int c = 0; c < kC2; ++c) s[c][m] = M::mma(kf, qf[c][kb], s[c][m]);
+      }
+    const bool whole = mask.all(pw0, pw1, j0, j0 + kKeys - 1);
+#pragma unroll
+    for (int c = 0; c < kC2; ++c) {
+      const int p = pw0 + 16 * c + r;
+      if (!whole)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (!mask.sees(p, j0 + 16 * m + 4 * g + x)) s[c][m][x] = kMinusInf;
+      float top = mx[c];
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top = fmaxf(top, s[c][m][x]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float use = top == kMinusInf ? 0.f : top * sc;  // (nothing seen yet)
+      if (__any(top > mx[c])) {
+        const float f = mx[c] == kMinusInf ? 0.f : fast_exp2(fmaf(mx[c], sc, -use));
+        l[c] *= f;
+#pragma unroll
+        for (int d = 0; d < DK / 16; ++d) o[c][d] *= f;
+        mx[c] = top;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float e = s[c][m][x];
+          float pr = fast_exp2(fmaf(e, sc, -use));
+          if (!whole) pr = e == kMinusInf ? 0.f : pr;
+          s[c][m][x] = pr;
+          sum += pr;
+        }
+      l[c] += sum;
+    }
+#pragma unroll
+    for (int kb = 0; kb < kKeys / M::kDepth; ++kb) {
+      typename M::Frag pf[kC2];
+#pragma unroll
+      for (int c = 0; c < kC2; ++c) pf[c] = M::pack(&s[c][kb * M::kTiles]);
+#pragma unroll
+      for (int d = 0; d < DK / 16; ++d) {
+        const auto vf = kt.cols(sv, d, kb);
+#pragma unroll
+        for (int c = 0; c < kC2; ++c) o[c][d] = M::mma(vf, pf[c], o[c][d]);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kC2; ++c) {
+    const int i = w0 + 16 * c + r;
+    const float sum = across_groups(l[c]);
+    if (i >= nq) continue;
+    const int64_t row = (qs.first + q0 + i) * a.hq + h;
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+    if (a.lse && g == 0)
+      a.lse[row] = sum == 0.f ? kMinusInf : fmaf(mx[c], sc, __builtin_amdgcn_logf(sum)) * kLn2;
+    E* to = static_cast<E*>(a.out) + row * a.dim;
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) o[c][d] *= inv;
+#pragma unroll
+    for (int d = 0; d < DK / 16; d += M::kTiles)
+      if (KT::value(d, g, 0) < a.dim) store_operand(to + KT::value(d, g, 0), &o[c][d]);
+  }
+}
+
+template <typename E, int DK>
+int launch_fwd(const WinArgs& a, hipStream_t s) {
+  const uint32_t blocks =
+      (uint32_t)(tile_slots(a.seqlen, a.nseq, a.q_offsets != nullptr, kQueries<E>) * a.hq);
+  hipLaunchKernelGGL((window_fwd_kernel<E, DK>), wide_grid(blocks, 256), dim3(256), 0, s, a, blocks);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace window
+}  // namespace mamba
+
+using namespace mamba;
+using namespace mamba::window;
+
+extern "C" {
+
+int mamba_window_attn_fwd(const void* q, const void* k, const void* v, const int64_t* q_offsets,
+                          const int64_t* kv_offsets, float scale, void* out, float* lse, const mamba_window_dims* dims,
+                          void* stream) {
+  int st = check_window(dims, q_offsets != nullptr);
+  if (st != MAMBA_OK) return st;
+  if (!out) return MAMBA_ERR_NULL;
+  if ((st = check_window_inputs(q, k, v, q_offsets, kv_offsets)) != MAMBA_OK) return st;
+  if (!aligned(out, 16) || (lse && !aligned(lse, 4))) return MAMBA_ERR_ALIGN;
+  WinArgs a = window_args(dims, scale, q, k, v, q_offsets, kv_offsets);
+  a.out = out;
+  a.lse = lse;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dims->io_dtype == MAMBA_BF16)
+    return a.dim <= 64 ? launch_fwd<uint16_t, 64>(a, s) : launch_fwd<uint16_t, 128>(a, s);
+  return a.dim <= 64 ? launch_fwd<float, 64>(a, s) : launch_fwd<float, 128>(a, s);
+}
+
+}  // extern "C"

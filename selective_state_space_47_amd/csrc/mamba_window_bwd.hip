@@ -1,0 +1,538 @@
+// mamba_window_bwd.hip -- gradients of attention with a sliding window and sinks on gfx950.
+//
+//     P_ij = exp(s_ij - lse_i),  D_i = sum_j P_ij (dO_i . v_j) = dO_i . out_i,  dS_ij = P_ij (dO_i . v_j - D_i)
+//     dV_j = sum_i P_ij dO_i,   dK_j = scale sum_i dS_ij q_i,   dQ_i = scale sum_j dS_ij k_j
+//
+//   window_stat_kernel  fp32 storage: lse log2(e) and D = dO . out of every query and head, head by head
+//   window_dq_kernel    as the forward, 128 queries (fp32 storage: 64) through their keys; with bf16 storage twice, first
+//                       for D, which it leaves for the next kernel with lse log2(e)
+//   window_dkv_kernel   128 keys (64) of one head, through the queries that see them, heads that share it one after
+//                       another: sums in accumulators in a fixed order, no atomics
+// The sinks are seen by every later query: the queries past the windows of a sinks' tile are cut into stretches,
+// which window_dkv_kernel takes first, as workgroups of their own that leave fp32 sums; the tile's own workgroup, of
+// a launch after that, adds them in order.  Without this one workgroup would go through a whole long sequence.
+//
+// The scores are made again in each kernel (nine products in place of five): dQ summed over the keys' workgroups
+// would need atomics, whose order changes results, or a sum in memory per tile of keys.  And D from the rounded out
+// would carry 2^-9 of dO . out into dS, which is the small difference of two numbers of that size where a few keys have
+// all the weight (4 keys, scores of deviation 3.4: dq was off by 5.4e-3).
+//
+// Rounding, bf16 storage: P and dS enter their products as one bf16 part each; the rest is fp32.
+#include "mamba_window.h"
+
+namespace mamba {
+namespace window {
+namespace {
+
+template <typename E>
+constexpr int kTilesW = sizeof(E) == 2 ? 2 : 1;  // 16-row tiles of a wave
+template <typename E>
+constexpr int kRows = 4 * 16 * kTilesW<E>;       // of a workgroup
+constexpr int kFar = 1024;                       // queries of a stretch past the sinks' windows
+
+// 8 lanes per row; a row without a key has weights of zero: its log-sum counts as +infinity
+template <typename E>
+__global__ __launch_bounds__(256) void window_stat_kernel(WinArgs a, int64_t tokens) {
+  const int64_t row = ((int64_t)wide_index() * 256 + threadIdx.x) / 8;  // head by head, token by token
+  if (row >= tokens * a.hq) return;
+  const int64_t h = row / tokens, t = row - h * tokens;
+  const int64_t at = t * a.hq + h;
+  const E* x = static_cast<const E*>(a.out) + at * a.dim;
+  const E* y = static_cast<const E*>(a.dout) + at * a.dim;
+  constexpr int kV = 16 / sizeof(E);
+  typedef typename Mma<E>::Frag Frag;
+  float s = 0.f;
+  for (int c = (threadIdx.x & 7) * kV; c < a.dim; c += 8 * kV) {
+    const Frag u = *reinterpret_cast<const Frag*>(x + c), v = *reinterpret_cast<const Frag*>(y + c);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) s = fmaf((float)u[i], (float)v[i], s);
+  }
+  s += __shfl_xor(s, 1);
+  s += __shfl_xor(s, 2);
+  s += __shfl_xor(s, 4);
+  if ((threadIdx.x & 7) == 0) {
+    const float lse = a.lse[at];
+    a.stat[row] = lse == kMinusInf ? -kMinusInf : lse * kLog2e;
+    a.stat[tokens * a.hq + row] = s;
+  }
+}
+
+// kFarPart: a stretch of queries past the windows of a sinks' tile; otherwise a tile of keys
+template <typename E, int DK, bool kFarPart>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(WinArgs a, uint32_t blocks,
+                                                                                 int64_t tokens) {
+  using M = Mma<E>;
+  using KT = KeyTile<E, DK>;
+  constexpr int kC2 = kTilesW<E>, kN = kRows<E>, kStage = 2 * KT::kBytes;
+  __shared__ __align__(1024) char smem[2 * kStage];
+  __shared__ __align__(16) float stats[2][2][kKeys];
+  const uint32_t id = wide_index();
+  if (id >= blocks) return;
+  int64_t seq, tile, far_slot = 0, stretch = 0;
+  int kh;
+  if (kFarPart) {
+    const uint32_t per = (uint32_t)(a.hk * a.sink_tiles);
+    far_slot = id / per;
+    const int rest = (int)(id - far_slot * per);
+    kh = rest / a.sink_tiles;
+    tile = rest - kh * a.sink_tiles;
+    seq = tile_seq(a.q_offsets, a.seqlen, a.nseq, far_slot, kFar);
+  } else {
+    const int64_t slot = id / (uint32_t)a.hk;
+    kh = (int)(id - slot * a.hk);
+    seq = tile_seq(a.kv_offsets, a.kv_len, a.nseq, slot, kN);
+    tile = slot;
+  }
+  const Seq qs = seq_of(a.q_offsets, a.seqlen, seq), ks = seq_of(a.kv_offsets, a.kv_len, seq);
+  if (kFarPart)
+    stretch = far_slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
+  else
+    tile -= tile_base(a.kv_offsets, a.kv_len, seq, ks.first, kN);
+  if (tile < 0 || tile * kN >= ks.len || stretch < 0) return;
+  const int j0 = (int)tile * kN, nk = min(ks.len - j0, kN);
+  const int shift = ks.len - qs.len;
+  const Mask mask = mask_of(a);
+  // Queries: those whose position is not before the tile's first key and, windows of the tile or not, up to the last
+  // that has its last key in its window; the stretches begin behind those.
+  const int64_t near_end = min((int64_t)j0 + nk - 1 + a.window - shift, (int64_t)qs.len);  // first query past them
+  int q_lo = max(j0 - shift, 0), q_hi = (int)max(near_end, (int64_t)0);
+  if (kFarPart) {
+    const int64_t b = max(near_end, (int64_t)q_lo) + stretch * kFar;
+    q_lo = (int)min(b, (int64_t)qs.len);
+    q_hi = (int)min(b + kFar, (int64_t)qs.len);
+    if (q_lo >= q_hi) return;
+  }
+  const int t_lo = q_lo / kKeys, tiles = q_hi > q_lo ? (q_hi - 1) / kKeys - t_lo + 1 : 0;
+  const int count = tiles * a.rep;  // heads one after another
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w0 = 16 * kC2 * w;
+
+  const int64_t o_stride = (int64_t)a.hq * a.dim;
+  const E* qp = static_cast<const E*>(a.q) + qs.first * a.q_stride + (int64_t)kh * a.rep * a.dim;
+  const E* op = static_cast<const E*>(a.dout) + qs.first * o_stride + (int64_t)kh * a.rep * a.dim;
+  const uint32_t lds0 = lds_address(smem);
+  const RowCopy<E, KT, kKeys, 4> cq(w, lane, a.q_stride, a.dim), co(w, lane, o_stride, a.dim);
+  auto copy = [&](int i, int st) {
+    const int h = i / tiles, t = (t_lo + i - h * tiles) * kKeys;
+    const int64_t n = min(kKeys, qs.len - t);
+    cq(rows_buffer(qp + t * a.q_stride + (int64_t)h * a.dim, n, a.q_stride, a.dim), lds0 + st * kStage, w);
+    co(rows_buffer(op + t * o_stride + (int64_t)h * a.dim, n, o_stride, a.dim), lds0 + st * kStage + KT::kBytes, w);
+  };
+  // threads 0-63 the log-sums, 64-127 the dots; past the sequence +infinity and 0
+  auto load_stat = [&](int i) {
+    const int h = i / tiles, t = (t_lo + i - h * tiles) * kKeys + (threadIdx.x & 63);
+    const int which = threadIdx.x >> 6;
+    if (which > 1) return 0.f;
+    return t < qs.len ? a.stat[((int64_t)which * a.hq + kh * a.rep + h) * tokens + qs.first + t]
+                      : which ? 0.f : -kMinusInf;
+  };
+  auto put_stat = [&](float v, int st) {
+    if (threadIdx.x < 128) stats[st][threadIdx.x >> 6][threadIdx.x & 63] = v;
+  };
+  if (count) {
+    copy(0, 0);
+    put_stat(load_stat(0), 0);
+  }
+  typename M::Frag kf[kC2][DK / M::kDepth], vf[kC2][DK / M::kDepth];
+  const E* kp = static_cast<const E*>(a.k) + (ks.first + j0) * a.k_stride + (int64_t)kh * a.dim;
+  const E* vp = static_cast<const E*>(a.v) + (ks.first + j0) * a.v_stride + (int64_t)kh * a.dim;
+#pragma unroll
+  for (int c = 0; c < kC2; ++c) {
+    load_rows<E, DK>(kp, a.k_stride, w0 + 16 * c + r, nk, a.dim, g, kf[c]);
+    load_rows<E, DK>(vp, a.v_stride, w0 + 16 * c + r, nk, a.dim, g, vf[c]);
+  }
+  const float sc = a.scale * kLog2e;
+  f32x4 dk[kC2][DK / 16], dv[kC2][DK / 16];
+#pragma unroll
+  for (int c = 0; c < kC2; ++c)
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) dk[c][d] = dv[c][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const KT kt(lane);
+  const int jw0 = j0 + w0, jw1 = jw0 + 16 * kC2 - 1;
+  for (int i = 0; i < count; ++i) {
+    const int st = i & 1, h = i / tiles, q0 = (t_lo + i - h * tiles) * kKeys;
+    float next = 0.f;
+    copies_done();
+    if (i + 1 < count) {
+      next = load_stat(i + 1);
+      copy(i + 1, st ^ 1);
+    }
+    const lds_ptr sq = (lds_ptr)(smem + st * kStage), so = sq + KT::kBytes;
+    const int p0 = q0 + shift;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int ph = p0 + 32 * half;
+      if (mask.none(ph, ph + 31, jw0, jw1)) continue;
+      // 32 queries: scores and dO V^T, rows = queries, column = key
+      f32x4 s[kC2][2], e[kC2][2];
+#pragma unroll
+      for (int c = 0; c < kC2; ++c)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < DK / M::kDepth; ++kb)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const auto qf = kt.rows(sq, 2 * half + m, kb), of = kt.rows(so, 2 * half + m, kb);
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) {
+            s[c][m] = M::mma(qf, kf[c][kb], s[c][m]);
+            e[c][m] = M::mma(of, vf[c][kb], e[c][m]);
+          }
+        }
+      const bool whole = !kFarPart && mask.all(ph, ph + 31, jw0, jw1) && q0 + 32 * half + 32 <= q_hi;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int at = 32 * half + 16 * m + 4 * g;
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[st][0][at]);
+        const f32x4 ds = *reinterpret_cast<const f32x4*>(&stats[st][1][at]);
+#pragma unroll
+        for (int c = 0; c < kC2; ++c)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float p = fast_exp2(fmaf(s[c][m][x], sc, -ls[x]));
+            if (!whole) {
+              const int qi = q0 + at + x, j = jw0 + 16 * c + r;
+              bool live = mask.sees(qi + shift, j);
+              if (kFarPart) live = live && qi >= q_lo && qi < q_hi;
+              else live = live && qi < q_hi;
+              p = live ? p : 0.f;
+            }
+            s[c][m][x] = p;
+            e[c][m][x] = p == 0.f ? 0.f : p * (e[c][m][x] - ds[x]);
+          }
+      }
+#pragma unroll
+      for (int kb = 0; kb < 32 / M::kDepth; ++kb) {
+        typename M::Frag pf[kC2], ef[kC2];
+#pragma unroll
+        for (int c = 0; c < kC2; ++c) {
+          pf[c] = M::pack(&s[c][kb * M::kTiles]);
+          ef[c] = M::pack(&e[c][kb * M::kTiles]);
+        }
+        const int b = half * (32 / M::kDepth) + kb;
+#pragma unroll
+        for (int d = 0; d < DK / 16; ++d) {
+          const auto of = kt.cols(so, d, b), qf = kt.cols(sq, d, b);
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) {
+            dv[c][d] = M::mma(of, pf[c], dv[c][d]);
+            dk[c][d] = M::mma(qf, ef[c], dk[c][d]);
+          }
+        }
+      }
+    }
+    if (i + 1 < count) put_stat(next, st ^ 1);
+  }
+  // sums of a stretch: (far slot, head, tile, dk and dv, keys, DK)
+  const int64_t far_size = 2ll * kN * a.dim;
+  auto far_at = [&](int64_t slot) {
+    return a.far + ((slot * a.hk + kh) * a.sink_tiles + tile) * far_size;
+  };
+  if (!kFarPart && tile < a.sink_tiles) {
+    const int64_t first = max(near_end, (int64_t)max(j0 - shift, 0)), base = tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
+    const int64_t stretches = first < qs.len ? (qs.len - first + kFar - 1) / kFar : 0;
+    for (int64_t x = 0; x < stretches; ++x) {
+      const float* from = far_at(base + x);
+#pragma unroll
+      for (int c = 0; c < kC2; ++c) {
+        const int j = w0 + 16 * c + r;
+        if (j < nk)
+#pragma unroll
+          for (int d = 0; d < DK / 16; ++d) {
+            const int v = KT::value(d, g, 0);
+            if (v < a.dim) {
+              dk[c][d] += *reinterpret_cast<const f32x4*>(from + j * a.dim + v);
+              dv[c][d] += *reinterpret_cast<const f32x4*>(from + (kN + j) * a.dim + v);
+            }
+          }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kC2; ++c) {
+    const int j = w0 + 16 * c + r;
+    if (j >= nk) continue;
+    if (kFarPart) {
+      float* to = far_at(far_slot);
+#pragma unroll
+      for (int d = 0; d < DK / 16; ++d) {
+        const int v = KT::value(d, g, 0);
+        if (v < a.dim) {
+          *reinterpret_cast<f32x4*>(to + j * a.dim + v) = dk[c][d];
+          *reinterpret_cast<f32x4*>(to + (kN + j) * a.dim + v) = dv[c][d];
+        }
+      }
+    } else {
+      const int64_t at = ((ks.first + j0 + j) * a.hk + kh) * (int64_t)a.dim;
+#pragma unroll
+      for (int d = 0; d < DK / 16; ++d) dk[c][d] *= a.scale;
+#pragma unroll
+      for (int d = 0; d < DK / 16; d += M::kTiles) {
+        const int v = KT::value(d, g, 0);
+        if (v < a.dim) {
+          store_operand(static_cast<E*>(a.dk) + at + v, &dk[c][d]);
+          store_operand(static_cast<E*>(a.dv) + at + v, &dv[c][d]);
+        }
+      }
+    }
+  }
+}
+
+template <typename E, int DK>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(WinArgs a, uint32_t blocks,
+                                                                                int64_t tokens) {
+  using M = Mma<E>;
+  using KT = KeyTile<E, DK>;
+  constexpr int kC2 = kTilesW<E>, kQ = kRows<E>, kStage = 2 * KT::kBytes;
+  __shared__ __align__(1024) char smem[2 * kStage];
+  const uint32_t id = wide_index();
+  if (id >= blocks) return;
+  const int64_t wg = spread_index(id, blocks, a.rep);
+  const int64_t slot = wg / a.hq;
+  const int h = (int)(wg - slot * a.hq), kh = h / a.rep;
+  const int64_t seq = tile_seq(a.q_offsets, a.seqlen, a.nseq, slot, kQ);
+  const Seq qs = seq_of(a.q_offsets, a.seqlen, seq), ks = seq_of(a.kv_offsets, a.kv_len, seq);
+  const int64_t tile = slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, kQ);
+  if (tile < 0 || tile * kQ >= qs.len) return;
+  const int q0 = (int)tile * kQ, nq = min(qs.len - q0, kQ);
+  const int shift = ks.len - qs.len;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w0 = 16 * kC2 * w;
+  const Mask mask = mask_of(a);
+  const int p0 = q0 + shift, p1 = p0 + nq - 1;
+  const int lo = (int)(max((int64_t)p0 - a.window + 1, (int64_t)0) / kKeys);
+  const int sink_tiles = min((mask.sinks + (kKeys - 1ll)) / kKeys, (int64_t)lo);
+  const int count = p1 < 0 ? 0 : sink_tiles + p1 / kKeys - lo + 1;
+  auto tile_at = [&](int i) { return i < sink_tiles ? i : lo + i - sink_tiles; };
+  const E* kp = static_cast<const E*>(a.k) + ks.first * a.k_stride + (int64_t)kh * a.dim;
+  const E* vp = static_cast<const E*>(a.v) + ks.first * a.v_stride + (int64_t)kh * a.dim;
+  const uint32_t lds0 = lds_address(smem);
+  const RowCopy<E, KT, kKeys, 4> ck(w, lane, a.k_stride, a.dim), cv(w, lane, a.v_stride, a.dim);
+  auto copy = [&](int t, int st) {
+    const int64_t j = (int64_t)t * kKeys, n = min((int64_t)kKeys, ks.len - j);
+    ck(rows_buffer(kp + j * a.k_stride, n, a.k_stride, a.dim), lds0 + st * kStage, w);
+    cv(rows_buffer(vp + j * a.v_stride, n, a.v_stride, a.dim), lds0 + st * kStage + KT::kBytes, w);
+  };
+  if (count) copy(tile_at(0), 0);
+  typename M::Frag qf[kC2][DK / M::kDepth], of[kC2][DK / M::kDepth];
+  const int64_t o_stride = (int64_t)a.hq * a.dim;
+  const E* qp = static_cast<const E*>(a.q) + (qs.first + q0) * a.q_stride + (int64_t)h * a.dim;
+  const E* op = static_cast<const E*>(a.dout) + (qs.first + q0) * o_stride + (int64_t)h * a.dim;
+  constexpr bool kTwice = sizeof(E) == 2;
+  float ls[kC2], ds[kC2];
+#pragma unroll
+  for (int c = 0; c < kC2; ++c) {
+    const int i = w0 + 16 * c + r;
+    load_rows<E, DK>(qp, a.q_stride, i, nq, a.dim, g, qf[c]);
+    load_rows<E, DK>(op, o_stride, i, nq, a.dim, g, of[c]);
+    const int64_t at = (int64_t)h * tokens + qs.first + q0 + i;
+    ls[c] = -kMinusInf;
+    ds[c] = 0.f;
+    if (i < nq && !kTwice) {
+      ls[c] = a.stat[at];
+      ds[c] = a.stat[tokens * a.hq + at];
+    }
+    if (i < nq && kTwice) {
+      const float lse = a.lse[(qs.first + q0 + i) * a.hq + h];
+      ls[c] = lse == kMinusInf ? -kMinusInf : lse * kLog2e;
+      if (g == 0) a.stat[at] = ls[c];
+    }
+  }
+  const float sc = a.scale * kLog2e;
+  f32x4 dq[kC2][DK / 16];
+#pragma unroll
+  for (int c = 0; c < kC2; ++c)
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) dq[c][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const KT kt(lane);
+  const int pw0 = p0 + w0, pw1 = pw0 + 16 * kC2 - 1;
+  // 32 keys of the stage at sk: P and dO V^T, rows = keys, column = query
+  auto scores = [&](lds_ptr sk, int j0, int half, f32x4 (&s)[kC2][2], f32x4 (&e)[kC2][2]) {
+    const lds_ptr sv = sk + KT::kBytes;
+    const int jh = j0 + 32 * half;
+#pragma unroll
+    for (int c = 0; c < kC2; ++c)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const auto kf = kt.rows(sk, 2 * half + m, kb), vf = kt.rows(sv, 2 * half + m, kb);
+#pragma unroll
+        for (int c = 0; c < kC2; ++c) {
+          s[c][m] = M::mma(kf, qf[c][kb], s[c][m]);
+          e[c][m] = M::mma(vf, of[c][kb], e[c][m]);
+        }
+      }
+    const bool whole = mask.all(pw0, pw1, jh, jh + 31);
+#pragma unroll
+    for (int c = 0; c < kC2; ++c)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float p = fast_exp2(fmaf(s[c][m][x], sc, -ls[c]));
+          s[c][m][x] = whole || mask.sees(pw0 + 16 * c + r, jh + 16 * m + 4 * g + x) ? p : 0.f;
+        }
+  };
+  int turn = 0;  // stages
+  if constexpr (kTwice) {
+    for (int i = 0; i < count; ++i, ++turn) {
+      const int st = turn & 1, j0 = tile_at(i) * kKeys;
+      copies_done();
+      copy(tile_at(i + 1 < count ? i + 1 : 0), st ^ 1);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (mask.none(pw0, pw1, j0 + 32 * half, j0 + 32 * half + 31)) continue;
+        f32x4 s[kC2][2], e[kC2][2];
+        scores((lds_ptr)(smem + st * kStage), j0, half, s, e);
+#pragma unroll
+        for (int c = 0; c < kC2; ++c)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) ds[c] += s[c][m][x] == 0.f ? 0.f : s[c][m][x] * e[c][m][x];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kC2; ++c) {
+      ds[c] = across_groups(ds[c]);
+      const int i = w0 + 16 * c + r;
+      if (g == 0 && i < nq) a.stat[tokens * a.hq + (int64_t)h * tokens + qs.first + q0 + i] = ds[c];
+    }
+  }
+  for (int i = 0; i < count; ++i, ++turn) {
+    const int st = turn & 1, j0 = tile_at(i) * kKeys;
+    copies_done();
+    if (i + 1 < count) copy(tile_at(i + 1), st ^ 1);
+    const lds_ptr sk = (lds_ptr)(smem + st * kStage);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (mask.none(pw0, pw1, j0 + 32 * half, j0 + 32 * half + 31)) continue;
+      f32x4 s[kC2][2], e[kC2][2];
+      scores(sk, j0, half, s, e);
+#pragma unroll
+      for (int c = 0; c < kC2; ++c)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) e[c][m][x] = s[c][m][x] == 0.f ? 0.f : s[c][m][x] * (e[c][m][x] - ds[c]);
+#pragma unroll
+      for (int kb = 0; kb < 32 / M::kDepth; ++kb) {
+        typename M::Frag ef[kC2];
+#pragma unroll
+        for (int c = 0; c < kC2; ++c) ef[c] = M::pack(&e[c][kb * M::kTiles]);
+#pragma unroll
+        for (int d = 0; d < DK / 16; ++d) {
+          const auto kc = kt.cols(sk, d, half * (32 / M::kDepth) + kb);
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) dq[c][d] = M::mma(kc, ef[c], dq[c][d]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kC2; ++c) {
+    const int i = w0 + 16 * c + r;
+    if (i >= nq) continue;
+    E* to = static_cast<E*>(a.dq) + ((qs.first + q0 + i) * a.hq + h) * (int64_t)a.dim;
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) dq[c][d] *= a.scale;
+#pragma unroll
+    for (int d = 0; d < DK / 16; d += M::kTiles)
+      if (KT::value(d, g, 0) < a.dim) store_operand(to + KT::value(d, g, 0), &dq[c][d]);
+  }
+}
+
+struct BwdLayout {  // workspace regions in bytes
+  size_t far, total;
+  int64_t far_slots, tokens;
+  int32_t sink_tiles;
+};
+BwdLayout layout(const mamba_window_dims* d, bool packed) {
+  BwdLayout l = {};
+  l.tokens = packed ? d->seqlen : d->batch * d->seqlen;
+  l.far = ((size_t)l.tokens * (size_t)d->q_heads * 2 * sizeof(float) + 255) / 256 * 256;
+  l.total = l.far;
+  const int rows = d->io_dtype == MAMBA_BF16 ? kRows<uint16_t> : kRows<float>;
+  if (d->sinks && d->window < d->kv_len) {  // (a window of every key leaves no query past it)
+    l.far_slots = tile_slots(d->seqlen, d->batch, packed, kFar);
+    l.sink_tiles = (int32_t)((std::min(d->sinks, d->kv_len) + rows - 1) / rows);
+    l.total += (size_t)l.far_slots * (size_t)d->kv_heads * (size_t)l.sink_tiles * 2 * rows * (size_t)d->dim * sizeof(float);
+  }
+  return l;
+}
+
+template <typename E, int DK>
+int launch_bwd(const WinArgs& a, int64_t tokens, hipStream_t s) {
+  const bool packed = a.q_offsets != nullptr;
+  int st = MAMBA_OK;
+  if constexpr (sizeof(E) == 4) {
+    const int64_t rows = tokens * a.hq;
+    hipLaunchKernelGGL((window_stat_kernel<E>), wide_grid((uint64_t)((rows + 31) / 32), 256), dim3(256), 0, s, a, tokens);
+    if ((st = launch_status()) != MAMBA_OK) return st;
+  }
+  const uint32_t queries = (uint32_t)(tile_slots(a.seqlen, a.nseq, packed, kRows<E>) * a.hq);
+  hipLaunchKernelGGL((window_dq_kernel<E, DK>), wide_grid(queries, 256), dim3(256), 0, s, a, queries, tokens);
+  if ((st = launch_status()) != MAMBA_OK) return st;
+  if (a.sink_tiles) {
+    const uint32_t blocks = (uint32_t)(a.far_slots * a.hk * a.sink_tiles);
+    hipLaunchKernelGGL((window_dkv_kernel<E, DK, true>), wide_grid(blocks, 256), dim3(256), 0, s, a, blocks, tokens);
+    if ((st = launch_status()) != MAMBA_OK) return st;
+  }
+  const uint32_t keys = (uint32_t)(tile_slots(a.kv_len, a.nseq, packed, kRows<E>) * a.hk);
+  hipLaunchKernelGGL((window_dkv_kernel<E, DK, false>), wide_grid(keys, 256), dim3(256), 0, s, a, keys, tokens);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace window
+}  // namespace mamba
+
+using namespace mamba;
+using namespace mamba::window;
+
+extern "C" {
+
+size_t mamba_window_attn_bwd_workspace_bytes(const mamba_window_dims* dims, int packed) {
+  if (check_window(dims, packed != 0) != MAMBA_OK) return 0;
+  return layout(dims, packed != 0).total;
+}
+
+int mamba_window_attn_bwd(const void* q, const void* k, const void* v, const int64_t* q_offsets,
+                          const int64_t* kv_offsets, float scale, const void* out, const float* lse, const void* dout,
+                          void* dq, void* dk, void* dv, const mamba_window_dims* dims, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const bool packed = q_offsets != nullptr;
+  int st = check_window(dims, packed);
+  if (st != MAMBA_OK) return st;
+  if (!out || !lse || !dout || !dq || !dk || !dv) return MAMBA_ERR_NULL;
+  if ((st = check_window_inputs(q, k, v, q_offsets, kv_offsets)) != MAMBA_OK) return st;
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) ||
+      !aligned(dv, 16))
+    return MAMBA_ERR_ALIGN;
+  const BwdLayout l = layout(dims, packed);
+  if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGN;
+  WinArgs a = window_args(dims, scale, q, k, v, q_offsets, kv_offsets);
+  a.out = const_cast<void*>(out);
+  a.lse = const_cast<float*>(lse);
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.stat = static_cast<float*>(workspace);
+  a.far = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.far);
+  a.far_slots = l.far_slots;
+  a.sink_tiles = l.sink_tiles;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dims->io_dtype == MAMBA_BF16)
+    return a.dim <= 64 ? launch_bwd<uint16_t, 64>(a, l.tokens, s) : launch_bwd<uint16_t, 128>(a, l.tokens, s);
+  return a.dim <= 64 ? launch_bwd<float, 64>(a, l.tokens, s) : launch_bwd<float, 128>(a, l.tokens, s);
+}
+
+}  // extern "C"
