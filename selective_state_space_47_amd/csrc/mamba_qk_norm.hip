@@ -34,26 +34,43 @@ struct QkArgs {
   float* part;             // partial weight gradients: (workgroups, dim)
   int64_t rows, x_stride[2];
   uint32_t split;          // gradients: workgroups of the queries
-  int32_t heads[2], dim, rotary, interleaved;
+  int32_t heads[2], dim, rotary;
   float eps;
 };
 
-// 8 values of a 16-byte aligned address (fp32: 32 bytes of it)
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 f = unpack(u[k]);
-    v[2 * k] = f.x;
-    v[2 * k + 1] = f.y;
+// 8 values as they are stored, at a 16-byte aligned address (those on their way take no more registers)
+template <typename E>
+struct Vec8;
+template <>
+struct Vec8<uint16_t> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint16_t* p, bool in) {
+    w = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack(u[k]);
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+    }
+  }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, bool in) {
+    a = in ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+    b = in ? *reinterpret_cast<const float4*>(p + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <typename E>
+using Pair = Vec8<E>[2];
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) =
       make_uint4(pack_bf16(make_float2(v[0], v[1])), pack_bf16(make_float2(v[2], v[3])),
@@ -67,14 +84,14 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 // A lane's two vectors of a head: where they begin, whether they exist, whether their pairs turn.  Halves: vector
 // a of the first half with the same of the second, then the unturned rest two by two.  Interleaved: two vectors
 // one after the other, whose own neighbours are pairs.
-template <int T>
+template <int T, bool kInter>
 struct Lane {
   int l, a, b;
   bool has_a, has_b, turns;
   __device__ __forceinline__ Lane(const QkArgs& q) : l(threadIdx.x % T) {
     const int pairs = q.rotary / 16;  // lanes that turn 8 pairs each
     turns = l < pairs;
-    if (q.interleaved) {
+    if (kInter) {
       a = 16 * l;
       b = a + 8;
     } else {
@@ -85,11 +102,19 @@ struct Lane {
     has_b = b < q.dim;
   }
   template <typename E>
-  __device__ __forceinline__ void load(const E* p, float (&v)[2][8]) const {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[0][k] = v[1][k] = 0.f;
-    if (has_a) load8(p + a, v[0]);
-    if (has_b) load8(p + b, v[1]);
+  __device__ __forceinline__ void load(const E* p, Pair<E>& v, bool in = true) const {
+    v[0].load(p + a, in && has_a);
+    v[1].load(p + b, in && has_b);
+  }
+  __device__ __forceinline__ void load(const float* p, float (&v)[2][8]) const {
+    Pair<float> x;
+    load(p, x);
+    get<float>(x, v);
+  }
+  template <typename E>
+  __device__ __forceinline__ void get(const Pair<E>& x, float (&v)[2][8]) const {
+    x[0].get(v[0]);
+    x[1].get(v[1]);
   }
   template <typename E>
   __device__ __forceinline__ void store(E* p, const float (&v)[2][8]) const {
@@ -97,14 +122,14 @@ struct Lane {
     if (has_b) store8(p + b, v[1]);
   }
   // turn by the table's angle (sign 1) or back (-1)
-  __device__ __forceinline__ void turn(const float2* row, bool interleaved, float sign, float (&v)[2][8]) const {
+  __device__ __forceinline__ void turn(const float2* row, float sign, float (&v)[2][8]) const {
     if (!turns) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float2 cs = row[8 * l + k];
       const float s = sign * cs.y;
-      float& x = interleaved ? v[k >> 2][2 * (k & 3)] : v[0][k];
-      float& y = interleaved ? v[k >> 2][2 * (k & 3) + 1] : v[1][k];
+      float& x = kInter ? v[k >> 2][2 * (k & 3)] : v[0][k];
+      float& y = kInter ? v[k >> 2][2 * (k & 3) + 1] : v[1][k];
       const float t = x;
       x = fmaf(x, cs.x, -y * s);
       y = fmaf(y, cs.x, t * s);
@@ -160,24 +185,31 @@ __device__ __forceinline__ void angles(const QkArgs& a, int64_t row0, int n, flo
   }
 }
 
-template <typename E, int T>
+template <typename E, int T, bool kInter>
 __global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int32_t per) {
   __shared__ float2 table[kQkRows][kQkMaxDim / 2];
-  const Lane<T> lane(a);
+  const Lane<T, kInter> lane(a);
   const int64_t row0 = (int64_t)wide_index() * per;
   if (row0 >= a.rows) return;
   const int n = (int)min((int64_t)per, a.rows - row0);
+  const int heads = a.heads[0] + a.heads[1], units = n * heads;
+  // a unit's values are read a turn ahead, the first before the angles are made (lanes of one team run together)
+  Pair<E> ahead;
+  auto load = [&](int u) {
+    const int r = u / heads, h = u - r * heads, key = h >= a.heads[0], hh = key ? h - a.heads[0] : h;
+    lane.load(static_cast<const E*>(a.x[key]) + (row0 + r) * a.x_stride[key] + (int64_t)hh * a.dim, ahead, u < units);
+  };
+  load(threadIdx.x / T);
   angles(a, row0, n, table);
   __syncthreads();
-  const int heads = a.heads[0] + a.heads[1];
-  // (lanes of one team run together)
-  for (int u = threadIdx.x / T; u < n * heads; u += kQkThreads / T) {
+  for (int u = threadIdx.x / T; u < units; u += kQkThreads / T) {
     const int r = u / heads, h = u - r * heads;
     const int key = h >= a.heads[0];
     const int hh = key ? h - a.heads[0] : h;
     const int64_t row = row0 + r;
     float v[2][8], w[2][8];
-    lane.load(static_cast<const E*>(a.x[key]) + row * a.x_stride[key] + (int64_t)hh * a.dim, v);
+    lane.template get<E>(ahead, v);
+    load(u + kQkThreads / T);
     lane.load(a.w[key], w);
     float s = 0.f;
 #pragma unroll
@@ -185,17 +217,17 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int32_t p
     const float rs = rsqrtf(team_sum<T>(s) / a.dim + a.eps);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] *= rs * w[i >> 3][i & 7];
-    lane.turn(table[r], a.interleaved, 1.f, v);
+    lane.turn(table[r], 1.f, v);
     lane.store(static_cast<E*>(a.out[key]) + (row * a.heads[key] + hh) * (int64_t)a.dim, v);
   }
 }
 
 // A workgroup takes rows of the queries or of the keys, so that its weight sums are of one kind.
-template <typename E, int T>
-__global__ __launch_bounds__(kQkThreads) void qk_norm_bwd_kernel(QkArgs a) {
+template <typename E, int T, bool kInter>
+__global__ __launch_bounds__(kQkThreads, sizeof(E) == 2 ? 4 : 3) void qk_norm_bwd_kernel(QkArgs a) {
   __shared__ float2 table[kQkRows][kQkMaxDim / 2];
   __shared__ float sum[kQkThreads / 64][kQkMaxDim];
-  const Lane<T> lane(a);
+  const Lane<T, kInter> lane(a);
   const int key = blockIdx.x >= a.split;
   const uint32_t wg = key ? blockIdx.x - a.split : blockIdx.x, wgs = key ? gridDim.x - a.split : a.split;
   const int heads = a.heads[key];
@@ -204,18 +236,28 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_bwd_kernel(QkArgs a) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i >> 3][i & 7] = 0.f;
   const double inv = 1.0 / a.dim;
+  Pair<E> ax, ad;  // a unit's values a turn ahead
+  auto load = [&](int64_t row0, int u, int units) {
+    const int r = u / heads, h = u - r * heads;
+    const int64_t row = row0 + r;
+    lane.load(static_cast<const E*>(a.x[key]) + row * a.x_stride[key] + (int64_t)h * a.dim, ax, u < units);
+    lane.load(static_cast<const E*>(a.dout[key]) + (row * heads + h) * (int64_t)a.dim, ad, u < units);
+  };
   for (int64_t row0 = (int64_t)wg * kQkRows; row0 < a.rows; row0 += (int64_t)wgs * kQkRows) {
-    const int n = (int)min((int64_t)kQkRows, a.rows - row0);
+    const int n = (int)min((int64_t)kQkRows, a.rows - row0), units = n * heads;
+    load(row0, threadIdx.x / T, units);
     __syncthreads();  // the table of the rows before has been read
     angles(a, row0, n, table);
     __syncthreads();
-    for (int u = threadIdx.x / T; u < n * heads; u += kQkThreads / T) {
+#pragma unroll 1
+    for (int u = threadIdx.x / T; u < units; u += kQkThreads / T) {
       const int r = u / heads, h = u - r * heads;
       const int64_t row = row0 + r, at = (row * heads + h) * (int64_t)a.dim;
       float x[2][8], d[2][8];
-      lane.load(static_cast<const E*>(a.x[key]) + row * a.x_stride[key] + (int64_t)h * a.dim, x);
-      lane.load(static_cast<const E*>(a.dout[key]) + at, d);
-      lane.turn(table[r], a.interleaved, -1.f, d);
+      lane.template get<E>(ax, x);
+      lane.template get<E>(ad, d);
+      load(row0, u + kQkThreads / T, units);
+      lane.turn(table[r], -1.f, d);
       // statistics in fp64: next to nothing is left of a where it is nearly parallel to n
       double sq = 0.0, dot = 0.0;
 #pragma unroll
@@ -229,6 +271,9 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_bwd_kernel(QkArgs a) {
       const double ms = fma(sq, inv, (double)a.eps), r2 = 1.0 / ms;
       const float rs = ms > 1e-37 && ms < 1e37 ? rsqrtf((float)ms) : (float)(1.0 / sqrt(ms));
       const double m = dot * r2 * inv;
+      // (opaque: the values are widened again rather than kept wide, which would take 64 registers more)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) asm("" : "+v"(x[i >> 3][i & 7]), "+v"(d[i >> 3][i & 7]));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float& v = x[i >> 3][i & 7];
@@ -320,7 +365,6 @@ QkArgs qk_args(const mamba_qk_norm_rope_dims* d, const void* q, const void* k, c
   a.x_stride[1] = d->k_stride ? d->k_stride : d->k_heads * d->dim;
   a.dim = (int32_t)d->dim;
   a.rotary = (int32_t)d->rotary_dim;
-  a.interleaved = d->interleaved != 0;
   a.eps = eps;
   return a;
 }
@@ -337,23 +381,28 @@ QkGrid qk_grid(const mamba_qk_norm_rope_dims* d) {
   return {(uint32_t)q, (uint32_t)(q + k)};
 }
 
-template <typename E, int T>
+template <typename E, int T, bool kInter>
 int launch_qk_t(const QkArgs& a, bool bwd, QkGrid grid, hipStream_t s) {
   if (bwd) {
-    hipLaunchKernelGGL((qk_norm_bwd_kernel<E, T>), dim3(grid.all), dim3(kQkThreads), 0, s, a);
+    hipLaunchKernelGGL((qk_norm_bwd_kernel<E, T, kInter>), dim3(grid.all), dim3(kQkThreads), 0, s, a);
   } else {
     // few rows: a workgroup each
     const int per = a.rows >= 1024 ? kQkRows : 1;
-    hipLaunchKernelGGL((qk_norm_kernel<E, T>), wide_grid((uint64_t)((a.rows + per - 1) / per), kQkThreads),
+    hipLaunchKernelGGL((qk_norm_kernel<E, T, kInter>), wide_grid((uint64_t)((a.rows + per - 1) / per), kQkThreads),
                        dim3(kQkThreads), 0, s, a, per);
   }
   return launch_status();
 }
-template <typename E>
-int launch_qk(const QkArgs& a, bool bwd, QkGrid grid, hipStream_t s) {
-  if (a.dim <= 64) return launch_qk_t<E, 4>(a, bwd, grid, s);
-  if (a.dim <= 128) return launch_qk_t<E, 8>(a, bwd, grid, s);
-  return launch_qk_t<E, 16>(a, bwd, grid, s);
+template <typename E, bool kInter>
+int launch_qk_d(const QkArgs& a, bool bwd, QkGrid grid, hipStream_t s) {
+  if (a.dim <= 64) return launch_qk_t<E, 4, kInter>(a, bwd, grid, s);
+  if (a.dim <= 128) return launch_qk_t<E, 8, kInter>(a, bwd, grid, s);
+  return launch_qk_t<E, 16, kInter>(a, bwd, grid, s);
+}
+int launch_qk(const QkArgs& a, const mamba_qk_norm_rope_dims* d, bool bwd, QkGrid grid, hipStream_t s) {
+  if (d->io_dtype == MAMBA_BF16)
+    return d->interleaved ? launch_qk_d<uint16_t, true>(a, bwd, grid, s) : launch_qk_d<uint16_t, false>(a, bwd, grid, s);
+  return d->interleaved ? launch_qk_d<float, true>(a, bwd, grid, s) : launch_qk_d<float, false>(a, bwd, grid, s);
 }
 
 }  // namespace
@@ -375,7 +424,7 @@ int mamba_qk_norm_rope_fwd(const void* q, const void* k, const float* q_weight, 
   a.out[0] = q_out;
   a.out[1] = k_out;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dims->io_dtype == MAMBA_BF16 ? launch_qk<uint16_t>(a, false, {}, s) : launch_qk<float>(a, false, {}, s);
+  return launch_qk(a, dims, false, {}, s);
 }
 
 size_t mamba_qk_norm_rope_bwd_workspace_bytes(const mamba_qk_norm_rope_dims* dims) {
@@ -406,7 +455,7 @@ int mamba_qk_norm_rope_bwd(const void* q, const void* k, const float* q_weight, 
   const QkGrid grid = qk_grid(dims);
   a.split = grid.split;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  st = dims->io_dtype == MAMBA_BF16 ? launch_qk<uint16_t>(a, true, grid, s) : launch_qk<float>(a, true, grid, s);
+  st = launch_qk(a, dims, true, grid, s);
   if (st != MAMBA_OK) return st;
   hipLaunchKernelGGL(qk_fold_kernel, dim3((unsigned)((a.dim + kQkFoldCols - 1) / kQkFoldCols), 2), dim3(1024), 0, s,
                      a.part, dq_weight, dk_weight, (int)grid.split, (int)grid.all, a.dim);
