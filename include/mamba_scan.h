@@ -564,7 +564,7 @@ size_t mamba_window_attn_update_workspace_bytes(const mamba_window_dims* dims);
  *                      are not read
  *   out              : (batch, q_heads, dim), io_dtype, contiguous
  *   workspace        : >= mamba_window_attn_update_workspace_bytes bytes, 16-byte aligned (NULL where that is 0)
- * fp32 arithmetic.
+ * fp32 arithmetic (with bf16 storage the weights enter the product with v as two bf16 parts).
  */
 int mamba_window_attn_update(void* k_cache, void* v_cache, const void* q, const void* k, const void* v,
                              const int64_t* positions, float scale, void* out, const mamba_window_dims* dims,

@@ -10,9 +10,9 @@ namespace window {
 namespace {
 
 constexpr int kStepThreads = 256;
-constexpr int kStepHeads = 8;        // query heads that share a pass over a key head's slots
-constexpr int64_t kStepWG = 1024;    // workgroups that fill the GPU
-constexpr int64_t kStepSlots = 128;  // slots of a part, at least
+constexpr int kStepHeads = 16;       // query heads that share a pass over a key head's slots: columns of a product
+constexpr int64_t kStepWG = 512;     // workgroups that fill the GPU
+constexpr int64_t kStepSlots = 256;  // slots of a part, at least
 
 struct StepArgs {
   void* k_cache;
@@ -22,204 +22,153 @@ struct StepArgs {
   const void* v;
   const int64_t* positions;
   void* out;
-  float* part;  // (parts, batch * hq, 2 + 128): maximum, sum, unnormalised output
+  float* part;  // (parts, batch * hq, 2 + 128): maximum times log2(e), sum, unnormalised output
   int64_t q_stride, k_stride, v_stride;
   int64_t batch, slots, window, sinks;
   int32_t hq, hk, rep, dim, parts;
   float scale;
 };
 
-template <typename E>
-struct Vec8;
-template <>
-struct Vec8<uint16_t> {
-  uint4 w;
-  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = w; }
-  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack(u[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-};
-template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
-  }
-  __device__ __forceinline__ void store(float* p) const {
-    *reinterpret_cast<float4*>(p) = a;
-    *reinterpret_cast<float4*>(p + 4) = b;
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-};
-
-// sum over the T lanes of a slot, in each of them
-template <int T>
-__device__ __forceinline__ float lanes_sum(float v) {
-  if constexpr (T == 16) {
-    v += dpp_row<0x128>(v);
-    v += dpp_row<0x124>(v);
-    v += dpp_row<0x122>(v);
-    v += dpp_row<0x121>(v);
-  } else {
-    v += dpp_row<0xb1>(v);   // lane ^ 1
-    v += dpp_row<0x4e>(v);   // lane ^ 2
-    v += dpp_row<0x141>(v);  // half row mirrored
-  }
-  return v;
-}
-
-// One sequence, key head and part of the slots; R query heads of it at a time.  T lanes hold a slot's key and value,
-// 8 values each, so that a wave reads 64 / T slots at once, kAhead of those on their way; each group of lanes
-// goes through its own slots with its own maximum and sum, which are joined at the end.  Bound by the caches'
-// traffic (read once; fp32 arithmetic).  The new key and value are taken from the inputs and written to their slot
-// by the lanes that come to it: nobody reads that slot.
-template <typename E, int T, int R>
-__global__ __launch_bounds__(kStepThreads) void window_step_kernel(StepArgs a, uint32_t blocks) {
-  constexpr int kGroups = kStepThreads / T, kAhead = 4, kWaves = kStepThreads / 64;
-  __shared__ float sm[kWaves][R][2], so[kWaves][R][8 * T];
+// One sequence, key head and part of the slots; up to 16 query heads of it are the columns of the products.  Each wave
+// goes through its own tiles of slots with its own maximum and sum, without a barrier: keys come from memory as
+// operands, values straight into the wave's LDS, both of a whole tile at once; the waves are joined at the end.
+// Bound by the caches' traffic (read once).  The new key and value are taken from the inputs and written to their slot
+// by the wave that comes to it: nobody reads that slot.  With bf16 storage the weights enter the product with V as two
+// bf16 parts (2^-17 of each), so that the output's rounding is the only one that shows.
+template <typename E, int DK>
+__global__ __launch_bounds__(kStepThreads, 2) void window_step_kernel(StepArgs a, uint32_t blocks) {
+  using M = Mma<E>;
+  using KT = KeyTile<E, DK>;
+  constexpr int kWaves = kStepThreads / 64, kSlots = sizeof(E) == 2 ? 64 : 32, kT = kSlots / 16, kV = 16 / sizeof(E);
+  constexpr int kTile = kSlots * KT::kRow, kP = M::parts(2);
+  static_assert(kTile >= kStepHeads * DK * 4, "a wave's output takes its tile's place");
+  __shared__ __align__(1024) char smem[kWaves * kTile];
+  __shared__ float sm[kWaves][kStepHeads][2];
   const uint32_t wg = wide_index();
   if (wg >= blocks) return;
   const uint32_t part = wg % (uint32_t)a.parts, rest = wg / (uint32_t)a.parts;
   const int64_t seq = rest / (uint32_t)a.hk;
   const int kh = (int)(rest - seq * a.hk);
-  const int tid = threadIdx.x, l = tid % T, grp = tid / T, lane = tid & 63, w = tid >> 6;
-  const int c = 8 * l;
-  const bool has = c < a.dim;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t p = a.positions[seq];
   const int64_t live = p < 0 ? 0 : min(p + 1, a.slots);  // slots that hold a position
   const int64_t mine = p < a.sinks ? p : a.sinks + (p - a.sinks) % a.window;
   const int64_t per = (live + a.parts - 1) / a.parts;
   const int64_t s0 = (int64_t)part * per, s1 = min(s0 + per, live);
   const int64_t row = (int64_t)a.hk * a.dim;
-  E* kc = static_cast<E*>(a.k_cache) + (seq * a.slots * a.hk + kh) * (int64_t)a.dim + c;
-  E* vc = static_cast<E*>(a.v_cache) + (seq * a.slots * a.hk + kh) * (int64_t)a.dim + c;
-  const E* kn = static_cast<const E*>(a.k) + seq * a.k_stride + (int64_t)kh * a.dim + c;
-  const E* vn = static_cast<const E*>(a.v) + seq * a.v_stride + (int64_t)kh * a.dim + c;
-  for (int h0 = 0; h0 < a.rep; h0 += R) {
-    float q[R][8], o[R][8], m[R], sum[R];
+  E* kc = static_cast<E*>(a.k_cache) + (seq * a.slots * a.hk + kh) * (int64_t)a.dim;
+  E* vc = static_cast<E*>(a.v_cache) + (seq * a.slots * a.hk + kh) * (int64_t)a.dim;
+  const E* kn = static_cast<const E*>(a.k) + seq * a.k_stride + (int64_t)kh * a.dim;
+  const E* vn = static_cast<const E*>(a.v) + seq * a.v_stride + (int64_t)kh * a.dim;
+  char* const mem = smem + w * kTile;
+  const lds_ptr sv = (lds_ptr)mem;
+  const uint32_t lds = lds_address(smem) + w * kTile;
+  const RowCopy<E, KT, kSlots, 1> cv(0, lane, row, a.dim);
+  const KT kt(lane);
+  const float sc = fabsf(a.scale) * kLog2e;
+  for (int h0 = 0; h0 < a.rep; h0 += kStepHeads) {
+    const int heads = min(a.rep - h0, kStepHeads);
+    typename M::Frag q[DK / M::kDepth];  // column = head; a negative scale goes into the sign of q
+    load_rows<E, DK>(static_cast<const E*>(a.q) + seq * a.q_stride + (int64_t)(kh * a.rep + h0) * a.dim, a.dim, r, heads,
+                     a.dim, g, q);
+    if (a.scale < 0.f)
 #pragma unroll
-    for (int x = 0; x < R; ++x) {
-      m[x] = kMinusInf;
-      sum[x] = 0.f;
+      for (int kb = 0; kb < DK / M::kDepth; ++kb) q[kb] = -q[kb];
+    f32x4 o[DK / 16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[x][i] = o[x][i] = 0.f;
-      if (has && h0 + x < a.rep) {
-        Vec8<E> v;
-        v.load(static_cast<const E*>(a.q) + seq * a.q_stride + (int64_t)(kh * a.rep + h0 + x) * a.dim + c);
-        v.get(q[x]);
+    for (int d = 0; d < DK / 16; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float mx = kMinusInf, l = 0.f;
+    for (int64_t s = s0 + w * kSlots; s < s1; s += kWaves * kSlots) {
+      const int n = (int)min((int64_t)kSlots, s1 - s);
+      cv(rows_buffer(vc + s * row, n, row, a.dim), lds, 0);  // (slots past the part read as zero)
+      typename M::Frag kf[kT][DK / M::kDepth];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[x][i] *= a.scale * kLog2e;
-      }
-    }
-    for (int64_t s = s0 + grp; s < s1; s += kAhead * kGroups) {
-      Vec8<E> kv[kAhead], vv[kAhead];
+      for (int m = 0; m < kT; ++m) {
+        const int i = 16 * m + r;
+        const E* from = s + i == mine ? kn : kc + (s + i) * row;
 #pragma unroll
-      for (int y = 0; y < kAhead; ++y) {
-        const int64_t at = s + y * kGroups;
-        kv[y].zero();
-        vv[y].zero();
-        if (has && at < s1) {
-          const bool now = at == mine;
-          kv[y].load(now ? kn : kc + at * row);
-          vv[y].load(now ? vn : vc + at * row);
+        for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+          const int c = kb * M::kDepth + g * kV;
+          kf[m][kb] = i < n && c < a.dim ? *reinterpret_cast<const typename M::Frag*>(from + c) : typename M::Frag{};
         }
       }
-      float e[R][kAhead];
+      f32x4 e[kT];
 #pragma unroll
-      for (int y = 0; y < kAhead; ++y) {
-        float kf[8];
-        kv[y].get(kf);
+      for (int m = 0; m < kT; ++m) {
+        e[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int x = 0; x < R; ++x) {
-          float d = 0.f;
+        for (int kb = 0; kb < DK / M::kDepth; ++kb) e[m] = M::mma(kf[m][kb], q[kb], e[m]);
+      }
+      float top = mx;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d = fmaf(q[x][i], kf[i], d);
-          d = lanes_sum<T>(d);
-          e[x][y] = s + y * kGroups < s1 ? d : kMinusInf;
+      for (int m = 0; m < kT; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (16 * m + 4 * g + x >= n) e[m][x] = kMinusInf;
+          top = fmaxf(top, e[m][x]);
         }
-      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float use = top == kMinusInf ? 0.f : top * sc, f = mx == kMinusInf ? 0.f : fast_exp2(fmaf(mx, sc, -use));
+      mx = top;
+      l *= f;
 #pragma unroll
-      for (int x = 0; x < R; ++x) {
-        float top = m[x];
+      for (int d = 0; d < DK / 16; ++d) o[d] *= f;
 #pragma unroll
-        for (int y = 0; y < kAhead; ++y) top = fmaxf(top, e[x][y]);
-        const float use = top == kMinusInf ? 0.f : top, f = fast_exp2(m[x] - use);
-        m[x] = top;
-        sum[x] *= f;
+      for (int m = 0; m < kT; ++m)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[x][i] *= f;
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-          e[x][y] = fast_exp2(e[x][y] - use);
-          sum[x] += e[x][y];
+        for (int x = 0; x < 4; ++x) {
+          e[m][x] = 16 * m + 4 * g + x < n ? fast_exp2(fmaf(e[m][x], sc, -use)) : 0.f;
+          l += e[m][x];
         }
-      }
-#pragma unroll
-      for (int y = 0; y < kAhead; ++y) {
-        float vf[8];
-        vv[y].get(vf);
-#pragma unroll
-        for (int x = 0; x < R; ++x)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[x][i] = fmaf(e[x][y], vf[i], o[x][i]);
-      }
-      if (h0 == 0)
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y)
-          if (has && s + y * kGroups == mine) {
-            kv[y].store(kc + mine * row);
-            vv[y].store(vc + mine * row);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's values have landed
+      if (mine >= s && mine < s + n) {
+        const int at = (int)(mine - s);
+        if (lane * kV < a.dim) {
+          const uint4 nv = *reinterpret_cast<const uint4*>(vn + lane * kV);
+          *reinterpret_cast<uint4*>(mem + at * KT::kRow + ((lane ^ KT::key(at)) << 4)) = nv;
+          if (h0 == 0) {
+            *reinterpret_cast<uint4*>(vc + mine * row + lane * kV) = nv;
+            *reinterpret_cast<uint4*>(kc + mine * row + lane * kV) = *reinterpret_cast<const uint4*>(kn + lane * kV);
           }
-    }
-    // groups of a wave, then waves
-#pragma unroll
-    for (int x = 0; x < R; ++x) {
-#pragma unroll
-      for (int d = T; d < 64; d *= 2) {
-        const float mo = __shfl_xor(m[x], d), so_ = __shfl_xor(sum[x], d);
-        const float top = fmaxf(m[x], mo), use = top == kMinusInf ? 0.f : top;
-        const float fa = fast_exp2(m[x] - use), fb = fast_exp2(mo - use);
-        sum[x] = sum[x] * fa + so_ * fb;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[x][i] = o[x][i] * fa + __shfl_xor(o[x][i], d) * fb;
-        m[x] = top;
+        }
+        wave_lds_fence();
       }
-      if (lane < T) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) so[w][x][c + i] = o[x][i];
-        if (lane == 0) {
-          sm[w][x][0] = m[x];
-          sm[w][x][1] = sum[x];
+      for (int kb = 0; kb < kSlots / M::kDepth; ++kb) {
+        const auto f = M::template split<kP>(&e[kb * M::kTiles]);
+#pragma unroll
+        for (int d = 0; d < DK / 16; ++d) {
+          const auto vf = kt.cols(sv, d, kb);
+#pragma unroll
+          for (int x = 0; x < kP; ++x) o[d] = M::mma(vf, f.p[x], o[d]);
         }
       }
+      wave_lds_fence();  // (the tile has been read)
     }
+    l = across_groups(l);
+    if (g == 0) {
+      sm[w][r][0] = mx;
+      sm[w][r][1] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d)
+      *reinterpret_cast<f32x4*>(mem + (r * DK + KT::value(d, g, 0)) * 4) = o[d];
     __syncthreads();
-    for (int i = tid; i < R * 8 * T; i += kStepThreads) {
-      const int x = i / (8 * T), d = i % (8 * T);
-      if (h0 + x >= a.rep || d >= a.dim) continue;
+    for (int i = tid; i < heads * DK; i += kStepThreads) {
+      const int x = i / DK, d = i % DK;
+      if (d >= a.dim) continue;
       float top = kMinusInf;
 #pragma unroll
       for (int y = 0; y < kWaves; ++y) top = fmaxf(top, sm[y][x][0]);
-      const float use = top == kMinusInf ? 0.f : top;
+      const float use = top == kMinusInf ? 0.f : top * sc;
       float t = 0.f, v = 0.f;
 #pragma unroll
       for (int y = 0; y < kWaves; ++y) {
-        const float f = fast_exp2(sm[y][x][0] - use);
+        const float f = sm[y][x][0] == kMinusInf ? 0.f : fast_exp2(fmaf(sm[y][x][0], sc, -use));
         t = fmaf(f, sm[y][x][1], t);
-        v = fmaf(f, so[y][x][d], v);
+        v = fmaf(f, reinterpret_cast<const float*>(smem + y * kTile)[i], v);
       }
       const int64_t head = seq * a.hq + kh * a.rep + h0 + x;
       if (a.parts == 1) {
@@ -228,7 +177,7 @@ __global__ __launch_bounds__(kStepThreads) void window_step_kernel(StepArgs a, u
         float* to = a.part + ((int64_t)part * a.batch * a.hq + head) * (2 + kMaxDk);
         to[2 + d] = v;
         if (d == 0) {
-          to[0] = top;
+          to[0] = top == kMinusInf ? top : use;
           to[1] = t;
         }
       }
@@ -291,22 +240,15 @@ int32_t step_parts(const mamba_window_dims* d) {
       1, std::min<int64_t>({(slots + kStepSlots - 1) / kStepSlots, kStepWG / std::max<int64_t>(wgs, 1), 256}));
 }
 
-template <typename E, int T, int R>
-int launch_step_t(const StepArgs& a, hipStream_t s) {
+template <typename E, int DK>
+int launch_step(const StepArgs& a, hipStream_t s) {
   const uint32_t blocks = (uint32_t)(a.batch * a.hk * a.parts);
-  hipLaunchKernelGGL((window_step_kernel<E, T, R>), wide_grid(blocks, kStepThreads), dim3(kStepThreads), 0, s, a,
+  hipLaunchKernelGGL((window_step_kernel<E, DK>), wide_grid(blocks, kStepThreads), dim3(kStepThreads), 0, s, a,
                      blocks);
   int st = launch_status();
   if (st != MAMBA_OK || a.parts == 1) return st;
   hipLaunchKernelGGL((window_join_kernel<E>), dim3((unsigned)(a.batch * a.hq)), dim3(64), 0, s, a);
   return launch_status();
-}
-template <typename E, int T>
-int launch_step(const StepArgs& a, hipStream_t s) {
-  if (a.rep == 1) return launch_step_t<E, T, 1>(a, s);
-  if (a.rep == 2) return launch_step_t<E, T, 2>(a, s);
-  if (a.rep <= 4) return launch_step_t<E, T, 4>(a, s);
-  return launch_step_t<E, T, kStepHeads>(a, s);
 }
 
 int check_cache(const mamba_window_dims* d) {
@@ -394,8 +336,8 @@ int mamba_window_attn_update(void* k_cache, void* v_cache, const void* q, const 
   a.scale = scale;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dims->io_dtype == MAMBA_BF16)
-    return a.dim <= 64 ? launch_step<uint16_t, 8>(a, s) : launch_step<uint16_t, 16>(a, s);
-  return a.dim <= 64 ? launch_step<float, 8>(a, s) : launch_step<float, 16>(a, s);
+    return a.dim <= 64 ? launch_step<uint16_t, 64>(a, s) : launch_step<uint16_t, 128>(a, s);
+  return a.dim <= 64 ? launch_step<float, 64>(a, s) : launch_step<float, 128>(a, s);
 }
 
 }  // extern "C"
