@@ -25,7 +25,7 @@ struct WinArgs {
   void* dk;
   void* dv;
   float* stat;                // (2, hq, tokens): log-sums times log2(e), and sums of dout out
-  float* far;                 // (far slots, hk, sink tiles, 2, keys, dim): the sinks' sums over queries past their window
+  float* far;                 // (far slots, hq, tiles of 16 sinks, 2, 16, dim): sums over queries past the sinks' windows
   int64_t seqlen, kv_len, nseq;
   int64_t q_stride, k_stride, v_stride;
   int64_t window, sinks;

@@ -28,7 +28,7 @@ template <typename E>
 constexpr int kTilesW = sizeof(E) == 2 ? 2 : 1;  // 16-row tiles of a wave
 template <typename E>
 constexpr int kRows = 4 * 16 * kTilesW<E>;       // of a workgroup
-constexpr int kFar = 1024;                       // queries of a stretch past the sinks' windows
+constexpr int kFar = 512;                        // queries of a stretch past the sinks' windows
 
 // 8 lanes per row; a row without a key has weights of zero: its log-sum counts as +infinity
 template <typename E>
@@ -57,29 +57,35 @@ __global__ __launch_bounds__(256) void window_stat_kernel(WinArgs a, int64_t tok
   }
 }
 
-// kFarPart: a stretch of queries past the windows of a sinks' tile; otherwise a tile of keys
+// kFarPart: one wave, 16 sinks and one query head over a stretch of queries past the sinks' windows; otherwise a tile
+// of keys, the heads that share it one after another.
 template <typename E, int DK, bool kFarPart>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(WinArgs a, uint32_t blocks,
-                                                                                 int64_t tokens) {
+__global__ __launch_bounds__(kFarPart ? 64 : 256, sizeof(E) == 2 && !kFarPart ? 2 : 1) void window_dkv_kernel(
+    WinArgs a, uint32_t blocks, int64_t tokens) {
   using M = Mma<E>;
   using KT = KeyTile<E, DK>;
-  constexpr int kC2 = kTilesW<E>, kN = kRows<E>, kStage = 2 * KT::kBytes;
+  constexpr int kNW = kFarPart ? 1 : 4, kC2 = kFarPart ? 1 : kTilesW<E>, kN = kFarPart ? 16 : kRows<E>;
+  constexpr int kStage = 2 * KT::kBytes, kHalf = 32 / 16;
   __shared__ __align__(1024) char smem[2 * kStage];
   __shared__ __align__(16) float stats[2][2][kKeys];
   const uint32_t id = wide_index();
   if (id >= blocks) return;
   int64_t seq, tile, far_slot = 0, stretch = 0;
-  int kh;
+  int kh, h0, heads;
   if (kFarPart) {
-    const uint32_t per = (uint32_t)(a.hk * a.sink_tiles);
+    const uint32_t per = (uint32_t)(a.hq * a.sink_tiles);
     far_slot = id / per;
-    const int rest = (int)(id - far_slot * per);
-    kh = rest / a.sink_tiles;
-    tile = rest - kh * a.sink_tiles;
+    const int rest = (int)(id - far_slot * per), h = rest / a.sink_tiles;
+    tile = rest - h * a.sink_tiles;
+    kh = h / a.rep;
+    h0 = h - kh * a.rep;
+    heads = 1;
     seq = tile_seq(a.q_offsets, a.seqlen, a.nseq, far_slot, kFar);
   } else {
     const int64_t slot = id / (uint32_t)a.hk;
     kh = (int)(id - slot * a.hk);
+    h0 = 0;
+    heads = a.rep;
     seq = tile_seq(a.kv_offsets, a.kv_len, a.nseq, slot, kN);
     tile = slot;
   }
@@ -92,43 +98,51 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
   const int j0 = (int)tile * kN, nk = min(ks.len - j0, kN);
   const int shift = ks.len - qs.len;
   const Mask mask = mask_of(a);
-  // Queries: those whose position is not before the tile's first key and, windows of the tile or not, up to the last
-  // that has its last key in its window; the stretches begin behind those.
-  const int64_t near_end = min((int64_t)j0 + nk - 1 + a.window - shift, (int64_t)qs.len);  // first query past them
-  int q_lo = max(j0 - shift, 0), q_hi = (int)max(near_end, (int64_t)0);
+  // Queries: those whose position is not before the tile's first key, up to the last that has a key of the tile in its
+  // window; the queries behind those, which see only sinks, go by stretches.  (Both kinds of tile begin them with
+  // the same query: that past the window of the last key of the sinks' first tile of kRows keys.)
+  auto near = [&](int64_t t) {  // first query past the windows of the t-th kRows keys
+    const int64_t last = min((t + 1) * kRows<E>, (int64_t)ks.len) - 1;
+    return max(min(last + a.window - shift, (int64_t)qs.len), max(t * kRows<E> - shift, (int64_t)0));
+  };
+  int q_lo = max(j0 - shift, 0), q_hi;
   if (kFarPart) {
-    const int64_t b = max(near_end, (int64_t)q_lo) + stretch * kFar;
+    const int64_t b = near(j0 / kRows<E>) + stretch * kFar;
     q_lo = (int)min(b, (int64_t)qs.len);
     q_hi = (int)min(b + kFar, (int64_t)qs.len);
     if (q_lo >= q_hi) return;
+  } else {
+    q_hi = (int)min(near(tile), (int64_t)qs.len);
   }
   const int t_lo = q_lo / kKeys, tiles = q_hi > q_lo ? (q_hi - 1) / kKeys - t_lo + 1 : 0;
-  const int count = tiles * a.rep;  // heads one after another
+  const int count = tiles * heads;  // heads one after another
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w0 = 16 * kC2 * w;
 
   const int64_t o_stride = (int64_t)a.hq * a.dim;
-  const E* qp = static_cast<const E*>(a.q) + qs.first * a.q_stride + (int64_t)kh * a.rep * a.dim;
-  const E* op = static_cast<const E*>(a.dout) + qs.first * o_stride + (int64_t)kh * a.rep * a.dim;
+  const int hq0 = kh * a.rep + h0;
+  const E* qp = static_cast<const E*>(a.q) + qs.first * a.q_stride + (int64_t)hq0 * a.dim;
+  const E* op = static_cast<const E*>(a.dout) + qs.first * o_stride + (int64_t)hq0 * a.dim;
   const uint32_t lds0 = lds_address(smem);
-  const RowCopy<E, KT, kKeys, 4> cq(w, lane, a.q_stride, a.dim), co(w, lane, o_stride, a.dim);
+  const RowCopy<E, KT, kKeys, kNW> cq(w, lane, a.q_stride, a.dim), co(w, lane, o_stride, a.dim);
   auto copy = [&](int i, int st) {
     const int h = i / tiles, t = (t_lo + i - h * tiles) * kKeys;
     const int64_t n = min(kKeys, qs.len - t);
     cq(rows_buffer(qp + t * a.q_stride + (int64_t)h * a.dim, n, a.q_stride, a.dim), lds0 + st * kStage, w);
     co(rows_buffer(op + t * o_stride + (int64_t)h * a.dim, n, o_stride, a.dim), lds0 + st * kStage + KT::kBytes, w);
   };
-  // threads 0-63 the log-sums, 64-127 the dots; past the sequence +infinity and 0
+  // wave 0: the log-sums and the dots; past the sequence +infinity and 0
   auto load_stat = [&](int i) {
-    const int h = i / tiles, t = (t_lo + i - h * tiles) * kKeys + (threadIdx.x & 63);
-    const int which = threadIdx.x >> 6;
-    if (which > 1) return 0.f;
-    return t < qs.len ? a.stat[((int64_t)which * a.hq + kh * a.rep + h) * tokens + qs.first + t]
-                      : which ? 0.f : -kMinusInf;
+    const int h = i / tiles, t = (t_lo + i - h * tiles) * kKeys + lane;
+    const float* p = a.stat + (int64_t)(hq0 + h) * tokens + qs.first + t;
+    return w == 0 && t < qs.len ? make_float2(p[0], p[tokens * a.hq]) : make_float2(-kMinusInf, 0.f);
   };
-  auto put_stat = [&](float v, int st) {
-    if (threadIdx.x < 128) stats[st][threadIdx.x >> 6][threadIdx.x & 63] = v;
+  auto put_stat = [&](float2 v, int st) {
+    if (w == 0) {
+      stats[st][0][lane] = v.x;
+      stats[st][1][lane] = v.y;
+    }
   };
   if (count) {
     copy(0, 0);
@@ -152,7 +166,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
   const int jw0 = j0 + w0, jw1 = jw0 + 16 * kC2 - 1;
   for (int i = 0; i < count; ++i) {
     const int st = i & 1, h = i / tiles, q0 = (t_lo + i - h * tiles) * kKeys;
-    float next = 0.f;
+    float2 next = make_float2(0.f, 0.f);
     copies_done();
     if (i + 1 < count) {
       next = load_stat(i + 1);
@@ -164,16 +178,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     for (int half = 0; half < 2; ++half) {
       const int ph = p0 + 32 * half;
       if (mask.none(ph, ph + 31, jw0, jw1)) continue;
-      // 32 queries: scores and dO V^T, rows = queries, column = key
-      f32x4 s[kC2][2], e[kC2][2];
+      const bool whole = !kFarPart && mask.all(ph, ph + 31, jw0, jw1) && q0 + 32 * half + 32 <= q_hi;
+      // 16 queries at a time: scores and dO V^T, rows = queries, column = key; then P and dS, as operands
+      f32x4 s[kC2][kHalf], e[kC2][kHalf];
 #pragma unroll
-      for (int c = 0; c < kC2; ++c)
+      for (int m = 0; m < kHalf; ++m) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < kC2; ++c) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int kb = 0; kb < DK / M::kDepth; ++kb)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
+        for (int kb = 0; kb < DK / M::kDepth; ++kb) {
           const auto qf = kt.rows(sq, 2 * half + m, kb), of = kt.rows(so, 2 * half + m, kb);
 #pragma unroll
           for (int c = 0; c < kC2; ++c) {
@@ -181,9 +194,6 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
             e[c][m] = M::mma(of, vf[c][kb], e[c][m]);
           }
         }
-      const bool whole = !kFarPart && mask.all(ph, ph + 31, jw0, jw1) && q0 + 32 * half + 32 <= q_hi;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
         const int at = 32 * half + 16 * m + 4 * g;
         const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[st][0][at]);
         const f32x4 ds = *reinterpret_cast<const f32x4*>(&stats[st][1][at]);
@@ -194,10 +204,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
             float p = fast_exp2(fmaf(s[c][m][x], sc, -ls[x]));
             if (!whole) {
               const int qi = q0 + at + x, j = jw0 + 16 * c + r;
-              bool live = mask.sees(qi + shift, j);
-              if (kFarPart) live = live && qi >= q_lo && qi < q_hi;
-              else live = live && qi < q_hi;
-              p = live ? p : 0.f;
+              p = mask.sees(qi + shift, j) && qi < q_hi && (!kFarPart || qi >= q_lo) ? p : 0.f;
             }
             s[c][m][x] = p;
             e[c][m][x] = p == 0.f ? 0.f : p * (e[c][m][x] - ds[x]);
@@ -225,56 +232,53 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     }
     if (i + 1 < count) put_stat(next, st ^ 1);
   }
-  // sums of a stretch: (far slot, head, tile, dk and dv, keys, DK)
-  const int64_t far_size = 2ll * kN * a.dim;
-  auto far_at = [&](int64_t slot) {
-    return a.far + ((slot * a.hk + kh) * a.sink_tiles + tile) * far_size;
+  // sums of a stretch: (far slot, query head, tile of 16 sinks, dk and dv, 16, dim)
+  auto far_at = [&](int64_t slot, int h, int64_t t) {
+    return a.far + ((slot * a.hq + h) * a.sink_tiles + t) * 32ll * a.dim;
   };
-  if (!kFarPart && tile < a.sink_tiles) {
-    const int64_t first = max(near_end, (int64_t)max(j0 - shift, 0)), base = tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
-    const int64_t stretches = first < qs.len ? (qs.len - first + kFar - 1) / kFar : 0;
-    for (int64_t x = 0; x < stretches; ++x) {
-      const float* from = far_at(base + x);
-#pragma unroll
-      for (int c = 0; c < kC2; ++c) {
-        const int j = w0 + 16 * c + r;
-        if (j < nk)
-#pragma unroll
-          for (int d = 0; d < DK / 16; ++d) {
-            const int v = KT::value(d, g, 0);
-            if (v < a.dim) {
-              dk[c][d] += *reinterpret_cast<const f32x4*>(from + j * a.dim + v);
-              dv[c][d] += *reinterpret_cast<const f32x4*>(from + (kN + j) * a.dim + v);
-            }
-          }
-      }
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < kC2; ++c) {
-    const int j = w0 + 16 * c + r;
-    if (j >= nk) continue;
-    if (kFarPart) {
-      float* to = far_at(far_slot);
+  if (kFarPart) {
+    if (r < nk) {
+      float* to = far_at(far_slot, hq0, tile) + r * a.dim;
 #pragma unroll
       for (int d = 0; d < DK / 16; ++d) {
         const int v = KT::value(d, g, 0);
         if (v < a.dim) {
-          *reinterpret_cast<f32x4*>(to + j * a.dim + v) = dk[c][d];
-          *reinterpret_cast<f32x4*>(to + (kN + j) * a.dim + v) = dv[c][d];
+          *reinterpret_cast<f32x4*>(to + v) = dk[0][d];
+          *reinterpret_cast<f32x4*>(to + 16 * a.dim + v) = dv[0][d];
         }
       }
-    } else {
-      const int64_t at = ((ks.first + j0 + j) * a.hk + kh) * (int64_t)a.dim;
+    }
+    return;
+  }
+  const int64_t first = near(tile), stretches = first < qs.len ? (qs.len - first + kFar - 1) / kFar : 0;
+  const int64_t far_base = tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
 #pragma unroll
-      for (int d = 0; d < DK / 16; ++d) dk[c][d] *= a.scale;
+  for (int c = 0; c < kC2; ++c) {
+    const int j = w0 + 16 * c + r;
+    const int64_t t16 = (j0 + w0) / 16 + c;  // these 16 keys among the sinks' tiles
+    if (t16 < a.sink_tiles && j < nk)
+      for (int64_t x = 0; x < stretches; ++x)
+        for (int h = 0; h < a.rep; ++h) {
+          const float* from = far_at(far_base + x, kh * a.rep + h, t16) + r * a.dim;
 #pragma unroll
-      for (int d = 0; d < DK / 16; d += M::kTiles) {
-        const int v = KT::value(d, g, 0);
-        if (v < a.dim) {
-          store_operand(static_cast<E*>(a.dk) + at + v, &dk[c][d]);
-          store_operand(static_cast<E*>(a.dv) + at + v, &dv[c][d]);
+          for (int d = 0; d < DK / 16; ++d) {
+            const int v = KT::value(d, g, 0);
+            if (v < a.dim) {
+              dk[c][d] += *reinterpret_cast<const f32x4*>(from + v);
+              dv[c][d] += *reinterpret_cast<const f32x4*>(from + 16 * a.dim + v);
+            }
+          }
         }
+    if (j >= nk) continue;
+    const int64_t at = ((ks.first + j0 + j) * a.hk + kh) * (int64_t)a.dim;
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) dk[c][d] *= a.scale;
+#pragma unroll
+    for (int d = 0; d < DK / 16; d += M::kTiles) {
+      const int v = KT::value(d, g, 0);
+      if (v < a.dim) {
+        store_operand(static_cast<E*>(a.dk) + at + v, &dk[c][d]);
+        store_operand(static_cast<E*>(a.dv) + at + v, &dv[c][d]);
       }
     }
   }
@@ -458,11 +462,10 @@ BwdLayout layout(const mamba_window_dims* d, bool packed) {
   l.tokens = packed ? d->seqlen : d->batch * d->seqlen;
   l.far = ((size_t)l.tokens * (size_t)d->q_heads * 2 * sizeof(float) + 255) / 256 * 256;
   l.total = l.far;
-  const int rows = d->io_dtype == MAMBA_BF16 ? kRows<uint16_t> : kRows<float>;
   if (d->sinks && d->window < d->kv_len) {  // (a window of every key leaves no query past it)
     l.far_slots = tile_slots(d->seqlen, d->batch, packed, kFar);
-    l.sink_tiles = (int32_t)((std::min(d->sinks, d->kv_len) + rows - 1) / rows);
-    l.total += (size_t)l.far_slots * (size_t)d->kv_heads * (size_t)l.sink_tiles * 2 * rows * (size_t)d->dim * sizeof(float);
+    l.sink_tiles = (int32_t)((std::min(d->sinks, d->kv_len) + 15) / 16);
+    l.total += (size_t)l.far_slots * (size_t)d->q_heads * (size_t)l.sink_tiles * 32 * (size_t)d->dim * sizeof(float);
   }
   return l;
 }
@@ -480,8 +483,8 @@ int launch_bwd(const WinArgs& a, int64_t tokens, hipStream_t s) {
   hipLaunchKernelGGL((window_dq_kernel<E, DK>), wide_grid(queries, 256), dim3(256), 0, s, a, queries, tokens);
   if ((st = launch_status()) != MAMBA_OK) return st;
   if (a.sink_tiles) {
-    const uint32_t blocks = (uint32_t)(a.far_slots * a.hk * a.sink_tiles);
-    hipLaunchKernelGGL((window_dkv_kernel<E, DK, true>), wide_grid(blocks, 256), dim3(256), 0, s, a, blocks, tokens);
+    const uint32_t blocks = (uint32_t)(a.far_slots * a.hq * a.sink_tiles);
+    hipLaunchKernelGGL((window_dkv_kernel<E, DK, true>), wide_grid(blocks, 64), dim3(64), 0, s, a, blocks, tokens);
     if ((st = launch_status()) != MAMBA_OK) return st;
   }
   const uint32_t keys = (uint32_t)(tile_slots(a.kv_len, a.nseq, packed, kRows<E>) * a.hk);
