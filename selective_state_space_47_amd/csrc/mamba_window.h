@@ -107,6 +107,14 @@ __device__ __forceinline__ void load_rows(const E* p, int64_t stride, int row, i
   }
 }
 
+// Operands are read from LDS a step before the products that take them, as one or two waves per SIMD leave nobody
+// else to hide the reads behind; nothing is moved past the end of a step.
+__device__ __forceinline__ void end_step() { __builtin_amdgcn_sched_barrier(0); }
+
+// Every load of this wave has landed, said so that the compiler counts it too.  Operands loaded before a loop would
+// otherwise be waited for again at their first use in every turn, and with them the copies of the next tile.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
 constexpr int64_t kMaxTokens = 0x7fffffff - 1024;
 constexpr int64_t kMaxWindow = (int64_t)1 << 40;
 

@@ -85,6 +85,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
   }
   const KT kt(lane);
   const int pw0 = p0 + w0, pw1 = pw0 + 16 * kC2 - 1;
+  loads_done();
   for (int i = 0; i < count; ++i) {
     const int st = i & 1, j0 = tile_at(i) * kKeys;
     copies_done();
@@ -96,14 +97,28 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
     for (int c = 0; c < kC2; ++c)
 #pragma unroll
       for (int m = 0; m < 4; ++m) s[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int kStepsK = DK / M::kDepth, kGroups = DK / 64, kStepsV = kKeys / M::kDepth * kGroups;
+    typename M::Frag f[2][4];
+    auto read_k = [&](int i) {
 #pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb)
+      for (int m = 0; m < 4; ++m) f[i & 1][m] = kt.rows(sk, m, i);
+    };
+    auto read_v = [&](int i) {  // (kStepsK is even)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const auto kf = kt.rows(sk, m, kb);
+      for (int x = 0; x < 4; ++x) f[i & 1][x] = kt.cols(sv, i % kGroups * 4 + x, i / kGroups);
+    };
+    read_k(0);
 #pragma unroll
-        for (int c = 0; c < kC2; ++c) s[c][m] = M::mma(kf, qf[c][kb], s[c][m]);
-      }
+    for (int kb = 0; kb < kStepsK; ++kb) {
+      end_step();
+      if (kb + 1 < kStepsK) read_k(kb + 1); else read_v(0);
+      end_step();
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int c = 0; c < kC2; ++c) s[c][m] = M::mma(f[kb & 1][m], qf[c][kb], s[c][m]);
+    }
+    end_step();
     const bool whole = mask.all(pw0, pw1, j0, j0 + kKeys - 1);
 #pragma unroll
     for (int c = 0; c < kC2; ++c) {
@@ -133,27 +148,35 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float e = s[c][m][x];
-          float pr = fast_exp2(fmaf(e, sc, -use));
-          if (!whole) pr = e == kMinusInf ? 0.f : pr;
-          s[c][m][x] = pr;
-          sum += pr;
-        }
+        for (int x = 0; x < 4; ++x) s[c][m][x] = fast_exp2(fmaf(s[c][m][x], sc, -use));
+      if (!whole && sc == 0.f)  // (a scale of zero makes NaN of the masked scores)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (!mask.sees(p, j0 + 16 * m + 4 * g + x)) s[c][m][x] = 0.f;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) sum += (s[c][m][0] + s[c][m][1]) + (s[c][m][2] + s[c][m][3]);
       l[c] += sum;
     }
+    typename M::Frag pf[kC2];
 #pragma unroll
-    for (int kb = 0; kb < kKeys / M::kDepth; ++kb) {
-      typename M::Frag pf[kC2];
+    for (int i = 0; i < kStepsV; ++i) {
+      if (i % kGroups == 0)
 #pragma unroll
-      for (int c = 0; c < kC2; ++c) pf[c] = M::pack(&s[c][kb * M::kTiles]);
+        for (int c = 0; c < kC2; ++c) pf[c] = M::pack(&s[c][i / kGroups * M::kTiles]);
+      end_step();
+      if (i + 1 < kStepsV) read_v(i + 1);
+      end_step();
 #pragma unroll
-      for (int d = 0; d < DK / 16; ++d) {
-        const auto vf = kt.cols(sv, d, kb);
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int c = 0; c < kC2; ++c) o[c][d] = M::mma(vf, pf[c], o[c][d]);
-      }
+        for (int c = 0; c < kC2; ++c) {
+          f32x4& to = o[c][i % kGroups * 4 + x];
+          to = M::mma(f[i & 1][x], pf[c], to);
+        }
     }
+    end_step();
   }
 #pragma unroll
   for (int c = 0; c < kC2; ++c) {

@@ -60,12 +60,12 @@ __global__ __launch_bounds__(256) void window_stat_kernel(WinArgs a, int64_t tok
 // kFarPart: one wave, 16 sinks and one query head over a stretch of queries past the sinks' windows; otherwise a tile
 // of keys, the heads that share it one after another.
 template <typename E, int DK, bool kFarPart>
-__global__ __launch_bounds__(kFarPart ? 64 : 256, sizeof(E) == 2 && !kFarPart ? 2 : 1) void window_dkv_kernel(
+__global__ __launch_bounds__(kFarPart ? 64 : 256, 1) void window_dkv_kernel(
     WinArgs a, uint32_t blocks, int64_t tokens) {
   using M = Mma<E>;
   using KT = KeyTile<E, DK>;
   constexpr int kNW = kFarPart ? 1 : 4, kC2 = kFarPart ? 1 : kTilesW<E>, kN = kFarPart ? 16 : kRows<E>;
-  constexpr int kStage = 2 * KT::kBytes, kHalf = 32 / 16;
+  constexpr int kStage = 2 * KT::kBytes;
   __shared__ __align__(1024) char smem[2 * kStage];
   __shared__ __align__(16) float stats[2][2][kKeys];
   const uint32_t id = wide_index();
@@ -164,6 +164,7 @@ __global__ __launch_bounds__(kFarPart ? 64 : 256, sizeof(E) == 2 && !kFarPart ? 
     for (int d = 0; d < DK / 16; ++d) dk[c][d] = dv[c][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   const KT kt(lane);
   const int jw0 = j0 + w0, jw1 = jw0 + 16 * kC2 - 1;
+  loads_done();
   for (int i = 0; i < count; ++i) {
     const int st = i & 1, h = i / tiles, q0 = (t_lo + i - h * tiles) * kKeys;
     float2 next = make_float2(0.f, 0.f);
@@ -179,56 +180,90 @@ __global__ __launch_bounds__(kFarPart ? 64 : 256, sizeof(E) == 2 && !kFarPart ? 
       const int ph = p0 + 32 * half;
       if (mask.none(ph, ph + 31, jw0, jw1)) continue;
       const bool whole = !kFarPart && mask.all(ph, ph + 31, jw0, jw1) && q0 + 32 * half + 32 <= q_hi;
-      // 16 queries at a time: scores and dO V^T, rows = queries, column = key; then P and dS, as operands
-      f32x4 s[kC2][kHalf], e[kC2][kHalf];
+      // 32 queries: scores and dO V^T, rows = queries, column = key; then P and dS, as operands
+      f32x4 s[kC2][2], e[kC2][2];
 #pragma unroll
-      for (int m = 0; m < kHalf; ++m) {
+      for (int c = 0; c < kC2; ++c)
 #pragma unroll
-        for (int c = 0; c < kC2; ++c) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int m = 0; m < 2; ++m) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      constexpr int kStepsK = DK / M::kDepth, kGroups = DK / 32, kStepsV = 32 / M::kDepth * kGroups;
+      typename M::Frag f[2][4];
+      auto read_k = [&](int i) {
 #pragma unroll
-        for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-          const auto qf = kt.rows(sq, 2 * half + m, kb), of = kt.rows(so, 2 * half + m, kb);
+        for (int m = 0; m < 2; ++m) {
+          f[i & 1][m] = kt.rows(sq, 2 * half + m, i);
+          f[i & 1][2 + m] = kt.rows(so, 2 * half + m, i);
+        }
+      };
+      auto read_v = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int d = i % kGroups * 2 + x, b = half * (32 / M::kDepth) + i / kGroups;
+          f[i & 1][x] = kt.cols(sq, d, b);
+          f[i & 1][2 + x] = kt.cols(so, d, b);
+        }
+      };
+      read_k(0);
+#pragma unroll
+      for (int kb = 0; kb < kStepsK; ++kb) {
+        end_step();
+        if (kb + 1 < kStepsK) read_k(kb + 1); else read_v(0);
+        end_step();
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int c = 0; c < kC2; ++c) {
-            s[c][m] = M::mma(qf, kf[c][kb], s[c][m]);
-            e[c][m] = M::mma(of, vf[c][kb], e[c][m]);
+            s[c][m] = M::mma(f[kb & 1][m], kf[c][kb], s[c][m]);
+            e[c][m] = M::mma(f[kb & 1][2 + m], vf[c][kb], e[c][m]);
           }
-        }
-        const int at = 32 * half + 16 * m + 4 * g;
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[st][0][at]);
-        const f32x4 ds = *reinterpret_cast<const f32x4*>(&stats[st][1][at]);
+      }
+      end_step();
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[st][0][32 * half + 16 * m + 4 * g]);
 #pragma unroll
         for (int c = 0; c < kC2; ++c)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float p = fast_exp2(fmaf(s[c][m][x], sc, -ls[x]));
-            if (!whole) {
-              const int qi = q0 + at + x, j = jw0 + 16 * c + r;
-              p = mask.sees(qi + shift, j) && qi < q_hi && (!kFarPart || qi >= q_lo) ? p : 0.f;
-            }
-            s[c][m][x] = p;
-            e[c][m][x] = p == 0.f ? 0.f : p * (e[c][m][x] - ds[x]);
-          }
+          for (int x = 0; x < 4; ++x) s[c][m][x] = fast_exp2(fmaf(s[c][m][x], sc, -ls[x]));
       }
+      if (!whole)
 #pragma unroll
-      for (int kb = 0; kb < 32 / M::kDepth; ++kb) {
-        typename M::Frag pf[kC2], ef[kC2];
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int c = 0; c < kC2; ++c) {
-          pf[c] = M::pack(&s[c][kb * M::kTiles]);
-          ef[c] = M::pack(&e[c][kb * M::kTiles]);
-        }
-        const int b = half * (32 / M::kDepth) + kb;
+          for (int c = 0; c < kC2; ++c)
 #pragma unroll
-        for (int d = 0; d < DK / 16; ++d) {
-          const auto of = kt.cols(so, d, b), qf = kt.cols(sq, d, b);
+            for (int x = 0; x < 4; ++x) {
+              const int qi = q0 + 32 * half + 16 * m + 4 * g + x, j = jw0 + 16 * c + r;
+              if (!(mask.sees(qi + shift, j) && qi < q_hi && (!kFarPart || qi >= q_lo))) s[c][m][x] = 0.f;
+            }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const f32x4 ds = *reinterpret_cast<const f32x4*>(&stats[st][1][32 * half + 16 * m + 4 * g]);
+#pragma unroll
+        for (int c = 0; c < kC2; ++c) e[c][m] = s[c][m] * (e[c][m] - ds);
+      }
+      typename M::Frag pf[kC2], ef[kC2];
+#pragma unroll
+      for (int i = 0; i < kStepsV; ++i) {
+        if (i % kGroups == 0)
 #pragma unroll
           for (int c = 0; c < kC2; ++c) {
-            dv[c][d] = M::mma(of, pf[c], dv[c][d]);
-            dk[c][d] = M::mma(qf, ef[c], dk[c][d]);
+            pf[c] = M::pack(&s[c][i / kGroups * M::kTiles]);
+            ef[c] = M::pack(&e[c][i / kGroups * M::kTiles]);
           }
-        }
+        end_step();
+        if (i + 1 < kStepsV) read_v(i + 1);
+        end_step();
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) {
+            const int d = i % kGroups * 2 + x;
+            dk[c][d] = M::mma(f[i & 1][x], ef[c], dk[c][d]);
+            dv[c][d] = M::mma(f[i & 1][2 + x], pf[c], dv[c][d]);
+          }
       }
+      end_step();
     }
     if (i + 1 < count) put_stat(next, st ^ 1);
   }
@@ -353,37 +388,61 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     for (int d = 0; d < DK / 16; ++d) dq[c][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   const KT kt(lane);
   const int pw0 = p0 + w0, pw1 = pw0 + 16 * kC2 - 1;
-  // 32 keys of the stage at sk: P and dO V^T, rows = keys, column = query
-  auto scores = [&](lds_ptr sk, int j0, int half, f32x4 (&s)[kC2][2], f32x4 (&e)[kC2][2]) {
+  constexpr int kStepsK = DK / M::kDepth, kGroups = DK / 64, kStepsV = 32 / M::kDepth * kGroups;
+  typename M::Frag f[2][4];
+  auto read_cols = [&](lds_ptr sk, int half, int i) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      f[i & 1][x] = kt.cols(sk, i % kGroups * 4 + x, half * (32 / M::kDepth) + i / kGroups);
+  };
+  // 32 keys of the stage at sk: P and dO V^T, rows = keys, column = query; `then` reads what the products after them
+  // take first
+  auto scores = [&](lds_ptr sk, int j0, int half, f32x4 (&s)[kC2][2], f32x4 (&e)[kC2][2], auto then) {
     const lds_ptr sv = sk + KT::kBytes;
     const int jh = j0 + 32 * half;
 #pragma unroll
     for (int c = 0; c < kC2; ++c)
 #pragma unroll
       for (int m = 0; m < 2; ++m) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb)
+    auto read = [&](int kb) {
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const auto kf = kt.rows(sk, 2 * half + m, kb), vf = kt.rows(sv, 2 * half + m, kb);
+        f[kb & 1][m] = kt.rows(sk, 2 * half + m, kb);
+        f[kb & 1][2 + m] = kt.rows(sv, 2 * half + m, kb);
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int kb = 0; kb < kStepsK; ++kb) {
+      end_step();
+      if (kb + 1 < kStepsK) read(kb + 1); else then();
+      end_step();
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int c = 0; c < kC2; ++c) {
-          s[c][m] = M::mma(kf, qf[c][kb], s[c][m]);
-          e[c][m] = M::mma(vf, of[c][kb], e[c][m]);
+          s[c][m] = M::mma(f[kb & 1][m], qf[c][kb], s[c][m]);
+          e[c][m] = M::mma(f[kb & 1][2 + m], of[c][kb], e[c][m]);
         }
-      }
-    const bool whole = mask.all(pw0, pw1, jh, jh + 31);
+    }
+    end_step();
 #pragma unroll
     for (int c = 0; c < kC2; ++c)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float p = fast_exp2(fmaf(s[c][m][x], sc, -ls[c]));
-          s[c][m][x] = whole || mask.sees(pw0 + 16 * c + r, jh + 16 * m + 4 * g + x) ? p : 0.f;
-        }
+        for (int x = 0; x < 4; ++x) s[c][m][x] = fast_exp2(fmaf(s[c][m][x], sc, -ls[c]));
+    if (!mask.all(pw0, pw1, jh, jh + 31))
+#pragma unroll
+      for (int c = 0; c < kC2; ++c)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (!mask.sees(pw0 + 16 * c + r, jh + 16 * m + 4 * g + x)) s[c][m][x] = 0.f;
   };
   int turn = 0;  // stages
+  loads_done();
   if constexpr (kTwice) {
     for (int i = 0; i < count; ++i, ++turn) {
       const int st = turn & 1, j0 = tile_at(i) * kKeys;
@@ -393,13 +452,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
       for (int half = 0; half < 2; ++half) {
         if (mask.none(pw0, pw1, j0 + 32 * half, j0 + 32 * half + 31)) continue;
         f32x4 s[kC2][2], e[kC2][2];
-        scores((lds_ptr)(smem + st * kStage), j0, half, s, e);
+        scores((lds_ptr)(smem + st * kStage), j0, half, s, e, [] {});
 #pragma unroll
         for (int c = 0; c < kC2; ++c)
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) ds[c] += s[c][m][x] == 0.f ? 0.f : s[c][m][x] * e[c][m][x];
+            for (int x = 0; x < 4; ++x) ds[c] = fmaf(s[c][m][x], e[c][m][x], ds[c]);
       }
     }
 #pragma unroll
@@ -418,25 +477,30 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     for (int half = 0; half < 2; ++half) {
       if (mask.none(pw0, pw1, j0 + 32 * half, j0 + 32 * half + 31)) continue;
       f32x4 s[kC2][2], e[kC2][2];
-      scores(sk, j0, half, s, e);
+      scores(sk, j0, half, s, e, [&] { read_cols(sk, half, 0); });
 #pragma unroll
       for (int c = 0; c < kC2; ++c)
 #pragma unroll
         for (int m = 0; m < 2; ++m)
+          e[c][m] = s[c][m] * (e[c][m] - ds[c]);
+      typename M::Frag ef[kC2];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) e[c][m][x] = s[c][m][x] == 0.f ? 0.f : s[c][m][x] * (e[c][m][x] - ds[c]);
+      for (int i = 0; i < kStepsV; ++i) {
+        if (i % kGroups == 0)
 #pragma unroll
-      for (int kb = 0; kb < 32 / M::kDepth; ++kb) {
-        typename M::Frag ef[kC2];
+          for (int c = 0; c < kC2; ++c) ef[c] = M::pack(&e[c][i / kGroups * M::kTiles]);
+        end_step();
+        if (i + 1 < kStepsV) read_cols(sk, half, i + 1);
+        end_step();
 #pragma unroll
-        for (int c = 0; c < kC2; ++c) ef[c] = M::pack(&e[c][kb * M::kTiles]);
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int d = 0; d < DK / 16; ++d) {
-          const auto kc = kt.cols(sk, d, half * (32 / M::kDepth) + kb);
-#pragma unroll
-          for (int c = 0; c < kC2; ++c) dq[c][d] = M::mma(kc, ef[c], dq[c][d]);
-        }
+          for (int c = 0; c < kC2; ++c) {
+            f32x4& to = dq[c][i % kGroups * 4 + x];
+            to = M::mma(f[i & 1][x], ef[c], to);
+          }
       }
+      end_step();
     }
   }
 #pragma unroll
