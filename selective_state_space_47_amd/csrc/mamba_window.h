@@ -61,6 +61,21 @@ __device__ __forceinline__ int64_t tile_seq(const int64_t* offsets, int64_t tota
   }
   return lo;
 }
+// The sequence and the tile of a workgroup's slot; a tile below zero or past the sequence is an unused slot of a packed
+// batch.  Equally long sequences go tile by tile, all of them beside each other, from the end where kLast: the tiles
+// with the most work start first, and a sequence's (of one head) share an XCD where their number allows.
+struct Tile {
+  int64_t seq, tile;
+};
+template <bool kLast>
+__device__ __forceinline__ Tile tile_of(const int64_t* offsets, int64_t total, int64_t nseq, int64_t slot, int unit) {
+  if (!offsets) {
+    const int64_t n = (total + unit - 1) / unit, t = slot / nseq;
+    return {slot - t * nseq, kLast ? n - 1 - t : t};
+  }
+  const int64_t seq = tile_seq(offsets, total, nseq, slot, unit);
+  return {seq, slot - tile_base(offsets, total, seq, min(max(offsets[seq], (int64_t)0), total), unit)};
+}
 inline int64_t tile_slots(int64_t total, int64_t nseq, bool packed, int unit) {
   return packed ? total / unit + nseq : nseq * ((total + unit - 1) / unit);
 }
@@ -132,9 +147,9 @@ inline int check_window(const mamba_window_dims* d, bool packed) {
   if (seqs * (double)d->seqlen * (double)d->q_heads * (double)d->dim > lim ||
       seqs * (double)d->kv_len * (double)d->kv_heads * (double)d->dim > lim)
     return MAMBA_ERR_SHAPE;
-  // the grids: one workgroup per 64 tokens and head
+  // the grids: one workgroup per 64 queries or 32 keys and head
   if ((seqs * (double)d->seqlen / kKeys + (double)d->batch) * (double)d->q_heads > 2147483647.0 ||
-      (seqs * (double)d->kv_len / kKeys + (double)d->batch) * (double)d->kv_heads > 2147483647.0)
+      (seqs * (double)d->kv_len / 32 + (double)d->batch) * (double)d->kv_heads > 2147483647.0)
     return MAMBA_ERR_SHAPE;
   // tokens are read as 16-byte words
   const int64_t vec = d->io_dtype == MAMBA_BF16 ? 8 : 4;

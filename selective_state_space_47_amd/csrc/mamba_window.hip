@@ -34,9 +34,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
   const int64_t wg = spread_index(id, blocks, a.rep);
   const int64_t slot = wg / a.hq;
   const int h = (int)(wg - slot * a.hq), kh = h / a.rep;
-  const int64_t seq = tile_seq(a.q_offsets, a.seqlen, a.nseq, slot, kQ);
+  const auto [seq, tile] = tile_of<true>(a.q_offsets, a.seqlen, a.nseq, slot, kQ);
   const Seq qs = seq_of(a.q_offsets, a.seqlen, seq), ks = seq_of(a.kv_offsets, a.kv_len, seq);
-  const int64_t tile = slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, kQ);
   if (tile < 0 || tile * kQ >= qs.len) return;  // an unused slot of a packed batch
   const int q0 = (int)tile * kQ, nq = min(qs.len - q0, kQ);
   const int shift = ks.len - qs.len;  // position of query 0

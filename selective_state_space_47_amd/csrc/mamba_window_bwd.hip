@@ -6,7 +6,7 @@
 //   window_stat_kernel  fp32 storage: lse log2(e) and D = dO . out of every query and head, head by head
 //   window_dq_kernel    as the forward, 128 queries (fp32 storage: 64) through their keys; with bf16 storage twice, first
 //                       for D, which it leaves for the next kernel with lse log2(e)
-//   window_dkv_kernel   128 keys (64) of one head, through the queries that see them, heads that share it one after
+//   window_dkv_kernel   64 keys (32) of one head, through the queries that see them, heads that share it one after
 //                       another: sums in accumulators in a fixed order, no atomics
 // The sinks are seen by every later query: the queries past the windows of a sinks' tile are cut into stretches,
 // which window_dkv_kernel takes first, as workgroups of their own that leave fp32 sums; the tile's own workgroup, of
@@ -28,6 +28,9 @@ template <typename E>
 constexpr int kTilesW = sizeof(E) == 2 ? 2 : 1;  // 16-row tiles of a wave
 template <typename E>
 constexpr int kRows = 4 * 16 * kTilesW<E>;       // of a workgroup
+constexpr int kPairs = 2;                        // pairs of waves that share the keys of a workgroup of the keys' pass
+template <typename E>
+constexpr int kKeyRows = kPairs * 16 * kTilesW<E>;
 constexpr int kFar = 512;                        // queries of a stretch past the sinks' windows
 
 // 8 lanes per row; a row without a key has weights of zero: its log-sum counts as +infinity
@@ -57,15 +60,146 @@ __global__ __launch_bounds__(256) void window_stat_kernel(WinArgs a, int64_t tok
   }
 }
 
-// kFarPart: one wave, 16 sinks and one query head over a stretch of queries past the sinks' windows; otherwise a tile
-// of keys, the heads that share it one after another.
-template <typename E, int DK, bool kFarPart>
-__global__ __launch_bounds__(kFarPart ? 64 : 256, 1) void window_dkv_kernel(
-    WinArgs a, uint32_t blocks, int64_t tokens) {
+// What a wave of the keys' pass makes: dV (from P), or dK (from P and dO V^T).  Two waves share 32 keys (fp32 storage:
+// 16): with both sums in one wave there is room for one wave on a SIMD, which has nobody to hide its waits behind.
+// (8 x 2048 tokens, 20 and 4 heads of 128, window 1024: 395 us; both sums in one wave and 128 keys per workgroup 491,
+// by roles with 128 keys 503, as the longest workgroups then ran alone at the end.)
+enum Role { kMakeDv, kMakeDk };
+
+// The queries' tiles of a workgroup of the keys' pass
+struct KeyWork {
+  int q_lo, q_hi;    // queries
+  int t_lo, tiles;   // their tiles
+  int count;         // tiles times heads, the heads one after another
+  int shift;         // position of query 0
+};
+
+// A wave's share: 16 kC2 keys from jw0 on against the tiles of queries that come into the stages.
+template <typename E, int DK, bool kFarPart, int kC2, Role kRole, typename Copy, typename Load, typename Put>
+__device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, const Mask& mask, char* smem,
+                                         const float (&stats)[2][2][kKeys], int jw0, float sc,
+                                         const typename Mma<E>::Frag (&kf)[kC2][DK / Mma<E>::kDepth],
+                                         const typename Mma<E>::Frag (&vf)[kC2][DK / Mma<E>::kDepth],
+                                         f32x4 (&acc)[kC2][DK / 16], Copy copy, Load load_stat, Put put_stat) {
   using M = Mma<E>;
   using KT = KeyTile<E, DK>;
-  constexpr int kNW = kFarPart ? 1 : 4, kC2 = kFarPart ? 1 : kTilesW<E>, kN = kFarPart ? 16 : kRows<E>;
   constexpr int kStage = 2 * KT::kBytes;
+  constexpr int kPer = kRole == kMakeDv ? 2 : 1;  // depths of a step of the scores
+  constexpr int kStepsK = DK / M::kDepth / kPer, kGroups = DK / 64, kStepsV = 32 / M::kDepth * kGroups;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const KT kt(lane);
+  const int jw1 = jw0 + 16 * kC2 - 1;
+  for (int i = 0; i < k.count; ++i) {
+    const int st = i & 1, h = i / k.tiles, q0 = (k.t_lo + i - h * k.tiles) * kKeys;
+    float2 next = make_float2(0.f, 0.f);
+    copies_done();
+    if (i + 1 < k.count) {
+      next = load_stat(i + 1);
+      copy(i + 1, st ^ 1);
+    }
+    const lds_ptr sq = (lds_ptr)(smem + st * kStage), so = sq + KT::kBytes;
+    const lds_ptr sums = kRole == kMakeDv ? so : sq;  // whose transpose the sums take
+    const int p0 = q0 + k.shift;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int ph = p0 + 32 * half;
+      if (mask.none(ph, ph + 31, jw0, jw1)) continue;
+      const bool whole = !kFarPart && mask.all(ph, ph + 31, jw0, jw1) && q0 + 32 * half + 32 <= k.q_hi;
+      // 32 queries: scores and dO V^T, rows = queries, column = key; then P or dS, as operands
+      f32x4 s[kC2][2], e[kC2][2];
+#pragma unroll
+      for (int c = 0; c < kC2; ++c)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      typename M::Frag f[2][4];
+      auto read_k = [&](int i) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          f[i & 1][m] = kt.rows(sq, 2 * half + m, kPer * i);
+          f[i & 1][2 + m] = kRole == kMakeDv ? kt.rows(sq, 2 * half + m, kPer * i + 1) : kt.rows(so, 2 * half + m, i);
+        }
+      };
+      auto read_v = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          f[(i + kStepsK) & 1][x] = kt.cols(sums, i % kGroups * 4 + x, half * (32 / M::kDepth) + i / kGroups);
+      };
+      read_k(0);
+#pragma unroll
+      for (int kb = 0; kb < kStepsK; ++kb) {
+        end_step();
+        if (kb + 1 < kStepsK) read_k(kb + 1); else read_v(0);
+        end_step();
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) {
+            s[c][m] = M::mma(f[kb & 1][m], kf[c][kPer * kb], s[c][m]);
+            if constexpr (kRole == kMakeDv)
+              e[c][m] = M::mma(f[kb & 1][2 + m], kf[c][kPer * kb + 1], e[c][m]);  // (the other half of the scores)
+            else
+              e[c][m] = M::mma(f[kb & 1][2 + m], vf[c][kb], e[c][m]);
+          }
+      }
+      end_step();
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[st][0][32 * half + 16 * m + 4 * g]);
+#pragma unroll
+        for (int c = 0; c < kC2; ++c) {
+          if (kRole == kMakeDv) s[c][m] += e[c][m];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[c][m][x] = fast_exp2(fmaf(s[c][m][x], sc, -ls[x]));
+        }
+      }
+      if (!whole)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int c = 0; c < kC2; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int qi = q0 + 32 * half + 16 * m + 4 * g + x, j = jw0 + 16 * c + r;
+              if (!(mask.sees(qi + k.shift, j) && qi < k.q_hi && (!kFarPart || qi >= k.q_lo))) s[c][m][x] = 0.f;
+            }
+      if constexpr (kRole == kMakeDk)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const f32x4 ds = *reinterpret_cast<const f32x4*>(&stats[st][1][32 * half + 16 * m + 4 * g]);
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) s[c][m] = s[c][m] * (e[c][m] - ds);
+        }
+      typename M::Frag pf[kC2];
+#pragma unroll
+      for (int i = 0; i < kStepsV; ++i) {
+        if (i % kGroups == 0)
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) pf[c] = M::pack(&s[c][i / kGroups * M::kTiles]);
+        end_step();
+        if (i + 1 < kStepsV) read_v(i + 1);
+        end_step();
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) {
+            f32x4& to = acc[c][i % kGroups * 4 + x];
+            to = M::mma(f[(i + kStepsK) & 1][x], pf[c], to);
+          }
+      }
+      end_step();
+    }
+    if (i + 1 < k.count) put_stat(next, st ^ 1);
+  }
+}
+
+// kFarPart: 16 sinks and one query head over a stretch of queries past the sinks' windows; otherwise a tile of keys, the
+// heads that share it one after another.
+template <typename E, int DK, bool kFarPart>
+__global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(WinArgs a, uint32_t blocks, int64_t tokens) {
+  using M = Mma<E>;
+  using KT = KeyTile<E, DK>;
+  constexpr int kP = kFarPart ? 1 : kPairs, kNW = 2 * kP, kC2 = kFarPart ? 1 : kTilesW<E>;
+  constexpr int kN = kFarPart ? 16 : kKeyRows<E>, kStage = 2 * KT::kBytes;
   __shared__ __align__(1024) char smem[2 * kStage];
   __shared__ __align__(16) float stats[2][2][kKeys];
   const uint32_t id = wide_index();
@@ -86,39 +220,40 @@ __global__ __launch_bounds__(kFarPart ? 64 : 256, 1) void window_dkv_kernel(
     kh = (int)(id - slot * a.hk);
     h0 = 0;
     heads = a.rep;
-    seq = tile_seq(a.kv_offsets, a.kv_len, a.nseq, slot, kN);
-    tile = slot;
+    const Tile t = tile_of<false>(a.kv_offsets, a.kv_len, a.nseq, slot, kN);
+    seq = t.seq;
+    tile = t.tile;
   }
   const Seq qs = seq_of(a.q_offsets, a.seqlen, seq), ks = seq_of(a.kv_offsets, a.kv_len, seq);
-  if (kFarPart)
-    stretch = far_slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
-  else
-    tile -= tile_base(a.kv_offsets, a.kv_len, seq, ks.first, kN);
+  if (kFarPart) stretch = far_slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
   if (tile < 0 || tile * kN >= ks.len || stretch < 0) return;
   const int j0 = (int)tile * kN, nk = min(ks.len - j0, kN);
-  const int shift = ks.len - qs.len;
   const Mask mask = mask_of(a);
+  KeyWork k;
+  k.shift = ks.len - qs.len;
   // Queries: those whose position is not before the tile's first key, up to the last that has a key of the tile in its
   // window; the queries behind those, which see only sinks, go by stretches.  (Both kinds of tile begin them with
-  // the same query: that past the window of the last key of the sinks' first tile of kRows keys.)
-  auto near = [&](int64_t t) {  // first query past the windows of the t-th kRows keys
-    const int64_t last = min((t + 1) * kRows<E>, (int64_t)ks.len) - 1;
-    return max(min(last + a.window - shift, (int64_t)qs.len), max(t * kRows<E> - shift, (int64_t)0));
+  // the same query: that past the window of the last of the kKeyRows keys that the sinks lie in.)
+  auto near = [&](int64_t t) {  // first query past the windows of the t-th kKeyRows keys
+    const int64_t last = min((t + 1) * kKeyRows<E>, (int64_t)ks.len) - 1;
+    return max(min(last + a.window - k.shift, (int64_t)qs.len), max(t * kKeyRows<E> - k.shift, (int64_t)0));
   };
-  int q_lo = max(j0 - shift, 0), q_hi;
   if (kFarPart) {
-    const int64_t b = near(j0 / kRows<E>) + stretch * kFar;
-    q_lo = (int)min(b, (int64_t)qs.len);
-    q_hi = (int)min(b + kFar, (int64_t)qs.len);
-    if (q_lo >= q_hi) return;
+    const int64_t b = near(j0 / kKeyRows<E>) + stretch * kFar;
+    k.q_lo = (int)min(b, (int64_t)qs.len);
+    k.q_hi = (int)min(b + kFar, (int64_t)qs.len);
+    if (k.q_lo >= k.q_hi) return;
   } else {
-    q_hi = (int)min(near(tile), (int64_t)qs.len);
+    k.q_lo = max(j0 - k.shift, 0);
+    k.q_hi = (int)min(near(tile), (int64_t)qs.len);
   }
-  const int t_lo = q_lo / kKeys, tiles = q_hi > q_lo ? (q_hi - 1) / kKeys - t_lo + 1 : 0;
-  const int count = tiles * heads;  // heads one after another
+  k.t_lo = k.q_lo / kKeys;
+  k.tiles = k.q_hi > k.q_lo ? (k.q_hi - 1) / kKeys - k.t_lo + 1 : 0;
+  k.count = k.tiles * heads;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int w0 = 16 * kC2 * w;
+  const int w0 = 16 * kC2 * (w % kP);
+  const bool makes_dk = w >= kP;
 
   const int64_t o_stride = (int64_t)a.hq * a.dim;
   const int hq0 = kh * a.rep + h0;
@@ -127,14 +262,14 @@ __global__ __launch_bounds__(kFarPart ? 64 : 256, 1) void window_dkv_kernel(
   const uint32_t lds0 = lds_address(smem);
   const RowCopy<E, KT, kKeys, kNW> cq(w, lane, a.q_stride, a.dim), co(w, lane, o_stride, a.dim);
   auto copy = [&](int i, int st) {
-    const int h = i / tiles, t = (t_lo + i - h * tiles) * kKeys;
+    const int h = i / k.tiles, t = (k.t_lo + i - h * k.tiles) * kKeys;
     const int64_t n = min(kKeys, qs.len - t);
     cq(rows_buffer(qp + t * a.q_stride + (int64_t)h * a.dim, n, a.q_stride, a.dim), lds0 + st * kStage, w);
     co(rows_buffer(op + t * o_stride + (int64_t)h * a.dim, n, o_stride, a.dim), lds0 + st * kStage + KT::kBytes, w);
   };
   // wave 0: the log-sums and the dots; past the sequence +infinity and 0
   auto load_stat = [&](int i) {
-    const int h = i / tiles, t = (t_lo + i - h * tiles) * kKeys + lane;
+    const int h = i / k.tiles, t = (k.t_lo + i - h * k.tiles) * kKeys + lane;
     const float* p = a.stat + (int64_t)(hq0 + h) * tokens + qs.first + t;
     return w == 0 && t < qs.len ? make_float2(p[0], p[tokens * a.hq]) : make_float2(-kMinusInf, 0.f);
   };
@@ -144,149 +279,46 @@ __global__ __launch_bounds__(kFarPart ? 64 : 256, 1) void window_dkv_kernel(
       stats[st][1][lane] = v.y;
     }
   };
-  if (count) {
+  if (k.count) {
     copy(0, 0);
     put_stat(load_stat(0), 0);
   }
   typename M::Frag kf[kC2][DK / M::kDepth], vf[kC2][DK / M::kDepth];
   const E* kp = static_cast<const E*>(a.k) + (ks.first + j0) * a.k_stride + (int64_t)kh * a.dim;
   const E* vp = static_cast<const E*>(a.v) + (ks.first + j0) * a.v_stride + (int64_t)kh * a.dim;
+  f32x4 acc[kC2][DK / 16];
 #pragma unroll
   for (int c = 0; c < kC2; ++c) {
     load_rows<E, DK>(kp, a.k_stride, w0 + 16 * c + r, nk, a.dim, g, kf[c]);
-    load_rows<E, DK>(vp, a.v_stride, w0 + 16 * c + r, nk, a.dim, g, vf[c]);
+    if (makes_dk) load_rows<E, DK>(vp, a.v_stride, w0 + 16 * c + r, nk, a.dim, g, vf[c]);
+#pragma unroll
+    for (int d = 0; d < DK / 16; ++d) acc[c][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   const float sc = a.scale * kLog2e;
-  f32x4 dk[kC2][DK / 16], dv[kC2][DK / 16];
-#pragma unroll
-  for (int c = 0; c < kC2; ++c)
-#pragma unroll
-    for (int d = 0; d < DK / 16; ++d) dk[c][d] = dv[c][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const KT kt(lane);
-  const int jw0 = j0 + w0, jw1 = jw0 + 16 * kC2 - 1;
   loads_done();
-  for (int i = 0; i < count; ++i) {
-    const int st = i & 1, h = i / tiles, q0 = (t_lo + i - h * tiles) * kKeys;
-    float2 next = make_float2(0.f, 0.f);
-    copies_done();
-    if (i + 1 < count) {
-      next = load_stat(i + 1);
-      copy(i + 1, st ^ 1);
-    }
-    const lds_ptr sq = (lds_ptr)(smem + st * kStage), so = sq + KT::kBytes;
-    const int p0 = q0 + shift;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int ph = p0 + 32 * half;
-      if (mask.none(ph, ph + 31, jw0, jw1)) continue;
-      const bool whole = !kFarPart && mask.all(ph, ph + 31, jw0, jw1) && q0 + 32 * half + 32 <= q_hi;
-      // 32 queries: scores and dO V^T, rows = queries, column = key; then P and dS, as operands
-      f32x4 s[kC2][2], e[kC2][2];
-#pragma unroll
-      for (int c = 0; c < kC2; ++c)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) s[c][m] = e[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-      constexpr int kStepsK = DK / M::kDepth, kGroups = DK / 32, kStepsV = 32 / M::kDepth * kGroups;
-      typename M::Frag f[2][4];
-      auto read_k = [&](int i) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          f[i & 1][m] = kt.rows(sq, 2 * half + m, i);
-          f[i & 1][2 + m] = kt.rows(so, 2 * half + m, i);
-        }
-      };
-      auto read_v = [&](int i) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int d = i % kGroups * 2 + x, b = half * (32 / M::kDepth) + i / kGroups;
-          f[i & 1][x] = kt.cols(sq, d, b);
-          f[i & 1][2 + x] = kt.cols(so, d, b);
-        }
-      };
-      read_k(0);
-#pragma unroll
-      for (int kb = 0; kb < kStepsK; ++kb) {
-        end_step();
-        if (kb + 1 < kStepsK) read_k(kb + 1); else read_v(0);
-        end_step();
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int c = 0; c < kC2; ++c) {
-            s[c][m] = M::mma(f[kb & 1][m], kf[c][kb], s[c][m]);
-            e[c][m] = M::mma(f[kb & 1][2 + m], vf[c][kb], e[c][m]);
-          }
-      }
-      end_step();
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[st][0][32 * half + 16 * m + 4 * g]);
-#pragma unroll
-        for (int c = 0; c < kC2; ++c)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s[c][m][x] = fast_exp2(fmaf(s[c][m][x], sc, -ls[x]));
-      }
-      if (!whole)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int c = 0; c < kC2; ++c)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int qi = q0 + 32 * half + 16 * m + 4 * g + x, j = jw0 + 16 * c + r;
-              if (!(mask.sees(qi + shift, j) && qi < q_hi && (!kFarPart || qi >= q_lo))) s[c][m][x] = 0.f;
-            }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const f32x4 ds = *reinterpret_cast<const f32x4*>(&stats[st][1][32 * half + 16 * m + 4 * g]);
-#pragma unroll
-        for (int c = 0; c < kC2; ++c) e[c][m] = s[c][m] * (e[c][m] - ds);
-      }
-      typename M::Frag pf[kC2], ef[kC2];
-#pragma unroll
-      for (int i = 0; i < kStepsV; ++i) {
-        if (i % kGroups == 0)
-#pragma unroll
-          for (int c = 0; c < kC2; ++c) {
-            pf[c] = M::pack(&s[c][i / kGroups * M::kTiles]);
-            ef[c] = M::pack(&e[c][i / kGroups * M::kTiles]);
-          }
-        end_step();
-        if (i + 1 < kStepsV) read_v(i + 1);
-        end_step();
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int c = 0; c < kC2; ++c) {
-            const int d = i % kGroups * 2 + x;
-            dk[c][d] = M::mma(f[i & 1][x], ef[c], dk[c][d]);
-            dv[c][d] = M::mma(f[i & 1][2 + x], pf[c], dv[c][d]);
-          }
-      }
-      end_step();
-    }
-    if (i + 1 < count) put_stat(next, st ^ 1);
-  }
+  if (makes_dk)
+    key_sums<E, DK, kFarPart, kC2, kMakeDk>(a, k, mask, smem, stats, j0 + w0, sc, kf, vf, acc, copy, load_stat, put_stat);
+  else
+    key_sums<E, DK, kFarPart, kC2, kMakeDv>(a, k, mask, smem, stats, j0 + w0, sc, kf, vf, acc, copy, load_stat, put_stat);
   // sums of a stretch: (far slot, query head, tile of 16 sinks, dk and dv, 16, dim)
   auto far_at = [&](int64_t slot, int h, int64_t t) {
-    return a.far + ((slot * a.hq + h) * a.sink_tiles + t) * 32ll * a.dim;
+    return a.far + (((slot * a.hq + h) * a.sink_tiles + t) * 32 + (makes_dk ? 0 : 16) + r) * (int64_t)a.dim;
   };
   if (kFarPart) {
     if (r < nk) {
-      float* to = far_at(far_slot, hq0, tile) + r * a.dim;
+      float* to = far_at(far_slot, hq0, tile);
 #pragma unroll
       for (int d = 0; d < DK / 16; ++d) {
         const int v = KT::value(d, g, 0);
-        if (v < a.dim) {
-          *reinterpret_cast<f32x4*>(to + v) = dk[0][d];
-          *reinterpret_cast<f32x4*>(to + 16 * a.dim + v) = dv[0][d];
-        }
+        if (v < a.dim) *reinterpret_cast<f32x4*>(to + v) = acc[0][d];
       }
     }
     return;
   }
   const int64_t first = near(tile), stretches = first < qs.len ? (qs.len - first + kFar - 1) / kFar : 0;
   const int64_t far_base = tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
+  E* const out = static_cast<E*>(makes_dk ? a.dk : a.dv);
+  const float scale = makes_dk ? a.scale : 1.f;
 #pragma unroll
   for (int c = 0; c < kC2; ++c) {
     const int j = w0 + 16 * c + r;
@@ -294,27 +326,21 @@ __global__ __launch_bounds__(kFarPart ? 64 : 256, 1) void window_dkv_kernel(
     if (t16 < a.sink_tiles && j < nk)
       for (int64_t x = 0; x < stretches; ++x)
         for (int h = 0; h < a.rep; ++h) {
-          const float* from = far_at(far_base + x, kh * a.rep + h, t16) + r * a.dim;
+          const float* from = far_at(far_base + x, kh * a.rep + h, t16);
 #pragma unroll
           for (int d = 0; d < DK / 16; ++d) {
             const int v = KT::value(d, g, 0);
-            if (v < a.dim) {
-              dk[c][d] += *reinterpret_cast<const f32x4*>(from + v);
-              dv[c][d] += *reinterpret_cast<const f32x4*>(from + 16 * a.dim + v);
-            }
+            if (v < a.dim) acc[c][d] += *reinterpret_cast<const f32x4*>(from + v);
           }
         }
     if (j >= nk) continue;
     const int64_t at = ((ks.first + j0 + j) * a.hk + kh) * (int64_t)a.dim;
 #pragma unroll
-    for (int d = 0; d < DK / 16; ++d) dk[c][d] *= a.scale;
+    for (int d = 0; d < DK / 16; ++d) acc[c][d] *= scale;
 #pragma unroll
     for (int d = 0; d < DK / 16; d += M::kTiles) {
       const int v = KT::value(d, g, 0);
-      if (v < a.dim) {
-        store_operand(static_cast<E*>(a.dk) + at + v, &dk[c][d]);
-        store_operand(static_cast<E*>(a.dv) + at + v, &dv[c][d]);
-      }
+      if (v < a.dim) store_operand(out + at + v, &acc[c][d]);
     }
   }
 }
@@ -331,9 +357,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
   const int64_t wg = spread_index(id, blocks, a.rep);
   const int64_t slot = wg / a.hq;
   const int h = (int)(wg - slot * a.hq), kh = h / a.rep;
-  const int64_t seq = tile_seq(a.q_offsets, a.seqlen, a.nseq, slot, kQ);
+  const auto [seq, tile] = tile_of<true>(a.q_offsets, a.seqlen, a.nseq, slot, kQ);
   const Seq qs = seq_of(a.q_offsets, a.seqlen, seq), ks = seq_of(a.kv_offsets, a.kv_len, seq);
-  const int64_t tile = slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, kQ);
   if (tile < 0 || tile * kQ >= qs.len) return;
   const int q0 = (int)tile * kQ, nq = min(qs.len - q0, kQ);
   const int shift = ks.len - qs.len;
@@ -548,11 +573,11 @@ int launch_bwd(const WinArgs& a, int64_t tokens, hipStream_t s) {
   if ((st = launch_status()) != MAMBA_OK) return st;
   if (a.sink_tiles) {
     const uint32_t blocks = (uint32_t)(a.far_slots * a.hq * a.sink_tiles);
-    hipLaunchKernelGGL((window_dkv_kernel<E, DK, true>), wide_grid(blocks, 64), dim3(64), 0, s, a, blocks, tokens);
+    hipLaunchKernelGGL((window_dkv_kernel<E, DK, true>), wide_grid(blocks, 128), dim3(128), 0, s, a, blocks, tokens);
     if ((st = launch_status()) != MAMBA_OK) return st;
   }
-  const uint32_t keys = (uint32_t)(tile_slots(a.kv_len, a.nseq, packed, kRows<E>) * a.hk);
-  hipLaunchKernelGGL((window_dkv_kernel<E, DK, false>), wide_grid(keys, 256), dim3(256), 0, s, a, keys, tokens);
+  const uint32_t keys = (uint32_t)(tile_slots(a.kv_len, a.nseq, packed, kKeyRows<E>) * a.hk);
+  hipLaunchKernelGGL((window_dkv_kernel<E, DK, false>), wide_grid(keys, 128 * kPairs), dim3(128 * kPairs), 0, s, a, keys, tokens);
   return launch_status();
 }
 
