@@ -35,40 +35,48 @@ struct PassArgs {
   Args f;              // q, k, v, out in the pass's roles (backwards: k, q, dout, dv); offsets, s0 and last
   const float* gate;   // (tokens, hv)
   float* seg_decay;    // (segment slots, hv): what a segment leaves of the state before it
-  char* img;           // states before (backwards: after) every kUnit tokens, as tiles of dv x dk
-  int64_t img_item;    // bytes of one unit and value head
+  float* img;          // states before (backwards: after) every kUnit tokens: see image_at
+  int64_t img_item;    // floats of one unit and value head
+  const float* other;  // kDots: the images of the other direction
+  float* dots;         // kDots: (units, hv, column blocks, waves), parts of <state before, adjoint after> a unit
 };
 
-template <typename E>
-constexpr int kImgParts = Mma<E>::parts(2);
-// bytes of one part of a state's image
-template <typename E>
-inline int64_t image_part(const mamba_delta_dims* d) {
-  return (d->dv + 31) / 32 * 32 * (d->dk <= 64 ? 64 : 128) * (int64_t)sizeof(E);
+// floats of a state's image: fp32, so that the decays' gradients, fp32 numbers, are right to fp32
+inline int64_t image_size(const mamba_delta_dims* d) { return (d->dv + 31) / 32 * 32 * (d->dk <= 64 ? 64 : 128); }
+
+// Images lie as the accumulators do, so that a wave reads and writes whole KBs: (units, hv, dv padded to 32s / 16,
+// DK / 16, 64 lanes, 4), a unit's and head's img_item floats apart.
+template <int DK>
+__device__ __forceinline__ int64_t image_at(int col, int m, int lane) {
+  return (int64_t)(col / 16) * (16 * DK) + m * 256 + lane * 4;
 }
 
-// What a pass does: writes the output; keeps images of the states; goes backwards.
-enum : int { kOutput = 1, kImages = 2, kReverse = 4, kSegmentOnly = 8 };
+// What a pass does: writes the output; keeps images of the states; goes backwards; starts from zero and leaves only the
+// state; multiplies its images with the other direction's.
+enum : int { kOutput = 1, kImages = 2, kReverse = 4, kSegmentOnly = 8, kDots = 16 };
 
+// LDS: Y and X of a chunk once, the next chunk's wait in registers until these have been read; Z twice.  Without an
+// output two stages of Y and Z, copied straight to LDS.  Three workgroups share a CU (bf16).
 template <typename E, int DK, int kWhat>
 struct Smem {
   static constexpr bool kO = kWhat & kOutput;
-  static constexpr int kY = 0;
-  static constexpr int kX = KeyTile<E, DK>::kBytes;
+  static constexpr int kYBytes = KeyTile<E, DK>::kBytes;
   // the triangular matrix takes the place of X once that has been read
   static constexpr int kTri = Mma<E>::parts(2) * TriTile<E>::kBytes;
-  static constexpr int kXBytes = KeyTile<E, DK>::kBytes > kTri ? KeyTile<E, DK>::kBytes : kTri;
-  static constexpr int kZ = kX + (kO ? kXBytes : 0);
-  static constexpr int kStage = kZ + ValueTile<E, kCols>::kBytes;
+  static constexpr int kXBytes = kO ? (kYBytes > kTri ? kYBytes : kTri) : kYBytes;  // (no output: the second Y)
+  static constexpr int kY = 0, kX = kYBytes, kZ = kX + kXBytes, kZBytes = ValueTile<E, kCols>::kBytes;
   // gates of two chunks: G as two floats, fx, fy (64 each), last
   static constexpr int kGateFloats = 4 * kC + 4;
-  static constexpr int bytes(int stages) { return stages * kStage + 2 * kGateFloats * 4; }
+  static constexpr int kGate = kZ + 2 * kZBytes;
+  static constexpr int kBytes = kGate + 2 * kGateFloats * 4;
+  static_assert(sizeof(E) == 4 || 3 * kBytes <= 160 * 1024, "three workgroups per CU");
 };
 
-// RowCopy whose tile row x holds row 63 - x of memory where kRev
+// RowCopy whose tile row x holds row 63 - x of memory where kRev, and the same by way of registers
 template <typename E, typename Tile, bool kRev>
 struct TokenCopy {
   static constexpr int kI = kC * Tile::kRow / 1024 / kWaves4;
+  typedef uint32_t Word __attribute__((ext_vector_type(4)));
   uint32_t off[kI];
   __device__ __forceinline__ TokenCopy(int w, int lane, int64_t stride, int cols) {
 #pragma unroll
@@ -82,35 +90,76 @@ struct TokenCopy {
 #pragma unroll
     for (int i = 0; i < kI; ++i) copy_lds(buf, off[i], lds + (w + i * kWaves4) * 1024);
   }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buf, Word (&v)[kI]) const {
+#pragma unroll
+    for (int i = 0; i < kI; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)off[i], 0, 0);
+  }
+  __device__ __forceinline__ static void put(char* lds, int w, int lane, const Word (&v)[kI]) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i) *reinterpret_cast<Word*>(lds + (w + i * kWaves4) * 1024 + 16 * lane) = v[i];
+  }
 };
 
-// sum of v over lanes 0 .. lane
-__device__ __forceinline__ double prefix_sum(double v, int lane) {
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) {
-    const double t = __shfl_up(v, m);
-    if (lane >= m) v += t;
-  }
+// `n` rows of `cols` values, zeros past them
+template <typename E>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_resource(const E* p, int64_t n, int64_t stride, int cols) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(p), 0, (int)(((n - 1) * stride + cols) * (int64_t)sizeof(E)),
+                                           0x00020000);
+}
+
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+  const int2 x = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, int2{__builtin_amdgcn_update_dpp(0, x.x, kCtrl, kRows, 0xf, false),
+                                         __builtin_amdgcn_update_dpp(0, x.y, kCtrl, kRows, 0xf, false)});
+}
+// sum of v over lanes 0 .. lane: within rows of 16 lanes, then the rows before
+__device__ __forceinline__ double prefix_sum(double v) {
+  v += dpp_or_zero<0x111, 0xf>(v);  // lane - 1
+  v += dpp_or_zero<0x112, 0xf>(v);
+  v += dpp_or_zero<0x114, 0xf>(v);
+  v += dpp_or_zero<0x118, 0xf>(v);
+  v += dpp_or_zero<0x142, 0xa>(v);  // row 1 + lane 15, row 3 + lane 47
+  v += dpp_or_zero<0x143, 0xc>(v);  // rows 2 and 3 + lane 31
   return v;
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const int2 x = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, int2{__builtin_amdgcn_readlane(x.x, 63), __builtin_amdgcn_readlane(x.y, 63)});
+}
+
+// The output of a chunk in LDS: rows of kCols values, 16-byte words swizzled by the row.
+template <typename E>
+__device__ __forceinline__ int out_word(int row, int word) {
+  return word ^ (row & (kCols * (int)sizeof(E) / 16 - 1));
+}
+template <typename E>
+__device__ __forceinline__ void put_out(char* lds, int row, int col, f32x4 v) {
+  const int byte = col * (int)sizeof(E);
+  char* at = lds + row * (kCols * (int)sizeof(E)) + (out_word<E>(row, byte >> 4) << 4) + (byte & 15);
+  if constexpr (sizeof(E) == 2)
+    *reinterpret_cast<uint2*>(at) = uint2{pack_bf16(make_float2(v[0], v[1])), pack_bf16(make_float2(v[2], v[3]))};
+  else
+    *reinterpret_cast<f32x4*>(at) = v;
 }
 
 // Below -200 exp is 0 in fp32; the clamp keeps -inf (a reset) out of differences and lets NaN through.
 __device__ __forceinline__ float clamp_gate(float g) { return g < -200.f ? -200.f : g; }
 
-// Rounding, bf16 storage: z times its factor enters the state as kPE bf16 parts (3: to 24 bits; 2, where the state
-// is only kept as an image of two parts: to 16); the state and the triangular matrix enter the output as two parts
-// each, so that its own rounding is the only one that shows.
-template <typename E, int DK, int kWhat, int kStages>
-__global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void linear_pass_kernel(
+// Rounding, bf16 storage: z times its factor enters the state as three bf16 parts (24 bits); the state and the
+// triangular matrix enter the output as two parts each, so that its own rounding is the only one that shows.
+template <typename E, int DK, int kWhat>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kernel(
     PassArgs p, int32_t col_blocks, uint32_t blocks) {
   using M = Mma<E>;
   using Sm = Smem<E, DK, kWhat>;
   using KT = KeyTile<E, DK>;
   using TT = TriTile<E>;
   using VT = ValueTile<E, kCols>;
-  constexpr bool kO = kWhat & kOutput, kI = kWhat & kImages, kRev = kWhat & kReverse, kSum = kWhat & kSegmentOnly;
-  constexpr int kPS = M::parts(2), kPP = M::parts(2), kPE = M::parts(kI ? 2 : 3);
-  __shared__ __align__(1024) char smem[Sm::bytes(kStages)];
+  constexpr bool kO = kWhat & kOutput, kI = kWhat & kImages, kRev = kWhat & kReverse, kSum = kWhat & kSegmentOnly,
+                 kD = kWhat & kDots;
+  constexpr int kPS = M::parts(2), kPP = M::parts(2), kPE = M::parts(3);
+  __shared__ __align__(1024) char smem[Sm::kBytes];
   const Args& a = p.f;
   const uint32_t id = wide_index();
   if (id >= blocks) return;
@@ -131,39 +180,69 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
   if (kSum && (kRev ? first == 0 : end == nchunks)) return;  // no segment follows
   const int col0 = (int)(wg - sh * col_blocks) * kCols;  // this workgroup's first column
   const int col = col0 + 16 * w;                         // this wave's
-  const bool has_col = col + r < a.dv;
+  const bool has_col = col + r < a.dv, has_image = col < (a.dv + 31) / 32 * 32;
   const E* yp = static_cast<const E*>(a.k) + sp.first * a.k_stride + (int64_t)kh * a.dk;
   const E* xp = static_cast<const E*>(a.q) + sp.first * a.q_stride + (int64_t)kh * a.dk;
   const E* zp = static_cast<const E*>(a.v) + sp.first * a.v_stride + (int64_t)vh * a.dv + col0;
   const float* gp = p.gate + sp.first * a.hv + vh;
   const int64_t o_stride = (int64_t)a.hv * a.dv;
-  E* op = static_cast<E*>(a.out) + sp.first * o_stride + (int64_t)vh * a.dv + col;
-  const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
-  const int64_t g_at = (seg_slot * a.hv + vh) * (int64_t)a.dk * a.dv + col + r;
+  E* op = static_cast<E*>(a.out) + sp.first * o_stride + (int64_t)vh * a.dv + col0;
+  const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv;
+  const int64_t g_at = (seg_slot * a.hv + vh) * (int64_t)a.dk * a.dv;
   const float* from = kSum ? nullptr : a.seg_chunks ? a.seg_state + g_at : a.s0 ? a.s0 + s_at : nullptr;
 
+  // row 4 g + x of accumulator m and column col + r of a (dk, dv) matrix, past its end if there is none
+  auto state_at = [&](int m, int x) {
+    const int row = KT::value(m, g, x);
+    return has_col && row < a.dk ? (uint32_t)(row * a.dv + col + r) * 4u : kOutside;
+  };
+  auto state_resource = [&](const float* q) {  // (none: every load is past its end)
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(q), 0, q ? a.dk * a.dv * 4 : 0, 0x00020000);
+  };
   f32x4 S[DK / 16];
+  {
+    const auto buf = state_resource(from);
 #pragma unroll
-  for (int m = 0; m < DK / 16; ++m)
+    for (int m = 0; m < DK / 16; ++m)
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int row = KT::value(m, g, x);
-      S[m][x] = from && has_col && row < a.dk ? from[(int64_t)row * a.dv] : 0.f;
-    }
+      for (int x = 0; x < 4; ++x)
+        S[m][x] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, (int)state_at(m, x), 0, 0));
+  }
 
   const uint32_t lds0 = lds_address(smem);
   const int vcols = min(a.dv - col0, kCols);
   const TokenCopy<E, KT, kRev> cy(w, lane, a.k_stride, a.dk), cx(w, lane, a.q_stride, a.dk);
   const TokenCopy<E, VT, kRev> cz(w, lane, a.v_stride, vcols);
-  // copies chunk ch into stage st; tokens past the sequence are past the buffers and read as zero
+  // Y and X of a chunk to registers and from there to LDS (with an output), Z, or Y and Z, straight to stage st; tokens
+  // past the sequence are past the buffers and read as zero
+  typename decltype(cy)::Word next_y[kO ? decltype(cy)::kI : 1], next_x[kO ? decltype(cx)::kI : 1];
+  auto load = [&](int64_t ch) {
+    if constexpr (kO) {
+      const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
+      cy.load(rows_resource(yp + t * a.k_stride, n, a.k_stride, a.dk), next_y);
+      cx.load(rows_resource(xp + t * a.q_stride, n, a.q_stride, a.dk), next_x);
+    }
+  };
   auto copy = [&](int64_t ch, int st) {
     const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
-    const uint32_t to = lds0 + st * Sm::kStage;
-    cy(rows_buffer(yp + t * a.k_stride, n, a.k_stride, a.dk), to + Sm::kY, w);
-    if (kO) cx(rows_buffer(xp + t * a.q_stride, n, a.q_stride, a.dk), to + Sm::kX, w);
-    cz(rows_buffer(zp + t * a.v_stride, n, a.v_stride, vcols), to + Sm::kZ, w);
+    if constexpr (!kO) cy(rows_buffer(yp + t * a.k_stride, n, a.k_stride, a.dk), lds0 + st * Sm::kX, w);
+    cz(rows_buffer(zp + t * a.v_stride, n, a.v_stride, vcols), lds0 + Sm::kZ + st * Sm::kZBytes, w);
   };
-  float* const gates = reinterpret_cast<float*>(smem + kStages * Sm::kStage);
+  // a chunk's output from stage st: each wave the KBs that it fills with the next Z, which it has read when it copies
+  auto store_out = [&](int64_t ch, int st) {
+    constexpr int kWords = kCols * (int)sizeof(E) / 16;  // of a row
+    const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
+    const auto buf = rows_resource(op + t * o_stride, n, o_stride, vcols);
+#pragma unroll
+    for (int i = 0; i < decltype(cz)::kI; ++i) {
+      const int at = (w + i * kWaves4) * 64 + lane, x = at / kWords, c = out_word<E>(x, at % kWords) * (16 / (int)sizeof(E));
+      const auto v = *reinterpret_cast<const typename decltype(cz)::Word*>(smem + Sm::kZ + st * Sm::kZBytes + 16 * at);
+      __builtin_amdgcn_raw_buffer_store_b128(
+          v, buf, (int)(c < vcols ? (uint32_t)((kRev ? kC - 1 - x : x) * o_stride + c) * (uint32_t)sizeof(E) : kOutside), 0, 0);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (the copy is not the compiler's to order)
+  };
+  float* const gates = reinterpret_cast<float*>(smem + Sm::kGate);
   // Wave 0: prefix sums of a chunk's log decays in fp64, kept as two floats, so that a difference of two of them is as
   // exact as its own size whatever came before in the chunk; lane = token.
   auto load_gate = [&](int64_t ch) {
@@ -173,7 +252,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
   double all = 0.0;  // of the segment
   auto put_gates = [&](float v, int slot) {
     float* to = gates + slot * Sm::kGateFloats;
-    const double G = prefix_sum((double)v, lane), total = __shfl(G, 63);
+    const double G = prefix_sum((double)v), total = last_lane(G);
     const float hi = (float)G, lo = (float)(G - (double)hi);
     const float eg = a.scale * exp_f32(hi), c = exp_f32((float)(total - G));
     const int x = kRev ? kC - 1 - lane : lane;
@@ -190,38 +269,63 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
   const VT vt(lane, 16 * w);
   const int64_t count = end - first;
   auto chunk_at = [&](int64_t it) { return kRev ? end - 1 - it : first + it; };
+  constexpr int kPer = kUnit<E> / kC;  // chunks of a unit
+  auto unit_item = [&](int64_t ch) {
+    return (slot_base(a, seq, sp.first, kUnit<E>) + ch / kPer) * a.hv + vh;
+  };
+  f32x4 other[kD ? DK / 16 : 1];  // of the next unit
+  auto load_other = [&](int64_t ch) {
+    if constexpr (kD) {
+      const float* img = p.other + unit_item(ch) * p.img_item;
+#pragma unroll
+      for (int m = 0; m < DK / 16; ++m)
+        other[m] = has_image ? *reinterpret_cast<const f32x4*>(img + image_at<DK>(col, m, lane)) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  };
   if (count > 0) {
+    load(chunk_at(0));
     copy(chunk_at(0), 0);
     if (w == 0) put_gates(load_gate(chunk_at(0)), 0);
+    load_other(chunk_at(0));
+    if constexpr (kO) {
+      cy.put(smem + Sm::kY, w, lane, next_y);
+      cx.put(smem + Sm::kX, w, lane, next_x);
+    }
   }
   for (int64_t it = 0; it < count; ++it) {
     const int64_t ch = chunk_at(it);
-    const int st = kStages == 2 ? (int)(it & 1) : 0;
+    const int st = (int)(it & 1);
     float next_gate = 0.f;
     copies_done();
-    const lds_ptr sm = (lds_ptr)(smem + st * Sm::kStage);
-    const float* gt = gates + (it & 1) * Sm::kGateFloats;
-    if (w == 0 && it + 1 < count) next_gate = load_gate(chunk_at(it + 1));
-    if (kStages == 2 && it + 1 < count) copy(chunk_at(it + 1), st ^ 1);
-    const int n = (int)min((int64_t)kC, sp.len - ch * kC);
+    const lds_ptr sm = (lds_ptr)smem;
+    const lds_ptr sy = sm + (kO ? 0 : st * Sm::kX), sz = sm + Sm::kZ + st * Sm::kZBytes;
+    const float* gt = gates + st * Sm::kGateFloats;
+    if (kO && it) store_out(chunk_at(it - 1), st ^ 1);
+    if (it + 1 < count) {
+      if (w == 0) next_gate = load_gate(chunk_at(it + 1));
+      load(chunk_at(it + 1));
+      copy(chunk_at(it + 1), st ^ 1);
+    }
 
     if constexpr (kI) {
-      // the state before the unit: 16 bytes of one column per operand
-      constexpr int kPer = kUnit<E> / kC;
+      // the state before the unit
       if (kRev ? ch % kPer == kPer - 1 || ch == nchunks - 1 : ch % kPer == 0) {
-        const int64_t part = (a.dv + 31) / 32 * 32 * (int64_t)KT::kRow;
-        char* img = p.img + ((slot_base(a, seq, sp.first, kUnit<E>) + ch / kPer) * a.hv + vh) * p.img_item +
-                    (int64_t)(col + r) * KT::kRow;
-        if (col + r < (a.dv + 31) / 32 * 32) {
+        const int64_t item = unit_item(ch);
+        float* img = p.img + item * p.img_item;
+        if (has_image)
 #pragma unroll
-          for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-            const auto s = M::template split<kImgParts<E>>(&S[kb * M::kTiles]);
+          for (int m = 0; m < DK / 16; ++m) *reinterpret_cast<f32x4*>(img + image_at<DK>(col, m, lane)) = S[m];
+        if constexpr (kD) {
+          f32x4 d = S[0] * other[0];
 #pragma unroll
-            for (int x = 0; x < kImgParts<E>; ++x)
-              *reinterpret_cast<typename M::Frag*>(img + x * part + (((4 * kb + g) ^ KT::key(col + r)) << 4)) = s.p[x];
-          }
+          for (int m = 1; m < DK / 16; ++m) d += S[m] * other[m];
+          float sum = (d[0] + d[1]) + (d[2] + d[3]);
+#pragma unroll
+          for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
+          if (lane == 0) p.dots[(item * col_blocks + (wg - sh * col_blocks)) * kWaves4 + w] = sum;
         }
       }
+      if (kD && it + 1 < count && chunk_at(it + 1) % kPer == 0) load_other(chunk_at(it + 1));
     }
     f32x4 o[4], s[4];
     if constexpr (kO) {
@@ -233,8 +337,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
         const auto xi = kt.rows(sm + Sm::kX, w, kb);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          if (m <= w) s[m] = M::mma(kt.rows(sm + Sm::kY, m, kb), xi, s[m]);
+          if (m <= w) s[m] = M::mma(kt.rows(sy, m, kb), xi, s[m]);
       }
+      __builtin_amdgcn_sched_barrier(0);
       const int i = 16 * w + r;
       const float hi = gt[i], lo = gt[kC + i];
 #pragma unroll
@@ -242,10 +347,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
         if (m <= w) {
           const f32x4 yh = *reinterpret_cast<const f32x4*>(gt + 16 * m + 4 * g),
                       yl = *reinterpret_cast<const f32x4*>(gt + kC + 16 * m + 4 * g);
+          const f32x4 e = (hi - yh) + (lo - yl);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            s[m][x] = 16 * m + 4 * g + x <= i ? s[m][x] * (a.scale * exp_f32((hi - yh[x]) + (lo - yl[x]))) : 0.f;
+          for (int x = 0; x < 4; ++x) s[m][x] *= a.scale * exp_f32(e[x]);
+          if (m == w)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (4 * g + x > r) s[m][x] = 0.f;
         }
+      __builtin_amdgcn_sched_barrier(0);
       // (X S)^T, columns x tokens
 #pragma unroll
       for (int kb = 0; kb < DK / M::kDepth; ++kb) {
@@ -260,6 +370,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
 #pragma unroll
       for (int m = 0; m < 4; ++m) o[m] *= gt[2 * kC + 16 * m + r];
     }
+    __builtin_amdgcn_sched_barrier(0);
     // S' = last S + Y^T diag(fy) Z
     const float last = gt[4 * kC];
 #pragma unroll
@@ -269,20 +380,21 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
       f32x4 e[M::kTiles];
 #pragma unroll
       for (int x = 0; x < M::kTiles; ++x)
-        e[x] = vt.tile(sm + Sm::kZ, kb * M::kTiles + x) *
+        e[x] = vt.tile(sz, kb * M::kTiles + x) *
                *reinterpret_cast<const f32x4*>(gt + 3 * kC + 16 * (kb * M::kTiles + x) + 4 * g);
       const auto es = M::template split<kPE>(e);
 #pragma unroll
       for (int m = 0; m < DK / 16; ++m) {
-        const auto yc = kt.cols(sm + Sm::kY, m, kb);
+        const auto yc = kt.cols(sy, m, kb);
 #pragma unroll
         for (int x = 0; x < kPE; ++x) S[m] = M::mma(yc, es.p[x], S[m]);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
     if (w == 0 && it + 1 < count) put_gates(next_gate, (int)((it + 1) & 1));
     if constexpr (kO) {
-      __syncthreads();  // X has been read
-      char* const psm = smem + st * Sm::kStage + Sm::kX;
+      __syncthreads();  // X and Y have been read
+      char* const psm = smem + Sm::kX;
 #pragma unroll
       for (int kb = 0; kb < TT::kBlocks; ++kb)
         if (16 * w >= kb * M::kDepth) {
@@ -291,42 +403,40 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && kStages == 1 ? 3 : 1) void l
           for (int x = 0; x < kPP; ++x)
             *reinterpret_cast<typename M::Frag*>(psm + x * TT::kBytes + TT::word_at(kb, 16 * w + r, g)) = f.p[x];
         }
+      if (it + 1 < count) cy.put(smem + Sm::kY, w, lane, next_y);
       __syncthreads();  // the triangular matrix is whole
       const lds_ptr pm = (lds_ptr)psm;
 #pragma unroll
       for (int kb = 0; kb < TT::kBlocks; ++kb) {
-        const auto z = vt.operand(sm + Sm::kZ, kb);
+        const auto z = vt.operand(sz, kb);
 #pragma unroll
         for (int x = 0; x < kPP; ++x)
 #pragma unroll
           for (int m = kb * M::kTiles; m < 4; ++m)
             o[m] = M::mma(z, tt.rows(pm + x * TT::kBytes, m, kb), o[m]);
       }
-      const auto buf = __builtin_amdgcn_make_buffer_rsrc(
-          op + ch * kC * o_stride, 0, (int)(((n - 1) * o_stride + max(a.dv - col, 0)) * (int64_t)sizeof(E)),
-          0x00020000);
+      __syncthreads();  // the triangular matrix and Z have been read
+      // the output in Z's place, from where whole rows are stored behind the next barrier
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int t = kRev ? kC - 1 - (16 * m + r) : 16 * m + r;
-        store_four<E>(buf, col + 4 * g < a.dv ? (uint32_t)(t * o_stride + 4 * g) * (uint32_t)sizeof(E) : kOutside,
-                      o[m]);
-      }
+      for (int m = 0; m < 4; ++m) put_out<E>(smem + Sm::kZ + st * Sm::kZBytes, 16 * m + r, 16 * w + 4 * g, o[m]);
+      if (it + 1 < count) cx.put(smem + Sm::kX, w, lane, next_x);
     }
-    if (kStages == 1 && it + 1 < count) {
-      __syncthreads();  // every wave has read the stage
-      copy(chunk_at(it + 1), 0);
-    }
+  }
+  if (kO && count > 0) {
+    __syncthreads();
+    store_out(chunk_at(count - 1), (int)((count - 1) & 1));
   }
   if (kSum && col0 == 0 && w == 0 && lane == 0) p.seg_decay[seg_slot * a.hv + vh] = exp_f32((float)all);
   float* to = kSum ? a.seg_state + g_at
                    : a.last && (kRev ? first == 0 : end == nchunks) ? a.last + s_at : nullptr;
-  if (to && has_col) {
+  if (to) {
+    const auto buf = state_resource(to);
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int row = KT::value(m, g, x);
-        if (row < a.dk) to[(int64_t)row * a.dv] = S[m][x];
+        const float v = S[m][x];
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), buf, (int)state_at(m, x), 0, 0);
       }
   }
 }
@@ -335,7 +445,7 @@ template <typename E, int DK, int kWhat>
 int launch_pass_t(const PassArgs& p, hipStream_t s) {
   const int cols = (p.f.dv + kCols - 1) / kCols;
   const uint32_t blocks = (uint32_t)(p.f.seg_slots * p.f.hv * cols);
-  hipLaunchKernelGGL((linear_pass_kernel<E, DK, kWhat, 1>), wide_grid(blocks, 256), dim3(256), 0, s, p, cols, blocks);
+  hipLaunchKernelGGL((linear_pass_kernel<E, DK, kWhat>), wide_grid(blocks, 256), dim3(256), 0, s, p, cols, blocks);
   return launch_status();
 }
 template <typename E, int kWhat>

@@ -10,9 +10,9 @@
 // Every term of dg_t is of pairs of tokens on both sides of t, so that nothing cancels: the gradient of a strong
 // decay is as small as its pairs make it, and that of a reset is zero.
 //
-// Launches: linear_pass_kernel (mamba_linear.h) forwards leaves the states, backwards dV and the adjoints;
-// linear_grad_kernel the rest, a workgroup per unit and key head, value heads added in accumulators in a fixed
-// order.  Where units and key heads alone would leave CUs idle the value heads of a key head are split among
+// Launches: linear_pass_kernel (mamba_linear.h) backwards leaves dV and the adjoints, forwards the states and <S, dS'>;
+// linear_grad_kernel first dK and the part of dg that comes from keys, then dQ and dg, a workgroup per unit and key
+// head, value heads added in accumulators in a fixed order.  Where units and key heads alone would leave CUs idle the value heads of a key head are split among
 // workgroups, whose fp32 sums linear_fold_kernel adds in order.  No atomics.
 #include "mamba_linear.h"
 
@@ -24,9 +24,12 @@ struct GradArgs {
   Args f;            // q, k, v, offsets and sizes
   const float* gate;
   const void* dout;  // (tokens, hv, dv)
-  const char* s_img;
-  const char* ds_img;
+  const float* s_img;
+  const float* ds_img;
   int64_t img_item;
+  const float* dots; // (units, hv, dot_parts): parts of <S, dS'>
+  int32_t dot_parts;
+  float* dgz;        // (tokens, hv): what keys and <S, dS'> give dg
   void* dq;          // (tokens, hk, dk)
   void* dk;
   float* dg;         // (tokens, hv)
@@ -35,48 +38,103 @@ struct GradArgs {
   int32_t groups;    // workgroups that share a key head's value heads
 };
 
-// LDS of a workgroup: Q and K of the unit throughout; two stages of 32 columns of V and dO with the state's rows of
-// them; one of the adjoint's.
+// Parts that stand for a state's value: with bf16 storage three, all of its 24 bits, for the sake of dg, which is
+// fp32 and made of the same products as dQ and dK.
+template <typename E>
+constexpr int kImgParts = Mma<E>::parts(3);
+
+// One of the two sides of a unit: dQ, of queries, dO and S, or dK, of keys, V and dS'.  LDS of a workgroup: the other
+// side's keys or queries of the unit throughout; two stages of 32 columns of the other side's V or dO; 32 of the
+// state's rows.  Two workgroups fit a CU, so that one's products hide the other's reads.
 template <typename E, int DK>
 struct GradSmem {
   static constexpr int kT = kUnit<E>;
-  static constexpr int kNW = kT / 16;  // a wave has 16 tokens
+  static constexpr int kNT = kT / 16;   // tiles of 16 tokens
+  static constexpr int kNW = kT / 32;   // a wave has 32 tokens
   using KT = KeyTile<E, DK>;
   using BT = KeyTile<E, 32>;
-  static constexpr int kQ = 0;
-  static constexpr int kK = kT * KT::kRow;
-  static constexpr int kA = 2 * kT * KT::kRow;
-  static constexpr int kV = 0, kO = kT * BT::kRow, kS = 2 * kT * BT::kRow;  // inside a stage
-  static constexpr int kState = 32 * KT::kRow;                             // a part of 32 rows
-  static constexpr int kABytes = kS + kImgParts<E> * kState;
-  static constexpr int kDS = kA + 2 * kABytes;
-  static constexpr int kGate = kDS + kImgParts<E> * kState;  // G as two floats, eg, c (kT each), exp(G_end)
-  static constexpr int kRed = kGate + (4 * kT + 4) * 4;      // pairs' sums of a wave's tokens: (kNW, kT)
-  static constexpr int kTok = kRed + kNW * kT * 4;           // R, Z (kT each)
-  static constexpr int kDot = kTok + 2 * kT * 4;             // a wave's part of <S, dS'>
-  static constexpr int kBytes = kDot + 2 * kNW * 4;
-  static_assert(kBytes <= 160 * 1024, "LDS");
+  static constexpr int kX = 0;
+  static constexpr int kA = kT * KT::kRow;
+  static constexpr int kABytes = kT * BT::kRow;
+  static constexpr int kState = 32 * KT::kRow;               // a part of 32 rows
+  static constexpr int kS = kA + 2 * kABytes;
+  static constexpr int kGate = kS + kImgParts<E> * kState;   // G as two floats, the tokens' factors (kT each), exp(G_end)
+  static constexpr int kRed = kGate + (3 * kT + 4) * 4;      // pairs' sums of a tile's tokens: (kNT, kT)
+  static constexpr int kTok = kRed + kNT * kT * 4;           // R or Z (kT)
+  static constexpr int kBytes = kTok + kT * 4;
+  static_assert(2 * kBytes <= 160 * 1024, "two workgroups per CU");
 };
 
+// A thread's share of 32 columns of a state's image: words of 16 bytes of an operand, on their way in registers.
+template <typename E, int DK, int kThreads>
+struct StateRows {
+  static constexpr int kV = 16 / sizeof(E), kF = kV / 4, kItems = 32 * DK / kV;
+  static constexpr int kN = (kItems + kThreads - 1) / kThreads;
+  f32x4 v[kN][kF];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = threadIdx.x + i * kThreads;  // word at / 64 of the image's kF KBs each
+#pragma unroll
+      for (int x = 0; x < kF; ++x)
+        v[i][x] = at < kItems ? *reinterpret_cast<const f32x4*>(p + (at / 64 * kF + x) * 256 + at % 64 * 4)
+                              : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+  // as parts to LDS, laid out like a tile of keys
+  __device__ __forceinline__ void put(char* lds) const {
+    using KT = KeyTile<E, DK>;
+    constexpr int kPer = DK / 4 / kV;  // words of 64 lanes for 16 columns
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = threadIdx.x + i * kThreads, lane = at % 64;
+      const int row = at / 64 / kPer * 16 + (lane & 15), word = at / 64 % kPer * 4 + (lane >> 4);
+      if (kItems % kThreads && at >= kItems) continue;
+      const auto f = Mma<E>::template split<kImgParts<E>>(v[i]);
+#pragma unroll
+      for (int x = 0; x < kImgParts<E>; ++x)
+        *reinterpret_cast<typename Mma<E>::Frag*>(lds + x * 32 * KT::kRow + row * KT::kRow + ((word ^ KT::key(row)) << 4)) =
+            f.p[x];
+    }
+  }
+};
+
+// The same value, but as a new one for the compiler: addresses made from it are made again for each head, not held
+// in registers through the loop over heads.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// 16 bytes of a buffer, zeros past its end
+template <typename F>
+__device__ __forceinline__ F load_16(__amdgpu_buffer_rsrc_t buf, uint32_t offset) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(F, (u32x4)__builtin_amdgcn_raw_buffer_load_b128(buf, (int)offset, 0, 0));
+}
 template <typename V>
 __device__ __forceinline__ V across_groups(V v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
 
-template <typename E, int DK>
-__global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64)) void linear_grad_kernel(GradArgs b, uint32_t blocks) {
+// Per value head first the pairs of tokens (tiles of dO V^T, columns = a wave's own 32 tokens, which both sides make in
+// their own orientation: no wave needs another's), then the state's terms.
+template <typename E, int DK, bool kKeys>
+__global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_kernel(GradArgs b, uint32_t blocks) {
   using M = Mma<E>;
   using Sm = GradSmem<E, DK>;
   using KT = typename Sm::KT;
   using BT = typename Sm::BT;
-  constexpr int kT = Sm::kT, kNW = Sm::kNW, kTiles = DK / 16, kP = kImgParts<E>;
+  constexpr int kT = Sm::kT, kNT = Sm::kNT, kNW = Sm::kNW, kTiles = DK / 16, kP = kImgParts<E>, kV = 16 / sizeof(E);
+  constexpr int kDB = 32 / M::kDepth;  // depths of a block of columns
   __shared__ __align__(1024) char smem[Sm::kBytes];
   const Args& a = b.f;
   const uint32_t wg = wide_index();
   if (wg >= blocks) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int own0 = 2 * w;  // this wave's tiles: own0, own0 + 1
   const uint32_t grp = wg % (uint32_t)b.groups, rest = wg / (uint32_t)b.groups;
   const int64_t slot = rest / (uint32_t)a.hk;
   const int kh = (int)(rest - slot * a.hk);
@@ -92,52 +150,65 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64)) void linear_grad_kerne
   const uint32_t lds0 = lds_address(smem);
   const lds_ptr sm = (lds_ptr)smem;
   const int64_t o_stride = (int64_t)a.hv * a.dv;
-  {
-    const RowCopy<E, KT, kT, kNW> cq(w, lane, a.q_stride, a.dk), ck(w, lane, a.k_stride, a.dk);
-    cq(rows_buffer(static_cast<const E*>(a.q) + t0 * a.q_stride + (int64_t)kh * a.dk, n, a.q_stride, a.dk),
-       lds0 + Sm::kQ, w);
-    ck(rows_buffer(static_cast<const E*>(a.k) + t0 * a.k_stride + (int64_t)kh * a.dk, n, a.k_stride, a.dk),
-       lds0 + Sm::kK, w);
-  }
+  // own: q and dO, or k and v; other: k and v, or q and dO
+  const E* const q = static_cast<const E*>(a.q) + t0 * a.q_stride + (int64_t)kh * a.dk;
+  const E* const k = static_cast<const E*>(a.k) + t0 * a.k_stride + (int64_t)kh * a.dk;
+  const E* const v = static_cast<const E*>(a.v) + t0 * a.v_stride;
+  const E* const o = static_cast<const E*>(b.dout) + t0 * o_stride;
+  const E *const own_x = kKeys ? k : q, *const other_x = kKeys ? q : k, *const own_y = kKeys ? v : o,
+          *const other_y = kKeys ? o : v;
+  const int64_t own_xs = kKeys ? a.k_stride : a.q_stride, other_xs = kKeys ? a.q_stride : a.k_stride;
+  const int64_t own_ys = kKeys ? a.v_stride : o_stride, other_ys = kKeys ? o_stride : a.v_stride;
+  const RowCopy<E, KT, kT, kNW> cx(w, lane, other_xs, a.dk);
+  cx(rows_buffer(other_x, n, other_xs, a.dk), lds0 + Sm::kX, w);
   const int dblocks = (a.dv + 31) / 32;
-  const int64_t part = (int64_t)dblocks * Sm::kState;
-  // columns [32 db, ...) of V and dO and the state's rows of them, of value head vh
-  auto copy_a = [&](int vh, int db, int st) {
+  // columns [32 db, ...) of the other side's V or dO of value head vh into a stage
+  auto copy = [&](int vh, int db, int st) {
     const int cols = min(a.dv - 32 * db, 32);
-    const uint32_t to = lds0 + Sm::kA + st * Sm::kABytes;
-    const RowCopy<E, BT, kT, kNW> cv(w, lane, a.v_stride, cols), co(w, lane, o_stride, cols);
-    cv(rows_buffer(static_cast<const E*>(a.v) + t0 * a.v_stride + (int64_t)vh * a.dv + 32 * db, n, a.v_stride, cols),
-       to + Sm::kV, w);
-    co(rows_buffer(static_cast<const E*>(b.dout) + t0 * o_stride + (int64_t)vh * a.dv + 32 * db, n, o_stride, cols),
-       to + Sm::kO, w);
-    const char* img = b.s_img + (slot * a.hv + vh) * b.img_item + (int64_t)db * Sm::kState;
-#pragma unroll
-    for (int x = 0; x < kP; ++x) copy_linear<Sm::kState, kNW>(img + x * part, to + Sm::kS + x * Sm::kState, w, lane);
+    const RowCopy<E, BT, kT, kNW> cy(w, lane, other_ys, cols);
+    cy(rows_buffer(other_y + (int64_t)vh * a.dv + 32 * db, n, other_ys, cols), lds0 + Sm::kA + st * Sm::kABytes, w);
   };
-  auto copy_ds = [&](int vh, int db) {
-    const char* img = b.ds_img + (slot * a.hv + vh) * b.img_item + (int64_t)db * Sm::kState;
+  // this wave's own tokens of dO or V as operands
+  typename M::Frag own[2][kDB];
+  auto fetch_own = [&](int vh, int db) {
+    const auto buf = rows_resource(own_y + (int64_t)vh * a.dv, n, own_ys, a.dv);
 #pragma unroll
-    for (int x = 0; x < kP; ++x) copy_linear<Sm::kState, kNW>(img + x * part, lds0 + Sm::kDS + x * Sm::kState, w, lane);
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int kb = 0; kb < kDB; ++kb) {
+        const int col = 32 * db + kb * M::kDepth + g * kV;
+        const uint32_t at = (uint32_t)((16 * (own0 + c) + r) * own_ys + col) * (uint32_t)sizeof(E);
+        own[c][kb] = load_16<typename M::Frag>(buf, col < a.dv ? at : kOutside);
+      }
   };
-  const KT kt(lane);
-  const BT bt(lane);
+  // and tile c of them of q or k
+  auto load_x = [&](int c, typename M::Frag(&f)[DK / M::kDepth]) {
+    const auto buf = rows_resource(own_x, n, own_xs, a.dk);
+#pragma unroll
+    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+      const int col = kb * M::kDepth + g * kV;
+      const uint32_t at = (uint32_t)((16 * (own0 + c) + r) * own_xs + col) * (uint32_t)sizeof(E);
+      f[kb] = load_16<typename M::Frag>(buf, col < a.dk ? at : kOutside);
+    }
+  };
+  StateRows<E, DK, kNW * 64> rows;
+  auto fetch_state = [&](int vh, int db) {
+    rows.load((kKeys ? b.ds_img : b.s_img) + (slot * a.hv + vh) * b.img_item + (int64_t)db * 32 * DK);
+  };
   float* const gate = reinterpret_cast<float*>(smem + Sm::kGate);
   float* const red = reinterpret_cast<float*>(smem + Sm::kRed);
   float* const tok = reinterpret_cast<float*>(smem + Sm::kTok);
-  float* const dots = reinterpret_cast<float*>(smem + Sm::kDot);
-  const int i = 16 * w + r;  // this lane's token
 
-  // Slot t <= w: rows j of tile t, column i; t > w, and slot kNW for tile w: rows i' of tile t, column j' = i.  With both
-  // orientations no wave needs another's tiles, and every wave has kNW + 1.
-  f32x4 B[kNW + 1], dQ[kTiles], dK[kTiles];
+  f32x4 X[2][kTiles];  // dQ or dK, transposed: rows = values, column = token
 #pragma unroll
-  for (int t = 0; t <= kNW; ++t) B[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m) dQ[m] = dK[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  copy_a(kh * a.rep + h0, 0, 0);
+    for (int m = 0; m < kTiles; ++m) X[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  copy(kh * a.rep + h0, 0, 0);
   int st = 0;
   for (int h = h0; h < h1; ++h) {
     const int vh = kh * a.rep + h;
+    fetch_own(vh, 0);
     // gates: wave 0, prefix sums in fp64, kept as two floats
     if (w == 0) {
       double before = 0.0, G[kT / 64];
@@ -145,8 +216,8 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64)) void linear_grad_kerne
       for (int x = 0; x < kT / 64; ++x) {
         const int t = 64 * x + lane;
         const float v = t < n ? clamp_gate(b.gate[(t0 + t) * a.hv + vh]) : 0.f;
-        G[x] = before + prefix_sum((double)v, lane);
-        before = __shfl(G[x], 63);
+        G[x] = before + prefix_sum((double)v);
+        before = last_lane(G[x]);
       }
 #pragma unroll
       for (int x = 0; x < kT / 64; ++x) {
@@ -154,230 +225,239 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64)) void linear_grad_kerne
         const float hi = (float)G[x];
         gate[t] = hi;
         gate[kT + t] = (float)(G[x] - (double)hi);
-        gate[2 * kT + t] = a.scale * exp_f32(hi);
-        gate[3 * kT + t] = exp_f32((float)(before - G[x]));
+        gate[2 * kT + t] = kKeys ? exp_f32((float)(before - G[x])) : a.scale * exp_f32(hi);
       }
-      if (lane == 0) gate[4 * kT] = exp_f32((float)before);
+      if (lane == 0) gate[3 * kT] = exp_f32((float)before);
     }
-    f32x4 bb[kNW + 1], sq[kTiles], sk[kTiles];
+    {
+      // dO V^T: rows of tile t of the other side, columns = own tokens (tiles past the diagonal too: they cost less
+      // than branches)
+      f32x4 B[2][kNT];
 #pragma unroll
-    for (int t = 0; t <= kNW; ++t) bb[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) sq[m] = sk[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float dot = 0.f;
-    for (int db = 0; db < dblocks; ++db) {
-      copies_done();
-      const lds_ptr sa = sm + Sm::kA + st * Sm::kABytes;
-      copy_ds(vh, db);
-      if (db + 1 < dblocks) copy_a(vh, db + 1, st ^ 1);
-      else if (h + 1 < h1) copy_a(vh + 1, 0, st ^ 1);
+        for (int t = 0; t < kNT; ++t) B[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const BT bt(opaque(lane));
+      for (int db = 0; db < dblocks; ++db) {
+        copies_done();
+        const lds_ptr sa = sm + Sm::kA + st * Sm::kABytes;
+        typename M::Frag x[2][kDB];
 #pragma unroll
-      for (int kb = 0; kb < 32 / M::kDepth; ++kb) {
-        const auto vw = bt.rows(sa + Sm::kV, w, kb), ow = bt.rows(sa + Sm::kO, w, kb);
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int t = 0; t < kNW; ++t) {
-          if (t <= w) bb[t] = M::mma(bt.rows(sa + Sm::kV, t, kb), ow, bb[t]);
-          else bb[t] = M::mma(bt.rows(sa + Sm::kO, t, kb), vw, bb[t]);
+          for (int kb = 0; kb < kDB; ++kb) x[c][kb] = own[c][kb];
+        fetch_own(vh, db + 1 < dblocks ? db + 1 : 0);  // (the last turn: for the state's terms)
+        if (db + 1 < dblocks) copy(vh, db + 1, st ^ 1);
+        else if (h + 1 < h1) copy(vh + 1, 0, st ^ 1);
+#pragma unroll
+        for (int kb = 0; kb < kDB; ++kb)
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) {
+            const auto f = bt.rows(sa, t, kb);
+            B[0][t] = M::mma(f, x[0][kb], B[0][t]);
+            B[1][t] = M::mma(f, x[1][kb], B[1][t]);
+          }
+        st ^= 1;
+      }
+      const KT kt(opaque(lane));
+      // times scale D; on the queries' side times q . k for dg.  (The barriers keep the compiler from drawing the
+      // tiles into each other: it spilled 168 registers.)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int tile = own0 + c, i = 16 * tile + r;
+        const float hi = gate[i], lo = gate[kT + i];
+        f32x4 qk[kKeys ? 1 : kNT];
+        if constexpr (!kKeys) {
+          typename M::Frag qi[DK / M::kDepth];
+          load_x(c, qi);
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) qk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kb = 0; kb < DK / M::kDepth; ++kb)
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) qk[t] = M::mma(kt.rows(sm + Sm::kX, t, kb), qi[kb], qk[t]);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        bb[kNW] = M::mma(ow, vw, bb[kNW]);
+        float base = 0.f;  // sum over the rows of the tiles before
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
+        for (int t = 0; t < kNT; ++t) {
+          if (kKeys ? t < tile : t > tile) {
+            B[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            continue;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          const f32x4 rh = *reinterpret_cast<const f32x4*>(gate + 16 * t + 4 * g),
+                      rl = *reinterpret_cast<const f32x4*>(gate + kT + 16 * t + 4 * g);
+          const f32x4 e = (hi - rh) + (lo - rl);
 #pragma unroll
-          for (int x = 0; x < kP; ++x)
-            sq[m] = M::mma(kt.template cols<true>(sa + Sm::kS + x * Sm::kState, m, kb), ow, sq[m]);
-      }
-      copies_done();
+          for (int x = 0; x < 4; ++x) B[c][t][x] *= a.scale * exp_f32(kKeys ? -e[x] : e[x]);
+          if (t == tile)
 #pragma unroll
-      for (int kb = 0; kb < 32 / M::kDepth; ++kb) {
-        const auto vw = bt.rows(sa + Sm::kV, w, kb);
+            for (int x = 0; x < 4; ++x)
+              if (kKeys ? 4 * g + x < r : 4 * g + x > r) B[c][t][x] = 0.f;
+          if constexpr (!kKeys) {
+            // then for every row t of the tile the sum over the rows before it, over columns i >= t
+            const f32x4 s = qk[t] * B[c][t];
+            const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+            const float up1 = __shfl_up(sum, 16), up2 = __shfl_up(sum, 32), up3 = __shfl_up(sum, 48);
+            float before = base + (g > 0 ? up1 : 0.f) + (g > 1 ? up2 : 0.f) + (g > 2 ? up3 : 0.f);
+            base += across_groups(sum);
+            f32x4 v;
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-          for (int x = 0; x < kP; ++x)
-            sk[m] = M::mma(kt.template cols<true>(sm + Sm::kDS + x * Sm::kState, m, kb), vw, sk[m]);
-      }
-      // <S, dS'> of these columns (the images are alike, so their order does not matter)
-      for (int x = threadIdx.x; x < Sm::kState / 16; x += kNW * 64) {
-        float s[16 / sizeof(E)], d[16 / sizeof(E)];
-#pragma unroll
-        for (int y = 0; y < kP; ++y) {
-          const auto fs = lds_read<typename M::Frag>(sa + Sm::kS + y * Sm::kState + 16 * x);
-          const auto fd = lds_read<typename M::Frag>(sm + Sm::kDS + y * Sm::kState + 16 * x);
-#pragma unroll
-          for (int z = 0; z < (int)(16 / sizeof(E)); ++z) {
-            s[z] = (y ? s[z] : 0.f) + (float)fs[z];
-            d[z] = (y ? d[z] : 0.f) + (float)fd[z];
+            for (int x = 0; x < 4; ++x) {
+              v[x] = t < tile || 4 * g + x <= r ? before : 0.f;
+              before += s[x];
+              v[x] += dpp_row<0x128>(v[x]);
+              v[x] += dpp_row<0x124>(v[x]);
+              v[x] += dpp_row<0x122>(v[x]);
+              v[x] += dpp_row<0x121>(v[x]);
+            }
+            if (r == 0) *reinterpret_cast<f32x4*>(red + tile * kT + 16 * t + 4 * g) = v;
           }
         }
-#pragma unroll
-        for (int z = 0; z < (int)(16 / sizeof(E)); ++z) dot = fmaf(s[z], d[z], dot);
       }
-      st ^= 1;
-    }
-    // pairs of tokens
-    const float hi = gate[i], lo = gate[kT + i];
-    float base = 0.f;  // sum over the rows of the tiles before
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_state(vh, 0);
+      // dQ += K^T B, or dK += Q^T B
 #pragma unroll
-    for (int t = 0; t <= kNW; ++t) {
-      const bool lower = t <= w && t < kNW;
-      const int tile = t < kNW ? t : w;
-      const f32x4 rh = *reinterpret_cast<const f32x4*>(gate + 16 * tile + 4 * g),
-                  rl = *reinterpret_cast<const f32x4*>(gate + kT + 16 * tile + 4 * g);
+      for (int kb = 0; kb < kT / M::kDepth; ++kb) {
+        if (kKeys ? (kb + 1) * M::kTiles <= own0 : kb * M::kTiles > own0 + 1) continue;
+        const auto f0 = M::template split<M::parts(2)>(&B[0][kb * M::kTiles]);
+        const auto f1 = M::template split<M::parts(2)>(&B[1][kb * M::kTiles]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = 16 * tile + 4 * g + x;
-        const float e = (hi - rh[x]) + (lo - rl[x]);
-        const bool live = lower ? row <= i : row >= i;
-        bb[t][x] = live ? bb[t][x] * (a.scale * exp_f32(lower ? e : -e)) : 0.f;
-      }
-      B[t] += bb[t];
-      if (lower) {
-        // B_ij (q_i . k_j), then for every row t of the tile the sum over the rows before it, over columns i >= t
-        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        for (int m = 0; m < kTiles; ++m) {
+          const auto xc = kt.cols(sm + Sm::kX, m, kb);
 #pragma unroll
-        for (int kb = 0; kb < DK / M::kDepth; ++kb)
-          s = M::mma(kt.rows(sm + Sm::kK, t, kb), kt.rows(sm + Sm::kQ, w, kb), s);
-        s *= bb[t];
-        float own = (s[0] + s[1]) + (s[2] + s[3]);
-        const float up1 = __shfl_up(own, 16), up2 = __shfl_up(own, 32), up3 = __shfl_up(own, 48);
-        float before = base + (g > 0 ? up1 : 0.f) + (g > 1 ? up2 : 0.f) + (g > 2 ? up3 : 0.f);
-        base += across_groups(own);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 16 * t + 4 * g + x;
-          float v = row <= i ? before : 0.f;
-          before += s[x];
-          v += dpp_row<0x128>(v);
-          v += dpp_row<0x124>(v);
-          v += dpp_row<0x122>(v);
-          v += dpp_row<0x121>(v);
-          if (r == 0) red[w * kT + row] = v;
+          for (int x = 0; x < M::parts(2); ++x) {
+            X[0][m] = M::mma(xc, f0.p[x], X[0][m]);
+            X[1][m] = M::mma(xc, f1.p[x], X[1][m]);
+          }
         }
       }
     }
-    // the state's terms, and their dots with q_i and k_i
-    {
-      const float eg = gate[2 * kT + i], ci = gate[3 * kT + i];
-      float rq = 0.f, rk = 0.f;
+    __builtin_amdgcn_sched_barrier(0);
+    // the state's terms: S dO_i, or dS' v_j
+    f32x4 s[2][kTiles];
 #pragma unroll
-      for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-        const auto qi = kt.rows(sm + Sm::kQ, w, kb), ki = kt.rows(sm + Sm::kK, w, kb);
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) s[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const KT kt(opaque(lane));
+    for (int db = 0; db < dblocks; ++db) {
+      rows.put(smem + Sm::kS);
+      typename M::Frag x[2][kDB];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int kb = 0; kb < kDB; ++kb) x[c][kb] = own[c][kb];
+      __syncthreads();
+      if (db + 1 < dblocks) {
+        fetch_state(vh, db + 1);
+        fetch_own(vh, db + 1);
+      }
+#pragma unroll
+      for (int kb = 0; kb < kDB; ++kb)
+#pragma unroll
+        for (int p = 0; p < kP; ++p)
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m) {
+            const auto f = kt.template cols<true>(sm + Sm::kS + p * Sm::kState, m, kb);
+            s[0][m] = M::mma(f, x[0][kb], s[0][m]);
+            s[1][m] = M::mma(f, x[1][kb], s[1][m]);
+          }
+      __syncthreads();  // the state's rows have been read
+    }
+    // with their token's factor, and their dots with q_i or k_j
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int i = 16 * (own0 + c) + r;
+      const float f = gate[2 * kT + i];
+      typename M::Frag xi[DK / M::kDepth];
+      load_x(c, xi);
+      float sum = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < DK / M::kDepth; ++kb)
 #pragma unroll
         for (int y = 0; y < M::kTiles; ++y)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int m = kb * M::kTiles + y;
-            const float fq = eg * sq[m][x], fk = ci * sk[m][x];
-            rq = fmaf((float)qi[4 * y + x], fq, rq);
-            rk = fmaf((float)ki[4 * y + x], fk, rk);
-            dQ[m][x] += fq;
-            dK[m][x] += fk;
+            const float v = f * s[c][kb * M::kTiles + y][x];
+            sum = fmaf((float)xi[kb][4 * y + x], v, sum);
+            X[c][kb * M::kTiles + y][x] += v;
           }
-      }
-      rq = across_groups(rq);
-      rk = across_groups(rk);
-      if (g == 0) {
-        tok[i] = rq;
-        tok[kT + i] = rk;
-      }
-#pragma unroll
-      for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
-      if (lane == 0) dots[w] = dot;
+      sum = across_groups(sum);
+      if (g == 0) tok[i] = sum;
     }
     __syncthreads();
     if (w == 0) {
-      float all = 0.f;
+      float sums[kT / 64], whole = 0.f;
+      if constexpr (kKeys) {
+        // <S, dS'> and the sums of Z before each token: 64 x + lane
+        const float* d = b.dots + (slot * a.hv + vh) * b.dot_parts;
+        float all = 0.f;
+        for (int x = 0; x < b.dot_parts; ++x) all += d[x];
+        whole = all * gate[3 * kT];
 #pragma unroll
-      for (int x = 0; x < kNW; ++x) all += dots[x];
-      all *= gate[4 * kT];
-      // tokens lane, 64 + lane: sums of Z before and of R from there on, fp32: all have one sign or are independent
-      float z0 = 0.f, later[kT / 64], earlier[kT / 64];
+        for (int x = 0; x < kT / 64; ++x) {
+          float sum = tok[64 * x + lane];
 #pragma unroll
-      for (int x = 0; x < kT / 64; ++x) {
-        float z = tok[kT + 64 * x + lane], s = z;
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) {
-          const float t = __shfl_up(s, m);
-          if (lane >= m) s += t;
+          for (int m = 1; m < 64; m *= 2) {
+            const float t = __shfl_up(sum, m);
+            if (lane >= m) sum += t;
+          }
+          const float one = __shfl_up(sum, 1);
+          sums[x] = whole + (lane ? one : 0.f);
+          whole += __shfl(sum, 63);
         }
-        const float one = __shfl_up(s, 1);
-        earlier[x] = z0 + (lane ? one : 0.f);
-        z0 += __shfl(s, 63);
-      }
-      float r0 = 0.f;
+      } else {
+        // the sums of R from each token on
 #pragma unroll
-      for (int x = kT / 64 - 1; x >= 0; --x) {
-        float s = tok[64 * x + lane];
+        for (int x = kT / 64 - 1; x >= 0; --x) {
+          float sum = tok[64 * x + lane];
 #pragma unroll
-        for (int m = 1; m < 64; m *= 2) {
-          const float t = __shfl_down(s, m);
-          if (lane + m < 64) s += t;
+          for (int m = 1; m < 64; m *= 2) {
+            const float t = __shfl_down(sum, m);
+            if (lane + m < 64) sum += t;
+          }
+          sums[x] = whole + sum;
+          whole += __shfl(sum, 0);
         }
-        later[x] = r0 + s;
-        r0 += __shfl(s, 0);
       }
 #pragma unroll
       for (int x = 0; x < kT / 64; ++x) {
         const int t = 64 * x + lane;
-        float pairs = 0.f;
-        for (int y = t / 16; y < kNW; ++y) pairs += red[y * kT + t];
-        if (t < n) b.dg[(t0 + t) * a.hv + vh] = ((all + earlier[x]) + later[x]) + pairs;
+        const int64_t at = (t0 + t) * a.hv + vh;
+        if (t >= n) continue;
+        if constexpr (kKeys) {
+          b.dgz[at] = sums[x];
+        } else {
+          float pairs = 0.f;
+          for (int y = t / 16; y < kNT; ++y) pairs += red[y * kT + t];
+          b.dg[at] = (b.dgz[at] + sums[x]) + pairs;
+        }
       }
     }
     __syncthreads();  // gates and sums have been read
   }
-  // dQ += K^T B^T, dK += Q^T B
+  E* const out = static_cast<E*>(kKeys ? b.dk : b.dq);
 #pragma unroll
-  for (int kb = 0; kb < kT / M::kDepth; ++kb) {
-    f32x4 lo[M::kTiles], up[M::kTiles];
+  for (int c = 0; c < 2; ++c) {
+    const int i = 16 * (own0 + c) + r;
+    if (i >= n) continue;
+    const int64_t at = ((t0 + i) * a.hk + kh) * (int64_t)a.dk;
+    if (b.groups > 1) {
+      float* to = b.part + ((kKeys ? b.groups : 0) + (int64_t)grp) * (b.tokens * a.hk * (int64_t)a.dk) + at;
 #pragma unroll
-    for (int y = 0; y < M::kTiles; ++y) {
-      const int t = kb * M::kTiles + y;
-      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-      lo[y] = t <= w ? B[t] : zero;
-      up[y] = t == w ? B[kNW] : t > w ? B[t] : zero;
+      for (int m = 0; m < kTiles; ++m)
+        if (KT::value(m, g, 0) < a.dk) *reinterpret_cast<f32x4*>(to + KT::value(m, g, 0)) = X[c][m];
+      continue;
     }
-    if (kb * M::kTiles <= w) {
-      const auto f = M::template split<M::parts(2)>(lo);
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        const auto kc = kt.cols(sm + Sm::kK, m, kb);
-#pragma unroll
-        for (int x = 0; x < M::parts(2); ++x) dQ[m] = M::mma(kc, f.p[x], dQ[m]);
-      }
-    }
-    if (kb * M::kTiles + M::kTiles > w) {
-      const auto f = M::template split<M::parts(2)>(up);
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        const auto qc = kt.cols(sm + Sm::kQ, m, kb);
-#pragma unroll
-        for (int x = 0; x < M::parts(2); ++x) dK[m] = M::mma(qc, f.p[x], dK[m]);
-      }
-    }
-  }
-  if (i >= n) return;
-  const int64_t at = ((t0 + i) * a.hk + kh) * (int64_t)a.dk;
-  if (b.groups > 1) {
-    const int64_t size = b.tokens * a.hk * (int64_t)a.dk;
-    float* pq = b.part + (int64_t)grp * size + at;
-    float* pk = pq + (int64_t)b.groups * size;
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
+    for (int m = 0; m < kTiles; m += M::kTiles) {
       const int v = KT::value(m, g, 0);
-      if (v < a.dk) {
-        *reinterpret_cast<f32x4*>(pq + v) = dQ[m];
-        *reinterpret_cast<f32x4*>(pk + v) = dK[m];
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int m = 0; m < kTiles; m += M::kTiles) {
-    const int v = KT::value(m, g, 0);
-    if (v < a.dk) {
-      *reinterpret_cast<typename M::Frag*>(static_cast<E*>(b.dq) + at + v) = M::pack(&dQ[m]);
-      *reinterpret_cast<typename M::Frag*>(static_cast<E*>(b.dk) + at + v) = M::pack(&dK[m]);
+      if (v < a.dk) *reinterpret_cast<typename M::Frag*>(out + at + v) = M::pack(&X[c][m]);
     }
   }
 }
@@ -407,7 +487,7 @@ __global__ __launch_bounds__(256) void linear_fold_kernel(GradArgs b) {
 
 struct BwdLayout {  // workspace regions in bytes
   SegLayout seg;
-  size_t s, ds, part, total;
+  size_t s, ds, dots, dgz, part, total;
   int64_t item, units;
   int32_t groups;
 };
@@ -416,20 +496,23 @@ BwdLayout layout_t(const mamba_delta_dims* d, bool packed) {
   BwdLayout l = {};
   l.seg = seg_layout(d, packed);
   l.units = slots_of(d, packed, kUnit<E>);
-  l.item = kImgParts<E> * image_part<E>(d);
-  const size_t img = (size_t)l.units * (size_t)d->v_heads * (size_t)l.item;
+  l.item = image_size(d);
+  const size_t img = (size_t)l.units * (size_t)d->v_heads * (size_t)l.item * sizeof(float);
   l.s = (l.seg.total + 1023) / 1024 * 1024;
   l.ds = l.s + img;
-  l.part = l.ds + img;
-  // enough workgroups for two rounds of the CUs
+  l.dots = l.ds + img;
+  const size_t tokens = (size_t)(packed ? d->seqlen : d->batch * d->seqlen);
+  l.dgz = l.dots + ((size_t)l.units * (size_t)d->v_heads * (size_t)((d->dv + kCols - 1) / kCols) * kWaves4 * sizeof(float) +
+                    255) / 256 * 256;
+  l.part = l.dgz + (tokens * (size_t)d->v_heads * sizeof(float) + 255) / 256 * 256;
+  // enough workgroups for one round of two per CU
   const int64_t rep = d->v_heads / d->qk_heads, wgs = l.units * d->qk_heads;
   l.groups = (int32_t)std::max<int64_t>(1, std::min<int64_t>(rep, 512 / std::max<int64_t>(wgs, 1)));
   const int64_t per = (rep + l.groups - 1) / l.groups;
   l.groups = (int32_t)((rep + per - 1) / per);  // (none without heads)
   l.total = l.part;
   if (l.groups > 1)
-    l.total += 2 * (size_t)l.groups * (size_t)(packed ? d->seqlen : d->batch * d->seqlen) *
-               (size_t)(d->qk_heads * d->dk) * sizeof(float);
+    l.total += 2 * (size_t)l.groups * tokens * (size_t)(d->qk_heads * d->dk) * sizeof(float);
   return l;
 }
 BwdLayout layout(const mamba_delta_dims* d, bool packed) {
@@ -440,8 +523,11 @@ template <typename E, int DK>
 int launch_grad(const GradArgs& b, int64_t units, hipStream_t s) {
   using Sm = GradSmem<E, DK>;
   const uint32_t blocks = (uint32_t)(units * b.f.hk * b.groups);
-  hipLaunchKernelGGL((linear_grad_kernel<E, DK>), wide_grid(blocks, Sm::kNW * 64), dim3(Sm::kNW * 64), 0, s, b,
-                     blocks);
+  const dim3 grid = wide_grid(blocks, Sm::kNW * 64), threads(Sm::kNW * 64);
+  hipLaunchKernelGGL((linear_grad_kernel<E, DK, true>), grid, threads, 0, s, b, blocks);
+  const int st = launch_status();
+  if (st != MAMBA_OK) return st;
+  hipLaunchKernelGGL((linear_grad_kernel<E, DK, false>), grid, threads, 0, s, b, blocks);
   return launch_status();
 }
 
@@ -449,10 +535,10 @@ template <typename E>
 int launch_bwd(const PassArgs& fwd, const PassArgs& rev, const GradArgs& b, int64_t units, hipStream_t s) {
   constexpr bool bf = sizeof(E) == 2;
   int st = MAMBA_OK;
-  if (fwd.f.seg_chunks && (st = launch_segments(fwd, bf, false, s)) != MAMBA_OK) return st;
-  if ((st = launch_pass<E, kImages>(fwd, s)) != MAMBA_OK) return st;
   if (rev.f.seg_chunks && (st = launch_segments(rev, bf, true, s)) != MAMBA_OK) return st;
   if ((st = launch_pass<E, kOutput | kImages | kReverse>(rev, s)) != MAMBA_OK) return st;
+  if (fwd.f.seg_chunks && (st = launch_segments(fwd, bf, false, s)) != MAMBA_OK) return st;
+  if ((st = launch_pass<E, kImages | kDots>(fwd, s)) != MAMBA_OK) return st;
   st = b.f.dk <= 64 ? launch_grad<E, 64>(b, units, s) : launch_grad<E, 128>(b, units, s);
   if (st != MAMBA_OK || b.groups == 1) return st;
   hipLaunchKernelGGL((linear_fold_kernel<E>), dim3((unsigned)b.f.slots, 2), dim3(256), 0, s, b);
@@ -492,7 +578,7 @@ int mamba_linear_attn_bwd(const void* q, const void* k, const void* v, const flo
   PassArgs fwd = {}, rev = {};
   fwd.f = make_args(dims, scale, q, k, v, g, nullptr, initial_state, seq_offsets);
   fwd.gate = g;
-  fwd.img = ws + l.s;
+  fwd.img = reinterpret_cast<float*>(ws + l.s);
   fwd.img_item = l.item;
   set_segments(fwd, l.seg, ws);
   rev = fwd;
@@ -505,7 +591,9 @@ int mamba_linear_attn_bwd(const void* q, const void* k, const void* v, const flo
   rev.f.out = dv;
   rev.f.s0 = dlast;
   rev.f.last = dinitial_state;
-  rev.img = ws + l.ds;
+  rev.img = reinterpret_cast<float*>(ws + l.ds);
+  fwd.other = rev.img;
+  fwd.dots = reinterpret_cast<float*>(ws + l.dots);
   GradArgs b = {};
   b.f = fwd.f;
   b.gate = g;
@@ -513,6 +601,9 @@ int mamba_linear_attn_bwd(const void* q, const void* k, const void* v, const flo
   b.s_img = fwd.img;
   b.ds_img = rev.img;
   b.img_item = l.item;
+  b.dots = fwd.dots;
+  b.dot_parts = (int32_t)((dims->dv + kCols - 1) / kCols) * kWaves4;
+  b.dgz = reinterpret_cast<float*>(ws + l.dgz);
   b.dq = dq;
   b.dk = dk;
   b.dg = dg;
