@@ -108,13 +108,18 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_resource(const E* p, int6
 }
 
 template <int kCtrl, int kRows>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, kRows, 0xf, false));
+}
+template <int kCtrl, int kRows>
 __device__ __forceinline__ double dpp_or_zero(double v) {
   const int2 x = __builtin_bit_cast(int2, v);
   return __builtin_bit_cast(double, int2{__builtin_amdgcn_update_dpp(0, x.x, kCtrl, kRows, 0xf, false),
                                          __builtin_amdgcn_update_dpp(0, x.y, kCtrl, kRows, 0xf, false)});
 }
 // sum of v over lanes 0 .. lane: within rows of 16 lanes, then the rows before
-__device__ __forceinline__ double prefix_sum(double v) {
+template <typename V>
+__device__ __forceinline__ V prefix_sum(V v) {
   v += dpp_or_zero<0x111, 0xf>(v);  // lane - 1
   v += dpp_or_zero<0x112, 0xf>(v);
   v += dpp_or_zero<0x114, 0xf>(v);

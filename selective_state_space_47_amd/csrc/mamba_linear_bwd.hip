@@ -65,6 +65,13 @@ struct GradSmem {
   static_assert(2 * kBytes <= 160 * 1024, "two workgroups per CU");
 };
 
+// The same value, but as a new one for the compiler: addresses made from it are made again for each head, not held
+// in registers through the loop over heads.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // A thread's share of 32 columns of a state's image: words of 16 bytes of an operand, on their way in registers.
 template <typename E, int DK, int kThreads>
 struct StateRows {
@@ -72,9 +79,10 @@ struct StateRows {
   static constexpr int kN = (kItems + kThreads - 1) / kThreads;
   f32x4 v[kN][kF];
   __device__ __forceinline__ void load(const float* p) {
+    const int thread = opaque(threadIdx.x);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int at = threadIdx.x + i * kThreads;  // word at / 64 of the image's kF KBs each
+      const int at = thread + i * kThreads;  // word at / 64 of the image's kF KBs each
 #pragma unroll
       for (int x = 0; x < kF; ++x)
         v[i][x] = at < kItems ? *reinterpret_cast<const f32x4*>(p + (at / 64 * kF + x) * 256 + at % 64 * 4)
@@ -85,9 +93,10 @@ struct StateRows {
   __device__ __forceinline__ void put(char* lds) const {
     using KT = KeyTile<E, DK>;
     constexpr int kPer = DK / 4 / kV;  // words of 64 lanes for 16 columns
+    const int thread = opaque(threadIdx.x);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int at = threadIdx.x + i * kThreads, lane = at % 64;
+      const int at = thread + i * kThreads, lane = at % 64;
       const int row = at / 64 / kPer * 16 + (lane & 15), word = at / 64 % kPer * 4 + (lane >> 4);
       if (kItems % kThreads && at >= kItems) continue;
       const auto f = Mma<E>::template split<kImgParts<E>>(v[i]);
@@ -98,13 +107,6 @@ struct StateRows {
     }
   }
 };
-
-// The same value, but as a new one for the compiler: addresses made from it are made again for each head, not held
-// in registers through the loop over heads.
-__device__ __forceinline__ int opaque(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
 
 // 16 bytes of a buffer, zeros past its end
 template <typename F>
@@ -134,7 +136,10 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
   if (wg >= blocks) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int own0 = 2 * w;  // this wave's tiles: own0, own0 + 1
+  // This wave's tiles of 16 tokens: one of each half, so that the waves have equally many pairs.  The first meets only
+  // the other side's tiles of one half, from kFirst on, the second all.
+  constexpr int kFirst = kKeys ? kNT / 2 : 0;
+  const int tile_of[2] = {kKeys ? kNT - 1 - w : w, kKeys ? w : kNT - 1 - w};
   const uint32_t grp = wg % (uint32_t)b.groups, rest = wg / (uint32_t)b.groups;
   const int64_t slot = rest / (uint32_t)a.hk;
   const int kh = (int)(rest - slot * a.hk);
@@ -165,31 +170,36 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
   // columns [32 db, ...) of the other side's V or dO of value head vh into a stage
   auto copy = [&](int vh, int db, int st) {
     const int cols = min(a.dv - 32 * db, 32);
-    const RowCopy<E, BT, kT, kNW> cy(w, lane, other_ys, cols);
+    const RowCopy<E, BT, kT, kNW> cy(w, opaque(lane), other_ys, cols);
     cy(rows_buffer(other_y + (int64_t)vh * a.dv + 32 * db, n, other_ys, cols), lds0 + Sm::kA + st * Sm::kABytes, w);
   };
   // this wave's own tokens of dO or V as operands
   typename M::Frag own[2][kDB];
   auto fetch_own = [&](int vh, int db) {
     const auto buf = rows_resource(own_y + (int64_t)vh * a.dv, n, own_ys, a.dv);
+    const int l = opaque(lane), g = l >> 4, r = l & 15;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int kb = 0; kb < kDB; ++kb) {
         const int col = 32 * db + kb * M::kDepth + g * kV;
-        const uint32_t at = (uint32_t)((16 * (own0 + c) + r) * own_ys + col) * (uint32_t)sizeof(E);
+        const uint32_t at = (uint32_t)((16 * tile_of[c] + r) * own_ys + col) * (uint32_t)sizeof(E);
         own[c][kb] = load_16<typename M::Frag>(buf, col < a.dv ? at : kOutside);
       }
   };
-  // and tile c of them of q or k
-  auto load_x = [&](int c, typename M::Frag(&f)[DK / M::kDepth]) {
+  // and of q or k
+  typename M::Frag xs[2][DK / M::kDepth];
+  auto fetch_x = [&]() {
     const auto buf = rows_resource(own_x, n, own_xs, a.dk);
+    const int l = opaque(lane), g = l >> 4, r = l & 15;
 #pragma unroll
-    for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-      const int col = kb * M::kDepth + g * kV;
-      const uint32_t at = (uint32_t)((16 * (own0 + c) + r) * own_xs + col) * (uint32_t)sizeof(E);
-      f[kb] = load_16<typename M::Frag>(buf, col < a.dk ? at : kOutside);
-    }
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+        const int col = kb * M::kDepth + g * kV;
+        const uint32_t at = (uint32_t)((16 * tile_of[c] + r) * own_xs + col) * (uint32_t)sizeof(E);
+        xs[c][kb] = load_16<typename M::Frag>(buf, col < a.dk ? at : kOutside);
+      }
   };
   StateRows<E, DK, kNW * 64> rows;
   auto fetch_state = [&](int vh, int db) {
@@ -209,19 +219,21 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
   for (int h = h0; h < h1; ++h) {
     const int vh = kh * a.rep + h;
     fetch_own(vh, 0);
+    if (!kKeys) fetch_x();
     // gates: wave 0, prefix sums in fp64, kept as two floats
     if (w == 0) {
+      const int l = opaque(lane);
       double before = 0.0, G[kT / 64];
 #pragma unroll
       for (int x = 0; x < kT / 64; ++x) {
-        const int t = 64 * x + lane;
+        const int t = 64 * x + l;
         const float v = t < n ? clamp_gate(b.gate[(t0 + t) * a.hv + vh]) : 0.f;
         G[x] = before + prefix_sum((double)v);
         before = last_lane(G[x]);
       }
 #pragma unroll
       for (int x = 0; x < kT / 64; ++x) {
-        const int t = 64 * x + lane;
+        const int t = 64 * x + l;
         const float hi = (float)G[x];
         gate[t] = hi;
         gate[kT + t] = (float)(G[x] - (double)hi);
@@ -232,11 +244,9 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
     {
       // dO V^T: rows of tile t of the other side, columns = own tokens (tiles past the diagonal too: they cost less
       // than branches)
-      f32x4 B[2][kNT];
+      f32x4 B0[kNT / 2], B1[kNT];
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int t = 0; t < kNT; ++t) B[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < kNT; ++t) B0[t / 2] = B1[t] = f32x4{0.f, 0.f, 0.f, 0.f};
       const BT bt(opaque(lane));
       for (int db = 0; db < dblocks; ++db) {
         copies_done();
@@ -254,66 +264,78 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
 #pragma unroll
           for (int t = 0; t < kNT; ++t) {
             const auto f = bt.rows(sa, t, kb);
-            B[0][t] = M::mma(f, x[0][kb], B[0][t]);
-            B[1][t] = M::mma(f, x[1][kb], B[1][t]);
+            if (t >= kFirst && t < kFirst + kNT / 2) B0[t - kFirst] = M::mma(f, x[0][kb], B0[t - kFirst]);
+            B1[t] = M::mma(f, x[1][kb], B1[t]);
           }
         st ^= 1;
       }
       const KT kt(opaque(lane));
-      // times scale D; on the queries' side times q . k for dg.  (The barriers keep the compiler from drawing the
-      // tiles into each other: it spilled 168 registers.)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        __builtin_amdgcn_sched_barrier(0);
-        const int tile = own0 + c, i = 16 * tile + r;
-        const float hi = gate[i], lo = gate[kT + i];
-        f32x4 qk[kKeys ? 1 : kNT];
-        if constexpr (!kKeys) {
-          typename M::Frag qi[DK / M::kDepth];
-          load_x(c, qi);
-#pragma unroll
-          for (int t = 0; t < kNT; ++t) qk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int kb = 0; kb < DK / M::kDepth; ++kb)
-#pragma unroll
-            for (int t = 0; t < kNT; ++t) qk[t] = M::mma(kt.rows(sm + Sm::kX, t, kb), qi[kb], qk[t]);
-          __builtin_amdgcn_sched_barrier(0);
+      // times scale D; on the queries' side the sums of q_i . k_t B for dg.  (The barriers keep the compiler from drawing
+      // the tiles into each other: it spilled 168 registers.)
+      auto weigh = [&](int tile, f32x4& Bt, int t, float hi, float lo) {
+        if (kKeys ? t < tile : t > tile) {
+          Bt = f32x4{0.f, 0.f, 0.f, 0.f};
+          return;
         }
-        float base = 0.f;  // sum over the rows of the tiles before
+        const f32x4 rh = *reinterpret_cast<const f32x4*>(gate + 16 * t + 4 * g),
+                    rl = *reinterpret_cast<const f32x4*>(gate + kT + 16 * t + 4 * g);
+        const f32x4 e = (hi - rh) + (lo - rl);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) Bt[x] *= a.scale * exp_f32(kKeys ? -e[x] : e[x]);
+        if (t == tile)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (kKeys ? 4 * g + x < r : 4 * g + x > r) Bt[x] = 0.f;
+      };
+      // pairs of own token i and tokens of tile t: of a tile before i's the sums over i, at red[i's tile][t's tokens], and
+      // `rows`, the sums over t; of i's own tile the sums over i >= t' > t for every t'
+      auto sum_pairs = [&](int tile, f32x4 s, int t, float& rows) {
+        f32x4 v = s;
+        const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+        if (t < tile) {
+          rows += sum;
+        } else {
+          const float up1 = __shfl_up(sum, 16), up2 = __shfl_up(sum, 32), up3 = __shfl_up(sum, 48);
+          float before = (g > 0 ? up1 : 0.f) + (g > 1 ? up2 : 0.f) + (g > 2 ? up3 : 0.f);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            v[x] = 4 * g + x <= r ? before : 0.f;
+            before += s[x];
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          v[x] += dpp_row<0x128>(v[x]);
+          v[x] += dpp_row<0x124>(v[x]);
+          v[x] += dpp_row<0x122>(v[x]);
+          v[x] += dpp_row<0x121>(v[x]);
+        }
+        if (r == 0) *reinterpret_cast<f32x4*>(red + tile * kT + 16 * t + 4 * g) = v;
+      };
+      float rows_sum[2] = {0.f, 0.f};
+      {
+        const int l = opaque(lane), i0 = 16 * tile_of[0] + (l & 15), i1 = 16 * tile_of[1] + (l & 15);
+        const float hi0 = gate[i0], lo0 = gate[kT + i0], hi1 = gate[i1], lo1 = gate[kT + i1];
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
-          if (kKeys ? t < tile : t > tile) {
-            B[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            continue;
-          }
           __builtin_amdgcn_sched_barrier(0);
-          const f32x4 rh = *reinterpret_cast<const f32x4*>(gate + 16 * t + 4 * g),
-                      rl = *reinterpret_cast<const f32x4*>(gate + kT + 16 * t + 4 * g);
-          const f32x4 e = (hi - rh) + (lo - rl);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) B[c][t][x] *= a.scale * exp_f32(kKeys ? -e[x] : e[x]);
-          if (t == tile)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (kKeys ? 4 * g + x < r : 4 * g + x > r) B[c][t][x] = 0.f;
+          const bool two = t >= kFirst && t < kFirst + kNT / 2;
+          f32x4 qk0 = {0.f, 0.f, 0.f, 0.f}, qk1 = qk0;
           if constexpr (!kKeys) {
-            // then for every row t of the tile the sum over the rows before it, over columns i >= t
-            const f32x4 s = qk[t] * B[c][t];
-            const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-            const float up1 = __shfl_up(sum, 16), up2 = __shfl_up(sum, 32), up3 = __shfl_up(sum, 48);
-            float before = base + (g > 0 ? up1 : 0.f) + (g > 1 ? up2 : 0.f) + (g > 2 ? up3 : 0.f);
-            base += across_groups(sum);
-            f32x4 v;
+            if (t <= tile_of[1]) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              v[x] = t < tile || 4 * g + x <= r ? before : 0.f;
-              before += s[x];
-              v[x] += dpp_row<0x128>(v[x]);
-              v[x] += dpp_row<0x124>(v[x]);
-              v[x] += dpp_row<0x122>(v[x]);
-              v[x] += dpp_row<0x121>(v[x]);
+              for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+                const auto f = kt.rows(sm + Sm::kX, t, kb);
+                if (two) qk0 = M::mma(f, xs[0][kb], qk0);
+                qk1 = M::mma(f, xs[1][kb], qk1);
+              }
             }
-            if (r == 0) *reinterpret_cast<f32x4*>(red + tile * kT + 16 * t + 4 * g) = v;
+          }
+          if (two) weigh(tile_of[0], B0[t - kFirst], t, hi0, lo0);
+          weigh(tile_of[1], B1[t], t, hi1, lo1);
+          if constexpr (!kKeys) {
+            if (two && t <= tile_of[0]) sum_pairs(tile_of[0], qk0 * B0[t - kFirst], t, rows_sum[0]);
+            if (t <= tile_of[1]) sum_pairs(tile_of[1], qk1 * B1[t], t, rows_sum[1]);
           }
         }
       }
@@ -322,17 +344,43 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
       // dQ += K^T B, or dK += Q^T B
 #pragma unroll
       for (int kb = 0; kb < kT / M::kDepth; ++kb) {
-        if (kKeys ? (kb + 1) * M::kTiles <= own0 : kb * M::kTiles > own0 + 1) continue;
-        const auto f0 = M::template split<M::parts(2)>(&B[0][kb * M::kTiles]);
-        const auto f1 = M::template split<M::parts(2)>(&B[1][kb * M::kTiles]);
+        const int t = kb * M::kTiles;
+        const bool two = t >= kFirst && t < kFirst + kNT / 2;
+        if (kKeys ? t + M::kTiles <= tile_of[1] : t > tile_of[1]) continue;
+        const auto f1 = M::template split<M::parts(2)>(&B1[t]);
+        const auto f0 = M::template split<M::parts(2)>(&B0[two ? t - kFirst : 0]);
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
           const auto xc = kt.cols(sm + Sm::kX, m, kb);
 #pragma unroll
           for (int x = 0; x < M::parts(2); ++x) {
-            X[0][m] = M::mma(xc, f0.p[x], X[0][m]);
+            if (two) X[0][m] = M::mma(xc, f0.p[x], X[0][m]);
             X[1][m] = M::mma(xc, f1.p[x], X[1][m]);
           }
+        }
+      }
+      if constexpr (!kKeys) {
+        // of each own tile: the pairs with tokens before t as sums over the tokens before it; the own tile's with the
+        // tokens of the tiles before
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int tile = tile_of[c];
+          float* const to = red + tile * kT;
+          float v = across_groups(rows_sum[c]);  // of token r
+          v += dpp_or_zero<0x101, 0xf>(v);       // and those behind it
+          v += dpp_or_zero<0x102, 0xf>(v);
+          v += dpp_or_zero<0x104, 0xf>(v);
+          v += dpp_or_zero<0x108, 0xf>(v);
+          float before = 0.f;
+#pragma unroll
+          for (int x = 0; x < kT / 64; ++x) {
+            const int t = 64 * x + lane;
+            const float s = t < 16 * tile ? to[t] : 0.f;
+            const float p = prefix_sum(s), q = __shfl_up(p, 1);
+            if (t < 16 * tile) to[t] = before + (lane ? q : 0.f);
+            before += __shfl(p, 63);
+          }
+          if (lane < 16) to[16 * tile + lane] += v;
         }
       }
     }
@@ -355,6 +403,8 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
       if (db + 1 < dblocks) {
         fetch_state(vh, db + 1);
         fetch_own(vh, db + 1);
+      } else if (!kKeys) {
+        fetch_x();
       }
 #pragma unroll
       for (int kb = 0; kb < kDB; ++kb)
@@ -368,14 +418,13 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
           }
       __syncthreads();  // the state's rows have been read
     }
+    if (kKeys) fetch_x();  // (registers for it sooner would be spilled ones: 274 -> 300 us)
     // with their token's factor, and their dots with q_i or k_j
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       __builtin_amdgcn_sched_barrier(0);
-      const int i = 16 * (own0 + c) + r;
+      const int l = opaque(lane), i = 16 * tile_of[c] + (l & 15);
       const float f = gate[2 * kT + i];
-      typename M::Frag xi[DK / M::kDepth];
-      load_x(c, xi);
       float sum = 0.f;
 #pragma unroll
       for (int kb = 0; kb < DK / M::kDepth; ++kb)
@@ -384,14 +433,15 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float v = f * s[c][kb * M::kTiles + y][x];
-            sum = fmaf((float)xi[kb][4 * y + x], v, sum);
+            sum = fmaf((float)xs[c][kb][4 * y + x], v, sum);
             X[c][kb * M::kTiles + y][x] += v;
           }
       sum = across_groups(sum);
-      if (g == 0) tok[i] = sum;
+      if (l < 16) tok[i] = sum;
     }
     __syncthreads();
     if (w == 0) {
+      const int l = opaque(lane);
       float sums[kT / 64], whole = 0.f;
       if constexpr (kKeys) {
         // <S, dS'> and the sums of Z before each token: 64 x + lane
@@ -401,7 +451,7 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
         whole = all * gate[3 * kT];
 #pragma unroll
         for (int x = 0; x < kT / 64; ++x) {
-          float sum = tok[64 * x + lane];
+          float sum = tok[64 * x + l];
 #pragma unroll
           for (int m = 1; m < 64; m *= 2) {
             const float t = __shfl_up(sum, m);
@@ -415,7 +465,7 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
         // the sums of R from each token on
 #pragma unroll
         for (int x = kT / 64 - 1; x >= 0; --x) {
-          float sum = tok[64 * x + lane];
+          float sum = tok[64 * x + l];
 #pragma unroll
           for (int m = 1; m < 64; m *= 2) {
             const float t = __shfl_down(sum, m);
@@ -427,7 +477,7 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
       }
 #pragma unroll
       for (int x = 0; x < kT / 64; ++x) {
-        const int t = 64 * x + lane;
+        const int t = 64 * x + l;
         const int64_t at = (t0 + t) * a.hv + vh;
         if (t >= n) continue;
         if constexpr (kKeys) {
@@ -444,7 +494,7 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
   E* const out = static_cast<E*>(kKeys ? b.dk : b.dq);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    const int i = 16 * (own0 + c) + r;
+    const int i = 16 * tile_of[c] + r;
     if (i >= n) continue;
     const int64_t at = ((t0 + i) * a.hk + kh) * (int64_t)a.dk;
     if (b.groups > 1) {
