@@ -75,27 +75,46 @@ struct Smem {
   static_assert(sizeof(E) == 4 || 3 * kBytes <= 160 * 1024, "three workgroups per CU");
 };
 
-// RowCopy whose tile row x holds row 63 - x of memory where kRev, and the same by way of registers
+// The same value, but as a new one for the compiler: addresses made from it are made again where they are needed,
+// not held in registers through a loop.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// RowCopy whose tile row x holds row 63 - x of memory where kRev, and the same by way of registers.  A lane's rows of a
+// tile whose swizzle repeats between them are whole steps apart, so that it keeps one offset.
 template <typename E, typename Tile, bool kRev>
 struct TokenCopy {
   static constexpr int kI = kC * Tile::kRow / 1024 / kWaves4;
+  static constexpr int kStep = kWaves4 * 64 / Tile::kWords;  // rows
+  static constexpr bool kOne = kStep % 16 == 0;
   typedef uint32_t Word __attribute__((ext_vector_type(4)));
-  uint32_t off[kI];
+  uint32_t off[kOne ? 1 : kI], step;
   __device__ __forceinline__ TokenCopy(int w, int lane, int64_t stride, int cols) {
 #pragma unroll
-    for (int i = 0; i < kI; ++i) {
+    for (int i = 0; i < (kOne ? 1 : kI); ++i) {
       const int at = (w + i * kWaves4) * 64 + lane, t = at / Tile::kWords;
       const int c = ((at % Tile::kWords) ^ Tile::key(t)) * (16 / (int)sizeof(E));
       off[i] = c < cols ? (uint32_t)((kRev ? kC - 1 - t : t) * stride + c) * (uint32_t)sizeof(E) : kOutside;
     }
+    step = (uint32_t)(kStep * stride) * (uint32_t)sizeof(E);
+  }
+  __device__ __forceinline__ uint32_t offset(int i) const {
+    if constexpr (kOne) {
+      if (i == 0) return off[0];
+      return off[0] == kOutside ? kOutside : kRev ? off[0] - i * step : off[0] + i * step;
+    } else {
+      return off[i];
+    }
   }
   __device__ __forceinline__ void operator()(i32x4 buf, uint32_t lds, int w) const {
 #pragma unroll
-    for (int i = 0; i < kI; ++i) copy_lds(buf, off[i], lds + (w + i * kWaves4) * 1024);
+    for (int i = 0; i < kI; ++i) copy_lds(buf, offset(i), lds + (w + i * kWaves4) * 1024);
   }
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buf, Word (&v)[kI]) const {
 #pragma unroll
-    for (int i = 0; i < kI; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)off[i], 0, 0);
+    for (int i = 0; i < kI; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)offset(i), 0, 0);
   }
   __device__ __forceinline__ static void put(char* lds, int w, int lane, const Word (&v)[kI]) {
 #pragma unroll
@@ -154,6 +173,16 @@ __device__ __forceinline__ void put_out(char* lds, int row, int col, f32x4 v) {
 // Below -200 exp is 0 in fp32; the clamp keeps -inf (a reset) out of differences and lets NaN through.
 __device__ __forceinline__ float clamp_gate(float g) { return g < -200.f ? -200.f : g; }
 
+// Which tiles (y, x) of the triangular matrix a wave makes: pairs of neighbouring y, as an operand holds them, one pair
+// for the waves 0 and 3 and two for the others (a row of tiles per wave would be two pairs for the last, on the way of
+// all, and nothing to do for the first).
+struct WaveTiles {
+  int w;
+  __device__ __forceinline__ int pairs() const { return w == 1 || w == 2 ? 2 : 1; }
+  __device__ __forceinline__ int x(int pair) const { return w == 1 ? pair : w == 2 ? 2 : 3; }
+  __device__ __forceinline__ int y(int pair) const { return w == 2 ? 2 * pair : w == 3 ? 2 : 0; }
+};
+
 // Rounding, bf16 storage: z times its factor enters the state as three bf16 parts (24 bits); the state and the
 // triangular matrix enter the output as two parts each, so that its own rounding is the only one that shows.
 template <typename E, int DK, int kWhat>
@@ -171,7 +200,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
   const Args& a = p.f;
   const uint32_t id = wide_index();
   if (id >= blocks) return;
-  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t wg = spread_index(id, blocks, a.rep * col_blocks);
   const int64_t sh = wg / col_blocks;
@@ -188,7 +217,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
   if (kSum && (kRev ? first == 0 : end == nchunks)) return;  // no segment follows
   const int col0 = (int)(wg - sh * col_blocks) * kCols;  // this workgroup's first column
   const int col = col0 + 16 * w;                         // this wave's
-  const bool has_col = col + r < a.dv, has_image = col < (a.dv + 31) / 32 * 32;
+  const bool has_image = col < (a.dv + 31) / 32 * 32;
   const E* yp = static_cast<const E*>(a.k) + sp.first * a.k_stride + (int64_t)kh * a.dk;
   const E* xp = static_cast<const E*>(a.q) + sp.first * a.q_stride + (int64_t)kh * a.dk;
   const E* zp = static_cast<const E*>(a.v) + sp.first * a.v_stride + (int64_t)vh * a.dv + col0;
@@ -200,9 +229,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
   const float* from = kSum ? nullptr : a.seg_chunks ? a.seg_state + g_at : a.s0 ? a.s0 + s_at : nullptr;
 
   // row 4 g + x of accumulator m and column col + r of a (dk, dv) matrix, past its end if there is none
-  auto state_at = [&](int m, int x) {
-    const int row = KT::value(m, g, x);
-    return has_col && row < a.dk ? (uint32_t)(row * a.dv + col + r) * 4u : kOutside;
+  auto state_at = [&](int l, int m, int x) {
+    const int row = KT::value(m, l >> 4, x), c = col + (l & 15);
+    return c < a.dv && row < a.dk ? (uint32_t)(row * a.dv + c) * 4u : kOutside;
   };
   auto state_resource = [&](const float* q) {  // (none: every load is past its end)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(q), 0, q ? a.dk * a.dv * 4 : 0, 0x00020000);
@@ -214,7 +243,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
     for (int m = 0; m < DK / 16; ++m)
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        S[m][x] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, (int)state_at(m, x), 0, 0));
+        S[m][x] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, (int)state_at(lane, m, x), 0, 0));
   }
 
   const uint32_t lds0 = lds_address(smem);
@@ -224,12 +253,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
   // Y and X of a chunk to registers and from there to LDS (with an output), Z, or Y and Z, straight to stage st; tokens
   // past the sequence are past the buffers and read as zero
   typename decltype(cy)::Word next_y[kO ? decltype(cy)::kI : 1], next_x[kO ? decltype(cx)::kI : 1];
-  auto load = [&](int64_t ch) {
-    if constexpr (kO) {
-      const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
-      cy.load(rows_resource(yp + t * a.k_stride, n, a.k_stride, a.dk), next_y);
-      cx.load(rows_resource(xp + t * a.q_stride, n, a.q_stride, a.dk), next_x);
-    }
+  auto load_y = [&](int64_t ch) {
+    const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
+    if constexpr (kO) cy.load(rows_resource(yp + t * a.k_stride, n, a.k_stride, a.dk), next_y);
+  };
+  auto load_x = [&](int64_t ch) {
+    const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
+    if constexpr (kO) cx.load(rows_resource(xp + t * a.q_stride, n, a.q_stride, a.dk), next_x);
   };
   auto copy = [&](int64_t ch, int st) {
     const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
@@ -241,9 +271,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
     constexpr int kWords = kCols * (int)sizeof(E) / 16;  // of a row
     const int64_t t = ch * kC, n = min((int64_t)kC, sp.len - t);
     const auto buf = rows_resource(op + t * o_stride, n, o_stride, vcols);
+    const int l = opaque(lane);
 #pragma unroll
     for (int i = 0; i < decltype(cz)::kI; ++i) {
-      const int at = (w + i * kWaves4) * 64 + lane, x = at / kWords, c = out_word<E>(x, at % kWords) * (16 / (int)sizeof(E));
+      const int at = (w + i * kWaves4) * 64 + l, x = at / kWords, c = out_word<E>(x, at % kWords) * (16 / (int)sizeof(E));
       const auto v = *reinterpret_cast<const typename decltype(cz)::Word*>(smem + Sm::kZ + st * Sm::kZBytes + 16 * at);
       __builtin_amdgcn_raw_buffer_store_b128(
           v, buf, (int)(c < vcols ? (uint32_t)((kRev ? kC - 1 - x : x) * o_stride + c) * (uint32_t)sizeof(E) : kOutside), 0, 0);
@@ -272,9 +303,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
     all += total;
   };
 
-  const KT kt(lane);
-  const TT tt(lane);
-  const VT vt(lane, 16 * w);
+  const WaveTiles tiles{w};
   const int64_t count = end - first;
   auto chunk_at = [&](int64_t it) { return kRev ? end - 1 - it : first + it; };
   constexpr int kPer = kUnit<E> / kC;  // chunks of a unit
@@ -291,7 +320,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
     }
   };
   if (count > 0) {
-    load(chunk_at(0));
+    load_y(chunk_at(0));
+    load_x(chunk_at(0));
     copy(chunk_at(0), 0);
     if (w == 0) put_gates(load_gate(chunk_at(0)), 0);
     load_other(chunk_at(0));
@@ -302,6 +332,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
   }
   for (int64_t it = 0; it < count; ++it) {
     const int64_t ch = chunk_at(it);
+    // (the last chunk reads itself again: a branch would hold the registers through the whole loop)
+    const int64_t next_chunk = chunk_at(min(it + 1, count - 1));
     const int st = (int)(it & 1);
     float next_gate = 0.f;
     copies_done();
@@ -311,7 +343,6 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
     if (kO && it) store_out(chunk_at(it - 1), st ^ 1);
     if (it + 1 < count) {
       if (w == 0) next_gate = load_gate(chunk_at(it + 1));
-      load(chunk_at(it + 1));
       copy(chunk_at(it + 1), st ^ 1);
     }
 
@@ -335,85 +366,129 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
       }
       if (kD && it + 1 < count && chunk_at(it + 1) % kPer == 0) load_other(chunk_at(it + 1));
     }
-    f32x4 o[4], s[4];
+    f32x4 o[4];
     if constexpr (kO) {
-      // columns x = 16 w + r of (Y X^T), rows y up to the diagonal: a lane holds 4 consecutive y of one x
+      const int l = opaque(lane), g = l >> 4, r = l & 15;
+      const KT kt(l);
+      // pairs of tiles of (Y X^T), a lane holding 4 consecutive y of one x, times scale D
+      f32x4 s[2][2];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) s[m] = o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j) s[j >> 1][j & 1] = o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      auto make_pair = [&](int j) {
+        const int tx = tiles.x(j), ty = tiles.y(j);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-        const auto xi = kt.rows(sm + Sm::kX, w, kb);
+        for (int kb = 0; kb < DK / M::kDepth; ++kb) {
+          const auto f = kt.rows(sm + Sm::kX, tx, kb);
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if (m <= w) s[m] = M::mma(kt.rows(sy, m, kb), xi, s[m]);
+          for (int c = 0; c < 2; ++c) s[j][c] = M::mma(kt.rows(sy, ty + c, kb), f, s[j][c]);
+        }
+        const int i = 16 * tx + r;
+        const float hi = gt[i], lo = gt[kC + i];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int t = 16 * (ty + c) + 4 * g;
+          const f32x4 e = (hi - *reinterpret_cast<const f32x4*>(gt + t)) + (lo - *reinterpret_cast<const f32x4*>(gt + kC + t));
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float v = s[j][c][x] * (a.scale * exp_f32(min(e[x], 0.f)));
+            s[j][c][x] = t + x <= i ? v : 0.f;
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      make_pair(0);
+      if (tiles.pairs() == 2) make_pair(1);
+      __builtin_amdgcn_sched_barrier(0);
+      load_y(next_chunk);
+      if (w == 0 && it + 1 < count) put_gates(next_gate, (int)((it + 1) & 1));
+      // (X S)^T, columns x tokens; operands are read a step ahead
+      constexpr int kKB = DK / M::kDepth;
+      typename M::Frag xi[2][4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) xi[0][m] = kt.rows(sm + Sm::kX, m, 0);
+      auto f = M::template split<kPS>(&S[0]);
+#pragma unroll
+      for (int kb = 0; kb < kKB; ++kb) {
+        __builtin_amdgcn_sched_barrier(0);
+        auto next = f;
+        if (kb + 1 < kKB) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) xi[(kb + 1) & 1][m] = kt.rows(sm + Sm::kX, m, kb + 1);
+          next = M::template split<kPS>(&S[(kb + 1) * M::kTiles]);
+        }
+#pragma unroll
+        for (int x = 0; x < kPS; ++x)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) o[m] = M::mma(f.p[x], xi[kb & 1][m], o[m]);
+        f = next;
       }
       __builtin_amdgcn_sched_barrier(0);
-      const int i = 16 * w + r;
-      const float hi = gt[i], lo = gt[kC + i];
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        if (m <= w) {
-          const f32x4 yh = *reinterpret_cast<const f32x4*>(gt + 16 * m + 4 * g),
-                      yl = *reinterpret_cast<const f32x4*>(gt + kC + 16 * m + 4 * g);
-          const f32x4 e = (hi - yh) + (lo - yl);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s[m][x] *= a.scale * exp_f32(e[x]);
-          if (m == w)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (4 * g + x > r) s[m][x] = 0.f;
-        }
-      __builtin_amdgcn_sched_barrier(0);
-      // (X S)^T, columns x tokens
-#pragma unroll
-      for (int kb = 0; kb < DK / M::kDepth; ++kb) {
-        const auto f = M::template split<kPS>(&S[kb * M::kTiles]);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const auto xi = kt.rows(sm + Sm::kX, m, kb);
-#pragma unroll
-          for (int x = 0; x < kPS; ++x) o[m] = M::mma(f.p[x], xi, o[m]);
-        }
-      }
+      load_x(next_chunk);
 #pragma unroll
       for (int m = 0; m < 4; ++m) o[m] *= gt[2 * kC + 16 * m + r];
+      __syncthreads();  // X has been read
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (j < tiles.pairs())
+#pragma unroll
+          for (int c = 0; c < 2; c += M::kTiles) {
+            const int kb = (tiles.y(j) + c) / M::kTiles, t = 16 * tiles.x(j);
+            if (t < kb * M::kDepth) continue;  // (fp32: a tile past the diagonal)
+            const auto f = M::template split<kPP>(&s[j][c]);
+#pragma unroll
+            for (int x = 0; x < kPP; ++x)
+              *reinterpret_cast<typename M::Frag*>(smem + Sm::kX + x * TT::kBytes + TT::word_at(kb, t + r, g)) = f.p[x];
+          }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    // S' = last S + Y^T diag(fy) Z
-    const float last = gt[4 * kC];
+    // S' = last S + Y^T diag(fy) Z, two accumulators at a time, operands a step ahead
+    {
+      const int l = opaque(lane), g = l >> 4;
+      const KT kt(l);
+      const VT vt(l, 16 * w);
+      const float last = gt[4 * kC];
 #pragma unroll
-    for (int m = 0; m < DK / 16; ++m) S[m] *= last;
+      for (int m = 0; m < DK / 16; ++m) S[m] *= last;
+      auto entering = [&](int kb) {
+        f32x4 e[M::kTiles];
 #pragma unroll
-    for (int kb = 0; kb < TT::kBlocks; ++kb) {
-      f32x4 e[M::kTiles];
+        for (int x = 0; x < M::kTiles; ++x)
+          e[x] = vt.tile(sz, kb * M::kTiles + x) *
+                 *reinterpret_cast<const f32x4*>(gt + 3 * kC + 16 * (kb * M::kTiles + x) + 4 * g);
+        return M::template split<kPE>(e);
+      };
+      typename M::Frag yc[2][2];
 #pragma unroll
-      for (int x = 0; x < M::kTiles; ++x)
-        e[x] = vt.tile(sz, kb * M::kTiles + x) *
-               *reinterpret_cast<const f32x4*>(gt + 3 * kC + 16 * (kb * M::kTiles + x) + 4 * g);
-      const auto es = M::template split<kPE>(e);
+      for (int c = 0; c < 2; ++c) yc[0][c] = kt.cols(sy, c, 0);
+      constexpr int kPairs = DK / 32;
+      auto es = entering(0);
 #pragma unroll
-      for (int m = 0; m < DK / 16; ++m) {
-        const auto yc = kt.cols(sy, m, kb);
+      for (int kb = 0; kb < TT::kBlocks; ++kb) {
+        auto next = es;
 #pragma unroll
-        for (int x = 0; x < kPE; ++x) S[m] = M::mma(yc, es.p[x], S[m]);
+        for (int m = 0; m < kPairs; ++m) {
+          const int step = kb * kPairs + m, now = step & 1;
+          __builtin_amdgcn_sched_barrier(0);
+          if (step + 1 < TT::kBlocks * kPairs)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              yc[now ^ 1][c] = kt.cols(sy, 2 * ((step + 1) % kPairs) + c, (step + 1) / kPairs);
+          if (m == kPairs - 2 && kb + 1 < TT::kBlocks) next = entering(kb + 1);
+#pragma unroll
+          for (int x = 0; x < kPE; ++x)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) S[2 * m + c] = M::mma(yc[now][c], es.p[x], S[2 * m + c]);
+        }
+        es = next;
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if (w == 0 && it + 1 < count) put_gates(next_gate, (int)((it + 1) & 1));
+    if (!kO && w == 0 && it + 1 < count) put_gates(next_gate, (int)((it + 1) & 1));
     if constexpr (kO) {
-      __syncthreads();  // X and Y have been read
-      char* const psm = smem + Sm::kX;
-#pragma unroll
-      for (int kb = 0; kb < TT::kBlocks; ++kb)
-        if (16 * w >= kb * M::kDepth) {
-          const auto f = M::template split<kPP>(&s[kb * M::kTiles]);
-#pragma unroll
-          for (int x = 0; x < kPP; ++x)
-            *reinterpret_cast<typename M::Frag*>(psm + x * TT::kBytes + TT::word_at(kb, 16 * w + r, g)) = f.p[x];
-        }
-      if (it + 1 < count) cy.put(smem + Sm::kY, w, lane, next_y);
-      __syncthreads();  // the triangular matrix is whole
-      const lds_ptr pm = (lds_ptr)psm;
+      __syncthreads();  // Y has been read and the triangular matrix is whole
+      const int l = opaque(lane), g = l >> 4, r = l & 15;
+      const TT tt(l);
+      const VT vt(l, 16 * w);
+      const lds_ptr pm = sm + Sm::kX;
 #pragma unroll
       for (int kb = 0; kb < TT::kBlocks; ++kb) {
         const auto z = vt.operand(sz, kb);
@@ -423,11 +498,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
           for (int m = kb * M::kTiles; m < 4; ++m)
             o[m] = M::mma(z, tt.rows(pm + x * TT::kBytes, m, kb), o[m]);
       }
+      cy.put(smem + Sm::kY, w, lane, next_y);
       __syncthreads();  // the triangular matrix and Z have been read
       // the output in Z's place, from where whole rows are stored behind the next barrier
 #pragma unroll
       for (int m = 0; m < 4; ++m) put_out<E>(smem + Sm::kZ + st * Sm::kZBytes, 16 * m + r, 16 * w + 4 * g, o[m]);
-      if (it + 1 < count) cx.put(smem + Sm::kX, w, lane, next_x);
+      cx.put(smem + Sm::kX, w, lane, next_x);
     }
   }
   if (kO && count > 0) {
@@ -439,12 +515,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
                    : a.last && (kRev ? first == 0 : end == nchunks) ? a.last + s_at : nullptr;
   if (to) {
     const auto buf = state_resource(to);
+    const int l = opaque(lane);
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const float v = S[m][x];
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), buf, (int)state_at(m, x), 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), buf, (int)state_at(l, m, x), 0, 0);
       }
   }
 }

@@ -65,13 +65,6 @@ struct GradSmem {
   static_assert(2 * kBytes <= 160 * 1024, "two workgroups per CU");
 };
 
-// The same value, but as a new one for the compiler: addresses made from it are made again for each head, not held
-// in registers through the loop over heads.
-__device__ __forceinline__ int opaque(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
-
 // A thread's share of 32 columns of a state's image: words of 16 bytes of an operand, on their way in registers.
 template <typename E, int DK, int kThreads>
 struct StateRows {
