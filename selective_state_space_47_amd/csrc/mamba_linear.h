@@ -173,14 +173,14 @@ __device__ __forceinline__ void put_out(char* lds, int row, int col, f32x4 v) {
 // Below -200 exp is 0 in fp32; the clamp keeps -inf (a reset) out of differences and lets NaN through.
 __device__ __forceinline__ float clamp_gate(float g) { return g < -200.f ? -200.f : g; }
 
-// Which tiles (y, x) of the triangular matrix a wave makes: pairs of neighbouring y, as an operand holds them, one pair
-// for the waves 0 and 3 and two for the others (a row of tiles per wave would be two pairs for the last, on the way of
-// all, and nothing to do for the first).
+// Which tiles (y, x) of the triangular matrix a wave makes: pairs of neighbouring y, as an operand holds them, two for
+// each wave but the first, which has the gates (their 64 lines take it 2000 cycles to ask for: with a row of tiles per
+// wave all waited for it).
 struct WaveTiles {
   int w;
-  __device__ __forceinline__ int pairs() const { return w == 1 || w == 2 ? 2 : 1; }
-  __device__ __forceinline__ int x(int pair) const { return w == 1 ? pair : w == 2 ? 2 : 3; }
-  __device__ __forceinline__ int y(int pair) const { return w == 2 ? 2 * pair : w == 3 ? 2 : 0; }
+  __device__ __forceinline__ int pairs() const { return w ? 2 : 0; }
+  __device__ __forceinline__ int x(int pair) const { return w == 1 ? pair : w; }
+  __device__ __forceinline__ int y(int pair) const { return w == 1 ? 0 : 2 * pair; }
 };
 
 // Rounding, bf16 storage: z times its factor enters the state as three bf16 parts (24 bits); the state and the
@@ -397,8 +397,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
         }
         __builtin_amdgcn_sched_barrier(0);
       };
-      make_pair(0);
-      if (tiles.pairs() == 2) make_pair(1);
+      if (tiles.pairs()) {
+        make_pair(0);
+        make_pair(1);
+      }
       __builtin_amdgcn_sched_barrier(0);
       load_y(next_chunk);
       if (w == 0 && it + 1 < count) put_gates(next_gate, (int)((it + 1) & 1));
