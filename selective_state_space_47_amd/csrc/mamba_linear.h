@@ -561,7 +561,7 @@ inline int64_t plan_segments(const mamba_delta_dims* d, bool packed) {
   };
   double best = 0.95 * pass(longest, nseq);
   int64_t chunks = 0;
-  for (int64_t c = 4; (double)c * 2.0 <= longest; c += c < 32 ? 2 : c / 16 * 2) {
+  for (int64_t c = 2; (double)c * 2.0 <= longest; c += c < 32 ? 2 : c / 16 * 2) {
     const double segments = packed ? tokens / (kC * (double)c) + nseq : std::ceil(longest / (double)c) * nseq;
     const double states = segments * (double)d->v_heads * (double)(d->dk * d->dv) * 8.0 / 5e6;
     const double time = 1.45 * pass((double)c, segments) + states + 15.0;

@@ -505,7 +505,7 @@ __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_ke
   }
 }
 
-// dq (y = 0) and dk (y = 1) of 64 tokens of a sequence: the groups' sums in order
+// dq (y = 0) and dk (y = 1) of 64 tokens of a sequence, in pieces (z): the groups' sums in order
 template <typename E>
 __global__ __launch_bounds__(256) void linear_fold_kernel(GradArgs b) {
   const Args& a = b.f;
@@ -517,7 +517,7 @@ __global__ __launch_bounds__(256) void linear_fold_kernel(GradArgs b) {
   const int64_t first = (sp.first + c0) * row, count = min((int64_t)kC, sp.len - c0) * row;
   const float* part = b.part + (blockIdx.y ? (int64_t)b.groups * size : 0) + first;
   E* out = static_cast<E*>(blockIdx.y ? b.dk : b.dq) + first;
-  for (int64_t x = threadIdx.x * 4; x < count; x += 1024) {
+  for (int64_t x = (blockIdx.z * 256 + threadIdx.x) * 4; x < count; x += gridDim.z * 1024) {
     f32x4 s = *reinterpret_cast<const f32x4*>(part + x);
 #pragma unroll 4
     for (int y = 1; y < b.groups; ++y) s += *reinterpret_cast<const f32x4*>(part + y * size + x);
@@ -584,7 +584,8 @@ int launch_bwd(const PassArgs& fwd, const PassArgs& rev, const GradArgs& b, int6
   if ((st = launch_pass<E, kImages | kDots>(fwd, s)) != MAMBA_OK) return st;
   st = b.f.dk <= 64 ? launch_grad<E, 64>(b, units, s) : launch_grad<E, 128>(b, units, s);
   if (st != MAMBA_OK || b.groups == 1) return st;
-  hipLaunchKernelGGL((linear_fold_kernel<E>), dim3((unsigned)b.f.slots, 2), dim3(256), 0, s, b);
+  const int64_t pieces = std::min<int64_t>((kC * (int64_t)b.f.hk * b.f.dk + 4095) / 4096, 256);
+  hipLaunchKernelGGL((linear_fold_kernel<E>), dim3((unsigned)b.f.slots, 2, (unsigned)pieces), dim3(256), 0, s, b);
   return launch_status();
 }
 
