@@ -68,8 +68,8 @@ struct Smem {
   static constexpr int kTri = Mma<E>::parts(2) * TriTile<E>::kBytes;
   static constexpr int kXBytes = kO ? (kYBytes > kTri ? kYBytes : kTri) : kYBytes;  // (no output: the second Y)
   static constexpr int kY = 0, kX = kYBytes, kZ = kX + kXBytes, kZBytes = ValueTile<E, kCols>::kBytes;
-  // gates of two chunks: G as two floats, fx, fy (64 each), last
-  static constexpr int kGateFloats = 4 * kC + 4;
+  // gates of two chunks: G as two floats, fx, fy, exp(G at the end of the token's tile - G) (64 each), last
+  static constexpr int kGateFloats = 5 * kC + 4;
   static constexpr int kGate = kZ + 2 * kZBytes;
   static constexpr int kBytes = kGate + 2 * kGateFloats * 4;
   static_assert(sizeof(E) == 4 || 3 * kBytes <= 160 * 1024, "three workgroups per CU");
@@ -299,7 +299,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
     to[kC + x] = kRev ? -lo : lo;
     to[2 * kC + x] = kRev ? c : eg;
     to[3 * kC + x] = kRev ? eg : c;
-    if (lane == 0) to[4 * kC] = exp_f32((float)total);
+    const double tile_end = dpp_or_zero<kRev ? 0x150 : 0x15f, 0xf>(G);  // lane 0 or 15 of the row of 16
+    to[4 * kC + x] = exp_f32((float)(kRev ? G - tile_end : tile_end - G));
+    if (lane == 0) to[5 * kC] = exp_f32((float)total);
     all += total;
   };
 
@@ -383,16 +385,22 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
 #pragma unroll
           for (int c = 0; c < 2; ++c) s[j][c] = M::mma(kt.rows(sy, ty + c, kb), f, s[j][c]);
         }
+        // scale D: of a tile before x's, factors of x and y on both sides of the tile's end; of x's own one by one
         const int i = 16 * tx + r;
         const float hi = gt[i], lo = gt[kC + i];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int t = 16 * (ty + c) + 4 * g;
-          const f32x4 e = (hi - *reinterpret_cast<const f32x4*>(gt + t)) + (lo - *reinterpret_cast<const f32x4*>(gt + kC + t));
+          const int t = 16 * (ty + c) + 4 * g, end = 16 * (ty + c) + 15;
+          if (ty + c < tx) {
+            const float f = a.scale * exp_f32((hi - gt[end]) + (lo - gt[kC + end]));
+            s[j][c] *= *reinterpret_cast<const f32x4*>(gt + 4 * kC + t) * f;
+          } else {
+            const f32x4 e = (hi - *reinterpret_cast<const f32x4*>(gt + t)) + (lo - *reinterpret_cast<const f32x4*>(gt + kC + t));
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float v = s[j][c][x] * (a.scale * exp_f32(min(e[x], 0.f)));
-            s[j][c][x] = t + x <= i ? v : 0.f;
+            for (int x = 0; x < 4; ++x) {
+              const float v = s[j][c][x] * (a.scale * exp_f32(e[x]));
+              s[j][c][x] = t + x <= i ? v : 0.f;
+            }
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -448,7 +456,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
       const int l = opaque(lane), g = l >> 4;
       const KT kt(l);
       const VT vt(l, 16 * w);
-      const float last = gt[4 * kC];
+      const float last = gt[5 * kC];
 #pragma unroll
       for (int m = 0; m < DK / 16; ++m) S[m] *= last;
       auto entering = [&](int kb) {
