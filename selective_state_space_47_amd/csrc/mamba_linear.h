@@ -38,6 +38,8 @@ struct PassArgs {
   Args f;              // q, k, v, out in the pass's roles (backwards: k, q, dout, dv); offsets, s0 and last
   const float* gate;   // (tokens, hv)
   float* seg_decay;    // (segment slots, hv): what a segment leaves of the state before it
+  int32_t group;       // workgroups that stay together on an XCD
+  int64_t seg_limit;   // sequences of up to so many chunks go through whole, in the place of their first segment
   float* img;          // states before (backwards: after) every kUnit tokens: see image_at
   int64_t img_item;    // floats of one unit and value head
   const float* other;  // kDots: the images of the other direction
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
   if (id >= blocks) return;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wg = spread_index(id, blocks, a.rep * col_blocks);
+  const int64_t wg = spread_index(id, blocks, p.group);
   const int64_t sh = wg / col_blocks;
   const int64_t seg_slot = sh / a.hv;
   const int vh = (int)(sh - seg_slot * a.hv), kh = vh / a.rep;
@@ -211,8 +213,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
   const Span sp = seq_span(a, seq);
   const int64_t seg = a.seg_chunks ? seg_slot - slot_base(a, seq, sp.first, unit) : 0;
   const int64_t nchunks = (sp.len + kC - 1) / kC;
-  const int64_t first = seg * a.seg_chunks;
-  const int64_t end = a.seg_chunks ? min(first + a.seg_chunks, nchunks) : nchunks;
+  const bool cut = a.seg_chunks && nchunks > p.seg_limit;
+  const int64_t first = seg * (cut ? a.seg_chunks : nchunks);
+  const int64_t end = cut ? min(first + a.seg_chunks, nchunks) : nchunks;
   if (seg < 0 || (first >= end && seg > 0)) return;  // an unused slot of a packed batch
   if (kSum && (kRev ? first == 0 : end == nchunks)) return;  // no segment follows
   const int col0 = (int)(wg - sh * col_blocks) * kCols;  // this workgroup's first column
@@ -226,7 +229,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
   E* op = static_cast<E*>(a.out) + sp.first * o_stride + (int64_t)vh * a.dv + col0;
   const int64_t s_at = (seq * a.hv + vh) * (int64_t)a.dk * a.dv;
   const int64_t g_at = (seg_slot * a.hv + vh) * (int64_t)a.dk * a.dv;
-  const float* from = kSum ? nullptr : a.seg_chunks ? a.seg_state + g_at : a.s0 ? a.s0 + s_at : nullptr;
+  const float* from = kSum ? nullptr : cut ? a.seg_state + g_at : a.s0 ? a.s0 + s_at : nullptr;
 
   // row 4 g + x of accumulator m and column col + r of a (dk, dv) matrix, past its end if there is none
   auto state_at = [&](int l, int m, int x) {
@@ -537,8 +540,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
 }
 
 template <typename E, int DK, int kWhat>
-int launch_pass_t(const PassArgs& p, hipStream_t s) {
+int launch_pass_t(PassArgs p, hipStream_t s) {
   const int cols = (p.f.dv + kCols - 1) / kCols;
+  // Workgroups that read the same keys share an XCD's L2, up to 8 of them: with all 80 heads of a key head in one place
+  // the slots that no sequence of a packed batch uses left XCDs without work (64 sequences of 300 tokens: 427 us).
+  p.group = 8;
+  while (p.f.rep * cols % p.group) --p.group;
   const uint32_t blocks = (uint32_t)(p.f.seg_slots * p.f.hv * cols);
   hipLaunchKernelGGL((linear_pass_kernel<E, DK, kWhat>), wide_grid(blocks, 256), dim3(256), 0, s, p, cols, blocks);
   return launch_status();
@@ -549,41 +556,46 @@ int launch_pass(const PassArgs& p, hipStream_t s) {
 }
 
 // Chunks per segment (even), 0 for whole sequences.  A chunk takes 6, 6.8 or 7.6 us where 1, 2 or 3 workgroups share a
-// CU (measured, bf16, dk = 128): a pass of equal sequences takes its rounds of three and the rest, one of a packed batch
-// the longer of its longest chain and its work, 12 ns a chunk, or, in segments, whose long ones do not begin first, a
-// chain behind half the work.  Segments cost a second pass that leaves only states,
-// under half the time, the states' way through memory (twice, 5 TB/s) and 15 us of launches.  Of a packed batch the
-// longest sequence is not known here: total / sqrt(sequences), between their mean and the total, is taken.  Measured
-// with and without: packed prompts of 1 to 4099 tokens, 8279 in all, 80 heads, 378 -> 238 us; 65536 tokens, 12 heads of
-// 128 x 128, 5.9 ms -> 319 us.
-inline int64_t plan_segments(const mamba_delta_dims* d, bool packed) {
-  const double nseq = (double)(packed ? std::min(d->batch, d->seqlen) : d->batch), tokens = (double)d->seqlen;
-  if (nseq < 1.0) return 0;
-  const double longest = std::ceil((packed ? tokens / std::sqrt(nseq) : tokens) / kC);
+// CU and 12 ns of a full GPU (measured, bf16, dk = 128).  Segments cost a second pass that leaves only states, under half
+// the time, the states' way through memory (twice, 5 TB/s) and 15 us of launches.
+//   Equal sequences: the time of the pass in its rounds of three workgroups per CU, with and without.
+//   Packed ones, whose lengths are not known here: segments where one sequence of all tokens would take twice as long as
+//   all work, which costs the launches where no sequence is long, as those whose chain takes no longer than about the
+//   work (`limit` chunks) are not cut; the length for which a chain behind half the work and the states take least.
+// Measured with and without: 65536 tokens, 12 heads of 128 x 128, 5.9 ms -> 337 us; 2 x 333 tokens, 12 heads of 64 x 96,
+// fp32, 41 -> 28 us; packed, 80 heads of 128 x 64: 8279 tokens in 8 sequences of up to 4099, 378 -> 225 us, 15 of 500 and
+// one of 12000, 1045 -> 405 us, 64 of 300, 286 -> 262 us.
+struct SegPlan {
+  int64_t chunks, limit;
+};
+inline SegPlan plan_segments(const mamba_delta_dims* d, bool packed) {
+  const double nseq = (double)(packed ? std::min(d->batch, d->seqlen) : d->batch);
+  const double length = std::ceil((double)d->seqlen / kC);  // (packed: of a sequence of all tokens)
   const double heads = (double)d->v_heads * (double)((d->dv + kCols - 1) / kCols);
+  const double work = 0.012 * heads * (length + nseq);
   auto pass = [&](double c, double segments) {  // segments of c chunks
-    const double work = 0.012 * heads * (tokens / kC + nseq);
-    if (packed) return c < longest ? 7.6 * c + 0.5 * work : std::max(6.0 * c, work);
+    if (packed) return 7.6 * c + 0.5 * work;
     const int64_t k = (int64_t)std::ceil(segments * heads / 256.0);
     return c * (7.6 * (double)(k / 3) + (k % 3 ? 5.2 + 0.8 * (double)(k % 3) : 0.0));
   };
-  double best = 0.95 * pass(longest, nseq);
-  int64_t chunks = 0;
-  for (int64_t c = 2; (double)c * 2.0 <= longest; c += c < 32 ? 2 : c / 16 * 2) {
-    const double segments = packed ? tokens / (kC * (double)c) + nseq : std::ceil(longest / (double)c) * nseq;
+  double best = packed ? (6.0 * length > 2.0 * work ? 1e30 : 0.0) : 0.95 * pass(length, nseq);
+  SegPlan plan = {0, packed ? (int64_t)(work / 8.0) : 0};
+  for (int64_t c = 2; (double)c * 2.0 <= length; c += c < 32 ? 2 : c / 16 * 2) {
+    const double segments = packed ? length / (double)c + nseq : std::ceil(length / (double)c) * nseq;
     const double states = segments * (double)d->v_heads * (double)(d->dk * d->dv) * 8.0 / 5e6;
     const double time = 1.45 * pass((double)c, segments) + states + 15.0;
-    if (time < best) best = time, chunks = c;
+    if (time < best) best = time, plan.chunks = c;
   }
-  return chunks;
+  return plan;
 }
 
 struct SegLayout {  // workspace regions in bytes
-  int64_t chunks, slots;
+  int64_t chunks, limit, slots;
   size_t decay, total;
 };
 inline SegLayout seg_layout(const mamba_delta_dims* d, bool packed) {
-  SegLayout l = {plan_segments(d, packed), d->batch, 0, 0};
+  const SegPlan plan = plan_segments(d, packed);
+  SegLayout l = {plan.chunks, plan.limit, d->batch, 0, 0};
   if (l.chunks) {
     l.slots = slots_of(d, packed, l.chunks * kC);
     const size_t heads = (size_t)l.slots * (size_t)d->v_heads;
@@ -595,6 +607,7 @@ inline SegLayout seg_layout(const mamba_delta_dims* d, bool packed) {
 // The pass's arguments for these segments in a workspace that begins at ws.
 inline void set_segments(PassArgs& p, const SegLayout& l, char* ws) {
   p.f.seg_chunks = l.chunks;
+  p.seg_limit = l.limit;
   p.f.seg_slots = l.slots;
   p.f.seg_state = reinterpret_cast<float*>(ws);
   p.seg_decay = reinterpret_cast<float*>(ws + l.decay);

@@ -11,8 +11,8 @@ namespace linear {
 namespace {
 
 // The states that the segments begin with, one after another: S <- decay S + (the segment's own); seg_state holds each
-// segment's own on entry.  The first one's (of sequences without tokens, too) is a copy of the initial state: the
-// output pass reads only these, as it may write the last state over the initial one.
+// segment's own on entry.  The first one's is a copy of the initial state: the output pass reads only these, as it may
+// write the last state over the initial one.
 template <bool kRev>
 __global__ __launch_bounds__(256) void linear_join_kernel(PassArgs p, int32_t blocks) {
   const Args& a = p.f;
@@ -23,7 +23,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(PassArgs p, int32_t bl
   if (at >= size) return;
   const int64_t unit = a.seg_chunks * kC;
   const Span sp = seq_span(a, seq);
-  const int64_t base = slot_base(a, seq, sp.first, unit), nseg = max((sp.len + unit - 1) / unit, (int64_t)1);
+  const int64_t base = slot_base(a, seq, sp.first, unit), nseg = (sp.len + unit - 1) / unit;
+  if ((sp.len + kC - 1) / kC <= p.seg_limit) return;  // goes through whole, from the initial state itself
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (a.s0) S = *reinterpret_cast<const f32x4*>(a.s0 + (seq * a.hv + vh) * size + at);
   constexpr int kAhead = 4;  // segments on their way

@@ -116,7 +116,7 @@ __device__ __forceinline__ V across_groups(V v) {
 // Per value head first the pairs of tokens (tiles of dO V^T, columns = a wave's own 32 tokens, which both sides make in
 // their own orientation: no wave needs another's), then the state's terms.
 template <typename E, int DK, bool kKeys>
-__global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), 2) void linear_grad_kernel(GradArgs b, uint32_t blocks) {
+__global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), sizeof(E) == 2 || DK == 64 ? 2 : 1) void linear_grad_kernel(GradArgs b, uint32_t blocks) {
   using M = Mma<E>;
   using Sm = GradSmem<E, DK>;
   using KT = typename Sm::KT;
