@@ -158,6 +158,29 @@ def test_packed(lengths, io):
             assert torch.equal(last[s], t["state"][s])
 
 
+# 40 heads, 21 chunks: sequences of more than one chunk are cut, the others go through whole
+CUT = [600, 64, 0, 1, 129, 486, 20]
+
+
+@IO
+def test_packed_partly_cut(io):
+    """A packed batch whose long sequences go through in segments and whose short ones do not; the last states are
+    written over the first."""
+    x, t, off, one, total = packed_case(CUT, io, Hk=2, Hv=40, dk=24, dv=16)
+    code = binding.MAMBA_BF16 if io == BF else binding.MAMBA_F32
+    dims = binding.mamba_delta_dims(len(CUT), total, 2, 40, 24, 16, 0, 0, 0, code, 0)
+    assert binding.mamba_linear_attn_workspace_bytes(dims, True) > 0
+    print(f"[linear partly cut] {io}", flush=True)
+    state = t["state"].clone()
+    out = torch.full((total, 40, 16), 7.0, device=DEV, dtype=io)
+    out, last = run_fwd(t, initial_state=state, last_state=state, seq_offsets=off, out=out)
+    assert last is state and bool((out[:3] == 7.0).all())
+    refs = [ref_fwd(one(s), 24 ** -0.5, x["state"][s:s + 1]) for s in range(len(CUT))]
+    check(out[3:], np.concatenate([r[0][0] for r in refs]), "out", io)
+    check(last, np.concatenate([r[1] for r in refs]), "last_state", io, wide=True)
+    assert torch.equal(last[2], t["state"][2])
+
+
 @IO
 @pytest.mark.parametrize("shape", [(1, 4133, 1, 2, 64, 64), (2, 2600, 1, 1, 40, 136), (1, 4096, 1, 1, 128, 72)],
                          ids=ids)
