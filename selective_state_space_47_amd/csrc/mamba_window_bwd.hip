@@ -17,7 +17,10 @@
 // would carry 2^-9 of dO . out into dS, which is the small difference of two numbers of that size where a few keys have
 // all the weight (4 keys, scores of deviation 3.4: dq was off by 5.4e-3).
 //
-// Rounding, bf16 storage: P and dS enter their products as one bf16 part each; the rest is fp32.
+// Rounding, bf16 storage: P enters its product as one bf16 part, which weighs as much in dV as its own rounding, and dS as
+// two: a row of dS sums to zero, and with one part dK and dQ were off by up to 1.48 times their own
+// rounding (8 x 2048 tokens, 20 and 4 heads of 128: the second part costs 103 of 938 us, one of P
+// would cost 25).  The rest is fp32.
 #include "mamba_window.h"
 
 namespace mamba {
@@ -62,8 +65,8 @@ __global__ __launch_bounds__(256) void window_stat_kernel(WinArgs a, int64_t tok
 
 // What a wave of the keys' pass makes: dV (from P), or dK (from P and dO V^T).  Two waves share 32 keys (fp32 storage:
 // 16): with both sums in one wave there is room for one wave on a SIMD, which has nobody to hide its waits behind.
-// (8 x 2048 tokens, 20 and 4 heads of 128, window 1024: 395 us; both sums in one wave and 128 keys per workgroup 491,
-// by roles with 128 keys 503, as the longest workgroups then ran alone at the end.)
+// (8 x 2048 tokens, 20 and 4 heads of 128, window 1024, dS in one part: 395 us; both sums in one wave and 128 keys per
+// workgroup 491, by roles with 128 keys 503, as the longest workgroups then ran alone at the end.  With dS in two: 460.)
 enum Role { kMakeDv, kMakeDk };
 
 // The queries' tiles of a workgroup of the keys' pass
@@ -169,22 +172,25 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
 #pragma unroll
           for (int c = 0; c < kC2; ++c) s[c][m] = s[c][m] * (e[c][m] - ds);
         }
-      typename M::Frag pf[kC2];
+      constexpr int kP = kRole == kMakeDv ? 1 : M::parts(2);
+      typename M::template Parts<kP> pf[kC2];
 #pragma unroll
       for (int i = 0; i < kStepsV; ++i) {
         if (i % kGroups == 0)
 #pragma unroll
-          for (int c = 0; c < kC2; ++c) pf[c] = M::pack(&s[c][i / kGroups * M::kTiles]);
+          for (int c = 0; c < kC2; ++c) pf[c] = M::template split<kP>(&s[c][i / kGroups * M::kTiles]);
         end_step();
         if (i + 1 < kStepsV) read_v(i + 1);
         end_step();
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int p = 0; p < kP; ++p)
 #pragma unroll
-          for (int c = 0; c < kC2; ++c) {
-            f32x4& to = acc[c][i % kGroups * 4 + x];
-            to = M::mma(f[(i + kStepsK) & 1][x], pf[c], to);
-          }
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int c = 0; c < kC2; ++c) {
+              f32x4& to = acc[c][i % kGroups * 4 + x];
+              to = M::mma(f[(i + kStepsK) & 1][x], pf[c].p[p], to);
+            }
       }
       end_step();
     }
@@ -508,22 +514,25 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 #pragma unroll
         for (int m = 0; m < 2; ++m)
           e[c][m] = s[c][m] * (e[c][m] - ds[c]);
-      typename M::Frag ef[kC2];
+      constexpr int kP = M::parts(2);
+      typename M::template Parts<kP> ef[kC2];
 #pragma unroll
       for (int i = 0; i < kStepsV; ++i) {
         if (i % kGroups == 0)
 #pragma unroll
-          for (int c = 0; c < kC2; ++c) ef[c] = M::pack(&e[c][i / kGroups * M::kTiles]);
+          for (int c = 0; c < kC2; ++c) ef[c] = M::template split<kP>(&e[c][i / kGroups * M::kTiles]);
         end_step();
         if (i + 1 < kStepsV) read_cols(sk, half, i + 1);
         end_step();
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int p = 0; p < kP; ++p)
 #pragma unroll
-          for (int c = 0; c < kC2; ++c) {
-            f32x4& to = dq[c][i % kGroups * 4 + x];
-            to = M::mma(f[i & 1][x], ef[c], to);
-          }
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int c = 0; c < kC2; ++c) {
+              f32x4& to = dq[c][i % kGroups * 4 + x];
+              to = M::mma(f[i & 1][x], ef[c].p[p], to);
+            }
       }
       end_step();
     }
