@@ -15,7 +15,13 @@
 //
 // One workgroup per sequence (or segment of one), value head and 64 columns of the state: four waves of 16 columns,
 // whose state stays in accumulators from the first chunk to the last.  The accumulators of one product are the next
-// one's operand, so that only the triangular matrix, a quarter of it made by each wave, goes through LDS.
+// one's operand, so that only the triangular matrix, which the waves share out, and the output, which is stored in whole
+// rows, go through LDS.
+//
+// Measured (8 x 2048 tokens, 20 key and 40 value heads of 128, bf16): forward 224 us (2.1 TB/s; its bytes at a copy's rate
+// 105), backwards with images 256, forwards with images and their products 212 (4.4 TB/s).  With an output the vector
+// unit is busy 60% and the matrix unit 34% of the time, and on this target the two add up: the state's and the entering
+// values' conversions to bf16 parts are most of it.  A chunk takes a workgroup that is alone on its CU 9500 cycles.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -187,6 +193,10 @@ struct WaveTiles {
 
 // Rounding, bf16 storage: z times its factor enters the state as three bf16 parts (24 bits); the state and the
 // triangular matrix enter the output as two parts each, so that its own rounding is the only one that shows.
+// A chunk: X's products, then its place is the triangular matrix's; the state, while that matrix is written; its
+// product; the output.  Three workgroups share a CU, whose LDS has no room for a second stage of X and Y: they wait in
+// registers, 32 of 168.  Operands are read a step ahead of their products, with barriers for the scheduler, which
+// otherwise spilled, and addresses are made again in each chunk.
 template <typename E, int DK, int kWhat>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kernel(
     PassArgs p, int32_t col_blocks, uint32_t blocks) {
@@ -562,9 +572,9 @@ int launch_pass(const PassArgs& p, hipStream_t s) {
 //   Packed ones, whose lengths are not known here: segments where one sequence of all tokens would take twice as long as
 //   all work, which costs the launches where no sequence is long, as those whose chain takes no longer than about the
 //   work (`limit` chunks) are not cut; the length for which a chain behind half the work and the states take least.
-// Measured with and without: 65536 tokens, 12 heads of 128 x 128, 5.9 ms -> 337 us; 2 x 333 tokens, 12 heads of 64 x 96,
-// fp32, 41 -> 28 us; packed, 80 heads of 128 x 64: 8279 tokens in 8 sequences of up to 4099, 378 -> 225 us, 15 of 500 and
-// one of 12000, 1045 -> 405 us, 64 of 300, 286 -> 262 us.
+// Measured without and with: 65536 tokens, 12 heads of 128 x 128, 5.9 ms and 328 us; 2 x 333 tokens, 12 heads of 64 x 96,
+// fp32, 41 and 28 us; packed, 80 heads of 128 x 64: 8279 tokens in 8 sequences of up to 4099, 378 and 196 us, 15 of 500
+// and one of 12000, 1045 and 334 us; 16 of 2048, 387 and 415 us, 64 of 300, 286 and 310 us.
 struct SegPlan {
   int64_t chunks, limit;
 };

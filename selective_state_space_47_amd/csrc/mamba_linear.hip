@@ -11,7 +11,7 @@ namespace linear {
 namespace {
 
 // The states that the segments begin with, one after another: S <- decay S + (the segment's own); seg_state holds each
-// segment's own on entry.  The first one's is a copy of the initial state: the output pass reads only these, as it may
+// segment's own on entry.  Bound by memory (packed prompts, 80 heads of 128 x 64: 28 us, 5.5 TB/s).  The first one's is a copy of the initial state: the output pass reads only these, as it may
 // write the last state over the initial one.
 template <bool kRev>
 __global__ __launch_bounds__(256) void linear_join_kernel(PassArgs p, int32_t blocks) {
@@ -66,7 +66,8 @@ struct StepArgs {
 };
 
 // One token of one value head and 32 columns: 8 lanes hold a row's float4s, 32 rows are held at a time, 4 per thread,
-// all of them loaded before the first is used.  Bound by the state's traffic (read and written once, fp32).
+// all of them loaded before the first is used.  Bound by the state's traffic, read and written once in fp32 (256
+// sequences, 80 heads of 128 x 64: 268 us, 5.0 TB/s, a copy's rate).
 template <typename E>
 __global__ __launch_bounds__(kStepThreads) void linear_step_kernel(StepArgs a, int32_t col_blocks) {
   constexpr int TC = 8, kStride = kStepThreads / TC, kRows = kMaxDk / kStride;

@@ -12,8 +12,13 @@
 //
 // Launches: linear_pass_kernel (mamba_linear.h) backwards leaves dV and the adjoints, forwards the states and <S, dS'>;
 // linear_grad_kernel first dK and the part of dg that comes from keys, then dQ and dg, a workgroup per unit and key
-// head, value heads added in accumulators in a fixed order.  Where units and key heads alone would leave CUs idle the value heads of a key head are split among
-// workgroups, whose fp32 sums linear_fold_kernel adds in order.  No atomics.
+// head, value heads added in accumulators in a fixed order.  Where units and key heads alone would leave CUs idle the
+// value heads of a key head are split among workgroups, whose fp32 sums linear_fold_kernel adds in order.  No atomics.
+//
+// Measured (8 x 2048 tokens, 20 and 40 heads of 128, bf16): dK 268 us at 4.2 TB/s, dQ and dg 331 at 4.0, bound by memory:
+// the states' images, 4 bytes a value, are a quarter of the bytes, V or dO comes in twice, as tiles and as a wave's own
+// operands.  Both sides in one kernel, with 154 KB of LDS and so one workgroup per CU, took 739.  Images of units of
+// 256 tokens would be half as large, for twice the pairs of tokens and tiles that do not fit two workgroups' LDS.
 #include "mamba_linear.h"
 
 namespace mamba {
@@ -113,7 +118,7 @@ __device__ __forceinline__ V across_groups(V v) {
   return v + __shfl_xor(v, 32);
 }
 
-// Per value head first the pairs of tokens (tiles of dO V^T, columns = a wave's own 32 tokens, which both sides make in
+// One side.  Per value head first the pairs of tokens (tiles of dO V^T, columns = a wave's own 32 tokens, which both sides make in
 // their own orientation: no wave needs another's), then the state's terms.
 template <typename E, int DK, bool kKeys>
 __global__ __launch_bounds__((GradSmem<E, DK>::kNW * 64), sizeof(E) == 2 || DK == 64 ? 2 : 1) void linear_grad_kernel(GradArgs b, uint32_t blocks) {

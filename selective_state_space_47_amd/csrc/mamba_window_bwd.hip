@@ -199,7 +199,8 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
 }
 
 // kFarPart: 16 sinks and one query head over a stretch of queries past the sinks' windows; otherwise a tile of keys, the
-// heads that share it one after another.
+// heads that share it one after another.  (Far part of 4 sinks and 8 x 2048 tokens: 27 us; with the sinks' tile as one
+// workgroup's work it was 564.)
 template <typename E, int DK, bool kFarPart>
 __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(WinArgs a, uint32_t blocks, int64_t tokens) {
   using M = Mma<E>;
@@ -351,6 +352,8 @@ __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeo
   }
 }
 
+// 8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16: 417 us for seven products per pair of tiles (S and dO V^T
+// twice, dS K in two parts and the queries' exponentials twice).
 template <typename E, int DK>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(WinArgs a, uint32_t blocks,
                                                                                 int64_t tokens) {

@@ -34,7 +34,8 @@ struct StepArgs {
 // operands, values straight into the wave's LDS, both of a whole tile at once; the waves are joined at the end.
 // Bound by the caches' traffic (read once).  The new key and value are taken from the inputs and written to their slot
 // by the wave that comes to it: nobody reads that slot.  With bf16 storage the weights enter the product with V as two
-// bf16 parts (2^-17 of each), so that the output's rounding is the only one that shows.
+// bf16 parts (2^-17 of each), so that the output's rounding is the only one that shows.  256 sequences, 20 and 4 heads of
+// 128, 1024 + 4 slots, bf16: 100 us, 4.7 TB/s, a copy's rate (heads one after another on the vector unit: 221).
 template <typename E, int DK>
 __global__ __launch_bounds__(kStepThreads, 2) void window_step_kernel(StepArgs a, uint32_t blocks) {
   using M = Mma<E>;
