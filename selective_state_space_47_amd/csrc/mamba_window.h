@@ -29,8 +29,11 @@ struct WinArgs {
   int64_t seqlen, kv_len, nseq;
   int64_t q_stride, k_stride, v_stride;
   int64_t window, sinks;
+  float* part;                // (2, groups, kv tokens, hk, dim): dv and dk where a key head's heads are split
   int64_t far_slots;
   int32_t hq, hk, rep, dim, sink_tiles;
+  int32_t far_len;            // queries of a stretch
+  int32_t groups;             // workgroups that share a key head's heads
   float scale;
 };
 

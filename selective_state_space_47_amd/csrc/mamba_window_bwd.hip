@@ -34,7 +34,7 @@ constexpr int kRows = 4 * 16 * kTilesW<E>;       // of a workgroup
 constexpr int kPairs = 2;                        // pairs of waves that share the keys of a workgroup of the keys' pass
 template <typename E>
 constexpr int kKeyRows = kPairs * 16 * kTilesW<E>;
-constexpr int kFar = 512;                        // queries of a stretch past the sinks' windows
+constexpr int kFar = 512;                        // queries of a stretch past the sinks' windows, at most
 
 // 8 lanes per row; a row without a key has weights of zero: its log-sum counts as +infinity
 template <typename E>
@@ -198,6 +198,11 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
   }
 }
 
+// floats of dk or dv
+__device__ __forceinline__ int64_t part_floats(const WinArgs& a) {
+  return (a.kv_offsets ? 1 : a.nseq) * a.kv_len * (int64_t)a.hk * a.dim;
+}
+
 // kFarPart: 16 sinks and one query head over a stretch of queries past the sinks' windows; otherwise a tile of keys, the
 // heads that share it one after another.  (Far part of 4 sinks and 8 x 2048 tokens: 27 us; with the sinks' tile as one
 // workgroup's work it was 564.)
@@ -221,18 +226,19 @@ __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeo
     kh = h / a.rep;
     h0 = h - kh * a.rep;
     heads = 1;
-    seq = tile_seq(a.q_offsets, a.seqlen, a.nseq, far_slot, kFar);
+    seq = tile_seq(a.q_offsets, a.seqlen, a.nseq, far_slot, a.far_len);
   } else {
-    const int64_t slot = id / (uint32_t)a.hk;
-    kh = (int)(id - slot * a.hk);
-    h0 = 0;
-    heads = a.rep;
+    const uint32_t rest = id / (uint32_t)a.groups, per = (uint32_t)((a.rep + a.groups - 1) / a.groups);
+    const int64_t slot = rest / (uint32_t)a.hk;
+    kh = (int)(rest - slot * a.hk);
+    h0 = (int)((id - rest * (uint32_t)a.groups) * per);
+    heads = min((int)per, a.rep - h0);
     const Tile t = tile_of<false>(a.kv_offsets, a.kv_len, a.nseq, slot, kN);
     seq = t.seq;
     tile = t.tile;
   }
   const Seq qs = seq_of(a.q_offsets, a.seqlen, seq), ks = seq_of(a.kv_offsets, a.kv_len, seq);
-  if (kFarPart) stretch = far_slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
+  if (kFarPart) stretch = far_slot - tile_base(a.q_offsets, a.seqlen, seq, qs.first, a.far_len);
   if (tile < 0 || tile * kN >= ks.len || stretch < 0) return;
   const int j0 = (int)tile * kN, nk = min(ks.len - j0, kN);
   const Mask mask = mask_of(a);
@@ -246,9 +252,9 @@ __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeo
     return max(min(last + a.window - k.shift, (int64_t)qs.len), max(t * kKeyRows<E> - k.shift, (int64_t)0));
   };
   if (kFarPart) {
-    const int64_t b = near(j0 / kKeyRows<E>) + stretch * kFar;
+    const int64_t b = near(j0 / kKeyRows<E>) + stretch * a.far_len;
     k.q_lo = (int)min(b, (int64_t)qs.len);
-    k.q_hi = (int)min(b + kFar, (int64_t)qs.len);
+    k.q_hi = (int)min(b + a.far_len, (int64_t)qs.len);
     if (k.q_lo >= k.q_hi) return;
   } else {
     k.q_lo = max(j0 - k.shift, 0);
@@ -322,18 +328,19 @@ __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeo
     }
     return;
   }
-  const int64_t first = near(tile), stretches = first < qs.len ? (qs.len - first + kFar - 1) / kFar : 0;
-  const int64_t far_base = tile_base(a.q_offsets, a.seqlen, seq, qs.first, kFar);
+  const int64_t first = near(tile), stretches = first < qs.len ? (qs.len - first + a.far_len - 1) / a.far_len : 0;
+  const int64_t far_base = tile_base(a.q_offsets, a.seqlen, seq, qs.first, a.far_len);
   E* const out = static_cast<E*>(makes_dk ? a.dk : a.dv);
   const float scale = makes_dk ? a.scale : 1.f;
+  const int64_t part_size = part_floats(a);
 #pragma unroll
   for (int c = 0; c < kC2; ++c) {
     const int j = w0 + 16 * c + r;
     const int64_t t16 = (j0 + w0) / 16 + c;  // these 16 keys among the sinks' tiles
     if (t16 < a.sink_tiles && j < nk)
       for (int64_t x = 0; x < stretches; ++x)
-        for (int h = 0; h < a.rep; ++h) {
-          const float* from = far_at(far_base + x, kh * a.rep + h, t16);
+        for (int h = 0; h < heads; ++h) {
+          const float* from = far_at(far_base + x, hq0 + h, t16);
 #pragma unroll
           for (int d = 0; d < DK / 16; ++d) {
             const int v = KT::value(d, g, 0);
@@ -344,11 +351,40 @@ __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeo
     const int64_t at = ((ks.first + j0 + j) * a.hk + kh) * (int64_t)a.dim;
 #pragma unroll
     for (int d = 0; d < DK / 16; ++d) acc[c][d] *= scale;
+    if (a.groups > 1) {
+      float* to = a.part + ((makes_dk ? a.groups : 0) + h0 / ((a.rep + a.groups - 1) / a.groups)) * part_size + at;
+#pragma unroll
+      for (int d = 0; d < DK / 16; ++d)
+        if (KT::value(d, g, 0) < a.dim) *reinterpret_cast<f32x4*>(to + KT::value(d, g, 0)) = acc[c][d];
+      continue;
+    }
 #pragma unroll
     for (int d = 0; d < DK / 16; d += M::kTiles) {
       const int v = KT::value(d, g, 0);
       if (v < a.dim) store_operand(out + at + v, &acc[c][d]);
     }
+  }
+}
+
+// dv (y = 0) and dk (y = 1) where a key head's heads are split: the groups' sums in order, four values a thread.  Tokens
+// that no sequence holds are left as they were.
+template <typename E>
+__global__ __launch_bounds__(256) void window_fold_kernel(WinArgs a) {
+  const int64_t seq = tile_seq(a.kv_offsets, a.kv_len, a.nseq, blockIdx.x, kKeys);
+  const Seq ks = seq_of(a.kv_offsets, a.kv_len, seq);
+  const int64_t tile = blockIdx.x - tile_base(a.kv_offsets, a.kv_len, seq, ks.first, kKeys);
+  if (tile < 0 || tile * kKeys >= ks.len) return;
+  const int64_t row = (int64_t)a.hk * a.dim, size = part_floats(a);
+  const int64_t first = (ks.first + tile * kKeys) * row, count = min((int64_t)kKeys, ks.len - tile * kKeys) * row;
+  const float* from = a.part + blockIdx.y * a.groups * size + first;
+  E* out = static_cast<E*>(blockIdx.y ? a.dk : a.dv) + first;
+  for (int64_t x = (blockIdx.z * 256 + threadIdx.x) * 4; x < count; x += gridDim.z * 1024) {
+    f32x4 s = *reinterpret_cast<const f32x4*>(from + x);
+    for (int y = 1; y < a.groups; ++y) s += *reinterpret_cast<const f32x4*>(from + y * size + x);
+    if constexpr (sizeof(E) == 2)
+      *reinterpret_cast<uint2*>(out + x) = uint2{pack_bf16(make_float2(s[0], s[1])), pack_bf16(make_float2(s[2], s[3]))};
+    else
+      *reinterpret_cast<f32x4*>(out + x) = s;
   }
 }
 
@@ -554,20 +590,39 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 }
 
 struct BwdLayout {  // workspace regions in bytes
-  size_t far, total;
+  size_t far, part, total;
   int64_t far_slots, tokens;
-  int32_t sink_tiles;
+  int32_t sink_tiles, far_len, groups;
 };
 BwdLayout layout(const mamba_window_dims* d, bool packed) {
   BwdLayout l = {};
+  l.far_len = kFar;
+  l.groups = 1;
   l.tokens = packed ? d->seqlen : d->batch * d->seqlen;
   l.far = ((size_t)l.tokens * (size_t)d->q_heads * 2 * sizeof(float) + 255) / 256 * 256;
   l.total = l.far;
   if (d->sinks && d->window < d->kv_len) {  // (a window of every key leaves no query past it)
-    l.far_slots = tile_slots(d->seqlen, d->batch, packed, kFar);
     l.sink_tiles = (int32_t)((std::min(d->sinks, d->kv_len) + 15) / 16);
+    // shorter stretches where they would leave CUs idle (2 x 333 tokens, 12 heads of 64, fp32: 22 -> 13 us)
+    auto slots = [&] { return tile_slots(d->seqlen, d->batch, packed, l.far_len); };
+    while (l.far_len > kKeys && (double)slots() * (double)d->q_heads * (double)l.sink_tiles < 256.0) l.far_len /= 2;
+    l.far_slots = slots();
     l.total += (size_t)l.far_slots * (size_t)d->q_heads * (size_t)l.sink_tiles * 32 * (size_t)d->dim * sizeof(float);
   }
+  // A key head's heads go to several workgroups where tiles of keys alone leave CUs idle and that shortens the longest
+  // chain by four tiles, which the sum of the parts costs (the same case: 42 -> 24 us and 5 for the sum).
+  const int64_t rep = d->q_heads / d->kv_heads, keys = d->io_dtype == MAMBA_BF16 ? kKeyRows<uint16_t> : kKeyRows<float>;
+  const int64_t wgs = tile_slots(d->kv_len, d->batch, packed, (int)keys) * d->kv_heads;
+  const int64_t groups = std::min<int64_t>(rep, 512 / std::max<int64_t>(wgs, 1));
+  const int64_t chain = (std::min(d->window + keys, d->seqlen) + kKeys - 1) / kKeys;
+  if (groups > 1) {
+    const int64_t per = (rep + groups - 1) / groups;
+    if ((rep - per) * chain >= 4) l.groups = (int32_t)((rep + per - 1) / per);
+  }
+  l.part = (l.total + 255) / 256 * 256;
+  if (l.groups > 1)
+    l.total = l.part + 2 * (size_t)l.groups * (size_t)(packed ? 1 : d->batch) * (size_t)d->kv_len *
+                           (size_t)(d->kv_heads * d->dim) * sizeof(float);
   return l;
 }
 
@@ -588,8 +643,12 @@ int launch_bwd(const WinArgs& a, int64_t tokens, hipStream_t s) {
     hipLaunchKernelGGL((window_dkv_kernel<E, DK, true>), wide_grid(blocks, 128), dim3(128), 0, s, a, blocks, tokens);
     if ((st = launch_status()) != MAMBA_OK) return st;
   }
-  const uint32_t keys = (uint32_t)(tile_slots(a.kv_len, a.nseq, packed, kKeyRows<E>) * a.hk);
+  const uint32_t keys = (uint32_t)(tile_slots(a.kv_len, a.nseq, packed, kKeyRows<E>) * a.hk * a.groups);
   hipLaunchKernelGGL((window_dkv_kernel<E, DK, false>), wide_grid(keys, 128 * kPairs), dim3(128 * kPairs), 0, s, a, keys, tokens);
+  if ((st = launch_status()) != MAMBA_OK || a.groups == 1) return st;
+  const int64_t pieces = std::min<int64_t>((kKeys * (int64_t)a.hk * a.dim + 4095) / 4096, 256);
+  hipLaunchKernelGGL((window_fold_kernel<E>), dim3((unsigned)tile_slots(a.kv_len, a.nseq, packed, kKeys), 2, (unsigned)pieces),
+                     dim3(256), 0, s, a);
   return launch_status();
 }
 
@@ -631,7 +690,10 @@ int mamba_window_attn_bwd(const void* q, const void* k, const void* v, const int
   a.dv = dv;
   a.stat = static_cast<float*>(workspace);
   a.far = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.far);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.part);
   a.far_slots = l.far_slots;
+  a.far_len = l.far_len;
+  a.groups = l.groups;
   a.sink_tiles = l.sink_tiles;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dims->io_dtype == MAMBA_BF16)
