@@ -418,8 +418,8 @@ int mamba_delta_bwd(const void* q, const void* k, const void* v, const void* g, 
  */
 
 /* Bytes of device workspace mamba_linear_attn_fwd needs (0 for invalid dims; MAMBA_OK calls may need none).
- * packed != 0: for a call with seq_offsets.  Sequences of few heads are worked on in segments and take an fp32
- * state (dk x dv) per segment and value head. */
+ * packed != 0: for a call with seq_offsets.  Long sequences of few heads, and most packed batches, may be worked on
+ * in segments and take an fp32 state (dk x dv) per segment and value head. */
 size_t mamba_linear_attn_workspace_bytes(const mamba_delta_dims* dims, int packed);
 
 /*
@@ -465,7 +465,8 @@ size_t mamba_linear_attn_bwd_workspace_bytes(const mamba_delta_dims* dims, int p
  *   dinitial_state : (batch, v_heads, dk, dv) fp32, or NULL: not written
  *   workspace      : >= mamba_linear_attn_bwd_workspace_bytes bytes, 256-byte aligned
  * Every output is overwritten; with seq_offsets, tokens that no sequence holds are not written.  Sums are taken
- * in a fixed order (bitwise reproducible).
+ * in a fixed order (bitwise reproducible).  A NaN or an infinity in a token's tensors also reaches the gradients of
+ * other tokens of its 128 (fp32 storage: 64), counted from its sequence's first, and what they reach by themselves.
  */
 int mamba_linear_attn_bwd(const void* q, const void* k, const void* v, const float* g,
                           const float* initial_state, const int64_t* seq_offsets, float scale,
@@ -518,8 +519,9 @@ int mamba_window_attn_fwd(const void* q, const void* k, const void* v, const int
                           const mamba_window_dims* dims, void* stream);
 
 /* Bytes of device workspace mamba_window_attn_bwd needs (0 for invalid dims; packed != 0: for a call with offsets):
- * two numbers per query and head, and with sinks that queries outside their window see, fp32 sums of dk and dv per
- * 1024 queries and key head for each 128 (fp32 storage: 64) of the sinks. */
+ * two numbers per query and head, with sinks that queries outside their window see fp32 sums of dk and dv per 64 to 512
+ * queries and query head for each 16 of the sinks, and where a few keys' tiles would leave the GPU idle such sums per
+ * part of the query heads of each key head. */
 size_t mamba_window_attn_bwd_workspace_bytes(const mamba_window_dims* dims, int packed);
 
 /*
