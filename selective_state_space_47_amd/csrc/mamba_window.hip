@@ -76,8 +76,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
     if (a.scale < 0.f)
 #pragma unroll
       for (int kb = 0; kb < DK / M::kDepth; ++kb) qf[c][kb] = -qf[c][kb];
+    if (a.scale == 0.f)  // (in q as well: of a masked score it would make NaN)
+#pragma unroll
+      for (int kb = 0; kb < DK / M::kDepth; ++kb) qf[c][kb] *= typename M::Frag{};
   }
-  const float sc = fabsf(a.scale) * kLog2e;
+  const float sc = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
   f32x4 o[kC2][DK / 16];
   float mx[kC2], l[kC2];
 #pragma unroll
@@ -123,16 +126,18 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
         for (int c = 0; c < kC2; ++c) s[c][m] = M::mma(f[kb & 1][m], qf[c][kb], s[c][m]);
     }
     end_step();
+    if (kStepsV > 1) read_v(1);  // (two steps ahead: transposing reads take longer than a step's products)
     const bool whole = mask.all(pw0, pw1, j0, j0 + kKeys - 1);
 #pragma unroll
     for (int c = 0; c < kC2; ++c) {
       const int p = pw0 + 16 * c + r;
-      if (!whole)
+      if (!whole) {
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             if (!mask.sees(p, j0 + 16 * m + 4 * g + x)) s[c][m][x] = kMinusInf;
+      }
       float top = mx[c];
 #pragma unroll
       for (int m = 0; m < 4; ++m)
@@ -140,25 +145,21 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
         for (int x = 0; x < 4; ++x) top = fmaxf(top, s[c][m][x]);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float use = top == kMinusInf ? 0.f : top * sc;  // (nothing seen yet)
-      if (__any(top > mx[c])) {
-        const float f = mx[c] == kMinusInf ? 0.f : fast_exp2(fmaf(mx[c], sc, -use));
+      // the maximum is followed only where weights would grow past 2^8: any reference gives the same softmax, and a
+      // wave's queries together would have nearly every tile rescale all sums
+      if (__any(top * sc > fmaf(mx[c], sc, 8.f))) {
+        const float f = mx[c] == kMinusInf ? 0.f : fast_exp2((mx[c] - top) * sc);
         l[c] *= f;
 #pragma unroll
         for (int d = 0; d < DK / 16; ++d) o[c][d] *= f;
         mx[c] = top;
       }
+      const float use = mx[c] == kMinusInf ? 0.f : mx[c] * sc;  // (nothing seen yet)
       float sum = 0.f;
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[c][m][x] = fast_exp2(fmaf(s[c][m][x], sc, -use));
-      if (!whole && sc == 0.f)  // (a scale of zero makes NaN of the masked scores)
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (!mask.sees(p, j0 + 16 * m + 4 * g + x)) s[c][m][x] = 0.f;
 #pragma unroll
       for (int m = 0; m < 4; ++m) sum += (s[c][m][0] + s[c][m][1]) + (s[c][m][2] + s[c][m][3]);
       l[c] += sum;
@@ -170,8 +171,6 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
 #pragma unroll
         for (int c = 0; c < kC2; ++c) pf[c] = M::pack(&s[c][i / kGroups * M::kTiles]);
       end_step();
-      if (i + 1 < kStepsV) read_v(i + 1);
-      end_step();
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -179,6 +178,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
           f32x4& to = o[c][i % kGroups * 4 + x];
           to = M::mma(f[i & 1][x], pf[c], to);
         }
+      end_step();
+      if (i + 2 < kStepsV) read_v(i + 2);
     }
     end_step();
   }

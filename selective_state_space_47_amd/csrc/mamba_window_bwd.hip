@@ -145,6 +145,7 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
           }
       }
       end_step();
+      if (kStepsV > 1) read_v(1);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[st][0][32 * half + 16 * m + 4 * g]);
@@ -180,8 +181,6 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
 #pragma unroll
           for (int c = 0; c < kC2; ++c) pf[c] = M::template split<kP>(&s[c][i / kGroups * M::kTiles]);
         end_step();
-        if (i + 1 < kStepsV) read_v(i + 1);
-        end_step();
 #pragma unroll
         for (int p = 0; p < kP; ++p)
 #pragma unroll
@@ -191,6 +190,8 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
               f32x4& to = acc[c][i % kGroups * 4 + x];
               to = M::mma(f[(i + kStepsK) & 1][x], pf[c].p[p], to);
             }
+        end_step();
+        if (i + 2 < kStepsV) read_v(i + 2);
       }
       end_step();
     }
@@ -467,7 +468,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
   };
   // 32 keys of the stage at sk: P and dO V^T, rows = keys, column = query; `then` reads what the products after them
   // take first
-  auto scores = [&](lds_ptr sk, int j0, int half, f32x4 (&s)[kC2][2], f32x4 (&e)[kC2][2], auto then) {
+  auto scores = [&](lds_ptr sk, int j0, int half, f32x4 (&s)[kC2][2], f32x4 (&e)[kC2][2], auto then,
+                    auto behind) {
     const lds_ptr sv = sk + KT::kBytes;
     const int jh = j0 + 32 * half;
 #pragma unroll
@@ -496,6 +498,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
         }
     }
     end_step();
+    behind();
 #pragma unroll
     for (int c = 0; c < kC2; ++c)
 #pragma unroll
@@ -522,7 +525,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
       for (int half = 0; half < 2; ++half) {
         if (mask.none(pw0, pw1, j0 + 32 * half, j0 + 32 * half + 31)) continue;
         f32x4 s[kC2][2], e[kC2][2];
-        scores((lds_ptr)(smem + st * kStage), j0, half, s, e, [] {});
+        scores((lds_ptr)(smem + st * kStage), j0, half, s, e, [] {}, [] {});
 #pragma unroll
         for (int c = 0; c < kC2; ++c)
 #pragma unroll
@@ -547,7 +550,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     for (int half = 0; half < 2; ++half) {
       if (mask.none(pw0, pw1, j0 + 32 * half, j0 + 32 * half + 31)) continue;
       f32x4 s[kC2][2], e[kC2][2];
-      scores(sk, j0, half, s, e, [&] { read_cols(sk, half, 0); });
+      scores(sk, j0, half, s, e, [&] { read_cols(sk, half, 0); }, [&] { if (kStepsV > 1) read_cols(sk, half, 1); });
 #pragma unroll
       for (int c = 0; c < kC2; ++c)
 #pragma unroll
@@ -561,8 +564,6 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 #pragma unroll
           for (int c = 0; c < kC2; ++c) ef[c] = M::template split<kP>(&e[c][i / kGroups * M::kTiles]);
         end_step();
-        if (i + 1 < kStepsV) read_cols(sk, half, i + 1);
-        end_step();
 #pragma unroll
         for (int p = 0; p < kP; ++p)
 #pragma unroll
@@ -572,6 +573,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
               f32x4& to = dq[c][i % kGroups * 4 + x];
               to = M::mma(f[i & 1][x], ef[c].p[p], to);
             }
+        end_step();
+        if (i + 2 < kStepsV) read_cols(sk, half, i + 2);
       }
       end_step();
     }
