@@ -464,14 +464,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
               *reinterpret_cast<typename M::Frag*>(smem + Sm::kX + x * TT::kBytes + TT::word_at(kb, t + r, g)) = f.p[x];
           }
     }
-    // S' = last S + Y^T diag(fy) Z, two accumulators at a time, operands a step ahead
+    // S' = last S + Y^T diag(fy) Z, two accumulators at a time, operands a step ahead.  The chunk's part is summed by
+    // itself: added token by token to a state that hardly decays, its rounding would grow with the sequence.
     {
       const int l = opaque(lane), g = l >> 4;
       const KT kt(l);
       const VT vt(l, 16 * w);
       const float last = gt[5 * kC];
-#pragma unroll
-      for (int m = 0; m < DK / 16; ++m) S[m] *= last;
       auto entering = [&](int kb) {
         f32x4 e[M::kTiles];
 #pragma unroll
@@ -480,29 +479,32 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 1) void linear_pass_kerne
                  *reinterpret_cast<const f32x4*>(gt + 3 * kC + 16 * (kb * M::kTiles + x) + 4 * g);
         return M::template split<kPE>(e);
       };
+      constexpr int kPairs = DK / 32, kB = TT::kBlocks;
       typename M::Frag yc[2][2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) yc[0][c] = kt.cols(sy, c, 0);
-      constexpr int kPairs = DK / 32;
-      auto es = entering(0);
+      typename M::template Parts<kPE> es[kB];
+      es[0] = entering(0);
 #pragma unroll
-      for (int kb = 0; kb < TT::kBlocks; ++kb) {
-        auto next = es;
+      for (int m = 0; m < kPairs; ++m) {
+        f32x4 own[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-        for (int m = 0; m < kPairs; ++m) {
-          const int step = kb * kPairs + m, now = step & 1;
+        for (int kb = 0; kb < kB; ++kb) {
+          const int step = m * kB + kb, now = step & 1;
           __builtin_amdgcn_sched_barrier(0);
-          if (step + 1 < TT::kBlocks * kPairs)
+          if (step + 1 < kB * kPairs)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              yc[now ^ 1][c] = kt.cols(sy, 2 * ((step + 1) % kPairs) + c, (step + 1) / kPairs);
-          if (m == kPairs - 2 && kb + 1 < TT::kBlocks) next = entering(kb + 1);
+            for (int c = 0; c < 2; ++c) yc[now ^ 1][c] = kt.cols(sy, 2 * ((step + 1) / kB) + c, (step + 1) % kB);
+          if (m == 0 && kb + 1 < kB) es[kb + 1] = entering(kb + 1);
 #pragma unroll
           for (int x = 0; x < kPE; ++x)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) S[2 * m + c] = M::mma(yc[now][c], es.p[x], S[2 * m + c]);
+            for (int c = 0; c < 2; ++c) own[c] = M::mma(yc[now][c], es[kb].p[x], own[c]);
         }
-        es = next;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) S[2 * m + c][x] = fmaf(S[2 * m + c][x], last, own[c][x]);
       }
     }
     if (!kO && w == 0 && it + 1 < count) put_gates(next_gate, (int)((it + 1) & 1));

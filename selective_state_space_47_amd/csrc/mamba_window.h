@@ -129,6 +129,26 @@ __device__ __forceinline__ void load_rows(const E* p, int64_t stride, int row, i
 // else to hide the reads behind; nothing is moved past the end of a step.
 __device__ __forceinline__ void end_step() { __builtin_amdgcn_sched_barrier(0); }
 
+// fp32 storage: what a tile adds is summed by itself first.  Thousands of tokens one by one onto an accumulator leave an
+// error of many times its rounding (2 x 2048 queries of 5 heads: dk and dv were off by 1.3e-6, a matrix product in blocks
+// by 5e-7).
+template <typename E>
+constexpr bool kTileSums = sizeof(E) == 4;
+template <int kC2, int kD>
+__device__ __forceinline__ void clear(f32x4 (&t)[kC2][kD]) {
+#pragma unroll
+  for (int c = 0; c < kC2; ++c)
+#pragma unroll
+    for (int d = 0; d < kD; ++d) t[c][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+template <int kC2, int kD>
+__device__ __forceinline__ void add_to(f32x4 (&to)[kC2][kD], const f32x4 (&t)[kC2][kD]) {
+#pragma unroll
+  for (int c = 0; c < kC2; ++c)
+#pragma unroll
+    for (int d = 0; d < kD; ++d) to[c][d] += t[c][d];
+}
+
 // Every load of this wave has landed, said so that the compiler counts it too.  Operands loaded before a loop would
 // otherwise be waited for again at their first use in every turn, and with them the copies of the next tile.
 __device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)

@@ -165,6 +165,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
       l[c] += sum;
     }
     typename M::Frag pf[kC2];
+    f32x4 part[kTileSums<E> ? kC2 : 1][DK / 16];
+    if constexpr (kTileSums<E>) clear(part);
 #pragma unroll
     for (int i = 0; i < kStepsV; ++i) {
       if (i % kGroups == 0)
@@ -175,12 +177,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
       for (int x = 0; x < 4; ++x)
 #pragma unroll
         for (int c = 0; c < kC2; ++c) {
-          f32x4& to = o[c][i % kGroups * 4 + x];
+          f32x4& to = (kTileSums<E> ? part : o)[c][i % kGroups * 4 + x];
           to = M::mma(f[i & 1][x], pf[c], to);
         }
       end_step();
       if (i + 2 < kStepsV) read_v(i + 2);
     }
+    if constexpr (kTileSums<E>) add_to(o, part);
     end_step();
   }
 #pragma unroll

@@ -175,6 +175,8 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
         }
       constexpr int kP = kRole == kMakeDv ? 1 : M::parts(2);
       typename M::template Parts<kP> pf[kC2];
+      f32x4 part[kTileSums<E> ? kC2 : 1][DK / 16];
+      if constexpr (kTileSums<E>) clear(part);
 #pragma unroll
       for (int i = 0; i < kStepsV; ++i) {
         if (i % kGroups == 0)
@@ -187,12 +189,13 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
           for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int c = 0; c < kC2; ++c) {
-              f32x4& to = acc[c][i % kGroups * 4 + x];
+              f32x4& to = (kTileSums<E> ? part : acc)[c][i % kGroups * 4 + x];
               to = M::mma(f[(i + kStepsK) & 1][x], pf[c].p[p], to);
             }
         end_step();
         if (i + 2 < kStepsV) read_v(i + 2);
       }
+      if constexpr (kTileSums<E>) add_to(acc, part);
       end_step();
     }
     if (i + 1 < k.count) put_stat(next, st ^ 1);
@@ -558,6 +561,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
           e[c][m] = s[c][m] * (e[c][m] - ds[c]);
       constexpr int kP = M::parts(2);
       typename M::template Parts<kP> ef[kC2];
+      f32x4 part[kTileSums<E> ? kC2 : 1][DK / 16];
+      if constexpr (kTileSums<E>) clear(part);
 #pragma unroll
       for (int i = 0; i < kStepsV; ++i) {
         if (i % kGroups == 0)
@@ -570,12 +575,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
           for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int c = 0; c < kC2; ++c) {
-              f32x4& to = dq[c][i % kGroups * 4 + x];
+              f32x4& to = (kTileSums<E> ? part : dq)[c][i % kGroups * 4 + x];
               to = M::mma(f[i & 1][x], ef[c].p[p], to);
             }
         end_step();
         if (i + 2 < kStepsV) read_cols(sk, half, i + 2);
       }
+      if constexpr (kTileSums<E>) add_to(dq, part);
       end_step();
     }
   }
