@@ -286,6 +286,26 @@ def test_streams_and_graphs(io):
         assert torch.equal(out, w_out) and torch.equal(last, w_last) and torch.equal(step, w_step)
 
 
+@IO
+@pytest.mark.parametrize("heads", [2, 400])
+def test_state_that_hardly_decays(heads, io):
+    """16384 tokens in one state, in segments (few heads) or one after another.  256 chunks added one by one to a sum that
+    grows with their root leave 2.5e-8 sqrt(256 / 2) = 2.8e-7 of it (rounding to nearest is off by 2.5e-8, root mean
+    square, relative), the 64 tokens within a chunk half of that; token by token it would be 2.3e-6."""
+    L, d = 16384, 16
+    print(f"[linear long state] {heads} {io}", flush=True)
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    q, k = (torch.randn(1, L, 1, d, generator=gen, device=DEV).to(io) for _ in range(2))
+    v = torch.randn(1, L, heads, d, generator=gen, device=DEV).to(io)
+    g = torch.full((1, L, heads), -1e-5, device=DEV)
+    _, last = binding.mamba_linear_attn_fwd(q, k, v, g, return_last_state=True)
+    back = torch.arange(L - 1, -1, -1, device=DEV).double() * float(g[0, 0, 0])
+    want = torch.einsum("ti,thj->hij", k[0, :, 0].double() * back.exp()[:, None], v[0].double())
+    off = float((last[0].double() - want).norm() / want.norm())
+    print(f"[linear long state] {off:.2e}", flush=True)
+    assert off <= 1e-6
+
+
 def test_refusals():
     _, t = case(7, 2, 10, 1, 2, 64, 64, F32)
     bad = [dict(g=None), dict(g=t["g"].double()), dict(g=t["g"][:, :5]), dict(k=t["k"][:1]), dict(v=t["v"].bfloat16()),

@@ -445,3 +445,35 @@ def test_refusals():
         binding.mamba_window_attn_update(*cache, *step, pos, sinks=8)  # no window left
     with pytest.raises(ValueError):
         binding.mamba_window_cache_store(*cache, t["k"][:1], t["v"][:1])
+
+
+def test_long_sums_fp32():
+    """Thousands of tokens in one sum.  Rounding to nearest is off by 2.5e-8 (root mean square, relative) each time, and M
+    additions to a sum that grows with their root leave 2.5e-8 sqrt(M / 2) of it: dk and dv are sums over 5 heads of 2048
+    queries, 320 blocks of 32, 3.2e-7, and 1e-7 from within the blocks; weights of 1 / 2048 have arguments of 11 binary
+    digits before the point, 2e-7.  Token by token it would be 1.8e-6."""
+    L, Hq, d, window = 4096, 5, 64, 2048
+    print("[window long sums]", flush=True)
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    q, do = (torch.randn(1, L, Hq, d, generator=gen, device=DEV) for _ in range(2))
+    k, v = (torch.randn(1, L, 1, d, generator=gen, device=DEV) for _ in range(2))
+    out, lse = binding.mamba_window_attn_fwd(q, k, v, window, 0, return_lse=True)
+    got = binding.mamba_window_attn_bwd(q, k, v, out, lse, do, window, 0)
+    t = torch.arange(L, device=DEV)
+    see = (t[None] <= t[:, None]) & (t[:, None] - t[None] < window)
+    K, V = k[0, :, 0].double(), v[0, :, 0].double()
+    dk, dv, want, dq = torch.zeros_like(K), torch.zeros_like(V), [], []
+    for h in range(Hq):
+        Q, dO = q[0, :, h].double(), do[0, :, h].double()
+        P = torch.softmax((d ** -0.5 * (Q @ K.t())).masked_fill(~see, float("-inf")), 1)
+        dP = dO @ V.t()
+        dS = P * (dP - (P * dP).sum(1, keepdim=True)) * d ** -0.5
+        want.append(P @ V)
+        dq.append(dS @ K)
+        dk += dS.t() @ Q
+        dv += P.t() @ dO
+    for name, a, b in (("out", out[0], torch.stack(want, 1)), ("dq", got["dq"][0], torch.stack(dq, 1)),
+                       ("dk", got["dk"][0, :, 0], dk), ("dv", got["dv"][0, :, 0], dv)):
+        off = float((a.double() - b).norm() / b.norm())
+        print(f"[window long sums] {name}: {off:.2e}", flush=True)
+        assert off <= 1e-6, name
