@@ -18,10 +18,11 @@
 // one's operand, so that only the triangular matrix, which the waves share out, and the output, which is stored in whole
 // rows, go through LDS.
 //
-// Measured (8 x 2048 tokens, 20 key and 40 value heads of 128, bf16): forward 224 us (2.1 TB/s; its bytes at a copy's rate
-// 105), backwards with images 256, forwards with images and their products 212 (4.4 TB/s).  With an output the vector
-// unit is busy 60% and the matrix unit 34% of the time, and on this target the two add up: the state's and the entering
-// values' conversions to bf16 parts are most of it.  A chunk takes a workgroup that is alone on its CU 9500 cycles.
+// Measured (8 x 2048 tokens, 20 key and 40 value heads of 128, bf16): forward 227 us (2.2 TB/s; its bytes at a copy's
+// rate 105), backwards with images 259, forwards with images and their products 210 (4.5 TB/s).  With an output a wave
+// has 5.8 vector instructions of 4 cycles per product, and a product keeps the vector unit from issuing for half of its
+// 16 cycles (measured), so that the best would be 110 us: the state's and the entering values' conversions to bf16 parts
+// are most of it.  A chunk takes a workgroup that is alone on its CU 9500 cycles.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -574,7 +575,7 @@ int launch_pass(const PassArgs& p, hipStream_t s) {
 //   Packed ones, whose lengths are not known here: segments where one sequence of all tokens would take twice as long as
 //   all work, which costs the launches where no sequence is long, as those whose chain takes no longer than about the
 //   work (`limit` chunks) are not cut; the length for which a chain behind half the work and the states take least.
-// Measured without and with: 65536 tokens, 12 heads of 128 x 128, 5.9 ms and 328 us; 2 x 333 tokens, 12 heads of 64 x 96,
+// Measured without and with: 65536 tokens, 12 heads of 128 x 128, 5.9 ms and 326 us; 2 x 333 tokens, 12 heads of 64 x 96,
 // fp32, 41 and 28 us; packed, 80 heads of 128 x 64: 8279 tokens in 8 sequences of up to 4099, 378 and 196 us, 15 of 500
 // and one of 12000, 1045 and 334 us; 16 of 2048, 387 and 415 us, 64 of 300, 286 and 310 us.
 struct SegPlan {

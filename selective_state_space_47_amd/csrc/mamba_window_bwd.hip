@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256) void window_stat_kernel(WinArgs a, int64_t tok
 // What a wave of the keys' pass makes: dV (from P), or dK (from P and dO V^T).  Two waves share 32 keys (fp32 storage:
 // 16): with both sums in one wave there is room for one wave on a SIMD, which has nobody to hide its waits behind.
 // (8 x 2048 tokens, 20 and 4 heads of 128, window 1024, dS in one part: 395 us; both sums in one wave and 128 keys per
-// workgroup 491, by roles with 128 keys 503, as the longest workgroups then ran alone at the end.  With dS in two: 460.)
+// workgroup 491, by roles with 128 keys 503, as the longest workgroups then ran alone at the end.  With dS in two: 446.)
 enum Role { kMakeDv, kMakeDk };
 
 // The queries' tiles of a workgroup of the keys' pass
@@ -208,7 +208,7 @@ __device__ __forceinline__ int64_t part_floats(const WinArgs& a) {
 }
 
 // kFarPart: 16 sinks and one query head over a stretch of queries past the sinks' windows; otherwise a tile of keys, the
-// heads that share it one after another.  (Far part of 4 sinks and 8 x 2048 tokens: 27 us; with the sinks' tile as one
+// heads that share it one after another.  (Far part of 4 sinks and 8 x 2048 tokens: 28 us; with the sinks' tile as one
 // workgroup's work it was 564.)
 template <typename E, int DK, bool kFarPart>
 __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(WinArgs a, uint32_t blocks, int64_t tokens) {
@@ -392,7 +392,7 @@ __global__ __launch_bounds__(256) void window_fold_kernel(WinArgs a) {
   }
 }
 
-// 8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16: 417 us for seven products per pair of tiles (S and dO V^T
+// 8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16: 411 us for seven products per pair of tiles (S and dO V^T
 // twice, dS K in two parts and the queries' exponentials twice).
 template <typename E, int DK>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(WinArgs a, uint32_t blocks,
