@@ -21,6 +21,8 @@
 // two: a row of dS sums to zero, and with one part dK and dQ were off by up to 1.48 times their own
 // rounding (8 x 2048 tokens, 20 and 4 heads of 128: the second part costs 103 of 938 us, one of P
 // would cost 25).  The rest is fp32.
+#include <cstdint>
+
 #include "mamba_window.h"
 
 namespace mamba {
@@ -616,6 +618,11 @@ BwdLayout layout(const mamba_window_dims* d, bool packed) {
     auto slots = [&] { return tile_slots(d->seqlen, d->batch, packed, l.far_len); };
     while (l.far_len > kKeys && (double)slots() * (double)d->q_heads * (double)l.sink_tiles < 256.0) l.far_len /= 2;
     l.far_slots = slots();
+    // (sinks by the million: more than any workspace holds, and than the sum would)
+    if ((double)l.far_slots * (double)d->q_heads * (double)l.sink_tiles * 128.0 * (double)d->dim > 1e18) {
+      l.total = SIZE_MAX;
+      return l;
+    }
     l.total += (size_t)l.far_slots * (size_t)d->q_heads * (size_t)l.sink_tiles * 32 * (size_t)d->dim * sizeof(float);
   }
   // A key head's heads go to several workgroups where tiles of keys alone leave CUs idle and that shortens the longest
