@@ -11,8 +11,9 @@
 // accumulators of P are, rounded, the operand of the next product.
 //
 // Rounding, bf16 storage: P enters the product with V as one bf16 part (2^-9 of each weight, independent from key to
-// key, which weighs at most as much in the output as its own rounding: 2.0e-3 of the norm in all, its own is 1.66e-3);
-// scores, m, l and O are fp32.
+// key, which weighs at most as much in the output as its own rounding: 2.0e-3 to 2.4e-3 of the norm in all, its own is
+// 1.66e-3); scores, m, l and O are fp32.  The reference of the weights follows the maximum only past a factor of 2^8, so
+// that in a tile with a new maximum the sums are seldom rescaled (7% of the time).
 //
 // Measured (8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16): 188 us, 690 TFLOP/s of the pairs that are seen.  Of
 // a tile's 4850 cycles the copies' issue takes 620, the scores 740, the softmax 1370 and the values' product 1800, which
