@@ -508,8 +508,8 @@ typedef struct mamba_window_dims {
  *   out        : (batch, seqlen, q_heads, dim), io_dtype, contiguous
  *   lse        : (batch, seqlen, q_heads) fp32, or NULL: log sum_j exp(scale q . k_j)
  * q, k, v and out are 16-byte aligned.  Scores, maximum, sum and output are fp32; with bf16 storage the
- * probabilities enter the product with v as bf16.  seqlen and kv_len are below 2^31 - 1024, tokens * heads * dim
- * at most 2^40 (MAMBA_ERR_SHAPE otherwise).  Work goes by 32 queries and 64 keys: a NaN or an infinity in a v reaches,
+ * probabilities enter the product with v as two bf16 parts, so that out is the fp32 result rounded once.  seqlen and
+ * kv_len are below 2^31 - 1024, tokens * heads * dim at most 2^40 (MAMBA_ERR_SHAPE otherwise).  Work goes by 32 queries and 64 keys: a NaN or an infinity in a v reaches,
  * of its value column, also queries that do not see it where one of the same 32 sees a key of its 64 (one in a k does
  * not, and other sequences' tokens never do).  In the gradients one in any input reaches what shares such a block
  * with it.

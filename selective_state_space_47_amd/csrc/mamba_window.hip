@@ -10,14 +10,15 @@
 // values x queries: a lane holds one query's scores, so that the softmax needs two exchanges per tile, and the
 // accumulators of P are, rounded, the operand of the next product.
 //
-// Rounding, bf16 storage: P enters the product with V as one bf16 part (2^-9 of each weight, independent from key to
-// key, which weighs at most as much in the output as its own rounding: 2.0e-3 to 2.4e-3 of the norm in all, its own is
-// 1.66e-3); scores, m, l and O are fp32.  The reference of the weights follows the maximum only past a factor of 2^8, so
-// that in a tile with a new maximum the sums are seldom rescaled (7% of the time).
+// Rounding, bf16 storage: P enters the product with V as two bf16 parts (2^-17 of each weight), so that out's own rounding
+// is the only one that shows, as in the step and as fp32 arithmetic promises (one part: 2^-8 of a weight at most, out off
+// by 2.0e-3 to 2.4e-3 of its norm where rounding it is 1.66e-3; 169 us of the layer below in place of 211, 108 of the
+// packed prompts in place of 132); scores, m, l and O are fp32.  The reference of the weights follows the maximum only
+// past a factor of 2^8, so that in a tile with a new maximum the sums are seldom rescaled (7% of the time).
 //
-// Measured (8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16): 188 us, 690 TFLOP/s of the pairs that are seen.  Of
-// a tile's 4850 cycles the copies' issue takes 620, the scores 740, the softmax 1370 and the values' product 1800, which
-// waits for transposing reads.  Two workgroups share a CU, 8 waves of 32 queries: with 16 each a tile's operands would
+// Measured (8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16): 211 us, 615 TFLOP/s of the pairs that are seen, 1.5
+// times as many of products made.  The vector and the matrix unit are busy in turn: softmax, conversions and products of
+// the two waves of a SIMD add up.  Two workgroups share a CU, 8 waves of 32 queries: with 16 each a tile's operands would
 // be read twice as often.
 #include "mamba_window.h"
 
@@ -166,22 +167,25 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_fwd_kernel
       for (int m = 0; m < 4; ++m) sum += (s[c][m][0] + s[c][m][1]) + (s[c][m][2] + s[c][m][3]);
       l[c] += sum;
     }
-    typename M::Frag pf[kC2];
+    constexpr int kP = M::parts(2);
+    typename M::template Parts<kP> pf[kC2];
     f32x4 part[kTileSums<E> ? kC2 : 1][DK / 16];
     if constexpr (kTileSums<E>) clear(part);
 #pragma unroll
     for (int i = 0; i < kStepsV; ++i) {
       if (i % kGroups == 0)
 #pragma unroll
-        for (int c = 0; c < kC2; ++c) pf[c] = M::pack(&s[c][i / kGroups * M::kTiles]);
+        for (int c = 0; c < kC2; ++c) pf[c] = M::template split<kP>(&s[c][i / kGroups * M::kTiles]);
       end_step();
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int p = 0; p < kP; ++p)
 #pragma unroll
-        for (int c = 0; c < kC2; ++c) {
-          f32x4& to = (kTileSums<E> ? part : o)[c][i % kGroups * 4 + x];
-          to = M::mma(f[i & 1][x], pf[c], to);
-        }
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int c = 0; c < kC2; ++c) {
+            f32x4& to = (kTileSums<E> ? part : o)[c][i % kGroups * 4 + x];
+            to = M::mma(f[i & 1][x], pf[c].p[p], to);
+          }
       end_step();
       if (i + 2 < kStepsV) read_v(i + 2);
     }
