@@ -17,10 +17,10 @@
 // would carry 2^-9 of dO . out into dS, which is the small difference of two numbers of that size where a few keys have
 // all the weight (4 keys, scores of deviation 3.4: dq was off by 5.4e-3).
 //
-// Rounding, bf16 storage: P enters its product as one bf16 part, which weighs as much in dV as its own rounding, and dS as
-// two: a row of dS sums to zero, and with one part dK and dQ were off by up to 1.48 times their own
-// rounding (8 x 2048 tokens, 20 and 4 heads of 128: the second part costs 103 of 938 us, one of P
-// would cost 25).  The rest is fp32.
+// Rounding, bf16 storage: P and dS enter their products as two bf16 parts (2^-17 of each), so that the gradients' own
+// rounding is the only one that shows, 1.66e-3 of the norm (one part of P: dV off by 2.3e-3; one of dS, whose rows sum to
+// zero: dK and dQ by up to 1.48 times their rounding.  8 x 2048 tokens, 20 and 4 heads of 128: the second part of P costs
+// 23 of 785 us, that of dS 103).  The rest is fp32.
 #include <cstdint>
 
 #include "mamba_window.h"
@@ -68,7 +68,8 @@ __global__ __launch_bounds__(256) void window_stat_kernel(WinArgs a, int64_t tok
 // What a wave of the keys' pass makes: dV (from P), or dK (from P and dO V^T).  Two waves share 32 keys (fp32 storage:
 // 16): with both sums in one wave there is room for one wave on a SIMD, which has nobody to hide its waits behind.
 // (8 x 2048 tokens, 20 and 4 heads of 128, window 1024, dS in one part: 395 us; both sums in one wave and 128 keys per
-// workgroup 491, by roles with 128 keys 503, as the longest workgroups then ran alone at the end.  With dS in two: 446.)
+// workgroup 491, by roles with 128 keys 503, as the longest workgroups then ran alone at the end.  With dS in two: 446, and
+// P in two as well: 469.)
 enum Role { kMakeDv, kMakeDk };
 
 // The queries' tiles of a workgroup of the keys' pass
@@ -175,7 +176,7 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
 #pragma unroll
           for (int c = 0; c < kC2; ++c) s[c][m] = s[c][m] * (e[c][m] - ds);
         }
-      constexpr int kP = kRole == kMakeDv ? 1 : M::parts(2);
+      constexpr int kP = M::parts(2);
       typename M::template Parts<kP> pf[kC2];
       f32x4 part[kTileSums<E> ? kC2 : 1][DK / 16];
       if constexpr (kTileSums<E>) clear(part);

@@ -13,7 +13,7 @@ import torch
 
 from oracle import window as ref
 
-from .test_gpu_window import BF, _native, case, fwd, ids, refs  # noqa: F401
+from .test_gpu_window import BF, GRADS, _native, bwd, case, fwd, ids, refs, terms  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 FP32, PARTS = 2e-5, 2.0 ** -17
@@ -51,3 +51,16 @@ def test_out_rounds_once(shape):
     out, _ = fwd(t, window, sinks)
     want = np.stack([refs(x, b, window, sinks, d ** -0.5, grads=False)[0] for b in range(B)])
     rounded_once(out, want, "out", np.stack([sums_of_sizes(x, b, window, sinks, d ** -0.5)[0] for b in range(B)]))
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=ids)
+def test_gradients_round_once(shape):
+    B, n, m, Hq, Hk, d, window, sinks = shape
+    x, t = case(sum(shape[:6]) + 2, B, n, m, Hq, Hk, d, BF)
+    scale = d ** -0.5
+    out, lse = fwd(t, window, sinks)
+    got = bwd(t, out, lse, window, sinks)
+    want = [np.stack(a) for a in zip(*(refs(x, b, window, sinks, scale)[2:] for b in range(B)))]
+    sizes = [dict(terms(x, b, window, sinks, scale), dv=sums_of_sizes(x, b, window, sinks, scale)[1]) for b in range(B)]
+    for name, w in zip(GRADS, want):
+        rounded_once(got[name], w, name, np.stack([a[name] for a in sizes]), 0.0 if name == "dv" else 2.0 ** -20)
