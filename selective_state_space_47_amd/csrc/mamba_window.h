@@ -24,7 +24,7 @@ struct WinArgs {
   void* dq;
   void* dk;
   void* dv;
-  float* stat;                // (2, hq, tokens): log-sums times log2(e), and sums of dout out
+  float* stat;                // (2 or 3, hq, tokens): log-sums times log2(e), sums of dout out, and inverse sums of weights
   float* far;                 // (far slots, hq, tiles of 16 sinks, 2, 16, dim): sums over queries past the sinks' windows
   int64_t seqlen, kv_len, nseq;
   int64_t q_stride, k_stride, v_stride;

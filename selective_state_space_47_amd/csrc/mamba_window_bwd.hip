@@ -17,6 +17,15 @@
 // would carry 2^-9 of dO . out into dS, which is the small difference of two numbers of that size where a few keys have
 // all the weight (4 keys, scores of deviation 3.4: dq was off by 5.4e-3).
 //
+// lse is a number of fp32 and so is its product with log2(e): each is off by 2^-24 of itself, and the weights made from
+// them by as many powers of e, up to 6e-5 of themselves at a score of 500.  The queries' pass therefore sums the weights
+// and takes D as sum P (dO . v) / sum P: dO . v - D, which is small where a key has nearly all the weight, does not see
+// their common factor.  With bf16 storage log2(sum P) goes into lse log2(e) (which leaves 2^-24 of that, far below the
+// gradients' rounding); with fp32 storage dQ is divided by the sum, and the keys' pass, which sums the scores' products in
+// the same order and so makes the same weights, reads its inverse as a third number.
+// (Scores of 300 to 650, every query with one key, bf16: dq was off by 2.2e-6 of its terms, more at larger ones; fp32:
+// dv by 7e-5 of its norm.)
+//
 // Rounding, bf16 storage: P and dS enter their products as two bf16 parts (2^-17 of each), so that the gradients' own
 // rounding is the only one that shows, 1.66e-3 of the norm (one part of P: dV off by 2.3e-3; one of dS, whose rows sum to
 // zero: dK and dQ by up to 1.48 times their rounding.  8 x 2048 tokens, 20 and 4 heads of 128: the second part of P costs
@@ -36,6 +45,8 @@ constexpr int kRows = 4 * 16 * kTilesW<E>;       // of a workgroup
 constexpr int kPairs = 2;                        // pairs of waves that share the keys of a workgroup of the keys' pass
 template <typename E>
 constexpr int kKeyRows = kPairs * 16 * kTilesW<E>;
+template <typename E>
+constexpr int kStats = sizeof(E) == 2 ? 2 : 3;   // numbers of a query and head that the keys' pass reads
 constexpr int kFar = 512;                        // queries of a stretch past the sinks' windows, at most
 
 // 8 lanes per row; a row without a key has weights of zero: its log-sum counts as +infinity
@@ -83,7 +94,7 @@ struct KeyWork {
 // A wave's share: 16 kC2 keys from jw0 on against the tiles of queries that come into the stages.
 template <typename E, int DK, bool kFarPart, int kC2, Role kRole, typename Copy, typename Load, typename Put>
 __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, const Mask& mask, char* smem,
-                                         const float (&stats)[2][2][kKeys], int jw0, float sc,
+                                         const float (&stats)[2][kStats<E>][kKeys], int jw0, float sc,
                                          const typename Mma<E>::Frag (&kf)[kC2][DK / Mma<E>::kDepth],
                                          const typename Mma<E>::Frag (&vf)[kC2][DK / Mma<E>::kDepth],
                                          f32x4 (&acc)[kC2][DK / 16], Copy copy, Load load_stat, Put put_stat) {
@@ -91,13 +102,14 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
   using KT = KeyTile<E, DK>;
   constexpr int kStage = 2 * KT::kBytes;
   constexpr int kPer = kRole == kMakeDv ? 2 : 1;  // depths of a step of the scores
+  constexpr bool kSplit = kRole == kMakeDv && sizeof(E) == 2;
   constexpr int kStepsK = DK / M::kDepth / kPer, kGroups = DK / 64, kStepsV = 32 / M::kDepth * kGroups;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const KT kt(lane);
   const int jw1 = jw0 + 16 * kC2 - 1;
   for (int i = 0; i < k.count; ++i) {
     const int st = i & 1, h = i / k.tiles, q0 = (k.t_lo + i - h * k.tiles) * kKeys;
-    float2 next = make_float2(0.f, 0.f);
+    float3 next = make_float3(0.f, 0.f, 0.f);
     copies_done();
     if (i + 1 < k.count) {
       next = load_stat(i + 1);
@@ -141,10 +153,12 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
 #pragma unroll
           for (int c = 0; c < kC2; ++c) {
             s[c][m] = M::mma(f[kb & 1][m], kf[c][kPer * kb], s[c][m]);
-            if constexpr (kRole == kMakeDv)
-              e[c][m] = M::mma(f[kb & 1][2 + m], kf[c][kPer * kb + 1], e[c][m]);  // (the other half of the scores)
-            else
+            if constexpr (kRole == kMakeDk) {
               e[c][m] = M::mma(f[kb & 1][2 + m], vf[c][kb], e[c][m]);
+            } else {  // the other half of the scores (fp32 storage: in the order of the queries' pass)
+              f32x4& to = kSplit ? e[c][m] : s[c][m];
+              to = M::mma(f[kb & 1][2 + m], kf[c][kPer * kb + 1], to);
+            }
           }
       }
       end_step();
@@ -154,9 +168,11 @@ __device__ __forceinline__ void key_sums(const WinArgs& a, const KeyWork& k, con
         const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[st][0][32 * half + 16 * m + 4 * g]);
 #pragma unroll
         for (int c = 0; c < kC2; ++c) {
-          if (kRole == kMakeDv) s[c][m] += e[c][m];
+          if (kSplit) s[c][m] += e[c][m];
 #pragma unroll
           for (int x = 0; x < 4; ++x) s[c][m][x] = fast_exp2(fmaf(s[c][m][x], sc, -ls[x]));
+          if constexpr (kStats<E> == 3)
+            s[c][m] *= *reinterpret_cast<const f32x4*>(&stats[st][2][32 * half + 16 * m + 4 * g]);
         }
       }
       if (!whole)
@@ -220,7 +236,7 @@ __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeo
   constexpr int kP = kFarPart ? 1 : kPairs, kNW = 2 * kP, kC2 = kFarPart ? 1 : kTilesW<E>;
   constexpr int kN = kFarPart ? 16 : kKeyRows<E>, kStage = 2 * KT::kBytes;
   __shared__ __align__(1024) char smem[2 * kStage];
-  __shared__ __align__(16) float stats[2][2][kKeys];
+  __shared__ __align__(16) float stats[2][kStats<E>][kKeys];
   const uint32_t id = wide_index();
   if (id >= blocks) return;
   int64_t seq, tile, far_slot = 0, stretch = 0;
@@ -287,16 +303,18 @@ __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeo
     cq(rows_buffer(qp + t * a.q_stride + (int64_t)h * a.dim, n, a.q_stride, a.dim), lds0 + st * kStage, w);
     co(rows_buffer(op + t * o_stride + (int64_t)h * a.dim, n, o_stride, a.dim), lds0 + st * kStage + KT::kBytes, w);
   };
-  // wave 0: the log-sums and the dots; past the sequence +infinity and 0
+  // wave 0: the log-sums, the dots and the inverse sums; past the sequence +infinity and 0
   auto load_stat = [&](int i) {
     const int h = i / k.tiles, t = (k.t_lo + i - h * k.tiles) * kKeys + lane;
     const float* p = a.stat + (int64_t)(hq0 + h) * tokens + qs.first + t;
-    return w == 0 && t < qs.len ? make_float2(p[0], p[tokens * a.hq]) : make_float2(-kMinusInf, 0.f);
+    return w == 0 && t < qs.len ? make_float3(p[0], p[tokens * a.hq], kStats<E> == 3 ? p[2 * tokens * a.hq] : 0.f)
+                                : make_float3(-kMinusInf, 0.f, 0.f);
   };
-  auto put_stat = [&](float2 v, int st) {
+  auto put_stat = [&](float3 v, int st) {
     if (w == 0) {
       stats[st][0][lane] = v.x;
       stats[st][1][lane] = v.y;
+      if constexpr (kStats<E> == 3) stats[st][2][lane] = v.z;
     }
   };
   if (k.count) {
@@ -438,10 +456,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
   const E* qp = static_cast<const E*>(a.q) + (qs.first + q0) * a.q_stride + (int64_t)h * a.dim;
   const E* op = static_cast<const E*>(a.dout) + (qs.first + q0) * o_stride + (int64_t)h * a.dim;
   constexpr bool kTwice = sizeof(E) == 2;
-  float ls[kC2], ds[kC2];
+  float ls[kC2], ds[kC2], sums[kC2];  // sums of P: see the head of this file
 #pragma unroll
   for (int c = 0; c < kC2; ++c) {
     const int i = w0 + 16 * c + r;
+    sums[c] = 0.f;
     load_rows<E, DK>(qp, a.q_stride, i, nq, a.dim, g, qf[c]);
     load_rows<E, DK>(op, o_stride, i, nq, a.dim, g, of[c]);
     const int64_t at = (int64_t)h * tokens + qs.first + q0 + i;
@@ -454,7 +473,6 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     if (i < nq && kTwice) {
       const float lse = a.lse[(qs.first + q0 + i) * a.hq + h];
       ls[c] = lse == kMinusInf ? -kMinusInf : lse * kLog2e;
-      if (g == 0) a.stat[at] = ls[c];
     }
   }
   const float sc = a.scale * kLog2e;
@@ -520,6 +538,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
           for (int x = 0; x < 4; ++x)
             if (!mask.sees(pw0 + 16 * c + r, jh + 16 * m + 4 * g + x)) s[c][m][x] = 0.f;
   };
+  auto add_sums = [&](const f32x4 (&s)[kC2][2]) {
+#pragma unroll
+    for (int c = 0; c < kC2; ++c) {
+      const f32x4 t = s[c][0] + s[c][1];
+      sums[c] += (t[0] + t[1]) + (t[2] + t[3]);
+    }
+  };
   int turn = 0;  // stages
   loads_done();
   if constexpr (kTwice) {
@@ -532,6 +557,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
         if (mask.none(pw0, pw1, j0 + 32 * half, j0 + 32 * half + 31)) continue;
         f32x4 s[kC2][2], e[kC2][2];
         scores((lds_ptr)(smem + st * kStage), j0, half, s, e, [] {}, [] {});
+        add_sums(s);
 #pragma unroll
         for (int c = 0; c < kC2; ++c)
 #pragma unroll
@@ -542,9 +568,18 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     }
 #pragma unroll
     for (int c = 0; c < kC2; ++c) {
+      const float sum = across_groups(sums[c]);
       ds[c] = across_groups(ds[c]);
+      if (sum != 0.f) {
+        ds[c] /= sum;
+        ls[c] += __builtin_amdgcn_logf(sum);
+      }
       const int i = w0 + 16 * c + r;
-      if (g == 0 && i < nq) a.stat[tokens * a.hq + (int64_t)h * tokens + qs.first + q0 + i] = ds[c];
+      const int64_t at = (int64_t)h * tokens + qs.first + q0 + i;
+      if (g == 0 && i < nq) {
+        a.stat[at] = ls[c];
+        a.stat[tokens * a.hq + at] = ds[c];
+      }
     }
   }
   for (int i = 0; i < count; ++i, ++turn) {
@@ -557,6 +592,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
       if (mask.none(pw0, pw1, j0 + 32 * half, j0 + 32 * half + 31)) continue;
       f32x4 s[kC2][2], e[kC2][2];
       scores(sk, j0, half, s, e, [&] { read_cols(sk, half, 0); }, [&] { if (kStepsV > 1) read_cols(sk, half, 1); });
+      if constexpr (!kTwice) add_sums(s);
 #pragma unroll
       for (int c = 0; c < kC2; ++c)
 #pragma unroll
@@ -591,10 +627,16 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 #pragma unroll
   for (int c = 0; c < kC2; ++c) {
     const int i = w0 + 16 * c + r;
+    float f = a.scale;
+    if constexpr (!kTwice) {
+      const float sum = across_groups(sums[c]), inv = sum == 0.f ? 0.f : 1.f / sum;
+      f *= inv;
+      if (g == 0 && i < nq) a.stat[2 * tokens * a.hq + (int64_t)h * tokens + qs.first + q0 + i] = inv;
+    }
     if (i >= nq) continue;
     E* to = static_cast<E*>(a.dq) + ((qs.first + q0 + i) * a.hq + h) * (int64_t)a.dim;
 #pragma unroll
-    for (int d = 0; d < DK / 16; ++d) dq[c][d] *= a.scale;
+    for (int d = 0; d < DK / 16; ++d) dq[c][d] *= f;
 #pragma unroll
     for (int d = 0; d < DK / 16; d += M::kTiles)
       if (KT::value(d, g, 0) < a.dim) store_operand(to + KT::value(d, g, 0), &dq[c][d]);
@@ -611,7 +653,8 @@ BwdLayout layout(const mamba_window_dims* d, bool packed) {
   l.far_len = kFar;
   l.groups = 1;
   l.tokens = packed ? d->seqlen : d->batch * d->seqlen;
-  l.far = ((size_t)l.tokens * (size_t)d->q_heads * 2 * sizeof(float) + 255) / 256 * 256;
+  const size_t stats = d->io_dtype == MAMBA_BF16 ? kStats<uint16_t> : kStats<float>;
+  l.far = ((size_t)l.tokens * (size_t)d->q_heads * stats * sizeof(float) + 255) / 256 * 256;
   l.total = l.far;
   if (d->sinks && d->window < d->kv_len) {  // (a window of every key leaves no query past it)
     l.sink_tiles = (int32_t)((std::min(d->sinks, d->kv_len) + 15) / 16);

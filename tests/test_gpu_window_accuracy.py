@@ -64,3 +64,31 @@ def test_gradients_round_once(shape):
     sizes = [dict(terms(x, b, window, sinks, scale), dv=sums_of_sizes(x, b, window, sinks, scale)[1]) for b in range(B)]
     for name, w in zip(GRADS, want):
         rounded_once(got[name], w, name, np.stack([a[name] for a in sizes]), 0.0 if name == "dv" else 2.0 ** -20)
+
+
+@pytest.mark.parametrize("io", [torch.float32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("scale", [7.3, 41.0, -23.0])
+def test_gradients_where_one_key_has_all_the_weight(scale, io):
+    """Each query is one of its visible keys (of norms that differ), so that its score, hundreds or thousands, is far above
+    the others: one weight is one, the others and dq and dk are zero, dv are the output gradients of the queries that
+    chose the key.  lse, fp32, and its product with log2(e) are off by 2^-24 of themselves each, and so would be the
+    weight; its difference from one would stand in dq and dk with the full size of dout . v, and in dv."""
+    n, Hq, Hk, d, window, sinks = 150, 4, 2, 64, 40, 1
+    x, t = case(9, 1, n, n, Hq, Hk, d, io)
+    rng = np.random.default_rng(4)
+    for i in range(n):
+        for h in range(Hq):
+            x["q"][0, i, h] = x["k"][0, rng.integers(max(0, i - window + 1), i + 1), h // 2] * np.sign(scale)
+    t["q"] = torch.from_numpy(x["q"]).to(t["q"])
+    out, lse = fwd(t, window, sinks, scale=scale)
+    got = bwd(t, out, lse, window, sinks, scale=scale)
+    want, sizes = refs(x, 0, window, sinks, scale)[2:], terms(x, 0, window, sinks, scale)
+    assert float(lse.min()) > 20 * abs(scale)
+    for name, w in zip(GRADS, want):
+        off = np.linalg.norm(got[name][0].double().cpu().numpy() - w)
+        # dq, dk: what sums of 128 products leave of dout . v - D; dv: sums of some of 80 gradients, and one rounding
+        bound = 2.0 ** -20 * np.linalg.norm(sizes[name]) if name != "dv" else (
+            FP32 * np.linalg.norm(w) if io != BF else
+            np.linalg.norm(torch.from_numpy(w).to(BF).double().numpy() - w) + 2 * (FP32 + PARTS) * np.linalg.norm(w))
+        print(f"[window one key] {scale} {io} {name}: {off:.3e}, bound {bound:.3e}", flush=True)
+        assert off <= bound, name
