@@ -490,7 +490,8 @@ inline int check_delta(const mamba_delta_dims* d, bool packed) {
   if (tokens * (double)d->v_heads * (double)std::max(d->dk, d->dv) > (double)lim)
     return MAMBA_ERR_SHAPE;
   // the grids: one workgroup per chunk slot and head, and per sequence, value head and 16 columns.  (Launches that
-  // could have 2^32 threads are laid out by wide_grid; for the others the workspace would be past 300 GB by then.)
+  // could have 2^32 threads are laid out by wide_grid; for the others, which are the delta rule's chunk products and
+  // gradients, the workspace would be past 300 GB by then, and its segments are not used with so many heads.)
   if ((tokens / kC + (double)d->batch) * (double)d->v_heads > 2147483647.0 ||
       (double)d->batch * (double)d->v_heads * 64.0 > 2147483647.0)
     return MAMBA_ERR_SHAPE;

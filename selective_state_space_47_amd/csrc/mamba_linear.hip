@@ -11,15 +11,17 @@ namespace linear {
 namespace {
 
 // The states that the segments begin with, one after another: S <- decay S + (the segment's own); seg_state holds each
-// segment's own on entry.  Bound by memory (packed prompts, 80 heads of 128 x 64: 28 us, 5.5 TB/s).  The first one's is a copy of the initial state: the output pass reads only these, as it may
-// write the last state over the initial one.
+// segment's own on entry.  Bound by memory (packed prompts, 80 heads of 128 x 64: 28 us, 5.5 TB/s).  The first one's is a
+// copy of the initial state: the output pass reads only these, as it may write the last state over the initial one.
 template <bool kRev>
 __global__ __launch_bounds__(256) void linear_join_kernel(PassArgs p, int32_t blocks) {
   const Args& a = p.f;
-  const int64_t sh = blockIdx.x / (uint32_t)blocks;
+  const uint32_t id = wide_index();
+  const int64_t sh = id / (uint32_t)blocks;
   const int64_t seq = sh / a.hv;
+  if (seq >= a.nseq) return;
   const int vh = (int)(sh - seq * a.hv);
-  const int64_t size = (int64_t)a.dk * a.dv, at = ((int64_t)(blockIdx.x - sh * blocks) * 256 + threadIdx.x) * 4;
+  const int64_t size = (int64_t)a.dk * a.dv, at = ((int64_t)(id - sh * blocks) * 256 + threadIdx.x) * 4;
   if (at >= size) return;
   const int64_t unit = a.seg_chunks * kC;
   const Span sp = seq_span(a, seq);
@@ -145,7 +147,7 @@ int launch_segments_t(const PassArgs& p, hipStream_t s) {
   const int st = launch_pass<E, kSegmentOnly | (kRev ? kReverse : 0)>(p, s);
   if (st != MAMBA_OK) return st;
   const int blocks = (p.f.dk * p.f.dv + 1023) / 1024;
-  hipLaunchKernelGGL((linear_join_kernel<kRev>), dim3((unsigned)(p.f.nseq * p.f.hv * blocks)), dim3(256), 0, s, p,
+  hipLaunchKernelGGL((linear_join_kernel<kRev>), wide_grid((uint64_t)p.f.nseq * p.f.hv * blocks, 256), dim3(256), 0, s, p,
                      blocks);
   return launch_status();
 }
