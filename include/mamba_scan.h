@@ -519,9 +519,10 @@ int mamba_window_attn_fwd(const void* q, const void* k, const void* v, const int
                           const mamba_window_dims* dims, void* stream);
 
 /* Bytes of device workspace mamba_window_attn_bwd needs (0 for invalid dims; packed != 0: for a call with offsets):
- * two numbers (fp32 storage: three) per query and head, with sinks that queries outside their window see fp32 sums of dk
- * and dv per 64 to 512 queries and query head for each 16 of the sinks, and where a few keys' tiles would leave the GPU
- * idle such sums per part of the query heads of each key head. */
+ * two numbers (fp32 storage: three) per query and head, with a few sinks that queries outside their window see fp32 sums
+ * of dk and dv per 64 to 512 queries (more where these would exceed four times dk and dv in fp32 and 256 MB) and query
+ * head for each 16 of the sinks, and where a few keys' tiles would leave the GPU idle such sums per part of the query
+ * heads of each key head. */
 size_t mamba_window_attn_bwd_workspace_bytes(const mamba_window_dims* dims, int packed);
 
 /*

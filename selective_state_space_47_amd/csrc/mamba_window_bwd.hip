@@ -10,7 +10,8 @@
 //                       another: sums in accumulators in a fixed order, no atomics
 // The sinks are seen by every later query: the queries past the windows of a sinks' tile are cut into stretches,
 // which window_dkv_kernel takes first, as workgroups of their own that leave fp32 sums; the tile's own workgroup, of
-// a launch after that, adds them in order.  Without this one workgroup would go through a whole long sequence.
+// a launch after that, adds them in order.  Without this one workgroup would go through a whole long sequence; where the
+// sinks are many they are many workgroups, which do.
 //
 // The scores are made again in each kernel (nine products in place of five): dQ summed over the keys' workgroups
 // would need atomics, whose order changes results, or a sum in memory per tile of keys.  And D from the rounded out
@@ -47,7 +48,9 @@ template <typename E>
 constexpr int kKeyRows = kPairs * 16 * kTilesW<E>;
 template <typename E>
 constexpr int kStats = sizeof(E) == 2 ? 2 : 3;   // numbers of a query and head that the keys' pass reads
-constexpr int kFar = 512;                        // queries of a stretch past the sinks' windows, at most
+constexpr int kFar = 512;                        // queries of a stretch past the sinks' windows where there are few sinks
+constexpr double kSinkWG = 96.0;                 // workgroups of sinks from which on there are no stretches
+constexpr int64_t kFarBytes = (int64_t)256 << 20;  // sums of stretches: up to so much, or four times dk and dv in fp32
 
 // 8 lanes per row; a row without a key has weights of zero: its log-sum counts as +infinity
 template <typename E>
@@ -281,7 +284,7 @@ __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeo
     if (k.q_lo >= k.q_hi) return;
   } else {
     k.q_lo = max(j0 - k.shift, 0);
-    k.q_hi = (int)min(near(tile), (int64_t)qs.len);
+    k.q_hi = a.sink_tiles || j0 >= mask.sinks ? (int)min(near(tile), (int64_t)qs.len) : qs.len;  // (no far part: all)
   }
   k.t_lo = k.q_lo / kKeys;
   k.tiles = k.q_hi > k.q_lo ? (k.q_hi - 1) / kKeys - k.t_lo + 1 : 0;
@@ -656,18 +659,33 @@ BwdLayout layout(const mamba_window_dims* d, bool packed) {
   const size_t stats = d->io_dtype == MAMBA_BF16 ? kStats<uint16_t> : kStats<float>;
   l.far = ((size_t)l.tokens * (size_t)d->q_heads * stats * sizeof(float) + 255) / 256 * 256;
   l.total = l.far;
-  if (d->sinks && d->window < d->kv_len) {  // (a window of every key leaves no query past it)
-    l.sink_tiles = (int32_t)((std::min(d->sinks, d->kv_len) + 15) / 16);
+  // (queries times sinks for which inputs alone are past any memory are said to take a workspace that is)
+  if (d->window < d->kv_len && (double)l.tokens * (double)(d->q_heads * d->dim) * (double)std::min(d->sinks, d->kv_len) > 6.4e19) {
+    l.total = SIZE_MAX;
+    return l;
+  }
+  // Many sinks are many workgroups by themselves, which go through all their queries (1 x 16384 tokens, 20 and 4 heads of
+  // 128, window 1024, bf16, by stretches and so: 1024 sinks, 64 workgroups, 2.80 and 3.51 ms; 2048, 128 of them, 4.28 and
+  // 3.87; 4096 6.98 and 4.53; 12 and 12 heads, 512 sinks, 96, 1.26 and 1.06).  Packed: those of one sequence count.
+  const int64_t rows = d->io_dtype == MAMBA_BF16 ? kKeyRows<uint16_t> : kKeyRows<float>;
+  const double sink_wgs = (packed ? 1.0 : (double)d->batch) * (double)d->kv_heads * (double)((d->sinks + rows - 1) / rows);
+  // (as many sinks, or a window of as many tokens, as there are keys: every earlier key is seen, no query is far)
+  if (d->sinks && d->window < d->kv_len && d->sinks < d->kv_len && sink_wgs < kSinkWG) {
+    l.sink_tiles = (int32_t)((d->sinks + 15) / 16);
     // shorter stretches where they would leave CUs idle (2 x 333 tokens, 12 heads of 64, fp32: 22 -> 13 us)
     auto slots = [&] { return tile_slots(d->seqlen, d->batch, packed, l.far_len); };
     while (l.far_len > kKeys && (double)slots() * (double)d->q_heads * (double)l.sink_tiles < 256.0) l.far_len /= 2;
-    l.far_slots = slots();
-    // (sinks by the million: more than any workspace holds, and than the sum would)
-    if ((double)l.far_slots * (double)d->q_heads * (double)l.sink_tiles * 128.0 * (double)d->dim > 1e18) {
-      l.total = SIZE_MAX;
-      return l;
+    // longer ones where the sums would grow with queries times sinks, none where one for each sequence is too much
+    auto bytes = [&] { return (double)slots() * (double)d->q_heads * (double)l.sink_tiles * 128.0 * (double)d->dim; };
+    const double most = std::max((double)kFarBytes, 32.0 * (packed ? 1.0 : (double)d->batch) * (double)d->kv_len *
+                                                        (double)(d->kv_heads * d->dim));
+    while (bytes() > most && l.far_len < d->seqlen && l.far_len < 1 << 30) l.far_len *= 2;
+    if (bytes() > most) {
+      l.sink_tiles = 0;
+    } else {
+      l.far_slots = slots();
+      l.total += (size_t)l.far_slots * (size_t)d->q_heads * (size_t)l.sink_tiles * 32 * (size_t)d->dim * sizeof(float);
     }
-    l.total += (size_t)l.far_slots * (size_t)d->q_heads * (size_t)l.sink_tiles * 32 * (size_t)d->dim * sizeof(float);
   }
   // A key head's heads go to several workgroups where tiles of keys alone leave CUs idle and that shortens the longest
   // chain by four tiles, which the sum of the parts costs (the same case: 42 -> 24 us and 5 for the sum).
