@@ -1,10 +1,12 @@
-"""Launches of linear attention, window attention and the norm of queries and keys with 2^32 threads and more: a grid's
-dimension counts threads in 32 bits, and workgroups past that would never run, without an error."""
+"""Linear attention, window attention and the norm of queries and keys at the sizes where 32 bits end: launches with 2^32
+threads and more (a grid's dimension counts threads in 32 bits, and workgroups past that would never run, without an
+error), and gradients of tensors past 2^31 elements.  Bounds as in the files that their checks come from."""
 import numpy as np
 import pytest
 import torch
 
-from oracle import linear
+from oracle import linear, norm
+from oracle import window as wref
 from selective_state_space_47_amd import binding
 
 from .test_gpu_linear import BF, DEV, F32, _native, check  # noqa: F401
@@ -13,6 +15,7 @@ pytestmark = pytest.mark.gpu
 
 
 def room(gib):
+    torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < gib << 30:
         pytest.skip("memory")
 
@@ -36,3 +39,151 @@ def test_segments_of_many_sequences():
     check(out[L - 1000:], want[0, tail - 1000:], "out", F32)
     check(last[-1:], wlast, "last_state", F32)
     assert bool((last[:-1] == 0).all())
+
+
+def draws(seed, *shapes, dt=F32):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    return [torch.randn(*s, generator=gen, device=DEV, dtype=dt) for s in shapes]
+
+
+def near(got, want, name, bound):
+    """The 2-norm over tensors that stay on the GPU, in pieces."""
+    off = size = 0.0
+    for a, b in zip(got.split(1 << 16), want.split(1 << 16)):
+        off += float((a.double() - b.double()).square().sum())
+        size += float(b.double().square().sum())
+    print(f"[mixer grids] {name}: {(off / size) ** 0.5:.2e}", flush=True)
+    assert off ** 0.5 <= bound * size ** 0.5, name
+
+
+def test_linear_step_and_one_token():
+    """2^18 + 3 sequences of 64 heads, one token each: 2^24 + 192 workgroups of the step and of the pass."""
+    room(40)
+    B, H, d = (1 << 18) + 3, 64, 8
+    state, q, k, v = draws(2, (B, H, d, d), (B, H, d), (B, H, d), (B, H, d))
+    g = -torch.rand(B, H, device=DEV)
+    now = state.clone()
+    out = binding.mamba_linear_attn_update(now, q, k, v, g)
+    want = state * g.exp()[..., None, None] + k[..., None] * v[..., None, :]
+    near(now, want, "state", 2e-5)
+    o = (want * q[..., None]).sum(-2) * d ** -0.5
+    near(out, o, "out", 2e-5)
+    seq, last = binding.mamba_linear_attn_fwd(*(a[:, None] for a in (q, k, v, g)), initial_state=state, return_last_state=True)
+    near(seq[:, 0], o, "out of a sequence", 2e-5)
+    near(last, want, "last state", 2e-5)
+
+
+def test_window_forward_and_gradients():
+    """2^20 sequences of 17 heads, two tokens each."""
+    room(40)
+    B, L, H, d = 1 << 20, 2, 17, 8
+    q, k, v, do = draws(3, *[(B, L, H, d)] * 4)
+    out, lse = binding.mamba_window_attn_fwd(q, k, v, 2, return_lse=True)
+    got = binding.mamba_window_attn_bwd(q, k, v, out, lse, do, 2)
+    s = (q[:, 1, :, None] * k.transpose(1, 2)).sum(-1) * d ** -0.5       # (B, H, 2): of the second query
+    P = torch.softmax(s, -1)
+    near(out[:, 0], v[:, 0], "out, first", 2e-5)
+    near(out[:, 1], (P[..., None] * v.transpose(1, 2)).sum(2), "out, second", 2e-5)
+    dp = (do[:, 1, :, None] * v.transpose(1, 2)).sum(-1)
+    ds = P * (dp - (P * dp).sum(-1, keepdim=True)) * d ** -0.5
+    near(got["dq"][:, 1], (ds[..., None] * k.transpose(1, 2)).sum(2), "dq", 2e-5)
+    near(got["dk"][:, 0], ds[..., :1] * q[:, 1], "dk, first", 2e-5)
+    near(got["dk"][:, 1], ds[..., 1:] * q[:, 1], "dk, second", 2e-5)
+    near(got["dv"][:, 0], do[:, 0] + P[..., :1] * do[:, 1], "dv, first", 2e-5)
+    near(got["dv"][:, 1], P[..., 1:] * do[:, 1], "dv, second", 2e-5)
+
+
+def test_window_step():
+    """2^20 sequences of 17 key heads at their first and at a later position, two slots each."""
+    room(40)
+    B, H, d = 1 << 20, 17, 8
+    q, k, v, kc, vc = draws(4, *[(B, H, d)] * 3, *[(B, 2, H, d)] * 2)
+    pos = torch.zeros(B, dtype=torch.int64, device=DEV)
+    pos[1::2] = 5                                                         # slot 1, and slot 0 holds position 4
+    before = kc.clone(), vc.clone()
+    out = binding.mamba_window_attn_update(kc, vc, q, k, v, pos)
+    near(out[::2], v[::2], "out, first", 2e-5)
+    s = torch.stack([(q * before[0][:, 0]).sum(-1), (q * k).sum(-1)], -1)[1::2] * d ** -0.5
+    P = torch.softmax(s, -1)
+    near(out[1::2], P[..., :1] * before[1][1::2, 0] + P[..., 1:] * v[1::2], "out, later", 2e-5)
+    assert torch.equal(kc[::2, 0], k[::2]) and torch.equal(vc[1::2, 1], v[1::2])
+    assert torch.equal(kc[::2, 1], before[0][::2, 1]) and torch.equal(vc[1::2, 0], before[1][1::2, 0])
+
+
+def test_norm_of_many_rows():
+    """2^26 + 5 rows: 2^24 + 2 workgroups of four rows."""
+    room(40)
+    n, d = (1 << 26) + 5, 16
+    q, k = draws(5, (n, 1, d), (n, 1, d), dt=BF)
+    wq, wk = draws(6, (d,), (d,))
+    pos = torch.arange(n, device=DEV)
+    freq = torch.tensor(10000.0 ** (-np.arange(d // 2) / (d // 2)), device=DEV)
+    qo, ko = binding.mamba_qk_norm_rope_fwd(q, k, wq, wk, pos, freq)
+    for rows in (slice(0, 3000), slice((1 << 26) - 3000, (1 << 26) + 5)):
+        for x, w, got, name in ((q, wq, qo, "q"), (k, wk, ko, "k")):
+            want = norm.qk_norm_rope_ref(x[rows].double().cpu().numpy(), w.double().cpu().numpy(), pos[rows].cpu().numpy(),
+                                         freq.cpu().numpy(), 1e-5, False)
+            check(got[rows], want, name, BF)
+    for at in range(0, n, 1 << 24):  # every row is written: a turn keeps the norm of weight times x
+        rows = slice(at, at + (1 << 24))
+        h = q[rows].float() * (q[rows].float().square().mean(-1, keepdim=True) + 1e-5).rsqrt() * wq
+        a, b = qo[rows].float().square().sum(-1), h.square().sum(-1)
+        assert bool(((a - b).abs() <= 2.0 ** -6 * b).all())  # (a value is off by 2^-8 at most, its square by twice that)
+
+
+def test_window_gradients_past_2_31_elements():
+    """fp32, 2^29 rows of queries' statistics and 4.6e9 values of q: 2^19 sequences of 64 tokens, 17 query heads of 8."""
+    room(150)
+    B, L, H, d = 1 << 19, 64, 17, 8
+    q, do, k, v = draws(7, *[(B, L, H, d)] * 2, *[(B, L, 1, d)] * 2)
+    out, lse = binding.mamba_window_attn_fwd(q, k, v, 9, 2, return_lse=True)
+    got = binding.mamba_window_attn_bwd(q, k, v, out, lse, do, 9, 2)
+    for b in (0, B // 2 + 1, B - 1):
+        x = [a[b].double().cpu().numpy() for a in (q, k, v, do)]
+        check(out[b], wref.window_ref(*x[:3], 9, 2, d ** -0.5)[0], "out", F32)
+        for name, want in zip(("dq", "dk", "dv"), wref.window_ref(*x[:3], 9, 2, d ** -0.5, x[3])):
+            check(got[name][b], want, name, F32)
+
+
+def test_linear_gradients_past_2_31_elements():
+    """2.4e9 values of v: 2^18 tokens in two sequences, 72 heads of 128 columns.  With a decay of exp(-0.5) a token 200
+    tokens are all that a gradient of the last ones sees."""
+    room(100)
+    L, H, dk, dv = 1 << 18, 72, 16, 128
+    q, k, v, do = draws(8, (L, 1, dk), (L, 1, dk), (L, H, dv), (L, H, dv), dt=BF)
+    g = torch.full((L, H), -0.5, device=DEV)
+    off = torch.tensor([0, 5, L], device=DEV)
+    got = binding.mamba_linear_attn_bwd(q, k, v, g, do, seq_offsets=off)
+    x = [a[L - 500:].double().cpu().numpy()[None] for a in (q, k, v, g, do)]
+    want = linear.linear_bwd_ref(*x[:4], dk ** -0.5, x[4])
+    for name in ("dq", "dk", "dv", "dg"):
+        check(got[name][L - 250:], want[name][0, 250:], name, BF, wide=name == "dg")
+
+
+def test_norm_gradients_past_2_31_elements():
+    """2.4e9 values of the queries: 2^21 rows of 9 heads of 128."""
+    room(60)
+    n, H, d = 1 << 21, 9, 128
+    q, dq, k, dk = draws(9, *[(n, H, d)] * 2, *[(n, 1, d)] * 2, dt=BF)
+    wq, wk = draws(10, (d,), (d,))
+    pos = torch.arange(n, device=DEV)
+    freq = torch.tensor(10000.0 ** (-np.arange(d // 2) / (d // 2)), device=DEV)
+    got = binding.mamba_qk_norm_rope_bwd(q, k, wq, wk, pos, freq, dq, dk)
+    for rows in (slice(0, 100), slice(n - 100, n)):
+        for x, w, dx, name in ((q, wq, dq, "dq"), (k, wk, dk, "dk")):
+            want, _ = norm.qk_norm_rope_ref(x[rows].double().cpu().numpy(), w.double().cpu().numpy(), pos[rows].cpu().numpy(),
+                                            freq.cpu().numpy(), 1e-5, False, dx[rows].double().cpu().numpy())
+            check(got[name][rows], want, name, BF)
+    # the weights' gradients, all rows, without the rotation: d(h) turned back is the same as h turned, so of dot products
+    # of pairs with the turned norm of x
+    for x, w, dx, name in ((q, wq, dq, "dq_weight"), (k, wk, dk, "dk_weight")):
+        want = torch.zeros(d, device=DEV, dtype=torch.float64)
+        for r in range(0, n, 1 << 15):
+            rows = slice(r, r + (1 << 15))
+            X, D = x[rows].double(), dx[rows].double()
+            X = X * (X.square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+            a = pos[rows].double()[:, None, None] * freq
+            c, s = a.cos(), a.sin()
+            D = torch.cat([D[..., :d // 2] * c + D[..., d // 2:] * s, D[..., d // 2:] * c - D[..., :d // 2] * s], -1)
+            want += (X * D).sum((0, 1))
+        check(got[name], want.cpu().numpy(), name, F32)
