@@ -568,35 +568,50 @@ int launch_pass(const PassArgs& p, hipStream_t s) {
   return p.f.dk <= 64 ? launch_pass_t<E, 64, kWhat>(p, s) : launch_pass_t<E, 128, kWhat>(p, s);
 }
 
-// Chunks per segment (even), 0 for whole sequences.  A chunk takes 6, 6.8 or 7.6 us where 1, 2 or 3 workgroups share a
-// CU and 12 ns of a full GPU (measured, bf16, dk = 128).  Segments cost a second pass that leaves only states, under half
-// the time, the states' way through memory (twice, 5 TB/s) and 15 us of launches.
-//   Equal sequences: the time of the pass in its rounds of three workgroups per CU, with and without.
+// What a chunk of an output pass takes in us where 1, 2 or `per_cu` workgroups share a CU (measured: 2048 tokens whole, 12 to
+// 256, 320 and 384, and 640 workgroups).  fp32: LDS has room for one workgroup, or two of up to 64 values of dk.
+struct ChunkTime {
+  double us[3];
+  int64_t per_cu;
+};
+inline ChunkTime chunk_time(const mamba_delta_dims* d) {
+  if (d->io_dtype == MAMBA_BF16) return d->dk <= 64 ? ChunkTime{{2.8, 3.6, 4.8}, 3} : ChunkTime{{3.4, 4.6, 6.6}, 3};
+  return d->dk <= 64 ? ChunkTime{{5.8, 9.3}, 2} : ChunkTime{{9.2}, 1};
+}
+
+// Chunks per segment (even), 0 for whole sequences.  Segments cost a second pass that leaves only states, a quarter of the
+// time, half a chunk to begin one, the states' way through memory (twice, 5 TB/s) and 15 us of launches in place of 5.
+//   Equal sequences: the time of the pass in its rounds of workgroups, with and without.
 //   Packed ones, whose lengths are not known here: segments where one sequence of all tokens would take twice as long as
 //   all work, which costs the launches where no sequence is long, as those whose chain takes no longer than about the
 //   work (`limit` chunks) are not cut; the length for which a chain behind half the work and the states take least.
-// Measured without and with: 65536 tokens, 12 heads of 128 x 128, 5.9 ms and 326 us; 2 x 333 tokens, 12 heads of 64 x 96,
-// fp32, 41 and 28 us; packed, 80 heads of 128 x 64: 8279 tokens in 8 sequences of up to 4099, 378 and 196 us, 15 of 500
-// and one of 12000, 1045 and 334 us; 16 of 2048, 387 and 415 us, 64 of 300, 286 and 310 us.
+// Measured whole and cut, forward, dk and dv of 128 and 64 where nothing else is said: 65536 tokens, 12 heads of 128 x 128,
+// bf16, 5.9 ms and 326 us; sequences of 2048, by 12, 96, 192, 256 and 384 workgroups, bf16 108 and 30, 109 and 61, 110 and
+// 98, 110 and 122, 152 and 168 us; fp32 292 and 47, 295 and 189, 298 and 336, 299 and 443, 589 and 582; dk = 64, fp32, 182
+// and 33, 186 and 101, 187 and 179, 190 and 258, 300 and 303.  Sequences of 512, 192 workgroups, dk = 64: bf16 27 and 33,
+// fp32 52 and 63.  Packed, 80 heads: 8279 tokens in 8 sequences of up to 4099, bf16 228 and 202, fp32 595 and 588; 15 of 500
+// and one of 12000, 617 and 360, 1705 and 1286; but 16 of 2048, 405 and 428, 1483 and 1867; 64 of 300, 252 and 297, 1072
+// and 1246, which lengths on the host would tell apart.
 struct SegPlan {
   int64_t chunks, limit;
 };
 inline SegPlan plan_segments(const mamba_delta_dims* d, bool packed) {
+  const ChunkTime t = chunk_time(d);
   const double nseq = (double)(packed ? std::min(d->batch, d->seqlen) : d->batch);
   const double length = std::ceil((double)d->seqlen / kC);  // (packed: of a sequence of all tokens)
   const double heads = (double)d->v_heads * (double)((d->dv + kCols - 1) / kCols);
-  const double work = 0.012 * heads * (length + nseq);
+  const double full = t.us[t.per_cu - 1], work = full / (256.0 * (double)t.per_cu) * heads * (length + nseq);
   auto pass = [&](double c, double segments) {  // segments of c chunks
-    if (packed) return 7.6 * c + 0.5 * work;
-    const int64_t k = (int64_t)std::ceil(segments * heads / 256.0);
-    return c * (7.6 * (double)(k / 3) + (k % 3 ? 5.2 + 0.8 * (double)(k % 3) : 0.0));
+    if (packed) return full * c + 0.5 * work;
+    const int64_t k = (int64_t)std::ceil(segments * heads / 256.0), rest = k % t.per_cu;
+    return c * (full * (double)(k / t.per_cu) + (rest ? t.us[rest - 1] : 0.0));
   };
-  double best = packed ? (6.0 * length > 2.0 * work ? 1e30 : 0.0) : 0.95 * pass(length, nseq);
-  SegPlan plan = {0, packed ? (int64_t)(work / 8.0) : 0};
+  double best = packed ? (t.us[0] * length > 2.0 * work ? 1e30 : 0.0) : 0.95 * (pass(length, nseq) + 5.0);
+  SegPlan plan = {0, packed ? (int64_t)(work / full) : 0};
   for (int64_t c = 2; (double)c * 2.0 <= length; c += c < 32 ? 2 : c / 16 * 2) {
     const double segments = packed ? length / (double)c + nseq : std::ceil(length / (double)c) * nseq;
     const double states = segments * (double)d->v_heads * (double)(d->dk * d->dv) * 8.0 / 5e6;
-    const double time = 1.45 * pass((double)c, segments) + states + 15.0;
+    const double time = 1.25 * pass((double)c + 0.5, segments) + states + 15.0;
     if (time < best) best = time, plan.chunks = c;
   }
   return plan;
