@@ -18,11 +18,11 @@
 // one's operand, so that only the triangular matrix, which the waves share out, and the output, which is stored in whole
 // rows, go through LDS.
 //
-// Measured (8 x 2048 tokens, 20 key and 40 value heads of 128, bf16): forward 227 us (2.2 TB/s; its bytes at a copy's
-// rate 105), backwards with images 259, forwards with images and their products 210 (4.5 TB/s).  With an output a wave
+// Measured (8 x 2048 tokens, 20 key and 40 value heads of 128, bf16): forward 203 us (2.5 TB/s; its bytes at a copy's
+// rate 105), backwards with images 244, forwards with images and their products 208 (4.5 TB/s).  With an output a wave
 // has 5.8 vector instructions of 4 cycles per product, and a product keeps the vector unit from issuing for half of its
 // 16 cycles (measured), so that the best would be 110 us: the state's and the entering values' conversions to bf16 parts
-// are most of it.  A chunk takes a workgroup that is alone on its CU 9500 cycles.
+// are most of it.  A chunk takes a workgroup that is alone on its CU 3.4 us.
 #pragma once
 #include <algorithm>
 #include <cmath>

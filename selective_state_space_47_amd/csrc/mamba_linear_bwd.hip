@@ -15,7 +15,7 @@
 // head, value heads added in accumulators in a fixed order.  Where units and key heads alone would leave CUs idle the
 // value heads of a key head are split among workgroups, whose fp32 sums linear_fold_kernel adds in order.  No atomics.
 //
-// Measured (8 x 2048 tokens, 20 and 40 heads of 128, bf16): dK 271 us at 4.1 TB/s, dQ and dg 331 at 3.9, bound by memory:
+// Measured (8 x 2048 tokens, 20 and 40 heads of 128, bf16): dK 259 us at 4.7 TB/s, dQ and dg 326 at 4.5, bound by memory:
 // the states' images, 4 bytes a value, are a quarter of the bytes, V or dO comes in twice, as tiles and as a wave's own
 // operands.  Both sides in one kernel, with 154 KB of LDS and so one workgroup per CU, took 739.  Images of units of
 // 256 tokens would be half as large, for twice the pairs of tokens and tiles that do not fit two workgroups' LDS.

@@ -96,8 +96,8 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd, kQkFwd, kQkBwd, kLinearFwd, kLinearUpdate, kLinearBwd, kWindowFwd, kWindowBwd, kWindowUpdate,
-             kWindowStore, kEntries };
+enum Entry { kDeltaFwd, kDeltaUpdate, kDeltaBwd, kGatedFwd, kGatedBwd, kAddFwd, kAddBwd, kQkFwd, kQkBwd, kLinearFwd,
+             kLinearUpdate, kLinearBwd, kWindowFwd, kWindowBwd, kWindowUpdate, kWindowStore, kEntries };
 
 // call(entry, dims address, stream, factor, workspace bytes, *tensors) -> status.  The tensors stand in the
 // order of the entry point's pointers, `factor` is its scale or eps.

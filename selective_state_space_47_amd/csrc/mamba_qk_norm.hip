@@ -11,8 +11,8 @@
 // workgroup's rows are made once for all heads, in LDS: the angle in turns is a product in fp64 less its nearest
 // integer (a position of a million at one radian each would leave fp32 two digits), its sine and cosine fp32.
 // The weights' gradients are partial rows, one per workgroup, added by a second launch in a fixed order: no atomics.
-// 16384 rows, 20 and 4 heads of 128, bf16: 33 us (6.0 TB/s, some of it from the caches), gradients 82 (3.6 TB/s: half of a
-// copy's rate is lost to the conversions and sums, the vector unit is busy 68% of the time) and 4.
+// 16384 rows, 20 and 4 heads of 128, bf16: 33 us (6.0 TB/s, some of it from the caches), gradients 87 (3.4 TB/s: some of
+// a copy's rate is lost to the conversions and sums, the vector unit is busy 67% of the time) and 5.
 #include "mamba_common.h"
 #include "mamba_grid.h"
 

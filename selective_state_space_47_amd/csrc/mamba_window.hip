@@ -17,8 +17,8 @@
 // past a factor of 2^8, so that in a tile with a new maximum the sums are seldom rescaled (7% of the time).
 //
 // Measured (8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16): 211 us, 615 TFLOP/s of the pairs that are seen, 1.5
-// times as many of products made.  The vector and the matrix unit are busy in turn: softmax, conversions and products of
-// the two waves of a SIMD add up.  Two workgroups share a CU, 8 waves of 32 queries: with 16 each a tile's operands would
+// times as many of products made.  The matrix unit is busy for 45% of that, the vector unit for 55%, in turn: softmax,
+// conversions and products of the two waves of a SIMD add up.  Two workgroups share a CU, 8 waves of 32 queries: with 16 each a tile's operands would
 // be read twice as often.
 #include "mamba_window.h"
 

@@ -13,9 +13,10 @@
 // a launch after that, adds them in order.  Without this one workgroup would go through a whole long sequence; where the
 // sinks are many they are many workgroups, which do.
 //
-// The scores are made again in each kernel (nine products in place of five): dQ summed over the keys' workgroups
-// would need atomics, whose order changes results, or a sum in memory per tile of keys.  And D from the rounded out
-// would carry 2^-9 of dO . out into dS, which is the small difference of two numbers of that size where a few keys have
+// The scores are made again in each kernel (with bf16 storage six products in the queries' pass and seven in the keys', ten
+// in all without the second parts of P and dS, with fp32 storage eight, in place of five): dQ summed over the keys'
+// workgroups would need atomics, whose order changes results, or a sum in memory per tile of keys.  And D from the rounded
+// out would carry 2^-8 of dO . out into dS, which is the small difference of two numbers of that size where a few keys have
 // all the weight (4 keys, scores of deviation 3.4: dq was off by 5.4e-3).
 //
 // lse is a number of fp32 and so is its product with log2(e): each is off by 2^-24 of itself, and the weights made from
@@ -82,8 +83,8 @@ __global__ __launch_bounds__(256) void window_stat_kernel(WinArgs a, int64_t tok
 // What a wave of the keys' pass makes: dV (from P), or dK (from P and dO V^T).  Two waves share 32 keys (fp32 storage:
 // 16): with both sums in one wave there is room for one wave on a SIMD, which has nobody to hide its waits behind.
 // (8 x 2048 tokens, 20 and 4 heads of 128, window 1024, dS in one part: 395 us; both sums in one wave and 128 keys per
-// workgroup 491, by roles with 128 keys 503, as the longest workgroups then ran alone at the end.  With dS in two: 446, and
-// P in two as well: 469.)
+// workgroup 491, by roles with 128 keys 503, as the longest workgroups then ran alone at the end; these on a GPU whose clocks
+// had not risen.  Warm, with P and dS in two parts: 418, matrix unit 54% busy.)
 enum Role { kMakeDv, kMakeDk };
 
 // The queries' tiles of a workgroup of the keys' pass
@@ -230,7 +231,7 @@ __device__ __forceinline__ int64_t part_floats(const WinArgs& a) {
 }
 
 // kFarPart: 16 sinks and one query head over a stretch of queries past the sinks' windows; otherwise a tile of keys, the
-// heads that share it one after another.  (Far part of 4 sinks and 8 x 2048 tokens: 28 us; with the sinks' tile as one
+// heads that share it one after another.  (Far part of 4 sinks and 8 x 2048 tokens: 27 us; with the sinks' tile as one
 // workgroup's work it was 564.)
 template <typename E, int DK, bool kFarPart>
 __global__ __launch_bounds__(kFarPart ? 128 : 128 * kPairs, kFarPart ? 1 : sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(WinArgs a, uint32_t blocks, int64_t tokens) {
@@ -416,8 +417,8 @@ __global__ __launch_bounds__(256) void window_fold_kernel(WinArgs a) {
   }
 }
 
-// 8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16: 411 us for seven products per pair of tiles (S and dO V^T
-// twice, dS K in two parts and the queries' exponentials twice).
+// 8 x 2048 tokens, 20 and 4 heads of 128, window 1024, bf16: 365 us for six products per pair of tiles (S and dO V^T
+// twice, dS K in two parts; the exponentials are made twice too), matrix unit 51% busy.
 template <typename E, int DK>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(WinArgs a, uint32_t blocks,
                                                                                 int64_t tokens) {
