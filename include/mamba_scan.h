@@ -527,7 +527,8 @@ size_t mamba_window_attn_bwd_workspace_bytes(const mamba_window_dims* dims, int 
 
 /*
  * Gradients of mamba_window_attn_fwd for the loss sum(out * dout); out and lse are the forward's (with bf16 storage
- * dout . out is taken from the weights, not from the rounded out).
+ * dout . out is taken from the weights, not from the rounded out; the weights, which are made from lse, are divided by
+ * their sum).  With bf16 storage each gradient is the fp32 result rounded once.
  *   dout       : (batch, seqlen, q_heads, dim), io_dtype, contiguous
  *   dq         : like out;  dk, dv : (batch, kv_len, kv_heads, dim), io_dtype, contiguous, summed over the query
  *                heads that share the head

@@ -1,12 +1,13 @@
 """Gradients of window attention with many sinks: sinks of every length up to all keys, long stretches of the queries that
 see only them, and batches whose sinks' tiles go through all their queries.  Bounds as in test_gpu_window (2e-5 of the norm
 with fp32 storage, 2^-8 with bf16)."""
+import numpy as np
 import pytest
 import torch
 
 from selective_state_space_47_amd import binding
 
-from .test_gpu_window import BF, DEV, F32, GRADS, IO, _native, ids  # noqa: F401
+from .test_gpu_window import BF, DEV, F32, GRADS, IO, _native, bwd, case, check, fwd, ids, refs, terms  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,45 @@ def test_many_short_sequences(io):
     some = [0, 1, 999, 1999]
     want, grads = reference(*(a[some] for a in (q, k, v, dout)), window, sinks)
     compare({n: a.unflatten(0, (B, L))[some] for n, a in dict(got, out=out).items()}, dict(grads, out=want), io)
+
+
+@IO
+@pytest.mark.parametrize("shape", [(2, 150, 500, 4, 2, 64, 20, 500), (1, 300, 700, 16, 16, 24, 33, 400), (2, 400, 250, 2, 1, 40, 9, 250),
+                                   (1, 500, 320, 32, 32, 16, 50, 319), (1, 200, 200, 3, 1, 64, 200, 50)], ids=ids)
+@pytest.mark.parametrize("scale", [None, 0.0])
+def test_other_lengths(shape, scale, io):
+    """Earlier keys, and queries that see none, with as many sinks as keys and with sinks that are many workgroups; and a
+    scale of zero, whose weights are all the same."""
+    B, n, m, Hq, Hk, d, window, sinks = shape
+    x, t = case(sum(shape[:6]), B, n, m, Hq, Hk, d, io)
+    print(f"[window sinks] {shape} {scale} {io}", flush=True)
+    out, lse = fwd(t, window, sinks, scale=scale)
+    got = bwd(t, out, lse, window, sinks, scale=scale)
+    factor = d ** -0.5 if scale is None else scale
+    want = [np.stack(a) for a in zip(*(refs(x, b, window, sinks, factor) for b in range(B)))]
+    size = [terms(x, b, window, sinks, factor) for b in range(B)]
+    check(out, want[0], "out", io)
+    for name, w in zip(GRADS, want[2:]):
+        check(got[name], w, name, io, terms=None if name == "dv" else np.stack([a[name] for a in size]))
+
+
+@IO
+def test_packed_lengths_with_many_sinks(io):
+    """Sequences of different lengths, empty ones among them, with earlier keys, whose sinks are many workgroups."""
+    lengths, past, H, d, window, sinks = [130, 0, 1, 260, 65], 40, 32, 16, 11, 200
+    off, koff = np.cumsum([0] + lengths), np.cumsum([0] + [a + past for a in lengths])
+    x, t = case(77, 1, int(off[-1]), int(koff[-1]), H, H, d, io)
+    t = {a: b[0] for a, b in t.items()}
+    kw = dict(seq_offsets=torch.from_numpy(off).to(DEV), kv_offsets=torch.from_numpy(koff).to(DEV))
+    out, lse = fwd(t, window, sinks, **kw)
+    got = bwd(t, out, lse, window, sinks, **kw)
+    want, size = [], []
+    for s in range(len(lengths)):
+        one = dict(q=x["q"][:, off[s]:off[s + 1]], dout=x["dout"][:, off[s]:off[s + 1]],
+                   k=x["k"][:, koff[s]:koff[s + 1]], v=x["v"][:, koff[s]:koff[s + 1]])
+        want.append(refs(one, 0, window, sinks, d ** -0.5))
+        size.append(terms(one, 0, window, sinks, d ** -0.5))
+    want = [np.concatenate(a) for a in zip(*want)]
+    check(out, want[0], "out", io)
+    for name, w in zip(GRADS, want[2:]):
+        check(got[name], w, name, io, terms=None if name == "dv" else np.concatenate([a[name] for a in size]))
